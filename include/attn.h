@@ -277,6 +277,137 @@ ATTN_API attn_status attn_bwd_noalloc(const void* q, const void* k, const void* 
                                       void* dv, int B, int H, int N, int d, float scale,
                                       int causal, cudaStream_t stream);
 
+/*
+ * Serving: prompts of different lengths, and a paged INT8 cache
+ * ---------------------------------------------------------------
+ * These entry points work on PACKED sequences with GROUPED heads: a batch of B
+ * sequences lies one behind the other in tensors of T tokens, sequence b in
+ * tokens [cu_seqlens[b], cu_seqlens[b+1]); H query heads share H_kv key heads
+ * (H a multiple of H_kv, at most 64 times it), query head h using key head
+ * h / (H / H_kv).  d in {64, 128}, BF16 inputs.  Rows have d contiguous elements;
+ * token and head strides (in elements, multiples of 8) are given, so q, k and v
+ * may be views of one projection's output.
+ *
+ * Lengths, page numbers and plans lie in device memory and are read by the
+ * kernels, so a call can be captured in a CUDA graph and replayed on new ones.
+ * They cannot be checked before the launch: a value out of range never leads
+ * outside the tensors; the kernel ignores what it points to, and
+ * attn_check_status() reports ATTN_ERR_INVALID_ARG.  A sequence may have no
+ * token at all.
+ *
+ * The cache: codes k_cache, v_cache int8 [num_pages, H_kv, page_size, d],
+ * contiguous, and scales k_scale, v_scale FP32 [num_pages, H_kv]; a code c stands
+ * for c * scale.  Position t of sequence b is row t % page_size of page
+ * block_table[b * max_blocks + t / page_size].  page_size in {16, 32, 64, 128};
+ * num_pages * H_kv * page_size < 2^31.  Entries of the table behind a sequence's
+ * last page are never used.
+ */
+
+/* Bytes of the plan of attn_varlen_plan (0 on invalid arguments). */
+ATTN_API size_t attn_varlen_plan_bytes(int B, int T, int H, int H_kv);
+
+/*
+ * Lists the work of attn_varlen_fwd on a packed batch, heaviest first, from the
+ * sequences' lengths.  One plan serves any number of calls with the same
+ * cu_seqlens, T, H, H_kv and causal flag (every layer of a model, say).
+ *   cu_seqlens : int32 [B+1], device: 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <= T.
+ *                Tokens from cu_seqlens[B] on belong to no sequence.
+ *   plan       : device buffer of attn_varlen_plan_bytes(...) bytes, 16-byte
+ *                aligned, written.
+ */
+ATTN_API attn_status attn_varlen_plan(const int* cu_seqlens, int B, int T, int H, int H_kv, int causal,
+                                      void* plan, size_t plan_bytes, cudaStream_t stream);
+
+/*
+ * Attention over whole prompts: for every token i of a sequence and head h,
+ * O = sum_j softmax_j(scale q_i . k_j) v_j over the sequence's own tokens j
+ * (causal != 0: j <= i), and the natural-log LSE.
+ *   q    : [T,H,d] BF16;  k, v : [T,H_kv,d] BF16, with the given strides.
+ *   plan : of attn_varlen_plan for the same B, T, H, H_kv and causal; a plan made
+ *          for another T, group size, H_kv or causal flag is reported by
+ *          attn_check_status() and nothing is computed.
+ *   o    : [T,H,d] BF16, contiguous.   lse : [T,H] FP32.
+ * Rows of o and lse that belong to no sequence are left as they were.  What lies
+ * in other sequences' rows (a NaN, say) does not reach a sequence; a NaN or an
+ * infinity in v at token j of a sequence may reach the rows of earlier tokens in
+ * j's block of 128 keys, although the causal mask hides it from them.
+ */
+ATTN_API attn_status attn_varlen_fwd(const void* q, const void* k, const void* v,
+                                     long long q_token_stride, long long q_head_stride,
+                                     long long k_token_stride, long long k_head_stride,
+                                     long long v_token_stride, long long v_head_stride,
+                                     const void* plan, size_t plan_bytes, void* o, float* lse, int B,
+                                     int T, int H, int H_kv, int d, float scale, int causal,
+                                     cudaStream_t stream);
+
+/*
+ * Writes new rows into the cache: token cu_seqlens[b] + i goes to position
+ * starts[b] + i of sequence b.  For every page and head the new rows fall into,
+ * with a the largest |x| of their finite elements:
+ *   a page whose first row is among them takes scale s = a / 127 (FP32);
+ *   a page begun earlier takes s = max(its scale, a / 127), and where that is
+ *   larger than before, the rows it holds become rint(c * s_old / s).
+ * New codes are rint(x / s), all clamped to [-127, 127], with rint half to even
+ * of the exact quotient (s = 0: codes 0; NaN: 0; an infinity: +-127).  Rows of a
+ * page behind the new ones are left as they were.
+ *   k, v   : [T,H_kv,d] BF16, with the given strides.
+ *   starts : int32 [B], device: positions each sequence holds already.
+ * The pages that one call writes must be distinct: a page shared by two
+ * sequences is copied before either writes to it.
+ */
+ATTN_API attn_status attn_cache_append_int8(const void* k, const void* v, long long k_token_stride,
+                                            long long k_head_stride, long long v_token_stride,
+                                            long long v_head_stride, void* k_cache, void* v_cache,
+                                            float* k_scale, float* v_scale, const int* block_table,
+                                            const int* cu_seqlens, const int* starts, int B, int T,
+                                            int H_kv, int d, int num_pages, int page_size,
+                                            int max_blocks, cudaStream_t stream);
+
+/*
+ * Reads ranges of positions back as values code * scale: packed token
+ * cu_seqlens[b] + i of the outputs is position starts[b] + i of sequence b.
+ *   k, v : [T,H_kv,d] of type dt (FP32, or BF16 rounded to nearest even),
+ *          contiguous, written; cu_seqlens[0] = 0, cu_seqlens[B] = T.  Tokens
+ *          outside the sequences or without a valid page become 0 and are
+ *          reported by attn_check_status().
+ */
+ATTN_API attn_status attn_cache_read_int8(const void* k_cache, const void* v_cache,
+                                          const float* k_scale, const float* v_scale,
+                                          const int* block_table, const int* cu_seqlens,
+                                          const int* starts, void* k, void* v, int B, int T, int H_kv,
+                                          int d, int num_pages, int page_size, int max_blocks,
+                                          attn_dtype dt, cudaStream_t stream);
+
+/* Bytes of device workspace attn_decode_int8 needs (0 also on invalid arguments). */
+ATTN_API size_t attn_decode_int8_workspace_bytes(int B, int n_q, int H, int H_kv, int d,
+                                                 int page_size, int max_blocks);
+
+/*
+ * Attention of the newest n_q tokens of every sequence over the cache: token i of
+ * them sees positions j <= seqlens[b] - n_q + i.  With ck, cv the codes and ks, vs
+ * the scales of position j's page and the query head's key head,
+ * O = sum_j softmax_j(scale q . (ck_j ks_j)) (cv_j vs_j), LSE = ln sum_j exp.
+ * A row that sees no position (seqlens[b] < n_q - i) gets O = 0, LSE = -inf.
+ *   q       : [B,n_q,H,d] BF16, with the given strides; 1 <= n_q <= 256.
+ *   seqlens : int32 [B], device: positions each sequence holds, the newest n_q
+ *             tokens' among them; at most max_blocks * page_size.
+ *   o       : [B,n_q,H,d] BF16, contiguous.   lse : [B,n_q,H] FP32.
+ *   workspace : device buffer, 256-byte aligned, that no concurrently running call
+ *             uses (also not the replay of another graph); needs no initialisation.
+ * Softmax weights keep 11 bits down to 2^-29 of the row's largest; below that they
+ * are rounded to multiples of 2^-40 of it.
+ * Scales must be >= 0 and finite.  A position whose page number is out of range
+ * is not seen.
+ */
+ATTN_API attn_status attn_decode_int8(const void* q, long long q_batch_stride,
+                                      long long q_token_stride, long long q_head_stride,
+                                      const void* k_cache, const void* v_cache, const float* k_scale,
+                                      const float* v_scale, const int* block_table,
+                                      const int* seqlens, void* o, float* lse, int B, int n_q, int H,
+                                      int H_kv, int d, int num_pages, int page_size, int max_blocks,
+                                      float scale, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,9 @@ name; all arithmetic runs in the library's CUDA kernels.  There is no CPU
 fallback: if the library is missing or a call fails, an exception is raised.
 
 Tensors are [B, H, N, d], contiguous, on the current CUDA device, either all
-torch.bfloat16 (tensor-core path) or all torch.float32 (reference mode).
+torch.bfloat16 (tensor-core path) or all torch.float32 (reference mode).  The
+serving calls at the end (packed sequences, paged INT8 cache) state their own
+layouts.
 """
 from __future__ import annotations
 
@@ -25,7 +27,10 @@ EXPORTED = ("attn_version", "attn_status_string", "attn_last_error", "attn_fwd",
             "attn_bwd_workspace_bytes", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main",
             "attn_bwd_dq_convert", "attn_check_status", "attn_selftest_wait_timeout",
             "attn_bwd_noalloc", "attn_fwd_stable", "attn_quantize_int8", "attn_fwd_int8",
-            "attn_quantize_int8_as_bf16", "attn_fwd_int8_as_bf16")
+            "attn_quantize_int8_as_bf16", "attn_fwd_int8_as_bf16",
+            "attn_varlen_plan_bytes", "attn_varlen_plan", "attn_varlen_fwd",
+            "attn_cache_append_int8", "attn_cache_read_int8",
+            "attn_decode_int8_workspace_bytes", "attn_decode_int8")
 
 
 class AttnError(RuntimeError):
@@ -37,6 +42,7 @@ class AttnError(RuntimeError):
 
 _LIB = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 _SIGNATURES = {
     "attn_version": (_i, []),
@@ -56,6 +62,13 @@ _SIGNATURES = {
     "attn_fwd_int8": (_i, [_vp] * 7 + [_i, _i, _i, _i, _f, _i, _vp]),
     "attn_quantize_int8_as_bf16": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp]),
     "attn_fwd_int8_as_bf16": (_i, [_vp] * 7 + [_i, _i, _i, _i, _f, _i, _vp]),
+    "attn_varlen_plan_bytes": (_sz, [_i] * 4),
+    "attn_varlen_plan": (_i, [_vp] + [_i] * 5 + [_vp, _sz, _vp]),
+    "attn_varlen_fwd": (_i, [_vp] * 3 + [_ll] * 6 + [_vp, _sz, _vp, _vp] + [_i] * 5 + [_f, _i, _vp]),
+    "attn_cache_append_int8": (_i, [_vp] * 2 + [_ll] * 4 + [_vp] * 7 + [_i] * 7 + [_vp]),
+    "attn_cache_read_int8": (_i, [_vp] * 9 + [_i] * 8 + [_vp]),
+    "attn_decode_int8_workspace_bytes": (_sz, [_i] * 7),
+    "attn_decode_int8": (_i, [_vp] + [_ll] * 3 + [_vp] * 8 + [_i] * 8 + [_f, _vp, _sz, _vp]),
 }
 
 
@@ -338,3 +351,188 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, scale=None, causal=False, 
           lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, N, d,
           _default_scale(d, scale), int(bool(causal)), _stream(stream))
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# Serving: packed sequences, grouped heads, the paged INT8 cache
+# ---------------------------------------------------------------------------
+# include/attn.h states the layouts.  A cache is the five tensors (k_cache,
+# v_cache, k_scale, v_scale, block_table).  Tensors on another device than the
+# current one are refused by the library.
+
+def _check_rows(name, t, shape):
+    """A BF16 CUDA tensor of this shape whose rows of d elements are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows (last stride 1)")
+
+
+def _check_packed_rows(name, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [T, heads, d]")
+    _check_rows(name, t, t.shape)
+
+
+def _check_dense(name, t, shape, dtype):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _check_ints(name, t, n=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if (not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
+            or (n is not None and t.shape[0] != n)):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor" + (f" [{n}]" if n is not None else ""))
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table):
+    """Shape of the cache: (B, pages, H_kv, page_size, d, max_blocks)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a tensor [pages, H_kv, page_size, d]")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [B, max_blocks]")
+    pages, hk, page, d = k_cache.shape
+    _check_dense("k_cache", k_cache, k_cache.shape, torch.int8)
+    _check_dense("v_cache", v_cache, k_cache.shape, torch.int8)
+    _check_dense("k_scale", k_scale, (pages, hk), torch.float32)
+    _check_dense("v_scale", v_scale, (pages, hk), torch.float32)
+    _check_dense("block_table", block_table, block_table.shape, torch.int32)
+    return block_table.shape[0], pages, hk, page, d, block_table.shape[1]
+
+
+def attn_varlen_plan_bytes(B: int, T: int, H: int, H_kv: int) -> int:
+    return int(load_library().attn_varlen_plan_bytes(B, T, H, H_kv))
+
+
+def attn_varlen_plan(cu_seqlens, T, H, H_kv, causal=True, plan=None, stream=None):
+    """The work list of attn_varlen_fwd for a packed batch: cu_seqlens int32 [B+1] on
+    the device.  Returns a uint8 tensor that serves every call on the same batch."""
+    _check_ints("cu_seqlens", cu_seqlens)
+    B = cu_seqlens.shape[0] - 1
+    if plan is None:
+        plan = torch.empty(max(attn_varlen_plan_bytes(B, T, H, H_kv), 1), dtype=torch.uint8,
+                           device=cu_seqlens.device)
+    _call("attn_varlen_plan", cu_seqlens.data_ptr(), B, T, H, H_kv, int(bool(causal)), plan.data_ptr(),
+          _nbytes(plan), _stream(stream))
+    return plan
+
+
+def _plan_batch(plan, T, H, H_kv):
+    """Sequences a plan of this size has room for (its buffer grows by 16 bytes each)."""
+    if not isinstance(plan, torch.Tensor) or not plan.is_cuda or not plan.is_contiguous():
+        raise ValueError("plan must be a tensor made by attn_varlen_plan")
+    B = (_nbytes(plan) - 256) // 16 - T // (2 * (128 // max(1, min(128, H // H_kv))))
+    if B < 1:
+        raise ValueError("plan is too small for this T, H and H_kv")
+    return B
+
+
+def attn_varlen_fwd(q, k, v, plan, scale=None, causal=True, o=None, lse=None, stream=None):
+    """Attention over packed prompts: q [T,H,d], k, v [T,H_kv,d] BF16 (rows contiguous,
+    token and head strides free), plan of attn_varlen_plan.  Returns (o [T,H,d], lse [T,H]);
+    rows that belong to no sequence are left as they are."""
+    _check_packed_rows("q", q)
+    _check_packed_rows("k", k)
+    T, H, d = q.shape
+    hk = k.shape[1]
+    _check_rows("k", k, (T, hk, d))
+    _check_rows("v", v, (T, hk, d))
+    if hk < 1 or H < 1 or H % hk:
+        raise ValueError(f"H = {H} is not a multiple of H_kv = {hk}")
+    if o is None:
+        o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    else:
+        _check_dense("o", o, (T, H, d), torch.bfloat16)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    else:
+        _check_dense("lse", lse, (T, H), torch.float32)
+    B = _plan_batch(plan, T, H, hk)
+    _call("attn_varlen_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), q.stride(1),
+          k.stride(0), k.stride(1), v.stride(0), v.stride(1), plan.data_ptr(), _nbytes(plan),
+          o.data_ptr(), lse.data_ptr(), B, T, H, hk, d, _default_scale(d, scale), int(bool(causal)),
+          _stream(stream))
+    return o, lse
+
+
+def attn_cache_append_int8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, starts,
+                           stream=None):
+    """Write the packed rows k, v [T,H_kv,d] BF16 behind the starts[b] positions that every
+    sequence holds (see include/attn.h for the scales' rule).  Returns (k_cache, v_cache)."""
+    B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    _check_packed_rows("k", k)
+    T = k.shape[0]
+    _check_rows("k", k, (T, hk, d))
+    _check_rows("v", v, (T, hk, d))
+    _check_ints("cu_seqlens", cu_seqlens, B + 1)
+    _check_ints("starts", starts, B)
+    _call("attn_cache_append_int8", k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0),
+          v.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+          block_table.data_ptr(), cu_seqlens.data_ptr(), starts.data_ptr(), B, T, hk, d, pages, page,
+          blocks, _stream(stream))
+    return k_cache, v_cache
+
+
+def attn_cache_read_int8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, starts, T,
+                         dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """Values of positions starts[b] .. of every sequence, packed as cu_seqlens says (T tokens in
+    all), in dtype bfloat16 or float32.  Returns (k, v) [T,H_kv,d]."""
+    B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    _check_ints("cu_seqlens", cu_seqlens, B + 1)
+    _check_ints("starts", starts, B)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+    if k is None:
+        k = torch.empty((T, hk, d), dtype=dtype, device=k_cache.device)
+    else:
+        _check_dense("k", k, (T, hk, d), dtype)
+    if v is None:
+        v = torch.empty((T, hk, d), dtype=dtype, device=k_cache.device)
+    else:
+        _check_dense("v", v, (T, hk, d), dtype)
+    _call("attn_cache_read_int8", k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), starts.data_ptr(),
+          k.data_ptr(), v.data_ptr(), B, T, hk, d, pages, page, blocks, _dtype_code(k), _stream(stream))
+    return k, v
+
+
+def attn_decode_int8_workspace_bytes(B: int, n_q: int, H: int, H_kv: int, d: int, page_size: int,
+                                     max_blocks: int) -> int:
+    return int(load_library().attn_decode_int8_workspace_bytes(B, n_q, H, H_kv, d, page_size, max_blocks))
+
+
+def attn_decode_int8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, scale=None, o=None,
+                     lse=None, workspace=None, stream=None):
+    """Attention of the newest n_q tokens q [B,n_q,H,d] BF16 over the cache; seqlens int32 [B]
+    counts them in.  Returns (o [B,n_q,H,d], lse [B,n_q,H])."""
+    B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a tensor [B, n_q, H, d]")
+    n_q, H = q.shape[1], q.shape[2]
+    _check_rows("q", q, (B, n_q, H, d))
+    _check_ints("seqlens", seqlens, B)
+    if o is None:
+        o = torch.empty((B, n_q, H, d), dtype=q.dtype, device=q.device)
+    else:
+        _check_dense("o", o, (B, n_q, H, d), torch.bfloat16)
+    if lse is None:
+        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
+    else:
+        _check_dense("lse", lse, (B, n_q, H), torch.float32)
+    if workspace is None:
+        need = attn_decode_int8_workspace_bytes(B, n_q, H, hk, d, page, blocks)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    _call("attn_decode_int8", q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+          seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, n_q, H, hk, d, pages, page, blocks,
+          _default_scale(d, scale), workspace.data_ptr(), _nbytes(workspace), _stream(stream))
+    return o, lse

@@ -19,6 +19,14 @@ namespace {
 
 thread_local std::string t_last_error;
 
+attn_status cuda_fail(cudaError_t err, const char* what) {
+  return fail(ATTN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
+}
+
+}  // namespace
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
 attn_status fail(attn_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -28,14 +36,6 @@ attn_status fail(attn_status s, const char* fmt, ...) {
   t_last_error = buf;
   return s;
 }
-
-attn_status cuda_fail(cudaError_t err, const char* what) {
-  return fail(ATTN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
-}
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-}  // namespace
 
 // Shape and scalar checks shared by every entry point.
 attn_status check_problem(int B, int H, int N, int d, attn_dtype dt, float scale, bool need_scale,
@@ -63,14 +63,12 @@ attn_status check_problem(int B, int H, int N, int d, attn_dtype dt, float scale
   return ATTN_OK;
 }
 
-namespace {
-
-// Pointer must be non-null, 16-byte aligned and reachable from the current
-// device (device memory of this device, or managed memory).
-attn_status check_ptr(const void* p, const char* name) {
+// Pointer must be non-null, aligned and reachable from the current device
+// (device memory of this device, or managed memory).
+attn_status check_ptr(const void* p, const char* name, unsigned align) {
   if (p == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) & 15u)
-    return fail(ATTN_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  if (reinterpret_cast<uintptr_t>(p) & (align - 1u))
+    return fail(ATTN_ERR_INVALID_ARG, "%s is not %u-byte aligned", name, align);
   cudaPointerAttributes attr;
   cudaError_t err = cudaPointerGetAttributes(&attr, p);
   if (err != cudaSuccess) {
@@ -88,11 +86,7 @@ attn_status check_ptr(const void* p, const char* name) {
   return ATTN_OK;
 }
 
-#define ATTN_CHECK(expr)          \
-  do {                            \
-    attn_status _s = (expr);      \
-    if (_s != ATTN_OK) return _s; \
-  } while (0)
+namespace {
 
 // One-block kernel that waits on a barrier nobody arrives at, with a limit.
 __global__ void wait_selftest_kernel(unsigned long long limit_ns) {
@@ -199,13 +193,13 @@ attn_status check_workspace(const Problem& p, void* workspace, size_t bytes) {
   return check_ptr(workspace, "workspace");
 }
 
+}  // namespace
+
 attn_status launched(cudaError_t err, const char* what) {
   if (err != cudaSuccess) return cuda_fail(err, what);
   t_last_error.clear();
   return ATTN_OK;
 }
-
-}  // namespace
 
 }  // namespace attn
 
@@ -410,17 +404,26 @@ attn_status attn_bwd(const void* q, const void* k, const void* v, const void* o,
 attn_status attn_check_status(cudaStream_t stream) {
   cudaError_t err = cudaStreamSynchronize(stream);
   if (err != cudaSuccess) return cuda_fail(err, "attn_check_status: stream");
-  unsigned int a = 0, b = 0, c = 0;
+  // Every word is read and cleared before any is reported.
+  unsigned int a = 0, b = 0, c = 0, prompt = 0, cache = 0, decode = 0;
   if ((err = read_and_clear_status_fwd(&a, stream)) != cudaSuccess ||
       (err = read_and_clear_status_bwd(&b, stream)) != cudaSuccess ||
-      (err = read_and_clear_status_misc(&c, stream)) != cudaSuccess)
+      (err = read_and_clear_status_misc(&c, stream)) != cudaSuccess ||
+      (err = read_and_clear_status_varlen(&prompt, stream)) != cudaSuccess ||
+      (err = read_and_clear_status_cache(&cache, stream)) != cudaSuccess ||
+      (err = read_and_clear_status_decode(&decode, stream)) != cudaSuccess)
     return cuda_fail(err, "attn_check_status: status read");
-  const unsigned int any = a | b | c;
-  if (any & ATTN_ERR_TIMEOUT)
-    return fail(ATTN_ERR_TIMEOUT, "a kernel gave up on a bounded wait (status %u/%u/%u)", a, b, c);
+  const unsigned int any = a | b | c, serving = prompt | cache | decode;
+  if ((any | serving) & ATTN_ERR_TIMEOUT)
+    return fail(ATTN_ERR_TIMEOUT, "a kernel gave up on a bounded wait (status %u/%u/%u/%u/%u/%u)", a,
+                b, c, prompt, cache, decode);
   if (any != 0)
     return fail(ATTN_ERR_INVALID_ARG, "a kernel reported a bad launch setup (status %u/%u/%u)", a,
                 b, c);
+  if (serving != 0)
+    return fail(ATTN_ERR_INVALID_ARG,
+                "a kernel met a length, page number or plan out of range in device memory (varlen %u, "
+                "cache %u, decode %u)", prompt, cache, decode);
   t_last_error.clear();
   return ATTN_OK;
 }

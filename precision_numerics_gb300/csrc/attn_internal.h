@@ -93,15 +93,67 @@ cudaError_t launch_fwd_int8_as_bf16(const Problem& p, const void* qc, const floa
                                     const void* kc, const float* ks, const void* v, void* o,
                                     float* lse, cudaStream_t stream);
 
+// Paged INT8 cache: codes [P, Hkv, page, d], one FP32 scale per page and head
+// [P, Hkv], and the pages of B sequences [B, max_blocks].
+struct PagedCache {
+  const void *k, *v;
+  const float *k_scale, *v_scale;
+  const int* table;
+  int B, Hkv, d, P, page, max_blocks;
+};
+// Base-2 logarithm of a page size (16, 32, 64 or 128).
+inline int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+// strides: token and head stride of the K rows, then of the V rows (elements).
+cudaError_t launch_cache_append_int8(const PagedCache& c, const void* k, const void* v,
+                                     const long long* strides, const int* cu, const int* starts,
+                                     int T, cudaStream_t stream);
+cudaError_t launch_cache_read_int8(const PagedCache& c, const int* cu, const int* starts, void* k,
+                                   void* v, int T, bool fp32, cudaStream_t stream);
+// strides: batch, token and head stride of q (elements).
+size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H);
+cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides,
+                               const int* lens, void* o, float* lse, int n_q, int H, float scale,
+                               void* workspace, cudaStream_t stream);
+
+// Attention over packed sequences (csrc/fwd_varlen.cu).
+struct VarlenProblem {
+  int B, T, H, Hkv, d, causal;
+  float scale;
+};
+size_t varlen_plan_bytes(int B, int T, int H, int Hkv);
+cudaError_t launch_varlen_plan(const VarlenProblem& p, const int* cu, void* plan, cudaStream_t stream);
+// strides: token and head stride of q, k, v and o (elements).
+cudaError_t launch_varlen_fwd(const VarlenProblem& p, const void* q, const void* k, const void* v,
+                              const void* plan, void* o, float* lse, const long long* strides,
+                              cudaStream_t stream);
+
 // Device status words (one per kernel translation unit): read and clear.
 cudaError_t read_and_clear_status_fwd(unsigned int* out, cudaStream_t stream);
 cudaError_t read_and_clear_status_bwd(unsigned int* out, cudaStream_t stream);
 cudaError_t read_and_clear_status_misc(unsigned int* out, cudaStream_t stream);
+cudaError_t read_and_clear_status_varlen(unsigned int* out, cudaStream_t stream);
+cudaError_t read_and_clear_status_cache(unsigned int* out, cudaStream_t stream);
+cudaError_t read_and_clear_status_decode(unsigned int* out, cudaStream_t stream);
 
 // Shape and scalar checks shared by every entry point (d, N, B*H*N*d, dtype,
 // and the scale when need_scale); fills *out and records the error detail.
 attn_status check_problem(int B, int H, int N, int d, attn_dtype dt, float scale, bool need_scale,
                           Problem* out);
+
+// Helpers of the entry points.  fail() records the detail text and returns its
+// status; check_ptr() refuses a pointer that is NULL, not `align`-byte aligned or
+// not device memory of the current device; launched() maps a launch's result.
+attn_status fail(attn_status s, const char* fmt, ...);
+attn_status check_ptr(const void* p, const char* name, unsigned align = 16);
+attn_status launched(cudaError_t err, const char* what);
+size_t align256(size_t x);
+
+#define ATTN_CHECK(expr)          \
+  do {                            \
+    attn_status _s = (expr);      \
+    if (_s != ATTN_OK) return _s; \
+  } while (0)
 
 // Record the detail text returned by attn_last_error() on this thread.
 void set_last_error(const char* msg);

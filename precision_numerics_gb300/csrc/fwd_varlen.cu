@@ -1,0 +1,658 @@
+// BF16 attention over packed sequences with grouped heads, for sm_103a.
+//
+// What is computed, for token i of a sequence, query head h and key head
+// h / G (G = H / Hkv): O = sum_j softmax_j(scale q_i . k_j) v_j and the natural-
+// log LSE, j over the sequence's own keys (causal: j <= i).  The softmax is the
+// blockwise one of fwd_bf16.cu (FP32 statistics, P rounded to BF16 as the P V
+// operand only), with the same roles of the warps, barriers and TMEM columns;
+// that file's head gives them.  What differs:
+//
+//  - A 128-row query tile holds tq = 128 / G tokens of all G heads of one key
+//    head: row r is token r / G, head r % G, which one TMA box of tq tokens x G
+//    heads x 64 columns lays out directly.  The rows of a tile share their keys,
+//    so short sequences fill a tile G times better than with a tile per head.
+//    Where G does not divide 128 the last rows of a tile are idle.
+//  - The work items (2 tq tokens of one sequence, for every key head) are listed
+//    by a plan kernel, heaviest first, from the sequences' lengths in device
+//    memory; the plan serves every call on the same packed batch.
+//  - A key tile that runs past its sequence's end holds rows of the next
+//    sequence.  Their scores are masked; their V rows, which P = 0 would turn
+//    into NaN if they held an infinity or a NaN, are overwritten with zeros by
+//    the MMA warp before the P V product reads the tile (only in such tiles).
+//  - Output rows are written from registers, since a tile's last tokens may
+//    belong to the next sequence's tile.
+//
+// Bound, as in fwd_bf16.cu, by the softmax and its hand-over to the tensor pipe
+// for long sequences, and by the latency of an item's chain for short ones.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attn_internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+
+static __device__ unsigned int g_status_varlen;
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRegsWG0 = 80, kRegsCorr = 80, kRegsSoftmax = 176;
+static_assert(kRegsWG0 + kRegsCorr + 2 * kRegsSoftmax <= 512, "setmaxnreg split exceeds the launch pool");
+static_assert(kRegsWG0 <= 128 && kRegsCorr <= 128 && kRegsSoftmax >= 128, "setmaxnreg directions");
+
+__device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_varlen, code); }
+
+// ---------------------------------------------------------------------------
+// Plan: a header of 64 words, then one item per 2 tq tokens of a sequence.
+// ---------------------------------------------------------------------------
+constexpr int kPlanMagic = 0x564c504e;
+constexpr int kPlanHeader = 64;  // words
+struct PlanItem {
+  int first, len, q0, pad;  // sequence's first packed token and length; item's first token in it
+};
+static_assert(sizeof(PlanItem) == 16, "one 16-byte load per item");
+
+inline int tile_tokens(int H, int Hkv) { return kBlockM / (H / Hkv); }
+inline long long plan_capacity(int B, int T, int H, int Hkv) { return (long long)T / (2 * tile_tokens(H, Hkv)) + B; }
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBins = 1024;
+
+// One CTA: counts the items by their number of key tiles (kPlanBins classes,
+// heaviest first), then writes each into its class's range.  The order within
+// a class is that of the atomics; no result depends on it.
+__global__ void __launch_bounds__(kPlanThreads)
+    varlen_plan_kernel(const int* __restrict__ cu, int* __restrict__ plan, int B, int T, int G, int Hkv, int tq,
+                       int causal, int capacity) {
+  __shared__ int s_count[kPlanBins], s_warp[32], s_max;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  s_count[tid] = 0;
+  if (tid == 0) s_max = 1;
+  __syncthreads();
+  int longest = 0;
+  for (int b = tid; b < B; b += kPlanThreads) {
+    const int x = __ldcg(cu + b), y = __ldcg(cu + b + 1);
+    if (x < 0 || y < x || y > T) set_fail(ATTN_ERR_INVALID_ARG);
+    const int first = min(max(x, 0), T);
+    longest = max(longest, min(max(y, first), T) - first);
+  }
+  atomicMax(&s_max, (longest + kBlockN - 1) / kBlockN);
+  __syncthreads();
+  const int most = s_max;
+  auto each = [&](auto&& put) {
+    for (int b = warp; b < B; b += kPlanThreads / 32) {
+      const int first = min(max(__ldcg(cu + b), 0), T);
+      const int len = min(max(__ldcg(cu + b + 1), first), T) - first;
+      const int n = (len + 2 * tq - 1) / (2 * tq);
+      for (int i = lane; i < n; i += 32) {
+        const int q0 = i * 2 * tq;
+        const int keys = causal ? min(q0 + 2 * tq, len) : len;
+        const int tiles = (keys + kBlockN - 1) / kBlockN;
+        put(kPlanBins - 1 - (int)((long long)(tiles - 1) * kPlanBins / most), first, len, q0);
+      }
+    }
+  };
+  each([&](int bin, int, int, int) { atomicAdd(&s_count[bin], 1); });
+  __syncthreads();
+  const int mine = s_count[tid];
+  int upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += y;
+  }
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += s_warp[w];
+  s_count[tid] = upto - mine;
+  if (tid == kPlanThreads - 1) {
+    plan[0] = kPlanMagic;
+    plan[1] = T;
+    plan[2] = G;
+    plan[3] = Hkv;
+    plan[4] = causal;
+    plan[5] = min(upto, capacity);  // more than the capacity only for cu_seqlens that run backwards
+  }
+  __syncthreads();
+  PlanItem* items = reinterpret_cast<PlanItem*>(plan + kPlanHeader);
+  each([&](int bin, int first, int len, int q0) {
+    const int at = atomicAdd(&s_count[bin], 1);
+    if (at < capacity) items[at] = PlanItem{first, len, q0, 0};
+  });
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+template <int D>
+struct Cfg {
+  static constexpr int kStages = (D == 128) ? 2 : 3;
+  static constexpr int kChunks = D / 64;          // 64-column (128-byte) chunks per row
+  static constexpr int kChunkBytes = 128 * 128;   // 128 rows x 128 bytes
+  static constexpr int kTileBytes = 128 * D * 2;  // 128 rows x d BF16
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+  // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S],
+  // s_full[2], p_full[2], o_done[2], mma_final, alpha[2][4]
+  static constexpr int kNumBars = 2 + 4 * kStages + 15;
+  static constexpr int kOffAlpha = kOffBar + kNumBars * 8 + 16;  // FP32 [2][128]
+  static constexpr int kSmemBytes = kOffAlpha + 2 * 128 * 4;
+  static constexpr uint32_t kTmemCols = 512;
+  static __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
+  static __device__ __forceinline__ uint32_t col_o(int t) { return 256u + D * t; }
+};
+
+// Item of round r for this CTA: the list is dealt in snake order (CTA c takes
+// item c of round 0, item G-1-c of round 1, ...), so that heavy and light items
+// even out.  -1 once the list is done.
+__device__ __forceinline__ int item_of(int r, int total) {
+  const long long n = gridDim.x;
+  const long long c = (r & 1) ? (n - 1 - (long long)blockIdx.x) : (long long)blockIdx.x;
+  const long long idx = (long long)r * n + c;
+  return idx < total ? (int)idx : -1;
+}
+
+// q0: first token (in the sequence) of tile 0; n: key tiles of the two tiles.
+struct Item {
+  int first, len, head, q0, n[2], nmax;
+};
+template <bool CAUSAL>
+__device__ __forceinline__ Item load_item(const int* __restrict__ plan, int L, int Hkv, int tq) {
+  const int4 p = __ldcg(reinterpret_cast<const int4*>(plan + kPlanHeader) + L / Hkv);
+  Item it;
+  it.first = p.x;
+  it.len = p.y;
+  it.q0 = p.z;
+  it.head = L % Hkv;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int q = it.q0 + t * tq;
+    const int keys = CAUSAL ? min(q + tq, it.len) : it.len;
+    it.n[t] = q >= it.len ? 0 : (keys + kBlockN - 1) / kBlockN;
+  }
+  it.nmax = max(it.n[0], it.n[1]);
+  return it;
+}
+// Rows of key tile j that belong to the sequence.
+__device__ __forceinline__ int tile_keys(const Item& it, int j) { return min(kBlockN, it.len - j * kBlockN); }
+
+template <int D, bool CAUSAL>
+__global__ void __launch_bounds__(kThreads, 1)
+    varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const int* __restrict__ plan,
+                      uint16_t* __restrict__ out, float* __restrict__ lse, int T, int H, int Hkv, int G, int tq,
+                      int capacity, float scale, float scale_log2) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* bar_q = bars;
+  uint64_t* bar_qempty = bars + 1;
+  uint64_t* bar_kfull = bars + 2;
+  uint64_t* bar_kempty = bar_kfull + C::kStages;
+  uint64_t* bar_vfull = bar_kempty + C::kStages;
+  uint64_t* bar_vempty = bar_vfull + C::kStages;
+  uint64_t* bar_sfull = bar_vempty + C::kStages;
+  uint64_t* bar_pfull = bar_sfull + 2;
+  uint64_t* bar_odone = bar_pfull + 2;
+  uint64_t* bar_final = bar_odone + 2;
+  uint64_t* bar_alpha = bar_final + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  float* s_alpha = reinterpret_cast<float*>(smem + C::kOffAlpha);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    *s_abort = (smem_u32(smem) & 1023u) != 0;
+    mbar_init(bar_q, 1);
+    mbar_init(bar_qempty, 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&bar_kfull[s], 1);
+      mbar_init(&bar_kempty[s], 1);
+      mbar_init(&bar_vfull[s], 1);
+      mbar_init(&bar_vempty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar_sfull[t], 1);
+      mbar_init(&bar_pfull[t], 256);  // softmax (P stored) + correction (O rescaled)
+      for (int q = 0; q < 4; ++q) mbar_init(&bar_alpha[t * 4 + q], 32);
+      mbar_init(&bar_odone[t], 1);
+    }
+    mbar_init(bar_final, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Set-up above touches no global memory; from here on the previous kernel's
+  // results must be complete and visible.
+  griddep_wait();
+  // The plan must be one for this call: anything else is reported and nothing
+  // is computed, so that no item can reach outside the tensors.
+  const bool plan_ok = __ldcg(plan) == kPlanMagic && __ldcg(plan + 1) == T && __ldcg(plan + 2) == G &&
+                       __ldcg(plan + 3) == Hkv && __ldcg(plan + 4) == (CAUSAL ? 1 : 0) &&
+                       __ldcg(plan + 5) >= 0 && __ldcg(plan + 5) <= capacity;
+  const bool abort_all = *s_abort != 0 || !plan_ok;
+  const int total = plan_ok ? __ldcg(plan + 5) * Hkv : 0;
+  if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
+
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+
+  // Barrier phases run on across items: every role counts the completions it
+  // has consumed (K/V ring position g, items, S and P tiles per query tile).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWG0));
+    if (warp == 0 && lane == 0 && !abort_all) {
+      // ------------------------------------------------------------ producer
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      const uint32_t q_bytes = 128u * G * tq;  // one chunk of a query tile
+      bool ok = true;
+      int g = 0, items = 0, issued_k = 0, issued_v = 0;
+      for (int r = 0; ok; ++r) {
+        const int L = item_of(r, total);
+        if (L < 0) break;
+        const Item it = load_item<CAUSAL>(plan, L, Hkv, tq);
+        // The Q slots are free once the previous item's last S products have run.
+        if (items > 0 && !mbar_wait(bar_qempty, (items - 1) & 1)) { ok = false; break; }
+        mbar_arrive_expect_tx(bar_q, 2 * C::kChunks * q_bytes);
+        for (int t = 0; t < 2; ++t)
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tmQ, bar_q, c * 64, it.head * G,
+                        it.first + it.q0 + t * tq);
+        ++items;
+        for (int j = 0; j < it.nmax; ++j, ++g) {
+          const int st = g % C::kStages;
+          const int use = g / C::kStages;
+          if (use > 0 && !mbar_wait(&bar_kempty[st], (use - 1) & 1)) { ok = false; break; }
+          mbar_arrive_expect_tx(&bar_kfull[st], C::kTileBytes);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(sK + st * C::kTileBytes + c * C::kChunkBytes, &tmK, &bar_kfull[st], c * 64,
+                        it.first + j * kBlockN, it.head);
+          issued_k = g + 1;
+          if (use > 0 && !mbar_wait(&bar_vempty[st], (use - 1) & 1)) { ok = false; break; }
+          mbar_arrive_expect_tx(&bar_vfull[st], C::kTileBytes);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(sV + st * C::kTileBytes + c * C::kChunkBytes, &tmV, &bar_vfull[st], c * 64,
+                        it.first + j * kBlockN, it.head);
+          issued_v = g + 1;
+        }
+      }
+      if (!ok) set_fail(ATTN_ERR_TIMEOUT);
+      // Do not leave while copies into this CTA's shared memory are in flight.
+      if (items > 0) mbar_wait(bar_q, (items - 1) & 1);
+      for (int x = max(0, issued_k - C::kStages); x < issued_k; ++x)
+        mbar_wait(&bar_kfull[x % C::kStages], (x / C::kStages) & 1);
+      for (int x = max(0, issued_v - C::kStages); x < issued_v; ++x)
+        mbar_wait(&bar_vfull[x % C::kStages], (x / C::kStages) & 1);
+    } else if (warp == 1 && !abort_all) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+      const uint64_t descQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t descK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t descV = sdesc_sw128(smem_u32(sV), C::kChunkBytes, 1024);
+      auto issue_s = [&](int t, int st) {
+        const uint64_t a0 = sdesc_add(descQ, t * C::kTileBytes);
+        const uint64_t b0 = sdesc_add(descK, st * C::kTileBytes);
+        const uint32_t d = tmem + C::col_s(t);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+          mma_ss_elect(d, sdesc_add(a0, off), sdesc_add(b0, off), idesc_qk, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int t, int st, bool acc) {
+        const uint64_t b0 = sdesc_add(descV, st * C::kTileBytes);
+        const uint32_t d = tmem + C::col_o(t), a = tmem + C::col_s(t);
+#pragma unroll
+        for (int kk = 0; kk < kBlockN / 16; ++kk)
+          mma_ts_elect(d, a + kk * 8, sdesc_add(b0, kk * 2048), idesc_pv, (acc || kk > 0) ? 1u : 0u);
+      };
+      bool ok = true;
+      int g = 0, items = 0;
+      int pc[2] = {0, 0};   // P tiles consumed per query tile (p_full phases)
+      for (int r = 0; ok; ++r) {
+        const int L = item_of(r, total);
+        if (L < 0) break;
+        const Item it = load_item<CAUSAL>(plan, L, Hkv, tq);
+        // S_t(0).  S_t's columns are free: the previous item's P_t V, issued
+        // earlier on this thread, reads P_t before these products run.
+        ok = warp_wait(bar_q, items & 1);
+        if (ok) ok = warp_wait(&bar_kfull[g % C::kStages], (g / C::kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t) {
+          if (it.n[t] == 0) continue;
+          issue_s(t, g % C::kStages);
+          mma_commit_elect(&bar_sfull[t]);
+        }
+        mma_commit_elect(&bar_kempty[g % C::kStages]);  // K is free once S(0) has completed
+        if (it.nmax == 1) mma_commit_elect(bar_qempty);  // every S product of the item issued
+        ++items;
+        for (int j = 0; j < it.nmax && ok; ++j) {
+          const int gj = g + j;
+          const int st = gj % C::kStages;
+          const int st1 = (gj + 1) % C::kStages;
+          const bool has_next = j + 1 < it.nmax;
+          if (!warp_wait(&bar_vfull[st], (gj / C::kStages) & 1)) { ok = false; break; }
+          // Rows past the sequence's end become zero while the softmax works on
+          // the tile's scores.  Rows are 128 bytes in every 64-column chunk; the
+          // swizzle moves units within a row only.
+          if (const int keys = tile_keys(it, j); keys < kBlockN) {
+            for (int c = 0; c < C::kChunks; ++c)
+              for (int i = keys * 8 + lane; i < kBlockN * 8; i += 32)
+                st_shared_v4(smem_u32(sV + st * C::kTileBytes + c * C::kChunkBytes + i * 16), 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (has_next && !warp_wait(&bar_kfull[st1], ((gj + 1) / C::kStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j >= it.n[t]) continue;
+            if (!warp_wait(&bar_pfull[t], (pc[t] + j) & 1)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv(t, st, j > 0);
+            if (j + 1 < it.n[t]) {
+              issue_s(t, st1);
+              mma_commit_elect(&bar_sfull[t]);
+            } else {
+              mma_commit_elect(&bar_odone[t]);
+            }
+          }
+          if (!ok) break;
+          mma_commit_elect(&bar_vempty[st]);
+          // Release K_{j+1} as soon as the S(j+1) products above have read it, so
+          // the producer can start loading K_{j+1+S} a full iteration ahead.
+          if (has_next) mma_commit_elect(&bar_kempty[st1]);
+          // The item's last S products were issued above: Q may be replaced.
+          if (j + 2 == it.nmax) mma_commit_elect(bar_qempty);
+        }
+        g += it.nmax;
+        pc[0] += it.n[0];
+        pc[1] += it.n[1];
+      }
+      if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
+      // Every MMA this warp issued completes before TMEM is released.
+      mma_commit_elect(bar_final);
+      mbar_wait(bar_final, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCorr));
+    // -------------------------------------------------------------- correction
+    // O_t(j-1) has completed when the softmax of tile t publishes alpha(j):
+    // that happens after S_t(j) completed, and the commit that signalled S_t(j)
+    // covers every earlier MMA, PV_t(j-1) included.
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    bool ok = !abort_all;
+    int ac[2] = {0, 0};  // alpha phases consumed per query tile
+    for (int rr = 0; ok; ++rr) {
+      const int L = item_of(rr, total);
+      if (L < 0) break;
+      const Item it = load_item<CAUSAL>(plan, L, Hkv, tq);
+      for (int j = 0; j < it.nmax && ok; ++j) {
+        for (int t = 0; t < 2; ++t) {
+          if (j >= it.n[t]) continue;
+          // Only the softmax warp that owns the same 32 TMEM lanes is waited for.
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar_alpha[t * 4 + (warp & 3)], (ac[t] + j) & 1));
+          if (!ok) break;
+          const float alpha = s_alpha[t * 128 + r];
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            tc_fence_after();
+            const uint32_t tO = tmem + lane_off + C::col_o(t);
+            const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float lo, hi;
+                f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2), lo, hi);
+                o[2 * i] = __float_as_uint(lo);
+                o[2 * i + 1] = __float_as_uint(hi);
+              }
+              tmem_st32(tO + c * 32, o);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          mbar_arrive(&bar_pfull[t]);
+        }
+      }
+      ac[0] += it.n[0];
+      ac[1] += it.n[1];
+    }
+    if (!ok && !abort_all) set_fail(ATTN_ERR_TIMEOUT);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // -------------------------------------------------------------- softmax
+    const int t = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;  // query row within the tile = TMEM lane
+    const int row_tok = r / G, row_head = r - row_tok * G;
+    const bool row_used = row_tok < tq;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::col_s(t);
+    const uint32_t tO = tmem + lane_off + C::col_o(t);
+    bool ok = !abort_all;
+    int sc = 0;  // S_t tiles consumed so far (s_full phases)
+    int oc = 0;  // items whose O_t was completed so far (o_done phases)
+    for (int rr = 0; ok; ++rr) {
+      const int L = item_of(rr, total);
+      if (L < 0) break;
+      const Item it = load_item<CAUSAL>(plan, L, Hkv, tq);
+      const int n = it.n[t];
+      const int q_first = it.q0 + t * tq;
+      const int tok = q_first + (row_used ? row_tok : 0);  // token within the sequence
+      const int limit = CAUSAL ? min(tok + 1, it.len) : it.len;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar_sfull[t], (sc + j) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+
+        const int kv0 = j * kBlockN;
+        if (kv0 + kBlockN > it.len || (CAUSAL && kv0 + kBlockN - 1 > q_first)) {
+          const int lim = limit - kv0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= lim) s[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+        }
+        // Row max as four independent chains of three-input maxima.
+        float mx4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float m = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+          for (int e = 2; e < 32; e += 2)
+            m = fmax3(m, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+          mx4[c] = m;
+        }
+        const float m_new = fmaxf(fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]), m_run);
+        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+        const float neg_ms = -m_use * scale_log2;
+        const float alpha = ex2((m_run - m_use) * scale_log2);
+        s_alpha[t * 128 + r] = alpha;
+        mbar_arrive(&bar_alpha[t * 4 + (warp & 3)]);  // the correction warp rescales O_t meanwhile
+        uint64_t sums2[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sums2[u] = 0ull;
+        const uint64_t c2 = f2_pack(scale_log2, scale_log2);
+        const uint64_t nm2 = f2_pack(neg_ms, neg_ms);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x0, x1;
+            f2_unpack(fma2(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), c2, nm2), x0, x1);
+            const float p0 = ex2(x0);
+            const float p1 = ex2(x1);
+            sums2[i & 3] = add2(sums2[i & 3], f2_pack(p0, p1));
+            pk[i] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tS + c * 16, pk);
+        }
+        float sums[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) f2_unpack(sums2[u], sums[2 * u], sums[2 * u + 1]);
+        const float tile_sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) +
+                               ((sums[4] + sums[5]) + (sums[6] + sums[7]));
+        l_run = l_run * alpha + tile_sum;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar_pfull[t]);
+        m_run = m_new;
+      }
+      sc += n;
+      if (!ok || n == 0) continue;
+      // ------------------------------------------------------------ epilogue
+      // O = O_acc / l and LSE = m * scale + ln(l).  The next item's first P V
+      // product, which overwrites O_t, waits for this warpgroup's next P, so it
+      // cannot run before O_t has been read here.
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar_odone[t], oc & 1));
+      if (!ok) break;
+      ++oc;
+      tc_fence_after();
+      const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+      const uint64_t il2 = f2_pack(inv_l, inv_l);
+      const bool have = row_used && tok < it.len;
+      const size_t row_at = (size_t)(it.first + tok) * H + it.head * G + row_head;
+      uint4* row = reinterpret_cast<uint4*>(out + row_at * D);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_wait_ld();
+        reg_fence(o);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float lo, hi;
+          f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il2), lo, hi);
+          pk[i] = pack_bf16x2(lo, hi);
+        }
+        if (have) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            row[c * 4 + u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        }
+      }
+      if (have) lse[row_at] = m_run * scale + logf(l_run);
+    }
+    if (!ok && !abort_all) set_fail(ATTN_ERR_TIMEOUT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// 3-D BF16 map of a [T, heads, d] tensor with strides in elements.  `rows`
+// first: (d, T, heads) with a 64 x n x 1 box (keys), else (d, heads, T) with a
+// 64 x G x n box (queries).
+bool make_tmap_packed(CUtensorMap* map, const void* base, int T, int heads, int d, long long token_stride,
+                      long long head_stride, bool keys, int G, int n) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t tok = (cuuint64_t)token_stride * 2, head = (cuuint64_t)head_stride * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)(keys ? T : heads), (cuuint64_t)(keys ? heads : T)};
+  const cuuint64_t strides[2] = {keys ? tok : head, keys ? head : tok};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(keys ? n : G), (cuuint32_t)(keys ? 1 : n)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool CAUSAL>
+cudaError_t launch_impl(const VarlenProblem& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                        const void* plan, void* o, float* lse, cudaStream_t stream) {
+  using C = Cfg<D>;
+  auto kernel = varlen_fwd_kernel<D, CAUSAL>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (err != cudaSuccess) return err;
+  const long long capacity = plan_capacity(p.B, p.T, p.H, p.Hkv);
+  // One CTA per SM (one fits); without an SM count, one per item.
+  const int sms = device_sm_count();
+  const long long most = capacity * p.Hkv;
+  const unsigned grid = (unsigned)(sms > 0 ? std::min<long long>(most, sms) : most);
+  return launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, mq, mk, mv,
+                    static_cast<const int*>(plan), static_cast<uint16_t*>(o), lse, p.T, p.H, p.Hkv, p.H / p.Hkv,
+                    tile_tokens(p.H, p.Hkv), (int)capacity, p.scale, p.scale * 1.4426950408889634f);
+}
+
+}  // namespace
+
+size_t varlen_plan_bytes(int B, int T, int H, int Hkv) {
+  return kPlanHeader * 4 + (size_t)plan_capacity(B, T, H, Hkv) * sizeof(PlanItem);
+}
+
+cudaError_t launch_varlen_plan(const VarlenProblem& p, const int* cu, void* plan, cudaStream_t stream) {
+  return launch_pdl(varlen_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, cu, static_cast<int*>(plan), p.B, p.T,
+                    p.H / p.Hkv, p.Hkv, tile_tokens(p.H, p.Hkv), p.causal,
+                    (int)plan_capacity(p.B, p.T, p.H, p.Hkv));
+}
+
+cudaError_t launch_varlen_fwd(const VarlenProblem& p, const void* q, const void* k, const void* v, const void* plan,
+                              void* o, float* lse, const long long* strides, cudaStream_t stream) {
+  CUtensorMap mq, mk, mv;
+  const int G = p.H / p.Hkv;
+  if (!make_tmap_packed(&mq, q, p.T, p.H, p.d, strides[0], strides[1], false, G, tile_tokens(p.H, p.Hkv)) ||
+      !make_tmap_packed(&mk, k, p.T, p.Hkv, p.d, strides[2], strides[3], true, G, kBlockN) ||
+      !make_tmap_packed(&mv, v, p.T, p.Hkv, p.d, strides[4], strides[5], true, G, kBlockN))
+    return cudaErrorInvalidValue;
+  if (p.d == 128)
+    return p.causal ? launch_impl<128, true>(p, mq, mk, mv, plan, o, lse, stream)
+                    : launch_impl<128, false>(p, mq, mk, mv, plan, o, lse, stream);
+  return p.causal ? launch_impl<64, true>(p, mq, mk, mv, plan, o, lse, stream)
+                  : launch_impl<64, false>(p, mq, mk, mv, plan, o, lse, stream);
+}
+
+cudaError_t read_and_clear_status_varlen(unsigned int* out, cudaStream_t stream) {
+  static const unsigned int zero = 0;
+  cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_status_varlen, sizeof(unsigned int), 0,
+                                              cudaMemcpyDeviceToHost, stream);
+  if (err != cudaSuccess) return err;
+  err = cudaStreamSynchronize(stream);
+  if (err != cudaSuccess) return err;
+  err = cudaMemcpyToSymbolAsync(g_status_varlen, &zero, sizeof(unsigned int), 0,
+                                cudaMemcpyHostToDevice, stream);
+  if (err != cudaSuccess) return err;
+  return cudaStreamSynchronize(stream);
+}
+
+}  // namespace attn
