@@ -25,7 +25,15 @@
 // Each warp streams its own 32-position tiles of K and V by TMA through its own
 // ring (no barrier is shared between warps), with its own running maximum,
 // sum and accumulator; the four warps of a CTA take every fourth tile and are
-// merged through shared memory once at the end of a (sequence, key head).
+// merged through shared memory once at the end of a segment, the tiles of one
+// (sequence, key head, row block) that the CTA has.
+//
+// Where a sequence can be longer than kWholeTiles tiles, the tiles of all
+// segments, one behind the other, are dealt to the CTAs in equal runs, so that
+// ragged lengths and few sequences keep every SM busy alike.  A run that holds a
+// whole segment writes its output; of a segment that runs on into the next
+// CTAs' runs every part leaves (m, l, unnormalised O) in the workspace, two slots
+// a CTA at most, and decode_join_kernel joins them in the order of the CTAs.
 #include <math.h>
 #include <stdint.h>
 
@@ -44,6 +52,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;   // positions per tile
 constexpr int kRows = 16;   // query rows (token, head of the group) per pass over the keys
+constexpr int kWholeTiles = 16;  // sequences up to this long are not split
+constexpr int kLeastRun = 4;     // tiles a CTA takes at least: one a warp
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_decode, code); }
 
@@ -117,6 +127,11 @@ __device__ __forceinline__ uint32_t unit_offset(uint32_t r, uint32_t u) {
   return D == 128 ? r * 128u + ((u ^ (r & 7u)) << 4) : r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
 }
 
+// Natural-log LSE from the base-2 maximum and the row sum, which carries 2^15.
+__device__ __forceinline__ float lse_of(float M, float L) {
+  return L > 0.f ? (M + log2f(L) - 15.f) * 0.69314718055994531f : -INFINITY;
+}
+
 struct Args {
   const uint16_t* q;
   long long q_batch, q_token, q_head;
@@ -126,7 +141,14 @@ struct Args {
   float* lse;
   int B, n_q, H, Hkv, G, P, page, page_shift, max_blocks, row_blocks;
   float scale_log2;
+  // Split mode (else null): parts [CTA][2], and what each CTA's last segment is.
+  float* parts;
+  int4* chains;
 };
+
+// A part in the workspace: O [16][D], m [16], l [16], FP32.
+template <int D>
+constexpr int part_floats() { return kRows * (D + 2); }
 
 __device__ __forceinline__ int length_of(const Args& a, int b) {
   const long long cap = (long long)a.max_blocks << a.page_shift;
@@ -138,20 +160,55 @@ __device__ __forceinline__ int length_of(const Args& a, int b) {
   return len;
 }
 
-// One segment: tiles [ta, tb) of (sequence b, key head h, row block rb).
-struct Segment {
+__device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + kTile - 1) / kTile); }
+
+// A position in a CTA's run of tiles: tiles [ta, tb) of (sequence b, key head h,
+// row block rb), `left` tiles behind them.
+struct Walk {
   int b, h, rb, len, ta, tb;
+  long long left;
+  __device__ __forceinline__ int count(int warp) const {  // tiles of warp `warp`: ta + warp + kWarps * k
+    return tb > ta + warp ? (tb - ta - warp + kWarps - 1) / kWarps : 0;
+  }
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (left <= 0) return false;
+    if (++rb == a.row_blocks) {
+      rb = 0;
+      if (++h == a.Hkv) {
+        h = 0;
+        do {
+          if (++b >= a.B) return false;
+          len = length_of(a, b);
+        } while (len == 0);
+      }
+    }
+    ta = 0;
+    tb = (int)min((long long)tiles_of(len), left);
+    left -= tb;
+    return true;
+  }
 };
 
-// A warp's position in the list of its tiles: the next one is segment tile
-// ta + warp + kWarps * k.
-template <int D>
-struct Loader {
-  int k = 0;         // tiles of this segment issued so far
-  int base = 0;      // first tile of the page ids held by the lanes
-  int id0 = -1, id1 = -1;
-  uint32_t issued = 0;
-};
+// Sum over the CTA's threads before this one, and over all of them.
+__device__ __forceinline__ long long scan_before(long long x, long long* s_warp, long long& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long upto = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += s_warp[w];
+    all += s_warp[w];
+  }
+  return upto - x;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -181,71 +238,138 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_wait();
   if (!ok && threadIdx.x == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
-  Segment sg;
-  {
+  Walk sg;
+  long long per = 0, begin = 0, run = 0;  // tiles of a run; where this CTA's begins, its length
+  if (a.parts == nullptr) {
     const int x = blockIdx.x;
     sg.rb = x % a.row_blocks;
     sg.h = (x / a.row_blocks) % a.Hkv;
     sg.b = x / a.row_blocks / a.Hkv;
     sg.len = length_of(a, sg.b);
     sg.ta = 0;
-    sg.tb = (int)(((unsigned)sg.len + kTile - 1) / kTile);
+    sg.tb = tiles_of(sg.len);
+    sg.left = 0;
+  } else {
+    // All tiles, and the sequence in which this CTA's run begins.
+    long long* s_warp = reinterpret_cast<long long*>(s_merge);
+    const long long copies = (long long)a.Hkv * a.row_blocks;
+    long long total = 0, sum;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      scan_before(b < a.B ? tiles_of(length_of(a, b)) : 0, s_warp, sum);
+      total += sum;
+    }
+    total *= copies;
+    per = max((total + gridDim.x - 1) / gridDim.x, (long long)kLeastRun);
+    begin = per * blockIdx.x;
+    int4* s_start = reinterpret_cast<int4*>(s_m);
+    if (threadIdx.x == 0) s_start[0].x = -1;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B && before <= begin; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int len = b < a.B ? length_of(a, b) : 0;
+      const int tiles = tiles_of(len);
+      const long long at = before + copies * scan_before(tiles, s_warp, sum);
+      if (begin >= at && begin < at + copies * tiles) {
+        const long long rest = begin - at;
+        s_start[0] = make_int4(b, len, (int)(rest / tiles), (int)(rest % tiles));
+      }
+      before += copies * sum;
+    }
+    __syncthreads();
+    const int4 st = s_start[0];
+    __syncthreads();
+    if (threadIdx.x == 0) a.chains[blockIdx.x] = make_int4(0, 0, 0, 0);
+    // Sequences without a position have no tile: their rows are empty.
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      if (length_of(a, b) > 0) continue;
+      const size_t row = (size_t)b * a.n_q * a.H;
+      for (int i = threadIdx.x; i < a.n_q * a.H * (D / 8); i += kThreads)
+        reinterpret_cast<uint4*>(a.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) a.lse[row + i] = -INFINITY;
+    }
+    if (st.x < 0) return;  // more CTAs than runs
+    run = min(per, total - begin);
+    sg.b = st.x;
+    sg.len = st.y;
+    sg.h = st.z / a.row_blocks;
+    sg.rb = st.z % a.row_blocks;
+    sg.ta = st.w;
+    sg.left = run;
+    sg.tb = (int)min((long long)tiles_of(sg.len), sg.ta + sg.left);
+    sg.left -= sg.tb - sg.ta;
   }
 
   // ------------------------------------------------------------------ loads
-  Loader<D> ld;
-  auto look_up = [&](int k) {
-    // Lane l holds the pages of this warp's tile k + l.
-    const long long pos = ((long long)sg.ta + warp + (long long)kWarps * (k + lane)) * kTile;
-    ld.base = k;
-    ld.id0 = ld.id1 = -1;
-    if (pos < (long long)sg.tb * kTile && pos < sg.len) {
-      const int* row = a.table + (size_t)sg.b * a.max_blocks;
-      ld.id0 = __ldcg(row + (pos >> a.page_shift));
-      if (ld.id0 < 0 || ld.id0 >= a.P) {
+  // The loads run kStages tiles ahead, into the next segments too.
+  Walk lw = sg;
+  int ld_n = lw.count(warp);     // this warp's tiles of lw
+  int ld_k = 0;                  // those issued
+  int ld_base = 0;               // first tile whose page ids the lanes hold
+  int id0 = -1, id1 = -1;        // pages of the two halves of tile ld_base + lane
+  uint32_t issued = 0;
+  bool more = ok;
+  auto look_up = [&]() {
+    ld_base = ld_k;
+    id0 = id1 = -1;
+    const long long pos = ((long long)lw.ta + warp + (long long)kWarps * (ld_k + lane)) * kTile;
+    if (ld_k + lane < ld_n) {
+      const int* row = a.table + (size_t)lw.b * a.max_blocks;
+      id0 = __ldcg(row + (pos >> a.page_shift));
+      if (id0 < 0 || id0 >= a.P) {
         set_fail(ATTN_ERR_INVALID_ARG);
-        ld.id0 = -1;
+        id0 = -1;
       }
       if (a.page >= kTile) {
-        ld.id1 = ld.id0;
-      } else if (pos + 16 < sg.len) {
-        ld.id1 = __ldcg(row + ((pos + 16) >> a.page_shift));
-        if (ld.id1 < 0 || ld.id1 >= a.P) {
+        id1 = id0;
+      } else if (pos + 16 < lw.len) {
+        id1 = __ldcg(row + ((pos + 16) >> a.page_shift));
+        if (id1 < 0 || id1 >= a.P) {
           set_fail(ATTN_ERR_INVALID_ARG);
-          ld.id1 = -1;
+          id1 = -1;
         }
       }
     }
   };
   auto issue = [&]() {
-    if (ld.k - ld.base >= 32) look_up(ld.k);
-    const int p0 = __shfl_sync(0xffffffffu, ld.id0, ld.k - ld.base);
-    const int p1 = __shfl_sync(0xffffffffu, ld.id1, ld.k - ld.base);
-    const uint32_t st = ld.issued % C::kStages;
+    if (!more) return;
+    if (ld_k == ld_n) {
+      do {
+        more = lw.next(a);
+        ld_n = more ? lw.count(warp) : 0;
+      } while (more && ld_n == 0);
+      if (!more) return;
+      ld_k = 0;
+      look_up();
+    } else if (ld_k - ld_base == 32) {
+      look_up();
+    }
+    const int p0 = __shfl_sync(0xffffffffu, id0, ld_k - ld_base);
+    const int p1 = __shfl_sync(0xffffffffu, id1, ld_k - ld_base);
+    const uint32_t st = issued % C::kStages;
     uint64_t* bar = &bars[st];
     const uint32_t head = heads + st * C::kHeadBytes;
     const uint32_t dst = ring + st * C::kStageBytes;
     if (lane == 0) {
       const uint32_t flags = (p0 >= 0 ? 1u : 0u) | (p1 >= 0 ? 2u : 0u);
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(head + 16), "r"(flags) : "memory");
-      const long long pos = ((long long)sg.ta + warp + (long long)kWarps * ld.k) * kTile;
-      const int in_page = (int)(pos & (a.page - 1));
       if (a.page >= kTile) {
         mbar_arrive_expect_tx(bar, p0 >= 0 ? C::kStageBytes : 0);
         if (p0 >= 0) {
-          const int row = ((p0 * a.Hkv + sg.h) << a.page_shift) + in_page;
+          const int in_page = ((lw.ta + warp + kWarps * ld_k) * kTile) & (a.page - 1);
+          const int row = ((p0 * a.Hkv + lw.h) << a.page_shift) + in_page;
           tma_load_2d(dst, &tmK, bar, 0, row);
           tma_load_2d(dst + C::kHalfBytes, &tmV, bar, 0, row);
         }
       } else {
         mbar_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * (C::kStageBytes / 2));
         if (p0 >= 0) {
-          const int row = (p0 * a.Hkv + sg.h) << a.page_shift;
+          const int row = (p0 * a.Hkv + lw.h) << a.page_shift;
           tma_load_2d(dst, &tmK, bar, 0, row);
           tma_load_2d(dst + C::kHalfBytes, &tmV, bar, 0, row);
         }
         if (p1 >= 0) {
-          const int row = (p1 * a.Hkv + sg.h) << a.page_shift;
+          const int row = (p1 * a.Hkv + lw.h) << a.page_shift;
           tma_load_2d(dst + 16 * D, &tmK, bar, 0, row);
           tma_load_2d(dst + C::kHalfBytes + 16 * D, &tmV, bar, 0, row);
         }
@@ -255,26 +379,27 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ks, vs of half 0, ks, vs of half 1.  A half without a page takes any
       // valid scale: its flag hides it.
       const int p = max(lane < 2 ? p0 : p1, 0);
-      copy4_arrive(head + 4 * lane, ((lane & 1) ? a.v_scale : a.k_scale) + (size_t)p * a.Hkv + sg.h, bar);
+      copy4_arrive(head + 4 * lane, ((lane & 1) ? a.v_scale : a.k_scale) + (size_t)p * a.Hkv + lw.h, bar);
     }
-    ++ld.issued;
-    ++ld.k;
+    ++issued;
+    ++ld_k;
   };
+  if (more) look_up();
+  for (int i = 0; i < C::kStages; ++i) issue();
 
+  const int rows_total = a.n_q * a.G;
+  uint32_t used = 0;
+  bool last_segment = false;
+  while (!last_segment) {
   // ------------------------------------------------------------------ Q rows
   // Row r of the block: token (rb * 16 + r) / G, head (rb * 16 + r) % G of the
   // group.  K step ks of the products covers head dims [16 ks, 16 ks + 16), of
   // which this thread holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
   // k = 2c + 8, 2c + 9 (the same assignment as the K operand's).
-  const int rows_total = a.n_q * a.G;
   int my_last[2];   // last visible position of rows g and g + 8 (-1: none)
   float f_row[2];   // factor of the scores, in base 2
   uint32_t qf[D / 16][4];
-  const int tiles = sg.tb > sg.ta + warp ? (sg.tb - sg.ta - warp + kWarps - 1) / kWarps : 0;
-  if (ok) {
-    look_up(0);
-    for (int i = 0; i < C::kStages && ld.k < tiles; ++i) issue();
-  }
+  const int tiles = sg.count(warp);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = sg.rb * kRows + g + 8 * i;
@@ -314,7 +439,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
   float R = 0x1p-126f;  // power of two the accumulators' values are relative to
 
-  uint32_t used = 0;
   for (int k = 0; k < tiles && ok; ++k) {
     const uint32_t st = used % C::kStages;
     ok = warp_wait(&bars[st], (used / C::kStages) & 1);
@@ -422,15 +546,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     __syncwarp();
-    if (ld.k < tiles) issue();
-  }
-  if (!ok) {
-    if (lane == 0) set_fail(ATTN_ERR_TIMEOUT);
-    // Do not leave while copies into this CTA's shared memory are in flight.
-    for (; used < ld.issued; ++used) mbar_wait(&bars[used % C::kStages], (used / C::kStages) & 1);
+    issue();
   }
 
   // ------------------------------------------------------------------ merge
+  const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len);
+  float* part = nullptr;
+  if (!whole) {
+    part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats<D>();
+    if (sg.ta == 0 && threadIdx.x == 0) {
+      // The segment runs on into as many CTAs as hold the rest of its tiles.
+      const long long end = begin + run - sg.tb + tiles_of(sg.len);
+      a.chains[blockIdx.x] = make_int4((int)((end - 1) / per) - (int)blockIdx.x, sg.b, sg.h, sg.rb);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
@@ -450,11 +579,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float M_use = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) L += s_l[w * kRows + g + 8 * i] * ex2(s_m[w * kRows + g + 8 * i] - M_use);
-    fac[i] = ex2(m_run[i] - M_use) * (L > 0.f ? R / L : 0.f);
+    fac[i] = ex2(m_run[i] - M_use) * R;
     const int r = sg.rb * kRows + g + 8 * i;
-    if (warp == 0 && c == 0 && r < rows_total) {
-      const size_t row = ((size_t)sg.b * a.n_q + r / a.G) * a.H + sg.h * a.G + r % a.G;
-      a.lse[row] = L > 0.f ? (M + log2f(L) - 15.f) * 0.69314718055994531f : -INFINITY;
+    if (whole) {
+      fac[i] = L > 0.f ? fac[i] / L : 0.f;
+      if (warp == 0 && c == 0 && r < rows_total) {
+        const size_t row = ((size_t)sg.b * a.n_q + r / a.G) * a.H + sg.h * a.G + r % a.G;
+        a.lse[row] = lse_of(M, L);
+      }
+    } else if (warp == 0 && c == 0) {
+      part[kRows * D + g + 8 * i] = M;
+      part[kRows * D + kRows + g + 8 * i] = L;
     }
   }
 #pragma unroll
@@ -474,27 +609,100 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncthreads();
     // 16 rows x 64 columns over 128 threads: 8 columns each.
-    const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
+    const int r = threadIdx.x >> 3, part8 = threadIdx.x & 7;
     float v[8] = {};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float4 x = *reinterpret_cast<const float4*>(
-            s_merge + (w * kRows + r) * 64 + (((part * 2 + e) ^ ((r & 1) << 2)) << 2));
+            s_merge + (w * kRows + r) * 64 + (((part8 * 2 + e) ^ ((r & 1) << 2)) << 2));
         v[4 * e] += x.x;
         v[4 * e + 1] += x.y;
         v[4 * e + 2] += x.z;
         v[4 * e + 3] += x.w;
       }
     const int rr = sg.rb * kRows + r;
-    if (rr < rows_total) {
+    if (!whole) {
+      float4* p = reinterpret_cast<float4*>(part + r * D + half * 64 + part8 * 8);
+      p[0] = make_float4(v[0], v[1], v[2], v[3]);
+      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (rr < rows_total) {
       const size_t row = ((size_t)sg.b * a.n_q + rr / a.G) * a.H + sg.h * a.G + rr % a.G;
-      *reinterpret_cast<uint4*>(a.o + row * D + half * 64 + part * 8) =
+      *reinterpret_cast<uint4*>(a.o + row * D + half * 64 + part8 * 8) =
           make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                      pack_bf16x2(v[6], v[7]));
     }
   }
+  last_segment = !sg.next(a);
+  }  // segments
+  if (!ok) {
+    if (lane == 0) set_fail(ATTN_ERR_TIMEOUT);
+    // Do not leave while copies into this CTA's shared memory are in flight.
+    for (; used < issued; ++used) mbar_wait(&bars[used % C::kStages], (used / C::kStages) & 1);
+  }
+}
+
+// Joins the parts of the segments that begin in one CTA's run and end in
+// another's: grid (CTAs of the main kernel, rows), one row per CTA, whose warps
+// take every fourth part.  The order of the sums is that of the parts.
+template <int D>
+__global__ void __launch_bounds__(kThreads) decode_join_kernel(const Args a) {
+  __shared__ float s_o[kWarps][D], s_l[kWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int4 ch = __ldcg(a.chains + blockIdx.x);
+  const int rr = ch.w * kRows + blockIdx.y;
+  if (ch.x == 0 || rr >= a.n_q * a.G) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = ch.x + 1;
+  auto part = [&](int i) {
+    return a.parts + (size_t)(2 * (blockIdx.x + i) + (i == 0)) * part_floats<D>();
+  };
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + kRows * D + blockIdx.y));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float M_use = M == -INFINITY ? 0.f : M;
+  float L = 0.f, o[D / 32] = {};
+#pragma unroll 4
+  for (int i = warp; i < n; i += kWarps) {
+    const float* p = part(i);
+    const float f = ex2(__ldcg(p + kRows * D + blockIdx.y) - M_use);
+    L += f * __ldcg(p + kRows * D + kRows + blockIdx.y);
+    const float* x = p + blockIdx.y * D + lane * (D / 32);
+    if constexpr (D == 128) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(x));
+      o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(x));
+      o[0] += f * v.x, o[1] += f * v.y;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) s_o[warp][lane * (D / 32) + e] = o[e];
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  const size_t row = ((size_t)ch.y * a.n_q + rr / a.G) * a.H + ch.z * a.G + rr % a.G;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) L += s_l[w];
+  if (threadIdx.x < D / 2) {
+    const int d = threadIdx.x * 2;
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x += s_o[w][d], y += s_o[w][d + 1];
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    *reinterpret_cast<uint32_t*>(a.o + row * D + d) = pack_bf16x2(x * inv, y * inv);
+  }
+  if (threadIdx.x == 0) a.lse[row] = lse_of(M, L);
+}
+
+// Runs the tiles are dealt in: two CTAs fit an SM.  (The largest device's count
+// where there is no device to ask, for workspace sizes.)
+unsigned decode_runs() {
+  const int sms = device_sm_count();
+  return 2u * (sms > 0 ? sms : 152);
 }
 
 bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
@@ -519,13 +727,25 @@ cudaError_t launch_decode_impl(const PagedCache& cache, const Args& a, cudaStrea
   auto kernel = decode_int8_kernel<D>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (err != cudaSuccess) return err;
-  const unsigned grid = (unsigned)((long long)a.B * a.Hkv * a.row_blocks);
-  return launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
+  if (a.parts == nullptr) {
+    const unsigned grid = (unsigned)((long long)a.B * a.Hkv * a.row_blocks);
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
+  }
+  const unsigned runs = decode_runs();
+  err = launch_pdl(kernel, dim3(runs), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(decode_join_kernel<D>, dim3(runs, std::min(kRows, a.n_q * a.G)), dim3(kThreads), 0, stream, a);
 }
+
+bool splits(const PagedCache& c) { return (long long)c.max_blocks * c.page > (long long)kWholeTiles * kTile; }
 
 }  // namespace
 
-size_t decode_workspace_bytes(const PagedCache&, int, int) { return 0; }
+size_t decode_workspace_bytes(const PagedCache& c, int, int) {
+  if (!splits(c)) return 0;
+  const size_t part = (c.d == 128 ? part_floats<128>() : part_floats<64>()) * sizeof(float);
+  return align256(decode_runs() * 2 * part) + align256(decode_runs() * sizeof(int4));
+}
 
 cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides, const int* lens,
                                void* o, float* lse, int n_q, int H, float scale, void* workspace,
@@ -546,6 +766,13 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   a.max_blocks = c.max_blocks;
   a.row_blocks = ceil_div(n_q * a.G, kRows);
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.parts = nullptr;
+  a.chains = nullptr;
+  if (splits(c)) {
+    const size_t part = (c.d == 128 ? part_floats<128>() : part_floats<64>()) * sizeof(float);
+    a.parts = static_cast<float*>(workspace);
+    a.chains = reinterpret_cast<int4*>(static_cast<char*>(workspace) + align256(decode_runs() * 2 * part));
+  }
   return c.d == 128 ? launch_decode_impl<128>(c, a, stream) : launch_decode_impl<64>(c, a, stream);
 }
 

@@ -362,6 +362,38 @@ def test_decode_long(A, lens):
         check_decode(c, q, lens, 0.05, o, lse)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_short(A, page, d):
+    """A table too narrow for the keys to be split: one CTA a sequence and key head."""
+    H, Hkv, lens = 6, 3, [0, 1, 16, 17, 31, 250, 512, 499]
+    tables, pages = scattered([-(-n // page) for n in lens], 13)
+    c = Cache(pages, Hkv, page, d, tables)
+    for n_q in (1, 9):
+        q = normal((len(lens), n_q, H, d), 1)
+        o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens))
+        A.attn_check_status()
+        check_decode(c, q, lens, 1 / math.sqrt(d), o, lse)
+
+
+@pytest.mark.parametrize("most,page", [(2000, 16), (9000, 128)])
+def test_decode_ragged_batch(A, most, page):
+    """More sequences than a CTA scans at a time, among them empty ones; runs of tiles that begin and
+    end anywhere in a segment, hold several, or lie inside one."""
+    H, Hkv, d, B = 4, 2, 64, 171
+    g = torch.Generator().manual_seed(most)
+    lens = torch.randint(0, 70, (B,), generator=g).tolist()
+    lens[::9] = torch.randint(0, most, (len(lens[::9]),), generator=g).tolist()
+    lens[5:8] = lens[-3:] = [0, 0, 0]
+    tables, pages = scattered([-(-n // page) for n in lens], 14)
+    c = Cache(pages, Hkv, page, d, tables, width=-(-most // page))
+    q = normal((B, 1, H, d), 1)
+    o = torch.full((B, 1, H, d), 7.0, dtype=BF, device="cuda")
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens), o=o)
+    A.attn_check_status()
+    check_decode(c, q, lens, 1 / math.sqrt(d), o, lse)
+
+
 def test_decode_scales_of_every_size(A):
     """Pages whose value scales differ by 2^60, pages of zeros, keys of zero scale, queries of zeros
     and of extreme size."""
