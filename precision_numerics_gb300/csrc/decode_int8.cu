@@ -7,11 +7,13 @@
 // with codes ck, cv and the scales ks, vs of position j's page and head.
 //
 // What bounds it: every code is read once and used for n_q * G rows, so the
-// bytes of the cache (2 d per position and head) over HBM's rate.  The rows of
-// one key head (16 at a time) form the M side of mma.sync m16n8k16: with so
-// few rows the tensor work is a small part of the time the bytes take, and
-// the accumulators stay in registers.  A 128-row tcgen05 tile would be mostly
-// padding here.
+// bytes of the cache (2 d per position and head) over HBM's rate.  With so few
+// rows the tensor work is a small part of the time the bytes take; a 128-row
+// tcgen05 tile would be mostly padding.  The products are mma.sync m16n8k16
+// with the codes on the 16-row side, S^T = K Q^T and O^T = V^T P^T, and the query
+// rows of one key head on the 8-column side, NT blocks of 8: the conversion of a
+// code, which costs the most instructions, serves all of them, and few rows
+// leave little of a product empty.
 //
 // Codes become FP16 exactly (|c| <= 127): the byte c + 128 under the exponent
 // of 1024 is the FP16 number 1152 + c.  Q becomes FP16 after division by a
@@ -51,26 +53,35 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;   // positions per tile
-constexpr int kRows = 16;   // query rows (token, head of the group) per pass over the keys
 constexpr int kWholeTiles = 16;  // sequences up to this long are not split
 constexpr int kLeastRun = 4;     // tiles a CTA takes at least: one a warp
+// A segment's start and end (its Q rows, the merge of the warps, its output) take
+// as long as so many tiles: runs are measured in tiles plus this for each segment
+// that begins in them.
+constexpr int kSegmentCost = 10;
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_decode, code); }
 
-template <int D>
+// NT blocks of 8 query rows (token, head of the group) per pass over the keys.
+// 12 warps an SM for 8 rows, 8 beyond, as the registers allow; the rings take the
+// shared memory that is left.
+template <int D, int NT>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kCtas = NT == 1 ? 3 : 2;  // per SM
+  static constexpr int kStages = NT == 2 ? (D == 128 ? 3 : 5) : 2 * (128 / D);
   static constexpr int kHalfBytes = kTile * D;          // K or V of a tile
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kOffMerge = kWarps * kRingBytes;  // FP32 [warp][16 rows][64 columns]
-  static constexpr int kOffStat = kOffMerge + kWarps * kRows * 64 * 4;  // m, l: FP32 [2][warp][16]
+  static constexpr int kOffMerge = kWarps * kRingBytes;  // FP32 [warp][rows][64 columns]
+  static constexpr int kOffStat = kOffMerge + kWarps * kRows * 64 * 4;  // m, l: FP32 [2][warp][rows]
   // Per warp and stage: ks, vs of the tile's two halves (16 positions each),
   // then one word of flags (bit per half that was loaded).
   static constexpr int kOffHead = kOffStat + 2 * kWarps * kRows * 4;
   static constexpr int kHeadBytes = 32;
   static constexpr int kOffBar = kOffHead + kWarps * kStages * kHeadBytes;
   static constexpr int kSmemBytes = kOffBar + kWarps * kStages * 8;
+  static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
@@ -107,6 +118,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Transposes an 8x8 matrix of 16-bit values held one row (two columns) per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -132,6 +149,13 @@ __device__ __forceinline__ float lse_of(float M, float L) {
   return L > 0.f ? (M + log2f(L) - 15.f) * 0.69314718055994531f : -INFINITY;
 }
 
+// A segment in several parts: those behind the first (0: nothing to join), its
+// sequence, key head * row_blocks + row block, and the CTA it begins in.
+struct Chain {
+  int more, b, hr, cta;
+};
+static_assert(sizeof(Chain) == 16, "one 16-byte access");
+
 struct Args {
   const uint16_t* q;
   long long q_batch, q_token, q_head;
@@ -139,16 +163,27 @@ struct Args {
   const int *table, *lens;
   uint16_t* o;
   float* lse;
+  uint32_t by_G;  // ceil(2^32 / G)
   int B, n_q, H, Hkv, G, P, page, page_shift, max_blocks, row_blocks;
   float scale_log2;
-  // Split mode (else null): parts [CTA][2], and what each CTA's last segment is.
+  // Split mode (else null): parts [CTA][2], and the segments that are joined, by
+  // the segment's number if by_segment, else by the CTA it begins in.
   float* parts;
-  int4* chains;
+  Chain* chains;
+  int by_segment;
 };
 
-// A part in the workspace: O [16][D], m [16], l [16], FP32.
-template <int D>
-constexpr int part_floats() { return kRows * (D + 2); }
+// A part in the workspace: O [rows][D], m [rows], l [rows], FP32.
+__host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
+
+// Query token of row r (< 2^14) of a key head's rows, and its row of o and lse.
+__device__ __forceinline__ int token_of(const Args& a, int r) {
+  return a.G == 1 ? r : (int)__umulhi((uint32_t)r, a.by_G);
+}
+__device__ __forceinline__ size_t out_row(const Args& a, int b, int h, int r) {
+  const int t = token_of(a, r);
+  return ((size_t)b * a.n_q + t) * a.H + h * a.G + (r - t * a.G);
+}
 
 __device__ __forceinline__ int length_of(const Args& a, int b) {
   const long long cap = (long long)a.max_blocks << a.page_shift;
@@ -162,13 +197,23 @@ __device__ __forceinline__ int length_of(const Args& a, int b) {
 
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + kTile - 1) / kTile); }
 
-// A position in a CTA's run of tiles: tiles [ta, tb) of (sequence b, key head h,
-// row block rb), `left` tiles behind them.
+// Cost of a segment: kSegmentCost, then one per tile.
+__device__ __forceinline__ int cost_of(int len) { return len > 0 ? tiles_of(len) + kSegmentCost : 0; }
+
+// A position in a CTA's run: tiles [ta, tb) of (sequence b, key head h, row block
+// rb), cost `left` behind them.
 struct Walk {
   int b, h, rb, len, ta, tb;
   long long left;
   __device__ __forceinline__ int count(int warp) const {  // tiles of warp `warp`: ta + warp + kWarps * k
     return tb > ta + warp ? (tb - ta - warp + kWarps - 1) / kWarps : 0;
+  }
+  // The tiles that the run has of this segment, whose first `from` units of cost are before it.
+  __device__ __forceinline__ void take(int from) {
+    const int to = (int)min((long long)cost_of(len), from + left);
+    left -= to - from;
+    ta = max(from - kSegmentCost, 0);
+    tb = max(to - kSegmentCost, 0);
   }
   __device__ __forceinline__ bool next(const Args& a) {
     if (left <= 0) return false;
@@ -182,10 +227,8 @@ struct Walk {
         } while (len == 0);
       }
     }
-    ta = 0;
-    tb = (int)min((long long)tiles_of(len), left);
-    left -= tb;
-    return true;
+    take(0);
+    return tb > 0;  // a run may end before the first tile
   }
 };
 
@@ -210,11 +253,12 @@ __device__ __forceinline__ long long scan_before(long long x, long long* s_warp,
   return upto - x;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const Args a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, NT>;
+  constexpr int kRows = C::kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -225,7 +269,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* s_m = reinterpret_cast<float*>(smem + C::kOffStat);
   float* s_l = s_m + kWarps * kRows;
 
-  griddep_launch_dependents();
+  // No griddep_launch_dependents() here: the next launch of this kernel would fill
+  // the slots that free up first and keep an uneven share of the SMs (one long
+  // sequence 54 us a call without it, 72 us with it).
   bool ok = (smem_u32(smem) & 1023u) == 0;
   if (lane == 0) {
     // Five arrivals per tile: lane 0's, with the bytes of K and V, and the four
@@ -239,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!ok && threadIdx.x == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
   Walk sg;
-  long long per = 0, begin = 0, run = 0;  // tiles of a run; where this CTA's begins, its length
+  long long per = 0;  // cost of a run
   if (a.parts == nullptr) {
     const int x = blockIdx.x;
     sg.rb = x % a.row_blocks;
@@ -250,36 +296,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     sg.tb = tiles_of(sg.len);
     sg.left = 0;
   } else {
-    // All tiles, and the sequence in which this CTA's run begins.
+    // All segments' cost, and the sequence in which this CTA's run begins.
     long long* s_warp = reinterpret_cast<long long*>(s_merge);
     const long long copies = (long long)a.Hkv * a.row_blocks;
     long long total = 0, sum;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      scan_before(b < a.B ? tiles_of(length_of(a, b)) : 0, s_warp, sum);
+      scan_before(b < a.B ? cost_of(length_of(a, b)) : 0, s_warp, sum);
       total += sum;
     }
     total *= copies;
+    // One run for every CTA that the SMs hold at a time: more and shorter runs cost
+    // more to start than they even out (ragged batch 106 us, with two to a slot 110).
     per = max((total + gridDim.x - 1) / gridDim.x, (long long)kLeastRun);
-    begin = per * blockIdx.x;
+    const long long begin = per * blockIdx.x;
     int4* s_start = reinterpret_cast<int4*>(s_m);
     if (threadIdx.x == 0) s_start[0].x = -1;
     long long before = 0;
     for (int b0 = 0; b0 < a.B && before <= begin; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
       const int len = b < a.B ? length_of(a, b) : 0;
-      const int tiles = tiles_of(len);
-      const long long at = before + copies * scan_before(tiles, s_warp, sum);
-      if (begin >= at && begin < at + copies * tiles) {
+      const int cost = cost_of(len);
+      const long long at = before + copies * scan_before(cost, s_warp, sum);
+      if (begin >= at && begin < at + copies * cost) {
         const long long rest = begin - at;
-        s_start[0] = make_int4(b, len, (int)(rest / tiles), (int)(rest % tiles));
+        s_start[0] = make_int4(b, len, (int)(rest / cost), (int)(rest % cost));
       }
       before += copies * sum;
     }
     __syncthreads();
     const int4 st = s_start[0];
     __syncthreads();
-    if (threadIdx.x == 0) a.chains[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!a.by_segment && threadIdx.x == 0) a.chains[blockIdx.x] = Chain{0, 0, 0, 0};
     // Sequences without a position have no tile: their rows are empty.
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       if (length_of(a, b) > 0) continue;
@@ -287,17 +335,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = threadIdx.x; i < a.n_q * a.H * (D / 8); i += kThreads)
         reinterpret_cast<uint4*>(a.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
       for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) a.lse[row + i] = -INFINITY;
+      if (a.by_segment)
+        for (int i = threadIdx.x; i < copies; i += kThreads) a.chains[b * copies + i] = Chain{0, 0, 0, 0};
     }
     if (st.x < 0) return;  // more CTAs than runs
-    run = min(per, total - begin);
     sg.b = st.x;
     sg.len = st.y;
     sg.h = st.z / a.row_blocks;
     sg.rb = st.z % a.row_blocks;
-    sg.ta = st.w;
-    sg.left = run;
-    sg.tb = (int)min((long long)tiles_of(sg.len), sg.ta + sg.left);
-    sg.left -= sg.tb - sg.ta;
+    sg.left = min(per, total - begin);
+    sg.take(st.w);
+    if (sg.tb == sg.ta) return;  // the run ends before the segment's first tile
   }
 
   // ------------------------------------------------------------------ loads
@@ -392,19 +440,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   bool last_segment = false;
   while (!last_segment) {
   // ------------------------------------------------------------------ Q rows
-  // Row r of the block: token (rb * 16 + r) / G, head (rb * 16 + r) % G of the
+  // Row r of the block: token (rb * rows + r) / G, head (rb * rows + r) % G of the
   // group.  K step ks of the products covers head dims [16 ks, 16 ks + 16), of
   // which this thread holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
-  // k = 2c + 8, 2c + 9 (the same assignment as the K operand's).
-  int my_last[2];   // last visible position of rows g and g + 8 (-1: none)
-  float f_row[2];   // factor of the scores, in base 2
-  uint32_t qf[D / 16][4];
+  // k = 2c + 8, 2c + 9 (the same assignment as the codes') of rows 8 n + g.  The
+  // scores and accumulators it holds are those of rows 8 n + 2 c + {0, 1}.
+  int my_last[NT][2];   // last visible position of those (-1: none)
+  float f_row[NT][2];   // factor of their scores, in base 2
+  uint32_t qf[NT][D / 16][2];
   const int tiles = sg.count(warp);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = sg.rb * kRows + g + 8 * i;
+  for (int n = 0; n < NT; ++n) {
+    const int r = sg.rb * kRows + 8 * n + g;
     const bool have = r < rows_total;
-    const int t = r / a.G, hq = sg.h * a.G + r % a.G;
+    const int t = token_of(a, r), hq = sg.h * a.G + (r - t * a.G);
     const uint16_t* src = a.q + sg.b * a.q_batch + t * a.q_token + hq * a.q_head;
     uint2 w[D / 16];
     float m = 0.f;
@@ -421,22 +470,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      qf[ks][i] = pack_f16x2(__uint_as_float(w[ks].x << 16) * down, __uint_as_float(w[ks].x & 0xFFFF0000u) * down);
-      qf[ks][2 + i] = pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down);
+      qf[n][ks][0] = pack_f16x2(__uint_as_float(w[ks].x << 16) * down, __uint_as_float(w[ks].x & 0xFFFF0000u) * down);
+      qf[n][ks][1] = pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down);
     }
-    f_row[i] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-    my_last[i] = have ? sg.len - a.n_q + t : -1;
+    const float f = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+    const int last = have ? sg.len - a.n_q + t : -1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f_row[n][i] = __shfl_sync(0xffffffffu, f, (2 * c + i) * 4);
+      my_last[n][i] = __shfl_sync(0xffffffffu, last, (2 * c + i) * 4);
+    }
   }
 
   // ------------------------------------------------------------------ tiles
-  float acc[D / 16][2][4];
+  float acc[D / 16][NT][4];  // head dims 16 u + 2 g + {0, 0, 1, 1}, rows 2 c + {0, 1, 0, 1}
 #pragma unroll
   for (int u = 0; u < D / 16; ++u)
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[u][e][x] = 0.f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+      for (int x = 0; x < 4; ++x) acc[u][n][x] = 0.f;
+  float m_run[NT][2], l_run[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m_run[n][i] = -INFINITY, l_run[n][i] = 0.f;
   float R = 0x1p-126f;  // power of two the accumulators' values are relative to
 
   for (int k = 0; k < tiles && ok; ++k) {
@@ -455,42 +513,50 @@ __global__ void __launch_bounds__(kThreads, 2)
                    : "memory");
       asm volatile("ld.shared.b32 %0, [%1];" : "=r"(flags) : "r"(head + 16) : "memory");
     }
-    // S = Q K^T: 4 blocks of 8 positions.
-    float s[4][4];
+    // S^T = K Q^T for the tile's halves of 16 positions: of s[h][n], elements 0
+    // and 1 are position g, 2 and 3 position g + 8.
+    float s[2][NT][4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int u = 0; u < D / 16; u += 4) {
-        uint32_t r[4];
-        ldsm4(r, tK + unit_offset<D>(n * 8 + (lane & 7), u + (lane >> 3)));
+      for (int n = 0; n < NT; ++n) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t b = r[x] ^ 0x80808080u;
-          mma_f16(s[n], qf[u + x], codes_f16(b, 0x4140u), codes_f16(b, 0x4342u));
+      for (int u = 0; u < D / 16; u += 2) {
+        uint32_t r[4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
+        ldsm4(r, tK + unit_offset<D>(h * 16 + (lane & 15), u + (lane >> 4)));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t b0 = r[2 * x] ^ 0x80808080u, b1 = r[2 * x + 1] ^ 0x80808080u;
+          const uint32_t af[4] = {codes_f16(b0, 0x4140u), codes_f16(b1, 0x4140u), codes_f16(b0, 0x4342u),
+                                  codes_f16(b1, 0x4342u)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(s[h][n], af, qf[n][u + x][0], qf[n][u + x][1]);
         }
       }
     }
     // Scores in base 2; positions behind a row's last one are hidden.
     const int pos0 = (sg.ta + warp + kWarps * k) * kTile;
-    const bool all = pos0 + kTile - 1 <= sg.len - a.n_q && flags == 3u;
-    float mx[2] = {-INFINITY, -INFINITY};
+    if (pos0 + kTile - 1 <= sg.len - a.n_q && flags == 3u) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float f0 = f_row[i] * ksc[0], f1 = f_row[i] * ksc[1];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float v = s[n][2 * i + x] * (n < 2 ? f0 : f1);
-          if (!all && (pos0 + n * 8 + 2 * c + x > my_last[i] || !(flags & (n < 2 ? 1u : 2u)))) v = -INFINITY;
-          s[n][2 * i + x] = v;
-          mx[i] = fmaxf(mx[i], v);
-        }
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+          for (int x = 0; x < 4; ++x) s[h][n][x] *= f_row[n][x & 1] * ksc[h];
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const bool seen = pos0 + h * 16 + (x >> 1) * 8 + g <= my_last[n][x & 1] && ((flags >> h) & 1u);
+            s[h][n][x] = seen ? s[h][n][x] * (f_row[n][x & 1] * ksc[h]) : -INFINITY;
+          }
+      if (!(flags & 1u)) vsc[0] = 0.f;
+      if (!(flags & 2u)) vsc[1] = 0.f;
     }
-    const float v_big = fmaxf((flags & 1u) ? vsc[0] : 0.f, (flags & 2u) ? vsc[1] : 0.f);
+    const float v_big = fmaxf(vsc[0], vsc[1]);
     float shrink = 1.f;
     if (v_big > R) {
       // The power of two at or above v_big (at most 2^126).
@@ -498,51 +564,67 @@ __global__ void __launch_bounds__(kThreads, 2)
       shrink = R / r_new;
       R = r_new;
     }
-    const float inv_r = 1.f / R;
-    const float vr[2] = {(flags & 1u) ? vsc[0] * inv_r : 0.f, (flags & 2u) ? vsc[1] * inv_r : 0.f};
-    float alpha[2];
-    uint32_t pf[2][4];  // P as the A operand: K step (16 positions), register
+    const float inv_r = __uint_as_float(0x7F000000u - __float_as_uint(R));  // 1 / R of a power of two
+    const float vr[2] = {vsc[0] * inv_r, vsc[1] * inv_r};
+    float alpha[NT][2];
+    uint32_t pf[2][NT][2];  // P^T as the B operand of the halves
+    bool same = shrink == 1.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float m_new = fmaxf(m_run[i], mx[i]);
-      const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      alpha[i] = ex2(m_run[i] - m_use);
-      m_run[i] = m_new;
-      float sum = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      float m_use[2];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float p0 = ex2(s[n][2 * i] - m_use + 15.f), p1 = ex2(s[n][2 * i + 1] - m_use + 15.f);
-        sum += p0 + p1;
-        const float w = vr[n >> 1];
-        pf[n >> 1][(n & 1) * 2 + i] = pack_f16x2(p0 * w, p1 * w);
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        mx = fmaxf(m_run[n][i], mx);
+        m_use[i] = mx == -INFINITY ? 0.f : mx;
+        alpha[n][i] = ex2(m_run[n][i] - m_use[i]);
+        same = same && alpha[n][i] == 1.f;
+        m_run[n][i] = mx;
+        m_use[i] -= 15.f;
+        l_run[n][i] *= alpha[n][i];
       }
-      l_run[i] = l_run[i] * alpha[i] + sum;
-    }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f || shrink != 1.f)) {
-      const float s0 = alpha[0] * shrink, s1 = alpha[1] * shrink;
 #pragma unroll
-      for (int u = 0; u < D / 16; ++u)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          acc[u][e][0] *= s0;
-          acc[u][e][1] *= s0;
-          acc[u][e][2] *= s1;
-          acc[u][e][3] *= s1;
+        for (int y = 0; y < 2; ++y) {
+          const float p0 = ex2(s[h][n][2 * y] - m_use[0]), p1 = ex2(s[h][n][2 * y + 1] - m_use[1]);
+          l_run[n][0] += p0;
+          l_run[n][1] += p1;
+          pf[h][n][y] = transpose8(pack_f16x2(p0 * vr[h], p1 * vr[h]));
         }
     }
-    // O += P V.  A transposed load gives positions 2c, 2c + 1 of the columns
-    // d = 16 u + 2 g (even bytes) and + 1 (odd bytes).
+    if (!__all_sync(0xffffffffu, same)) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+      for (int n = 0; n < NT; ++n) {
+        const float s0 = alpha[n][0] * shrink, s1 = alpha[n][1] * shrink;
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+          acc[u][n][0] *= s0;
+          acc[u][n][1] *= s1;
+          acc[u][n][2] *= s0;
+          acc[u][n][3] *= s1;
+        }
+      }
+    }
+    // O^T += V^T P^T.  A transposed load gives positions 2c, 2c + 1 of the columns
+    // d = 16 u + 2 g (even bytes) and + 1 (odd bytes), rows g and g + 8 of the
+    // A operand.
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int u = 0; u < D / 16; u += 2) {
         uint32_t r[4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
-        ldsm4_trans(r, tV + unit_offset<D>(kk * 16 + (lane & 15), u + (lane >> 4)));
+        ldsm4_trans(r, tV + unit_offset<D>(h * 16 + (lane & 15), u + (lane >> 4)));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint32_t b0 = r[2 * x] ^ 0x80808080u, b1 = r[2 * x + 1] ^ 0x80808080u;
-          mma_f16(acc[u + x][0], pf[kk], codes_f16(b0, 0x4240u), codes_f16(b1, 0x4240u));
-          mma_f16(acc[u + x][1], pf[kk], codes_f16(b0, 0x4341u), codes_f16(b1, 0x4341u));
+          const uint32_t af[4] = {codes_f16(b0, 0x4240u), codes_f16(b0, 0x4341u), codes_f16(b1, 0x4240u),
+                                  codes_f16(b1, 0x4341u)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(acc[u + x][n], af, pf[h][n][0], pf[h][n][1]);
         }
       }
     __syncwarp();
@@ -552,89 +634,76 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ------------------------------------------------------------------ merge
   const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len);
   float* part = nullptr;
-  if (!whole) {
-    part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats<D>();
-    if (sg.ta == 0 && threadIdx.x == 0) {
-      // The segment runs on into as many CTAs as hold the rest of its tiles.
-      const long long end = begin + run - sg.tb + tiles_of(sg.len);
-      a.chains[blockIdx.x] = make_int4((int)((end - 1) / per) - (int)blockIdx.x, sg.b, sg.h, sg.rb);
-    }
+  if (!whole) part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats(D, kRows);
+  if (a.parts != nullptr && sg.ta == 0 && threadIdx.x == 0 && (a.by_segment || !whole)) {
+    const int hr = sg.h * a.row_blocks + sg.rb;
+    const long long slot = a.by_segment ? (long long)sg.b * a.Hkv * a.row_blocks + hr : blockIdx.x;
+    // The segment runs on into as many CTAs as hold the rest of its tiles.
+    const unsigned rest = tiles_of(sg.len) - sg.tb;
+    const int more = rest == 0 ? 0 : 1 + (int)((rest - 1) / (unsigned)min(per, 0x7fffffffll));
+    a.chains[slot] = Chain{more, sg.b, hr, (int)blockIdx.x};
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
-    l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
-    if (c == 0) {
-      s_m[warp * kRows + g + 8 * i] = m_run[i];
-      s_l[warp * kRows + g + 8 * i] = l_run[i];
-    }
-  }
-  __syncthreads();
-  float fac[2];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float M = -INFINITY, L = 0.f;
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + g + 8 * i]);
-    const float M_use = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) L += s_l[w * kRows + g + 8 * i] * ex2(s_m[w * kRows + g + 8 * i] - M_use);
-    fac[i] = ex2(m_run[i] - M_use) * R;
-    const int r = sg.rb * kRows + g + 8 * i;
-    if (whole) {
-      fac[i] = L > 0.f ? fac[i] / L : 0.f;
-      if (warp == 0 && c == 0 && r < rows_total) {
-        const size_t row = ((size_t)sg.b * a.n_q + r / a.G) * a.H + sg.h * a.G + r % a.G;
-        a.lse[row] = lse_of(M, L);
+      for (int off = 4; off < 32; off <<= 1) l_run[n][i] += __shfl_xor_sync(0xffffffffu, l_run[n][i], off);
+      if (g == 0) {
+        s_m[warp * kRows + 8 * n + 2 * c + i] = m_run[n][i];
+        s_l[warp * kRows + 8 * n + 2 * c + i] = l_run[n][i];
       }
-    } else if (warp == 0 && c == 0) {
-      part[kRows * D + g + 8 * i] = M;
-      part[kRows * D + kRows + g + 8 * i] = L;
     }
-  }
 #pragma unroll
   for (int half = 0; half < D / 64; ++half) {
     if (half > 0) __syncthreads();
+    // Pairs of columns, moved by four for every second row, so that the 16 lanes
+    // of a phase cover all banks.
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float(&x)[2][4] = acc[half * 4 + u];
-        const float4 v = make_float4(x[0][2 * i] * fac[i], x[1][2 * i] * fac[i], x[0][2 * i + 1] * fac[i],
-                                     x[1][2 * i + 1] * fac[i]);
-        // Odd rows' units are moved by four, so a phase of eight lanes covers all banks.
-        *reinterpret_cast<float4*>(s_merge + (warp * kRows + r) * 64 + (((u * 4 + c) ^ ((r & 1) << 2)) << 2)) = v;
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * n + 2 * c + i;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * 64 + (((8 * u + g) ^ (c << 2)) << 1)) =
+              make_float2(acc[half * 4 + u][n][i] * R, acc[half * 4 + u][n][2 + i] * R);
       }
-    }
     __syncthreads();
-    // 16 rows x 64 columns over 128 threads: 8 columns each.
-    const int r = threadIdx.x >> 3, part8 = threadIdx.x & 7;
-    float v[8] = {};
+    // rows x 64 columns over 128 threads, 4 columns at a time.
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+    for (int x = threadIdx.x; x < kRows * 16; x += kThreads) {
+      const int r = x >> 4, part4 = x & 15;
+      float M = -INFINITY, L = 0.f, v[4] = {};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 x = *reinterpret_cast<const float4*>(
-            s_merge + (w * kRows + r) * 64 + (((part8 * 2 + e) ^ ((r & 1) << 2)) << 2));
-        v[4 * e] += x.x;
-        v[4 * e + 1] += x.y;
-        v[4 * e + 2] += x.z;
-        v[4 * e + 3] += x.w;
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + r]);
+      const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_m[w * kRows + r] - M_use);
+        L += s_l[w * kRows + r] * f;
+        const float4 y = *reinterpret_cast<const float4*>(
+            s_merge + (w * kRows + r) * 64 + (((2 * part4) ^ (((r >> 1) & 3) << 2)) << 1));
+        v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
       }
-    const int rr = sg.rb * kRows + r;
-    if (!whole) {
-      float4* p = reinterpret_cast<float4*>(part + r * D + half * 64 + part8 * 8);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if (rr < rows_total) {
-      const size_t row = ((size_t)sg.b * a.n_q + rr / a.G) * a.H + sg.h * a.G + rr % a.G;
-      *reinterpret_cast<uint4*>(a.o + row * D + half * 64 + part8 * 8) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
+      const int rr = sg.rb * kRows + r;
+      if (!whole) {
+        *reinterpret_cast<float4*>(part + r * D + half * 64 + part4 * 4) = make_float4(v[0], v[1], v[2], v[3]);
+        if (half == 0 && part4 == 0) {
+          part[kRows * D + r] = M;
+          part[kRows * D + kRows + r] = L;
+        }
+      } else if (rr < rows_total) {
+        const size_t row = out_row(a, sg.b, sg.h, rr);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        *reinterpret_cast<uint2*>(a.o + row * D + half * 64 + part4 * 4) =
+            make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+        if (half == 0 && part4 == 0) a.lse[row] = lse_of(M, L);
+      }
     }
   }
   last_segment = !sg.next(a);
+  if (!last_segment) __syncthreads();  // before the next segment's m and l
   }  // segments
   if (!ok) {
     if (lane == 0) set_fail(ATTN_ERR_TIMEOUT);
@@ -644,33 +713,35 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the parts of the segments that begin in one CTA's run and end in
-// another's: grid (CTAs of the main kernel, rows), one row per CTA, whose warps
-// take every fourth part.  The order of the sums is that of the parts.
+// another's: grid (chains, groups of rows).  `per_row` warps (1 or kJoinWarps) share a row
+// and take every per_row-th part: one where there are many chains of a few parts,
+// all where few chains have many.  The order of the sums is that of the parts.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const Args a) {
-  __shared__ float s_o[kWarps][D], s_l[kWarps];
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args a, int rows, int per_row) {
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const int4 ch = __ldcg(a.chains + blockIdx.x);
-  const int rr = ch.w * kRows + blockIdx.y;
-  if (ch.x == 0 || rr >= a.n_q * a.G) return;
+  const int4 ch = __ldcg(reinterpret_cast<const int4*>(a.chains) + blockIdx.x);  // more, b, hr, cta
+  if (ch.x == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = ch.x + 1;
-  auto part = [&](int i) {
-    return a.parts + (size_t)(2 * (blockIdx.x + i) + (i == 0)) * part_floats<D>();
-  };
+  const int r = blockIdx.y * (kJoinWarps / per_row) + warp / per_row;
+  const int rr = ch.z % a.row_blocks * rows + r;
+  const bool have = r < rows && rr < a.n_q * a.G;
+  const int n = have ? ch.x + 1 : 0;
+  auto part = [&](int i) { return a.parts + (size_t)(2 * (ch.w + i) + (i == 0)) * part_floats(D, rows); };
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + kRows * D + blockIdx.y));
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + rows * D + r));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   const float M_use = M == -INFINITY ? 0.f : M;
   float L = 0.f, o[D / 32] = {};
-#pragma unroll 4
-  for (int i = warp; i < n; i += kWarps) {
+#pragma unroll 8
+  for (int i = warp % per_row; i < n; i += per_row) {
     const float* p = part(i);
-    const float f = ex2(__ldcg(p + kRows * D + blockIdx.y) - M_use);
-    L += f * __ldcg(p + kRows * D + kRows + blockIdx.y);
-    const float* x = p + blockIdx.y * D + lane * (D / 32);
+    const float f = ex2(__ldcg(p + rows * D + r) - M_use);
+    L += f * __ldcg(p + rows * D + rows + r);
+    const float* x = p + r * D + lane * (D / 32);
     if constexpr (D == 128) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(x));
       o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
@@ -679,32 +750,36 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const Args a) {
       o[0] += f * v.x, o[1] += f * v.y;
     }
   }
+  if (per_row > 1) {  // the same for all warps
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) s_o[warp][lane * (D / 32) + e] = o[e];
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  const size_t row = ((size_t)ch.y * a.n_q + rr / a.G) * a.H + ch.z * a.G + rr % a.G;
-  L = 0.f;
+    for (int e = 0; e < D / 32; ++e) s_o[warp][lane * (D / 32) + e] = o[e];
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    if (warp > 0) return;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) L += s_l[w];
-  if (threadIdx.x < D / 2) {
-    const int d = threadIdx.x * 2;
-    float x = 0.f, y = 0.f;
+    for (int w = 1; w < kJoinWarps; ++w) {
+      L += s_l[w];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) x += s_o[w][d], y += s_o[w][d + 1];
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    *reinterpret_cast<uint32_t*>(a.o + row * D + d) = pack_bf16x2(x * inv, y * inv);
+      for (int e = 0; e < D / 32; ++e) o[e] += s_o[w][lane * (D / 32) + e];
+    }
   }
-  if (threadIdx.x == 0) a.lse[row] = lse_of(M, L);
+  if (!have) return;
+  const size_t row = out_row(a, ch.y, ch.z / a.row_blocks, rr);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint16_t* out = a.o + row * D + lane * (D / 32);
+  if constexpr (D == 128)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0] * inv, o[1] * inv);
+  if (lane == 0) a.lse[row] = lse_of(M, L);
 }
 
-// Runs the tiles are dealt in: two CTAs fit an SM.  (The largest device's count
-// where there is no device to ask, for workspace sizes.)
-unsigned decode_runs() {
+// Runs the tiles are dealt in: the CTAs that the SMs hold at a time.  (The full
+// device's SM count where there is no device to ask, for workspace sizes.)
+unsigned decode_runs(int nt) {
   const int sms = device_sm_count();
-  return 2u * (sms > 0 ? sms : 152);
+  return (nt == 1 ? 3u : 2u) * (sms > 0 ? sms : 152);
 }
-
 bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
@@ -718,33 +793,38 @@ bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-cudaError_t launch_decode_impl(const PagedCache& cache, const Args& a, cudaStream_t stream) {
-  using C = Cfg<D>;
-  CUtensorMap mk, mv;
-  if (!make_tmap_codes(&mk, cache.k, cache) || !make_tmap_codes(&mv, cache.v, cache))
-    return cudaErrorInvalidValue;
-  auto kernel = decode_int8_kernel<D>;
+template <int D, int NT>
+cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, unsigned runs, cudaStream_t stream) {
+  using C = Cfg<D, NT>;
+  auto kernel = decode_int8_kernel<D, NT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (err != cudaSuccess) return err;
-  if (a.parts == nullptr) {
-    const unsigned grid = (unsigned)((long long)a.B * a.Hkv * a.row_blocks);
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
-  }
-  const unsigned runs = decode_runs();
+  if (a.parts == nullptr)
+    return launch_pdl(kernel, dim3((unsigned)((long long)a.B * a.Hkv * a.row_blocks)), dim3(kThreads), C::kSmemBytes,
+                      stream, mk, mv, a);
   err = launch_pdl(kernel, dim3(runs), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(decode_join_kernel<D>, dim3(runs, std::min(kRows, a.n_q * a.G)), dim3(kThreads), 0, stream, a);
+  const long long segments = (long long)a.B * a.Hkv * a.row_blocks;
+  const int per_row = segments * 4 <= runs ? kJoinWarps : 1;
+  const int rows = std::min(C::kRows, a.n_q * a.G);
+  return launch_pdl(decode_join_kernel<D>, dim3(a.by_segment ? (unsigned)segments : runs, ceil_div(rows * per_row, kJoinWarps)),
+                    dim3(32 * kJoinWarps), 0, stream, a, C::kRows, per_row);
 }
 
 bool splits(const PagedCache& c) { return (long long)c.max_blocks * c.page > (long long)kWholeTiles * kTile; }
 
+// Blocks of 8 rows a pass takes, and passes: as few passes as possible, then as
+// few blocks.
+int row_passes(int rows) { return ceil_div(rows, 32); }
+int row_tiles(int rows) { return ceil_div(rows, 8 * row_passes(rows)); }
+
 }  // namespace
 
-size_t decode_workspace_bytes(const PagedCache& c, int, int) {
+size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H) {
   if (!splits(c)) return 0;
-  const size_t part = (c.d == 128 ? part_floats<128>() : part_floats<64>()) * sizeof(float);
-  return align256(decode_runs() * 2 * part) + align256(decode_runs() * sizeof(int4));
+  const int rows = n_q * (H / c.Hkv), nt = row_tiles(rows);
+  const size_t runs = decode_runs(nt);
+  return align256(runs * 2 * part_floats(c.d, 8 * nt) * sizeof(float)) + runs * sizeof(Chain);
 }
 
 cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides, const int* lens,
@@ -761,19 +841,37 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   a.lens = lens;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
-  a.B = c.B, a.n_q = n_q, a.H = H, a.Hkv = c.Hkv, a.G = H / c.Hkv, a.P = c.P, a.page = c.page;
+  a.B = c.B, a.n_q = n_q, a.H = H, a.Hkv = c.Hkv, a.G = H / c.Hkv, a.by_G = (uint32_t)(((1ull << 32) + a.G - 1) / a.G), a.P = c.P, a.page = c.page;
   a.page_shift = page_shift(c.page);
   a.max_blocks = c.max_blocks;
-  a.row_blocks = ceil_div(n_q * a.G, kRows);
+  a.row_blocks = row_passes(n_q * a.G);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.parts = nullptr;
   a.chains = nullptr;
+  const int nt = row_tiles(n_q * a.G);
+  a.by_segment = 0;
+  unsigned runs = 0;
   if (splits(c)) {
-    const size_t part = (c.d == 128 ? part_floats<128>() : part_floats<64>()) * sizeof(float);
+    runs = decode_runs(nt);
+    a.by_segment = (long long)a.B * a.Hkv * a.row_blocks <= runs;
     a.parts = static_cast<float*>(workspace);
-    a.chains = reinterpret_cast<int4*>(static_cast<char*>(workspace) + align256(decode_runs() * 2 * part));
+    a.chains = reinterpret_cast<Chain*>(static_cast<char*>(workspace) +
+                                        align256((size_t)runs * 2 * part_floats(c.d, 8 * nt) * sizeof(float)));
   }
-  return c.d == 128 ? launch_decode_impl<128>(c, a, stream) : launch_decode_impl<64>(c, a, stream);
+  CUtensorMap mk, mv;
+  if (!make_tmap_codes(&mk, c.k, c) || !make_tmap_codes(&mv, c.v, c)) return cudaErrorInvalidValue;
+#define ATTN_DECODE_CASE(DD, TT) \
+  if (c.d == DD && nt == TT) return launch_impl<DD, TT>(mk, mv, a, runs, stream);
+  ATTN_DECODE_CASE(64, 1)
+  ATTN_DECODE_CASE(64, 2)
+  ATTN_DECODE_CASE(64, 3)
+  ATTN_DECODE_CASE(64, 4)
+  ATTN_DECODE_CASE(128, 1)
+  ATTN_DECODE_CASE(128, 2)
+  ATTN_DECODE_CASE(128, 3)
+  ATTN_DECODE_CASE(128, 4)
+#undef ATTN_DECODE_CASE
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t read_and_clear_status_decode(unsigned int* out, cudaStream_t stream) {
