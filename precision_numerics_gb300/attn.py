@@ -108,7 +108,8 @@ def _call(name: str, *args) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # torch.cuda.current_stream() without the Stream object around the handle.
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -360,8 +361,13 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, scale=None, causal=False, 
 # v_cache, k_scale, v_scale, block_table).  Tensors on another device than the
 # current one are refused by the library.
 
+# Each check first asks for everything at once, and looks for what is wrong only
+# then: attribute reads are most of what a call costs on the host.
+
 def _check_rows(name, t, shape):
     """A BF16 CUDA tensor of this shape whose rows of d elements are contiguous."""
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype is torch.bfloat16 and t.is_cuda and t.stride(-1) == 1:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.dtype != torch.bfloat16:
@@ -379,6 +385,8 @@ def _check_packed_rows(name, t):
 
 
 def _check_dense(name, t, shape, dtype):
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
@@ -387,6 +395,9 @@ def _check_dense(name, t, shape, dtype):
 
 
 def _check_ints(name, t, n=None):
+    if (type(t) is torch.Tensor and t.dtype is torch.int32 and t.is_cuda and t.dim() == 1 and t.is_contiguous()
+            and (n is None or t.shape[0] == n)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if (not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
@@ -400,13 +411,15 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table):
         raise ValueError("k_cache must be a tensor [pages, H_kv, page_size, d]")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [B, max_blocks]")
-    pages, hk, page, d = k_cache.shape
-    _check_dense("k_cache", k_cache, k_cache.shape, torch.int8)
-    _check_dense("v_cache", v_cache, k_cache.shape, torch.int8)
+    shape = k_cache.shape
+    pages, hk, page, d = shape
+    _check_dense("k_cache", k_cache, shape, torch.int8)
+    _check_dense("v_cache", v_cache, shape, torch.int8)
     _check_dense("k_scale", k_scale, (pages, hk), torch.float32)
     _check_dense("v_scale", v_scale, (pages, hk), torch.float32)
-    _check_dense("block_table", block_table, block_table.shape, torch.int32)
-    return block_table.shape[0], pages, hk, page, d, block_table.shape[1]
+    B, blocks = block_table.shape
+    _check_dense("block_table", block_table, (B, blocks), torch.int32)
+    return B, pages, hk, page, d, blocks
 
 
 def attn_varlen_plan_bytes(B: int, T: int, H: int, H_kv: int) -> int:
