@@ -15,11 +15,16 @@
 // matters: x = a / 2 lies next to the border between 63 and 64 for every a, and
 // there an FP32 quotient's own rounding would decide the code.
 //
-// One CTA per (page, head, K or V), found from the sequences' lengths by a
-// scan over the batch; the new rows stay in registers between the maximum and
-// the codes, so every byte moves once.
+// Both directions move a byte or two per element and do little with it, so HBM
+// bounds them for long inputs and the chain of dependent loads (lengths, page
+// number, rows) for a decoding step.  For prompts one CTA takes a (page, head, K
+// or V) and keeps the new rows in registers between the maximum and the codes, so
+// every byte moves once; for a step's few rows a page a CTA takes a page of K or
+// V and its warps the heads, so that the search for the page is done once.
 #include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "attn_internal.h"
 #include "ptx.cuh"
@@ -31,6 +36,7 @@ static __device__ unsigned int g_status_cache;
 namespace {
 
 constexpr int kAppendThreads = 128;
+constexpr int kStepRows = 8;  // up to so many rows a sequence (on average) are a step
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_cache, code); }
 
@@ -47,7 +53,7 @@ __device__ __forceinline__ float rint_quotient(float xh, float xl, float s) {
   return k;
 }
 
-__device__ __forceinline__ int code_of(float xh, float xl, float s) {
+__device__ __noinline__ int code_of(float xh, float xl, float s) {
   // NaN becomes 0, an infinity +-127.
   if (!(s > 0.f) || isnan(xh)) return 0;
   if (isinf(xh)) return xh > 0.f ? 127 : -127;
@@ -56,6 +62,127 @@ __device__ __forceinline__ int code_of(float xh, float xl, float s) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// A scale and what its codes need: 1 / s, and the bound on |x - k s| below which
+// the rounded x * (1 / s) is the code (0 where the scale is too small or large
+// for that: every code then goes through code_of).
+struct Quantizer {
+  float s, inv, near;
+  __device__ __forceinline__ explicit Quantizer(float scale) : s(scale) {
+    const bool usual = s > 0x1p-100f && s < 0x1p100f;
+    inv = usual ? 1.f / s : 0.f;
+    near = usual ? s * 0.4999f : 0.f;
+  }
+  // Codes of 8 BF16 values.  x (1 / s) is off by less than 2^-22 of at most 127, so
+  // k = rint of it (adding 1.5 * 2^23 rounds, half to even, and leaves k in the
+  // sum's low byte) is the code unless x lies within 1e-4 s of a border between
+  // two, where |x - k s|, which is exact, is not below 0.4999 s.  Then its double
+  // against s decides, as in rint_quotient; what is no finite multiple of the scale
+  // at all is done one by one.
+  __device__ __forceinline__ uint2 codes(const uint4& w) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t q[8];
+    float far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = (e & 1) ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]);
+      const float y = fmaf(x, inv, 12582912.f);
+      const float rest = fabsf(fmaf(-(y - 12582912.f), s, x));
+      far = rest < near ? far : INFINITY;
+      q[e] = __float_as_uint(y);
+    }
+    if (far > 0.f) {
+      bool plain = near > 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = (e & 1) ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]);
+        const float rest = fmaf(-(__uint_as_float(q[e]) - 12582912.f), s, x);
+        const float twice = 2.f * fabsf(rest);
+        plain = plain && twice < 1.001f * s;
+        if (twice > s || (twice == s && (q[e] & 1u))) q[e] += rest > 0.f ? 1u : ~0u;
+      }
+      if (!plain) {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w;
+          const uint32_t lo = code_of(bf16_lo(u), 0.f, s), hi = code_of(bf16_hi(u), 0.f, s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i == e) q[2 * i] = lo, q[2 * i + 1] = hi;
+        }
+      }
+    }
+    return make_uint2(
+        __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+        __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+  }
+  // Four held codes on this scale instead of `old`; ratio = old / s.  As above: the
+  // rounded c * ratio is the code unless it lies next to a border.
+  __device__ __forceinline__ uint32_t again(uint32_t c4, float old, float ratio) const {
+    const uint32_t u = c4 ^ 0x80808080u;
+    float c[4];
+    uint32_t q[4];
+    bool fine = near > 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + e)) - 8388736.f;  // 2^23 + (c + 128)
+      const float y = fmaf(c[e], ratio, 12582912.f);
+      fine = fine && fabsf(fmaf(c[e], ratio, 12582912.f - y)) < 0.4999f;
+      q[e] = __float_as_uint(y);
+    }
+    if (!fine) {
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const float x = static_cast<float>(static_cast<int8_t>(c4 >> (8 * e)));
+        const float hi = x * old;
+        const uint32_t k = code_of(hi, fmaf(x, old, -hi), s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i == e) q[i] = k;
+      }
+    }
+    return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+  }
+};
+
+// Rows of a page that were held on scale `old`, 16 codes at a time by threads
+// first, first + step, ...
+__device__ __forceinline__ void requantize(int8_t* codes, int units, const Quantizer& qz, float old, int first,
+                                           int step) {
+  const float ratio = old / qz.s;
+  for (int u = first; u < units; u += step) {
+    uint4* p = reinterpret_cast<uint4*>(codes) + u;
+    uint4 c = __ldcg(p);
+    c.x = qz.again(c.x, old, ratio);
+    c.y = qz.again(c.y, old, ratio);
+    c.z = qz.again(c.z, old, ratio);
+    c.w = qz.again(c.w, old, ratio);
+    *p = c;
+  }
+}
+
+// Largest |x| of 8 BF16 values, as bits in both halves of the result, with `m`.
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, const uint4& w) {
+  m = __vmaxu2(m, w.x & 0x7FFF7FFFu);
+  m = __vmaxu2(m, w.y & 0x7FFF7FFFu);
+  m = __vmaxu2(m, w.z & 0x7FFF7FFFu);
+  return __vmaxu2(m, w.w & 0x7FFF7FFFu);
+}
+// The same over finite values only.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t m, const uint4& w) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t lo = v[e] & 0x7FFFu, hi = (v[e] >> 16) & 0x7FFFu;
+    m = max(m, lo < 0x7F80u ? lo : 0u);
+    m = max(m, hi < 0x7F80u ? hi : 0u);
+  }
+  return m;
+}
+__device__ __forceinline__ uint32_t one_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+__device__ __forceinline__ uint32_t warp_max(uint32_t m) { return __reduce_max_sync(0xffffffffu, m); }
+// The scale that a page needs for new rows whose largest |x| has these bits.
+__device__ __forceinline__ float scale_for(uint32_t bits) { return __uint_as_float(bits << 16) / 127.f; }
 
 // Sequence b's new rows: `first` is its first row of the packed input, n their
 // number (clamped to the rows there are, whatever cu_seqlens holds).
@@ -73,27 +200,27 @@ struct AppendArgs {
   int B, T, Hkv, P, page, page_shift, max_blocks;
 };
 
-// D head dims; kUnits: 16-byte units of new rows a thread holds at most
-// (page * D / 8 units over 128 threads).
-template <int D, int kUnits>
-__global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const AppendArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  __shared__ int s_warp[kAppendThreads / 32];
-  __shared__ int s_found[4];  // sequence, page number in it, first row, rows
-  __shared__ float s_max[kAppendThreads / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int item = blockIdx.x, head = blockIdx.y, kv = blockIdx.z;
+// What a CTA writes: rows [r0, r1) of page `page` take the packed rows from row0 on.
+struct Found {
+  int page, r0, r1;
+  long long row0;
+};
 
-  // Which page of which sequence is number `item` of the touched ones?
-  if (tid == 0) s_found[0] = -1;
+// Number `item` of the pages that new rows fall into, over all sequences.  Every
+// thread of the CTA calls it; page < 0: there is none, or it is out of range.
+template <int kThreads>
+__device__ __forceinline__ Found find_page(const AppendArgs& a, int item) {
+  __shared__ int s_warp[kThreads / 32];
+  __shared__ Found s_found;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) s_found.page = -1;
   int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kAppendThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
     const int b = b0 + tid;
     int first = 0, n = 0, start = 0, count = 0;
     if (b < a.B) {
-      new_rows(a.cu, b, a.T, first, n);
       start = max(__ldcg(a.starts + b), 0);
+      new_rows(a.cu, b, a.T, first, n);
       if (n > 0) count = ((n - 1 + (start & (a.page - 1))) >> a.page_shift) + 1;
     }
     int upto = count;
@@ -107,44 +234,53 @@ __global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const Appen
     __syncthreads();
     int chunk = 0;
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) upto += s_warp[w];
       chunk += s_warp[w];
     }
     const int at = item - before - (upto - count);
     if (at >= 0 && at < count) {
-      s_found[0] = b;
-      s_found[1] = at;
-      s_found[2] = first;
-      s_found[3] = n;
+      const int in_page = start & (a.page - 1);
+      const long long blk = (long long)(start >> a.page_shift) + at;
+      int id = blk < a.max_blocks ? __ldcg(a.table + (size_t)b * a.max_blocks + blk) : -1;
+      if (id < 0 || id >= a.P) {
+        set_fail(ATTN_ERR_INVALID_ARG);
+        id = -1;
+      }
+      const int done = at == 0 ? 0 : at * a.page - in_page;  // rows that go to earlier pages
+      Found f;
+      f.page = id;
+      f.r0 = at == 0 ? in_page : 0;
+      f.r1 = min(a.page, f.r0 + n - done);
+      f.row0 = (long long)first + done;
+      s_found = f;
     }
     before += chunk;
     if (before > item) break;
   }
   __syncthreads();
-  const int b = s_found[0];
-  if (b < 0) return;  // fewer pages are touched than the launch allows for
-  const int start = max(__ldcg(a.starts + b), 0);
-  const long long blk = (long long)(start >> a.page_shift) + s_found[1];
-  const int page_id = blk < a.max_blocks ? __ldcg(a.table + (size_t)b * a.max_blocks + blk) : -1;
-  if (page_id < 0 || page_id >= a.P) {
-    if (tid == 0) set_fail(ATTN_ERR_INVALID_ARG);
-    return;
-  }
-  // Rows [r0, r1) of the page take the packed rows from `row0` on.
-  const int r0 = s_found[1] == 0 ? (start & (a.page - 1)) : 0;
-  const int done = s_found[1] == 0 ? 0 : s_found[1] * a.page - (start & (a.page - 1));
-  const int r1 = min(a.page, r0 + s_found[3] - done);
-  const long long row0 = (long long)s_found[2] + done;
-  const uint16_t* x = a.x[kv] + row0 * a.token_stride[kv] + head * a.head_stride[kv];
-  const size_t slot = (size_t)page_id * a.Hkv + head;
+  return s_found;
+}
+
+// D head dims; kUnits: 16-byte units of new rows a thread holds at most
+// (page * D / 8 units over 128 threads).
+template <int D, int kUnits>
+__global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const __grid_constant__ AppendArgs a) {
+  griddep_wait();
+  __shared__ uint32_t s_max[kAppendThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kv = blockIdx.z;
+  const Found f = find_page<kAppendThreads>(a, blockIdx.x);
+  if (f.page < 0) return;
+  for (int head = blockIdx.y; head < a.Hkv; head += gridDim.y) {
+  const uint16_t* x = a.x[kv] + f.row0 * a.token_stride[kv] + head * a.head_stride[kv];
+  const size_t slot = (size_t)f.page * a.Hkv + head;
   int8_t* codes = a.codes[kv] + slot * a.page * D;
   float* scale = a.scales[kv] + slot;
 
   constexpr int kPerRow = D / 8;
-  const int units = (r1 - r0) * kPerRow;
+  const int units = (f.r1 - f.r0) * kPerRow;
   uint4 w[kUnits];
-  float m = 0.f;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int u = tid + i * kAppendThreads;
@@ -152,53 +288,70 @@ __global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const Appen
     if (u < units)
       w[i] = __ldcg(reinterpret_cast<const uint4*>(x + (u / kPerRow) * a.token_stride[kv] + (u % kPerRow) * 8));
   }
+  const float s_old = f.r0 > 0 ? __ldcg(scale) : 0.f;
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+  for (int i = 0; i < kUnits; ++i) m = max_bits(m, w[i]);
+  m = warp_max(one_half(m));
+  if (m >= 0x7F80u) {  // an infinity or a NaN in this warp's values
+    m = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = fabsf(bf16_lo(v[e])), hi = fabsf(bf16_hi(v[e]));
-      if (lo < INFINITY) m = fmaxf(m, lo);
-      if (hi < INFINITY) m = fmaxf(m, hi);
-    }
+    for (int i = 0; i < kUnits; ++i) m = finite_bits(m, w[i]);
+    m = warp_max(m);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   if (lane == 0) s_max[warp] = m;
-  const float s_old = r0 > 0 ? __ldcg(scale) : 0.f;
   __syncthreads();  // the maxima, and everyone has read the old scale
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) m = fmaxf(m, s_max[i]);
-  const float s = fmaxf(s_old, m / 127.f);
-  if (tid == 0) *scale = s;
+  for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, s_max[i]);
+  const Quantizer qz(fmaxf(s_old, scale_for(m)));
+  if (tid == 0) *scale = qz.s;
 
-  if (s > s_old) {
-    // Rows the page holds already, on the coarser scale.
-    for (int u = tid; u < r0 * (D / 4); u += kAppendThreads) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(codes) + u;
-      const uint32_t c4 = __ldcg(p);
-      uint32_t out = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float c = static_cast<float>(static_cast<int8_t>(c4 >> (8 * e)));
-        const float hi = c * s_old;
-        out |= (static_cast<uint32_t>(code_of(hi, fmaf(c, s_old, -hi), s)) & 255u) << (8 * e);
-      }
-      *p = out;
-    }
+  if (qz.s > s_old) {  // rows the page holds already, on the coarser scale
+    requantize(codes, f.r0 * (D / 16), qz, s_old, tid, kAppendThreads);
   }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int u = tid + i * kAppendThreads;
-    if (u >= units) continue;
-    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    uint32_t out[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float f = (e & 1) ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]);
-      out[e >> 2] |= (static_cast<uint32_t>(code_of(f, 0.f, s)) & 255u) << (8 * (e & 3));
+    if (u < units) *reinterpret_cast<uint2*>(codes + (size_t)f.r0 * D + (size_t)u * 8) = qz.codes(w[i]);
+  }
+  __syncthreads();  // before the next head's maxima
+  }
+}
+
+// The same for few rows a page: a warp takes one head at a time and reads its
+// rows twice.
+constexpr int kStepThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kStepThreads) append_step_int8_kernel(const __grid_constant__ AppendArgs a) {
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = blockIdx.y;
+  const Found f = find_page<kStepThreads>(a, blockIdx.x);
+  if (f.page < 0) return;
+  constexpr int kPerRow = D / 8;
+  const int units = (f.r1 - f.r0) * kPerRow;
+  for (int head = warp; head < a.Hkv; head += kStepThreads / 32) {
+    const uint16_t* x = a.x[kv] + f.row0 * a.token_stride[kv] + head * a.head_stride[kv];
+    const size_t slot = (size_t)f.page * a.Hkv + head;
+    int8_t* codes = a.codes[kv] + slot * a.page * D;
+    float* scale = a.scales[kv] + slot;
+    const float s_old = f.r0 > 0 ? __ldcg(scale) : 0.f;
+    auto unit = [&](int u) {
+      return __ldcg(reinterpret_cast<const uint4*>(x + (u / kPerRow) * a.token_stride[kv] + (u % kPerRow) * 8));
+    };
+    uint32_t m = 0;
+    for (int u = lane; u < units; u += 32) m = max_bits(m, unit(u));
+    m = warp_max(one_half(m));
+    if (m >= 0x7F80u) {
+      m = 0;
+      for (int u = lane; u < units; u += 32) m = finite_bits(m, unit(u));
+      m = warp_max(m);
     }
-    *reinterpret_cast<uint2*>(codes + (size_t)r0 * D + (size_t)u * 8) = make_uint2(out[0], out[1]);
+    const Quantizer qz(fmaxf(s_old, scale_for(m)));
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *scale = qz.s;
+    if (qz.s > s_old) requantize(codes, f.r0 * (D / 16), qz, s_old, lane, 32);
+    for (int u = lane; u < units; u += 32)
+      *reinterpret_cast<uint2*>(codes + (size_t)f.r0 * D + (size_t)u * 8) = qz.codes(unit(u));
   }
 }
 
@@ -211,72 +364,98 @@ struct ReadArgs {
   int B, T, Hkv, P, page, page_shift, max_blocks;
 };
 
-constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 16;  // packed tokens per CTA
+constexpr int kReadWarps = 8;
+constexpr int kReadCu = 1024;
+constexpr int kReadTimes = 4;
 
-// A CTA reads kReadTokens packed tokens' rows of every head, 16 codes at a
-// time.  Positions without a valid page read as zeros.
+// A lane reads 4 codes for FP32 values, 8 for BF16, and writes 16 bytes; a row of
+// a head is D / that many lanes, and a warp takes as many tokens at a time as it
+// has rows' worth of lanes, head by head.  Positions without a valid page read as
+// zeros.
 template <int D, bool FP32>
-__global__ void __launch_bounds__(kReadThreads) read_int8_kernel(const ReadArgs a) {
-  griddep_launch_dependents();
+struct ReadCfg {
+  static constexpr int kCodes = FP32 ? 4 : 8;
+  static constexpr int kLanes = D / kCodes;
+  static constexpr int kAtOnce = 32 / kLanes;              // tokens of a warp at a time
+  static constexpr int kTokens = kReadWarps * kAtOnce;     // of a CTA at a time
+};
+template <int D, bool FP32>
+__global__ void __launch_bounds__(32 * kReadWarps) read_int8_kernel(const __grid_constant__ ReadArgs a, int times) {
+  using C = ReadCfg<D, FP32>;
   griddep_wait();
-  __shared__ long long s_row[kReadTokens];  // page * Hkv * page_size + row in page, or -1
-  const int tid = threadIdx.x, kv = blockIdx.y;
-  const int t0 = blockIdx.x * kReadTokens;
-  if (tid < kReadTokens && t0 + tid < a.T) {
-    const int t = t0 + tid;
+  __shared__ long long s_row[kReadTimes * C::kTokens];  // row of the pool's head 0 in the token's page, or -1
+  __shared__ int s_cu[kReadCu];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kv = blockIdx.y;
+  const int t0 = blockIdx.x * times * C::kTokens;
+  // The search runs in shared memory where the sequences' ends fit it.
+  const bool near_cu = a.B < kReadCu;
+  if (near_cu) {
+    for (int b = tid; b <= a.B; b += 32 * kReadWarps) s_cu[b] = __ldcg(a.cu + b);
+    __syncthreads();
+  }
+  auto cu = [&](int b) { return near_cu ? s_cu[b] : __ldcg(a.cu + b); };
+  for (int i = tid; i < times * C::kTokens && t0 + i < a.T; i += 32 * kReadWarps) {
+    const int t = t0 + i;
     int lo = 0, hi = a.B;  // the last sequence that begins at or before t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldcg(a.cu + mid) <= t) lo = mid; else hi = mid;
+      if (cu(mid) <= t) lo = mid; else hi = mid;
     }
     long long row = -1;
-    const int first = __ldcg(a.cu + lo);
-    if (t >= first && t < __ldcg(a.cu + lo + 1)) {
+    const int first = cu(lo);
+    if (t >= first && t < cu(lo + 1)) {
       const long long pos = (long long)max(__ldcg(a.starts + lo), 0) + (t - first);
       const long long blk = pos >> a.page_shift;
       const int id = blk < a.max_blocks ? __ldcg(a.table + (size_t)lo * a.max_blocks + blk) : -1;
       if (id >= 0 && id < a.P)
         row = ((long long)id * a.Hkv << a.page_shift) + (pos & (a.page - 1));
-      else
-        set_fail(ATTN_ERR_INVALID_ARG);
-    } else {
-      set_fail(ATTN_ERR_INVALID_ARG);
     }
-    s_row[tid] = row;
+    if (row < 0) set_fail(ATTN_ERR_INVALID_ARG);
+    s_row[i] = row;
   }
   __syncthreads();
-  constexpr int kPerRow = D / 16;
-  const int per_token = a.Hkv * kPerRow;
-  const int n = min(kReadTokens, a.T - t0) * per_token;
-  for (int u = tid; u < n; u += kReadThreads) {
-    const int t = u / per_token, rest = u - t * per_token;
-    const int head = rest / kPerRow, col = rest % kPerRow;
-    uint4 c4 = make_uint4(0u, 0u, 0u, 0u);
-    float s = 0.f;
-    if (s_row[t] >= 0) {
-      const long long row = s_row[t] + ((long long)head << a.page_shift);
-      c4 = __ldcg(reinterpret_cast<const uint4*>(a.codes[kv] + row * D + col * 16));
-      s = __ldcg(a.scales[kv] + (row >> a.page_shift));
-    }
-    const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-    float f[16];
+  const int col = lane % C::kLanes * C::kCodes;
+  const int8_t* codes = a.codes[kv] + col;
+  const float* scales = a.scales[kv];
+  for (int i = 0; i < times; ++i) {
+    const int t = (i * kReadWarps + warp) * C::kAtOnce + lane / C::kLanes;
+    if (t0 + t >= a.T) continue;
+    const long long at = s_row[t];
+    const bool have = at >= 0;
+    const long long row = have ? at : 0;
+    const size_t out = (size_t)(t0 + t) * a.Hkv * D + col;
+#pragma unroll 4
+    for (int h = 0; h < a.Hkv; ++h) {
+      const long long r = row + ((long long)h << a.page_shift);
+      const float s = have ? __ldcg(scales + (r >> a.page_shift)) : 0.f;
+      uint32_t c[C::kCodes / 4];
+      if constexpr (FP32) {
+        c[0] = __ldcg(reinterpret_cast<const uint32_t*>(codes + r * D));
+      } else {
+        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(codes + r * D));
+        c[0] = v.x, c[1] = v.y;
+      }
+      float f[C::kCodes];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      f[e] = static_cast<float>(static_cast<int8_t>(c[e >> 2] >> (8 * (e & 3)))) * s;
-    const size_t o = ((size_t)(t0 + t) * a.Hkv + head) * D + col * 16;
-    if (FP32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out[kv]) + o);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-    } else {
-      uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[kv]) + o);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        p[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                          pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+      for (int e = 0; e < C::kCodes; ++e)
+        f[e] = have ? static_cast<float>(static_cast<int8_t>(c[e >> 2] >> (8 * (e & 3)))) * s : 0.f;
+      if constexpr (FP32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out[kv]) + out + h * D) = make_float4(f[0], f[1], f[2], f[3]);
+      else
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[kv]) + out + h * D) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
     }
   }
+}
+
+template <int D, bool FP32>
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t stream) {
+  // Up to kReadTimes rounds a CTA, fewer while that leaves SMs without 8 CTAs.
+  const int sms = device_sm_count(), once = ceil_div(a.T, ReadCfg<D, FP32>::kTokens);
+  const int times = std::max(1, std::min(kReadTimes, sms > 0 ? once * 2 / (sms * 8) : 1));
+  return launch_pdl(read_int8_kernel<D, FP32>, dim3(ceil_div(once, times), 2), dim3(32 * kReadWarps), 0, stream, a,
+                    times);
 }
 
 }  // namespace
@@ -300,7 +479,17 @@ cudaError_t launch_cache_append_int8(const PagedCache& c, const void* k, const v
   a.page_shift = page_shift(c.page);
   // A token touches one page at most, a sequence of n tokens (n - 1) / page + 2.
   const long long pages = (long long)T / c.page + 2ll * c.B;
-  const dim3 grid((unsigned)(pages < T ? pages : T), c.Hkv, 2);
+  const unsigned most = (unsigned)(pages < T ? pages : T);
+  // A step appends a row or a few to every sequence.
+  if ((long long)T <= (long long)kStepRows * c.B) {
+    auto kernel = c.d == 128 ? append_step_int8_kernel<128> : append_step_int8_kernel<64>;
+    return launch_pdl(kernel, dim3(most, 2), dim3(kStepThreads), 0, stream, a);
+  }
+  // As many heads a CTA as make one wave of 8 CTAs an SM: the search for the page
+  // takes as long as a head's rows.
+  const int sms = device_sm_count();
+  const long long waves = sms > 0 ? ((long long)most * c.Hkv * 2 + sms * 8ll - 1) / (sms * 8ll) : 1;
+  const dim3 grid(most, ceil_div(c.Hkv, (int)std::min<long long>(waves, c.Hkv)), 2);
   const int units = ceil_div(c.page * c.d / 8, kAppendThreads);
 #define ATTN_APPEND_CASE(DD, UU) \
   if (c.d == DD && units == UU)  \
@@ -331,12 +520,8 @@ cudaError_t launch_cache_read_int8(const PagedCache& c, const int* cu, const int
   a.starts = starts;
   a.B = c.B, a.T = T, a.Hkv = c.Hkv, a.P = c.P, a.page = c.page, a.max_blocks = c.max_blocks;
   a.page_shift = page_shift(c.page);
-  const dim3 grid(ceil_div(T, kReadTokens), 2);
-  if (c.d == 128)
-    return fp32 ? launch_pdl(read_int8_kernel<128, true>, grid, dim3(kReadThreads), 0, stream, a)
-                : launch_pdl(read_int8_kernel<128, false>, grid, dim3(kReadThreads), 0, stream, a);
-  return fp32 ? launch_pdl(read_int8_kernel<64, true>, grid, dim3(kReadThreads), 0, stream, a)
-              : launch_pdl(read_int8_kernel<64, false>, grid, dim3(kReadThreads), 0, stream, a);
+  if (c.d == 128) return fp32 ? launch_read<128, true>(a, stream) : launch_read<128, false>(a, stream);
+  return fp32 ? launch_read<64, true>(a, stream) : launch_read<64, false>(a, stream);
 }
 
 cudaError_t read_and_clear_status_cache(unsigned int* out, cudaStream_t stream) {

@@ -216,6 +216,33 @@ def test_append(A, page, d):
         assert c.equal()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 64])
+def test_append_few_rows(A, page, d):
+    """A step: a row or a few a sequence, more heads than warps, scales that grow by little and by much
+    (held codes on and next to the border), special values."""
+    Hkv = 11
+    starts = [0, 1, 5, page - 1, 2 * page, 3 * page - 2, 9, 0, 13, 15]
+    lens = [1, 1, 2, 2, 1, 5, 0, page + 2, 1, 1]
+    tables, pages = scattered([-(-(s + n) // page) for s, n in zip(starts, lens)], 21)
+    c = Cache(pages, Hkv, page, d, tables)
+    T, cu = sum(lens), sums(lens)
+    assert T <= 8 * len(lens) or page > 16
+    g = torch.Generator().manual_seed(9)
+    rows = [normal((T, Hkv, d), i) * torch.exp(2 * torch.randn(T, Hkv, 1, generator=g)).to(BF) for i in (1, 2)]
+    rows[0][2, 3, 4], rows[0][2, 4, 4], rows[1][2, 5, 0] = torch.nan, torch.inf, -torch.inf
+    c.scales[0][tables[2][0]] = 2.0 ** -6  # doubled exactly: every odd code is a tie
+    rows[0][2:4] = 0
+    rows[0][2:4, :, 7] = 127 * 2.0 ** -5
+    c.upload()
+    c.append(rows, cu, starts)
+    args = (rows[0].cuda(), rows[1].cuda(), *c.gpu, ints(cu), ints(starts))
+    for _ in range(2):
+        A.attn_cache_append_int8(*args)
+        A.attn_check_status()
+        assert c.equal()
+
+
 def test_append_views_zeros_and_special_values(A):
     """Rows of a fused projection; rows of zeros on a fresh page; a NaN and infinities stay out of the
     scale and become 0 and +-127; tiny and huge values."""
