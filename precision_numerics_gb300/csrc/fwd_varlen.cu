@@ -19,8 +19,9 @@
 //    sequence.  Their scores are masked; their V rows, which P = 0 would turn
 //    into NaN if they held an infinity or a NaN, are overwritten with zeros by
 //    the MMA warp before the P V product reads the tile (only in such tiles).
-//  - Output rows are written from registers, since a tile's last tokens may
-//    belong to the next sequence's tile.
+//  - A tile's last tokens may belong to the next sequence's tile, so output rows
+//    are written one by one, 8 lanes a 128-byte line, after a turn through shared
+//    memory that gives each lane 16 bytes of it.
 //
 // Bound, as in fwd_bf16.cu, by the softmax and its hand-over to the tensor pipe
 // for long sequences, and by the latency of an item's chain for short ones.
@@ -137,7 +138,9 @@ struct Cfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+  // Output staging: 32 rows x 128 bytes per softmax warp.
+  static constexpr int kOffStage = kOffV + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffStage + 8 * 32 * 128;
   // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S],
   // s_full[2], p_full[2], o_done[2], mma_final, alpha[2][4]
   static constexpr int kNumBars = 2 + 4 * kStages + 15;
@@ -147,6 +150,15 @@ struct Cfg {
   static __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
   static __device__ __forceinline__ uint32_t col_o(int t) { return 256u + D * t; }
 };
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(saddr)
+               : "memory");
+  return v;
+}
 
 // Item of round r for this CTA: the list is dealt in snake order (CTA c takes
 // item c of round 0, item G-1-c of round 1, ...), so that heavy and light items
@@ -164,12 +176,15 @@ struct Item {
 };
 template <bool CAUSAL>
 __device__ __forceinline__ Item load_item(const int* __restrict__ plan, int L, int Hkv, int tq) {
-  const int4 p = __ldcg(reinterpret_cast<const int4*>(plan + kPlanHeader) + L / Hkv);
+  // Through L1: the producer, which runs ahead, has brought the line by the time
+  // the other roles ask for it.
+  const int at = L / Hkv;
+  const int4 p = *(reinterpret_cast<const int4*>(plan + kPlanHeader) + at);
   Item it;
   it.first = p.x;
   it.len = p.y;
   it.q0 = p.z;
-  it.head = L % Hkv;
+  it.head = L - at * Hkv;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int q = it.q0 + t * tq;
@@ -455,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;  // query row within the tile = TMEM lane
     const int row_tok = r / G, row_head = r - row_tok * G;
     const bool row_used = row_tok < tq;
+    const uint32_t by_G = (65536u + G - 1) / G;  // (x * by_G) >> 16 is x / G for x < 128, G <= 128
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::col_s(t);
     const uint32_t tO = tmem + lane_off + C::col_o(t);
@@ -548,25 +564,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t il2 = f2_pack(inv_l, inv_l);
       const bool have = row_used && tok < it.len;
       const size_t row_at = (size_t)(it.first + tok) * H + it.head * G + row_head;
-      uint4* row = reinterpret_cast<uint4*>(out + row_at * D);
+      const uint32_t stage = smem_u32(smem + C::kOffStage) + (warp - 4) * 32 * 128;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + c * 32, o);
-        tmem_wait_ld();
-        reg_fence(o);
-        uint32_t pk[16];
+      for (int c = 0; c < C::kChunks; ++c) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float lo, hi;
-          f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il2), lo, hi);
-          pk[i] = pack_bf16x2(lo, hi);
-        }
-        if (have) {
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 64 + h * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float lo, hi;
+            f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il2), lo, hi);
+            pk[i] = pack_bf16x2(lo, hi);
+          }
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            row[c * 4 + u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+            st_shared_v4(stage + sw128_offset(lane, h * 4 + u), pk[4 * u], pk[4 * u + 1], pk[4 * u + 2],
+                         pk[4 * u + 3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3);  // row of this warp's 32
+          const int tile_row = (warp & 3) * 32 + rr;
+          const int rt = (int)(((uint32_t)tile_row * by_G) >> 16), rh = tile_row - rt * G;
+          if (rt < tq && q_first + rt < it.len) {
+            const uint4 v = ld_shared_v4(stage + sw128_offset(rr, lane & 7));
+            *reinterpret_cast<uint4*>(out + ((size_t)(it.first + q_first + rt) * H + it.head * G + rh) * D + c * 64 +
+                                      (lane & 7) * 8) = v;
+          }
+        }
+        __syncwarp();
       }
       if (have) lse[row_at] = m_run * scale + logf(l_run);
     }
