@@ -13,6 +13,8 @@ layouts.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 
@@ -89,6 +91,23 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     if path == _build.LIB:
         _LIB = lib
     return lib
+
+
+_BINDING = None
+
+
+def _binding():
+    """The module _attn_torch (csrc/torch_calls.cpp): the serving calls in C++."""
+    global _BINDING
+    if _BINDING is None:
+        load_library()
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+                               "(python -m precision_numerics_gb300.build)")
+        loader = importlib.machinery.ExtensionFileLoader("_attn_torch", path)
+        _BINDING = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn_torch", loader))
+    return _BINDING
 
 
 def _status_string(status: int) -> str:
@@ -360,6 +379,10 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, scale=None, causal=False, 
 # include/attn.h states the layouts.  A cache is the five tensors (k_cache,
 # v_cache, k_scale, v_scale, block_table).  Tensors on another device than the
 # current one are refused by the library.
+#
+# A call on the current stream goes through the C++ binding first, which takes a
+# third of the time; it returns None where something is not as it should be, and
+# the function's own checks then find out what.
 
 # Each check first asks for everything at once, and looks for what is wrong only
 # then: attribute reads are most of what a call costs on the host.
@@ -453,6 +476,10 @@ def attn_varlen_fwd(q, k, v, plan, scale=None, causal=True, o=None, lse=None, st
     """Attention over packed prompts: q [T,H,d], k, v [T,H_kv,d] BF16 (rows contiguous,
     token and head strides free), plan of attn_varlen_plan.  Returns (o [T,H,d], lse [T,H]);
     rows that belong to no sequence are left as they are."""
+    if stream is None:
+        done = (_BINDING or _binding()).varlen_fwd(q, k, v, plan, scale, causal, o, lse)
+        if done is not None:
+            return done
     _check_packed_rows("q", q)
     _check_packed_rows("k", k)
     T, H, d = q.shape
@@ -481,6 +508,11 @@ def attn_cache_append_int8(k, v, k_cache, v_cache, k_scale, v_scale, block_table
                            stream=None):
     """Write the packed rows k, v [T,H_kv,d] BF16 behind the starts[b] positions that every
     sequence holds (see include/attn.h for the scales' rule).  Returns (k_cache, v_cache)."""
+    if stream is None:
+        done = (_BINDING or _binding()).cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
+                                                     cu_seqlens, starts)
+        if done is not None:
+            return done
     B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
     _check_packed_rows("k", k)
     T = k.shape[0]
@@ -499,6 +531,11 @@ def attn_cache_read_int8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq
                          dtype=torch.bfloat16, k=None, v=None, stream=None):
     """Values of positions starts[b] .. of every sequence, packed as cu_seqlens says (T tokens in
     all), in dtype bfloat16 or float32.  Returns (k, v) [T,H_kv,d]."""
+    if stream is None:
+        done = (_BINDING or _binding()).cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                   starts, T, dtype, k, v)
+        if done is not None:
+            return done
     B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
     _check_ints("cu_seqlens", cu_seqlens, B + 1)
     _check_ints("starts", starts, B)
@@ -527,6 +564,11 @@ def attn_decode_int8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens
                      lse=None, workspace=None, stream=None):
     """Attention of the newest n_q tokens q [B,n_q,H,d] BF16 over the cache; seqlens int32 [B]
     counts them in.  Returns (o [B,n_q,H,d], lse [B,n_q,H])."""
+    if stream is None:
+        done = (_BINDING or _binding()).decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, scale, o,
+                                               lse, workspace)
+        if done is not None:
+            return done
     B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a tensor [B, n_q, H, d]")

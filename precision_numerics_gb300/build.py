@@ -6,6 +6,10 @@ CUDA runtime linked statically.  build_test_variant() makes the test build
 (_lib/libattn_testhooks.so, objects under _build_testhooks/), which only the
 test suite loads.  A rebuild happens when any source or
 header is newer than the library.
+
+csrc/torch_calls.cpp becomes the Python module _lib/_attn_torch.<torch version>.so
+(g++ against the installed PyTorch's headers, linked to libattn.so beside it), the
+serving calls' binding; the ctypes binding of the whole C ABI needs no part of it.
 """
 from __future__ import annotations
 
@@ -16,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +30,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libattn.so")
+BINDING_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -43,7 +49,7 @@ def _sources():
 
 
 def _inputs():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + [BINDING_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
@@ -58,12 +64,20 @@ def lib_path(variant: str = "") -> str:
     return LIB if not variant else os.path.join(LIB_DIR, f"libattn_{variant}.so")
 
 
+def binding_path() -> str:
+    """The tensor binding of the installed PyTorch (another version has another ABI)."""
+    import torch
+    return os.path.join(LIB_DIR, f"_attn_torch.{torch.__version__}.so")
+
+
 def needs_build(variant: str = "") -> bool:
-    lib = lib_path(variant)
-    if not os.path.exists(lib):
-        return True
-    t = os.path.getmtime(lib)
-    return any(os.path.getmtime(p) > t for p in _inputs())
+    for lib in (lib_path(variant),) if variant else (lib_path(), binding_path()):
+        if not os.path.exists(lib):
+            return True
+        t = os.path.getmtime(lib)
+        if any(os.path.getmtime(p) > t for p in _inputs()):
+            return True
+    return False
 
 
 @contextlib.contextmanager
@@ -109,15 +123,50 @@ def _build_locked(lib, verbose, extra_flags, variant) -> str:
         return obj
 
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = None if variant else ex.submit(_compile_binding, build_dir)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding and binding.result()
     tmp = f"{lib}.tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {os.path.basename(lib)} failed:\n{r.stderr}\n{r.stdout}")
     os.replace(tmp, lib)
+    if binding_obj:
+        _link_binding(binding_obj)
     return lib
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr}\n{r.stdout}")
+
+
+def _compile_binding(build_dir) -> str:
+    obj = os.path.join(build_dir, "torch_calls.cpp.o")
+    include = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    _run([os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+          "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c", BINDING_SOURCE, "-o", obj],
+         "g++ on torch_calls.cpp")
+    return obj
+
+
+def _link_binding(obj) -> None:
+    path = binding_path()
+    tmp = f"{path}.tmp{os.getpid()}"
+    _run([os.environ.get("CXX") or "g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libattn.so",
+          "-Wl,-rpath,$ORIGIN", "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+          "-ltorch_cuda", "-lc10", "-lc10_cuda"], "link of the tensor binding")
+    os.replace(tmp, path)
 
 
 def build_test_variant(force: bool = False) -> str:

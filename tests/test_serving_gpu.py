@@ -544,3 +544,32 @@ def test_the_same_call_twice_gives_the_same_bits(A):
                *A.attn_varlen_fwd(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], plan))
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_calls_with_a_stream_given(A):
+    """The binding's two ways, with and without an explicit stream, and a scale that is no float."""
+    H, Hkv, d, page, lens = 4, 2, 64, 16, [70, 9]
+    T, cu = sum(lens), sums(lens)
+    x = normal((T, H + 2 * Hkv, d), 1).cuda()
+    q, k, v = x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+    tables, pages = scattered([5, 1], 3)
+    results = []
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream, scale in ((None, 1.0), (side, 1.0), (side.cuda_stream, 1.0), (None, 1)):
+        c = Cache(pages, Hkv, page, d, tables)
+        torch.cuda.synchronize()
+        plan = A.attn_varlen_plan(ints(cu), T, H, Hkv, stream=stream)
+        torch.cuda.synchronize()
+        got = [*A.attn_varlen_fwd(q, k, v, plan, scale=scale, stream=stream)]
+        args = ints(cu), ints([0, 0]), ints(lens)
+        qd = q[[lens[0] - 1, T - 1]].view(2, 1, H, d)
+        torch.cuda.synchronize()
+        assert A.attn_cache_append_int8(k, v, *c.gpu, *args[:2], stream=stream)[0] is c.gpu[0]
+        got += A.attn_cache_read_int8(*c.gpu, *args[:2], T, stream=stream)
+        got += A.attn_decode_int8(qd, *c.gpu, args[2], scale=scale, stream=stream)
+        torch.cuda.synchronize()
+        results.append(got)
+    for got in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], got))
+    A.attn_check_status()
