@@ -185,10 +185,15 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t m) { return __reduce_max_s
 __device__ __forceinline__ float scale_for(uint32_t bits) { return __uint_as_float(bits << 16) / 127.f; }
 
 // Sequence b's new rows: `first` is its first row of the packed input, n their
-// number (clamped to the rows there are, whatever cu_seqlens holds).
-__device__ __forceinline__ void new_rows(const int* cu, int b, int T, int& first, int& n) {
-  first = min(max(__ldcg(cu + b), 0), T);
-  n = min(max(__ldcg(cu + b + 1), first), T) - first;
+// number, `start` the position of the first (clamped to what there is, whatever
+// the lengths in memory are).
+__device__ __forceinline__ void new_rows(const int* cu, const int* starts, int b, int T, int& first, int& n,
+                                         int& start) {
+  const int x = __ldcg(cu + b), y = __ldcg(cu + b + 1), z = __ldcg(starts + b);
+  if (x < 0 || y < x || y > T || z < 0) set_fail(ATTN_ERR_INVALID_ARG);
+  first = min(max(x, 0), T);
+  n = min(max(y, first), T) - first;
+  start = max(z, 0);
 }
 
 struct AppendArgs {
@@ -219,8 +224,7 @@ __device__ __forceinline__ Found find_page(const AppendArgs& a, int item) {
     const int b = b0 + tid;
     int first = 0, n = 0, start = 0, count = 0;
     if (b < a.B) {
-      start = max(__ldcg(a.starts + b), 0);
-      new_rows(a.cu, b, a.T, first, n);
+      new_rows(a.cu, a.starts, b, a.T, first, n, start);
       if (n > 0) count = ((n - 1 + (start & (a.page - 1))) >> a.page_shift) + 1;
     }
     int upto = count;
@@ -404,9 +408,9 @@ __global__ void __launch_bounds__(32 * kReadWarps) read_int8_kernel(const __grid
     long long row = -1;
     const int first = cu(lo);
     if (t >= first && t < cu(lo + 1)) {
-      const long long pos = (long long)max(__ldcg(a.starts + lo), 0) + (t - first);
+      const long long pos = (long long)__ldcg(a.starts + lo) + (t - first);
       const long long blk = pos >> a.page_shift;
-      const int id = blk < a.max_blocks ? __ldcg(a.table + (size_t)lo * a.max_blocks + blk) : -1;
+      const int id = pos >= 0 && blk < a.max_blocks ? __ldcg(a.table + (size_t)lo * a.max_blocks + blk) : -1;
       if (id >= 0 && id < a.P)
         row = ((long long)id * a.Hkv << a.page_shift) + (pos & (a.page - 1));
     }

@@ -433,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     ++ld_k;
   };
   if (more) look_up();
+#pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) issue();
 
   const int rows_total = a.n_q * a.G;
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
     __syncthreads();
     // rows x 64 columns over 128 threads, 4 columns at a time.
-#pragma unroll
+#pragma unroll 1
     for (int x = threadIdx.x; x < kRows * 16; x += kThreads) {
       const int r = x >> 4, part4 = x & 15;
       float M = -INFINITY, L = 0.f, v[4] = {};
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args a, int rows, int per_row) {
-  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
+  __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
   const int4 ch = __ldcg(reinterpret_cast<const int4*>(a.chains) + blockIdx.x);  // more, b, hr, cta
@@ -729,38 +730,66 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
   const int rr = ch.z % a.row_blocks * rows + r;
   const bool have = r < rows && rr < a.n_q * a.G;
   const int n = have ? ch.x + 1 : 0;
-  auto part = [&](int i) { return a.parts + (size_t)(2 * (ch.w + i) + (i == 0)) * part_floats(D, rows); };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + rows * D + r));
+  // kBatch parts at a time, all their loads in flight together.
+  constexpr int kBatch = 8;
+  float M = -INFINITY, L = 0.f, o[D / 32] = {};
+  for (int i0 = warp % per_row; i0 < n; i0 += kBatch * per_row) {
+    float m[kBatch], l[kBatch], x[kBatch][D / 32];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float M_use = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[D / 32] = {};
-#pragma unroll 8
-  for (int i = warp % per_row; i < n; i += per_row) {
-    const float* p = part(i);
-    const float f = ex2(__ldcg(p + rows * D + r) - M_use);
-    L += f * __ldcg(p + rows * D + rows + r);
-    const float* x = p + r * D + lane * (D / 32);
-    if constexpr (D == 128) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(x));
-      o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(x));
-      o[0] += f * v.x, o[1] += f * v.y;
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * per_row;
+      m[k] = -INFINITY, l[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x[k][e] = 0.f;
+      if (i < n) {
+        const float* p = a.parts + (size_t)(2 * (ch.w + i) + (i == 0)) * part_floats(D, rows);
+        m[k] = __ldcg(p + rows * D + r);
+        l[k] = __ldcg(p + rows * D + rows + r);
+        const float* q = p + r * D + lane * (D / 32);
+        if constexpr (D == 128) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(q));
+          x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(q));
+          x[k][0] = v.x, x[k][1] = v.y;
+        }
+      }
+    }
+    float m_new = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) m_new = fmaxf(m_new, m[k]);
+    const float m_use = m_new == -INFINITY ? 0.f : m_new;
+    const float keep = ex2(M - m_use);
+    M = m_new;
+    L *= keep;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] *= keep;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float f = ex2(m[k] - m_use);
+      L += f * l[k];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] += f * x[k][e];
     }
   }
   if (per_row > 1) {  // the same for all warps
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) s_o[warp][lane * (D / 32) + e] = o[e];
-    if (lane == 0) s_l[warp] = L;
+    if (lane == 0) s_m[warp] = M, s_l[warp] = L;
     __syncthreads();
     if (warp > 0) return;
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
-      L += s_l[w];
+    for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w]);
+    const float m_use = M == -INFINITY ? 0.f : M;
+    L = 0.f;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] += s_o[w][lane * (D / 32) + e];
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = ex2(s_m[w] - m_use);
+      L += f * s_l[w];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] += f * s_o[w][lane * (D / 32) + e];
     }
   }
   if (!have) return;

@@ -326,6 +326,14 @@ def test_bad_pages_are_reported_and_skipped(A):
     with pytest.raises(A.AttnError, match="out of range"):
         A.attn_check_status()
     assert (k[16:48] == 0).all() and torch.equal(k[:16].cpu(), c.values(0, 0, 16).float())
+    # Lengths that run backwards or past T, negative starts.
+    for cu, starts in (([0, 40, 30], [0, 0]), ([0, 10, 70], [0, 0]), ([0, 16, 16], [-1, 0])):
+        A.attn_cache_append_int8(rows[0].cuda(), rows[1].cuda(), *c.gpu, ints(cu), ints(starts))
+        with pytest.raises(A.AttnError, match="out of range"):
+            A.attn_check_status()
+        A.attn_cache_read_int8(*c.gpu, ints(cu), ints(starts), 64)
+        with pytest.raises(A.AttnError, match="out of range"):
+            A.attn_check_status()
     # Beyond the table's width.
     A.attn_cache_append_int8(rows[0].cuda(), rows[1].cuda(), *c.gpu, ints([0, 32, 64]), ints([30, 2**31 - 1]))
     with pytest.raises(A.AttnError, match="out of range"):
@@ -481,6 +489,31 @@ def test_decode_refusals(A):
         A.attn_decode_int8(normal((1, 1, 5, 64), 0).cuda(), *c.gpu, ints([5]))
 
 
+def test_cache_beyond_four_gib(A):
+    """Pages whose bytes lie past 2^32 (and whose rows' number times d does)."""
+    Hkv, page, d, H = 8, 128, 128, 16
+    pages = 2 ** 32 // (Hkv * page * d) + 40
+    last = [pages - 1, pages - 3, pages - 2, 5, pages - 7]
+    k_cache, v_cache = (torch.zeros((pages, Hkv, page, d), dtype=torch.int8, device="cuda") for _ in range(2))
+    k_scale, v_scale = (torch.zeros((pages, Hkv), device="cuda") for _ in range(2))
+    c = Cache(5, Hkv, page, d, [[0, 1, 2, 3, 4]])  # the same five pages, small enough for the host
+    for i, (codes, scale) in enumerate(((k_cache, k_scale), (v_cache, v_scale))):
+        codes[last], scale[last] = c.codes[i].cuda(), c.scales[i].cuda()
+    gpu = k_cache, v_cache, k_scale, v_scale, ints([last])
+    n, new = 500, 20
+    rows = [normal((new, Hkv, d), 1), normal((new, Hkv, d), 2)]
+    c.append(rows, [0, new], [n])
+    A.attn_cache_append_int8(rows[0].cuda(), rows[1].cuda(), *gpu, ints([0, new]), ints([n]))
+    A.attn_check_status()
+    assert all(torch.equal(x[last].cpu(), y) for x, y in zip(gpu, c.codes + c.scales))
+    k, _ = A.attn_cache_read_int8(*gpu, ints([0, n + new]), ints([0]), n + new, dtype=torch.float32)
+    assert torch.equal(k.cpu(), c.values(0, 0, n + new).float())
+    q = normal((1, 1, H, d), 3)
+    o, lse = A.attn_decode_int8(q.cuda(), *gpu, ints([n + new]))
+    A.attn_check_status()
+    check_decode(c, q, [n + new], 1 / math.sqrt(d), o, lse)
+
+
 # ----------------------------------------------------------------- together
 def test_prompt_then_steps(A):
     """A serving run: prompts attend and enter the cache, then tokens are appended and attend over it,
@@ -529,6 +562,27 @@ def test_prompt_then_steps(A):
             c.append([rows[:, H:H + Hkv], rows[:, H + Hkv:]], [2 * b for b in range(B + 1)], [n + 2 * s for n in lens])
             assert c.equal()
             check_decode(c, x[:, :, :H], [n + 2 * s + 2 for n in lens], 1 / math.sqrt(d), o, lse)
+
+
+def test_prompts_in_a_graph(A):
+    """The plan and the attention captured once, replayed on other lengths of the same total."""
+    H, Hkv, d, T = 4, 1, 64, 400
+    x = normal((T, H + 2 * Hkv, d), 1)
+    cu = ints([0, 100, 200, 300, 400])
+    o, lse = torch.zeros((T, H, d), dtype=BF, device="cuda"), torch.zeros((T, H), device="cuda")
+    plan = torch.empty(A.attn_varlen_plan_bytes(4, T, H, Hkv), dtype=torch.uint8, device="cuda")
+    y = x.cuda()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        A.attn_varlen_plan(cu, T, H, Hkv, plan=plan)
+        A.attn_varlen_fwd(y[:, :H], y[:, H:H + Hkv], y[:, H + Hkv:], plan, o=o, lse=lse)
+    for lens in ([100] * 4, [399, 0, 0, 1], [1, 129, 128, 142]):
+        cu.copy_(ints(sums(lens)))
+        graph.replay()
+        A.attn_check_status()
+        check_prompt(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], lens, True, 1 / math.sqrt(d), o, lse)
 
 
 def test_the_same_call_twice_gives_the_same_bits(A):
