@@ -268,6 +268,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   float* s_merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* s_m = reinterpret_cast<float*>(smem + C::kOffStat);
   float* s_l = s_m + kWarps * kRows;
+  // In the merge's buffer between merges: Q, then per row the factor of its scores
+  // and its last visible position.
+  uint2* s_q = reinterpret_cast<uint2*>(s_merge);
+  float* s_f = reinterpret_cast<float*>(s_q + NT * (D / 16) * 32);
+  int* s_last = reinterpret_cast<int*>(s_f + kRows);
 
   // No griddep_launch_dependents() here: the next launch of this kernel would fill
   // the slots that free up first and keep an uneven share of the SMs (one long
@@ -443,15 +448,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   // ------------------------------------------------------------------ Q rows
   // Row r of the block: token (rb * rows + r) / G, head (rb * rows + r) % G of the
   // group.  K step ks of the products covers head dims [16 ks, 16 ks + 16), of
-  // which this thread holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
-  // k = 2c + 8, 2c + 9 (the same assignment as the codes') of rows 8 n + g.  The
-  // scores and accumulators it holds are those of rows 8 n + 2 c + {0, 1}.
-  int my_last[NT][2];   // last visible position of those (-1: none)
-  float f_row[NT][2];   // factor of their scores, in base 2
-  uint32_t qf[NT][D / 16][2];
-  const int tiles = sg.count(warp);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  // which a lane holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
+  // k = 2c + 8, 2c + 9 (the same assignment as the codes') of rows 8 n + g.  Warp n
+  // prepares block n for all; the merge's buffer holds the fragments meanwhile.
+  for (int n = warp; n < NT; n += kWarps) {
     const int r = sg.rb * kRows + 8 * n + g;
     const bool have = r < rows_total;
     const int t = token_of(a, r), hq = sg.h * a.G + (r - t * a.G);
@@ -459,29 +459,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     uint2 w[D / 16];
     float m = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
+    for (int ks = 0; ks < D / 16; ++ks)
       w[ks] = have ? __ldcg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * c)) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
       m = fmaxf(fmaxf(m, fmaxf(fabsf(__uint_as_float(w[ks].x << 16)), fabsf(__uint_as_float(w[ks].x & 0xFFFF0000u)))),
                 fmaxf(fabsf(__uint_as_float(w[ks].y << 16)), fabsf(__uint_as_float(w[ks].y & 0xFFFF0000u))));
-    }
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
     const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u) - 127, -126), 126);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      qf[n][ks][0] = pack_f16x2(__uint_as_float(w[ks].x << 16) * down, __uint_as_float(w[ks].x & 0xFFFF0000u) * down);
-      qf[n][ks][1] = pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down);
-    }
-    const float f = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-    const int last = have ? sg.len - a.n_q + t : -1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f_row[n][i] = __shfl_sync(0xffffffffu, f, (2 * c + i) * 4);
-      my_last[n][i] = __shfl_sync(0xffffffffu, last, (2 * c + i) * 4);
+    for (int ks = 0; ks < D / 16; ++ks)
+      s_q[(n * (D / 16) + ks) * 32 + lane] =
+          make_uint2(pack_f16x2(__uint_as_float(w[ks].x << 16) * down, __uint_as_float(w[ks].x & 0xFFFF0000u) * down),
+                     pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down));
+    if (c == 0) {
+      s_f[8 * n + g] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+      s_last[8 * n + g] = have ? sg.len - a.n_q + t : -1;
     }
   }
+  __syncthreads();
+  // The scores and accumulators a lane holds are those of rows 8 n + 2 c + {0, 1}.
+  int my_last[NT][2];   // last visible position of those (-1: none)
+  float f_row[NT][2];   // factor of their scores, in base 2
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f_row[n][i] = s_f[8 * n + 2 * c + i];
+      my_last[n][i] = s_last[8 * n + 2 * c + i];
+    }
+  const int tiles = sg.count(warp);
 
   // ------------------------------------------------------------------ tiles
   float acc[D / 16][NT][4];  // head dims 16 u + 2 g + {0, 0, 1, 1}, rows 2 c + {0, 1, 0, 1}
@@ -518,20 +528,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     // and 1 are position g, 2 and 3 position g + 8.
     float s[2][NT][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.f;
 #pragma unroll
-      for (int u = 0; u < D / 16; u += 2) {
-        uint32_t r[4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
-        ldsm4(r, tK + unit_offset<D>(h * 16 + (lane & 15), u + (lane >> 4)));
+    for (int u = 0; u < D / 16; u += 2) {
+      uint32_t r[2][4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t b0 = r[2 * x] ^ 0x80808080u, b1 = r[2 * x + 1] ^ 0x80808080u;
+      for (int h = 0; h < 2; ++h) ldsm4(r[h], tK + unit_offset<D>(h * 16 + (lane & 15), u + (lane >> 4)));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint2 qf[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) qf[n] = s_q[(n * (D / 16) + u + x) * 32 + lane];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t b0 = r[h][2 * x] ^ 0x80808080u, b1 = r[h][2 * x + 1] ^ 0x80808080u;
           const uint32_t af[4] = {codes_f16(b0, 0x4140u), codes_f16(b1, 0x4140u), codes_f16(b0, 0x4342u),
                                   codes_f16(b1, 0x4342u)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(s[h][n], af, qf[n][u + x][0], qf[n][u + x][1]);
+          for (int n = 0; n < NT; ++n) mma_f16(s[h][n], af, qf[n].x, qf[n].y);
         }
       }
     }
@@ -657,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
 #pragma unroll
   for (int half = 0; half < D / 64; ++half) {
-    if (half > 0) __syncthreads();
+    __syncthreads();  // the buffer holds Q, or the other half, until here
     // Pairs of columns, moved by four for every second row, so that the 16 lanes
     // of a phase cover all banks.
 #pragma unroll
