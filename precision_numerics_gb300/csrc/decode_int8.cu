@@ -58,7 +58,7 @@ constexpr int kLeastRun = 4;     // tiles a CTA takes at least: one a warp
 // A segment's start and end (its Q rows, the merge of the warps, its output) take
 // as long as so many tiles: runs are measured in tiles plus this for each segment
 // that begins in them.
-constexpr int kSegmentCost = 10;
+constexpr int kSegmentCost = 8;
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_decode, code); }
 
@@ -99,16 +99,18 @@ __device__ __forceinline__ void copy4_arrive(uint32_t dst, const float* src, uin
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+template <int kOffset>
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(addr), "n"(kOffset)
                : "memory");
 }
+template <int kOffset>
 __device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(addr), "n"(kOffset)
                : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -204,6 +206,7 @@ __device__ __forceinline__ int cost_of(int len) { return len > 0 ? tiles_of(len)
 // rb), cost `left` behind them.
 struct Walk {
   int b, h, rb, len, ta, tb;
+  int len_next;  // of sequence b + 1, read ahead
   long long left;
   __device__ __forceinline__ int count(int warp) const {  // tiles of warp `warp`: ta + warp + kWarps * k
     return tb > ta + warp ? (tb - ta - warp + kWarps - 1) / kWarps : 0;
@@ -215,6 +218,7 @@ struct Walk {
     ta = max(from - kSegmentCost, 0);
     tb = max(to - kSegmentCost, 0);
   }
+  __device__ __forceinline__ void read_ahead(const Args& a) { len_next = b + 1 < a.B ? length_of(a, b + 1) : 0; }
   __device__ __forceinline__ bool next(const Args& a) {
     if (left <= 0) return false;
     if (++rb == a.row_blocks) {
@@ -223,7 +227,8 @@ struct Walk {
         h = 0;
         do {
           if (++b >= a.B) return false;
-          len = length_of(a, b);
+          len = len_next;
+          read_ahead(a);
         } while (len == 0);
       }
     }
@@ -231,6 +236,27 @@ struct Walk {
     return tb > 0;  // a run may end before the first tile
   }
 };
+
+// x / y, in 32 bits where they suffice.
+__device__ __forceinline__ long long divide(long long x, int y) {
+  return x <= 0xffffffffll ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+
+// Sequences without a position have no tile: their rows are empty.  The CTAs take
+// them by turns; len_first is the length of sequence blockIdx.x.
+template <int D>
+__device__ __forceinline__ void fill_empty(const Args& a, int len_first) {
+  const int copies = a.Hkv * a.row_blocks;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if ((b == blockIdx.x ? len_first : length_of(a, b)) > 0) continue;
+    const size_t row = (size_t)b * a.n_q * a.H;
+    for (int i = threadIdx.x; i < a.n_q * a.H * (D / 8); i += kThreads)
+      reinterpret_cast<uint4*>(a.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) a.lse[row + i] = -INFINITY;
+    if (a.by_segment)
+      for (int i = threadIdx.x; i < copies; i += kThreads) a.chains[(long long)b * copies + i] = Chain{0, 0, 0, 0};
+  }
+}
 
 // Sum over the CTA's threads before this one, and over all of them.
 __device__ __forceinline__ long long scan_before(long long x, long long* s_warp, long long& all) {
@@ -290,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   if (!ok && threadIdx.x == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
   Walk sg;
+  int len_first = 1;
   long long per = 0;  // cost of a run
   if (a.parts == nullptr) {
     const int x = blockIdx.x;
@@ -297,35 +324,45 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.h = (x / a.row_blocks) % a.Hkv;
     sg.b = x / a.row_blocks / a.Hkv;
     sg.len = length_of(a, sg.b);
+    sg.len_next = 0;
     sg.ta = 0;
     sg.tb = tiles_of(sg.len);
     sg.left = 0;
   } else {
-    // All segments' cost, and the sequence in which this CTA's run begins.
+    // All segments' cost, and the sequence in which this CTA's run begins.  The
+    // first kThreads sequences are read and scanned once.
     long long* s_warp = reinterpret_cast<long long*>(s_merge);
     const long long copies = (long long)a.Hkv * a.row_blocks;
-    long long total = 0, sum;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      scan_before(b < a.B ? cost_of(length_of(a, b)) : 0, s_warp, sum);
+    auto len_at = [&](int b) { return b < a.B ? length_of(a, b) : 0; };
+    int len = len_at(threadIdx.x);
+    len_first = len_at(blockIdx.x);  // for fill_empty, after the first loads are under way
+    long long total, sum;
+    long long ahead = scan_before(cost_of(len), s_warp, total);
+    const long long first = total;
+    for (int b0 = kThreads; b0 < a.B; b0 += kThreads) {
+      scan_before(cost_of(len_at(b0 + threadIdx.x)), s_warp, sum);
       total += sum;
     }
     total *= copies;
     // One run for every CTA that the SMs hold at a time: more and shorter runs cost
     // more to start than they even out (ragged batch 106 us, with two to a slot 110).
-    per = max((total + gridDim.x - 1) / gridDim.x, (long long)kLeastRun);
+    per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)kLeastRun);
     const long long begin = per * blockIdx.x;
     int4* s_start = reinterpret_cast<int4*>(s_m);
     if (threadIdx.x == 0) s_start[0].x = -1;
+    __syncthreads();
     long long before = 0;
     for (int b0 = 0; b0 < a.B && before <= begin; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      const int len = b < a.B ? length_of(a, b) : 0;
+      sum = first;
+      if (b0 > 0) {
+        len = len_at(b0 + threadIdx.x);
+        ahead = scan_before(cost_of(len), s_warp, sum);
+      }
       const int cost = cost_of(len);
-      const long long at = before + copies * scan_before(cost, s_warp, sum);
-      if (begin >= at && begin < at + copies * cost) {
-        const long long rest = begin - at;
-        s_start[0] = make_int4(b, len, (int)(rest / cost), (int)(rest % cost));
+      const long long rest = begin - before - copies * ahead;
+      if (rest >= 0 && rest < copies * cost) {
+        const long long copy = divide(rest, cost);
+        s_start[0] = make_int4(b0 + threadIdx.x, len, (int)copy, (int)(rest - copy * cost));
       }
       before += copies * sum;
     }
@@ -333,24 +370,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     const int4 st = s_start[0];
     __syncthreads();
     if (!a.by_segment && threadIdx.x == 0) a.chains[blockIdx.x] = Chain{0, 0, 0, 0};
-    // Sequences without a position have no tile: their rows are empty.
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-      if (length_of(a, b) > 0) continue;
-      const size_t row = (size_t)b * a.n_q * a.H;
-      for (int i = threadIdx.x; i < a.n_q * a.H * (D / 8); i += kThreads)
-        reinterpret_cast<uint4*>(a.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-      for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) a.lse[row + i] = -INFINITY;
-      if (a.by_segment)
-        for (int i = threadIdx.x; i < copies; i += kThreads) a.chains[b * copies + i] = Chain{0, 0, 0, 0};
+    if (st.x < 0) {  // more CTAs than runs
+      fill_empty<D>(a, len_first);
+      return;
     }
-    if (st.x < 0) return;  // more CTAs than runs
     sg.b = st.x;
     sg.len = st.y;
     sg.h = st.z / a.row_blocks;
     sg.rb = st.z % a.row_blocks;
     sg.left = min(per, total - begin);
+    sg.read_ahead(a);
     sg.take(st.w);
-    if (sg.tb == sg.ta) return;  // the run ends before the segment's first tile
+    if (sg.tb == sg.ta) {  // the run ends before the segment's first tile
+      fill_empty<D>(a, len_first);
+      return;
+    }
   }
 
   // ------------------------------------------------------------------ loads
@@ -362,8 +396,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   int id0 = -1, id1 = -1;        // pages of the two halves of tile ld_base + lane
   uint32_t issued = 0;
   bool more = ok;
+  int ids_b = -1, ids_ta = 0, ids_n = 0;  // what they were read for
   auto look_up = [&]() {
     ld_base = ld_k;
+    ids_b = lw.b, ids_ta = lw.ta, ids_n = ld_n;
     id0 = id1 = -1;
     const long long pos = ((long long)lw.ta + warp + (long long)kWarps * (ld_k + lane)) * kTile;
     if (ld_k + lane < ld_n) {
@@ -393,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       } while (more && ld_n == 0);
       if (!more) return;
       ld_k = 0;
-      look_up();
+      // The next key head of a sequence has the same pages: the lanes may hold them.
+      if (lw.b != ids_b || lw.ta != ids_ta || ld_base != 0 || ld_n > ids_n) look_up();
     } else if (ld_k - ld_base == 32) {
       look_up();
     }
@@ -440,8 +477,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   if (more) look_up();
 #pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) issue();
+  if (a.parts != nullptr) fill_empty<D>(a, len_first);
 
   const int rows_total = a.n_q * a.G;
+  // Rows of Q that this warp prepares (below), read ahead of their segment.
+  static_assert(NT <= kWarps, "a warp prepares one block of rows");
+  auto load_q = [&](const Walk& x, uint2 (&w)[D / 16]) {
+    const int r = x.rb * kRows + 8 * warp + g;
+    const int t = token_of(a, r), hq = x.h * a.G + (r - t * a.G);
+    const uint16_t* src = a.q + x.b * a.q_batch + t * a.q_token + hq * a.q_head;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+      w[ks] = warp < NT && r < rows_total ? __ldcg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * c))
+                                          : make_uint2(0u, 0u);
+  };
   uint32_t used = 0;
   bool last_segment = false;
   while (!last_segment) {
@@ -451,16 +500,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   // which a lane holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
   // k = 2c + 8, 2c + 9 (the same assignment as the codes') of rows 8 n + g.  Warp n
   // prepares block n for all; the merge's buffer holds the fragments meanwhile.
-  for (int n = warp; n < NT; n += kWarps) {
-    const int r = sg.rb * kRows + 8 * n + g;
-    const bool have = r < rows_total;
-    const int t = token_of(a, r), hq = sg.h * a.G + (r - t * a.G);
-    const uint16_t* src = a.q + sg.b * a.q_batch + t * a.q_token + hq * a.q_head;
+  if (warp < NT) {
     uint2 w[D / 16];
+    load_q(sg, w);
+    const int n = warp, r = sg.rb * kRows + 8 * n + g;
+    const bool have = r < rows_total;
+    const int t = token_of(a, r);
     float m = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      w[ks] = have ? __ldcg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * c)) : make_uint2(0u, 0u);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
       m = fmaxf(fmaxf(m, fmaxf(fabsf(__uint_as_float(w[ks].x << 16)), fabsf(__uint_as_float(w[ks].x & 0xFFFF0000u)))),
@@ -494,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   const int tiles = sg.count(warp);
 
   // ------------------------------------------------------------------ tiles
+  // Unit (lane / 16) of row lane % 16; unit u more is at this ^ (u << 4) for even u.
+  const uint32_t lane_unit = unit_offset<D>(lane & 15, lane >> 4);
   float acc[D / 16][NT][4];  // head dims 16 u + 2 g + {0, 0, 1, 1}, rows 2 c + {0, 1, 0, 1}
 #pragma unroll
   for (int u = 0; u < D / 16; ++u)
@@ -513,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     ok = warp_wait(&bars[st], (used / C::kStages) & 1);
     if (!ok) break;
     ++used;
-    const uint32_t tK = ring + st * C::kStageBytes, tV = tK + C::kHalfBytes;
+    const uint32_t tile = ring + st * C::kStageBytes;
     float ksc[2], vsc[2];
     uint32_t flags;
     {
@@ -534,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
     for (int u = 0; u < D / 16; u += 2) {
       uint32_t r[2][4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
-#pragma unroll
-      for (int h = 0; h < 2; ++h) ldsm4(r[h], tK + unit_offset<D>(h * 16 + (lane & 15), u + (lane >> 4)));
+      ldsm4<0>(r[0], tile + (lane_unit ^ (u << 4)));
+      ldsm4<16 * D>(r[1], tile + (lane_unit ^ (u << 4)));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         uint2 qf[NT];
@@ -553,23 +601,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
     // Scores in base 2; positions behind a row's last one are hidden.
     const int pos0 = (sg.ta + warp + kWarps * k) * kTile;
-    if (pos0 + kTile - 1 <= sg.len - a.n_q && flags == 3u) {
+    const bool hide = pos0 + kTile - 1 > sg.len - a.n_q || flags != 3u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[h][n][x] *= f_row[n][x & 1] * ksc[h];
+    if (hide) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[h][n][x] *= f_row[n][x & 1] * ksc[h];
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const bool seen = pos0 + h * 16 + (x >> 1) * 8 + g <= my_last[n][x & 1] && ((flags >> h) & 1u);
-            s[h][n][x] = seen ? s[h][n][x] * (f_row[n][x & 1] * ksc[h]) : -INFINITY;
-          }
+          for (int x = 0; x < 4; ++x)
+            if (pos0 + h * 16 + (x >> 1) * 8 + g > my_last[n][x & 1] || !((flags >> h) & 1u)) s[h][n][x] = -INFINITY;
       if (!(flags & 1u)) vsc[0] = 0.f;
       if (!(flags & 2u)) vsc[1] = 0.f;
     }
@@ -607,7 +653,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float p0 = ex2(s[h][n][2 * y] - m_use[0]), p1 = ex2(s[h][n][2 * y + 1] - m_use[1]);
+          const float p0 = ex2(s[h][n][2 * y] - m_use[0]);
+          const float p1 = ex2(s[h][n][2 * y + 1] - m_use[1]);
           l_run[n][0] += p0;
           l_run[n][1] += p1;
           pf[h][n][y] = transpose8(pack_f16x2(p0 * vr[h], p1 * vr[h]));
@@ -630,25 +677,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     // d = 16 u + 2 g (even bytes) and + 1 (odd bytes), rows g and g + 8 of the
     // A operand.
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int u = 0; u < D / 16; u += 2) {
+      uint32_t r[2][4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
+      ldsm4_trans<C::kHalfBytes>(r[0], tile + (lane_unit ^ (u << 4)));
+      ldsm4_trans<C::kHalfBytes + 16 * D>(r[1], tile + (lane_unit ^ (u << 4)));
 #pragma unroll
-      for (int u = 0; u < D / 16; u += 2) {
-        uint32_t r[4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
-        ldsm4_trans(r, tV + unit_offset<D>(h * 16 + (lane & 15), u + (lane >> 4)));
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint32_t b0 = r[2 * x] ^ 0x80808080u, b1 = r[2 * x + 1] ^ 0x80808080u;
+          const uint32_t b0 = r[h][2 * x] ^ 0x80808080u, b1 = r[h][2 * x + 1] ^ 0x80808080u;
           const uint32_t af[4] = {codes_f16(b0, 0x4240u), codes_f16(b0, 0x4341u), codes_f16(b1, 0x4240u),
                                   codes_f16(b1, 0x4341u)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma_f16(acc[u + x][n], af, pf[h][n][0], pf[h][n][1]);
         }
-      }
+    }
     __syncwarp();
     issue();
   }
 
   // ------------------------------------------------------------------ merge
+  Walk after = sg;
   const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len);
   float* part = nullptr;
   if (!whole) part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats(D, kRows);
@@ -686,6 +735,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * 64 + (((8 * u + g) ^ (c << 2)) << 1)) =
               make_float2(acc[half * 4 + u][n][i] * R, acc[half * 4 + u][n][2 + i] * R);
       }
+    if (half == D / 64 - 1) {
+      last_segment = !after.next(a);
+    }
     __syncthreads();
     // rows x 64 columns over 128 threads, 4 columns at a time.
 #pragma unroll 1
@@ -719,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
     }
   }
-  last_segment = !sg.next(a);
-  if (!last_segment) __syncthreads();  // before the next segment's m and l
+  sg = after;
+  if (!last_segment) __syncthreads();  // before the next segment's Q
   }  // segments
   if (!ok) {
     if (lane == 0) set_fail(ATTN_ERR_TIMEOUT);
