@@ -277,48 +277,48 @@ __global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const __gri
   const Found f = find_page<kAppendThreads>(a, blockIdx.x);
   if (f.page < 0) return;
   for (int head = blockIdx.y; head < a.Hkv; head += gridDim.y) {
-  const uint16_t* x = a.x[kv] + f.row0 * a.token_stride[kv] + head * a.head_stride[kv];
-  const size_t slot = (size_t)f.page * a.Hkv + head;
-  int8_t* codes = a.codes[kv] + slot * a.page * D;
-  float* scale = a.scales[kv] + slot;
+    const uint16_t* x = a.x[kv] + f.row0 * a.token_stride[kv] + head * a.head_stride[kv];
+    const size_t slot = (size_t)f.page * a.Hkv + head;
+    int8_t* codes = a.codes[kv] + slot * a.page * D;
+    float* scale = a.scales[kv] + slot;
 
-  constexpr int kPerRow = D / 8;
-  const int units = (f.r1 - f.r0) * kPerRow;
-  uint4 w[kUnits];
+    constexpr int kPerRow = D / 8;
+    const int units = (f.r1 - f.r0) * kPerRow;
+    uint4 w[kUnits];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int u = tid + i * kAppendThreads;
-    w[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (u < units)
-      w[i] = __ldcg(reinterpret_cast<const uint4*>(x + (u / kPerRow) * a.token_stride[kv] + (u % kPerRow) * 8));
-  }
-  const float s_old = f.r0 > 0 ? __ldcg(scale) : 0.f;
-  uint32_t m = 0;
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = tid + i * kAppendThreads;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (u < units)
+        w[i] = __ldcg(reinterpret_cast<const uint4*>(x + (u / kPerRow) * a.token_stride[kv] + (u % kPerRow) * 8));
+    }
+    const float s_old = f.r0 > 0 ? __ldcg(scale) : 0.f;
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) m = max_bits(m, w[i]);
-  m = warp_max(one_half(m));
-  if (m >= 0x7F80u) {  // an infinity or a NaN in this warp's values
-    m = 0;
+    for (int i = 0; i < kUnits; ++i) m = max_bits(m, w[i]);
+    m = warp_max(one_half(m));
+    if (m >= 0x7F80u) {  // an infinity or a NaN in this warp's values
+      m = 0;
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) m = finite_bits(m, w[i]);
-    m = warp_max(m);
-  }
-  if (lane == 0) s_max[warp] = m;
-  __syncthreads();  // the maxima, and everyone has read the old scale
+      for (int i = 0; i < kUnits; ++i) m = finite_bits(m, w[i]);
+      m = warp_max(m);
+    }
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();  // the maxima, and everyone has read the old scale
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, s_max[i]);
-  const Quantizer qz(fmaxf(s_old, scale_for(m)));
-  if (tid == 0) *scale = qz.s;
+    for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, s_max[i]);
+    const Quantizer qz(fmaxf(s_old, scale_for(m)));
+    if (tid == 0) *scale = qz.s;
 
-  if (qz.s > s_old) {  // rows the page holds already, on the coarser scale
-    requantize(codes, f.r0 * (D / 16), qz, s_old, tid, kAppendThreads);
-  }
+    if (qz.s > s_old) {  // rows the page holds already, on the coarser scale
+      requantize(codes, f.r0 * (D / 16), qz, s_old, tid, kAppendThreads);
+    }
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int u = tid + i * kAppendThreads;
-    if (u < units) *reinterpret_cast<uint2*>(codes + (size_t)f.r0 * D + (size_t)u * 8) = qz.codes(w[i]);
-  }
-  __syncthreads();  // before the next head's maxima
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = tid + i * kAppendThreads;
+      if (u < units) *reinterpret_cast<uint2*>(codes + (size_t)f.r0 * D + (size_t)u * 8) = qz.codes(w[i]);
+    }
+    __syncthreads();  // before the next head's maxima
   }
 }
 

@@ -480,300 +480,289 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   if (a.parts != nullptr) fill_empty<D>(a, len_first);
 
   const int rows_total = a.n_q * a.G;
-  // Rows of Q that this warp prepares (below), read ahead of their segment.
   static_assert(NT <= kWarps, "a warp prepares one block of rows");
-  auto load_q = [&](const Walk& x, uint2 (&w)[D / 16]) {
-    const int r = x.rb * kRows + 8 * warp + g;
-    const int t = token_of(a, r), hq = x.h * a.G + (r - t * a.G);
-    const uint16_t* src = a.q + x.b * a.q_batch + t * a.q_token + hq * a.q_head;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      w[ks] = warp < NT && r < rows_total ? __ldcg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * c))
-                                          : make_uint2(0u, 0u);
-  };
   uint32_t used = 0;
   bool last_segment = false;
   while (!last_segment) {
-  // ------------------------------------------------------------------ Q rows
-  // Row r of the block: token (rb * rows + r) / G, head (rb * rows + r) % G of the
-  // group.  K step ks of the products covers head dims [16 ks, 16 ks + 16), of
-  // which a lane holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
-  // k = 2c + 8, 2c + 9 (the same assignment as the codes') of rows 8 n + g.  Warp n
-  // prepares block n for all; the merge's buffer holds the fragments meanwhile.
-  if (warp < NT) {
-    uint2 w[D / 16];
-    load_q(sg, w);
-    const int n = warp, r = sg.rb * kRows + 8 * n + g;
-    const bool have = r < rows_total;
-    const int t = token_of(a, r);
-    float m = 0.f;
+    // ------------------------------------------------------------------ Q rows
+    // Row r of the block: token (rb * rows + r) / G, head (rb * rows + r) % G of the
+    // group.  K step ks of the products covers head dims [16 ks, 16 ks + 16), of
+    // which a lane holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
+    // k = 2c + 8, 2c + 9 (the same assignment as the codes') of rows 8 n + g.  Warp n
+    // prepares block n for all; the merge's buffer holds the fragments meanwhile.
+    if (warp < NT) {
+      const int n = warp, r = sg.rb * kRows + 8 * n + g;
+      const bool have = r < rows_total;
+      const int t = token_of(a, r), hq = sg.h * a.G + (r - t * a.G);
+      const uint16_t* src = a.q + sg.b * a.q_batch + t * a.q_token + hq * a.q_head;
+      uint2 w[D / 16];
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      m = fmaxf(fmaxf(m, fmaxf(fabsf(__uint_as_float(w[ks].x << 16)), fabsf(__uint_as_float(w[ks].x & 0xFFFF0000u)))),
-                fmaxf(fabsf(__uint_as_float(w[ks].y << 16)), fabsf(__uint_as_float(w[ks].y & 0xFFFF0000u))));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
-    const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u) - 127, -126), 126);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      for (int ks = 0; ks < D / 16; ++ks)
+        w[ks] = have ? __ldcg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * c)) : make_uint2(0u, 0u);
+      float m = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      s_q[(n * (D / 16) + ks) * 32 + lane] =
-          make_uint2(pack_f16x2(__uint_as_float(w[ks].x << 16) * down, __uint_as_float(w[ks].x & 0xFFFF0000u) * down),
-                     pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down));
-    if (c == 0) {
-      s_f[8 * n + g] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-      s_last[8 * n + g] = have ? sg.len - a.n_q + t : -1;
+      for (int ks = 0; ks < D / 16; ++ks)
+        m = fmaxf(fmaxf(m, fmaxf(fabsf(__uint_as_float(w[ks].x << 16)), fabsf(__uint_as_float(w[ks].x & 0xFFFF0000u)))),
+                  fmaxf(fabsf(__uint_as_float(w[ks].y << 16)), fabsf(__uint_as_float(w[ks].y & 0xFFFF0000u))));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
+      const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u) - 127, -126), 126);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        s_q[(n * (D / 16) + ks) * 32 + lane] =
+            make_uint2(pack_f16x2(__uint_as_float(w[ks].x << 16) * down, __uint_as_float(w[ks].x & 0xFFFF0000u) * down),
+                       pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down));
+      if (c == 0) {
+        s_f[8 * n + g] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+        s_last[8 * n + g] = have ? sg.len - a.n_q + t : -1;
+      }
     }
-  }
-  __syncthreads();
-  // The scores and accumulators a lane holds are those of rows 8 n + 2 c + {0, 1}.
-  int my_last[NT][2];   // last visible position of those (-1: none)
-  float f_row[NT][2];   // factor of their scores, in base 2
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f_row[n][i] = s_f[8 * n + 2 * c + i];
-      my_last[n][i] = s_last[8 * n + 2 * c + i];
-    }
-  const int tiles = sg.count(warp);
-
-  // ------------------------------------------------------------------ tiles
-  // Unit (lane / 16) of row lane % 16; unit u more is at this ^ (u << 4) for even u.
-  const uint32_t lane_unit = unit_offset<D>(lane & 15, lane >> 4);
-  float acc[D / 16][NT][4];  // head dims 16 u + 2 g + {0, 0, 1, 1}, rows 2 c + {0, 1, 0, 1}
-#pragma unroll
-  for (int u = 0; u < D / 16; ++u)
+    __syncthreads();
+    // The scores and accumulators a lane holds are those of rows 8 n + 2 c + {0, 1}.
+    int my_last[NT][2];   // last visible position of those (-1: none)
+    float f_row[NT][2];   // factor of their scores, in base 2
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[u][n][x] = 0.f;
-  float m_run[NT][2], l_run[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) m_run[n][i] = -INFINITY, l_run[n][i] = 0.f;
-  float R = 0x1p-126f;  // power of two the accumulators' values are relative to
-
-  for (int k = 0; k < tiles && ok; ++k) {
-    const uint32_t st = used % C::kStages;
-    ok = warp_wait(&bars[st], (used / C::kStages) & 1);
-    if (!ok) break;
-    ++used;
-    const uint32_t tile = ring + st * C::kStageBytes;
-    float ksc[2], vsc[2];
-    uint32_t flags;
-    {
-      const uint32_t head = heads + st * C::kHeadBytes;
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(ksc[0]), "=f"(vsc[0]), "=f"(ksc[1]), "=f"(vsc[1])
-                   : "r"(head)
-                   : "memory");
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(flags) : "r"(head + 16) : "memory");
-    }
-    // S^T = K Q^T for the tile's halves of 16 positions: of s[h][n], elements 0
-    // and 1 are position g, 2 and 3 position g + 8.
-    float s[2][NT][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.f;
-#pragma unroll
-    for (int u = 0; u < D / 16; u += 2) {
-      uint32_t r[2][4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
-      ldsm4<0>(r[0], tile + (lane_unit ^ (u << 4)));
-      ldsm4<16 * D>(r[1], tile + (lane_unit ^ (u << 4)));
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint2 qf[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) qf[n] = s_q[(n * (D / 16) + u + x) * 32 + lane];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t b0 = r[h][2 * x] ^ 0x80808080u, b1 = r[h][2 * x + 1] ^ 0x80808080u;
-          const uint32_t af[4] = {codes_f16(b0, 0x4140u), codes_f16(b1, 0x4140u), codes_f16(b0, 0x4342u),
-                                  codes_f16(b1, 0x4342u)};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(s[h][n], af, qf[n].x, qf[n].y);
-        }
+      for (int i = 0; i < 2; ++i) {
+        f_row[n][i] = s_f[8 * n + 2 * c + i];
+        my_last[n][i] = s_last[8 * n + 2 * c + i];
       }
-    }
-    // Scores in base 2; positions behind a row's last one are hidden.
-    const int pos0 = (sg.ta + warp + kWarps * k) * kTile;
-    const bool hide = pos0 + kTile - 1 > sg.len - a.n_q || flags != 3u;
+    const int tiles = sg.count(warp);
+
+    // ------------------------------------------------------------------ tiles
+    // Unit (lane / 16) of row lane % 16; unit u more is at this ^ (u << 4) for even u.
+    const uint32_t lane_unit = unit_offset<D>(lane & 15, lane >> 4);
+    float acc[D / 16][NT][4];  // head dims 16 u + 2 g + {0, 0, 1, 1}, rows 2 c + {0, 1, 0, 1}
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int u = 0; u < D / 16; ++u)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[h][n][x] *= f_row[n][x & 1] * ksc[h];
-    if (hide) {
+        for (int x = 0; x < 4; ++x) acc[u][n][x] = 0.f;
+    float m_run[NT][2], l_run[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m_run[n][i] = -INFINITY, l_run[n][i] = 0.f;
+    float R = 0x1p-126f;  // power of two the accumulators' values are relative to
+
+    for (int k = 0; k < tiles && ok; ++k) {
+      const uint32_t st = used % C::kStages;
+      ok = warp_wait(&bars[st], (used / C::kStages) & 1);
+      if (!ok) break;
+      ++used;
+      const uint32_t tile = ring + st * C::kStageBytes;
+      float ksc[2], vsc[2];
+      uint32_t flags;
+      {
+        const uint32_t head = heads + st * C::kHeadBytes;
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(ksc[0]), "=f"(vsc[0]), "=f"(ksc[1]), "=f"(vsc[1])
+                     : "r"(head)
+                     : "memory");
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(flags) : "r"(head + 16) : "memory");
+      }
+      // S^T = K Q^T for the tile's halves of 16 positions: of s[h][n], elements 0
+      // and 1 are position g, 2 and 3 position g + 8.
+      float s[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.f;
+#pragma unroll
+      for (int u = 0; u < D / 16; u += 2) {
+        uint32_t r[2][4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
+        ldsm4<0>(r[0], tile + (lane_unit ^ (u << 4)));
+        ldsm4<16 * D>(r[1], tile + (lane_unit ^ (u << 4)));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint2 qf[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) qf[n] = s_q[(n * (D / 16) + u + x) * 32 + lane];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t b0 = r[h][2 * x] ^ 0x80808080u, b1 = r[h][2 * x + 1] ^ 0x80808080u;
+            const uint32_t af[4] = {codes_f16(b0, 0x4140u), codes_f16(b1, 0x4140u), codes_f16(b0, 0x4342u),
+                                    codes_f16(b1, 0x4342u)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(s[h][n], af, qf[n].x, qf[n].y);
+          }
+        }
+      }
+      // Scores in base 2; positions behind a row's last one are hidden.
+      const int pos0 = (sg.ta + warp + kWarps * k) * kTile;
+      const bool hide = pos0 + kTile - 1 > sg.len - a.n_q || flags != 3u;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (pos0 + h * 16 + (x >> 1) * 8 + g > my_last[n][x & 1] || !((flags >> h) & 1u)) s[h][n][x] = -INFINITY;
-      if (!(flags & 1u)) vsc[0] = 0.f;
-      if (!(flags & 2u)) vsc[1] = 0.f;
-    }
-    const float v_big = fmaxf(vsc[0], vsc[1]);
-    float shrink = 1.f;
-    if (v_big > R) {
-      // The power of two at or above v_big (at most 2^126).
-      const float r_new = __uint_as_float(min((__float_as_uint(v_big) + 0x7FFFFFu) & 0x7F800000u, 0x7E800000u));
-      shrink = R / r_new;
-      R = r_new;
-    }
-    const float inv_r = __uint_as_float(0x7F000000u - __float_as_uint(R));  // 1 / R of a power of two
-    const float vr[2] = {vsc[0] * inv_r, vsc[1] * inv_r};
-    float alpha[NT][2];
-    uint32_t pf[2][NT][2];  // P^T as the B operand of the halves
-    bool same = shrink == 1.f;
+          for (int x = 0; x < 4; ++x) s[h][n][x] *= f_row[n][x & 1] * ksc[h];
+      if (hide) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float m_use[2];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        mx = fmaxf(m_run[n][i], mx);
-        m_use[i] = mx == -INFINITY ? 0.f : mx;
-        alpha[n][i] = ex2(m_run[n][i] - m_use[i]);
-        same = same && alpha[n][i] == 1.f;
-        m_run[n][i] = mx;
-        m_use[i] -= 15.f;
-        l_run[n][i] *= alpha[n][i];
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (pos0 + h * 16 + (x >> 1) * 8 + g > my_last[n][x & 1] || !((flags >> h) & 1u)) s[h][n][x] = -INFINITY;
+        if (!(flags & 1u)) vsc[0] = 0.f;
+        if (!(flags & 2u)) vsc[1] = 0.f;
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float p0 = ex2(s[h][n][2 * y] - m_use[0]);
-          const float p1 = ex2(s[h][n][2 * y + 1] - m_use[1]);
-          l_run[n][0] += p0;
-          l_run[n][1] += p1;
-          pf[h][n][y] = transpose8(pack_f16x2(p0 * vr[h], p1 * vr[h]));
-        }
-    }
-    if (!__all_sync(0xffffffffu, same)) {
+      const float v_big = fmaxf(vsc[0], vsc[1]);
+      float shrink = 1.f;
+      if (v_big > R) {
+        // The power of two at or above v_big (at most 2^126).
+        const float r_new = __uint_as_float(min((__float_as_uint(v_big) + 0x7FFFFFu) & 0x7F800000u, 0x7E800000u));
+        shrink = R / r_new;
+        R = r_new;
+      }
+      const float inv_r = __uint_as_float(0x7F000000u - __float_as_uint(R));  // 1 / R of a power of two
+      const float vr[2] = {vsc[0] * inv_r, vsc[1] * inv_r};
+      float alpha[NT][2];
+      uint32_t pf[2][NT][2];  // P^T as the B operand of the halves
+      bool same = shrink == 1.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float s0 = alpha[n][0] * shrink, s1 = alpha[n][1] * shrink;
+        float m_use[2];
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-          acc[u][n][0] *= s0;
-          acc[u][n][1] *= s1;
-          acc[u][n][2] *= s0;
-          acc[u][n][3] *= s1;
+        for (int i = 0; i < 2; ++i) {
+          float mx = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(m_run[n][i], mx);
+          m_use[i] = mx == -INFINITY ? 0.f : mx;
+          alpha[n][i] = ex2(m_run[n][i] - m_use[i]);
+          same = same && alpha[n][i] == 1.f;
+          m_run[n][i] = mx;
+          m_use[i] -= 15.f;
+          l_run[n][i] *= alpha[n][i];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = ex2(s[h][n][2 * y] - m_use[0]);
+            const float p1 = ex2(s[h][n][2 * y + 1] - m_use[1]);
+            l_run[n][0] += p0;
+            l_run[n][1] += p1;
+            pf[h][n][y] = transpose8(pack_f16x2(p0 * vr[h], p1 * vr[h]));
+          }
+      }
+      if (!__all_sync(0xffffffffu, same)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float s0 = alpha[n][0] * shrink, s1 = alpha[n][1] * shrink;
+#pragma unroll
+          for (int u = 0; u < D / 16; ++u) {
+            acc[u][n][0] *= s0;
+            acc[u][n][1] *= s1;
+            acc[u][n][2] *= s0;
+            acc[u][n][3] *= s1;
+          }
         }
       }
+      // O^T += V^T P^T.  A transposed load gives positions 2c, 2c + 1 of the columns
+      // d = 16 u + 2 g (even bytes) and + 1 (odd bytes), rows g and g + 8 of the
+      // A operand.
+#pragma unroll
+      for (int u = 0; u < D / 16; u += 2) {
+        uint32_t r[2][4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
+        ldsm4_trans<C::kHalfBytes>(r[0], tile + (lane_unit ^ (u << 4)));
+        ldsm4_trans<C::kHalfBytes + 16 * D>(r[1], tile + (lane_unit ^ (u << 4)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t b0 = r[h][2 * x] ^ 0x80808080u, b1 = r[h][2 * x + 1] ^ 0x80808080u;
+            const uint32_t af[4] = {codes_f16(b0, 0x4240u), codes_f16(b0, 0x4341u), codes_f16(b1, 0x4240u),
+                                    codes_f16(b1, 0x4341u)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(acc[u + x][n], af, pf[h][n][0], pf[h][n][1]);
+          }
+      }
+      __syncwarp();
+      issue();
     }
-    // O^T += V^T P^T.  A transposed load gives positions 2c, 2c + 1 of the columns
-    // d = 16 u + 2 g (even bytes) and + 1 (odd bytes), rows g and g + 8 of the
-    // A operand.
-#pragma unroll
-    for (int u = 0; u < D / 16; u += 2) {
-      uint32_t r[2][4];  // positions 0-7 and 8-15 of unit u, then of unit u + 1
-      ldsm4_trans<C::kHalfBytes>(r[0], tile + (lane_unit ^ (u << 4)));
-      ldsm4_trans<C::kHalfBytes + 16 * D>(r[1], tile + (lane_unit ^ (u << 4)));
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t b0 = r[h][2 * x] ^ 0x80808080u, b1 = r[h][2 * x + 1] ^ 0x80808080u;
-          const uint32_t af[4] = {codes_f16(b0, 0x4240u), codes_f16(b0, 0x4341u), codes_f16(b1, 0x4240u),
-                                  codes_f16(b1, 0x4341u)};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(acc[u + x][n], af, pf[h][n][0], pf[h][n][1]);
-        }
-    }
-    __syncwarp();
-    issue();
-  }
 
-  // ------------------------------------------------------------------ merge
-  Walk after = sg;
-  const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len);
-  float* part = nullptr;
-  if (!whole) part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats(D, kRows);
-  if (a.parts != nullptr && sg.ta == 0 && threadIdx.x == 0 && (a.by_segment || !whole)) {
-    const int hr = sg.h * a.row_blocks + sg.rb;
-    const long long slot = a.by_segment ? (long long)sg.b * a.Hkv * a.row_blocks + hr : blockIdx.x;
-    // The segment runs on into as many CTAs as hold the rest of its tiles.
-    const unsigned rest = tiles_of(sg.len) - sg.tb;
-    const int more = rest == 0 ? 0 : 1 + (int)((rest - 1) / (unsigned)min(per, 0x7fffffffll));
-    a.chains[slot] = Chain{more, sg.b, hr, (int)blockIdx.x};
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) l_run[n][i] += __shfl_xor_sync(0xffffffffu, l_run[n][i], off);
-      if (g == 0) {
-        s_m[warp * kRows + 8 * n + 2 * c + i] = m_run[n][i];
-        s_l[warp * kRows + 8 * n + 2 * c + i] = l_run[n][i];
-      }
+    // ------------------------------------------------------------------ merge
+    const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len);
+    float* part = nullptr;
+    if (!whole) part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats(D, kRows);
+    if (a.parts != nullptr && sg.ta == 0 && threadIdx.x == 0 && (a.by_segment || !whole)) {
+      const int hr = sg.h * a.row_blocks + sg.rb;
+      const long long slot = a.by_segment ? (long long)sg.b * a.Hkv * a.row_blocks + hr : blockIdx.x;
+      // The segment runs on into as many CTAs as hold the rest of its tiles.
+      const unsigned rest = tiles_of(sg.len) - sg.tb;
+      const int more = rest == 0 ? 0 : 1 + (int)((rest - 1) / (unsigned)min(per, 0x7fffffffll));
+      a.chains[slot] = Chain{more, sg.b, hr, (int)blockIdx.x};
     }
-#pragma unroll
-  for (int half = 0; half < D / 64; ++half) {
-    __syncthreads();  // the buffer holds Q, or the other half, until here
-    // Pairs of columns, moved by four for every second row, so that the 16 lanes
-    // of a phase cover all banks.
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = 8 * n + 2 * c + i;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * 64 + (((8 * u + g) ^ (c << 2)) << 1)) =
-              make_float2(acc[half * 4 + u][n][i] * R, acc[half * 4 + u][n][2 + i] * R);
-      }
-    if (half == D / 64 - 1) {
-      last_segment = !after.next(a);
-    }
-    __syncthreads();
-    // rows x 64 columns over 128 threads, 4 columns at a time.
-#pragma unroll 1
-    for (int x = threadIdx.x; x < kRows * 16; x += kThreads) {
-      const int r = x >> 4, part4 = x & 15;
-      float M = -INFINITY, L = 0.f, v[4] = {};
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + r]);
-      const float M_use = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(s_m[w * kRows + r] - M_use);
-        L += s_l[w * kRows + r] * f;
-        const float4 y = *reinterpret_cast<const float4*>(
-            s_merge + (w * kRows + r) * 64 + (((2 * part4) ^ (((r >> 1) & 3) << 2)) << 1));
-        v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
-      }
-      const int rr = sg.rb * kRows + r;
-      if (!whole) {
-        *reinterpret_cast<float4*>(part + r * D + half * 64 + part4 * 4) = make_float4(v[0], v[1], v[2], v[3]);
-        if (half == 0 && part4 == 0) {
-          part[kRows * D + r] = M;
-          part[kRows * D + kRows + r] = L;
+        for (int off = 4; off < 32; off <<= 1) l_run[n][i] += __shfl_xor_sync(0xffffffffu, l_run[n][i], off);
+        if (g == 0) {
+          s_m[warp * kRows + 8 * n + 2 * c + i] = m_run[n][i];
+          s_l[warp * kRows + 8 * n + 2 * c + i] = l_run[n][i];
         }
-      } else if (rr < rows_total) {
-        const size_t row = out_row(a, sg.b, sg.h, rr);
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        *reinterpret_cast<uint2*>(a.o + row * D + half * 64 + part4 * 4) =
-            make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
-        if (half == 0 && part4 == 0) a.lse[row] = lse_of(M, L);
+      }
+#pragma unroll
+    for (int half = 0; half < D / 64; ++half) {
+      __syncthreads();  // the buffer holds Q, or the other half, until here
+      // Pairs of columns, moved by four for every second row, so that the 16 lanes
+      // of a phase cover all banks.
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * n + 2 * c + i;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * 64 + (((8 * u + g) ^ (c << 2)) << 1)) =
+                make_float2(acc[half * 4 + u][n][i] * R, acc[half * 4 + u][n][2 + i] * R);
+        }
+      __syncthreads();
+      // rows x 64 columns over 128 threads, 4 columns at a time.
+#pragma unroll 1
+      for (int x = threadIdx.x; x < kRows * 16; x += kThreads) {
+        const int r = x >> 4, part4 = x & 15;
+        float M = -INFINITY, L = 0.f, v[4] = {};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + r]);
+        const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(s_m[w * kRows + r] - M_use);
+          L += s_l[w * kRows + r] * f;
+          const float4 y = *reinterpret_cast<const float4*>(
+              s_merge + (w * kRows + r) * 64 + (((2 * part4) ^ (((r >> 1) & 3) << 2)) << 1));
+          v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
+        }
+        const int rr = sg.rb * kRows + r;
+        if (!whole) {
+          *reinterpret_cast<float4*>(part + r * D + half * 64 + part4 * 4) = make_float4(v[0], v[1], v[2], v[3]);
+          if (half == 0 && part4 == 0) {
+            part[kRows * D + r] = M;
+            part[kRows * D + kRows + r] = L;
+          }
+        } else if (rr < rows_total) {
+          const size_t row = out_row(a, sg.b, sg.h, rr);
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          *reinterpret_cast<uint2*>(a.o + row * D + half * 64 + part4 * 4) =
+              make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+          if (half == 0 && part4 == 0) a.lse[row] = lse_of(M, L);
+        }
       }
     }
+    last_segment = !sg.next(a);
+    if (!last_segment) __syncthreads();  // before the next segment's Q
   }
-  sg = after;
-  if (!last_segment) __syncthreads();  // before the next segment's Q
-  }  // segments
   if (!ok) {
     if (lane == 0) set_fail(ATTN_ERR_TIMEOUT);
     // Do not leave while copies into this CTA's shared memory are in flight.
@@ -782,9 +771,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 }
 
 // Joins the parts of the segments that begin in one CTA's run and end in
-// another's: grid (chains, groups of rows).  `per_row` warps (1 or kJoinWarps) share a row
-// and take every per_row-th part: one where there are many chains of a few parts,
-// all where few chains have many.  The order of the sums is that of the parts.
+// another's: grid (chains, groups of rows).  `per_row` warps (1 or kJoinWarps) share
+// a row and take every per_row-th part: one where there are many chains of a few
+// parts, all where few chains have many.  The order of the sums is that of the parts.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args a, int rows, int per_row) {
@@ -877,6 +866,7 @@ unsigned decode_runs(int nt) {
   const int sms = device_sm_count();
   return (nt == 1 ? 3u : 2u) * (sms > 0 ? sms : 152);
 }
+
 bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
@@ -891,7 +881,8 @@ bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
 }
 
 template <int D, int NT>
-cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, unsigned runs, cudaStream_t stream) {
+cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, unsigned runs,
+                        cudaStream_t stream) {
   using C = Cfg<D, NT>;
   auto kernel = decode_int8_kernel<D, NT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
@@ -904,8 +895,8 @@ cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args
   const long long segments = (long long)a.B * a.Hkv * a.row_blocks;
   const int per_row = segments * 4 <= runs ? kJoinWarps : 1;
   const int rows = std::min(C::kRows, a.n_q * a.G);
-  return launch_pdl(decode_join_kernel<D>, dim3(a.by_segment ? (unsigned)segments : runs, ceil_div(rows * per_row, kJoinWarps)),
-                    dim3(32 * kJoinWarps), 0, stream, a, C::kRows, per_row);
+  const dim3 grid(a.by_segment ? (unsigned)segments : runs, ceil_div(rows * per_row, kJoinWarps));
+  return launch_pdl(decode_join_kernel<D>, grid, dim3(32 * kJoinWarps), 0, stream, a, C::kRows, per_row);
 }
 
 bool splits(const PagedCache& c) { return (long long)c.max_blocks * c.page > (long long)kWholeTiles * kTile; }
@@ -938,7 +929,8 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   a.lens = lens;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
-  a.B = c.B, a.n_q = n_q, a.H = H, a.Hkv = c.Hkv, a.G = H / c.Hkv, a.by_G = (uint32_t)(((1ull << 32) + a.G - 1) / a.G), a.P = c.P, a.page = c.page;
+  a.B = c.B, a.n_q = n_q, a.H = H, a.Hkv = c.Hkv, a.G = H / c.Hkv, a.P = c.P, a.page = c.page;
+  a.by_G = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
   a.page_shift = page_shift(c.page);
   a.max_blocks = c.max_blocks;
   a.row_blocks = row_passes(n_q * a.G);
