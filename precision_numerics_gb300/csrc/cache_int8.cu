@@ -370,7 +370,6 @@ struct ReadArgs {
 
 constexpr int kReadWarps = 8;
 constexpr int kReadCu = 1024;
-constexpr int kReadTimes = 4;
 
 // A lane reads 4 codes for FP32 values, 8 for BF16, and writes 16 bytes; a row of
 // a head is D / that many lanes, and a warp takes as many tokens at a time as it
@@ -381,16 +380,16 @@ struct ReadCfg {
   static constexpr int kCodes = FP32 ? 4 : 8;
   static constexpr int kLanes = D / kCodes;
   static constexpr int kAtOnce = 32 / kLanes;              // tokens of a warp at a time
-  static constexpr int kTokens = kReadWarps * kAtOnce;     // of a CTA at a time
+  static constexpr int kTokens = kReadWarps * kAtOnce;      // of a CTA
 };
 template <int D, bool FP32>
-__global__ void __launch_bounds__(32 * kReadWarps) read_int8_kernel(const __grid_constant__ ReadArgs a, int times) {
+__global__ void __launch_bounds__(32 * kReadWarps) read_int8_kernel(const __grid_constant__ ReadArgs a) {
   using C = ReadCfg<D, FP32>;
   griddep_wait();
-  __shared__ long long s_row[kReadTimes * C::kTokens];  // row of the pool's head 0 in the token's page, or -1
+  __shared__ long long s_row[C::kTokens];  // row of the pool's head 0 in the token's page, or -1
   __shared__ int s_cu[kReadCu];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kv = blockIdx.y;
-  const int t0 = blockIdx.x * times * C::kTokens;
+  const int t0 = blockIdx.x * C::kTokens;
   // The search runs in shared memory where the sequences' ends fit it.
   const bool near_cu = a.B < kReadCu;
   if (near_cu) {
@@ -398,8 +397,8 @@ __global__ void __launch_bounds__(32 * kReadWarps) read_int8_kernel(const __grid
     __syncthreads();
   }
   auto cu = [&](int b) { return near_cu ? s_cu[b] : __ldcg(a.cu + b); };
-  for (int i = tid; i < times * C::kTokens && t0 + i < a.T; i += 32 * kReadWarps) {
-    const int t = t0 + i;
+  if (tid < C::kTokens && t0 + tid < a.T) {
+    const int t = t0 + tid;
     int lo = 0, hi = a.B;  // the last sequence that begins at or before t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -415,51 +414,47 @@ __global__ void __launch_bounds__(32 * kReadWarps) read_int8_kernel(const __grid
         row = ((long long)id * a.Hkv << a.page_shift) + (pos & (a.page - 1));
     }
     if (row < 0) set_fail(ATTN_ERR_INVALID_ARG);
-    s_row[i] = row;
+    s_row[tid] = row;
   }
   __syncthreads();
   const int col = lane % C::kLanes * C::kCodes;
   const int8_t* codes = a.codes[kv] + col;
   const float* scales = a.scales[kv];
-  for (int i = 0; i < times; ++i) {
-    const int t = (i * kReadWarps + warp) * C::kAtOnce + lane / C::kLanes;
-    if (t0 + t >= a.T) continue;
-    const long long at = s_row[t];
-    const bool have = at >= 0;
-    const long long row = have ? at : 0;
-    const size_t out = (size_t)(t0 + t) * a.Hkv * D + col;
+  const int t = warp * C::kAtOnce + lane / C::kLanes;
+  if (t0 + t >= a.T) return;
+  const long long at = s_row[t];
+  const bool have = at >= 0;
+  const long long row = have ? at : 0;
+  const size_t out = (size_t)(t0 + t) * a.Hkv * D + col;
 #pragma unroll 4
-    for (int h = 0; h < a.Hkv; ++h) {
-      const long long r = row + ((long long)h << a.page_shift);
-      const float s = have ? __ldcg(scales + (r >> a.page_shift)) : 0.f;
-      uint32_t c[C::kCodes / 4];
-      if constexpr (FP32) {
-        c[0] = __ldcg(reinterpret_cast<const uint32_t*>(codes + r * D));
-      } else {
-        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(codes + r * D));
-        c[0] = v.x, c[1] = v.y;
-      }
-      float f[C::kCodes];
-#pragma unroll
-      for (int e = 0; e < C::kCodes; ++e)
-        f[e] = have ? static_cast<float>(static_cast<int8_t>(c[e >> 2] >> (8 * (e & 3)))) * s : 0.f;
-      if constexpr (FP32)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out[kv]) + out + h * D) = make_float4(f[0], f[1], f[2], f[3]);
-      else
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[kv]) + out + h * D) =
-            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                       pack_bf16x2(f[6], f[7]));
+  for (int h = 0; h < a.Hkv; ++h) {
+    const long long r = row + ((long long)h << a.page_shift);
+    const float s = have ? __ldcg(scales + (r >> a.page_shift)) : 0.f;
+    uint32_t c[C::kCodes / 4];
+    if constexpr (FP32) {
+      c[0] = __ldcg(reinterpret_cast<const uint32_t*>(codes + r * D));
+    } else {
+      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(codes + r * D));
+      c[0] = v.x, c[1] = v.y;
     }
+    float f[C::kCodes];
+#pragma unroll
+    for (int e = 0; e < C::kCodes; ++e)
+      f[e] = have ? static_cast<float>(static_cast<int8_t>(c[e >> 2] >> (8 * (e & 3)))) * s : 0.f;
+    if constexpr (FP32)  // evicted first: four bytes a code would push everything else out of L2 (27 -> 24 us)
+      __stcs(reinterpret_cast<float4*>(static_cast<float*>(a.out[kv]) + out + h * D),
+             make_float4(f[0], f[1], f[2], f[3]));
+    else
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[kv]) + out + h * D) =
+          make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                     pack_bf16x2(f[6], f[7]));
   }
 }
 
 template <int D, bool FP32>
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t stream) {
-  // Up to kReadTimes rounds a CTA, fewer while that leaves SMs without 8 CTAs.
-  const int sms = device_sm_count(), once = ceil_div(a.T, ReadCfg<D, FP32>::kTokens);
-  const int times = std::max(1, std::min(kReadTimes, sms > 0 ? once * 2 / (sms * 8) : 1));
-  return launch_pdl(read_int8_kernel<D, FP32>, dim3(ceil_div(once, times), 2), dim3(32 * kReadWarps), 0, stream, a,
-                    times);
+  return launch_pdl(read_int8_kernel<D, FP32>, dim3(ceil_div(a.T, ReadCfg<D, FP32>::kTokens), 2),
+                    dim3(32 * kReadWarps), 0, stream, a);
 }
 
 }  // namespace
