@@ -627,3 +627,130 @@ def test_calls_with_a_stream_given(A):
     for got in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], got))
     A.attn_check_status()
+
+
+# ------------------------------------------------ sizes, layouts, several calls
+def test_thousands_of_sequences(A):
+    """More sequences than any kernel holds at a time, many of them empty."""
+    H, Hkv, d, page, B = 2, 1, 64, 16, 3000
+    g = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 9, (B,), generator=g).tolist()
+    lens[2500] = 700
+    T, cu = sum(lens), sums(lens)
+    q, k, v = normal((T, H, d), 1), normal((T, Hkv, d), 2), normal((T, Hkv, d), 3)
+    plan = A.attn_varlen_plan(ints(cu), T, H, Hkv)
+    o, lse = A.attn_varlen_fwd(q.cuda(), k.cuda(), v.cuda(), plan)
+    A.attn_check_status()
+    some = [b for b in range(0, B, 97)] + [2500, B - 1]
+    for b in some:
+        s = slice(cu[b], cu[b + 1])
+        check_prompt(q[s], k[s], v[s], [lens[b]], True, 1 / math.sqrt(d), o[s], lse[s])
+    starts = torch.randint(0, 20, (B,), generator=g).tolist()
+    tables, pages = scattered([-(-(s + n) // page) for s, n in zip(starts, lens)], 2)
+    c = Cache(pages, Hkv, page, d, tables)
+    c.append([k, v], cu, starts)
+    A.attn_cache_append_int8(k.cuda(), v.cuda(), *c.gpu, ints(cu), ints(starts))
+    A.attn_check_status()
+    assert c.equal()
+    got, _ = A.attn_cache_read_int8(*c.gpu, ints(cu), ints(starts), T, dtype=torch.float32)
+    A.attn_check_status()
+    want = torch.cat([c.values(0, b, s + n)[s:] for b, (s, n) in enumerate(zip(starts, lens))])
+    assert torch.equal(got.cpu(), want.float())
+    held = [s + n for s, n in zip(starts, lens)]
+    qd = normal((B, 1, H, d), 4)
+    o, lse = A.attn_decode_int8(qd.cuda(), *c.gpu, ints(held))
+    A.attn_check_status()
+    check_decode(c, qd, held, 1 / math.sqrt(d), o, lse, shown=some)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_of_seventy_thousand_tokens(A, causal):
+    H, Hkv, d, T = 2, 1, 64, 70001
+    q, k, v = normal((T, H, d), 1), normal((T, Hkv, d), 2), normal((T, Hkv, d), 3)
+    plan = A.attn_varlen_plan(ints([0, T]), T, H, Hkv, causal=causal)
+    o, lse = A.attn_varlen_fwd(q.cuda(), k.cuda(), v.cuda(), plan, causal=causal)
+    A.attn_check_status()
+    rows = [0, 1, 127, 128, 40000, 65535, 65536, T - 1]
+    for h in range(H):
+        r, rl, a, size = ref.attention(q[rows, h], k[:, 0], v[:, 0], 1 / math.sqrt(d), rows if causal else [T - 1] * len(rows))
+        assert ((o[rows, h].cpu().double() - r).abs() <= ref.output_bound(r, a, size, d, 2.0 ** -8)).all()
+        assert ((lse[rows, h].cpu().double() - rl).abs() <= ref.lse_bound(rl, size, d)).all()
+
+
+def test_head_major_tensors(A):
+    """q, k, v stored head by head (token stride below the head stride)."""
+    H, Hkv, d, lens = 6, 2, 128, [130, 77]
+    T = sum(lens)
+    q, k, v = (normal((n, T, d), i).transpose(0, 1) for i, n in enumerate((H, Hkv, Hkv)))
+    plan = A.attn_varlen_plan(ints(sums(lens)), T, H, Hkv)
+    gq, gk, gv = (x.transpose(0, 1).contiguous().cuda().transpose(0, 1) for x in (q, k, v))
+    assert gq.stride(0) == d
+    o, lse = A.attn_varlen_fwd(gq, gk, gv, plan)
+    A.attn_check_status()
+    check_prompt(q, k, v, lens, True, 1 / math.sqrt(d), o, lse)
+    tables, pages = scattered([9, 5], 3)
+    c = Cache(pages, Hkv, 16, d, tables)
+    c.append([k, v], sums(lens), [0, 0])
+    A.attn_cache_append_int8(gk, gv, *c.gpu, ints(sums(lens)), ints([0, 0]))
+    assert c.equal()
+    qd = q[:2].reshape(2, 1, H, d)
+    strided = qd.transpose(0, 2).contiguous().cuda().transpose(0, 2)
+    o, lse = A.attn_decode_int8(strided, *c.gpu, ints(lens))
+    A.attn_check_status()
+    check_decode(c, qd, lens, 1 / math.sqrt(d), o, lse)
+
+
+def test_batch_without_tokens(A):
+    """Sequences that are all empty, with rows of nobody behind them; no rows at all."""
+    H, Hkv, d = 4, 2, 64
+    q, k = normal((40, H, d), 1).cuda(), normal((40, Hkv, d), 2).cuda()
+    o, lse = torch.full((40, H, d), 7.0, dtype=BF, device="cuda"), torch.full((40, H), 7.0, device="cuda")
+    plan = A.attn_varlen_plan(ints([0, 0, 0, 0]), 40, H, Hkv)
+    A.attn_varlen_fwd(q, k, k, plan, o=o, lse=lse)
+    assert (o == 7).all() and (lse == 7).all()
+    plan = A.attn_varlen_plan(ints([0, 0]), 0, H, Hkv)
+    o, lse = A.attn_varlen_fwd(q[:0], k[:0], k[:0], plan)
+    assert o.shape == (0, H, d) and lse.shape == (0, H)
+    c = Cache(4, Hkv, 16, d, [[0, 1]])
+    A.attn_cache_append_int8(k[:0], k[:0], *c.gpu, ints([0, 0]), ints([3]))
+    x, _ = A.attn_cache_read_int8(*c.gpu, ints([0, 0]), ints([3]), 0)
+    assert x.shape == (0, Hkv, d) and c.equal()
+    for width in (2, 200):  # whole sequences, and split ones
+        c = Cache(4, Hkv, 16, d, [[], []], width=width)
+        o, lse = A.attn_decode_int8(normal((2, 3, H, d), 1).cuda(), *c.gpu, ints([0, 0]))
+        assert (o == 0).all() and (lse == -torch.inf).all()
+    A.attn_check_status()
+
+
+def test_two_streams_at_once(A):
+    """Calls of every kind overlap on two streams, each with its own workspace and outputs."""
+    H, Hkv, d, page, lens = 8, 2, 128, 64, [3000, 70, 900]
+    T, cu = 1500, [0, 700, 1500]
+    tables, pages = scattered([-(-n // page) for n in lens], 5)
+    c = Cache(pages, Hkv, page, d, tables)
+    q = normal((3, 1, H, d), 1).cuda()
+    x = normal((T, H + 2 * Hkv, d), 2).cuda()
+    L, cus, zero = ints(lens), ints(cu), ints([0, 0])
+    scratch = [Cache(30, Hkv, page, d, [list(range(14)), list(range(14, 28))], seed=i).gpu for i in range(2)]
+
+    def run(i):
+        plan = A.attn_varlen_plan(cus, T, H, Hkv)
+        out = []
+        for _ in range(6):
+            out += A.attn_varlen_fwd(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], plan)
+            out += A.attn_decode_int8(q, *c.gpu, L)
+            A.attn_cache_append_int8(x[:, H:H + Hkv], x[:, H + Hkv:], *scratch[i], cus, zero)
+            out += A.attn_cache_read_int8(*scratch[i], cus, zero, T)
+        return out
+
+    want = run(0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            got.append(run(i))
+    A.attn_check_status(streams[0])
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, g))
