@@ -466,7 +466,7 @@ def _plan_batch(plan, T, H, H_kv):
     """Sequences a plan of this size has room for (its buffer grows by 16 bytes each)."""
     if not isinstance(plan, torch.Tensor) or not plan.is_cuda or not plan.is_contiguous():
         raise ValueError("plan must be a tensor made by attn_varlen_plan")
-    B = (_nbytes(plan) - 256) // 16 - T // (2 * (128 // max(1, min(128, H // H_kv))))
+    B = (_nbytes(plan) - 256) // 16 - T // (128 // max(1, min(128, H // H_kv)))
     if B < 1:
         raise ValueError("plan is too small for this T, H and H_kv")
     return B

@@ -42,7 +42,7 @@ attn_status check_varlen(int B, int T, int H, int H_kv, int d, VarlenProblem* p)
   ATTN_CHECK(check_packed(B, T));
   ATTN_CHECK(check_heads(H, H_kv, d));
   const long long tq = kBlockM / (H / H_kv);
-  if (((long long)T / (2 * tq) + B) * H_kv > INT_MAX)
+  if (((long long)T / tq + B) * H_kv > INT_MAX)
     return fail(ATTN_ERR_INVALID_ARG, "B=%d, T=%d and H_kv=%d make more than 2^31 - 1 work items", B, T, H_kv);
   p->B = B, p->T = T, p->H = H, p->Hkv = H_kv, p->d = d, p->causal = 0, p->scale = 1.f;
   return ATTN_OK;

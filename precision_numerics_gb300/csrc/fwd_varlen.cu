@@ -12,7 +12,7 @@
 //    heads x 64 columns lays out directly.  The rows of a tile share their keys,
 //    so short sequences fill a tile G times better than with a tile per head.
 //    Where G does not divide 128 the last rows of a tile are idle.
-//  - The work items (2 tq tokens of one sequence, for every key head) are listed
+//  - The work items (tq or 2 tq tokens of one sequence, for every key head) are listed
 //    by a plan kernel, heaviest first, from the sequences' lengths in device
 //    memory; the plan serves every call on the same packed batch.
 //  - A key tile that runs past its sequence's end holds rows of the next
@@ -46,52 +46,64 @@ static_assert(kRegsWG0 <= 128 && kRegsCorr <= 128 && kRegsSoftmax >= 128, "setma
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_varlen, code); }
 
 // ---------------------------------------------------------------------------
-// Plan: a header of 64 words, then one item per 2 tq tokens of a sequence.
+// Plan: a header of 64 words, then one item per tile or two (tq or 2 tq tokens of
+// a sequence).
 // ---------------------------------------------------------------------------
 constexpr int kPlanMagic = 0x564c504e;
 constexpr int kPlanHeader = 64;  // words
 struct PlanItem {
-  int first, len, q0, pad;  // sequence's first packed token and length; item's first token in it
+  int first, len, q0, end;  // sequence's first packed token and length; item's tokens in it: [q0, end)
 };
 static_assert(sizeof(PlanItem) == 16, "one 16-byte load per item");
 
 inline int tile_tokens(int H, int Hkv) { return kBlockM / (H / Hkv); }
-inline long long plan_capacity(int B, int T, int H, int Hkv) { return (long long)T / (2 * tile_tokens(H, Hkv)) + B; }
+// Items at most, of one tile each.
+inline long long plan_capacity(int B, int T, int H, int Hkv) { return (long long)T / tile_tokens(H, Hkv) + B; }
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 1024;
 
 // One CTA: counts the items by their number of key tiles (kPlanBins classes,
 // heaviest first), then writes each into its class's range.  The order within
-// a class is that of the atomics; no result depends on it.
+// a class is that of the atomics; no result depends on it.  Where items of two
+// tiles would not fill the SMs once, an item is one tile, for the other SMs to
+// share the work (2048 tokens, 8 heads of 128: 36 -> 28 us).  Without a causal mask
+// all items weigh the same, and the tiles have to fit the SMs in one round (one
+// and a half rounds of tiles take longer than one of pairs: 30 -> 43 us).
 __global__ void __launch_bounds__(kPlanThreads)
     varlen_plan_kernel(const int* __restrict__ cu, int* __restrict__ plan, int B, int T, int G, int Hkv, int tq,
-                       int causal, int capacity) {
+                       int causal, int capacity, int sms) {
+  __shared__ int s_pairs;
   __shared__ int s_count[kPlanBins], s_warp[32], s_max;
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   s_count[tid] = 0;
-  if (tid == 0) s_max = 1;
+  if (tid == 0) s_max = 1, s_pairs = 0;
   __syncthreads();
-  int longest = 0;
+  int longest = 0, pairs = 0;
   for (int b = tid; b < B; b += kPlanThreads) {
     const int x = __ldcg(cu + b), y = __ldcg(cu + b + 1);
     if (x < 0 || y < x || y > T) set_fail(ATTN_ERR_INVALID_ARG);
     const int first = min(max(x, 0), T);
-    longest = max(longest, min(max(y, first), T) - first);
+    const int len = min(max(y, first), T) - first;
+    longest = max(longest, len);
+    pairs = min(pairs + (len + 2 * tq - 1) / (2 * tq), sms);
   }
   atomicMax(&s_max, (longest + kBlockN - 1) / kBlockN);
+  if (pairs > 0) atomicAdd(&s_pairs, pairs);
   __syncthreads();
   const int most = s_max;
+  const int tiles_per_item = (long long)s_pairs * Hkv * (causal ? 1 : 2) <= sms ? 1 : 2;
+  const int per_item = tiles_per_item * tq;  // tokens
   auto each = [&](auto&& put) {
     for (int b = warp; b < B; b += kPlanThreads / 32) {
       const int first = min(max(__ldcg(cu + b), 0), T);
       const int len = min(max(__ldcg(cu + b + 1), first), T) - first;
-      const int n = (len + 2 * tq - 1) / (2 * tq);
+      const int n = (len + per_item - 1) / per_item;
       for (int i = lane; i < n; i += 32) {
-        const int q0 = i * 2 * tq;
-        const int keys = causal ? min(q0 + 2 * tq, len) : len;
+        const int q0 = i * per_item;
+        const int keys = causal ? min(q0 + per_item, len) : len;
         const int tiles = (keys + kBlockN - 1) / kBlockN;
         put(kPlanBins - 1 - (int)((long long)(tiles - 1) * kPlanBins / most), first, len, q0);
       }
@@ -122,7 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   PlanItem* items = reinterpret_cast<PlanItem*>(plan + kPlanHeader);
   each([&](int bin, int first, int len, int q0) {
     const int at = atomicAdd(&s_count[bin], 1);
-    if (at < capacity) items[at] = PlanItem{first, len, q0, 0};
+    if (at < capacity) items[at] = PlanItem{first, len, q0, min(q0 + per_item, len)};
   });
 }
 
@@ -175,7 +187,7 @@ struct Item {
   int first, len, head, q0, n[2], nmax;
 };
 template <bool CAUSAL>
-__device__ __forceinline__ Item load_item(const int* __restrict__ plan, int L, int Hkv, int tq) {
+__device__ __forceinline__ Item load_item(const int* plan, int L, int Hkv, int tq) {
   // Through L1: the producer, which runs ahead, has brought the line by the time
   // the other roles ask for it.
   const int at = L / Hkv;
@@ -189,7 +201,7 @@ __device__ __forceinline__ Item load_item(const int* __restrict__ plan, int L, i
   for (int t = 0; t < 2; ++t) {
     const int q = it.q0 + t * tq;
     const int keys = CAUSAL ? min(q + tq, it.len) : it.len;
-    it.n[t] = q >= it.len ? 0 : (keys + kBlockN - 1) / kBlockN;
+    it.n[t] = q >= p.w ? 0 : (keys + kBlockN - 1) / kBlockN;
   }
   it.nmax = max(it.n[0], it.n[1]);
   return it;
@@ -200,7 +212,7 @@ __device__ __forceinline__ int tile_keys(const Item& it, int j) { return min(kBl
 template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const int* __restrict__ plan,
+                      const __grid_constant__ CUtensorMap tmV, const int* plan,
                       uint16_t* __restrict__ out, float* __restrict__ lse, int T, int H, int Hkv, int G, int tq,
                       int capacity, float scale, float scale_log2) {
   using C = Cfg<D>;
@@ -258,11 +270,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   // The plan must be one for this call: anything else is reported and nothing
   // is computed, so that no item can reach outside the tensors.
-  const bool plan_ok = __ldcg(plan) == kPlanMagic && __ldcg(plan + 1) == T && __ldcg(plan + 2) == G &&
-                       __ldcg(plan + 3) == Hkv && __ldcg(plan + 4) == (CAUSAL ? 1 : 0) &&
-                       __ldcg(plan + 5) >= 0 && __ldcg(plan + 5) <= capacity;
+  const int4 head0 = __ldcg(reinterpret_cast<const int4*>(plan));
+  const int4 head1 = __ldcg(reinterpret_cast<const int4*>(plan) + 1);
+  const bool plan_ok = head0.x == kPlanMagic && head0.y == T && head0.z == G && head0.w == Hkv &&
+                       head1.x == (CAUSAL ? 1 : 0) && head1.y >= 0 && head1.y <= capacity;
   const bool abort_all = *s_abort != 0 || !plan_ok;
-  const int total = plan_ok ? __ldcg(plan + 5) * Hkv : 0;
+  const int total = plan_ok ? head1.y * Hkv : 0;
   if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
 
   uint8_t* sQ = smem + C::kOffQ;
@@ -655,7 +668,7 @@ size_t varlen_plan_bytes(int B, int T, int H, int Hkv) {
 cudaError_t launch_varlen_plan(const VarlenProblem& p, const int* cu, void* plan, cudaStream_t stream) {
   return launch_pdl(varlen_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, cu, static_cast<int*>(plan), p.B, p.T,
                     p.H / p.Hkv, p.Hkv, tile_tokens(p.H, p.Hkv), p.causal,
-                    (int)plan_capacity(p.B, p.T, p.H, p.Hkv));
+                    (int)plan_capacity(p.B, p.T, p.H, p.Hkv), device_sm_count());
 }
 
 cudaError_t launch_varlen_fwd(const VarlenProblem& p, const void* q, const void* k, const void* v, const void* plan,

@@ -129,7 +129,7 @@ PyObject* varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       T > INT32_MAX || H > INT32_MAX || d > INT32_MAX || !scale_of(a[4], d, &scale))
     Py_RETURN_NONE;
   const int64_t bytes = (int64_t)plan->nbytes();
-  const int64_t per = 2 * (128 / std::max<int64_t>(1, std::min<int64_t>(128, H / hk)));
+  const int64_t per = 128 / std::max<int64_t>(1, std::min<int64_t>(128, H / hk));
   const int64_t B = (bytes - 256) / 16 - T / per;
   Tensor o, lse;
   if (B < 1 || B > INT32_MAX || !output(a[6], {T, H, d}, at::kBFloat16, *q, &o) ||
