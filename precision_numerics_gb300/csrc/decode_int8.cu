@@ -187,9 +187,11 @@ __device__ __forceinline__ size_t out_row(const Args& a, int b, int h, int r) {
   return ((size_t)b * a.n_q + t) * a.H + h * a.G + (r - t * a.G);
 }
 
-__device__ __forceinline__ int length_of(const Args& a, int b) {
+// A sequence's length as it is in memory, and what is made of it.  Separate, since
+// the check waits for the value.
+__device__ __forceinline__ int read_length(const Args& a, int b) { return b < a.B ? __ldcg(a.lens + b) : 0; }
+__device__ __forceinline__ int checked(const Args& a, int len) {
   const long long cap = (long long)a.max_blocks << a.page_shift;
-  const int len = __ldcg(a.lens + b);
   if (len < 0 || len > cap) {
     set_fail(ATTN_ERR_INVALID_ARG);
     return len < 0 ? 0 : (int)cap;
@@ -206,7 +208,7 @@ __device__ __forceinline__ int cost_of(int len) { return len > 0 ? tiles_of(len)
 // rb), cost `left` behind them.
 struct Walk {
   int b, h, rb, len, ta, tb;
-  int len_next;  // of sequence b + 1, read ahead
+  int len_next;  // of sequence b + 1, read ahead, not yet checked
   long long left;
   __device__ __forceinline__ int count(int warp) const {  // tiles of warp `warp`: ta + warp + kWarps * k
     return tb > ta + warp ? (tb - ta - warp + kWarps - 1) / kWarps : 0;
@@ -218,7 +220,6 @@ struct Walk {
     ta = max(from - kSegmentCost, 0);
     tb = max(to - kSegmentCost, 0);
   }
-  __device__ __forceinline__ void read_ahead(const Args& a) { len_next = b + 1 < a.B ? length_of(a, b + 1) : 0; }
   __device__ __forceinline__ bool next(const Args& a) {
     if (left <= 0) return false;
     if (++rb == a.row_blocks) {
@@ -227,8 +228,8 @@ struct Walk {
         h = 0;
         do {
           if (++b >= a.B) return false;
-          len = len_next;
-          read_ahead(a);
+          len = checked(a, len_next);
+          len_next = read_length(a, b + 1);
         } while (len == 0);
       }
     }
@@ -243,12 +244,12 @@ __device__ __forceinline__ long long divide(long long x, int y) {
 }
 
 // Sequences without a position have no tile: their rows are empty.  The CTAs take
-// them by turns; len_first is the length of sequence blockIdx.x.
+// them by turns; len_first is the unchecked length of sequence blockIdx.x.
 template <int D>
 __device__ __forceinline__ void fill_empty(const Args& a, int len_first) {
   const int copies = a.Hkv * a.row_blocks;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if ((b == blockIdx.x ? len_first : length_of(a, b)) > 0) continue;
+    if (checked(a, b == blockIdx.x ? len_first : read_length(a, b)) > 0) continue;
     const size_t row = (size_t)b * a.n_q * a.H;
     for (int i = threadIdx.x; i < a.n_q * a.H * (D / 8); i += kThreads)
       reinterpret_cast<uint4*>(a.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.rb = x % a.row_blocks;
     sg.h = (x / a.row_blocks) % a.Hkv;
     sg.b = x / a.row_blocks / a.Hkv;
-    sg.len = length_of(a, sg.b);
+    sg.len = checked(a, read_length(a, sg.b));
     sg.len_next = 0;
     sg.ta = 0;
     sg.tb = tiles_of(sg.len);
@@ -333,9 +334,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     // first kThreads sequences are read and scanned once.
     long long* s_warp = reinterpret_cast<long long*>(s_merge);
     const long long copies = (long long)a.Hkv * a.row_blocks;
-    auto len_at = [&](int b) { return b < a.B ? length_of(a, b) : 0; };
-    int len = len_at(threadIdx.x);
-    len_first = len_at(blockIdx.x);  // for fill_empty, after the first loads are under way
+    auto len_at = [&](int b) { return checked(a, read_length(a, b)); };
+    const int len_mine = read_length(a, threadIdx.x);
+    len_first = read_length(a, blockIdx.x);  // for fill_empty, after the first loads are under way
+    int len = checked(a, len_mine);
     long long total, sum;
     long long ahead = scan_before(cost_of(len), s_warp, total);
     const long long first = total;
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.h = st.z / a.row_blocks;
     sg.rb = st.z % a.row_blocks;
     sg.left = min(per, total - begin);
-    sg.read_ahead(a);
+    sg.len_next = read_length(a, sg.b + 1);
     sg.take(st.w);
     if (sg.tb == sg.ta) {  // the run ends before the segment's first tile
       fill_empty<D>(a, len_first);
@@ -404,20 +406,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     const long long pos = ((long long)lw.ta + warp + (long long)kWarps * (ld_k + lane)) * kTile;
     if (ld_k + lane < ld_n) {
       const int* row = a.table + (size_t)lw.b * a.max_blocks;
+      const bool second = pos + 16 < lw.len;
       id0 = __ldcg(row + (pos >> a.page_shift));
-      if (id0 < 0 || id0 >= a.P) {
-        set_fail(ATTN_ERR_INVALID_ARG);
-        id0 = -1;
-      }
-      if (a.page >= kTile) {
-        id1 = id0;
-      } else if (pos + 16 < lw.len) {
-        id1 = __ldcg(row + ((pos + 16) >> a.page_shift));
-        if (id1 < 0 || id1 >= a.P) {
-          set_fail(ATTN_ERR_INVALID_ARG);
-          id1 = -1;
-        }
-      }
+      id1 = second ? __ldcg(row + ((pos + 16) >> a.page_shift)) : -1;
+      const bool fine0 = id0 >= 0 && id0 < a.P, fine1 = id1 >= 0 && id1 < a.P;
+      if (!fine0 || (second && !fine1)) set_fail(ATTN_ERR_INVALID_ARG);
+      if (!fine0) id0 = -1;
+      if (!fine1) id1 = -1;
     }
   };
   auto issue = [&]() {
@@ -441,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     const uint32_t head = heads + st * C::kHeadBytes;
     const uint32_t dst = ring + st * C::kStageBytes;
     if (lane == 0) {
-      const uint32_t flags = (p0 >= 0 ? 1u : 0u) | (p1 >= 0 ? 2u : 0u);
+      // A page of 32 positions or more holds both halves.
+      const uint32_t flags = a.page >= kTile ? (p0 >= 0 ? 3u : 0u) : (p0 >= 0 ? 1u : 0u) | (p1 >= 0 ? 2u : 0u);
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(head + 16), "r"(flags) : "memory");
       if (a.page >= kTile) {
         mbar_arrive_expect_tx(bar, p0 >= 0 ? C::kStageBytes : 0);
@@ -468,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     if (lane < 4) {
       // ks, vs of half 0, ks, vs of half 1.  A half without a page takes any
       // valid scale: its flag hides it.
-      const int p = max(lane < 2 ? p0 : p1, 0);
+      const int p = max(lane < 2 || a.page >= kTile ? p0 : p1, 0);
       copy4_arrive(head + 4 * lane, ((lane & 1) ? a.v_scale : a.k_scale) + (size_t)p * a.Hkv + lw.h, bar);
     }
     ++issued;
