@@ -470,13 +470,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     ++issued;
     ++ld_k;
   };
+  const int rows_total = a.n_q * a.G;
+  static_assert(NT <= kWarps, "a warp prepares one block of rows");
+  uint2 w[D / 16];  // the segment's Q row 8 warp + g, as this lane prepares it
+  auto load_q = [&]() {
+    const int r = sg.rb * kRows + 8 * warp + g;
+    const int t = token_of(a, r), hq = sg.h * a.G + (r - t * a.G);
+    const uint16_t* src = a.q + sg.b * a.q_batch + t * a.q_token + hq * a.q_head;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+      w[ks] = warp < NT && r < rows_total ? __ldcg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * c))
+                                          : make_uint2(0u, 0u);
+  };
+  // Ahead of the first tiles: behind every CTA's these few bytes would wait for
+  // tens of megabytes (3.5 us).  With 17 rows and more the registers are needed
+  // elsewhere (64 sequences of 20 rows 153 us, 157 us with it).
+  constexpr bool kAhead = NT <= 2;
+  if (kAhead) load_q();
   if (more) look_up();
 #pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) issue();
   if (a.parts != nullptr) fill_empty<D>(a, len_first);
 
-  const int rows_total = a.n_q * a.G;
-  static_assert(NT <= kWarps, "a warp prepares one block of rows");
   uint32_t used = 0;
   bool last_segment = false;
   while (!last_segment) {
@@ -486,15 +501,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     // which a lane holds 4 c + {0, 1} as k = 2c, 2c + 1 and 4 c + {2, 3} as
     // k = 2c + 8, 2c + 9 (the same assignment as the codes') of rows 8 n + g.  Warp n
     // prepares block n for all; the merge's buffer holds the fragments meanwhile.
+    if (!kAhead) load_q();
     if (warp < NT) {
       const int n = warp, r = sg.rb * kRows + 8 * n + g;
       const bool have = r < rows_total;
-      const int t = token_of(a, r), hq = sg.h * a.G + (r - t * a.G);
-      const uint16_t* src = a.q + sg.b * a.q_batch + t * a.q_token + hq * a.q_head;
-      uint2 w[D / 16];
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        w[ks] = have ? __ldcg(reinterpret_cast<const uint2*>(src + 16 * ks + 4 * c)) : make_uint2(0u, 0u);
+      const int t = token_of(a, r);
       float m = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
@@ -757,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
     }
     last_segment = !sg.next(a);
+    if (kAhead && !last_segment) load_q();
     if (!last_segment) __syncthreads();  // before the next segment's Q
   }
   if (!ok) {
