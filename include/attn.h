@@ -366,7 +366,7 @@ ATTN_API attn_status attn_cache_append_int8(const void* k, const void* v, long l
 /*
  * Reads ranges of positions back as values code * scale: packed token
  * cu_seqlens[b] + i of the outputs is position starts[b] + i of sequence b.
- *   k, v : [T,H_kv,d] of type dt (FP32, or BF16 rounded to nearest even),
+ *   k, v : [T,H_kv,d] of type dt (the product in FP32, or that rounded to BF16),
  *          contiguous, written; cu_seqlens[0] = 0, cu_seqlens[B] = T.  Tokens
  *          outside the sequences or without a valid page become 0 and are
  *          reported by attn_check_status().

