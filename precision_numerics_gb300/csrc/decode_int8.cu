@@ -39,9 +39,9 @@
 //
 // Measured (d = 128, 8 key heads, pages of 64): 64 sequences of 500 to 16000
 // positions with 4 query rows a key head 102-104 us (5.9 TB/s, 87% of a copy's
-// rate), one of 131000 positions 50 us (5.4 TB/s); with 20 rows 64 sequences 153 us:
-// the accumulators then leave 8 warps an SM, and the dependent conversions and
-// products of a tile (2 us a warp) set the pace.
+// rate), one of 131000 positions 50 us (5.4 TB/s); d = 64: 57 us and 30 us; with 20
+// rows 64 sequences 153 us: the accumulators then leave 8 warps an SM, and the
+// dependent conversions and products of a tile (2 us a warp) set the pace.
 #include <math.h>
 #include <stdint.h>
 
@@ -68,14 +68,21 @@ constexpr int kSegmentCost = 8;
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_decode, code); }
 
+// CTAs an SM for blocks of 8 rows of d columns: as many as the registers allow.
+// More warps are worth more than deeper rings (d = 64, 8 rows: 4 CTAs with 2 stages
+// 56.7 us on a ragged batch, 3 with 4 stages 62.6, 2 with 5 stages 75.8);
+// 12 rows over 64 sequences: 3 CTAs with 3 stages 81 us, 2 with 5 stages 96.
+constexpr int ctas_per_sm(int d, int nt) {
+  if (d == 64) return nt == 1 ? 4 : nt == 2 ? 3 : 2;
+  return nt == 1 ? 3 : 2;
+}
+
 // NT blocks of 8 query rows (token, head of the group) per pass over the keys.
-// 12 warps an SM for 8 rows, 8 beyond, as the registers allow; the rings take the
-// shared memory that is left.
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtas = NT == 1 ? 3 : 2;  // per SM
-  static constexpr int kStages = NT == 2 ? (D == 128 ? 3 : 5) : 2 * (128 / D);
+  static constexpr int kCtas = ctas_per_sm(D, NT);
+  static constexpr int kStages = D == 64 ? (NT == 1 ? 2 : NT == 2 ? 3 : 4) : NT == 2 ? 3 : 2;
   static constexpr int kHalfBytes = kTile * D;          // K or V of a tile
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
@@ -876,9 +883,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
 
 // Runs the tiles are dealt in: the CTAs that the SMs hold at a time.  (The full
 // device's SM count where there is no device to ask, for workspace sizes.)
-unsigned decode_runs(int nt) {
+unsigned decode_runs(int d, int nt) {
   const int sms = device_sm_count();
-  return (nt == 1 ? 3u : 2u) * (sms > 0 ? sms : 152);
+  return (unsigned)(ctas_per_sm(d, nt) * (sms > 0 ? sms : 152));
 }
 
 bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
@@ -925,7 +932,7 @@ int row_tiles(int rows) { return ceil_div(rows, 8 * row_passes(rows)); }
 size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H) {
   if (!splits(c)) return 0;
   const int rows = n_q * (H / c.Hkv), nt = row_tiles(rows);
-  const size_t runs = decode_runs(nt);
+  const size_t runs = decode_runs(c.d, nt);
   return align256(runs * 2 * part_floats(c.d, 8 * nt) * sizeof(float)) + runs * sizeof(Chain);
 }
 
@@ -955,7 +962,7 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   a.by_segment = 0;
   unsigned runs = 0;
   if (splits(c)) {
-    runs = decode_runs(nt);
+    runs = decode_runs(c.d, nt);
     a.by_segment = (long long)a.B * a.Hkv * a.row_blocks <= runs;
     a.parts = static_cast<float*>(workspace);
     a.chains = reinterpret_cast<Chain*>(static_cast<char*>(workspace) +

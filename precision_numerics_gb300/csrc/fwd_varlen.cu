@@ -23,6 +23,10 @@
 //    are written one by one, 8 lanes a 128-byte line, after a turn through shared
 //    memory that gives each lane 16 bytes of it.
 //
+// Apart from fwd_bf16.cu so that what serves packed and grouped sequences (list of
+// items, masks at both ends, row-wise output) takes no register or instruction from
+// the forward over equal lengths.
+//
 // Bound, as in fwd_bf16.cu, by the softmax and its hand-over to the tensor pipe
 // for long sequences (16384 tokens, 16 query and 2 key heads of 128: 732 us, 1500
 // TFLOP/s), and by the ends of the items for short ones (12 sequences of 65 to 2048
