@@ -384,6 +384,9 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, scale=None, causal=False, 
 # third of the time; it returns None where something is not as it should be, and
 # the function's own checks then find out what.
 
+# With another stream given, what a call allocates is that stream's memory: the
+# current stream's allocator would hand it on while the kernels still use it.
+
 # Each check first asks for everything at once, and looks for what is wrong only
 # then: attribute reads are most of what a call costs on the host.
 
@@ -445,6 +448,15 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table):
     return B, pages, hk, page, d, blocks
 
 
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def attn_varlen_plan_bytes(B: int, T: int, H: int, H_kv: int) -> int:
     return int(load_library().attn_varlen_plan_bytes(B, T, H, H_kv))
 
@@ -455,8 +467,7 @@ def attn_varlen_plan(cu_seqlens, T, H, H_kv, causal=True, plan=None, stream=None
     _check_ints("cu_seqlens", cu_seqlens)
     B = cu_seqlens.shape[0] - 1
     if plan is None:
-        plan = torch.empty(max(attn_varlen_plan_bytes(B, T, H, H_kv), 1), dtype=torch.uint8,
-                           device=cu_seqlens.device)
+        plan = _empty(max(attn_varlen_plan_bytes(B, T, H, H_kv), 1), torch.uint8, cu_seqlens.device, stream)
     _call("attn_varlen_plan", cu_seqlens.data_ptr(), B, T, H, H_kv, int(bool(causal)), plan.data_ptr(),
           _nbytes(plan), _stream(stream))
     return plan
@@ -489,11 +500,11 @@ def attn_varlen_fwd(q, k, v, plan, scale=None, causal=True, o=None, lse=None, st
     if hk < 1 or H < 1 or H % hk:
         raise ValueError(f"H = {H} is not a multiple of H_kv = {hk}")
     if o is None:
-        o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        o = _empty((T, H, d), q.dtype, q.device, stream)
     else:
         _check_dense("o", o, (T, H, d), torch.bfloat16)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     else:
         _check_dense("lse", lse, (T, H), torch.float32)
     B = _plan_batch(plan, T, H, hk)
@@ -542,11 +553,11 @@ def attn_cache_read_int8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
     if k is None:
-        k = torch.empty((T, hk, d), dtype=dtype, device=k_cache.device)
+        k = _empty((T, hk, d), dtype, k_cache.device, stream)
     else:
         _check_dense("k", k, (T, hk, d), dtype)
     if v is None:
-        v = torch.empty((T, hk, d), dtype=dtype, device=k_cache.device)
+        v = _empty((T, hk, d), dtype, k_cache.device, stream)
     else:
         _check_dense("v", v, (T, hk, d), dtype)
     _call("attn_cache_read_int8", k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
@@ -576,16 +587,16 @@ def attn_decode_int8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens
     _check_rows("q", q, (B, n_q, H, d))
     _check_ints("seqlens", seqlens, B)
     if o is None:
-        o = torch.empty((B, n_q, H, d), dtype=q.dtype, device=q.device)
+        o = _empty((B, n_q, H, d), q.dtype, q.device, stream)
     else:
         _check_dense("o", o, (B, n_q, H, d), torch.bfloat16)
     if lse is None:
-        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
+        lse = _empty((B, n_q, H), torch.float32, q.device, stream)
     else:
         _check_dense("lse", lse, (B, n_q, H), torch.float32)
     if workspace is None:
         need = attn_decode_int8_workspace_bytes(B, n_q, H, hk, d, page, blocks)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 1), torch.uint8, q.device, stream)
     _call("attn_decode_int8", q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
           seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, n_q, H, hk, d, pages, page, blocks,

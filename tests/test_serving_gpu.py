@@ -629,6 +629,38 @@ def test_calls_with_a_stream_given(A):
     A.attn_check_status()
 
 
+def test_memory_of_calls_on_another_stream(A, monkeypatch):
+    """What a call on a given stream allocates is memory of that stream: once the call has returned,
+    and its tensors are gone, the current stream does not get it while the kernels may still run."""
+    H, Hkv, d, page, T = 2, 1, 64, 16, 600
+    q, kv = normal((T, H, d), 1).cuda(), normal((T, Hkv, d), 2).cuda()
+    tables, pages = scattered([40], 3)
+    c = Cache(pages, Hkv, page, d, tables)
+    cu, starts, lens = ints([0, T]), ints([0]), ints([T])
+    plan = A.attn_varlen_plan(cu, T, H, Hkv)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    used = []
+    call = A._call
+    monkeypatch.setattr(A, "_call", lambda name, *args: used.extend(
+        x for x in args if isinstance(x, int) and x > 1 << 32) or call(name, *args))
+    workspace = A.attn_decode_int8_workspace_bytes(1, 1, H, Hkv, d, page, 40)
+    calls = (
+        (lambda s: A.attn_varlen_plan(cu, T, H, Hkv, stream=s), [A.attn_varlen_plan_bytes(1, T, H, Hkv)]),
+        (lambda s: A.attn_varlen_fwd(q, kv, kv, plan, stream=s), [T * H * d * 2, T * H * 4]),
+        (lambda s: A.attn_cache_read_int8(*c.gpu, cu, starts, T, stream=s), [T * Hkv * d * 2] * 2),
+        (lambda s: A.attn_decode_int8(q[:1, None], *c.gpu, lens, stream=s), [H * d * 2, H * 4, workspace]),
+    )
+    for run, sizes in calls:
+        for stream in (side, side.cuda_stream):
+            used.clear()
+            run(stream)
+            after = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+            assert used and not set(used) & {x.data_ptr() for x in after}
+            torch.cuda.synchronize()
+    A.attn_check_status()
+
+
 # ------------------------------------------------ sizes, layouts, several calls
 def test_thousands_of_sequences(A):
     """More sequences than any kernel holds at a time, many of them empty."""
