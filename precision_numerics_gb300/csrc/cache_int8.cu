@@ -131,7 +131,7 @@ struct Quantizer {
       c[e] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + e)) - 8388736.f;  // 2^23 + (c + 128)
       const float y = fmaf(c[e], ratio, 12582912.f);
       fine = fine && fabsf(fmaf(c[e], ratio, 12582912.f - y)) < 0.4999f;
-      q[e] = __float_as_uint(y);
+      q[e] = __float_as_uint(fmaxf(y, 12582912.f - 127.f));  // a held -128 as well
     }
     if (!fine) {
 #pragma unroll 1

@@ -281,6 +281,24 @@ def test_append_values_on_the_border(A):
     assert c.equal()
 
 
+@pytest.mark.parametrize("rows", [1, 20])
+def test_append_rescales_the_lowest_code(A, rows):
+    """Held codes of -128, which the cache's own writes never leave, are clamped like all others
+    when their page's scale grows a little."""
+    page, d, start = 32, 64, 7
+    tables, pages = scattered([1], 5)
+    c = Cache(pages, 1, page, d, tables)
+    for codes in c.codes:
+        codes[:, :, :start, ::3] = -128
+    c.scales = [torch.full((pages, 1), 2.0125 / 127) for _ in range(2)]
+    c.upload()
+    new = torch.full((rows, 1, d), 2.015625, dtype=BF)
+    c.append([new, new], [0, rows], [start])
+    A.attn_cache_append_int8(new.cuda(), new.cuda(), *c.gpu, ints([0, rows]), ints([start]))
+    A.attn_check_status()
+    assert c.equal() and all((x[tables[0][0], 0, :start].amin() == -127) for x in c.codes)
+
+
 def test_append_many_sequences(A):
     """More sequences than a CTA scans at a time, one token each, as a decoding step does."""
     B, Hkv, page, d = 300, 2, 16, 64
