@@ -34,8 +34,10 @@
 // segments, one behind the other, are dealt to the CTAs in equal runs, so that
 // ragged lengths and few sequences keep every SM busy alike.  A run that holds a
 // whole segment writes its output; of a segment that runs on into the next
-// CTAs' runs every part leaves (m, l, unnormalised O) in the workspace, two slots
-// a CTA at most, and decode_join_kernel joins them in the order of the CTAs.
+// CTAs' runs every part leaves (m, l, O / l) in the workspace, two slots a CTA at
+// most, and decode_join_kernel joins them in the order of the CTAs.  Warps and parts
+// are joined as means with weights of at most 1, so that values up to the largest
+// that a scale allows do not overflow on the way.
 //
 // Measured (d = 128, 8 key heads, pages of 64): 64 sequences of 500 to 16000
 // positions with 4 query rows a key head 102-104 us (5.9 TB/s, 87% of a copy's
@@ -159,9 +161,13 @@ __device__ __forceinline__ uint32_t unit_offset(uint32_t r, uint32_t u) {
   return D == 128 ? r * 128u + ((u ^ (r & 7u)) << 4) : r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
 }
 
+// 1 / L (L < 2^47, off by 2 units of the last bit at most), or 0 where a row has seen
+// nothing.  A NaN stays one.
+__device__ __forceinline__ float inverse(float L) { return L == 0.f ? 0.f : __fdividef(1.f, L); }
+
 // Natural-log LSE from the base-2 maximum and the row sum, which carries 2^15.
 __device__ __forceinline__ float lse_of(float M, float L) {
-  return L > 0.f ? (M + log2f(L) - 15.f) * 0.69314718055994531f : -INFINITY;
+  return L == 0.f ? -INFINITY : (M + log2f(L) - 15.f) * 0.69314718055994531f;
 }
 
 // A segment in several parts: those behind the first (0: nothing to join), its
@@ -188,7 +194,7 @@ struct Args {
   int by_segment;
 };
 
-// A part in the workspace: O [rows][D], m [rows], l [rows], FP32.
+// A part in the workspace: O [rows][D] divided by l, m [rows], l [rows], FP32.
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
 
 // Query token of row r (< 2^14) of a key head's rows, and its row of o and lse.
@@ -731,6 +737,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           s_m[warp * kRows + 8 * n + 2 * c + i] = m_run[n][i];
           s_l[warp * kRows + 8 * n + 2 * c + i] = l_run[n][i];
         }
+        l_run[n][i] = inverse(l_run[n][i]);
       }
 #pragma unroll
     for (int half = 0; half < D / 64; ++half) {
@@ -745,21 +752,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * 64 + (((8 * u + g) ^ (c << 2)) << 1)) =
-                make_float2(acc[half * 4 + u][n][i] * R, acc[half * 4 + u][n][2 + i] * R);
+                make_float2(acc[half * 4 + u][n][i] * l_run[n][i] * R, acc[half * 4 + u][n][2 + i] * l_run[n][i] * R);
         }
       __syncthreads();
       // rows x 64 columns over 128 threads, 4 columns at a time.
 #pragma unroll 1
       for (int x = threadIdx.x; x < kRows * 16; x += kThreads) {
         const int r = x >> 4, part4 = x & 15;
-        float M = -INFINITY, L = 0.f, v[4] = {};
+        float M = -INFINITY, L = 0.f, v[4] = {}, share[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + r]);
         const float M_use = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2(s_m[w * kRows + r] - M_use);
-          L += s_l[w * kRows + r] * f;
+          share[w] = s_l[w * kRows + r] * ex2(s_m[w * kRows + r] - M_use);
+          L += share[w];
+        }
+        const float inv = inverse(L);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = share[w] * inv;
           const float4 y = *reinterpret_cast<const float4*>(
               s_merge + (w * kRows + r) * 64 + (((2 * part4) ^ (((r >> 1) & 3) << 2)) << 1));
           v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
@@ -773,9 +785,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           }
         } else if (rr < rows_total) {
           const size_t row = out_row(a, sg.b, sg.h, rr);
-          const float inv = L > 0.f ? 1.f / L : 0.f;
           *reinterpret_cast<uint2*>(a.o + row * D + half * 64 + part4 * 4) =
-              make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
           if (half == 0 && part4 == 0) a.lse[row] = lse_of(M, L);
         }
       }
@@ -808,11 +819,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
   const int rr = ch.z % a.row_blocks * rows + r;
   const bool have = r < rows && rr < a.n_q * a.G;
   const int n = have ? ch.x + 1 : 0;
+  // l, at most 2^15 a key of less than 2^31, becomes a weight below 1.
+  constexpr float kShare = 0x1p-46f;
   // kBatch parts at a time, all their loads in flight together.
   constexpr int kBatch = 8;
   float M = -INFINITY, L = 0.f, o[D / 32] = {};
   for (int i0 = warp % per_row; i0 < n; i0 += kBatch * per_row) {
-    float m[kBatch], l[kBatch], x[kBatch][D / 32];
+    float m[kBatch], l[kBatch], x[kBatch][D / 32];  // l times kShare
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * per_row;
@@ -822,7 +835,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
       if (i < n) {
         const float* p = a.parts + (size_t)(2 * (ch.w + i) + (i == 0)) * part_floats(D, rows);
         m[k] = __ldcg(p + rows * D + r);
-        l[k] = __ldcg(p + rows * D + rows + r);
+        l[k] = __ldcg(p + rows * D + rows + r) * kShare;
         const float* q = p + r * D + lane * (D / 32);
         if constexpr (D == 128) {
           const float4 v = __ldcg(reinterpret_cast<const float4*>(q));
@@ -844,8 +857,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
     for (int e = 0; e < D / 32; ++e) o[e] *= keep;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const float f = ex2(m[k] - m_use);
-      L += f * l[k];
+      const float f = ex2(m[k] - m_use) * l[k];
+      L += f;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) o[e] += f * x[k][e];
     }
@@ -872,13 +885,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
   }
   if (!have) return;
   const size_t row = out_row(a, ch.y, ch.z / a.row_blocks, rr);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = inverse(L);
   uint16_t* out = a.o + row * D + lane * (D / 32);
   if constexpr (D == 128)
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0] * inv, o[1] * inv);
-  if (lane == 0) a.lse[row] = lse_of(M, L);
+  if (lane == 0) a.lse[row] = lse_of(M, L * (1.f / kShare));
 }
 
 // Runs the tiles are dealt in: the CTAs that the SMs hold at a time.  (The full

@@ -466,6 +466,28 @@ def test_decode_scales_of_every_size(A):
     check_decode(c, q, lens, 1 / math.sqrt(d), o, lse)
 
 
+@pytest.mark.parametrize("d,n_q", [(64, 1), (128, 1), (128, 5)])
+@pytest.mark.parametrize("lens", [[40, 300], [3000, 9, 20000]])
+def test_decode_largest_values_and_nan_rows(A, lens, d, n_q):
+    """Value scales up to 2^118, whose sums over the keys leave the type; a NaN in a query stays in its
+    row of O and LSE."""
+    H, Hkv, page = 4, 2, 32
+    tables, pages = scattered([-(-n // page) for n in lens], 17)
+    c = Cache(pages, Hkv, page, d, tables)
+    c.scales[1][:] = 2.0 ** torch.randint(90, 119, c.scales[1].shape, generator=torch.Generator().manual_seed(4))
+    c.upload()
+    q = normal((len(lens), n_q, H, d), 1)
+    bad = q.clone()
+    bad[1, n_q - 1, 2, 3] = torch.nan
+    o, lse = A.attn_decode_int8(bad.cuda(), *c.gpu, ints(lens))
+    assert o[1, n_q - 1, 2].isnan().all() and lse[1, n_q - 1, 2].isnan()
+    good, good_lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens))
+    A.attn_check_status()
+    check_decode(c, q, lens, 1 / math.sqrt(d), good, good_lse)
+    o[1, n_q - 1, 2], lse[1, n_q - 1, 2] = good[1, n_q - 1, 2], good_lse[1, n_q - 1, 2]
+    assert torch.equal(o, good) and torch.equal(lse, good_lse)
+
+
 def test_decode_shared_pages_views_and_bad_lengths(A):
     """Two sequences share their first pages; q is a view of a fused projection's output; rows of the
     last page behind the length do not count; a length past the table and a bad page are reported."""
