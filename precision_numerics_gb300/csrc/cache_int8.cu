@@ -66,6 +66,13 @@ __device__ __noinline__ int code_of(float xh, float xl, float s) {
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
+// Largest of |a|, |b|, |c|; NaN where one is.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // A scale and what its codes need: 1 / s, and the bound on |x - k s| below which
 // the rounded x * (1 / s) is the code (0 where the scale is too small or large
 // for that: every code then goes through code_of).
@@ -85,16 +92,21 @@ struct Quantizer {
   __device__ __forceinline__ uint2 codes(const uint4& w) const {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
     uint32_t q[8];
-    float far = 0.f;
+    float far = 0.f;  // NaN as well: an infinity's rest
+    const uint64_t inv2 = f2_pack(inv, inv), up2 = f2_pack(12582912.f, 12582912.f),
+                   down2 = f2_pack(-12582912.f, -12582912.f), minus_s2 = f2_pack(-s, -s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = (e & 1) ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]);
-      const float y = fmaf(x, inv, 12582912.f);
-      const float rest = fabsf(fmaf(-(y - 12582912.f), s, x));
-      far = rest < near ? far : INFINITY;
-      q[e] = __float_as_uint(y);
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t x = f2_pack(bf16_lo(v[e]), bf16_hi(v[e]));
+      const uint64_t y = fma2(x, inv2, up2);
+      float r0, r1, y0, y1;
+      f2_unpack(fma2(add2(y, down2), minus_s2, x), r0, r1);
+      f2_unpack(y, y0, y1);
+      far = max3_abs_nan(far, r0, r1);
+      q[2 * e] = __float_as_uint(y0);
+      q[2 * e + 1] = __float_as_uint(y1);
     }
-    if (far > 0.f) {
+    if (!(far < near)) {
       bool plain = near > 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -166,10 +178,8 @@ __device__ __forceinline__ void requantize(int8_t* codes, int units, const Quant
 
 // Largest |x| of 8 BF16 values, as bits in both halves of the result, with `m`.
 __device__ __forceinline__ uint32_t max_bits(uint32_t m, const uint4& w) {
-  m = __vmaxu2(m, w.x & 0x7FFF7FFFu);
-  m = __vmaxu2(m, w.y & 0x7FFF7FFFu);
-  m = __vmaxu2(m, w.z & 0x7FFF7FFFu);
-  return __vmaxu2(m, w.w & 0x7FFF7FFFu);
+  m = __vimax3_u16x2(m, w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
+  return __vimax3_u16x2(m, w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu);
 }
 // The same over finite values only.
 __device__ __forceinline__ uint32_t finite_bits(uint32_t m, const uint4& w) {
