@@ -21,8 +21,8 @@
 // or V) and keeps the new rows in registers between the maximum and the codes, so
 // every byte moves once; for a step's few rows a page a CTA takes a page of K or
 // V and its warps the heads, so that the search for the page is done once.
-// Measured (8 heads of 128, pages of 64): 16 prompts of 150 to 4096 tokens appended in
-// 21 us (3.8 TB/s) and read back as FP32 in 23.5 us (5.7 TB/s); one token of each of 96
+// Measured (8 heads of 128, pages of 64): 16 prompts of 150 to 4096 tokens appended
+// and read back as FP32 in 41.4 us, 23.5 of them the reading (5.7 TB/s); one token of each of 96
 // sequences in 4.5 us.
 #include <math.h>
 #include <stdint.h>
@@ -38,7 +38,6 @@ static __device__ unsigned int g_status_cache;
 
 namespace {
 
-constexpr int kAppendThreads = 128;
 constexpr int kStepRows = 8;  // up to so many rows a sequence (on average) are a step
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_cache, code); }
@@ -280,14 +279,14 @@ __device__ __forceinline__ Found find_page(const AppendArgs& a, int item) {
 }
 
 // D head dims; kUnits: 16-byte units of new rows a thread holds at most
-// (page * D / 8 units over 128 threads).
-template <int D, int kUnits>
-__global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const __grid_constant__ AppendArgs a) {
+// (page * D / 8 units over its threads).
+template <int D, int kUnits, int kThreads>
+__global__ void __launch_bounds__(kThreads) append_int8_kernel(const __grid_constant__ AppendArgs a) {
   griddep_wait();
-  __shared__ uint32_t s_max[kAppendThreads / 32];
+  __shared__ uint32_t s_max[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kv = blockIdx.z;
-  const Found f = find_page<kAppendThreads>(a, blockIdx.x);
+  const Found f = find_page<kThreads>(a, blockIdx.x);
   if (f.page < 0) return;
   for (int head = blockIdx.y; head < a.Hkv; head += gridDim.y) {
     const uint16_t* x = a.x[kv] + f.row0 * a.token_stride[kv] + head * a.head_stride[kv];
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const __gri
     uint4 w[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int u = tid + i * kAppendThreads;
+      const int u = tid + i * kThreads;
       w[i] = make_uint4(0u, 0u, 0u, 0u);
       if (u < units)
         w[i] = __ldcg(reinterpret_cast<const uint4*>(x + (u / kPerRow) * a.token_stride[kv] + (u % kPerRow) * 8));
@@ -319,16 +318,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_int8_kernel(const __gri
     if (lane == 0) s_max[warp] = m;
     __syncthreads();  // the maxima, and everyone has read the old scale
 #pragma unroll
-    for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, s_max[i]);
+    for (int i = 0; i < kThreads / 32; ++i) m = max(m, s_max[i]);
     const Quantizer qz(fmaxf(s_old, scale_for(m)));
     if (tid == 0) *scale = qz.s;
 
     if (qz.s > s_old) {  // rows the page holds already, on the coarser scale
-      requantize(codes, f.r0 * (D / 16), qz, s_old, tid, kAppendThreads);
+      requantize(codes, f.r0 * (D / 16), qz, s_old, tid, kThreads);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int u = tid + i * kAppendThreads;
+      const int u = tid + i * kThreads;
       if (u < units) *reinterpret_cast<uint2*>(codes + (size_t)f.r0 * D + (size_t)u * 8) = qz.codes(w[i]);
     }
     __syncthreads();  // before the next head's maxima
@@ -497,23 +496,25 @@ cudaError_t launch_cache_append_int8(const PagedCache& c, const void* k, const v
     auto kernel = c.d == 128 ? append_step_int8_kernel<128> : append_step_int8_kernel<64>;
     return launch_pdl(kernel, dim3(most, 2), dim3(kStepThreads), 0, stream, a);
   }
-  // As many heads a CTA as make one wave of 8 CTAs an SM: the search for the page
-  // takes as long as a head's rows.
+  // As many heads a CTA as make three waves of 8 CTAs an SM: the search for the page
+  // takes as long as a head's rows, and a single wave waits for the SMs that have a CTA
+  // more (16 prompts 42.4 us with their read-back, 41.4 in three waves).
   const int sms = device_sm_count();
-  const long long waves = sms > 0 ? ((long long)most * c.Hkv * 2 + sms * 8ll - 1) / (sms * 8ll) : 1;
+  const long long waves = sms > 0 ? ((long long)most * c.Hkv * 2 + sms * 24ll - 1) / (sms * 24ll) : 1;
   const dim3 grid(most, ceil_div(c.Hkv, (int)std::min<long long>(waves, c.Hkv)), 2);
-  const int units = ceil_div(c.page * c.d / 8, kAppendThreads);
-#define ATTN_APPEND_CASE(DD, UU) \
-  if (c.d == DD && units == UU)  \
-    return launch_pdl(append_int8_kernel<DD, UU>, grid, dim3(kAppendThreads), 0, stream, a);
-  ATTN_APPEND_CASE(64, 1)
-  ATTN_APPEND_CASE(64, 2)
-  ATTN_APPEND_CASE(64, 4)
-  ATTN_APPEND_CASE(64, 8)
-  ATTN_APPEND_CASE(128, 2)
-  ATTN_APPEND_CASE(128, 4)
-  ATTN_APPEND_CASE(128, 8)
-  ATTN_APPEND_CASE(128, 16)
+  const int units = c.page * c.d / 8;
+  // 128 threads with up to 8 units each; 16 would cost half the CTAs of an SM.
+#define ATTN_APPEND_CASE(DD, UU, TT) \
+  if (c.d == DD && units == UU * TT) \
+    return launch_pdl(append_int8_kernel<DD, UU, TT>, grid, dim3(TT), 0, stream, a);
+  ATTN_APPEND_CASE(64, 1, 128)
+  ATTN_APPEND_CASE(64, 2, 128)
+  ATTN_APPEND_CASE(64, 4, 128)
+  ATTN_APPEND_CASE(64, 8, 128)
+  ATTN_APPEND_CASE(128, 2, 128)
+  ATTN_APPEND_CASE(128, 4, 128)
+  ATTN_APPEND_CASE(128, 8, 128)
+  ATTN_APPEND_CASE(128, 8, 256)
 #undef ATTN_APPEND_CASE
   return cudaErrorInvalidValue;
 }
