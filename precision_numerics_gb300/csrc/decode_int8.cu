@@ -73,10 +73,11 @@ __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status
 // CTAs an SM for blocks of 8 rows of d columns: as many as the registers allow.
 // More warps are worth more than deeper rings (d = 64, 8 rows: 4 CTAs with 2 stages
 // 56.7 us on a ragged batch, 3 with 4 stages 62.6, 2 with 5 stages 75.8);
-// 12 rows over 64 sequences: 3 CTAs with 3 stages 81 us, 2 with 5 stages 96.
+// 12 rows over 64 sequences: 3 CTAs with 3 stages 81 us, 2 with 5 stages 96; d = 128,
+// 12 rows: 3 CTAs with 2 stages 114 us, 2 with 3 stages 121.
 constexpr int ctas_per_sm(int d, int nt) {
   if (d == 64) return nt == 1 ? 4 : nt == 2 ? 3 : 2;
-  return nt == 1 ? 3 : 2;
+  return nt <= 2 ? 3 : 2;
 }
 
 // NT blocks of 8 query rows (token, head of the group) per pass over the keys.
@@ -84,12 +85,14 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kCtas = ctas_per_sm(D, NT);
-  static constexpr int kStages = D == 64 ? (NT == 1 ? 2 : NT == 2 ? 3 : 4) : NT == 2 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? (NT == 1 ? 2 : NT == 2 ? 3 : 4) : 2;
   static constexpr int kHalfBytes = kTile * D;          // K or V of a tile
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kOffMerge = kWarps * kRingBytes;  // FP32 [warp][rows][64 columns]
-  static constexpr int kOffStat = kOffMerge + kWarps * kRows * 64 * 4;  // m, l: FP32 [2][warp][rows]
+  // Columns that are merged at a time, and the buffer, FP32 [warp][rows][columns].
+  static constexpr int kMerge = D == 128 && NT == 2 ? 32 : 64;
+  static constexpr int kOffMerge = kWarps * kRingBytes;
+  static constexpr int kOffStat = kOffMerge + kWarps * kRows * kMerge * 4;  // m, l: FP32 [2][warp][rows]
   // Per warp and stage: ks, vs of the tile's two halves (16 positions each),
   // then one word of flags (bit per half that was loaded).
   static constexpr int kOffHead = kOffStat + 2 * kWarps * kRows * 4;
@@ -320,9 +323,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   float* s_f = reinterpret_cast<float*>(s_q + NT * (D / 16) * 32);
   int* s_last = reinterpret_cast<int*>(s_f + kRows);
 
-  // No griddep_launch_dependents() here: the next launch of this kernel would fill
-  // the slots that free up first and keep an uneven share of the SMs (one long
-  // sequence 54 us a call without it, 72 us with it).
+  // The dependents (the join, or the next launch) are let in when a warp has no more
+  // tiles to ask for, not here: they would fill the slots that free up first and the
+  // CTAs of the next launch keep an uneven share of the SMs (one long sequence 54 us a
+  // call, 72 with it).
   bool ok = (smem_u32(smem) & 1023u) == 0;
   if (lane == 0) {
     // Five arrivals per tile: lane 0's, with the bytes of K and V, and the four
@@ -441,7 +445,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         more = lw.next(a);
         ld_n = more ? lw.count(warp) : 0;
       } while (more && ld_n == 0);
-      if (!more) return;
+      if (!more) {
+        griddep_launch_dependents();
+        return;
+      }
       ld_k = 0;
       // The next key head of a sequence has the same pages: the lanes may hold them.
       if (lw.b != ids_b || lw.ta != ids_ta || ld_base != 0 || ld_n > ids_n) look_up();
@@ -740,26 +747,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         l_run[n][i] = inverse(l_run[n][i]);
       }
 #pragma unroll
-    for (int half = 0; half < D / 64; ++half) {
-      __syncthreads();  // the buffer holds Q, or the other half, until here
-      // Pairs of columns, moved by four for every second row, so that the 16 lanes
-      // of a phase cover all banks.
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 8 * n + 2 * c + i;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * 64 + (((8 * u + g) ^ (c << 2)) << 1)) =
-                make_float2(acc[half * 4 + u][n][i] * l_run[n][i] * R, acc[half * 4 + u][n][2 + i] * l_run[n][i] * R);
-        }
-      __syncthreads();
-      // rows x 64 columns over 128 threads, 4 columns at a time.
-#pragma unroll 1
-      for (int x = threadIdx.x; x < kRows * 16; x += kThreads) {
-        const int r = x >> 4, part4 = x & 15;
-        float M = -INFINITY, L = 0.f, v[4] = {}, share[kWarps];
+    for (int at = 0; at < D; at += C::kMerge) {
+      __syncthreads();  // the buffer holds Q, or the columns before, until here
+      if (at == 0 && threadIdx.x < kRows) {  // the warps' shares of a row, in place of their sums
+        const int r = threadIdx.x, rr = sg.rb * kRows + r;
+        float M = -INFINITY, L = 0.f, share[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * kRows + r]);
         const float M_use = M == -INFINITY ? 0.f : M;
@@ -770,24 +762,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         }
         const float inv = inverse(L);
 #pragma unroll
+        for (int w = 0; w < kWarps; ++w) s_l[w * kRows + r] = share[w] * inv;
+        if (!whole) {
+          part[kRows * D + r] = M;
+          part[kRows * D + kRows + r] = L;
+        } else if (rr < rows_total) {
+          a.lse[out_row(a, sg.b, sg.h, rr)] = lse_of(M, L);
+        }
+      }
+      // Pairs of columns, moved by four for every second row, so that the 16 lanes
+      // of a phase cover all banks.
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * n + 2 * c + i;
+#pragma unroll
+          for (int u = 0; u < C::kMerge / 16; ++u)
+            *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * C::kMerge + (((8 * u + g) ^ (c << 2)) << 1)) =
+                make_float2(acc[at / 16 + u][n][i] * l_run[n][i] * R, acc[at / 16 + u][n][2 + i] * l_run[n][i] * R);
+        }
+      __syncthreads();
+      // rows x columns over 128 threads, 4 columns at a time.
+#pragma unroll 1
+      for (int x = threadIdx.x; x < kRows * (C::kMerge / 4); x += kThreads) {
+        const int r = x / (C::kMerge / 4), part4 = x % (C::kMerge / 4);
+        float v[4] = {};
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float f = share[w] * inv;
+          const float f = s_l[w * kRows + r];
           const float4 y = *reinterpret_cast<const float4*>(
-              s_merge + (w * kRows + r) * 64 + (((2 * part4) ^ (((r >> 1) & 3) << 2)) << 1));
+              s_merge + (w * kRows + r) * C::kMerge + (((2 * part4) ^ (((r >> 1) & 3) << 2)) << 1));
           v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
         }
         const int rr = sg.rb * kRows + r;
         if (!whole) {
-          *reinterpret_cast<float4*>(part + r * D + half * 64 + part4 * 4) = make_float4(v[0], v[1], v[2], v[3]);
-          if (half == 0 && part4 == 0) {
-            part[kRows * D + r] = M;
-            part[kRows * D + kRows + r] = L;
-          }
+          *reinterpret_cast<float4*>(part + r * D + at + part4 * 4) = make_float4(v[0], v[1], v[2], v[3]);
         } else if (rr < rows_total) {
           const size_t row = out_row(a, sg.b, sg.h, rr);
-          *reinterpret_cast<uint2*>(a.o + row * D + half * 64 + part4 * 4) =
+          *reinterpret_cast<uint2*>(a.o + row * D + at + part4 * 4) =
               make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-          if (half == 0 && part4 == 0) a.lse[row] = lse_of(M, L);
         }
       }
     }
