@@ -382,7 +382,8 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, scale=None, causal=False, 
 #
 # A call on the current stream goes through the C++ binding first, which takes a
 # third of the time; it returns None where something is not as it should be, and
-# the function's own checks then find out what.
+# the function's own checks then find out what.  Its new outputs of up to 256 KB
+# together share one storage.
 
 # With another stream given, what a call allocates is that stream's memory: the
 # current stream's allocator would hand it on while the kernels still use it.

@@ -933,7 +933,8 @@ cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args
                         cudaStream_t stream) {
   using C = Cfg<D, NT>;
   auto kernel = decode_int8_kernel<D, NT>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
   if (a.parts == nullptr)
     return launch_pdl(kernel, dim3((unsigned)((long long)a.B * a.Hkv * a.row_blocks)), dim3(kThreads), C::kSmemBytes,

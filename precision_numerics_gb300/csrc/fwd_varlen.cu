@@ -663,7 +663,8 @@ cudaError_t launch_impl(const VarlenProblem& p, const CUtensorMap& mq, const CUt
                         const void* plan, void* o, float* lse, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kernel = varlen_fwd_kernel<D, CAUSAL>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
   const long long capacity = plan_capacity(p.B, p.T, p.H, p.Hkv);
   // One CTA per SM (one fits); without an SM count, one per item.
