@@ -28,10 +28,10 @@
 // the forward over equal lengths.
 //
 // Bound, as in fwd_bf16.cu, by the softmax and its hand-over to the tensor pipe
-// for long sequences (16384 tokens, 16 query and 2 key heads of 128: 732 us, 1500
+// for long sequences (16384 tokens, 16 query and 2 key heads of 128: 730 us, 1500
 // TFLOP/s), and by the ends of the items for short ones (12 sequences of 65 to 2048
-// tokens, 32 and 8 heads of 128: 86 us, 900 TFLOP/s; 0.8 us of softmax a key tile,
-// 0.85 us until the next scores, 2.6 us from an item's last key tile to the next
+// tokens, 32 and 8 heads of 128: 84 us, 925 TFLOP/s; 0.8 us of softmax a key tile,
+// 0.85 us until the next scores, 2.2 us from an item's last key tile to the next
 // item's first).
 #include <math.h>
 
