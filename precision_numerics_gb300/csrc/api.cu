@@ -86,6 +86,36 @@ attn_status check_ptr(const void* p, const char* name, unsigned align) {
   return ATTN_OK;
 }
 
+attn_status PtrCheck::operator()(const void* p, const char* name, unsigned align) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (at == 0 || (at & (align - 1u))) return check_ptr(p, name, align);
+  if (at >= begin_ && at < end_) return ATTN_OK;
+  typedef CUresult (*QueryFn)(unsigned int, CUpointer_attribute*, void**, CUdeviceptr);
+  static const QueryFn query = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &fn, 12000, cudaEnableDefault, &q) ==
+                       cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<QueryFn>(fn)
+               : nullptr;
+  }();
+  if (device_ < 0 && cudaGetDevice(&device_) != cudaSuccess) return check_ptr(p, name, align);
+  unsigned int type = 0;
+  int device = -1;
+  CUdeviceptr begin = 0;
+  size_t bytes = 0;
+  CUpointer_attribute what[4] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                 CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+  void* to[4] = {&type, &device, &begin, &bytes};
+  if (query == nullptr || query(4, what, to, (CUdeviceptr)at) != CUDA_SUCCESS || type != CU_MEMORYTYPE_DEVICE ||
+      device != device_)
+    return check_ptr(p, name, align);  // managed memory, or what is wrong with it
+  begin_ = (uintptr_t)begin;
+  end_ = begin_ + bytes;
+  return ATTN_OK;
+}
+
 namespace {
 
 // One-block kernel that waits on a barrier nobody arrives at, with a limit.

@@ -50,7 +50,7 @@ attn_status check_varlen(int B, int T, int H, int H_kv, int d, VarlenProblem* p)
 
 attn_status check_cache(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
                         const int* block_table, int B, int H_kv, int d, int num_pages, int page_size, int max_blocks,
-                        PagedCache* c) {
+                        PtrCheck& ptr, PagedCache* c) {
   ATTN_CHECK(check_heads(H_kv, H_kv, d));
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
     return fail(ATTN_ERR_UNSUPPORTED, "page_size = %d is not supported (16, 32, 64 or 128)", page_size);
@@ -60,11 +60,11 @@ attn_status check_cache(const void* k_cache, const void* v_cache, const float* k
     return fail(ATTN_ERR_UNSUPPORTED, "num_pages * H_kv * page_size exceeds 2^31 - 1 rows");
   if (max_blocks > (INT_MAX - 4096) / page_size)
     return fail(ATTN_ERR_UNSUPPORTED, "max_blocks * page_size exceeds 2^31 positions");
-  ATTN_CHECK(check_ptr(k_cache, "k_cache"));
-  ATTN_CHECK(check_ptr(v_cache, "v_cache"));
-  ATTN_CHECK(check_ptr(k_scale, "k_scale", 4));
-  ATTN_CHECK(check_ptr(v_scale, "v_scale", 4));
-  ATTN_CHECK(check_ptr(block_table, "block_table", 4));
+  ATTN_CHECK(ptr(k_cache, "k_cache"));
+  ATTN_CHECK(ptr(v_cache, "v_cache"));
+  ATTN_CHECK(ptr(k_scale, "k_scale", 4));
+  ATTN_CHECK(ptr(v_scale, "v_scale", 4));
+  ATTN_CHECK(ptr(block_table, "block_table", 4));
   *c = PagedCache{k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, d, num_pages, page_size, max_blocks};
   return ATTN_OK;
 }
@@ -95,12 +95,13 @@ size_t attn_varlen_plan_bytes(int B, int T, int H, int H_kv) {
 attn_status attn_varlen_plan(const int* cu_seqlens, int B, int T, int H, int H_kv, int causal, void* plan,
                              size_t plan_bytes, cudaStream_t stream) {
   VarlenProblem p;
+  PtrCheck ptr;
   ATTN_CHECK(check_varlen(B, T, H, H_kv, 64, &p));
   p.causal = causal != 0;
   if (plan_bytes < varlen_plan_bytes(B, T, H, H_kv))
     return fail(ATTN_ERR_INVALID_ARG, "plan has %zu bytes, %zu needed", plan_bytes, varlen_plan_bytes(B, T, H, H_kv));
-  ATTN_CHECK(check_ptr(cu_seqlens, "cu_seqlens", 4));
-  ATTN_CHECK(check_ptr(plan, "plan"));
+  ATTN_CHECK(ptr(cu_seqlens, "cu_seqlens", 4));
+  ATTN_CHECK(ptr(plan, "plan"));
   return launched(launch_varlen_plan(p, cu_seqlens, plan, stream), "attn_varlen_plan");
 }
 
@@ -110,6 +111,7 @@ attn_status attn_varlen_fwd(const void* q, const void* k, const void* v, long lo
                             void* o, float* lse, int B, int T, int H, int H_kv, int d, float scale, int causal,
                             cudaStream_t stream) {
   VarlenProblem p;
+  PtrCheck ptr;
   ATTN_CHECK(check_varlen(B, T, H, H_kv, d, &p));
   ATTN_CHECK(check_scale(scale));
   p.causal = causal != 0;
@@ -122,12 +124,12 @@ attn_status attn_varlen_fwd(const void* q, const void* k, const void* v, long lo
   if (plan_bytes < varlen_plan_bytes(B, T, H, H_kv))
     return fail(ATTN_ERR_INVALID_ARG, "plan has %zu bytes, %zu needed", plan_bytes, varlen_plan_bytes(B, T, H, H_kv));
   if (T == 0) return launched(cudaSuccess, "attn_varlen_fwd");
-  ATTN_CHECK(check_ptr(q, "q"));
-  ATTN_CHECK(check_ptr(k, "k"));
-  ATTN_CHECK(check_ptr(v, "v"));
-  ATTN_CHECK(check_ptr(plan, "plan"));
-  ATTN_CHECK(check_ptr(o, "o"));
-  ATTN_CHECK(check_ptr(lse, "lse", 4));
+  ATTN_CHECK(ptr(q, "q"));
+  ATTN_CHECK(ptr(k, "k"));
+  ATTN_CHECK(ptr(v, "v"));
+  ATTN_CHECK(ptr(plan, "plan"));
+  ATTN_CHECK(ptr(o, "o"));
+  ATTN_CHECK(ptr(lse, "lse", 4));
   if (encode_tiled_fn() == nullptr)
     return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
   return launched(launch_varlen_fwd(p, q, k, v, plan, o, lse, strides, stream), "attn_varlen_fwd");
@@ -139,17 +141,18 @@ attn_status attn_cache_append_int8(const void* k, const void* v, long long k_tok
                                    const int* starts, int B, int T, int H_kv, int d, int num_pages, int page_size,
                                    int max_blocks, cudaStream_t stream) {
   PagedCache c;
+  PtrCheck ptr;
   ATTN_CHECK(check_packed(B, T));
   const long long strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
   const char* names[4] = {"k_token_stride", "k_head_stride", "v_token_stride", "v_head_stride"};
   for (int i = 0; i < 4; ++i) ATTN_CHECK(check_stride(strides[i], names[i]));
   ATTN_CHECK(check_cache(k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, d, num_pages, page_size,
-                         max_blocks, &c));
-  ATTN_CHECK(check_ptr(cu_seqlens, "cu_seqlens", 4));
-  ATTN_CHECK(check_ptr(starts, "starts", 4));
+                         max_blocks, ptr, &c));
+  ATTN_CHECK(ptr(cu_seqlens, "cu_seqlens", 4));
+  ATTN_CHECK(ptr(starts, "starts", 4));
   if (T == 0) return launched(cudaSuccess, "attn_cache_append_int8");
-  ATTN_CHECK(check_ptr(k, "k"));
-  ATTN_CHECK(check_ptr(v, "v"));
+  ATTN_CHECK(ptr(k, "k"));
+  ATTN_CHECK(ptr(v, "v"));
   return launched(launch_cache_append_int8(c, k, v, strides, cu_seqlens, starts, T, stream),
                   "attn_cache_append_int8");
 }
@@ -159,17 +162,18 @@ attn_status attn_cache_read_int8(const void* k_cache, const void* v_cache, const
                                  int B, int T, int H_kv, int d, int num_pages, int page_size, int max_blocks,
                                  attn_dtype dt, cudaStream_t stream) {
   PagedCache c;
+  PtrCheck ptr;
   if (dt != ATTN_DTYPE_BF16 && dt != ATTN_DTYPE_FP32)
     return fail(ATTN_ERR_INVALID_ARG, "dt must be ATTN_DTYPE_BF16 or ATTN_DTYPE_FP32 (got %d)", (int)dt);
   ATTN_CHECK(check_packed(B, T));
   ATTN_CHECK(check_cache(k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, d, num_pages, page_size,
-                         max_blocks, &c));
+                         max_blocks, ptr, &c));
   if ((long long)H_kv * d * 16 > INT_MAX) return fail(ATTN_ERR_UNSUPPORTED, "H_kv * d is too large");
-  ATTN_CHECK(check_ptr(cu_seqlens, "cu_seqlens", 4));
-  ATTN_CHECK(check_ptr(starts, "starts", 4));
+  ATTN_CHECK(ptr(cu_seqlens, "cu_seqlens", 4));
+  ATTN_CHECK(ptr(starts, "starts", 4));
   if (T == 0) return launched(cudaSuccess, "attn_cache_read_int8");
-  ATTN_CHECK(check_ptr(k, "k"));
-  ATTN_CHECK(check_ptr(v, "v"));
+  ATTN_CHECK(ptr(k, "k"));
+  ATTN_CHECK(ptr(v, "v"));
   return launched(launch_cache_read_int8(c, cu_seqlens, starts, k, v, T, dt == ATTN_DTYPE_FP32, stream),
                   "attn_cache_read_int8");
 }
@@ -186,22 +190,23 @@ attn_status attn_decode_int8(const void* q, long long q_batch_stride, long long 
                              int B, int n_q, int H, int H_kv, int d, int num_pages, int page_size, int max_blocks,
                              float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   PagedCache c;
+  PtrCheck ptr;
   ATTN_CHECK(check_decode(B, n_q, H, H_kv, d));
   ATTN_CHECK(check_scale(scale));
   ATTN_CHECK(check_stride(q_batch_stride, "q_batch_stride"));
   ATTN_CHECK(check_stride(q_token_stride, "q_token_stride"));
   ATTN_CHECK(check_stride(q_head_stride, "q_head_stride"));
   ATTN_CHECK(check_cache(k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, d, num_pages, page_size,
-                         max_blocks, &c));
-  ATTN_CHECK(check_ptr(q, "q"));
-  ATTN_CHECK(check_ptr(seqlens, "seqlens", 4));
-  ATTN_CHECK(check_ptr(o, "o"));
-  ATTN_CHECK(check_ptr(lse, "lse", 4));
+                         max_blocks, ptr, &c));
+  ATTN_CHECK(ptr(q, "q"));
+  ATTN_CHECK(ptr(seqlens, "seqlens", 4));
+  ATTN_CHECK(ptr(o, "o"));
+  ATTN_CHECK(ptr(lse, "lse", 4));
   const size_t need = decode_workspace_bytes(c, n_q, H);
   if (need > 0) {
     if (workspace_bytes < need)
       return fail(ATTN_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
-    ATTN_CHECK(check_ptr(workspace, "workspace", 256));
+    ATTN_CHECK(ptr(workspace, "workspace", 256));
   }
   if (encode_tiled_fn() == nullptr)
     return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");

@@ -701,6 +701,30 @@ def test_memory_of_calls_on_another_stream(A, monkeypatch):
     A.attn_check_status()
 
 
+def test_host_memory_is_refused(A):
+    """Pinned host memory among device pointers, in every place but the outputs'."""
+    page, d, Hkv = 16, 64, 2
+    tables, pages = scattered([1], 3)
+    c = Cache(pages, Hkv, page, d, tables)
+    rows, q = normal((3, Hkv, d), 1).cuda(), normal((1, 1, 4, d), 2).cuda()
+    host = torch.zeros(pages * Hkv * page * d, dtype=torch.int8).pin_memory().data_ptr()
+    cu, starts, lens = ints([0, 3]), ints([0]), ints([3])
+    o, lse = torch.empty_like(q), torch.empty((1, 1, 4), device="cuda")
+    pointers = [x.data_ptr() for x in (rows, rows)], [x.data_ptr() for x in (*c.gpu, cu, starts)]
+    for i in range(9):
+        p = [*pointers[0], *pointers[1]]
+        p[i] = host
+        with pytest.raises(A.AttnError, match="is not device memory"):
+            A._call("attn_cache_append_int8", *p[:2], Hkv * d, d, Hkv * d, d, *p[2:], 1, 3, Hkv, d, pages, page, 1, 0)
+    for i in range(7):
+        p = [q.data_ptr(), *(x.data_ptr() for x in (*c.gpu, lens))]
+        p[i] = host
+        with pytest.raises(A.AttnError, match="is not device memory"):
+            A._call("attn_decode_int8", p[0], 4 * d, 4 * d, d, *p[1:], o.data_ptr(), lse.data_ptr(), 1, 1, 4, Hkv, d, pages,
+                    page, 1, 0.125, 0, 0, 0)
+    A.attn_check_status()
+
+
 # ------------------------------------------------ sizes, layouts, several calls
 def test_thousands_of_sequences(A):
     """More sequences than any kernel holds at a time, many of them empty."""
