@@ -30,14 +30,15 @@
 // merged through shared memory once at the end of a segment, the tiles of one
 // (sequence, key head, row block) that the CTA has.
 //
-// Where a sequence can be longer than kWholeTiles tiles, the tiles of all
-// segments, one behind the other, are dealt to the CTAs in equal runs, so that
-// ragged lengths and few sequences keep every SM busy alike.  A run that holds a
-// whole segment writes its output; of a segment that runs on into the next
-// CTAs' runs every part leaves (m, l, O / l) in the workspace, two slots a CTA at
-// most, and decode_join_kernel joins them in the order of the CTAs.  Warps and parts
-// are joined as means with weights of at most 1, so that values up to the largest
-// that a scale allows do not overflow on the way.
+// Short sequences have a CTA for every segment.  Where the segments are fewer than the
+// CTAs that the SMs hold, and not too long, a cluster of CTAs shares one and joins its
+// parts through their shared memory.  Else the tiles of all segments, one behind the
+// other, are dealt to the CTAs in equal runs, so that ragged lengths and few sequences
+// keep every SM busy alike.  A run that holds a whole segment writes its output; of a
+// segment that runs on into the next CTAs' runs every part leaves (m, l, O / l) in the
+// workspace, two slots a CTA at most, and decode_join_kernel joins them in the order of
+// the CTAs.  Warps and parts are joined as means with weights of at most 1, so that
+// values up to the largest that a scale allows do not overflow on the way.
 //
 // Measured (d = 128, 8 key heads, pages of 64): 64 sequences of 500 to 16000
 // positions with 4 query rows a key head 102-104 us (5.9 TB/s, 87% of a copy's
@@ -67,6 +68,9 @@ constexpr int kLeastRun = 4;     // tiles a CTA takes at least: one a warp
 // as long as so many tiles: runs are measured in tiles plus this for each segment
 // that begins in them.
 constexpr int kSegmentCost = 8;
+constexpr int kMaxCluster = 8;  // CTAs that can share a segment through their shared memory
+constexpr int kClusterTiles = 16;  // tiles a CTA that the join is worth
+constexpr int kLoneTiles = 8;      // sequences up to this long are not shared by a cluster
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_decode, code); }
 
@@ -157,6 +161,31 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t sel) {
   return r;
 }
 
+// The same place in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer(uint32_t saddr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// All threads of the cluster; what was written before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Byte offset of 16-byte unit u of row r, as TMA's 128-byte (D = 128) or 64-byte
 // (D = 64) swizzle places it: eight consecutive rows' units u cover all banks.
 template <int D>
@@ -195,6 +224,7 @@ struct Args {
   float* parts;
   Chain* chains;
   int by_segment;
+  unsigned cluster;  // without split mode: CTAs that share a segment
 };
 
 // A part in the workspace: O [rows][D] divided by l, m [rows], l [rows], FP32.
@@ -343,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   int len_first = 1;
   long long per = 0;  // cost of a run
   if (a.parts == nullptr) {
-    const int x = blockIdx.x;
+    unsigned x = blockIdx.x, rank = 0;
+    if (a.cluster > 1) rank = x % a.cluster, x /= a.cluster;
     sg.rb = x % a.row_blocks;
     sg.h = (x / a.row_blocks) % a.Hkv;
     sg.b = x / a.row_blocks / a.Hkv;
@@ -351,6 +382,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.len_next = 0;
     sg.ta = 0;
     sg.tb = tiles_of(sg.len);
+    if (a.cluster > 1) {  // its share of the tiles (products below 2^26 * 8)
+      sg.ta = sg.tb * rank / a.cluster;
+      sg.tb = sg.tb * (rank + 1) / a.cluster;
+    }
     sg.left = 0;
   } else {
     // All segments' cost, and the sequence in which this CTA's run begins.  The
@@ -723,9 +758,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
 
     // ------------------------------------------------------------------ merge
-    const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len);
+    // In a cluster the part stays in shared memory, where the rings were.
+    const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len) && a.cluster <= 1;
     float* part = nullptr;
-    if (!whole) part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats(D, kRows);
+    if (a.cluster > 1)
+      part = reinterpret_cast<float*>(smem);
+    else if (!whole) part = a.parts + (size_t)(2 * blockIdx.x + (sg.ta == 0)) * part_floats(D, kRows);
     if (a.parts != nullptr && sg.ta == 0 && threadIdx.x == 0 && (a.by_segment || !whole)) {
       const int hr = sg.h * a.row_blocks + sg.rb;
       const long long slot = a.by_segment ? (long long)sg.b * a.Hkv * a.row_blocks + hr : blockIdx.x;
@@ -808,6 +846,43 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     last_segment = !sg.next(a);
     if (kAhead && !last_segment) load_q();
     if (!last_segment) __syncthreads();  // before the next segment's Q
+  }
+  if (a.cluster > 1) {
+    // Every CTA of the cluster joins the parts of its share of the rows and columns.
+    const unsigned rank = blockIdx.x % a.cluster;
+    const uint32_t mine = smem_u32(smem);
+    cluster_sync();
+    for (int x = rank * kThreads + threadIdx.x; x < kRows * (D / 4); x += a.cluster * kThreads) {
+      const int r = x / (D / 4), col = x % (D / 4) * 4, rr = sg.rb * kRows + r;
+      float m[kMaxCluster], l[kMaxCluster], M = -INFINITY, L = 0.f;
+      float4 y[kMaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (unsigned w = 0; w < kMaxCluster; ++w) {
+        m[w] = -INFINITY, l[w] = 0.f, y[w] = v;
+        if (w >= a.cluster) continue;
+        const uint32_t at = peer(mine, w);
+        m[w] = load_peer(at + 4 * (kRows * D + r));
+        l[w] = load_peer(at + 4 * (kRows * D + kRows + r));
+        y[w] = load_peer4(at + 4 * (r * D + col));
+      }
+#pragma unroll
+      for (int w = 0; w < kMaxCluster; ++w) M = fmaxf(M, m[w]);
+      const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kMaxCluster; ++w) L += l[w] *= ex2(m[w] - M_use);
+      const float inv = inverse(L);
+#pragma unroll
+      for (int w = 0; w < kMaxCluster; ++w) {
+        const float f = l[w] * inv;
+        v.x += f * y[w].x, v.y += f * y[w].y, v.z += f * y[w].z, v.w += f * y[w].w;
+      }
+      if (rr < rows_total) {
+        const size_t row = out_row(a, sg.b, sg.h, rr);
+        *reinterpret_cast<uint2*>(a.o + row * D + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        if (col == 0) a.lse[row] = lse_of(M, L);
+      }
+    }
+    cluster_sync();  // nobody leaves while its part is read
   }
   if (!ok) {
     if (lane == 0) set_fail(ATTN_ERR_TIMEOUT);
@@ -936,19 +1011,18 @@ cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
+  const long long segments = (long long)a.B * a.Hkv * a.row_blocks;
   if (a.parts == nullptr)
-    return launch_pdl(kernel, dim3((unsigned)((long long)a.B * a.Hkv * a.row_blocks)), dim3(kThreads), C::kSmemBytes,
-                      stream, mk, mv, a);
+    return launch_pdl_cluster(kernel, dim3((unsigned)(segments * a.cluster)), dim3(kThreads), C::kSmemBytes, stream,
+                      a.cluster, mk, mv, a);
   err = launch_pdl(kernel, dim3(runs), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
   if (err != cudaSuccess) return err;
-  const long long segments = (long long)a.B * a.Hkv * a.row_blocks;
   const int per_row = segments * 4 <= runs ? kJoinWarps : 1;
   const int rows = std::min(C::kRows, a.n_q * a.G);
   const dim3 grid(a.by_segment ? (unsigned)segments : runs, ceil_div(rows * per_row, kJoinWarps));
   return launch_pdl(decode_join_kernel<D>, grid, dim3(32 * kJoinWarps), 0, stream, a, C::kRows, per_row);
 }
 
-bool splits(const PagedCache& c) { return (long long)c.max_blocks * c.page > (long long)kWholeTiles * kTile; }
 
 // Blocks of 8 rows a pass takes, and passes: as few passes as possible, then as
 // few blocks.
@@ -956,6 +1030,70 @@ int row_passes(int rows) { return ceil_div(rows, 32); }
 int row_tiles(int rows) { return ceil_div(rows, 8 * row_passes(rows)); }
 
 }  // namespace
+
+// Clusters of `size` CTAs that the device holds at a time (the GPCs' SMs do not divide by
+// every size).
+template <int D, int NT>
+int clusters_held(int size) {
+  using C = Cfg<D, NT>;
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];  // and one
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kDevices && (n = known[dev][size].load(std::memory_order_relaxed)) > 0) return n - 1;
+  auto kernel = decode_int8_kernel<D, NT>;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)size, 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (allow_smem(kernel, C::kSmemBytes, allowed) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < kDevices) known[dev][size].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+int clusters_held(int d, int nt, int size) {
+#define ATTN_DECODE_CASE(DD, TT) \
+  if (d == DD && nt == TT) return clusters_held<DD, TT>(size);
+  ATTN_DECODE_CASE(64, 1)
+  ATTN_DECODE_CASE(64, 2)
+  ATTN_DECODE_CASE(64, 3)
+  ATTN_DECODE_CASE(64, 4)
+  ATTN_DECODE_CASE(128, 1)
+  ATTN_DECODE_CASE(128, 2)
+  ATTN_DECODE_CASE(128, 3)
+  ATTN_DECODE_CASE(128, 4)
+#undef ATTN_DECODE_CASE
+  return 0;
+}
+
+bool splits(const PagedCache& c) { return (long long)c.max_blocks * c.page > (long long)kWholeTiles * kTile; }
+
+// CTAs that share a segment through their shared memory, or 0 where its tiles are dealt
+// in runs instead.  The cluster saves the join (25 sequences of 1024 to 1850 positions, 4
+// key heads of 128: 16.5 -> 13.4 us; one of 2000, 8 heads: 8.4 -> 7.3), the runs use all CTAs
+// and even out ragged lengths.  By the longest sequences that the table has room for: a
+// share against the run if the lengths were half of that.
+int cluster_size(const PagedCache& c, int n_q, int H) {
+  const int rows = n_q * (H / c.Hkv), nt = row_tiles(rows);
+  const long long tiles = (long long)c.max_blocks * c.page / kTile;
+  const long long segments = (long long)c.B * c.Hkv * row_passes(rows), runs = decode_runs(c.d, nt);
+  if (tiles <= kLoneTiles) return 0;  // (250 positions 5.9 us, 6.5 in clusters; 500 7.8 and 5.9)
+  for (long long size = std::min({runs / segments, (long long)kMaxCluster, tiles / 4}); size >= 2; --size) {
+    if (tiles / size - tiles * segments / (2 * runs) > kClusterTiles) return 0;
+    if (clusters_held(c.d, nt, (int)size) >= segments) return (int)size;
+  }
+  return 0;
+}
 
 size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H) {
   if (!splits(c)) return 0;
@@ -989,7 +1127,9 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   const int nt = row_tiles(n_q * a.G);
   a.by_segment = 0;
   unsigned runs = 0;
-  if (splits(c)) {
+  a.cluster = cluster_size(c, n_q, H);
+  if (a.cluster == 0 && !splits(c)) a.cluster = 1;
+  if (a.cluster == 0) {
     runs = decode_runs(c.d, nt);
     a.by_segment = (long long)a.B * a.Hkv * a.row_blocks <= runs;
     a.parts = static_cast<float*>(workspace);

@@ -429,6 +429,26 @@ def test_decode_short(A, page, d):
         check_decode(c, q, lens, 1 / math.sqrt(d), o, lse)
 
 
+@pytest.mark.parametrize("d,G,n_q", [(64, 1, 1), (64, 4, 4), (128, 2, 1), (128, 5, 4), (128, 8, 4), (64, 20, 2)])
+@pytest.mark.parametrize("B", [1, 19, 23, 31, 47, 70])
+def test_decode_shared_by_clusters(A, B, d, G, n_q):
+    """Segments shared by 2 to 8 CTAs each, as their number allows; sequences of fewer tiles than
+    CTAs, and empty ones; the same bits twice."""
+    Hkv, page, most = 2, 32, 700
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, most + 1, (B,), generator=g).tolist()
+    lens[0] = most
+    lens[1:6] = [0, 1, 33, 64, 250][:B - 1]
+    tables, pages = scattered([-(-n // page) for n in lens], 18)
+    c = Cache(pages, Hkv, page, d, tables)
+    q = normal((B, n_q, Hkv * G, d), 1)
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens))
+    again, lse_again = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens))
+    A.attn_check_status()
+    assert torch.equal(o, again) and torch.equal(lse, lse_again)
+    check_decode(c, q, lens, 1 / math.sqrt(d), o, lse)
+
+
 @pytest.mark.parametrize("most,page", [(2000, 16), (9000, 128)])
 def test_decode_ragged_batch(A, most, page):
     """More sequences than a CTA scans at a time, among them empty ones; runs of tiles that begin and
