@@ -64,6 +64,11 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;   // positions per tile
 constexpr int kWholeTiles = 16;  // sequences up to this long are not split
 constexpr int kLeastRun = 4;     // tiles a CTA takes at least: one a warp
+// Parts that the warps of a row's join have in flight together; no segment has more
+// (one sequence of 114589 positions, 1 key head of 64 and 6 rows: 14.8 us; 21.2 in runs of 4
+// tiles, 600 parts, by half as many warps).
+constexpr int kJoinBatch = 8, kJoinShared = 16;
+constexpr int kPartsAtOnce = kJoinBatch * kJoinShared;
 // A segment's start and end (its Q rows, the merge of the warps, its output) take
 // as long as so many tiles: runs are measured in tiles plus this for each segment
 // that begins in them.
@@ -391,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     // All segments' cost, and the sequence in which this CTA's run begins.  The
     // first kThreads sequences are read and scanned once.
     long long* s_warp = reinterpret_cast<long long*>(s_merge);
+    int* s_longest = reinterpret_cast<int*>(s_l);
     const long long copies = (long long)a.Hkv * a.row_blocks;
     auto len_at = [&](int b) { return checked(a, read_length(a, b)); };
     const int len_mine = read_length(a, threadIdx.x);
@@ -399,14 +405,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     long long total, sum;
     long long ahead = scan_before(cost_of(len), s_warp, total);
     const long long first = total;
+    int longest = len;
     for (int b0 = kThreads; b0 < a.B; b0 += kThreads) {
-      scan_before(cost_of(len_at(b0 + threadIdx.x)), s_warp, sum);
+      const int more = len_at(b0 + threadIdx.x);
+      longest = max(longest, more);
+      scan_before(cost_of(more), s_warp, sum);
       total += sum;
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) s_longest[warp] = longest;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) longest = max(longest, s_longest[w]);
     total *= copies;
     // One run for every CTA that the SMs hold at a time: more and shorter runs cost
     // more to start than they even out (ragged batch 106 us, with two to a slot 110).
-    per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)kLeastRun);
+    // Runs are not so short that a segment has more parts than a join takes at once.
+    per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)max(kLeastRun, tiles_of(longest) / kPartsAtOnce));
     const long long begin = per * blockIdx.x;
     int4* s_start = reinterpret_cast<int4*>(s_m);
     if (threadIdx.x == 0) s_start[0].x = -1;
@@ -892,12 +907,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 }
 
 // Joins the parts of the segments that begin in one CTA's run and end in
-// another's: grid (chains, groups of rows).  `per_row` warps (1 or kJoinWarps) share
-// a row and take every per_row-th part: one where there are many chains of a few
-// parts, all where few chains have many.  The order of the sums is that of the parts.
-constexpr int kJoinWarps = 8;
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args a, int rows, int per_row) {
+// another's: grid (chains, groups of rows).  Either a warp takes a row (SHARED false, where
+// there are many chains of a few parts), or all of a CTA's warps share one and take its
+// parts in turn (few chains of many).  The order of the sums is that of the parts.
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_kernel(const Args a, int rows) {
+  constexpr int kJoinWarps = SHARED ? kJoinShared : 8, per_row = SHARED ? kJoinWarps : 1;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
@@ -911,7 +926,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
   // l, at most 2^15 a key of less than 2^31, becomes a weight below 1.
   constexpr float kShare = 0x1p-46f;
   // kBatch parts at a time, all their loads in flight together.
-  constexpr int kBatch = 8;
+  constexpr int kBatch = kJoinBatch;
   float M = -INFINITY, L = 0.f, o[D / 32] = {};
   for (int i0 = warp % per_row; i0 < n; i0 += kBatch * per_row) {
     float m[kBatch], l[kBatch], x[kBatch][D / 32];  // l times kShare
@@ -952,7 +967,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Args
       for (int e = 0; e < D / 32; ++e) o[e] += f * x[k][e];
     }
   }
-  if (per_row > 1) {  // the same for all warps
+  if constexpr (SHARED) {
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) s_o[warp][lane * (D / 32) + e] = o[e];
     if (lane == 0) s_m[warp] = M, s_l[warp] = L;
@@ -1017,10 +1032,12 @@ cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args
                       a.cluster, mk, mv, a);
   err = launch_pdl(kernel, dim3(runs), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
   if (err != cudaSuccess) return err;
-  const int per_row = segments * 4 <= runs ? kJoinWarps : 1;
+  const bool shared = segments * 4 <= runs;
   const int rows = std::min(C::kRows, a.n_q * a.G);
-  const dim3 grid(a.by_segment ? (unsigned)segments : runs, ceil_div(rows * per_row, kJoinWarps));
-  return launch_pdl(decode_join_kernel<D>, grid, dim3(32 * kJoinWarps), 0, stream, a, C::kRows, per_row);
+  const unsigned chains = a.by_segment ? (unsigned)segments : runs;
+  if (shared)
+    return launch_pdl(decode_join_kernel<D, true>, dim3(chains, rows), dim3(32 * kJoinShared), 0, stream, a, C::kRows);
+  return launch_pdl(decode_join_kernel<D, false>, dim3(chains, ceil_div(rows, 8)), dim3(256), 0, stream, a, C::kRows);
 }
 
 
