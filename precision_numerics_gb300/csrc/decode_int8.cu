@@ -64,7 +64,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;   // positions per tile
 constexpr int kWholeTiles = 16;  // sequences up to this long are not split
 constexpr int kLeastRun = 4;     // tiles a CTA takes at least: one a warp
-// Parts that the warps of a row's join have in flight together; no segment has more
+// Parts that the warps of a row's join have in flight together; a segment has hardly more
 // (one sequence of 114589 positions, 1 key head of 64 and 6 rows: 14.8 us; 21.2 in runs of 4
 // tiles, 600 parts, by half as many warps).
 constexpr int kJoinBatch = 8, kJoinShared = 16;
@@ -83,9 +83,10 @@ __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status
 // More warps are worth more than deeper rings (d = 64, 8 rows: 4 CTAs with 2 stages
 // 56.7 us on a ragged batch, 3 with 4 stages 62.6, 2 with 5 stages 75.8);
 // 12 rows over 64 sequences: 3 CTAs with 3 stages 81 us, 2 with 5 stages 96; d = 128,
-// 12 rows: 3 CTAs with 2 stages 114 us, 2 with 3 stages 121.
+// 12 rows: 3 CTAs with 2 stages 114 us, 2 with 3 stages 121; d = 64, 20 rows: 3 CTAs
+// with 3 stages 99 us, 2 with 4 stages 111 (one sequence and key head 17.3 and 15.8).
 constexpr int ctas_per_sm(int d, int nt) {
-  if (d == 64) return nt == 1 ? 4 : nt == 2 ? 3 : 2;
+  if (d == 64) return nt == 1 ? 4 : nt <= 3 ? 3 : 2;
   return nt <= 2 ? 3 : 2;
 }
 
@@ -94,7 +95,7 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kCtas = ctas_per_sm(D, NT);
-  static constexpr int kStages = D == 64 ? (NT == 1 ? 2 : NT == 2 ? 3 : 4) : 2;
+  static constexpr int kStages = D == 64 ? (NT == 1 ? 2 : NT == 4 ? 4 : 3) : 2;
   static constexpr int kHalfBytes = kTile * D;          // K or V of a tile
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
