@@ -605,15 +605,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
     __syncthreads();
     // The scores and accumulators a lane holds are those of rows 8 n + 2 c + {0, 1}.
-    int my_last[NT][2];   // last visible position of those (-1: none)
-    float f_row[NT][2];   // factor of their scores, in base 2
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        f_row[n][i] = s_f[8 * n + 2 * c + i];
-        my_last[n][i] = s_last[8 * n + 2 * c + i];
-      }
+    // Factor of the scores of those, in base 2, and their last visible position (-1: none).
+    auto f_row = [&](int n, int i) { return s_f[8 * n + 2 * c + i]; };
+    auto my_last = [&](int n, int i) { return s_last[8 * n + 2 * c + i]; };
     const int tiles = sg.count(warp);
 
     // ------------------------------------------------------------------ tiles
@@ -684,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[h][n][x] *= f_row[n][x & 1] * ksc[h];
+          for (int x = 0; x < 4; ++x) s[h][n][x] *= f_row(n, x & 1) * ksc[h];
       if (hide) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -692,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if (pos0 + h * 16 + (x >> 1) * 8 + g > my_last[n][x & 1] || !((flags >> h) & 1u)) s[h][n][x] = -INFINITY;
+              if (pos0 + h * 16 + (x >> 1) * 8 + g > my_last(n, x & 1) || !((flags >> h) & 1u)) s[h][n][x] = -INFINITY;
         if (!(flags & 1u)) vsc[0] = 0.f;
         if (!(flags & 2u)) vsc[1] = 0.f;
       }
