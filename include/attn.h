@@ -330,7 +330,8 @@ ATTN_API attn_status attn_varlen_plan(const int* cu_seqlens, int B, int T, int H
  * Rows of o and lse that belong to no sequence are left as they were.  What lies
  * in other sequences' rows (a NaN, say) does not reach a sequence; a NaN or an
  * infinity in v at token j of a sequence may reach the rows of earlier tokens in
- * j's block of 128 keys, although the causal mask hides it from them.
+ * j's block of 128 keys, and of up to 127 tokens before that block, although the
+ * causal mask hides it from them.
  */
 ATTN_API attn_status attn_varlen_fwd(const void* q, const void* k, const void* v,
                                      long long q_token_stride, long long q_head_stride,

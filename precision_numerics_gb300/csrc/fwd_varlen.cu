@@ -27,6 +27,9 @@
 // items, masks at both ends, row-wise output) takes no register or instruction from
 // the forward over equal lengths.
 //
+// Where there are fewer items than SMs the two tiles of a CTA share the keys of one
+// instead (split items, below).
+//
 // Bound, as in fwd_bf16.cu, by the softmax and its hand-over to the tensor pipe
 // for long sequences (16384 tokens, 16 query and 2 key heads of 128: 730 us, 1500
 // TFLOP/s), and by the ends of the items for short ones (12 sequences of 65 to 2048
@@ -82,7 +85,7 @@ constexpr int kPlanBins = 1024;
 // without a partner (ungrouped heads of 200 to 1024 tokens: 20.5 -> 19.8 us).
 __global__ void __launch_bounds__(kPlanThreads)
     varlen_plan_kernel(const int* __restrict__ cu, int* __restrict__ plan, int B, int T, int G, int Hkv, int tq,
-                       int causal, int capacity, int sms) {
+                       int causal, int capacity, int sms, int split) {
   __shared__ int s_pairs;
   __shared__ int s_count[kPlanBins], s_warp[32], s_max;
   griddep_launch_dependents();
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (pairs > 0) atomicAdd(&s_pairs, pairs);
   __syncthreads();
   const int most = s_max;
-  const int tiles_per_item = (long long)s_pairs * Hkv * (causal ? 1 : 2) <= sms ? 1 : 2;
+  const int tiles_per_item = split || (long long)s_pairs * Hkv * (causal ? 1 : 2) <= sms ? 1 : 2;
   const int per_item = tiles_per_item * tq;  // tokens
   auto each = [&](auto&& put) {
     for (int b = warp; b < B; b += kPlanThreads / 32) {
@@ -165,10 +168,12 @@ struct Cfg {
   static constexpr int kOffStage = kOffV + kStages * kTileBytes;
   static constexpr int kOffBar = kOffStage + 8 * 32 * 128;
   // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S],
-  // s_full[2], p_full[2], o_done[2], mma_final, alpha[2][4]
-  static constexpr int kNumBars = 2 + 4 * kStages + 15;
+  // s_full[2], p_full[2], o_done[2], mma_final, alpha[2][4], stat, o_read
+  static constexpr int kNumBars = 2 + 4 * kStages + 17;
   static constexpr int kOffAlpha = kOffBar + kNumBars * 8 + 16;  // FP32 [2][128]
-  static constexpr int kSmemBytes = kOffAlpha + 2 * 128 * 4;
+  static constexpr int kOffSum = kOffAlpha + 2 * 128 * 4;  // FP32 [2][128]
+  static constexpr int kSmemBytes = kOffSum + 2 * 128 * 4;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
   static constexpr uint32_t kTmemCols = 512;
   static __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
   static __device__ __forceinline__ uint32_t col_o(int t) { return 256u + D * t; }
@@ -193,16 +198,22 @@ __device__ __forceinline__ int item_of(int r, int total) {
   return idx < total ? (int)idx : -1;
 }
 
-// q0: first token (in the sequence) of tile 0; n: key tiles of the two tiles.
+// q0: first token (in the sequence) of tile 0; n: key tiles of the two tiles, nmax: of the
+// item.  In a split item both tiles are the same queries; tile 0 takes the key tiles 0,
+// 2, ..., tile 1 the others, and their results are joined.  That halves the chain of
+// an item (one prompt of 2048 tokens, 8 heads of 128: 28.9 -> 20.2 us, 4096 tokens of 4 heads
+// 49.6 -> 33.8); the join takes as long as a key tile, so short items are not split.
+constexpr int kSplitTiles = 4;
 struct Item {
   int first, len, head, q0, n[2], nmax;
+  bool split;
 };
 // The plan's words of item L.  They take 0.6 us to come, so roles that would wait for
 // them ask ahead (ragged prompts with 7 items a CTA: 87.1 -> 85.6 us).
 __device__ __forceinline__ int4 item_words(const int* plan, int L, int Hkv) {
   return L >= 0 ? *(reinterpret_cast<const int4*>(plan + kPlanHeader) + L / Hkv) : make_int4(0, 0, 0, 0);
 }
-template <bool CAUSAL>
+template <bool CAUSAL, bool SPLIT>
 __device__ __forceinline__ Item make_item(const int4& p, int L, int Hkv, int tq) {
   Item it;
   it.first = p.x;
@@ -216,12 +227,14 @@ __device__ __forceinline__ Item make_item(const int4& p, int L, int Hkv, int tq)
     it.n[t] = q >= p.w ? 0 : (keys + kBlockN - 1) / kBlockN;
   }
   it.nmax = max(it.n[0], it.n[1]);
+  it.split = SPLIT && it.n[1] == 0 && it.nmax >= kSplitTiles;
+  if (it.split) it.n[0] = (it.nmax + 1) / 2, it.n[1] = it.nmax / 2;
   return it;
 }
 // Rows of key tile j that belong to the sequence.
 __device__ __forceinline__ int tile_keys(const Item& it, int j) { return min(kBlockN, it.len - j * kBlockN); }
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const int* plan,
@@ -245,8 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_odone = bar_pfull + 2;
   uint64_t* bar_final = bar_odone + 2;
   uint64_t* bar_alpha = bar_final + 1;
+  uint64_t* bar_stat = bar_alpha + 8;
+  uint64_t* bar_oread = bar_stat + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   float* s_alpha = reinterpret_cast<float*>(smem + C::kOffAlpha);
+  float* s_sum = reinterpret_cast<float*>(smem + C::kOffSum);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   griddep_launch_dependents();
@@ -267,6 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_odone[t], 1);
     }
     mbar_init(bar_final, 1);
+    mbar_init(bar_stat, 256);   // both softmax warpgroups
+    mbar_init(bar_oread, 256);
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -309,14 +327,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; ok; ++r) {
         const int L = item_of(r, total);
         if (L < 0) break;
-        const Item it = make_item<CAUSAL>(item_words(plan, L, Hkv), L, Hkv, tq);
+        const Item it = make_item<CAUSAL, SPLIT>(item_words(plan, L, Hkv), L, Hkv, tq);
         // The Q slots are free once the previous item's last S products have run.
         if (items > 0 && !mbar_wait(bar_qempty, (items - 1) & 1)) { ok = false; break; }
         mbar_arrive_expect_tx(bar_q, 2 * C::kChunks * q_bytes);
         for (int t = 0; t < 2; ++t)
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_3d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tmQ, bar_q, c * 64, it.head * G,
-                        it.first + it.q0 + t * tq);
+                        it.first + it.q0 + (SPLIT && it.split ? 0 : t * tq));
         ++items;
         for (int j = 0; j < it.nmax; ++j, ++g) {
           const int st = g % C::kStages;
@@ -366,18 +384,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < kBlockN / 16; ++kk)
           mma_ts_elect(d, a + kk * 8, sdesc_add(b0, kk * 2048), idesc_pv, (acc || kk > 0) ? 1u : 0u);
       };
+      // Rows past the sequence's end become zero while the softmax works on the tile's
+      // scores.  Rows are 128 bytes in every 64-column chunk; the swizzle moves units within
+      // a row only.
+      auto zero_behind = [&](const Item& it, int j, int st) {
+        const int keys = tile_keys(it, j);
+        if (keys >= kBlockN) return;
+        for (int c = 0; c < C::kChunks; ++c)
+          for (int i = keys * 8 + lane; i < kBlockN * 8; i += 32)
+            st_shared_v4(smem_u32(sV + st * C::kTileBytes + c * C::kChunkBytes + i * 16), 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
       bool ok = true;
       int g = 0, items = 0;
       int pc[2] = {0, 0};   // P tiles consumed per query tile (p_full phases)
       int L = item_of(0, total);
       int4 words = item_words(plan, L, Hkv);
       for (int r = 1; ok && L >= 0; ++r) {
-        const Item it = make_item<CAUSAL>(words, L, Hkv, tq);
+        const Item it = make_item<CAUSAL, SPLIT>(words, L, Hkv, tq);
         L = item_of(r, total);
         words = item_words(plan, L, Hkv);
         // S_t(0).  S_t's columns are free: the previous item's P_t V, issued
         // earlier on this thread, reads P_t before these products run.
         ok = warp_wait(bar_q, items & 1);
+        if (SPLIT && it.split) {
+          // Key tile e is tile t = e & 1's; the products of one tile run while the other's
+          // softmax works.
+          ++items;
+          auto s_of = [&](int e) {
+            const int ge = g + e;
+            if (!warp_wait(&bar_kfull[ge % C::kStages], (ge / C::kStages) & 1)) return false;
+            tc_fence_after();
+            issue_s(e & 1, ge % C::kStages);
+            mma_commit_elect(&bar_sfull[e & 1]);
+            mma_commit_elect(&bar_kempty[ge % C::kStages]);
+            if (e + 1 == it.nmax) mma_commit_elect(bar_qempty);
+            return true;
+          };
+          ok = ok && s_of(0) && s_of(1);
+          for (int e = 0; e < it.nmax && ok; ++e) {
+            const int t = e & 1, st = (g + e) % C::kStages;
+            ok = warp_wait(&bar_vfull[st], ((g + e) / C::kStages) & 1);
+            if (!ok) break;
+            zero_behind(it, e, st);
+            ok = warp_wait(&bar_pfull[t], (pc[t] + (e >> 1)) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, st, e >= 2);
+            mma_commit_elect(&bar_vempty[st]);
+            if (e + 2 < it.nmax)
+              ok = s_of(e + 2);
+            else
+              mma_commit_elect(&bar_odone[t]);
+          }
+          g += it.nmax;
+          pc[0] += it.n[0];
+          pc[1] += it.n[1];
+          continue;
+        }
         if (ok) ok = warp_wait(&bar_kfull[g % C::kStages], (g / C::kStages) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -395,16 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st1 = (gj + 1) % C::kStages;
           const bool has_next = j + 1 < it.nmax;
           if (!warp_wait(&bar_vfull[st], (gj / C::kStages) & 1)) { ok = false; break; }
-          // Rows past the sequence's end become zero while the softmax works on
-          // the tile's scores.  Rows are 128 bytes in every 64-column chunk; the
-          // swizzle moves units within a row only.
-          if (const int keys = tile_keys(it, j); keys < kBlockN) {
-            for (int c = 0; c < C::kChunks; ++c)
-              for (int i = keys * 8 + lane; i < kBlockN * 8; i += 32)
-                st_shared_v4(smem_u32(sV + st * C::kTileBytes + c * C::kChunkBytes + i * 16), 0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          zero_behind(it, j, st);
           if (has_next && !warp_wait(&bar_kfull[st1], ((gj + 1) / C::kStages) & 1)) {
             ok = false;
             break;
@@ -453,8 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int rr = 0; ok; ++rr) {
       const int L = item_of(rr, total);
       if (L < 0) break;
-      const Item it = make_item<CAUSAL>(item_words(plan, L, Hkv), L, Hkv, tq);
-      for (int j = 0; j < it.nmax && ok; ++j) {
+      const Item it = make_item<CAUSAL, SPLIT>(item_words(plan, L, Hkv), L, Hkv, tq);
+      const int steps = SPLIT ? max(it.n[0], it.n[1]) : it.nmax;
+      for (int j = 0; j < steps && ok; ++j) {
         for (int t = 0; t < 2; ++t) {
           if (j >= it.n[t]) continue;
           // Only the softmax warp that owns the same 32 TMEM lanes is waited for.
@@ -504,12 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = !abort_all;
     int sc = 0;  // S_t tiles consumed so far (s_full phases)
     int oc = 0;  // items whose O_t was completed so far (o_done phases)
+    int splits = 0;  // split items so far (stat and o_read phases)
     int L = item_of(0, total);
     int4 words = item_words(plan, L, Hkv);
     for (int round = 1; ok && L >= 0; ++round) {
-      const Item it = make_item<CAUSAL>(words, L, Hkv, tq);
+      const Item it = make_item<CAUSAL, SPLIT>(words, L, Hkv, tq);
       const int n = it.n[t];
-      const int q_first = it.q0 + t * tq;
+      const int q_first = it.q0 + (SPLIT && it.split ? 0 : t * tq);
       const int tok = q_first + (row_used ? row_tok : 0);  // token within the sequence
       const int limit = CAUSAL ? min(tok + 1, it.len) : it.len;
       float m_run = -INFINITY, l_run = 0.f;
@@ -524,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) reg_fence(s[c]);
 
-        const int kv0 = j * kBlockN;
+        const int kv0 = (SPLIT && it.split ? 2 * j + t : j) * kBlockN;
         if (kv0 + kBlockN > it.len || (CAUSAL && kv0 + kBlockN - 1 > q_first)) {
           const int lim = limit - kv0;
 #pragma unroll
@@ -589,24 +647,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++oc;
       tc_fence_after();
-      const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
-      const uint64_t il2 = f2_pack(inv_l, inv_l);
       const bool have = row_used && tok < it.len;
       const size_t row_at = (size_t)(it.first + tok) * H + it.head * G + row_head;
       const uint32_t stage = smem_u32(smem + C::kOffStage) + (warp - 4) * 32 * 128;
-#pragma unroll
-      for (int c = 0; c < C::kChunks; ++c) {
+      // 64 columns to memory; get(h, o) reads 32 of them, scaled, in pairs.
+      auto write_chunk = [&](int c, auto&& get) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 64 + h * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
+          uint64_t o2[16];
+          get(h, o2);
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float lo, hi;
-            f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il2), lo, hi);
+            f2_unpack(o2[i], lo, hi);
             pk[i] = pack_bf16x2(lo, hi);
           }
 #pragma unroll
@@ -627,8 +681,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+      };
+      auto load = [&](uint32_t from, uint32_t (&o)[32]) {
+        tmem_ld32(from, o);
+        tmem_wait_ld();
+        reg_fence(o);
+      };
+      if (!SPLIT || !it.split) {
+        const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+        const uint64_t il2 = f2_pack(inv_l, inv_l);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          write_chunk(c, [&](int h, uint64_t (&o2)[16]) {
+            uint32_t o[32];
+            load(tO + c * 64 + h * 32, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o2[i] = mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), il2);
+          });
+        if (have) lse[row_at] = m_run * scale + logf(l_run);
+      } else {
+        // Both halves of a row are in the same TMEM lane: with the other's maximum and
+        // sum, every warpgroup joins 64 columns (d = 64: the first one does).
+        s_alpha[t * 128 + r] = m_run;  // the correction has read the last factor: O_t is complete
+        s_sum[t * 128 + r] = l_run;
+        tc_fence_before();
+        mbar_arrive(bar_stat);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_stat, splits & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const float m_other = s_alpha[(t ^ 1) * 128 + r], l_other = s_sum[(t ^ 1) * 128 + r];
+        const float m = fmaxf(m_run, m_other), m_use = m == -INFINITY ? 0.f : m;
+        const float mine = ex2((m_run - m_use) * scale_log2), others = ex2((m_other - m_use) * scale_log2);
+        const float l = l_run * mine + l_other * others;
+        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        const float f0 = mine * inv_l, f1 = others * inv_l;
+        const uint64_t f02 = f2_pack(f0, f0), f12 = f2_pack(f1, f1);
+        const uint32_t tOther = tmem + lane_off + C::col_o(t ^ 1);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          if (c == t)
+            write_chunk(c, [&](int h, uint64_t (&o2)[16]) {
+              uint32_t o[32];
+              load(tO + c * 64 + h * 32, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                o2[i] = mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), f02);
+              load(tOther + c * 64 + h * 32, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                o2[i] = fma2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), f12, o2[i]);
+            });
+        if (have && t == 0) lse[row_at] = m * scale + logf(l);
+        // The next item's P V may overwrite O_t when both warpgroups have read it.
+        tc_fence_before();
+        mbar_arrive(bar_oread);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_oread, splits & 1));
+        if (!ok) break;
+        ++splits;
       }
-      if (have) lse[row_at] = m_run * scale + logf(l_run);
     }
     if (!ok && !abort_all) set_fail(ATTN_ERR_TIMEOUT);
   }
@@ -658,11 +769,20 @@ bool make_tmap_packed(CUtensorMap* map, const void* base, int T, int heads, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool CAUSAL>
+// Items are of one tile, and long ones split, where items of two would not fill the SMs
+// whatever the lengths of B sequences of T tokens are (at 1.5 to 3 times as many items the
+// two halves of a pair are the better use of an SM: ragged d = 64 23.5 us, 19.3 in pairs).
+bool splits_items(const VarlenProblem& p) {
+  const int sms = device_sm_count();
+  const long long pairs = (long long)p.T / (2 * tile_tokens(p.H, p.Hkv)) + p.B;
+  return p.T > (kSplitTiles - 1) * kBlockN && pairs * p.Hkv * (p.causal ? 1 : 2) <= sms;
+}
+
+template <int D, bool CAUSAL, bool SPLIT>
 cudaError_t launch_impl(const VarlenProblem& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                         const void* plan, void* o, float* lse, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kernel = varlen_fwd_kernel<D, CAUSAL>;
+  auto kernel = varlen_fwd_kernel<D, CAUSAL, SPLIT>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
@@ -685,7 +805,7 @@ size_t varlen_plan_bytes(int B, int T, int H, int Hkv) {
 cudaError_t launch_varlen_plan(const VarlenProblem& p, const int* cu, void* plan, cudaStream_t stream) {
   return launch_pdl(varlen_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, cu, static_cast<int*>(plan), p.B, p.T,
                     p.H / p.Hkv, p.Hkv, tile_tokens(p.H, p.Hkv), p.causal,
-                    (int)plan_capacity(p.B, p.T, p.H, p.Hkv), device_sm_count());
+                    (int)plan_capacity(p.B, p.T, p.H, p.Hkv), device_sm_count(), splits_items(p) ? 1 : 0);
 }
 
 cudaError_t launch_varlen_fwd(const VarlenProblem& p, const void* q, const void* k, const void* v, const void* plan,
@@ -696,11 +816,20 @@ cudaError_t launch_varlen_fwd(const VarlenProblem& p, const void* q, const void*
       !make_tmap_packed(&mk, k, p.T, p.Hkv, p.d, strides[2], strides[3], true, G, kBlockN) ||
       !make_tmap_packed(&mv, v, p.T, p.Hkv, p.d, strides[4], strides[5], true, G, kBlockN))
     return cudaErrorInvalidValue;
-  if (p.d == 128)
-    return p.causal ? launch_impl<128, true>(p, mq, mk, mv, plan, o, lse, stream)
-                    : launch_impl<128, false>(p, mq, mk, mv, plan, o, lse, stream);
-  return p.causal ? launch_impl<64, true>(p, mq, mk, mv, plan, o, lse, stream)
-                  : launch_impl<64, false>(p, mq, mk, mv, plan, o, lse, stream);
+  const bool split = splits_items(p);
+#define ATTN_VARLEN_CASE(DD, CC, SS)                   \
+  if (p.d == DD && (p.causal != 0) == CC && split == SS) \
+    return launch_impl<DD, CC, SS>(p, mq, mk, mv, plan, o, lse, stream);
+  ATTN_VARLEN_CASE(64, false, false)
+  ATTN_VARLEN_CASE(64, false, true)
+  ATTN_VARLEN_CASE(64, true, false)
+  ATTN_VARLEN_CASE(64, true, true)
+  ATTN_VARLEN_CASE(128, false, false)
+  ATTN_VARLEN_CASE(128, false, true)
+  ATTN_VARLEN_CASE(128, true, false)
+  ATTN_VARLEN_CASE(128, true, true)
+#undef ATTN_VARLEN_CASE
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t read_and_clear_status_varlen(unsigned int* out, cudaStream_t stream) {

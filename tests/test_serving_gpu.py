@@ -119,6 +119,29 @@ def test_prompt_matches_the_square_forward(A):
     assert torch.equal(o, pack(o0)) and torch.equal(lse, lse0.transpose(1, 2).reshape(B * N, H))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,d,lens", [((2, 2), 64, [385]), ((8, 2), 128, [498, 385, 384, 1, 513, 0, 70]),
+                                          ((5, 1), 64, [640, 129, 900]), ((7, 1), 128, [1500, 3]),
+                                          ((3, 3), 128, [511, 512, 640]), ((64, 1), 64, [400, 130])])
+def test_prompt_split_items(A, heads, d, lens, causal):
+    """Few items: the two tiles of a CTA share an item's keys where it has enough; CTAs with several
+    items, split ones and others; rows behind the sequences are left as they are; the same bits twice."""
+    H, Hkv = heads
+    T = sum(lens)
+    q, k, v = normal((T + 9, H, d), 1), normal((T + 9, Hkv, d), 2), normal((T + 9, Hkv, d), 3)
+    v[T:] = torch.nan
+    plan = A.attn_varlen_plan(ints(sums(lens)), T + 9, H, Hkv, causal=causal)
+    got = []
+    for _ in range(2):
+        o = torch.full((T + 9, H, d), 7.0, dtype=BF, device="cuda")
+        lse = torch.full((T + 9, H), 7.0, device="cuda")
+        got.append(A.attn_varlen_fwd(q.cuda(), k.cuda(), v.cuda(), plan, causal=causal, o=o, lse=lse))
+        A.attn_check_status()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert (got[0][0][T:] == 7).all() and (got[0][1][T:] == 7).all()
+    check_prompt(q, k, v, lens, causal, 1 / math.sqrt(d), *got[0])
+
+
 def test_prompt_large_scores(A):
     """Scores of several hundred: one key takes all the weight in most rows."""
     lens, H, Hkv, d = [150, 260], 4, 2, 64
