@@ -22,7 +22,8 @@
 // rounded to FP16 (relative 2^-11) as the P V operand, scaled by 2^15 so that
 // probabilities down to 2^-29 of the largest keep all their bits; the row sum
 // adds the FP32 values.  Value scales enter P relative to a running power of
-// two R >= vs, which the accumulators carry.
+// two R >= vs, which the accumulators carry, and the 2^15 with them: taken into the
+// exponent's maximum it would be lost in part where scores reach 2^24.
 //
 // Each warp streams its own 32-position tiles of K and V by TMA through its own
 // ring (no barrier is shared between warps), with its own running maximum,
@@ -199,13 +200,13 @@ __device__ __forceinline__ uint32_t unit_offset(uint32_t r, uint32_t u) {
   return D == 128 ? r * 128u + ((u ^ (r & 7u)) << 4) : r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
 }
 
-// 1 / L (L < 2^47, off by 2 units of the last bit at most), or 0 where a row has seen
+// 1 / L (L < 2^32, off by 2 units of the last bit at most), or 0 where a row has seen
 // nothing.  A NaN stays one.
 __device__ __forceinline__ float inverse(float L) { return L == 0.f ? 0.f : __fdividef(1.f, L); }
 
-// Natural-log LSE from the base-2 maximum and the row sum, which carries 2^15.
+// Natural-log LSE from the base-2 maximum and the row sum.
 __device__ __forceinline__ float lse_of(float M, float L) {
-  return L == 0.f ? -INFINITY : (M + log2f(L) - 15.f) * 0.69314718055994531f;
+  return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // A segment in several parts: those behind the first (0: nothing to join), its
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) m_run[n][i] = -INFINITY, l_run[n][i] = 0.f;
-    float R = 0x1p-126f;  // power of two the accumulators' values are relative to
+    float R = 0x1p-126f;  // power of two the accumulators' values times 2^-15 are relative to
 
     for (int k = 0; k < tiles && ok; ++k) {
       const uint32_t st = used % C::kStages;
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         R = r_new;
       }
       const float inv_r = __uint_as_float(0x7F000000u - __float_as_uint(R));  // 1 / R of a power of two
-      const float vr[2] = {vsc[0] * inv_r, vsc[1] * inv_r};
+      const float vr[2] = {vsc[0] * inv_r * 0x1p15f, vsc[1] * inv_r * 0x1p15f};
       float alpha[NT][2];
       uint32_t pf[2][NT][2];  // P^T as the B operand of the halves
       bool same = shrink == 1.f;
@@ -717,7 +718,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           alpha[n][i] = ex2(m_run[n][i] - m_use[i]);
           same = same && alpha[n][i] == 1.f;
           m_run[n][i] = mx;
-          m_use[i] -= 15.f;
           l_run[n][i] *= alpha[n][i];
         }
 #pragma unroll
@@ -794,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         }
         l_run[n][i] = inverse(l_run[n][i]);
       }
+    const float r_merge = R * 0x1p-15f;
 #pragma unroll
     for (int at = 0; at < D; at += C::kMerge) {
       __syncthreads();  // the buffer holds Q, or the columns before, until here
@@ -828,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
           for (int u = 0; u < C::kMerge / 16; ++u)
             *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * C::kMerge + (((8 * u + g) ^ (c << 2)) << 1)) =
-                make_float2(acc[at / 16 + u][n][i] * l_run[n][i] * R, acc[at / 16 + u][n][2 + i] * l_run[n][i] * R);
+                make_float2(acc[at / 16 + u][n][i] * l_run[n][i] * r_merge, acc[at / 16 + u][n][2 + i] * l_run[n][i] * r_merge);
         }
       __syncthreads();
       // rows x columns over 128 threads, 4 columns at a time.
@@ -918,8 +919,8 @@ __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_k
   const int rr = ch.z % a.row_blocks * rows + r;
   const bool have = r < rows && rr < a.n_q * a.G;
   const int n = have ? ch.x + 1 : 0;
-  // l, at most 2^15 a key of less than 2^31, becomes a weight below 1.
-  constexpr float kShare = 0x1p-46f;
+  // l, at most 1 a key of less than 2^31, becomes a weight below 1.
+  constexpr float kShare = 0x1p-31f;
   // kBatch parts at a time, all their loads in flight together.
   constexpr int kBatch = kJoinBatch;
   float M = -INFINITY, L = 0.f, o[D / 32] = {};
