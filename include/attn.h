@@ -395,8 +395,10 @@ ATTN_API size_t attn_decode_int8_workspace_bytes(int B, int n_q, int H, int H_kv
  *   o       : [B,n_q,H,d] BF16, contiguous.   lse : [B,n_q,H] FP32.
  *   workspace : device buffer, 256-byte aligned, that no concurrently running call
  *             uses (also not the replay of another graph); needs no initialisation.
- * Softmax weights keep 11 bits down to 2^-29 of the row's largest; below that they
- * are rounded to multiples of 2^-40 of it.
+ * The weights p_j vs_j of the codes (p the softmax) keep 11 bits down to 2^-20 of the
+ * row's largest weight; below that they are off by at most 2^-31 of it, whatever the
+ * scales of pages that the row does not see or barely weighs.  A p below 2^-126 of
+ * the row's largest counts as 0.
  * Scales must be >= 0 and finite.  A position whose page number is out of range
  * is not seen.
  */

@@ -18,12 +18,18 @@
 // Codes become FP16 exactly (|c| <= 127): the byte c + 128 under the exponent
 // of 1024 is the FP16 number 1152 + c.  Q becomes FP16 after division by a
 // power of two of its row's maximum, so it is exact down to 2^-17 of that
-// maximum, and what lies below is rounded by at most 2^-25 of it.  P is
-// rounded to FP16 (relative 2^-11) as the P V operand, scaled by 2^15 so that
-// probabilities down to 2^-29 of the largest keep all their bits; the row sum
-// adds the FP32 values.  Value scales enter P relative to a running power of
-// two R >= vs, which the accumulators carry, and the 2^15 with them: taken into the
-// exponent's maximum it would be lost in part where scores reach 2^24.
+// maximum, and what lies below is rounded by at most 2^-25 of it.  The weights
+// of the values' codes, P vs, are rounded to FP16 (relative 2^-11) as the P V
+// operand, times 2^15 / R with a running power of two R >= vs, which the
+// accumulators carry.  While the scales that a warp meets lie within 2^8 of R, one
+// R serves all rows, and a row's weights down to 2^-20 of its largest keep all their
+// bits.  Scales further apart could take a row's bits by values that it does not see
+// or barely weighs (a large V of a later token, say): the warp then goes on with an
+// R of each row's own, the power of two at or above its largest 2^(s - m) vs.  On 64
+// sequences of 500 to 16000 positions that takes 99 us in place of 102 with 4 rows a key
+// head, 131 in place of 111 with 12, 159 in place of 142 with 20 (d = 128).  The row
+// sum adds the FP32 values.  The 2^15 goes with the scale: taken into the exponent's
+// maximum it would be lost in part where scores reach 2^24.
 //
 // Each warp streams its own 32-position tiles of K and V by TMA through its own
 // ring (no barrier is shared between warps), with its own running maximum,
@@ -46,6 +52,7 @@
 // rate), one of 131000 positions 50 us (5.4 TB/s); d = 64: 57 us and 30 us; with 20
 // rows 64 sequences 153 us: the accumulators then leave 8 warps an SM, and the
 // dependent conversions and products of a tile (2 us a warp) set the pace.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -209,6 +216,19 @@ __device__ __forceinline__ float lse_of(float M, float L) {
   return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
+// The whole number W >= w that is nearest w + 1/2, given w + 1/2 (|w| < 2^21), plus 1.5 * 2^23; its
+// low byte and the bit above are W's.  And 2^(E - 127 + SIGN * W), of an exponent within 1 to 254.
+__device__ __forceinline__ float whole(float w_half) { return w_half + 12582912.f; }
+template <int E, int SIGN>
+__device__ __forceinline__ float exp2_whole(float w_half) {
+  const uint32_t W = __float_as_uint(whole(w_half)) << 23;
+  return __uint_as_float(SIGN > 0 ? ((uint32_t)E << 23) + W : ((uint32_t)E << 23) - W);
+}
+// Largest ratio of R to a scale that one R for all rows serves.
+constexpr float kNarrow = 0x1p8f;
+// Least w + 1/2: codes of a scale below 2^-110 lose bits that are multiples of 2^-150.
+constexpr float kLeastWeight = -110.f;
+
 // A segment in several parts: those behind the first (0: nothing to join), its
 // sequence, key head * row_blocks + row block, and the CTA it begins in.
 struct Chain {
@@ -354,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   float* s_merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* s_m = reinterpret_cast<float*>(smem + C::kOffStat);
   float* s_l = s_m + kWarps * kRows;
+  float* s_w = s_m + warp * kRows;  // per row while the warp has tiles: see `wide`
   // In the merge's buffer between merges: Q, then per row the factor of its scores
   // and its last visible position.
   uint2* s_q = reinterpret_cast<uint2*>(s_merge);
@@ -626,7 +647,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) m_run[n][i] = -INFINITY, l_run[n][i] = 0.f;
-    float R = 0x1p-126f;  // power of two the accumulators' values times 2^-15 are relative to
+    // The accumulators' values times 2^-15 are relative to R, or, where wide, to 2^whole(s_w) of
+    // their row (R is 2^15 then).  v_least: the smallest scale so far.
+    float R = 0x1p-110f, v_least = FLT_MAX;
+    bool wide = false;
 
     for (int k = 0; k < tiles && ok; ++k) {
       const uint32_t st = used % C::kStages;
@@ -688,25 +712,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               if (pos0 + h * 16 + (x >> 1) * 8 + g > my_last(n, x & 1) || !((flags >> h) & 1u)) s[h][n][x] = -INFINITY;
-        if (!(flags & 1u)) vsc[0] = 0.f;
-        if (!(flags & 2u)) vsc[1] = 0.f;
+        // A half that was not loaded has no weights: any scale will do.
+        if (!(flags & 1u)) vsc[0] = flags != 0u ? vsc[1] : 0.f;
+        if (!(flags & 2u)) vsc[1] = vsc[0];
       }
-      const float v_big = fmaxf(vsc[0], vsc[1]);
-      float shrink = 1.f;
-      if (v_big > R) {
-        // The power of two at or above v_big (at most 2^126).
-        const float r_new = __uint_as_float(min((__float_as_uint(v_big) + 0x7FFFFFu) & 0x7F800000u, 0x7E800000u));
-        shrink = R / r_new;
-        R = r_new;
-      }
-      const float inv_r = __uint_as_float(0x7F000000u - __float_as_uint(R));  // 1 / R of a power of two
-      const float vr[2] = {vsc[0] * inv_r * 0x1p15f, vsc[1] * inv_r * 0x1p15f};
-      float alpha[NT][2];
-      uint32_t pf[2][NT][2];  // P^T as the B operand of the halves
-      bool same = shrink == 1.f;
+      // P in place of the scores.
+      float back[NT][2];  // the accumulators' factors
+      bool same = true;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float m_use[2];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float mx = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
@@ -714,27 +728,67 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           mx = fmaxf(m_run[n][i], mx);
-          m_use[i] = mx == -INFINITY ? 0.f : mx;
-          alpha[n][i] = ex2(m_run[n][i] - m_use[i]);
-          same = same && alpha[n][i] == 1.f;
+          const float m_use = mx == -INFINITY ? 0.f : mx;
+          back[n][i] = ex2(m_run[n][i] - m_use);
+          l_run[n][i] *= back[n][i];
+          same = same && back[n][i] == 1.f;
           m_run[n][i] = mx;
-          l_run[n][i] *= alpha[n][i];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              s[h][n][2 * y + i] = ex2(s[h][n][2 * y + i] - m_use);
+              l_run[n][i] += s[h][n][2 * y + i];
+            }
+        }
+      const float v_big = fmaxf(vsc[0], vsc[1]), v_small = fminf(vsc[0], vsc[1]);
+      const bool other = v_big > R || v_small < v_least;  // always where wide
+      if (!__all_sync(0xffffffffu, same && !other)) {
+        float shrink = 1.f;
+        if (other && !wide) {
+          v_least = fminf(v_least, v_small);
+          // The power of two at or above v_big.
+          const float r_new = fmaxf(R, __uint_as_float((__float_as_uint(v_big) + 0x7FFFFFu) & 0x7F800000u));
+          if (r_new > v_least * kNarrow || r_new > 0x1p126f) {
+            wide = true;
+            if (g == 0) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                s_w[8 * n + 2 * c] = s_w[8 * n + 2 * c + 1] = (float)((int)(__float_as_uint(R) >> 23) - 127);
+            }
+            __syncwarp();
+            R = 0x1p15f, v_least = INFINITY;
+          } else {
+            shrink = R / r_new;
+            R = r_new;
+          }
+        }
+        if (wide) {
+          const float lv[2] = {__log2f(vsc[0]) + 0.5f, __log2f(vsc[1]) + 0.5f};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float w_old = s_w[8 * n + 2 * c + i];
+              float w = fmaxf(w_old + __log2f(back[n][i]), kLeastWeight);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float p = fmaxf(s[h][n][i], s[h][n][2 + i]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) p = fmaxf(p, __shfl_xor_sync(0xffffffffu, p, off));
+                w = fmaxf(w, __log2f(p) + lv[h]);
+              }
+              back[n][i] *= ex2(whole(w_old) - whole(w));
+              const float up = exp2_whole<142, -1>(w);  // 2^(15 - W)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) s[h][n][i] *= up, s[h][n][2 + i] *= up;
+              __syncwarp();
+              if (g == 0) s_w[8 * n + 2 * c + i] = w;
+            }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float p0 = ex2(s[h][n][2 * y] - m_use[0]);
-            const float p1 = ex2(s[h][n][2 * y + 1] - m_use[1]);
-            l_run[n][0] += p0;
-            l_run[n][1] += p1;
-            pf[h][n][y] = transpose8(pack_f16x2(p0 * vr[h], p1 * vr[h]));
-          }
-      }
-      if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float s0 = alpha[n][0] * shrink, s1 = alpha[n][1] * shrink;
+          const float s0 = back[n][0] * shrink, s1 = back[n][1] * shrink;
 #pragma unroll
           for (int u = 0; u < D / 16; ++u) {
             acc[u][n][0] *= s0;
@@ -744,6 +798,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           }
         }
       }
+      const float inv_r = __uint_as_float(0x86800000u - __float_as_uint(R));  // 2^15 / R
+      const float vr[2] = {vsc[0] * inv_r, vsc[1] * inv_r};
+      uint32_t pf[2][NT][2];  // P^T as the B operand of the halves
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            pf[h][n][y] = transpose8(pack_f16x2(s[h][n][2 * y] * vr[h], s[h][n][2 * y + 1] * vr[h]));
       // O^T += V^T P^T.  A transposed load gives positions 2c, 2c + 1 of the columns
       // d = 16 u + 2 g (even bytes) and + 1 (odd bytes), rows g and g + 8 of the
       // A operand.
@@ -782,6 +846,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       const int more = rest == 0 ? 0 : 1 + (int)((rest - 1) / (unsigned)min(per, 0x7fffffffll));
       a.chains[slot] = Chain{more, sg.b, hr, (int)blockIdx.x};
     }
+    float from[NT][2];  // what the accumulators are relative to
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) from[n][i] = wide ? exp2_whole<112, 1>(s_w[8 * n + 2 * c + i]) : R * 0x1p-15f;
+    __syncwarp();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -794,7 +864,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         }
         l_run[n][i] = inverse(l_run[n][i]);
       }
-    const float r_merge = R * 0x1p-15f;
 #pragma unroll
     for (int at = 0; at < D; at += C::kMerge) {
       __syncthreads();  // the buffer holds Q, or the columns before, until here
@@ -829,7 +898,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
           for (int u = 0; u < C::kMerge / 16; ++u)
             *reinterpret_cast<float2*>(s_merge + (warp * kRows + r) * C::kMerge + (((8 * u + g) ^ (c << 2)) << 1)) =
-                make_float2(acc[at / 16 + u][n][i] * l_run[n][i] * r_merge, acc[at / 16 + u][n][2 + i] * l_run[n][i] * r_merge);
+                make_float2(acc[at / 16 + u][n][i] * l_run[n][i] * from[n][i],
+                            acc[at / 16 + u][n][2 + i] * l_run[n][i] * from[n][i]);
         }
       __syncthreads();
       // rows x columns over 128 threads, 4 columns at a time.

@@ -1,10 +1,10 @@
-"""Serving operators at the ends of their ranges."""
+"""Serving operators at the ends of their ranges: scores and value scales of extreme size."""
 import math
 
 import pytest
 
 import serving_ref as ref
-from test_serving_gpu import A, BF, Cache, ints, scattered  # noqa: F401
+from test_serving_gpu import A, BF, Cache, ints, normal, scattered  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -46,3 +46,100 @@ def test_decode_scores_beyond_the_exponent(A, top, lens, d, G, n_q):
     # Nine roundings of 2^-24: the page's scale, the call's, log2 e, their product, that times the page's
     # scale, the score, its sum with log2 3, ln 2, the last product; and log2 3 < 1.6 beside 2^24 and more.
     assert ((lse.cpu().double() / (top * math.log(2.0)) - 1).abs() <= (9 + 1.6) * 2.0 ** -24 + 2.0 ** -40).all()
+
+
+# ------------------------------------------------------------- value scales
+def check_weighted(c, q, lens, scale, o, lse):
+    """The bound of a weight's rounding follows the row's own weighted values: with P_j the row's exact
+    softmax, weights P vs are FP16, relative 2^-11, as p 2^15 vs / R, and where that falls below 2^-14,
+    absolute 2^-25, i.e. 2^-40 R.  Either every scale that the row's warp has met is at least 2^-8 R, so that
+    the key of its largest p, which is 1 there, has a weight of 2^-8 R; or R is the row's own: at most twice
+    its largest weight, or, from the time before, 2^8 of it.  So R is below 2^9 times the row's largest
+    P_j vs_j, whatever the scales of pages that the row does not see or barely weighs, and a key is off by
+    at most 2^-31 * 127 of that."""
+    B, n_q, H, d = q.shape
+    Hkv, page = c.codes[0].shape[1], c.codes[0].shape[2]
+    G = H // Hkv
+    o, lse = o.cpu(), lse.cpu()
+    for b, n in enumerate(lens):
+        k, v = c.values(0, b, n), c.values(1, b, n)
+        last = torch.tensor([n - n_q + i for i in range(n_q) for _ in range(G)])
+        ids = c.tables[b][:-(-n // page)]
+        for h in range(Hkv):
+            hs = slice(h * G, (h + 1) * G)
+            qr = q[b, :, hs].reshape(-1, d)
+            r, rl, a, size = ref.attention(qr, k[:, h], v[:, h], scale, last)
+            vs = c.scales[1][ids, h].double().repeat_interleave(page)[:n]
+            s = torch.where(torch.arange(n)[None] <= last[:, None], scale * (qr.double() @ k[:, h].t()), -torch.inf)
+            p = torch.exp(s - torch.where(rl.isinf(), 0.0, rl)[:, None])
+            least = n * 127 * 2.0 ** -31 * (p * vs).amax(-1)[:, None]
+            got, gl = o[b, :, hs].reshape(-1, d).double(), lse[b, :, hs].reshape(-1).double()
+            bound = ref.output_bound(r, a, size, d, 2.0 ** -11) + least
+            assert ((got - r).abs() <= bound).all(), (b, h)
+            live = ~rl.isinf()
+            assert (got[~live] == 0).all() and (gl[~live] == -torch.inf).all()
+            assert ((gl - rl)[live].abs() <= ref.lse_bound(rl, size, d)[live]).all(), (b, h)
+
+
+ROWS = [(64, 1, 1), (128, 4, 1), (64, 4, 3), (128, 4, 3), (128, 4, 5), (64, 5, 4), (128, 8, 4)]
+
+
+@pytest.mark.parametrize("d,G,n_q", ROWS)
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("lens", PATHS)
+def test_decode_value_scales_of_every_ratio(A, lens, page, d, G, n_q):
+    """Value scales spread over 2^90 from page to page, and scores over some tens: the row's weight lies on
+    pages of any scale."""
+    Hkv = 2
+    tables, pages = scattered([-(-n // page) for n in lens], 7)
+    c = Cache(pages, Hkv, page, d, tables)
+    g = torch.Generator().manual_seed(len(lens) + page)
+    c.scales[1] *= 2.0 ** torch.randint(-45, 46, c.scales[1].shape, generator=g)
+    c.scales[1][tables[0][1]] = 0
+    c.upload()
+    q = normal((len(lens), n_q, Hkv * G, d), 1) * 2
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens))
+    A.attn_check_status()
+    check_weighted(c, q, lens, 1 / math.sqrt(d), o, lse)
+
+
+@pytest.mark.parametrize("d,G,n_q", [r for r in ROWS if r[2] > 1])
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("long", [1, 5, 70])
+def test_decode_large_values_of_later_tokens(A, long, page, d, G, n_q):
+    """The newest token opens a page whose value scale is 2^45 times the others': the tokens before it, which
+    must not see it, keep their precision; the newest one sees it.  In a tile's second half where the page is 16."""
+    Hkv = 2
+    lens = [page * long + 1, page * (long + 1) + 1]
+    tables, pages = scattered([-(-n // page) for n in lens], 7)
+    c = Cache(pages, Hkv, page, d, tables)
+    for t in tables:
+        c.scales[1][t[-1]] *= 2.0 ** 45
+    c.upload()
+    q = normal((2, n_q, Hkv * G, d), 1)
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens))
+    A.attn_check_status()
+    check_weighted(c, q, lens, 1 / math.sqrt(d), o, lse)
+
+
+@pytest.mark.parametrize("d,G,n_q", ROWS)
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("lens", PATHS)
+def test_decode_large_values_of_no_weight(A, lens, page, d, G, n_q):
+    """Every third page holds values 2^45 times as large as the others', behind keys whose weights are about
+    2^-90 of the row's largest: they change nothing that can be seen."""
+    Hkv = 2
+    tables, pages = scattered([-(-n // page) for n in lens], 7)
+    c = Cache(pages, Hkv, page, d, tables)
+    c.codes[0][..., 0] = 0
+    for t in tables:
+        for p in t[1::3]:
+            c.scales[1][p] *= 2.0 ** 45
+            c.codes[0][p, ..., 0] = -127
+    c.scales[0][:] = 0.01
+    c.upload()
+    q = normal((len(lens), n_q, Hkv * G, d), 1)
+    q[..., 0] = 49.0  # -127 * 0.01 * 49 = -62 = -90 ln 2
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens), scale=1.0)
+    A.attn_check_status()
+    check_weighted(c, q, lens, 1.0, o, lse)
