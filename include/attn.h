@@ -291,9 +291,10 @@ ATTN_API attn_status attn_bwd_noalloc(const void* q, const void* k, const void* 
  * Lengths, page numbers and plans lie in device memory and are read by the
  * kernels, so a call can be captured in a CUDA graph and replayed on new ones.
  * They cannot be checked before the launch: a value out of range never leads
- * outside the tensors; the kernel ignores what it points to, and
- * attn_check_status() reports ATTN_ERR_INVALID_ARG.  A sequence may have no
- * token at all.
+ * outside the tensors, and attn_check_status() reports ATTN_ERR_INVALID_ARG.  Pages
+ * whose number is out of range are neither written nor seen; attn_cache_append_int8
+ * leaves out a sequence whose length or start is, and the other calls cut lengths to
+ * what the tensors hold.  A sequence may have no token at all.
  *
  * The cache: codes k_cache, v_cache int8 [num_pages, H_kv, page_size, d],
  * contiguous, and scales k_scale, v_scale FP32 [num_pages, H_kv]; a code c stands

@@ -197,15 +197,16 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t m) { return __reduce_max_s
 __device__ __forceinline__ float scale_for(uint32_t bits) { return __uint_as_float(bits << 16) / 127.f; }
 
 // Sequence b's new rows: `first` is its first row of the packed input, n their
-// number, `start` the position of the first (clamped to what there is, whatever
-// the lengths in memory are).
+// number, `start` the position of the first.  None where a length in memory is out of
+// range: rows put elsewhere would overwrite what the pages hold.
 __device__ __forceinline__ void new_rows(const int* cu, const int* starts, int b, int T, int& first, int& n,
                                          int& start) {
   const int x = __ldcg(cu + b), y = __ldcg(cu + b + 1), z = __ldcg(starts + b);
-  if (x < 0 || y < x || y > T || z < 0) set_fail(ATTN_ERR_INVALID_ARG);
-  first = min(max(x, 0), T);
-  n = min(max(y, first), T) - first;
-  start = max(z, 0);
+  const bool fine = x >= 0 && y >= x && y <= T && z >= 0;
+  if (!fine) set_fail(ATTN_ERR_INVALID_ARG);
+  first = fine ? x : 0;
+  n = fine ? y - x : 0;
+  start = fine ? z : 0;
 }
 
 struct AppendArgs {

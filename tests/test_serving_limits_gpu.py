@@ -1,4 +1,5 @@
-"""Serving operators at the ends of their ranges: scores and value scales of extreme size."""
+"""Serving operators at the ends of their ranges: scores and value scales of extreme size, and
+lengths that are out of range."""
 import math
 
 import pytest
@@ -143,3 +144,28 @@ def test_decode_large_values_of_no_weight(A, lens, page, d, G, n_q):
     o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens), scale=1.0)
     A.attn_check_status()
     check_weighted(c, q, lens, 1.0, o, lse)
+
+
+# ------------------------------------------------------------------ lengths
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_of_lengths_out_of_range_leaves_the_cache(A, d, few):
+    """A sequence whose start is negative, or whose rows begin before the input, end behind it or run
+    backwards, is left out: what its pages hold stays as it is.  The others are written."""
+    page, Hkv, T = 16, 3, 12 if few else 64
+    tables = [[0, 1, 8, 9], [2, 3, 10, 11], [4, 5, 6, 7]]
+    rows = [normal((T, Hkv, d), 1), normal((T, Hkv, d), 2)]
+    gpu_rows = [x.cuda() for x in rows]
+    for cu, starts, good in (([0, 4, 8, T], [-1, 0, 5], (1, 2)), ([0, 4, 8, T], [3, -2 ** 31, 0], (0, 2)),
+                             ([-4, 4, 8, T], [0, 0, 0], (1, 2)), ([0, 4, 8, T + 1], [0, 2, 0], (0, 1)),
+                             ([0, 9, 4, T], [0, 0, 0], (0, 2)), ([0, 4, 2 ** 31 - 1, T], [0, 0, 0], (0,)),
+                             ([-2 ** 31, -1, 4, T], [0, 0, 3], (2,))):
+        c = Cache(12, Hkv, page, d, tables)
+        for b in good:
+            for i in range(2):
+                ref.append(rows[i][cu[b]:cu[b + 1]], c.codes[i], c.scales[i], tables[b], starts[b])
+        A.attn_cache_append_int8(*gpu_rows, *c.gpu, ints(cu), ints(starts))
+        with pytest.raises(A.AttnError, match="out of range"):
+            A.attn_check_status()
+        assert c.equal(), (cu, starts)
+    A.attn_check_status()
