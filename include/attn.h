@@ -369,9 +369,10 @@ ATTN_API attn_status attn_cache_append_int8(const void* k, const void* v, long l
  * Reads ranges of positions back as values code * scale: packed token
  * cu_seqlens[b] + i of the outputs is position starts[b] + i of sequence b.
  *   k, v : [T,H_kv,d] of type dt (the product in FP32, or that rounded to BF16),
- *          contiguous, written; cu_seqlens[0] = 0, cu_seqlens[B] = T.  Tokens
- *          outside the sequences or without a valid page become 0 and are
- *          reported by attn_check_status().
+ *          contiguous, written; 0 = cu_seqlens[0] <= cu_seqlens[b] <= cu_seqlens[b+1],
+ *          cu_seqlens[B] = T.  Other lengths are reported by attn_check_status();
+ *          tokens outside the sequences or without a valid page become 0 and are
+ *          reported as well.
  */
 ATTN_API attn_status attn_cache_read_int8(const void* k_cache, const void* v_cache,
                                           const float* k_scale, const float* v_scale,

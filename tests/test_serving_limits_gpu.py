@@ -169,3 +169,16 @@ def test_append_of_lengths_out_of_range_leaves_the_cache(A, d, few):
             A.attn_check_status()
         assert c.equal(), (cu, starts)
     A.attn_check_status()
+
+
+def test_read_reports_lengths_out_of_range(A):
+    """Lengths that do not begin at 0, end at T and rise are reported, also where every token of the output
+    has a page."""
+    page, d, Hkv = 16, 64, 2
+    c = Cache(12, Hkv, page, d, [[0, 1, 2, 3, 4], [5, 6, 7, 8, 9]])
+    for cu, T in (([-3, 20, 40], 40), ([0, 20, 41], 40), ([0, 40, 30], 40), ([0, 40, 39], 40), ([2, 20, 40], 40)):
+        A.attn_cache_read_int8(*c.gpu, ints(cu), ints([0, 0]), T)
+        with pytest.raises(A.AttnError, match="out of range"):
+            A.attn_check_status()
+    A.attn_cache_read_int8(*c.gpu, ints([0, 20, 40]), ints([0, 0]), 40)
+    A.attn_check_status()
