@@ -1,0 +1,34 @@
+"""Serving entry points: host-side checks at the ends of their ranges (no kernel is launched)."""
+import ctypes
+
+import pytest
+
+from precision_numerics_gb300 import attn, build
+
+F = ctypes.c_float
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return attn.load_library()
+
+
+def test_numbers_of_sequences_that_a_stride_would_pass(lib):
+    """The kernels go over the sequences in strides of up to 1024 in 32 bits."""
+    for B in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 1024):
+        calls = (
+            lambda: lib.attn_varlen_plan(16, B, 3, 1, 1, 1, 16, 1 << 50, None),
+            lambda: lib.attn_varlen_fwd(16, 16, 16, 64, 64, 64, 64, 64, 64, 16, 1 << 50, 16, 16, B, 3, 1, 1, 64, F(0.1), 1,
+                                        None),
+            lambda: lib.attn_cache_append_int8(16, 16, 64, 64, 64, 64, 16, 16, 16, 16, 16, 16, 16, B, 3, 1, 64, 9, 16, 4,
+                                               None),
+            lambda: lib.attn_cache_read_int8(16, 16, 16, 16, 16, 16, 16, 16, 16, B, 3, 1, 64, 9, 16, 4, 1, None),
+            lambda: lib.attn_decode_int8(16, 64, 64, 64, 16, 16, 16, 16, 16, 16, 16, 16, B, 1, 1, 1, 64, 9, 16, 4, F(0.1),
+                                         256, 1 << 50, None),
+        )
+        for call in calls:
+            assert call() == attn.ATTN_ERR_INVALID_ARG
+            assert "too large" in lib.attn_last_error().decode()
+        assert lib.attn_varlen_plan_bytes(B, 3, 1, 1) == 0
+        assert lib.attn_decode_int8_workspace_bytes(B, 1, 1, 1, 64, 16, 4) == 0
