@@ -49,9 +49,7 @@ attn_status check_varlen(int B, int T, int H, int H_kv, int d, VarlenProblem* p)
   return ATTN_OK;
 }
 
-attn_status check_cache(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
-                        const int* block_table, int B, int H_kv, int d, int num_pages, int page_size, int max_blocks,
-                        PtrCheck& ptr, PagedCache* c) {
+attn_status check_pages(int H_kv, int d, int num_pages, int page_size, int max_blocks) {
   ATTN_CHECK(check_heads(H_kv, H_kv, d));
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
     return fail(ATTN_ERR_UNSUPPORTED, "page_size = %d is not supported (16, 32, 64 or 128)", page_size);
@@ -61,6 +59,13 @@ attn_status check_cache(const void* k_cache, const void* v_cache, const float* k
     return fail(ATTN_ERR_UNSUPPORTED, "num_pages * H_kv * page_size exceeds 2^31 - 1 rows");
   if (max_blocks > (INT_MAX - 4096) / page_size)
     return fail(ATTN_ERR_UNSUPPORTED, "max_blocks * page_size exceeds 2^31 positions");
+  return ATTN_OK;
+}
+
+attn_status check_cache(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                        const int* block_table, int B, int H_kv, int d, int num_pages, int page_size, int max_blocks,
+                        PtrCheck& ptr, PagedCache* c) {
+  ATTN_CHECK(check_pages(H_kv, d, num_pages, page_size, max_blocks));
   ATTN_CHECK(ptr(k_cache, "k_cache"));
   ATTN_CHECK(ptr(v_cache, "v_cache"));
   ATTN_CHECK(ptr(k_scale, "k_scale", 4));
@@ -180,7 +185,7 @@ attn_status attn_cache_read_int8(const void* k_cache, const void* v_cache, const
 }
 
 size_t attn_decode_int8_workspace_bytes(int B, int n_q, int H, int H_kv, int d, int page_size, int max_blocks) {
-  if (check_decode(B, n_q, H, H_kv, d) != ATTN_OK) return 0;
+  if (check_decode(B, n_q, H, H_kv, d) != ATTN_OK || check_pages(H_kv, d, 1, page_size, max_blocks) != ATTN_OK) return 0;
   PagedCache c = {nullptr, nullptr, nullptr, nullptr, nullptr, B, H_kv, d, 1, page_size, max_blocks};
   return decode_workspace_bytes(c, n_q, H);
 }

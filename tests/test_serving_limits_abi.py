@@ -32,3 +32,17 @@ def test_numbers_of_sequences_that_a_stride_would_pass(lib):
             assert "too large" in lib.attn_last_error().decode()
         assert lib.attn_varlen_plan_bytes(B, 3, 1, 1) == 0
         assert lib.attn_decode_int8_workspace_bytes(B, 1, 1, 1, 64, 16, 4) == 0
+
+
+def test_workspace_of_invalid_arguments_is_zero(lib):
+    """What attn_decode_int8 refuses needs no workspace."""
+    good = dict(B=2, n_q=1, H=8, Hkv=2, d=64, page=16, blocks=4000)
+
+    def need(**kw):
+        x = {**good, **kw}
+        return lib.attn_decode_int8_workspace_bytes(x["B"], x["n_q"], x["H"], x["Hkv"], x["d"], x["page"], x["blocks"])
+
+    assert need() > 0
+    for kw in (dict(page=17), dict(page=256), dict(page=-16), dict(blocks=0), dict(blocks=-1), dict(blocks=2 ** 28),
+               dict(d=96), dict(H=9), dict(n_q=257), dict(B=0)):
+        assert need(**kw) == 0, kw
