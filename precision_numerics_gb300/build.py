@@ -9,7 +9,9 @@ header is newer than the library.
 
 csrc/torch_calls.cpp becomes the Python module _lib/_attn_torch.<torch version>.so
 (g++ against the installed PyTorch's headers, linked to libattn.so beside it), the
-serving calls' binding; the ctypes binding of the whole C ABI needs no part of it.
+serving calls' binding.  The library needs neither it nor PyTorch: a module that
+cannot be built is reported as a warning, and the serving calls go through ctypes,
+as all others do.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -49,7 +52,7 @@ def _sources():
 
 
 def _inputs():
-    return (_sources() + [BINDING_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
@@ -70,14 +73,23 @@ def binding_path() -> str:
     return os.path.join(LIB_DIR, f"_attn_torch.{torch.__version__}.so")
 
 
+def _older(lib, inputs) -> bool:
+    if not os.path.exists(lib):
+        return True
+    t = os.path.getmtime(lib)
+    return any(os.path.getmtime(p) > t for p in inputs)
+
+
+def _binding_needs_build() -> bool:
+    try:
+        path = binding_path()
+    except ImportError:  # no PyTorch, nothing to bind to
+        return False
+    return _older(path, [BINDING_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h")), os.path.abspath(__file__)])
+
+
 def needs_build(variant: str = "") -> bool:
-    for lib in (lib_path(variant),) if variant else (lib_path(), binding_path()):
-        if not os.path.exists(lib):
-            return True
-        t = os.path.getmtime(lib)
-        if any(os.path.getmtime(p) > t for p in _inputs()):
-            return True
-    return False
+    return _older(lib_path(variant), _inputs()) or (not variant and _binding_needs_build())
 
 
 @contextlib.contextmanager
@@ -103,10 +115,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
         # Another process may have built it while this one waited for the lock.
         if not force and not needs_build(variant):
             return lib
-        return _build_locked(lib, verbose, extra_flags, variant)
+        return _build_locked(lib, verbose, extra_flags, variant, force)
 
 
-def _build_locked(lib, verbose, extra_flags, variant) -> str:
+def _build_locked(lib, verbose, extra_flags, variant, force=False) -> str:
     nvcc = _nvcc()
     build_dir = BUILD if not variant else BUILD + "_" + variant
     os.makedirs(build_dir, exist_ok=True)
@@ -124,17 +136,20 @@ def _build_locked(lib, verbose, extra_flags, variant) -> str:
 
     srcs = _sources()
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        binding = None if variant else ex.submit(_compile_binding, build_dir)
-        objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding and binding.result()
-    tmp = f"{lib}.tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of {os.path.basename(lib)} failed:\n{r.stderr}\n{r.stdout}")
-    os.replace(tmp, lib)
-    if binding_obj:
-        _link_binding(binding_obj)
+        binding = None
+        if not variant and (force or _binding_needs_build()):
+            binding = ex.submit(_compile_binding, build_dir)
+        if force or _older(lib, _inputs()):
+            objs = list(ex.map(compile_one, srcs))
+            tmp = f"{lib}.tmp{os.getpid()}"
+            _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], f"link of {os.path.basename(lib)}")
+            os.replace(tmp, lib)
+    if binding is not None:
+        try:
+            _link_binding(binding.result())
+        except (OSError, ImportError, RuntimeError) as e:
+            warnings.warn(f"the tensor binding was not built, the serving calls go through ctypes: {e}", RuntimeWarning,
+                          stacklevel=3)
     return lib
 
 
