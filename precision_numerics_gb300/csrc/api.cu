@@ -198,18 +198,7 @@ cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t strea
   return cudaGetLastError();
 }
 
-cudaError_t read_and_clear_status_misc(unsigned int* out, cudaStream_t stream) {
-  static const unsigned int zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_status_misc, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  err = cudaStreamSynchronize(stream);
-  if (err != cudaSuccess) return err;
-  err = cudaMemcpyToSymbolAsync(g_status_misc, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (err != cudaSuccess) return err;
-  return cudaStreamSynchronize(stream);
-}
+cudaError_t status_word_misc(void** word) { return cudaGetSymbolAddress(word, g_status_misc); }
 
 namespace {
 
@@ -434,15 +423,26 @@ attn_status attn_bwd(const void* q, const void* k, const void* v, const void* o,
 attn_status attn_check_status(cudaStream_t stream) {
   cudaError_t err = cudaStreamSynchronize(stream);
   if (err != cudaSuccess) return cuda_fail(err, "attn_check_status: stream");
-  // Every word is read and cleared before any is reported.
-  unsigned int a = 0, b = 0, c = 0, prompt = 0, cache = 0, decode = 0;
-  if ((err = read_and_clear_status_fwd(&a, stream)) != cudaSuccess ||
-      (err = read_and_clear_status_bwd(&b, stream)) != cudaSuccess ||
-      (err = read_and_clear_status_misc(&c, stream)) != cudaSuccess ||
-      (err = read_and_clear_status_varlen(&prompt, stream)) != cudaSuccess ||
-      (err = read_and_clear_status_cache(&cache, stream)) != cudaSuccess ||
-      (err = read_and_clear_status_decode(&decode, stream)) != cudaSuccess)
-    return cuda_fail(err, "attn_check_status: status read");
+  // Every word is read, and cleared where something was set, before any is reported.
+  constexpr int kWords = 6;
+  cudaError_t (*const address[kWords])(void**) = {status_word_fwd,    status_word_bwd,   status_word_misc,
+                                                  status_word_varlen, status_word_cache, status_word_decode};
+  void* at[kWords];
+  unsigned int word[kWords] = {};
+  for (int i = 0; i < kWords && err == cudaSuccess; ++i) {
+    err = address[i](&at[i]);
+    if (err == cudaSuccess) err = cudaMemcpyAsync(&word[i], at[i], sizeof(word[i]), cudaMemcpyDeviceToHost, stream);
+  }
+  if (err == cudaSuccess) err = cudaStreamSynchronize(stream);
+  bool set = false;
+  for (int i = 0; i < kWords && err == cudaSuccess; ++i)
+    if (word[i] != 0) {
+      err = cudaMemsetAsync(at[i], 0, sizeof(word[i]), stream);
+      set = true;
+    }
+  if (set && err == cudaSuccess) err = cudaStreamSynchronize(stream);
+  if (err != cudaSuccess) return cuda_fail(err, "attn_check_status: status read");
+  const unsigned int a = word[0], b = word[1], c = word[2], prompt = word[3], cache = word[4], decode = word[5];
   const unsigned int any = a | b | c, serving = prompt | cache | decode;
   if ((any | serving) & ATTN_ERR_TIMEOUT)
     return fail(ATTN_ERR_TIMEOUT, "a kernel gave up on a bounded wait (status %u/%u/%u/%u/%u/%u)", a,

@@ -161,13 +161,13 @@ cudaError_t launch_varlen_fwd(const VarlenProblem& p, const void* q, const void*
                               const void* plan, void* o, float* lse, const long long* strides,
                               cudaStream_t stream);
 
-// Device status words (one per kernel translation unit): read and clear.
-cudaError_t read_and_clear_status_fwd(unsigned int* out, cudaStream_t stream);
-cudaError_t read_and_clear_status_bwd(unsigned int* out, cudaStream_t stream);
-cudaError_t read_and_clear_status_misc(unsigned int* out, cudaStream_t stream);
-cudaError_t read_and_clear_status_varlen(unsigned int* out, cudaStream_t stream);
-cudaError_t read_and_clear_status_cache(unsigned int* out, cudaStream_t stream);
-cudaError_t read_and_clear_status_decode(unsigned int* out, cudaStream_t stream);
+// Addresses of the device status words (one per kernel translation unit) on the current device.
+cudaError_t status_word_fwd(void** word);
+cudaError_t status_word_bwd(void** word);
+cudaError_t status_word_misc(void** word);
+cudaError_t status_word_varlen(void** word);
+cudaError_t status_word_cache(void** word);
+cudaError_t status_word_decode(void** word);
 
 // Shape and scalar checks shared by every entry point (d, N, B*H*N*d, dtype,
 // and the scale when need_scale); fills *out and records the error detail.

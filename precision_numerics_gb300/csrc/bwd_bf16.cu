@@ -1330,17 +1330,6 @@ extern "C" ATTN_API int attn_testhook_stall_bwd(int on) {
 }
 #endif
 
-cudaError_t read_and_clear_status_bwd(unsigned int* out, cudaStream_t stream) {
-  static const unsigned int zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_status_bwd, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  err = cudaStreamSynchronize(stream);
-  if (err != cudaSuccess) return err;
-  err = cudaMemcpyToSymbolAsync(g_status_bwd, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (err != cudaSuccess) return err;
-  return cudaStreamSynchronize(stream);
-}
+cudaError_t status_word_bwd(void** word) { return cudaGetSymbolAddress(word, g_status_bwd); }
 
 }  // namespace attn

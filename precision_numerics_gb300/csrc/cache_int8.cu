@@ -547,17 +547,6 @@ cudaError_t launch_cache_read_int8(const PagedCache& c, const int* cu, const int
   return fp32 ? launch_read<64, true>(a, stream) : launch_read<64, false>(a, stream);
 }
 
-cudaError_t read_and_clear_status_cache(unsigned int* out, cudaStream_t stream) {
-  static const unsigned int zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_status_cache, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  err = cudaStreamSynchronize(stream);
-  if (err != cudaSuccess) return err;
-  err = cudaMemcpyToSymbolAsync(g_status_cache, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (err != cudaSuccess) return err;
-  return cudaStreamSynchronize(stream);
-}
+cudaError_t status_word_cache(void** word) { return cudaGetSymbolAddress(word, g_status_cache); }
 
 }  // namespace attn

@@ -1235,17 +1235,6 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   return cudaErrorInvalidValue;
 }
 
-cudaError_t read_and_clear_status_decode(unsigned int* out, cudaStream_t stream) {
-  static const unsigned int zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_status_decode, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  err = cudaStreamSynchronize(stream);
-  if (err != cudaSuccess) return err;
-  err = cudaMemcpyToSymbolAsync(g_status_decode, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (err != cudaSuccess) return err;
-  return cudaStreamSynchronize(stream);
-}
+cudaError_t status_word_decode(void** word) { return cudaGetSymbolAddress(word, g_status_decode); }
 
 }  // namespace attn

@@ -787,17 +787,6 @@ extern "C" ATTN_API int attn_testhook_stall(int on) {
 }
 #endif
 
-cudaError_t read_and_clear_status_fwd(unsigned int* out, cudaStream_t stream) {
-  static const unsigned int zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_status_fwd, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  err = cudaStreamSynchronize(stream);
-  if (err != cudaSuccess) return err;
-  err = cudaMemcpyToSymbolAsync(g_status_fwd, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (err != cudaSuccess) return err;
-  return cudaStreamSynchronize(stream);
-}
+cudaError_t status_word_fwd(void** word) { return cudaGetSymbolAddress(word, g_status_fwd); }
 
 }  // namespace attn

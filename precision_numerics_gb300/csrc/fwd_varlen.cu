@@ -832,17 +832,6 @@ cudaError_t launch_varlen_fwd(const VarlenProblem& p, const void* q, const void*
   return cudaErrorInvalidValue;
 }
 
-cudaError_t read_and_clear_status_varlen(unsigned int* out, cudaStream_t stream) {
-  static const unsigned int zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbolAsync(out, g_status_varlen, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  err = cudaStreamSynchronize(stream);
-  if (err != cudaSuccess) return err;
-  err = cudaMemcpyToSymbolAsync(g_status_varlen, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (err != cudaSuccess) return err;
-  return cudaStreamSynchronize(stream);
-}
+cudaError_t status_word_varlen(void** word) { return cudaGetSymbolAddress(word, g_status_varlen); }
 
 }  // namespace attn

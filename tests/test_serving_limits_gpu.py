@@ -182,3 +182,17 @@ def test_read_reports_lengths_out_of_range(A):
             A.attn_check_status()
     A.attn_cache_read_int8(*c.gpu, ints([0, 20, 40]), ints([0, 0]), 40)
     A.attn_check_status()
+
+
+def test_status_of_several_calls_at_once(A):
+    """Reports of several calls since the last check are given together and cleared together."""
+    page, d, Hkv = 16, 64, 2
+    c = Cache(4, Hkv, page, d, [[0, 1]])
+    rows, q = normal((4, Hkv, d), 1).cuda(), normal((1, 1, 4, d), 2).cuda()
+    for _ in range(2):
+        A.attn_varlen_plan(ints([0, 9]), 4, 4, Hkv)
+        A.attn_cache_append_int8(rows, rows, *c.gpu, ints([0, 4]), ints([-1]))
+        A.attn_decode_int8(q, *c.gpu, ints([99]))
+        with pytest.raises(A.AttnError, match=r"varlen [1-9]\d*, cache [1-9]\d*, decode [1-9]"):
+            A.attn_check_status()
+        A.attn_check_status()
