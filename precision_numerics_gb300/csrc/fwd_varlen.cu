@@ -142,7 +142,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     plan[2] = G;
     plan[3] = Hkv;
     plan[4] = causal;
-    plan[5] = min(upto, capacity);  // more than the capacity only for cu_seqlens that run backwards
+    // More than the capacity only for cu_seqlens that run backwards: what is dropped is reported.
+    if (upto > capacity) set_fail(ATTN_ERR_INVALID_ARG);
+    plan[5] = min(upto, capacity);
   }
   __syncthreads();
   PlanItem* items = reinterpret_cast<PlanItem*>(plan + kPlanHeader);

@@ -46,3 +46,18 @@ def test_workspace_of_invalid_arguments_is_zero(lib):
     for kw in (dict(page=17), dict(page=256), dict(page=-16), dict(blocks=0), dict(blocks=-1), dict(blocks=2 ** 28),
                dict(d=96), dict(H=9), dict(n_q=257), dict(B=0)):
         assert need(**kw) == 0, kw
+
+
+def test_plan_has_room_for_items_of_one_tile(lib):
+    """An item is 128 // G tokens of a sequence where pairs of tiles would not fill the SMs: the plan's
+    16-byte entries behind its header suffice for every way to cut T tokens into B sequences."""
+    for H, Hkv in ((1, 1), (8, 2), (6, 2), (64, 1), (5, 1)):
+        tq = 128 // (H // Hkv)
+        for B in (1, 2, 5):
+            for T in (0, 1, tq - 1, tq, tq + 1, 2 * tq + 1, 7 * tq + 3):
+                cuts = [[T] + [0] * (B - 1)]
+                for x in (1, tq - 1, tq, tq + 1, 2 * tq + 1):  # B - 1 sequences of x tokens, as far as there are any
+                    cut = [max(0, min(x, T - x * i)) for i in range(B - 1)]
+                    cuts.append(cut + [T - sum(cut)])
+                items = max(sum(-(-n // tq) for n in cut) for cut in cuts)
+                assert items <= (lib.attn_varlen_plan_bytes(B, T, H, Hkv) - 256) // 16
