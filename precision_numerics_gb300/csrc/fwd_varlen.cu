@@ -560,6 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::col_s(t);
     const uint32_t tO = tmem + lane_off + C::col_o(t);
+    // The product m scale_log2 is rounded before the fma that takes it off, so that all weights of a
+    // row are off by 2^(half its last bit) together.  From 2^28 on that would leave the type (from
+    // 2^31), and any two scores lie 16 and more apart: a power of two in place of the scale, whose
+    // products are exact, then gives the same weights, all but 2^-16 of them.
+    const float scale_up = __uint_as_float((__float_as_uint(scale_log2) + 0x7FFFFFu) & 0x7F800000u);
     bool ok = !abort_all;
     int sc = 0;  // S_t tiles consumed so far (s_full phases)
     int oc = 0;  // items whose O_t was completed so far (o_done phases)
@@ -603,14 +608,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float m_new = fmaxf(fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]), m_run);
         const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-        const float neg_ms = -m_use * scale_log2;
+        const float unit = fabsf(m_use * scale_log2) < 0x1p28f ? scale_log2 : scale_up;
+        const float neg_ms = -m_use * unit;
         const float alpha = ex2((m_run - m_use) * scale_log2);
         s_alpha[t * 128 + r] = alpha;
         mbar_arrive(&bar_alpha[t * 4 + (warp & 3)]);  // the correction warp rescales O_t meanwhile
         uint64_t sums2[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) sums2[u] = 0ull;
-        const uint64_t c2 = f2_pack(scale_log2, scale_log2);
+        const uint64_t c2 = f2_pack(unit, unit);
         const uint64_t nm2 = f2_pack(neg_ms, neg_ms);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

@@ -5,7 +5,7 @@ import math
 import pytest
 
 import serving_ref as ref
-from test_serving_gpu import A, BF, Cache, ints, normal, scattered  # noqa: F401
+from test_serving_gpu import A, BF, Cache, ints, normal, scattered, sums  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -196,3 +196,34 @@ def test_status_of_several_calls_at_once(A):
         with pytest.raises(A.AttnError, match=r"varlen [1-9]\d*, cache [1-9]\d*, decode [1-9]"):
             A.attn_check_status()
         A.attn_check_status()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,d", [((4, 1), 64), ((2, 2), 128)])
+@pytest.mark.parametrize("lens", [[700], [300] * 40])
+@pytest.mark.parametrize("top", [2.0 ** 24 * 1.5625, 2.0 ** 28 * 1.40625, 2.0 ** 31 * 1.9375, 2.0 ** 33 * 1.0546875, 2.0 ** 60,
+                                 -(2.0 ** 34) * 1.15625])
+def test_prompt_scores_beyond_the_exponent(A, top, lens, heads, d, causal):
+    """Up to three keys of the same largest score far above all others, of the same value row: O is that row
+    and LSE the score plus the logarithm of the keys' number."""
+    H, Hkv = heads
+    T, cu = sum(lens), sums(lens)
+    q, k, v = torch.zeros((T, H, d), dtype=BF), torch.zeros((T, Hkv, d), dtype=BF), normal((T, Hkv, d), 3)
+    q[..., 0] = 2.0 ** 10
+    k[..., 0] = top * 2.0 ** -10 * (0.5 if top > 0 else 2.0)
+    row, seen = normal((Hkv, d), 4), torch.zeros(T)
+    for b, n in enumerate(lens):
+        for pos in (0, n // 2, n - 1):
+            k[cu[b] + pos, :, 0], v[cu[b] + pos] = top * 2.0 ** -10, row
+            seen[cu[b] + (pos if causal else 0):cu[b + 1]] += 1
+    plan = A.attn_varlen_plan(ints(cu), T, H, Hkv, causal=causal)
+    o, lse = A.attn_varlen_fwd(q.cuda(), k.cuda(), v.cuda(), plan, scale=1.0, causal=causal)
+    A.attn_check_status()
+    want = row.double().repeat_interleave(H // Hkv, 0)
+    # P is rounded to BF16 (2^-8), and so is O; 2^-18 for the FP32 sums, the exponential and the division.
+    assert ((o.cpu().double() - want).abs() <= (2.0 ** -7 + 2.0 ** -15) * want.abs()).all()
+    # In units of 2^-24 of the score: the maximum's product with log2 e, by which all weights of a row may be
+    # off together, log2 e itself, the maximum's product with the scale, the logarithm's sum, and ln 3 < 1.1
+    # beside 2^24; 2^-18 for the logarithm.
+    exact = top + torch.log(seen.double())[:, None]
+    assert ((lse.cpu().double() - exact).abs() <= 6 * 2.0 ** -24 * abs(top) + 2.0 ** -18).all()
