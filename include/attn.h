@@ -395,6 +395,9 @@ ATTN_API size_t attn_decode_int8_workspace_bytes(int B, int n_q, int H, int H_kv
  *   seqlens : int32 [B], device: positions each sequence holds, the newest n_q
  *             tokens' among them; at most max_blocks * page_size.
  *   o       : [B,n_q,H,d] BF16, contiguous.   lse : [B,n_q,H] FP32.
+ *   max_blocks : the room per sequence in the block table.  How the work is split over
+ *             the SMs follows from it and B: a table far wider than the histories
+ *             gives the same result, short ones a few microseconds later.
  *   workspace : device buffer, 256-byte aligned, that no concurrently running call
  *             uses (also not the replay of another graph); needs no initialisation.
  * The weights p_j vs_j of the codes (p the softmax) keep 11 bits down to 2^-20 of the

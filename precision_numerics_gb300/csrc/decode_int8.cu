@@ -6,14 +6,16 @@
 //   O   = sum_j softmax(s)_j (cv_j * vs_j),  LSE = ln sum_j exp(s_j)
 // with codes ck, cv and the scales ks, vs of position j's page and head.
 //
-// What bounds it: every code is read once and used for n_q * G rows, so the
-// bytes of the cache (2 d per position and head) over HBM's rate.  With so few
-// rows the tensor work is a small part of the time the bytes take; a 128-row
-// tcgen05 tile would be mostly padding.  The products are mma.sync m16n8k16
-// with the codes on the 16-row side, S^T = K Q^T and O^T = V^T P^T, and the query
-// rows of one key head on the 8-column side, NT blocks of 8: the conversion of a
-// code, which costs the most instructions, serves all of them, and few rows
-// leave little of a product empty.
+// What bounds it: up to 32 rows of a key head (n_q * G) use every code that is
+// read, so with few rows the bytes of the cache (2 d per position and head) over
+// HBM's rate, which leave the tensor pipe mostly idle.  The products are mma.sync
+// m16n8k16 with the codes on the 16-row side, S^T = K Q^T and O^T = V^T P^T, and the
+// query rows of one key head on the 8-column side, NT blocks of 8: the conversion of
+// a code, which costs the most instructions, serves all of them, and few rows leave
+// little of a product empty.  From 17 rows on the accumulators' registers leave 8
+// warps an SM, and the chain of a tile bounds it instead; tcgen05 with 128 positions
+// of codes on its rows and the accumulators in TMEM would not have that limit, and is
+// not built.  More than 32 rows take a pass over the keys for every 32.
 //
 // Codes become FP16 exactly (|c| <= 127): the byte c + 128 under the exponent
 // of 1024 is the FP16 number 1152 + c.  Q becomes FP16 after division by a
@@ -37,8 +39,11 @@
 // merged through shared memory once at the end of a segment, the tiles of one
 // (sequence, key head, row block) that the CTA has.
 //
-// Short sequences have a CTA for every segment.  Where the segments are fewer than the
-// CTAs that the SMs hold, and not too long, a cluster of CTAs shares one and joins its
+// Which way the work is split follows from the room in the block table, not from the
+// lengths, which are device data: 77 positions take 4.2 us in a table that is as wide
+// as they need and 6.9 in one of 2048 blocks.  In a table for short sequences a CTA
+// takes every segment.  Where the segments are fewer than the CTAs that the SMs hold,
+// and not too long, a cluster of CTAs shares one and joins its
 // parts through their shared memory.  Else the tiles of all segments, one behind the
 // other, are dealt to the CTAs in equal runs, so that ragged lengths and few sequences
 // keep every SM busy alike.  A run that holds a whole segment writes its output; of a
@@ -48,10 +53,10 @@
 // values up to the largest that a scale allows do not overflow on the way.
 //
 // Measured (d = 128, 8 key heads, pages of 64): 64 sequences of 500 to 16000
-// positions with 4 query rows a key head 102-104 us (5.9 TB/s, 87% of a copy's
-// rate), one of 131000 positions 50 us (5.4 TB/s); d = 64: 57 us and 30 us; with 20
-// rows 64 sequences 153 us: the accumulators then leave 8 warps an SM, and the
-// dependent conversions and products of a tile (2 us a warp) set the pace.
+// positions with 4 query rows a key head 102-105 us (5.9 TB/s, 86% of a copy's
+// rate), one of 131000 positions 50 us (5.4 TB/s); d = 64: 58 us and 30 us; with 20
+// rows 64 sequences 142 us, where the dependent conversions and products of a tile (2
+// us a warp) set the pace; 8 sequences of 4000 positions with 256 rows 148 us.
 #include <float.h>
 #include <math.h>
 #include <stdint.h>
