@@ -783,7 +783,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                 for (int off = 4; off < 32; off <<= 1) p = fmaxf(p, __shfl_xor_sync(0xffffffffu, p, off));
                 w = fmaxf(w, __log2f(p) + lv[h]);
               }
-              back[n][i] *= ex2(whole(w_old) - whole(w));
+              // At most 2^127 unless back is 0, and finite then too: a row that has seen nothing, or
+              // nothing of a p above 2^-126, has no W to come from.
+              back[n][i] *= ex2(fminf(whole(w_old) - whole(w), 127.f));
               const float up = exp2_whole<142, -1>(w);  // 2^(15 - W)
 #pragma unroll
               for (int h = 0; h < 2; ++h) s[h][n][i] *= up, s[h][n][2 + i] *= up;

@@ -227,3 +227,48 @@ def test_prompt_scores_beyond_the_exponent(A, top, lens, heads, d, causal):
     # beside 2^24; 2^-18 for the logarithm.
     exact = top + torch.log(seen.double())[:, None]
     assert ((lse.cpu().double() - exact).abs() <= 6 * 2.0 ** -24 * abs(top) + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 2)])
+@pytest.mark.parametrize("page,lens", [(32, [300, 470]), (16, [2000, 280]), (64, [9000, 290])])
+@pytest.mark.parametrize("big,small", [(40, -10), (-10, 40), (100, -100)])
+def test_decode_rows_that_see_nothing_of_a_warp(A, big, small, page, lens, d, G):
+    """256 newest tokens: a warp has tiles of which the first ones see nothing, and the value scales of
+    these differ by 2^50 and more."""
+    Hkv, n_q = 1, 256
+    tables, pages = scattered([-(-n // page) for n in lens], 7)
+    c = Cache(pages, Hkv, page, d, tables)
+    for t in tables:
+        for j, p in enumerate(t):
+            c.scales[1][p] *= 2.0 ** (big if j * page // 128 % 2 == 0 else small)
+    c.upload()
+    q = normal((2, n_q, Hkv * G, d), 1)
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens))
+    A.attn_check_status()
+    check_weighted(c, q, lens, 1 / math.sqrt(d), o, lse)
+
+
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 4)])
+@pytest.mark.parametrize("jump", [100.0, 150.0])
+@pytest.mark.parametrize("big", [40, 100])
+def test_decode_maximum_that_leaps(A, big, jump, d, G):
+    """The score's maximum leaps by more or less than FP32's exponents hold where the value scale falls by
+    2^60 to 2^200: what was summed before counts as long as its weights do."""
+    Hkv, page, lens = 1, 32, [500, 1500]
+    tables, pages = scattered([-(-n // page) for n in lens], 7)
+    c = Cache(pages, Hkv, page, d, tables)
+    c.codes[0][..., 0] = 0
+    c.scales[0][:] = 0.01
+    for t in tables:
+        for j, p in enumerate(t):
+            c.scales[1][p] *= 2.0 ** (big if j < 4 else -20 if big == 40 else -100)
+            if j >= 4:
+                c.codes[0][p, ..., 0] = 100
+    c.upload()
+    q = normal((2, 1, Hkv * G, d), 1)
+    q[..., 0] = jump  # times 100 * 0.01
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens), scale=math.log(2.0))
+    A.attn_check_status()
+    assert o.isfinite().all()
+    if jump < 126 or big == 40:  # else weights of p < 2^-126, which count as 0, would matter
+        check_weighted(c, q, lens, math.log(2.0), o, lse)
