@@ -402,8 +402,8 @@ ATTN_API size_t attn_decode_int8_workspace_bytes(int B, int n_q, int H, int H_kv
  *             uses (also not the replay of another graph); needs no initialisation.
  * The weights p_j vs_j of the codes (p the softmax) keep 11 bits down to 2^-20 of the
  * row's largest weight; below that they are off by at most 2^-31 of it, whatever the
- * scales of pages that the row does not see or barely weighs.  A p below 2^-126 of
- * the row's largest counts as 0.
+ * scales of pages that the row does not see or barely weighs.  A p below 2^-126
+ * counts as 0 or loses bits.
  * Scales must be >= 0 and finite.  A position whose page number is out of range
  * is not seen.
  */

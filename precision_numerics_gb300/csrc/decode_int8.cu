@@ -996,13 +996,12 @@ __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_k
   const int rr = ch.z % a.row_blocks * rows + r;
   const bool have = r < rows && rr < a.n_q * a.G;
   const int n = have ? ch.x + 1 : 0;
-  // l, at most 1 a key of less than 2^31, becomes a weight below 1.
-  constexpr float kShare = 0x1p-31f;
-  // kBatch parts at a time, all their loads in flight together.
+  // O is kept as the mean of the parts so far, whose weights are at most 1.  kBatch parts
+  // at a time, all their loads in flight together.
   constexpr int kBatch = kJoinBatch;
   float M = -INFINITY, L = 0.f, o[D / 32] = {};
   for (int i0 = warp % per_row; i0 < n; i0 += kBatch * per_row) {
-    float m[kBatch], l[kBatch], x[kBatch][D / 32];  // l times kShare
+    float m[kBatch], l[kBatch], x[kBatch][D / 32];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * per_row;
@@ -1012,7 +1011,7 @@ __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_k
       if (i < n) {
         const float* p = a.parts + (size_t)(2 * (ch.w + i) + (i == 0)) * part_floats(D, rows);
         m[k] = __ldcg(p + rows * D + r);
-        l[k] = __ldcg(p + rows * D + rows + r) * kShare;
+        l[k] = __ldcg(p + rows * D + rows + r);
         const float* q = p + r * D + lane * (D / 32);
         if constexpr (D == 128) {
           const float4 v = __ldcg(reinterpret_cast<const float4*>(q));
@@ -1027,17 +1026,18 @@ __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_k
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) m_new = fmaxf(m_new, m[k]);
     const float m_use = m_new == -INFINITY ? 0.f : m_new;
-    const float keep = ex2(M - m_use);
+    const float before = L * ex2(M - m_use);
     M = m_new;
-    L *= keep;
+    L = before;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] *= keep;
+    for (int k = 0; k < kBatch; ++k) L += l[k] *= ex2(m[k] - m_use);
+    const float inv = inverse(L);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] *= before * inv;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const float f = ex2(m[k] - m_use) * l[k];
-      L += f;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] += f * x[k][e];
+      for (int e = 0; e < D / 32; ++e) o[e] += l[k] * inv * x[k][e];
     }
   }
   if constexpr (SHARED) {
@@ -1053,22 +1053,23 @@ __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_k
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
 #pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) L += s_l[w] * ex2(s_m[w] - m_use);
+    const float inv = inverse(L);
+#pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-      const float f = ex2(s_m[w] - m_use);
-      L += f * s_l[w];
+      const float f = s_l[w] * ex2(s_m[w] - m_use) * inv;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) o[e] += f * s_o[w][lane * (D / 32) + e];
     }
   }
   if (!have) return;
   const size_t row = out_row(a, ch.y, ch.z / a.row_blocks, rr);
-  const float inv = inverse(L);
   uint16_t* out = a.o + row * D + lane * (D / 32);
   if constexpr (D == 128)
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
   else
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0] * inv, o[1] * inv);
-  if (lane == 0) a.lse[row] = lse_of(M, L * (1.f / kShare));
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0], o[1]);
+  if (lane == 0) a.lse[row] = lse_of(M, L);
 }
 
 // Runs the tiles are dealt in: the CTAs that the SMs hold at a time.  (The full

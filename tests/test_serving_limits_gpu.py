@@ -272,3 +272,26 @@ def test_decode_maximum_that_leaps(A, big, jump, d, G):
     assert o.isfinite().all()
     if jump < 126 or big == 40:  # else weights of p < 2^-126, which count as 0, would matter
         check_weighted(c, q, lens, math.log(2.0), o, lse)
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 4), (128, 4), (128, 20)])
+@pytest.mark.parametrize("lens", [[500, 200], [1500, 300], [9000, 2000], [3000] * 40])
+def test_decode_small_weights_of_large_values(A, lens, d, G):
+    """The first 128 positions have weights of about 2^-118 of the row's largest and value scales 2^140 times
+    the others': O is theirs, whichever way warps and parts are joined."""
+    Hkv, page = 1, 32
+    tables, pages = scattered([-(-n // page) for n in lens], 7)
+    c = Cache(pages, Hkv, page, d, tables)
+    c.codes[0][..., 0] = 0
+    c.scales[0][:] = 0.002
+    for t in tables:
+        for j, p in enumerate(t):
+            c.scales[1][p] *= 2.0 ** (100 if j < 4 else -40)
+            if j >= 4:
+                c.codes[0][p, ..., 0] = 100
+    c.upload()
+    q = normal((len(lens), 1, Hkv * G, d), 1)
+    q[..., 0] = 592.0  # 100 * 0.002 * 592 = 118.4
+    o, lse = A.attn_decode_int8(q.cuda(), *c.gpu, ints(lens), scale=math.log(2.0))
+    A.attn_check_status()
+    check_weighted(c, q[:3], lens[:3], math.log(2.0), o[:3], lse[:3])
