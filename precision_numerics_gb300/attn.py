@@ -473,7 +473,9 @@ def attn_varlen_plan_bytes(B: int, T: int, H: int, H_kv: int) -> int:
 
 def attn_varlen_plan(cu_seqlens, T, H, H_kv, causal=True, plan=None, stream=None):
     """The work list of attn_varlen_fwd for a packed batch: cu_seqlens int32 [B+1] on
-    the device.  Returns a uint8 tensor that serves every call on the same batch."""
+    the device.  Returns a uint8 tensor that serves every call on the same batch.  A plan
+    passed in has attn_varlen_plan_bytes(B, T, H, H_kv) bytes: attn_varlen_fwd takes B from
+    its size, and in a larger one splits fewer long prompts over an SM's two tiles."""
     _check_ints("cu_seqlens", cu_seqlens)
     B = cu_seqlens.shape[0] - 1
     if plan is None:
