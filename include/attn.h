@@ -416,6 +416,77 @@ ATTN_API attn_status attn_decode_int8(const void* q, long long q_batch_stride,
                                       float scale, void* workspace, size_t workspace_bytes,
                                       cudaStream_t stream);
 
+/* Bytes of device workspace attn_decode_shared_int8 needs (0 on invalid arguments). */
+ATTN_API size_t attn_decode_shared_int8_workspace_bytes(int B, int n_q, int H, int H_kv, int d,
+                                                        int page_size, int prefix_blocks,
+                                                        int max_blocks);
+
+/*
+ * attn_decode_int8 for a batch whose sequences all begin with the same prefix_len
+ * positions, which the cache holds once: token i of a sequence's newest n_q sees the
+ * whole prefix and its own positions j <= seqlens[b] - n_q + i.  The prefix's codes
+ * are read once for up to 256 of a key head's B * n_q * H / H_kv query rows.
+ *   prefix_table  : int32 [prefix_blocks], device: the prefix's pages; position t is
+ *                   row t % page_size of page prefix_table[t / page_size].
+ *   prefix_len    : int32 [1], device: 0 to prefix_blocks * page_size.
+ *   block_table   : int32 [B, max_blocks]: the pages of each sequence's own positions,
+ *                   which are counted from 0 behind the prefix (the first of them begins a
+ *                   page, also where the prefix ends inside one).
+ *   seqlens       : int32 [B]: own positions, the newest n_q tokens' among them.  A sequence
+ *                   may have fewer than n_q, or none: its tokens then see the prefix alone.
+ *   workspace     : device buffer, 256-byte aligned, that no concurrently running call
+ *                   uses (also not the replay of another graph); needs no initialisation.
+ * q, o, lse and the cache as for attn_decode_int8, and so is the weights' precision, with
+ * 11 bits down to 2^-20 of a row's largest weight in the prefix, or in the own positions.  A
+ * row that sees no position gets O = 0, LSE = -inf.  The same call gives the same bits.
+ */
+ATTN_API attn_status attn_decode_shared_int8(
+    const void* q, long long q_batch_stride, long long q_token_stride, long long q_head_stride,
+    const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+    const int* prefix_table, int prefix_blocks, const int* prefix_len, const int* block_table,
+    const int* seqlens, void* o, float* lse, int B, int n_q, int H, int H_kv, int d, int num_pages,
+    int page_size, int max_blocks, float scale, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream);
+
+/*
+ * Block tables, offsets and slots of a step from the requests' lengths.  Sequence b holds
+ * held[b] positions, whose pages are the first ceil(held[b] / page_size) of its row of the
+ * table, and is to hold wanted[b]: more (new tokens), fewer (rejected drafts), none (it has
+ * ended).  Pages that are held no longer go to the stack of free pages, then those that are
+ * needed are taken from it, both in the order of the sequences and of their positions:
+ *   - released pages are put at free_pages[n_free], free_pages[n_free + 1], ..., and their
+ *     entries in the table become -1;
+ *   - requests are served in their order for as long as the stack has the pages they need
+ *     together; one that needs none is always served.  Those that are served take the topmost
+ *     pages, the last one the topmost.  The entries that a request which is not served would
+ *     have needed become -1, and it holds what it held.
+ * So the reverse call (held = lens, wanted = the old held) takes a step back, table and stack
+ * and all.
+ *   block_table : int32 [B, max_blocks], device, updated.
+ *   held, wanted: int32 [B], device, 0 to max_blocks * page_size.  A sequence with another
+ *                 value is left as it is (lens = held, no tokens) and reported.
+ *   free_pages  : int32 [num_pages], device, updated; entries from n_free on are free room.
+ *   n_free      : int32 [1], device, updated.  Pages that the stack has no room for (more than
+ *                 num_pages: some were given back twice) are dropped and reported; a number
+ *                 out of range, in a table or in the stack, becomes -1 and is reported.
+ *   lens        : int32 [B], written: wanted[b], or held[b] where the request was not served.
+ *   cu_seqlens  : int32 [B+1], written: offsets of the packed new tokens, max(wanted - held, 0)
+ *                 of every sequence, served or not.
+ *   slots       : int32 [T], written: row block_table[..] * page_size + position % page_size of
+ *                 the pool for each new token; -1 where its request was not served, and behind
+ *                 the last token.
+ *   positions   : int32 [T], written: each new token's position in its sequence; -1 behind the
+ *                 last token.  More new tokens than T are reported, and the first T written.
+ * num_pages * page_size < 2^31.  lens, cu_seqlens, slots and positions, and what is updated, overlap
+ * nothing.  attn_cache_append_int8 takes cu_seqlens and held (as starts) for the new rows, and
+ * attn_decode_int8 takes lens.  The rows of a request that was not served still go into the room that its
+ * last page has if they are appended, unseen but counted into that page's scales.
+ */
+ATTN_API attn_status attn_cache_reserve(int* block_table, const int* held, const int* wanted,
+                                        int* free_pages, int* n_free, int* lens, int* cu_seqlens,
+                                        int* slots, int* positions, int B, int T, int num_pages,
+                                        int page_size, int max_blocks, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ from .attn import (AttnError, attn_bwd, attn_bwd_dq_convert, attn_bwd_main,  # n
                    attn_selftest_wait_timeout, attn_version, load_library,
                    attn_varlen_plan, attn_varlen_plan_bytes, attn_varlen_fwd,
                    attn_cache_append_int8, attn_cache_read_int8, attn_decode_int8,
-                   attn_decode_int8_workspace_bytes)
+                   attn_decode_int8_workspace_bytes, attn_decode_shared_int8,
+                   attn_decode_shared_int8_workspace_bytes, attn_cache_reserve)
 
 __all__ = ["AttnError", "attn_fwd", "attn_fwd_stable", "attn_quantize_int8", "attn_fwd_int8",
            "attn_quantize_int8_as_bf16", "attn_fwd_int8_as_bf16", "int8_scale_rows",
@@ -19,4 +20,5 @@ __all__ = ["AttnError", "attn_fwd", "attn_fwd_stable", "attn_quantize_int8", "at
            "attn_selftest_wait_timeout", "attn_version", "load_library",
            "attn_varlen_plan", "attn_varlen_plan_bytes", "attn_varlen_fwd",
            "attn_cache_append_int8", "attn_cache_read_int8", "attn_decode_int8",
-           "attn_decode_int8_workspace_bytes"]
+           "attn_decode_int8_workspace_bytes", "attn_decode_shared_int8",
+           "attn_decode_shared_int8_workspace_bytes", "attn_cache_reserve"]

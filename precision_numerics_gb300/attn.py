@@ -33,7 +33,8 @@ EXPORTED = ("attn_version", "attn_status_string", "attn_last_error", "attn_fwd",
             "attn_quantize_int8_as_bf16", "attn_fwd_int8_as_bf16",
             "attn_varlen_plan_bytes", "attn_varlen_plan", "attn_varlen_fwd",
             "attn_cache_append_int8", "attn_cache_read_int8",
-            "attn_decode_int8_workspace_bytes", "attn_decode_int8")
+            "attn_decode_int8_workspace_bytes", "attn_decode_int8",
+            "attn_decode_shared_int8_workspace_bytes", "attn_decode_shared_int8", "attn_cache_reserve")
 
 
 class AttnError(RuntimeError):
@@ -72,6 +73,10 @@ _SIGNATURES = {
     "attn_cache_read_int8": (_i, [_vp] * 9 + [_i] * 8 + [_vp]),
     "attn_decode_int8_workspace_bytes": (_sz, [_i] * 7),
     "attn_decode_int8": (_i, [_vp] + [_ll] * 3 + [_vp] * 8 + [_i] * 8 + [_f, _vp, _sz, _vp]),
+    "attn_decode_shared_int8_workspace_bytes": (_sz, [_i] * 8),
+    "attn_decode_shared_int8": (_i, [_vp] + [_ll] * 3 + [_vp] * 5 + [_i] + [_vp] * 5 + [_i] * 8
+                                + [_f, _vp, _sz, _vp]),
+    "attn_cache_reserve": (_i, [_vp] * 9 + [_i] * 5 + [_vp]),
 }
 
 
@@ -100,7 +105,7 @@ _BINDING = None
 class _NoBinding:
     """Takes no call: every one goes on to the checks and the ctypes call that follow."""
 
-    varlen_fwd = cache_append = cache_read = decode = staticmethod(lambda *args: None)
+    varlen_fwd = cache_append = cache_read = decode = decode_shared = cache_reserve = staticmethod(lambda *args: None)
 
 
 def _binding():
@@ -614,3 +619,78 @@ def attn_decode_int8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens
           seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, n_q, H, hk, d, pages, page, blocks,
           _default_scale(d, scale), workspace.data_ptr(), _nbytes(workspace), _stream(stream))
     return o, lse
+
+
+def attn_decode_shared_int8_workspace_bytes(B: int, n_q: int, H: int, H_kv: int, d: int, page_size: int,
+                                            prefix_blocks: int, max_blocks: int) -> int:
+    return int(load_library().attn_decode_shared_int8_workspace_bytes(B, n_q, H, H_kv, d, page_size, prefix_blocks,
+                                                                      max_blocks))
+
+
+def attn_decode_shared_int8(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len, block_table, seqlens,
+                            scale=None, o=None, lse=None, workspace=None, stream=None):
+    """attn_decode_int8 for a batch that shares a prefix: pages prefix_table int32 [blocks] of
+    prefix_len int32 [1] positions, then each sequence's own pages and positions (block_table,
+    seqlens).  Returns (o [B,n_q,H,d], lse [B,n_q,H])."""
+    if stream is None:
+        done = (_BINDING or _binding()).decode_shared(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len,
+                                                      block_table, seqlens, scale, o, lse, workspace)
+        if done is not None:
+            return done
+    B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a tensor [B, n_q, H, d]")
+    n_q, H = q.shape[1], q.shape[2]
+    _check_rows("q", q, (B, n_q, H, d))
+    _check_ints("prefix_table", prefix_table)
+    _check_ints("prefix_len", prefix_len, 1)
+    _check_ints("seqlens", seqlens, B)
+    if o is None:
+        o = _empty((B, n_q, H, d), q.dtype, q.device, stream)
+    else:
+        _check_dense("o", o, (B, n_q, H, d), torch.bfloat16)
+    if lse is None:
+        lse = _empty((B, n_q, H), torch.float32, q.device, stream)
+    else:
+        _check_dense("lse", lse, (B, n_q, H), torch.float32)
+    if workspace is None:
+        need = attn_decode_shared_int8_workspace_bytes(B, n_q, H, hk, d, page, prefix_table.shape[0], blocks)
+        workspace = _empty(max(need, 1), torch.uint8, q.device, stream)
+    _call("attn_decode_shared_int8", q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), prefix_table.data_ptr(), prefix_table.shape[0],
+          prefix_len.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, n_q, H,
+          hk, d, pages, page, blocks, _default_scale(d, scale), workspace.data_ptr(), _nbytes(workspace),
+          _stream(stream))
+    return o, lse
+
+
+def attn_cache_reserve(block_table, held, wanted, free_pages, n_free, page_size, T, lens=None, cu_seqlens=None,
+                       slots=None, positions=None, stream=None):
+    """Take the sequences from held to wanted positions (int32 [B]): pages move between block_table
+    [B,max_blocks] and the stack free_pages [pages] of n_free [1] entries, all int32 and updated.  Returns
+    (lens [B], cu_seqlens [B+1], slots [T], positions [T]) of the step's new tokens, T at most."""
+    if stream is None:
+        done = (_BINDING or _binding()).cache_reserve(block_table, held, wanted, free_pages, n_free, page_size, T, lens,
+                                                      cu_seqlens, slots, positions)
+        if done is not None:
+            return done
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [B, max_blocks]")
+    B, blocks = block_table.shape
+    _check_dense("block_table", block_table, (B, blocks), torch.int32)
+    _check_ints("held", held, B)
+    _check_ints("wanted", wanted, B)
+    _check_ints("free_pages", free_pages)
+    _check_ints("n_free", n_free, 1)
+    outs = []
+    for name, t, n in (("lens", lens, B), ("cu_seqlens", cu_seqlens, B + 1), ("slots", slots, T),
+                       ("positions", positions, T)):
+        if t is None:
+            t = _empty((n,), torch.int32, block_table.device, stream)
+        else:
+            _check_ints(name, t, n)
+        outs.append(t)
+    _call("attn_cache_reserve", block_table.data_ptr(), held.data_ptr(), wanted.data_ptr(), free_pages.data_ptr(),
+          n_free.data_ptr(), *(t.data_ptr() for t in outs), B, T, free_pages.shape[0], page_size, blocks,
+          _stream(stream))
+    return tuple(outs)

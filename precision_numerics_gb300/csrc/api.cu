@@ -424,9 +424,10 @@ attn_status attn_check_status(cudaStream_t stream) {
   cudaError_t err = cudaStreamSynchronize(stream);
   if (err != cudaSuccess) return cuda_fail(err, "attn_check_status: stream");
   // Every word is read, and cleared where something was set, before any is reported.
-  constexpr int kWords = 6;
-  cudaError_t (*const address[kWords])(void**) = {status_word_fwd,    status_word_bwd,   status_word_misc,
-                                                  status_word_varlen, status_word_cache, status_word_decode};
+  constexpr int kWords = 8;
+  cudaError_t (*const address[kWords])(void**) = {status_word_fwd,    status_word_bwd,    status_word_misc,
+                                                  status_word_varlen, status_word_cache,  status_word_decode,
+                                                  status_word_shared, status_word_tables};
   void* at[kWords];
   unsigned int word[kWords] = {};
   for (int i = 0; i < kWords && err == cudaSuccess; ++i) {
@@ -442,18 +443,19 @@ attn_status attn_check_status(cudaStream_t stream) {
     }
   if (set && err == cudaSuccess) err = cudaStreamSynchronize(stream);
   if (err != cudaSuccess) return cuda_fail(err, "attn_check_status: status read");
-  const unsigned int a = word[0], b = word[1], c = word[2], prompt = word[3], cache = word[4], decode = word[5];
-  const unsigned int any = a | b | c, serving = prompt | cache | decode;
+  const unsigned int a = word[0], b = word[1], c = word[2], prompt = word[3], cache = word[4], decode = word[5],
+                     shared = word[6], tables = word[7];
+  const unsigned int any = a | b | c, serving = prompt | cache | decode | shared | tables;
   if ((any | serving) & ATTN_ERR_TIMEOUT)
-    return fail(ATTN_ERR_TIMEOUT, "a kernel gave up on a bounded wait (status %u/%u/%u/%u/%u/%u)", a,
-                b, c, prompt, cache, decode);
+    return fail(ATTN_ERR_TIMEOUT, "a kernel gave up on a bounded wait (status %u/%u/%u/%u/%u/%u/%u/%u)", a,
+                b, c, prompt, cache, decode, shared, tables);
   if (any != 0)
     return fail(ATTN_ERR_INVALID_ARG, "a kernel reported a bad launch setup (status %u/%u/%u)", a,
                 b, c);
   if (serving != 0)
     return fail(ATTN_ERR_INVALID_ARG,
                 "a kernel met a length, page number or plan out of range in device memory (varlen %u, "
-                "cache %u, decode %u)", prompt, cache, decode);
+                "cache %u, decode %u, prefix %u, tables %u)", prompt, cache, decode, shared, tables);
   t_last_error.clear();
   return ATTN_OK;
 }

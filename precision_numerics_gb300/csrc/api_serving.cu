@@ -1,6 +1,6 @@
 // C-ABI entry points of the serving operators: argument validation and
-// dispatch for attention over packed sequences, the paged INT8 cache, and
-// attention over that cache.
+// dispatch for attention over packed sequences, the paged INT8 cache and its
+// block tables, and attention over that cache.
 #include <limits.h>
 #include <math.h>
 
@@ -82,6 +82,30 @@ attn_status check_decode(int B, int n_q, int H, int H_kv, int d) {
     return fail(n_q < 1 ? ATTN_ERR_INVALID_ARG : ATTN_ERR_UNSUPPORTED, "n_q = %d is not supported (1 to 256)", n_q);
   if ((long long)B * n_q * H > INT_MAX)
     return fail(ATTN_ERR_INVALID_ARG, "B * n_q * H = %lld exceeds 2^31 - 1", (long long)B * n_q * H);
+  return ATTN_OK;
+}
+
+attn_status check_shared(int B, int n_q, int H, int H_kv, int d, int page_size, int prefix_blocks, int max_blocks) {
+  ATTN_CHECK(check_decode(B, n_q, H, H_kv, d));
+  ATTN_CHECK(check_pages(H_kv, d, 1, page_size, max_blocks));
+  if ((long long)B * n_q * H > INT_MAX - 1024)
+    return fail(ATTN_ERR_UNSUPPORTED, "B * n_q * H = %lld is not supported", (long long)B * n_q * H);
+  if (prefix_blocks < 1) return fail(ATTN_ERR_INVALID_ARG, "prefix_blocks must be >= 1 (got %d)", prefix_blocks);
+  if (prefix_blocks > (INT_MAX - 4096) / page_size)
+    return fail(ATTN_ERR_UNSUPPORTED, "prefix_blocks * page_size exceeds 2^31 positions");
+  return ATTN_OK;
+}
+
+// An int32 array of one call.
+struct Ints {
+  const char* name;
+  const int* p;
+  long long n;
+};
+attn_status check_apart(const Ints& x, const Ints& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  if (a != 0 && b != 0 && x.n > 0 && y.n > 0 && a < b + 4 * (uintptr_t)y.n && b < a + 4 * (uintptr_t)x.n)
+    return fail(ATTN_ERR_INVALID_ARG, "%s and %s overlap", x.name, y.name);
   return ATTN_OK;
 }
 
@@ -219,6 +243,75 @@ attn_status attn_decode_int8(const void* q, long long q_batch_stride, long long 
   const long long strides[3] = {q_batch_stride, q_token_stride, q_head_stride};
   return launched(launch_decode_int8(c, q, strides, seqlens, o, lse, n_q, H, scale, workspace, stream),
                   "attn_decode_int8");
+}
+
+size_t attn_decode_shared_int8_workspace_bytes(int B, int n_q, int H, int H_kv, int d, int page_size,
+                                               int prefix_blocks, int max_blocks) {
+  if (check_shared(B, n_q, H, H_kv, d, page_size, prefix_blocks, max_blocks) != ATTN_OK) return 0;
+  PagedCache c = {nullptr, nullptr, nullptr, nullptr, nullptr, B, H_kv, d, 1, page_size, max_blocks};
+  return decode_shared_workspace_bytes(c, n_q, H);
+}
+
+attn_status attn_decode_shared_int8(const void* q, long long q_batch_stride, long long q_token_stride,
+                                    long long q_head_stride, const void* k_cache, const void* v_cache,
+                                    const float* k_scale, const float* v_scale, const int* prefix_table,
+                                    int prefix_blocks, const int* prefix_len, const int* block_table,
+                                    const int* seqlens, void* o, float* lse, int B, int n_q, int H, int H_kv, int d,
+                                    int num_pages, int page_size, int max_blocks, float scale, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  PagedCache c;
+  PtrCheck ptr;
+  ATTN_CHECK(check_shared(B, n_q, H, H_kv, d, page_size, prefix_blocks, max_blocks));
+  ATTN_CHECK(check_scale(scale));
+  ATTN_CHECK(check_stride(q_batch_stride, "q_batch_stride"));
+  ATTN_CHECK(check_stride(q_token_stride, "q_token_stride"));
+  ATTN_CHECK(check_stride(q_head_stride, "q_head_stride"));
+  ATTN_CHECK(check_cache(k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, d, num_pages, page_size,
+                         max_blocks, ptr, &c));
+  ATTN_CHECK(ptr(q, "q"));
+  ATTN_CHECK(ptr(prefix_table, "prefix_table", 4));
+  ATTN_CHECK(ptr(prefix_len, "prefix_len", 4));
+  ATTN_CHECK(ptr(seqlens, "seqlens", 4));
+  ATTN_CHECK(ptr(o, "o"));
+  ATTN_CHECK(ptr(lse, "lse", 4));
+  const size_t need = decode_shared_workspace_bytes(c, n_q, H);
+  if (workspace_bytes < need)
+    return fail(ATTN_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  ATTN_CHECK(ptr(workspace, "workspace", 256));
+  if (encode_tiled_fn() == nullptr)
+    return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  const long long strides[3] = {q_batch_stride, q_token_stride, q_head_stride};
+  return launched(launch_decode_shared_int8(c, q, strides, prefix_table, prefix_blocks, prefix_len, seqlens, o, lse,
+                                            n_q, H, scale, workspace, stream),
+                  "attn_decode_shared_int8");
+}
+
+attn_status attn_cache_reserve(int* block_table, const int* held, const int* wanted, int* free_pages, int* n_free,
+                               int* lens, int* cu_seqlens, int* slots, int* positions, int B, int T, int num_pages,
+                               int page_size, int max_blocks, cudaStream_t stream) {
+  PtrCheck ptr;
+  ATTN_CHECK(check_packed(B, T));
+  ATTN_CHECK(check_pages(1, 64, num_pages, page_size, max_blocks));
+  if (T > INT_MAX - 4096) return fail(ATTN_ERR_INVALID_ARG, "T = %d is too large", T);
+  const Ints ins[5] = {{"block_table", block_table, (long long)B * max_blocks}, {"free_pages", free_pages, num_pages},
+                       {"n_free", n_free, 1},                                   {"held", held, B},
+                       {"wanted", wanted, B}};
+  const Ints outs[4] = {{"lens", lens, B}, {"cu_seqlens", cu_seqlens, B + 1ll}, {"slots", slots, T},
+                        {"positions", positions, T}};
+  // Every array that is written is apart from all others.
+  for (int i = 0; i < 4; ++i) {
+    for (const Ints& y : ins) ATTN_CHECK(check_apart(outs[i], y));
+    for (int j = 0; j < i; ++j) ATTN_CHECK(check_apart(outs[i], outs[j]));
+  }
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 5; ++j) ATTN_CHECK(check_apart(ins[i], ins[j]));
+  for (const Ints& x : ins) ATTN_CHECK(ptr(x.p, x.name, 4));
+  for (const Ints& x : outs)
+    if (x.n > 0) ATTN_CHECK(ptr(x.p, x.name, 4));
+  const Tables t = {block_table, held,       wanted, free_pages, n_free,    lens,
+                    cu_seqlens,  slots,      positions, B,       T,         num_pages,
+                    page_shift(page_size), max_blocks};
+  return launched(launch_cache_reserve(t, stream), "attn_cache_reserve");
 }
 
 }  // extern "C"

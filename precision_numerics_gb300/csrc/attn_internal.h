@@ -143,11 +143,27 @@ cudaError_t launch_cache_append_int8(const PagedCache& c, const void* k, const v
                                      int T, cudaStream_t stream);
 cudaError_t launch_cache_read_int8(const PagedCache& c, const int* cu, const int* starts, void* k,
                                    void* v, int T, bool fp32, cudaStream_t stream);
-// strides: batch, token and head stride of q (elements).
+// strides: batch, token and head stride of q (elements).  whole: FP32 means, maxima and sums in place
+// of o and lse (decode_int8.cu).
 size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H);
 cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides,
                                const int* lens, void* o, float* lse, int n_q, int H, float scale,
-                               void* workspace, cudaStream_t stream);
+                               void* workspace, cudaStream_t stream, float* whole = nullptr);
+// The same over a prefix that all sequences share and each one's own positions (c.table, lens).
+size_t decode_shared_workspace_bytes(const PagedCache& c, int n_q, int H);
+cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const long long* strides,
+                                      const int* prefix_table, int prefix_blocks, const int* prefix_len,
+                                      const int* lens, void* o, float* lse, int n_q, int H, float scale,
+                                      void* workspace, cudaStream_t stream);
+
+// Pages moved between the block table and the stack of free pages (csrc/cache_tables.cu).
+struct Tables {
+  int* table;
+  const int *held, *wanted;
+  int *free_pages, *n_free, *lens, *cu, *slots, *positions;
+  int B, T, P, page_shift, max_blocks;
+};
+cudaError_t launch_cache_reserve(const Tables& t, cudaStream_t stream);
 
 // Attention over packed sequences (csrc/fwd_varlen.cu).
 struct VarlenProblem {
@@ -168,6 +184,8 @@ cudaError_t status_word_misc(void** word);
 cudaError_t status_word_varlen(void** word);
 cudaError_t status_word_cache(void** word);
 cudaError_t status_word_decode(void** word);
+cudaError_t status_word_shared(void** word);
+cudaError_t status_word_tables(void** word);
 
 // Shape and scalar checks shared by every entry point (d, N, B*H*N*d, dtype,
 // and the scale when need_scale); fills *out and records the error detail.

@@ -257,6 +257,10 @@ struct Args {
   Chain* chains;
   int by_segment;
   unsigned cluster;  // without split mode: CTAs that share a segment
+  // In place of o and lse (else null): O / l [rows][D], m [rows], l [rows], FP32, of all B n_q H
+  // rows, for a caller that joins them with others.
+  float* whole;
+  size_t whole_rows;
 };
 
 // A part in the workspace: O [rows][D] divided by l, m [rows], l [rows], FP32.
@@ -269,6 +273,24 @@ __device__ __forceinline__ int token_of(const Args& a, int r) {
 __device__ __forceinline__ size_t out_row(const Args& a, int b, int h, int r) {
   const int t = token_of(a, r);
   return ((size_t)b * a.n_q + t) * a.H + h * a.G + (r - t * a.G);
+}
+
+// Four columns of a row of the output, and its maximum and sum.
+template <int D>
+__device__ __forceinline__ void put_columns(const Args& a, size_t row, int col, float x, float y, float z, float w) {
+  if (a.whole != nullptr)
+    *reinterpret_cast<float4*>(a.whole + row * D + col) = make_float4(x, y, z, w);
+  else
+    *reinterpret_cast<uint2*>(a.o + row * D + col) = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
+}
+template <int D>
+__device__ __forceinline__ void put_sums(const Args& a, size_t row, float M, float L) {
+  if (a.whole != nullptr) {
+    a.whole[a.whole_rows * D + row] = M;
+    a.whole[a.whole_rows * (D + 1) + row] = L;
+  } else {
+    a.lse[row] = lse_of(M, L);
+  }
 }
 
 // A sequence's length as it is in memory, and what is made of it.  Separate, since
@@ -335,9 +357,9 @@ __device__ __forceinline__ void fill_empty(const Args& a, int len_first) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (checked(a, b == blockIdx.x ? len_first : read_length(a, b)) > 0) continue;
     const size_t row = (size_t)b * a.n_q * a.H;
-    for (int i = threadIdx.x; i < a.n_q * a.H * (D / 8); i += kThreads)
-      reinterpret_cast<uint4*>(a.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) a.lse[row + i] = -INFINITY;
+    for (int i = threadIdx.x; i < a.n_q * a.H * (D / 4); i += kThreads)
+      put_columns<D>(a, row + i / (D / 4), i % (D / 4) * 4, 0.f, 0.f, 0.f, 0.f);
+    for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) put_sums<D>(a, row + i, -INFINITY, 0.f);
     if (a.by_segment)
       for (int i = threadIdx.x; i < copies; i += kThreads) a.chains[(long long)b * copies + i] = Chain{0, 0, 0, 0};
   }
@@ -892,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           part[kRows * D + r] = M;
           part[kRows * D + kRows + r] = L;
         } else if (rr < rows_total) {
-          a.lse[out_row(a, sg.b, sg.h, rr)] = lse_of(M, L);
+          put_sums<D>(a, out_row(a, sg.b, sg.h, rr), M, L);
         }
       }
       // Pairs of columns, moved by four for every second row, so that the 16 lanes
@@ -925,9 +947,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         if (!whole) {
           *reinterpret_cast<float4*>(part + r * D + at + part4 * 4) = make_float4(v[0], v[1], v[2], v[3]);
         } else if (rr < rows_total) {
-          const size_t row = out_row(a, sg.b, sg.h, rr);
-          *reinterpret_cast<uint2*>(a.o + row * D + at + part4 * 4) =
-              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          put_columns<D>(a, out_row(a, sg.b, sg.h, rr), at + part4 * 4, v[0], v[1], v[2], v[3]);
         }
       }
     }
@@ -966,8 +986,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
       if (rr < rows_total) {
         const size_t row = out_row(a, sg.b, sg.h, rr);
-        *reinterpret_cast<uint2*>(a.o + row * D + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        if (col == 0) a.lse[row] = lse_of(M, L);
+        put_columns<D>(a, row, col, v.x, v.y, v.z, v.w);
+        if (col == 0) put_sums<D>(a, row, M, L);
       }
     }
     cluster_sync();  // nobody leaves while its part is read
@@ -1064,12 +1084,14 @@ __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_k
   }
   if (!have) return;
   const size_t row = out_row(a, ch.y, ch.z / a.row_blocks, rr);
-  uint16_t* out = a.o + row * D + lane * (D / 32);
+  const int col = lane * (D / 32);
   if constexpr (D == 128)
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    put_columns<D>(a, row, col, o[0], o[1], o[2], o[3]);
+  else if (a.whole != nullptr)
+    *reinterpret_cast<float2*>(a.whole + row * D + col) = make_float2(o[0], o[1]);
   else
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0], o[1]);
-  if (lane == 0) a.lse[row] = lse_of(M, L);
+    *reinterpret_cast<uint32_t*>(a.o + row * D + col) = pack_bf16x2(o[0], o[1]);
+  if (lane == 0) put_sums<D>(a, row, M, L);
 }
 
 // Runs the tiles are dealt in: the CTAs that the SMs hold at a time.  (The full
@@ -1195,7 +1217,7 @@ size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H) {
 
 cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides, const int* lens,
                                void* o, float* lse, int n_q, int H, float scale, void* workspace,
-                               cudaStream_t stream) {
+                               cudaStream_t stream, float* whole) {
   Args a;
   a.q = static_cast<const uint16_t*>(q);
   a.q_batch = strides[0];
@@ -1207,6 +1229,8 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   a.lens = lens;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
+  a.whole = whole;
+  a.whole_rows = (size_t)c.B * n_q * H;
   a.B = c.B, a.n_q = n_q, a.H = H, a.Hkv = c.Hkv, a.G = H / c.Hkv, a.P = c.P, a.page = c.page;
   a.by_G = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
   a.page_shift = page_shift(c.page);

@@ -1,0 +1,847 @@
+// Attention of each sequence's newest tokens over the paged INT8 cache, where all
+// sequences of the batch share a prefix that is stored once.
+//
+// For query token i of n_q of sequence b and head h of group h / G, over the L positions
+// of the prefix and the sequence's own positions j <= len - n_q + i:
+//   s_j = scale * q . (ck_j * ks_j),   O = sum_j softmax(s)_j (cv_j * vs_j),   LSE = ln sum_j exp(s_j)
+// with codes ck, cv and the scales ks, vs of position j's page and key head.  Prefix and own
+// part are each reduced to (m, l, O / l), m the largest score, l the sum of exp(s - m), and joined as
+//   m = max m_x,   l = sum_x l_x e^(m_x - m),   O = sum_x (l_x e^(m_x - m) / l) (O / l)_x,
+// means with weights of at most 1.  The own part is attn_decode_int8's (decode_int8.cu); this
+// file has the prefix and the join.
+//
+// The rows of a key head over the prefix are those of all sequences, tokens and heads of
+// the group, R = B n_q G, so the prefix's codes are read once for 256 of them instead of once a
+// sequence, and the products have the rows of a tile of tcgen05.mma: S = Q K^T and O += P V of
+// 128 rows by 128 positions, accumulators in TMEM.  A CTA (one per SM) has two row tiles that
+// share each tile of keys; with up to 128 rows it has one, and its two halves take the
+// even and the odd key tiles of it.  Roles of the warps:
+//   warps 4-7, 8-11   softmax of row tile (or half) 0 and 1, one thread a row; also their Q rows
+//                     and the results' way out
+//   warps 12-15       codes to FP16: global memory -> registers -> swizzled shared memory
+//   warp 1            issues the products
+// The tiles of all (key head, row block) units, one behind the other, are dealt to the CTAs
+// in equal runs; every run leaves a part (m, l, O / l) of each unit it meets in the workspace.
+//
+// Numerics, as in decode_int8.cu: codes are exact in FP16; Q becomes FP16 after division by a
+// power of two of its row's maximum (exact down to 2^-17 of it); the weights p vs of the
+// values' codes are FP16 after a row's own power of two 2^E, by which its largest weight so far
+// is 2^11 to 2^15, so that they keep 11 bits down to 2^-25 of it.  m and E follow the
+// running maxima of s and of s + log2(vs) when one has grown by more than 2^4 (the accumulators
+// in TMEM are rescaled then, by the softmax's threads).  Sums and statistics are FP32.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "attn_internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+
+static __device__ unsigned int g_status_shared;
+
+namespace {
+
+constexpr int kThreads = 512;
+// Registers a thread of the four warpgroups: products, softmax (two), codes.
+constexpr int kRegsMma = 48, kRegsSoftmax = 176, kRegsCodes = 112;
+static_assert(kRegsMma + 2 * kRegsSoftmax + kRegsCodes <= 512, "setmaxnreg split exceeds the launch pool");
+constexpr int kUnitRows = 256;  // rows of a unit: two tiles
+// Cost of a key tile where the unit has two row tiles, and where it has one.
+constexpr int kCostTwo = 3, kCostOne = 2;
+constexpr int kLeastRun = 2;  // key tiles of a run at least
+constexpr int kHeads = 8;     // key tiles whose scales are held
+constexpr float kSlack = 4.f;  // growth of a maximum (base 2) that the accumulators take as it is
+constexpr float kTop = 11.f;   // log2 of the largest weight just after its row's references moved
+
+__device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_shared, code); }
+
+struct Args {
+  const uint16_t* q;
+  long long q_batch, q_token, q_head;
+  const uint8_t *k, *v;
+  const float *k_scale, *v_scale;
+  const int *table, *len;  // of the prefix
+  int B, n_q, H, Hkv, G, P, page_shift, blocks;
+  int rows, row_blocks, runs;
+  float scale_log2;
+  float* parts;
+  const float* own;  // O / l [B n_q H][D], m [B n_q H], l [B n_q H] of the own parts
+  uint16_t* o;
+  float* lse;
+};
+
+// A part: O / l as [D / 4][256 rows][4], m [256], l [256].
+__host__ __device__ constexpr size_t part_floats(int d) { return (size_t)kUnitRows * (d + 2); }
+
+// How the key tiles of all units (unit = key head * row_blocks + row block) are dealt.
+struct Deal {
+  int tiles;      // key tiles of the prefix
+  int runs;       // that are not empty
+  int last_cost;  // of a key tile of a head's last unit
+  long long head_cost;
+  __device__ __forceinline__ Deal(const Args& a, int len) {
+    tiles = (len + kBlockN - 1) / kBlockN;
+    last_cost = a.rows - (a.row_blocks - 1) * kUnitRows <= kBlockM ? kCostOne : kCostTwo;
+    head_cost = (long long)tiles * (kCostTwo * (a.row_blocks - 1) + last_cost);
+    const long long most = head_cost * a.Hkv / (kLeastRun * kCostTwo);
+    runs = tiles == 0 ? 0 : (int)max(1ll, min((long long)a.runs, most));
+  }
+  // First tile (unit * tiles + key tile) of run c.
+  __device__ __forceinline__ long long begin(const Args& a, int c) const {
+    if (c >= runs) return (long long)a.Hkv * a.row_blocks * tiles;
+    const long long x = head_cost * a.Hkv * c / runs, h = x / head_cost, y = x - h * head_cost;
+    const long long full = (long long)kCostTwo * tiles * (a.row_blocks - 1);
+    const long long i = y < full ? y / kCostTwo : (long long)tiles * (a.row_blocks - 1) + (y - full) / last_cost;
+    return h * a.row_blocks * tiles + i;
+  }
+};
+
+// The prefix's length as it is used; one that the table has no room for is cut and reported.
+__device__ __forceinline__ int prefix_length(const Args& a, bool report) {
+  const int len = __ldcg(a.len);
+  const long long cap = (long long)a.blocks << a.page_shift;
+  if (len >= 0 && len <= cap) return len;
+  if (report) set_fail(ATTN_ERR_INVALID_ARG);
+  return len < 0 ? 0 : (int)cap;
+}
+
+// The part of a run that lies in one unit.
+struct Segment {
+  int unit, h, rb, k0, nk;
+  bool two;  // two row tiles, else the tile's key tiles alternate between the two halves
+  int rows;  // of the unit
+};
+__device__ __forceinline__ bool next_segment(const Args& a, const Deal& deal, long long& at, long long end, Segment& s) {
+  if (at >= end) return false;
+  s.unit = (int)(at / deal.tiles);
+  s.k0 = (int)(at - (long long)s.unit * deal.tiles);
+  s.nk = (int)min((long long)(deal.tiles - s.k0), end - at);
+  s.h = s.unit / a.row_blocks;
+  s.rb = s.unit - s.h * a.row_blocks;
+  s.rows = min(kUnitRows, a.rows - s.rb * kUnitRows);
+  s.two = s.rows > kBlockM;
+  at += s.nk;
+  return true;
+}
+// Key tiles of half t.
+__device__ __forceinline__ int tiles_of(const Segment& s, int t) { return s.two ? s.nk : (s.nk + 1 - t) / 2; }
+
+// Scales of a key tile in groups of 16 positions, and how many of each are seen.
+struct Head {
+  float ks[8], vs[8], log_vs[8];
+  int seen[8];
+  int hidden;  // not all are seen
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kStagesK = 3;
+  static constexpr int kStagesV = D == 128 ? 2 : 3;
+  static constexpr int kChunks = D / 64;
+  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kStagesK * kTileBytes;
+  static constexpr int kOffHead = kOffV + kStagesV * kTileBytes;
+  static constexpr int kOffF = kOffHead + kHeads * (int)sizeof(Head);  // FP32 [2][128]: factor of a row's scores
+  static constexpr int kOffBar = (kOffF + 2 * 128 * 4 + 15) / 16 * 16;
+  // k_full, k_empty [K], v_full, v_empty [V], head [kHeads], q [2], s_full [2], p_full [2], o_done [2], final
+  static constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + kHeads + 9;
+  static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+  static constexpr uint32_t kTmemCols = 512;
+  static __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
+  static __device__ __forceinline__ uint32_t col_o(int t) { return 256u + D * t; }
+};
+
+// Instruction descriptor for kind::f16 with FP16 A and B, FP32 D (fields as in idesc_bf16).
+constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two of four codes as FP16: the byte c + 128 under the exponent of 1024 is 1152 + c.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t sel) {
+  const uint32_t x = __byte_perm(u, 0x64646464u, sel);
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64806480u));
+  return r;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 1 / L, or 0 where a row has seen nothing.  A NaN stays one.
+__device__ __forceinline__ float inverse(float L) { return L == 0.f ? 0.f : 1.f / L; }
+// 2^e for a whole e in [-126, 127].
+__device__ __forceinline__ float power2(float e) { return __uint_as_float((uint32_t)((int)e + 127) << 23); }
+
+// Sequence, token and head of row r of key head h's rows.
+__device__ __forceinline__ void row_of(const Args& a, int r, int& b, int& t, int& g) {
+  const int x = r / a.G;
+  g = r - x * a.G;
+  b = x / a.n_q;
+  t = x - b * a.n_q;
+}
+
+// GROUP: positions that share a page's scales for certain (16, or 32 in pages of 32 and more).
+template <int D, int GROUP>
+__global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* bar_kfull = bars;
+  uint64_t* bar_kempty = bar_kfull + C::kStagesK;
+  uint64_t* bar_vfull = bar_kempty + C::kStagesK;
+  uint64_t* bar_vempty = bar_vfull + C::kStagesV;
+  uint64_t* bar_head = bar_vempty + C::kStagesV;
+  uint64_t* bar_q = bar_head + kHeads;
+  uint64_t* bar_sfull = bar_q + 2;
+  uint64_t* bar_pfull = bar_sfull + 2;
+  uint64_t* bar_odone = bar_pfull + 2;
+  uint64_t* bar_final = bar_odone + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  float* s_f = reinterpret_cast<float*>(smem + C::kOffF);
+  Head* heads = reinterpret_cast<Head*>(smem + C::kOffHead);
+
+  if (threadIdx.x == 0) {
+    tmem_slot[1] = (smem_u32(smem) & 1023u) != 0;
+    for (int s = 0; s < C::kStagesK; ++s) {
+      mbar_init(&bar_kfull[s], 128);
+      mbar_init(&bar_kempty[s], 1);
+    }
+    for (int s = 0; s < C::kStagesV; ++s) {
+      mbar_init(&bar_vfull[s], 128);
+      mbar_init(&bar_vempty[s], 1);
+    }
+    for (int s = 0; s < kHeads; ++s) mbar_init(&bar_head[s], 8);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar_q[t], 128);
+      mbar_init(&bar_sfull[t], 1);
+      mbar_init(&bar_pfull[t], 128);
+      mbar_init(&bar_odone[t], 1);
+    }
+    mbar_init(bar_final, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  const bool abort_all = tmem_slot[1] != 0;
+  if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
+  const int len = prefix_length(a, threadIdx.x == 0 && blockIdx.x == 0);
+  const Deal deal(a, len);
+  long long at = abort_all ? 0 : deal.begin(a, blockIdx.x);
+  const long long end = abort_all ? 0 : deal.begin(a, blockIdx.x + 1);
+  Segment sg;
+
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (warp == 1) {
+      // ------------------------------------------------------------ products
+      constexpr uint32_t idesc_qk = idesc_f16(128, 128, false);
+      constexpr uint32_t idesc_pv = idesc_f16(128, D, true);
+      const uint64_t descQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t descK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t descV = sdesc_sw128(smem_u32(sV), C::kChunkBytes, 1024);
+      auto issue_s = [&](int t, int st) {
+        const uint64_t a0 = sdesc_add(descQ, t * C::kTileBytes);
+        const uint64_t b0 = sdesc_add(descK, st * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+          mma_ss_elect(tmem + C::col_s(t), sdesc_add(a0, off), sdesc_add(b0, off), idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_elect(&bar_sfull[t]);
+      };
+      auto issue_pv = [&](int t, int st, bool acc) {
+        const uint64_t b0 = sdesc_add(descV, st * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kBlockN / 16; ++kk)
+          mma_ts_elect(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, sdesc_add(b0, kk * 2048), idesc_pv,
+                       (acc || kk > 0) ? 1u : 0u);
+      };
+      bool ok = true;
+      int g = 0, items = 0;
+      int pc[2] = {0, 0};
+      auto k_ready = [&](int i) {
+        const bool r = warp_wait(&bar_kfull[i % C::kStagesK], (i / C::kStagesK) & 1);
+        tc_fence_after();
+        return r;
+      };
+      while (ok && next_segment(a, deal, at, end, sg)) {
+        // S_t's columns are free: the P V products issued before read them first.
+        ok = warp_wait(&bar_q[0], items & 1) && warp_wait(&bar_q[1], items & 1);
+        ++items;
+        const int step = sg.two ? 1 : 2;  // key tiles from one of a half's to its next
+        // S of key tile e, of one half or both.
+        auto s_of = [&](int e) {
+          if (!k_ready(g + e)) return false;
+          const int st = (g + e) % C::kStagesK;
+          if (sg.two) {
+            issue_s(0, st);
+            issue_s(1, st);
+          } else {
+            issue_s(e & 1, st);
+          }
+          mma_commit_elect(&bar_kempty[st]);
+          return true;
+        };
+        ok = ok && s_of(0);
+        if (!sg.two && sg.nk > 1) ok = ok && s_of(1);
+        for (int e = 0; e < sg.nk && ok; ++e) {
+          const int st = (g + e) % C::kStagesV;
+          const bool more = e + step < sg.nk;
+          ok = warp_wait(&bar_vfull[st], ((g + e) / C::kStagesV) & 1);
+          if (ok && sg.two && more) ok = k_ready(g + e + 1);
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (!sg.two && t != (e & 1)) continue;
+            ok = warp_wait(&bar_pfull[t], pc[t] & 1);
+            if (!ok) break;
+            ++pc[t];
+            tc_fence_after();
+            issue_pv(t, st, e >= step);
+            if (!more) mma_commit_elect(&bar_odone[t]);
+            if (sg.two && more) issue_s(t, (g + e + 1) % C::kStagesK);
+          }
+          if (!ok) break;
+          mma_commit_elect(&bar_vempty[st]);
+          if (sg.two && more) mma_commit_elect(&bar_kempty[(g + e + 1) % C::kStagesK]);
+          if (!sg.two && more) ok = s_of(e + 2);
+        }
+        // A half without a key tile is told too: it waits for the segment's end before the next.
+        if (ok && !sg.two && sg.nk == 1) mma_commit_elect(&bar_odone[1]);
+        g += sg.nk;
+      }
+      if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
+      // Every product that was issued completes before TMEM is released.
+      mma_commit_elect(bar_final);
+      mbar_wait(bar_final, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCodes));
+    // --------------------------------------------------------------- codes
+    // A thread has one 16-byte unit of a row, 128 / kPasses rows of the tile at a time, and
+    // holds the next tile's codes in registers while it waits for room for them.
+    constexpr int kUnits = D / 16, kRows = 128 / kUnits, kPasses = 128 / kRows;
+    const int tid = threadIdx.x - 384, unit = tid % kUnits, row = tid / kUnits;
+    bool ok = true;
+    long long at_l = at;  // of the tile that is loaded
+    Segment sl;
+    bool more = next_segment(a, deal, at_l, end, sl);
+    int e_l = 0;
+    // Lane x < 8: the page of positions [16 x, 16 x + 16) of key tile sl.k0 + e_l, or -1.
+    auto page_at = [&](int tile) {
+      const long long pos = (long long)tile * kBlockN + 16 * (lane & 7);
+      int id = -1;
+      if (pos < len) {
+        id = __ldcg(a.table + (pos >> a.page_shift));
+        if (id < 0 || id >= a.P) {
+          set_fail(ATTN_ERR_INVALID_ARG);
+          id = -1;
+        }
+      }
+      return id;
+    };
+    uint4 raw_k[kPasses], raw_v[kPasses];
+    int id = -1;
+    auto load = [&](const uint8_t* from, uint4 (&raw)[kPasses]) {
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = p * kRows + row;
+        const int page = __shfl_sync(0xffffffffu, id, r >> 4);
+        const int in_page = ((sl.k0 + e_l) * kBlockN + r) & ((1 << a.page_shift) - 1);
+        raw[p] = make_uint4(0u, 0u, 0u, 0u);
+        if (page >= 0)
+          raw[p] = __ldcg(reinterpret_cast<const uint4*>(
+              from + ((((long long)page * a.Hkv + sl.h) << a.page_shift) + in_page) * D + unit * 16));
+      }
+    };
+    auto put = [&](uint8_t* tile, const uint4 (&raw)[kPasses]) {
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = p * kRows + row;
+        const uint32_t w[4] = {raw[p].x ^ 0x80808080u, raw[p].y ^ 0x80808080u, raw[p].z ^ 0x80808080u,
+                               raw[p].w ^ 0x80808080u};
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = codes_f16(w[i], 0x4140u);
+          x[2 * i + 1] = codes_f16(w[i], 0x4342u);
+        }
+        const uint32_t to = smem_u32(tile) + (unit >> 2) * C::kChunkBytes;
+        const uint32_t u = (unit & 3) * 2;
+        // The eight lanes of a phase have one row of d = 128: those of its second chunk store
+        // their units in the other order, so that all banks are met.
+        if (unit < 4) {
+          st_shared_v4(to + sw128_offset(r, u), x[0], x[1], x[2], x[3]);
+          st_shared_v4(to + sw128_offset(r, u + 1), x[4], x[5], x[6], x[7]);
+        } else {
+          st_shared_v4(to + sw128_offset(r, u + 1), x[4], x[5], x[6], x[7]);
+          st_shared_v4(to + sw128_offset(r, u), x[0], x[1], x[2], x[3]);
+        }
+      }
+    };
+    int id_next = -1;
+    float ks = 0.f, vs = 0.f;
+    auto load_scales = [&]() {
+      if (warp == 12 && lane < 8) {
+        const size_t i = (size_t)max(id, 0) * a.Hkv + sl.h;
+        ks = id >= 0 ? __ldcg(a.k_scale + i) : 0.f;
+        vs = id >= 0 ? __ldcg(a.v_scale + i) : 0.f;
+      }
+    };
+    if (more) {
+      id = page_at(sl.k0);
+      load_scales();
+      load(a.k, raw_k);
+      load(a.v, raw_v);
+    }
+    for (int g = 0; more; ++g) {
+      const int stk = g % C::kStagesK, stv = g % C::kStagesV;
+      // The tile behind this one.
+      Segment sn = sl;
+      int e_n = e_l + 1;
+      bool more_n = true;
+      if (e_n == sl.nk) {
+        e_n = 0;
+        more_n = next_segment(a, deal, at_l, end, sn);
+      }
+      id_next = more_n ? page_at(sn.k0 + e_n) : -1;
+      if (g >= C::kStagesK) ok = warp_wait(&bar_kempty[stk], (g / C::kStagesK - 1) & 1);
+      if (!ok) break;
+      if (warp == 12 && lane < 8) {
+        // The slot's last tile, kHeads before, has been through the softmax: the products S of
+        // kStagesK tiles ago are complete, and were issued behind P V of the tile before.
+        Head& hd = heads[g % kHeads];
+        const int pos = (sl.k0 + e_l) * kBlockN + 16 * lane;
+        const int seen = id >= 0 ? max(0, min(16, len - pos)) : 0;
+        hd.ks[lane] = ks;
+        hd.vs[lane] = vs;
+        hd.log_vs[lane] = fmaxf(__log2f(vs), -126.f);
+        hd.seen[lane] = seen;
+        const bool hidden = __any_sync(0xffu, seen < 16);
+        if (lane == 0) hd.hidden = hidden;
+        mbar_arrive(&bar_head[g % kHeads]);
+      }
+      put(sK + stk * C::kTileBytes, raw_k);
+      fence_proxy_async_smem();
+      mbar_arrive(&bar_kfull[stk]);
+      if (g >= C::kStagesV) ok = warp_wait(&bar_vempty[stv], (g / C::kStagesV - 1) & 1);
+      if (!ok) break;
+      put(sV + stv * C::kTileBytes, raw_v);
+      fence_proxy_async_smem();
+      mbar_arrive(&bar_vfull[stv]);
+      sl = sn;
+      e_l = e_n;
+      more = more_n;
+      id = id_next;
+      if (more) {
+        load_scales();
+        load(a.k, raw_k);
+        load(a.v, raw_v);
+      }
+    }
+    if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // -------------------------------------------------------------- softmax
+    const int t = (warp - 4) >> 2, w0 = (warp & 3) * 32;
+    const int r = w0 + lane;  // row within the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)w0 << 16;
+    const uint32_t tS = tmem + lane_off + C::col_s(t);
+    const uint32_t tO = tmem + lane_off + C::col_o(t);
+    bool ok = true;
+    int sc = 0, oc = 0;  // S tiles consumed, segments completed
+    int g = 0;           // key tiles of the segments before
+    while (ok && next_segment(a, deal, at, end, sg)) {
+      const int first = sg.rb * kUnitRows + (sg.two ? t * kBlockM : 0);  // the tile's first row
+      const int have = min(kBlockM, a.rows - first);                     // and how many it has
+      // -------------------------------------------------------- Q rows
+      // This warp's 32 rows, kLanes lanes a row.  The products that read the rows before are
+      // complete: the softmax has had their results.
+      {
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kAtOnce;
+        const int u = lane % kLanes;
+        uint4 x[kTurns];
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+          const int rr = w0 + i * kAtOnce + lane / kLanes;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < have) {
+            int b, tok, gg;
+            row_of(a, first + rr, b, tok, gg);
+            x[i] = __ldcg(reinterpret_cast<const uint4*>(a.q + b * a.q_batch + tok * a.q_token +
+                                                         (long long)(sg.h * a.G + gg) * a.q_head + u * 8));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+          const int rr = w0 + i * kAtOnce + lane / kLanes;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+#pragma unroll
+          for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
+          const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u) - 127, -126), 126);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          st_shared_v4(smem_u32(sQ) + t * C::kTileBytes + (u >> 3) * C::kChunkBytes + sw128_offset(rr, u & 7), y[0],
+                       y[1], y[2], y[3]);
+          if (u == 0) s_f[t * 128 + rr] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        mbar_arrive(&bar_q[t]);
+      }
+      const float f = s_f[t * 128 + r];
+      const int n = tiles_of(sg, t);
+      const bool idle = w0 >= have;  // none of the warp's rows is one
+      float m_ref = -INFINITY, E = 0.f, l_run = 0.f;
+      for (int j = 0; j < n; ++j) {
+        ok = warp_wait(&bar_sfull[t], (sc + j) & 1);
+        const int tile = g + (sg.two ? j : 2 * j + t);
+        if (ok) ok = warp_wait(&bar_head[tile % kHeads], (tile / kHeads) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (idle) {
+          tc_fence_before();
+          mbar_arrive(&bar_pfull[t]);
+          continue;
+        }
+        const Head& hd = heads[tile % kHeads];
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+        // Scores in base 2.
+        constexpr int kGroups = 128 / GROUP;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          const float k = f * hd.ks[i * GROUP / 16];
+          const uint64_t k2 = f2_pack(k, k);
+#pragma unroll
+          for (int x = i * GROUP; x < (i + 1) * GROUP; x += 2) {
+            float lo, hi;
+            f2_unpack(mul2(f2_pack(__uint_as_float(s[x >> 5][x & 31]), __uint_as_float(s[x >> 5][(x & 31) + 1])), k2),
+                      lo, hi);
+            s[x >> 5][x & 31] = __float_as_uint(lo);
+            s[x >> 5][(x & 31) + 1] = __float_as_uint(hi);
+          }
+        }
+        if (hd.hidden) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int seen = hd.seen[i];
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (x >= seen) s[i >> 1][(i & 1) * 16 + x] = __float_as_uint(-INFINITY);
+          }
+        }
+        float mt = -INFINITY, mw = -INFINITY;  // largest score and largest log2 of a weight
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          const int x0 = i * GROUP;
+          float m = fmaxf(__uint_as_float(s[x0 >> 5][x0 & 31]), __uint_as_float(s[x0 >> 5][(x0 & 31) + 1]));
+#pragma unroll
+          for (int x = x0 + 2; x < x0 + GROUP; x += 2)
+            m = fmax3(m, __uint_as_float(s[x >> 5][x & 31]), __uint_as_float(s[x >> 5][(x & 31) + 1]));
+          mt = fmaxf(mt, m);
+          mw = fmaxf(mw, m + hd.log_vs[i * GROUP / 16]);
+        }
+        // The largest weight so far is 2^(m_ref - (E - kTop)) or less by kSlack.
+        if (__any_sync(0xffffffffu, fmaxf(mt, mw + (E - kTop)) > m_ref + kSlack)) {
+          const float m_new = fmaxf(m_ref, mt);
+          const bool some = m_new != -INFINITY;
+          const float w_new = fmaxf(m_ref - (E - kTop), mw);
+          const float e_new = some ? fminf(rintf(m_new - w_new) + kTop, 126.f) : 0.f;
+          const float back = some ? m_ref - m_new : 0.f;
+          l_run *= ex2(back);
+          const float f_o = ex2(back + (e_new - E));
+          m_ref = m_new;
+          E = e_new;
+          if (j > 0) {
+            const uint64_t f2 = f2_pack(f_o, f_o);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + c * 16, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float lo, hi;
+                f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), f2), lo, hi);
+                o[2 * i] = __float_as_uint(lo);
+                o[2 * i + 1] = __float_as_uint(hi);
+              }
+              tmem_st16(tO + c * 16, o);
+            }
+          }
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const float up = power2(E);
+        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        uint64_t sums2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums2[i] = 0ull;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float v = fminf(hd.vs[(c * 32 + 2 * i) / GROUP * (GROUP / 16)] * up, 0x1p127f);
+            float x0, x1;
+            f2_unpack(add2(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), nm2), x0, x1);
+            const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
+            sums2[i & 3] = add2(sums2[i & 3], p2);
+            f2_unpack(mul2(p2, f2_pack(v, v)), x0, x1);
+            pk[i] = pack_f16x2(x0, x1);
+          }
+          tmem_st16(tS + c * 16, pk);
+        }
+        float sums[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(sums2[i], sums[2 * i], sums[2 * i + 1]);
+        l_run += ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar_pfull[t]);
+      }
+      if (!ok) break;
+      sc += n;
+      g += sg.nk;
+      // ------------------------------------------------------------- part
+      ok = warp_wait(&bar_odone[t], oc & 1);
+      if (!ok) break;
+      ++oc;
+      tc_fence_after();
+      float* part = a.parts + (size_t)(blockIdx.x + sg.unit) * part_floats(D);
+      const int pr = t * kBlockM + r;  // row within the part
+      const float inv = inverse(l_run), down = power2(-E);
+      if (!idle) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          if (n > 0) {
+            tmem_ld16(tO + c * 16, o);
+            tmem_wait_ld();
+            reg_fence(o);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n > 0)
+              y = make_float4(__uint_as_float(o[4 * i]) * inv * down, __uint_as_float(o[4 * i + 1]) * inv * down,
+                              __uint_as_float(o[4 * i + 2]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
+            *reinterpret_cast<float4*>(part + ((size_t)(c * 4 + i) * kUnitRows + pr) * 4) = y;
+          }
+        }
+        part[D * kUnitRows + pr] = m_ref;
+        part[(D + 1) * kUnitRows + pr] = l_run;
+      }
+      // O_t has been read: the next segment's first P V, which overwrites it, waits for this
+      // warpgroup's next P.
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+__device__ __forceinline__ float4 weighted(const float4& x, float inv, float l) {
+  return make_float4(x.x * inv * l, x.y * inv * l, x.z * inv * l, x.w * inv * l);
+}
+
+// Joins the parts of 32 rows of a unit and their own part.  A lane has a row, a warp D / 8
+// of the columns; the order of the sums is that of the runs.
+constexpr int kJoinRows = 32, kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a) {
+  constexpr int kQuads = D / 32;  // of columns a thread
+  griddep_launch_dependents();
+  griddep_wait();
+  const int unit = blockIdx.x / (kUnitRows / kJoinRows), rows0 = blockIdx.x % (kUnitRows / kJoinRows) * kJoinRows;
+  const int h = unit / a.row_blocks, rb = unit - h * a.row_blocks;
+  if (rb * kUnitRows + rows0 >= a.rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Deal deal(a, prefix_length(a, false));
+  const long long from = (long long)unit * deal.tiles, to = from + deal.tiles;
+  const long long mine = threadIdx.x < deal.runs ? deal.begin(a, threadIdx.x) : to;
+  int c0 = __syncthreads_count(mine <= from && (int)threadIdx.x < deal.runs) - 1;
+  const int c1 = __syncthreads_count(mine < to) - 1;
+  const int r = rows0 + lane, row = rb * kUnitRows + r;
+  if (row >= a.rows) return;
+  const bool two = a.rows - rb * kUnitRows > kBlockM;
+  int b, tok, gg;
+  row_of(a, row, b, tok, gg);
+  const size_t out = ((size_t)b * a.n_q + tok) * a.H + h * a.G + gg;
+  const size_t all = (size_t)a.B * a.n_q * a.H;
+  float M = __ldcg(a.own + all * D + out), L = __ldcg(a.own + all * D + all + out);
+  float4 o[kQuads];
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i)
+    o[i] = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + (warp * kQuads + i) * 4));
+  const int halves = two ? 1 : 2;
+  const int n = deal.runs == 0 ? 0 : (c1 - c0 + 1) * halves;
+  constexpr int kBatch = 4;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float m[kBatch], l[kBatch];
+    float4 x[kBatch][kQuads];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      m[k] = -INFINITY, l[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) x[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + k < n) {
+        const int c = c0 + (i0 + k) / halves;
+        const int pr = r + (i0 + k) % halves * kBlockM;
+        const float* part = a.parts + (size_t)(c + unit) * part_floats(D);
+        m[k] = __ldcg(part + D * kUnitRows + pr);
+        l[k] = __ldcg(part + (D + 1) * kUnitRows + pr);
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+          x[k][i] = __ldcg(reinterpret_cast<const float4*>(part + ((size_t)(warp * kQuads + i) * kUnitRows + pr) * 4));
+      }
+    }
+    float m_new = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) m_new = fmaxf(m_new, m[k]);
+    const float m_use = m_new == -INFINITY ? 0.f : m_new;
+    const float before = L * ex2(M - m_use);
+    M = m_new;
+    L = before;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) L += l[k] *= ex2(m[k] - m_use);
+    const float inv = inverse(L);
+    // Values times 1 / L, then times their weight: the two factors' product could fall below FP32's
+    // range where a small weight meets large values.
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) o[i] = weighted(o[i], inv, before);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const float4 y = weighted(x[k][i], inv, l[k]);
+        o[i].x += y.x, o[i].y += y.y, o[i].z += y.z, o[i].w += y.w;
+      }
+  }
+  uint16_t* to_o = a.o + out * D + warp * kQuads * 4;
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i)
+    *reinterpret_cast<uint2*>(to_o + 4 * i) = make_uint2(pack_bf16x2(o[i].x, o[i].y), pack_bf16x2(o[i].z, o[i].w));
+  if (warp == 0) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// Runs that the prefix's tiles are dealt in: one CTA an SM.  (The full device's count where
+// there is no device to ask, for workspace sizes; a join's CTA has a thread for each.)
+int shared_runs() {
+  const int sms = device_sm_count();
+  return std::min(sms > 0 ? sms : 152, kJoinThreads);
+}
+
+struct Layout {
+  size_t parts, decode, bytes;  // byte offsets; the own part is at 0
+};
+Layout layout(const PagedCache& c, int n_q, int H) {
+  const size_t all = (size_t)c.B * n_q * H, rows = all / c.Hkv;
+  const size_t units = (size_t)c.Hkv * ((rows + kUnitRows - 1) / kUnitRows);
+  Layout w;
+  w.parts = align256(all * (c.d + 2) * sizeof(float));
+  w.decode = w.parts + align256((units + shared_runs()) * part_floats(c.d) * sizeof(float));
+  w.bytes = w.decode + decode_workspace_bytes(c, n_q, H);
+  return w;
+}
+
+template <int D, int GROUP>
+cudaError_t launch_prefix(const Args& a, cudaStream_t stream) {
+  using C = Cfg<D>;
+  auto kernel = shared_prefix_kernel<D, GROUP>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kernel, dim3(a.runs), dim3(kThreads), C::kSmemBytes, stream, a);
+}
+
+}  // namespace
+
+size_t decode_shared_workspace_bytes(const PagedCache& c, int n_q, int H) { return layout(c, n_q, H).bytes; }
+
+cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const long long* strides,
+                                      const int* prefix_table, int prefix_blocks, const int* prefix_len,
+                                      const int* lens, void* o, float* lse, int n_q, int H, float scale,
+                                      void* workspace, cudaStream_t stream) {
+  const Layout w = layout(c, n_q, H);
+  Args a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_batch = strides[0], a.q_token = strides[1], a.q_head = strides[2];
+  a.k = static_cast<const uint8_t*>(c.k), a.v = static_cast<const uint8_t*>(c.v);
+  a.k_scale = c.k_scale, a.v_scale = c.v_scale;
+  a.table = prefix_table, a.len = prefix_len;
+  a.B = c.B, a.n_q = n_q, a.H = H, a.Hkv = c.Hkv, a.G = H / c.Hkv, a.P = c.P;
+  a.page_shift = page_shift(c.page), a.blocks = prefix_blocks;
+  a.rows = c.B * n_q * a.G;
+  a.row_blocks = (a.rows - 1) / kUnitRows + 1;
+  a.runs = shared_runs();
+  a.scale_log2 = scale * 1.4426950408889634f;
+  char* ws = static_cast<char*>(workspace);
+  a.parts = reinterpret_cast<float*>(ws + w.parts);
+  a.own = reinterpret_cast<const float*>(ws);
+  a.o = static_cast<uint16_t*>(o), a.lse = lse;
+  cudaError_t err = cudaErrorInvalidValue;
+  if (c.d == 128)
+    err = c.page >= 32 ? launch_prefix<128, 32>(a, stream) : launch_prefix<128, 16>(a, stream);
+  else
+    err = c.page >= 32 ? launch_prefix<64, 32>(a, stream) : launch_prefix<64, 16>(a, stream);
+  if (err != cudaSuccess) return err;
+  err = launch_decode_int8(c, q, strides, lens, nullptr, nullptr, n_q, H, scale, ws + w.decode, stream,
+                           reinterpret_cast<float*>(ws));
+  if (err != cudaSuccess) return err;
+  const unsigned blocks = (unsigned)(a.Hkv * a.row_blocks) * (kUnitRows / kJoinRows);
+  auto join = c.d == 128 ? shared_join_kernel<128> : shared_join_kernel<64>;
+  return launch_pdl(join, dim3(blocks), dim3(kJoinThreads), 0, stream, a);
+}
+
+cudaError_t status_word_shared(void** word) { return cudaGetSymbolAddress(word, g_status_shared); }
+
+}  // namespace attn

@@ -240,11 +240,99 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len, block_table, seqlens, scale, o, lse, workspace)
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 13) Py_RETURN_NONE;
+  PyObject* const five[5] = {a[1], a[2], a[3], a[4], a[7]};
+  Cache c;
+  if (!cache_of(five, &c)) Py_RETURN_NONE;
+  const Tensor *q = tensor(a[0]), *pre = tensor(a[5]), *len = tensor(a[6]), *lens = tensor(a[8]);
+  float scale;
+  if (q == nullptr || q->dim() != 4 || pre == nullptr || pre->dim() != 1 || !scale_of(a[9], c.d, &scale))
+    Py_RETURN_NONE;
+  const int64_t n_q = q->size(1), H = q->size(2), blocks = pre->size(0);
+  Tensor o, lse, ws;
+  if (n_q > INT32_MAX || H > INT32_MAX || blocks > INT32_MAX || !rows(q, {c.B, n_q, H, c.d}) || !ints(pre, blocks) ||
+      !ints(len, 1) || !ints(lens, c.B) ||
+      !outputs(a[10], a[11], {c.B, n_q, H, c.d}, at::kBFloat16, {c.B, n_q, H}, at::kFloat, *q, &o, &lse))
+    Py_RETURN_NONE;
+  if (a[12] == Py_None) {
+    const size_t need = attn_decode_shared_int8_workspace_bytes(c.B, (int)n_q, (int)H, c.hk, c.d, c.page, (int)blocks,
+                                                                c.blocks);
+    ws = empty({(int64_t)std::max<size_t>(need, 1)}, at::kByte, *q);
+  } else {
+    const Tensor* t = tensor(a[12]);
+    if (t == nullptr || !t->is_cuda() || !t->is_contiguous()) Py_RETURN_NONE;
+    ws = *t;
+  }
+  const attn_status s = attn_decode_shared_int8(
+      q->data_ptr(), q->stride(0), q->stride(1), q->stride(2), c.k->data_ptr(), c.v->data_ptr(),
+      (const float*)c.ks->data_ptr(), (const float*)c.vs->data_ptr(), (const int*)pre->data_ptr(), (int)blocks,
+      (const int*)len->data_ptr(), (const int*)c.table->data_ptr(), (const int*)lens->data_ptr(), o.data_ptr(),
+      (float*)lse.data_ptr(), c.B, (int)n_q, (int)H, c.hk, c.d, c.pages, c.page, c.blocks, scale, ws.data_ptr(),
+      ws.nbytes(), stream());
+  return s == ATTN_OK ? pair(o, lse) : raise("attn_decode_shared_int8", s);
+  END_HANDLE_TH_ERRORS
+}
+
+// (block_table, held, wanted, free_pages, n_free, page_size, T, lens, cu_seqlens, slots, positions)
+PyObject* cache_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 11 || !PyLong_Check(a[5]) || !PyLong_Check(a[6])) Py_RETURN_NONE;
+  const Tensor *table = tensor(a[0]), *held = tensor(a[1]), *wanted = tensor(a[2]), *pages = tensor(a[3]),
+               *free = tensor(a[4]);
+  if (table == nullptr || table->dim() != 2 || pages == nullptr || pages->dim() != 1) Py_RETURN_NONE;
+  const int64_t B = table->size(0), blocks = table->size(1), P = pages->size(0);
+  int overflow = 0;
+  const long long page = PyLong_AsLongLongAndOverflow(a[5], &overflow);
+  if (overflow != 0 || page < INT32_MIN || page > INT32_MAX) Py_RETURN_NONE;
+  const long long T = PyLong_AsLongLongAndOverflow(a[6], &overflow);
+  if (overflow != 0 || T < 0 || T > INT32_MAX || B >= INT32_MAX || blocks > INT32_MAX || P > INT32_MAX ||
+      !dense(table, at::kInt, {B, blocks}) || !ints(held, B) || !ints(wanted, B) || !ints(pages, P) || !ints(free, 1))
+    Py_RETURN_NONE;
+  const int64_t sizes[4] = {B, B + 1, T, T};
+  Tensor out[4];
+  bool fresh = true;
+  for (int i = 0; i < 4; ++i) fresh = fresh && a[7 + i] == Py_None;
+  int64_t total = 0, at[4];
+  for (int i = 0; i < 4; ++i) at[i] = total, total += (sizes[i] + 63) / 64 * 64;
+  if (fresh && total * 4 <= kShared && T > 0) {  // one allocation
+    Tensor all = empty({total}, at::kInt, *table);
+    for (int i = 0; i < 4; ++i) {
+      out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                        c10::scalarTypeToTypeMeta(at::kInt));
+      out[i].unsafeGetTensorImpl()->set_storage_offset(at[i]);
+      out[i].unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
+    }
+  } else {
+    for (int i = 0; i < 4; ++i)
+      if (!output(a[7 + i], {sizes[i]}, at::kInt, *table, &out[i])) Py_RETURN_NONE;
+  }
+  int* p[4];
+  for (int i = 0; i < 4; ++i) p[i] = (int*)out[i].data_ptr();
+  const attn_status s = attn_cache_reserve((int*)table->data_ptr(), (const int*)held->data_ptr(),
+                                           (const int*)wanted->data_ptr(), (int*)pages->data_ptr(),
+                                           (int*)free->data_ptr(), p[0], p[1], p[2], p[3], (int)B, (int)T, (int)P,
+                                           (int)page, (int)blocks, stream());
+  if (s != ATTN_OK) return raise("attn_cache_reserve", s);
+  PyObject* r = PyTuple_New(4);
+  for (int i = 0; r != nullptr && i < 4; ++i) {
+    PyObject* x = THPVariable_Wrap(out[i]);
+    if (x == nullptr) Py_CLEAR(r);
+    else PyTuple_SET_ITEM(r, i, x);
+  }
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"varlen_fwd", (PyCFunction)(void (*)())varlen_fwd, METH_FASTCALL, nullptr},
     {"cache_append", (PyCFunction)(void (*)())cache_append, METH_FASTCALL, nullptr},
     {"cache_read", (PyCFunction)(void (*)())cache_read, METH_FASTCALL, nullptr},
     {"decode", (PyCFunction)(void (*)())decode, METH_FASTCALL, nullptr},
+    {"decode_shared", (PyCFunction)(void (*)())decode_shared, METH_FASTCALL, nullptr},
+    {"cache_reserve", (PyCFunction)(void (*)())cache_reserve, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -78,3 +78,42 @@ def cached(codes, scales, table, n):
     ids = list(table[:-(-n // page)])
     v = codes[ids].double() * scales[ids].double()[:, :, None, None]
     return v.permute(0, 2, 1, 3).reshape(-1, hk, d)[:n]
+
+
+def reserve(table, held, wanted, stack, free, page, T, pages):
+    """A step of attn_cache_reserve on lists, one request after the other: table [B][max_blocks] and stack
+    [pages] are updated; returns (lens, cu, slots, positions, free)."""
+    up = lambda n: -(-n // page)  # noqa: E731
+    room = len(table[0]) * page
+    wanted = [w if 0 <= h <= room and 0 <= w <= room else h for h, w in zip(held, wanted)]
+    fine = [0 <= h <= room for h in held]
+    valid = lambda p: p if 0 <= p < pages else -1  # noqa: E731
+    free = min(max(free, 0), pages)
+    for b, (h, w) in enumerate(zip(held, wanted)):
+        for j in range(up(w), up(h)) if fine[b] else ():
+            if free < pages:
+                stack[free] = valid(table[b][j])
+            table[b][j] = -1
+            free += 1
+    free = min(free, pages)
+    lens, asked, took = [], 0, 0
+    for b, (h, w) in enumerate(zip(held, wanted)):
+        need = max(0, up(w) - up(h)) if fine[b] else 0
+        asked += need
+        serve = need == 0 or asked <= free
+        took += need * serve
+        lens.append(w if serve else h)
+    free -= took
+    at, cu, slots, positions = free, [0], [], []
+    for b, (h, w) in enumerate(zip(held, wanted)):
+        serve = lens[b] == w
+        for j in range(up(h), up(w)) if fine[b] else ():
+            table[b][j] = valid(stack[at]) if serve else -1
+            at += serve
+        for t in range(h, w):
+            p = valid(table[b][t // page])
+            slots.append(p * page + t % page if serve and p >= 0 else -1)
+            positions.append(t)
+        cu.append(len(slots))
+    fill = [-1] * max(0, T - len(slots))
+    return lens, cu, (slots + fill)[:T], (positions + fill)[:T], free
