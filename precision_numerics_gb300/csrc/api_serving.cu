@@ -93,6 +93,11 @@ attn_status check_shared(int B, int n_q, int H, int H_kv, int d, int page_size, 
   if (prefix_blocks < 1) return fail(ATTN_ERR_INVALID_ARG, "prefix_blocks must be >= 1 (got %d)", prefix_blocks);
   if (prefix_blocks > (INT_MAX - 4096) / page_size)
     return fail(ATTN_ERR_UNSUPPORTED, "prefix_blocks * page_size exceeds 2^31 positions");
+  // Tiles of 256 rows and 128 positions are counted in 32 bits.
+  const long long units = (((long long)B * n_q * (H / H_kv) - 1) / 256 + 1) * H_kv;
+  if (units * (((long long)prefix_blocks * page_size - 1) / 128 + 1) > INT_MAX - 1024)
+    return fail(ATTN_ERR_UNSUPPORTED, "B * n_q * H = %lld rows over %d blocks of prefix are not supported",
+                (long long)B * n_q * H, prefix_blocks);
   return ATTN_OK;
 }
 

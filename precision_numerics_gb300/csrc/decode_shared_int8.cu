@@ -16,10 +16,14 @@
 // 128 rows by 128 positions, accumulators in TMEM.  A CTA (one per SM) has two row tiles that
 // share each tile of keys; with up to 128 rows it has one, and its two halves take the
 // even and the odd key tiles of it.  Roles of the warps:
+//   warp 0            asks for the codes of the pages (bulk copies to a ring in shared memory) and
+//                     for their scales
+//   warps 12-15       codes to FP16, from the ring to swizzled tiles
+//   warp 1            issues the products
 //   warps 4-7, 8-11   softmax of row tile (or half) 0 and 1, one thread a row; also their Q rows
 //                     and the results' way out
-//   warps 12-15       codes to FP16: global memory -> registers -> swizzled shared memory
-//   warp 1            issues the products
+// Loads to registers are avoided where much is in flight: shared memory leaves L1 28 KB, and codes that
+// were loaded through it kept the warps that ask for them waiting (a key tile took 3.9 us).
 // The tiles of all (key head, row block) units, one behind the other, are dealt to the CTAs
 // in equal runs; every run leaves a part (m, l, O / l) of each unit it meets in the workspace.
 //
@@ -45,13 +49,13 @@ namespace {
 
 constexpr int kThreads = 512;
 // Registers a thread of the four warpgroups: products, softmax (two), codes.
-constexpr int kRegsMma = 48, kRegsSoftmax = 176, kRegsCodes = 112;
+constexpr int kRegsMma = 96, kRegsSoftmax = 160, kRegsCodes = 96;
 static_assert(kRegsMma + 2 * kRegsSoftmax + kRegsCodes <= 512, "setmaxnreg split exceeds the launch pool");
+static_assert(kRegsMma <= 128 && kRegsCodes <= 128 && kRegsSoftmax >= 128, "setmaxnreg directions");
 constexpr int kUnitRows = 256;  // rows of a unit: two tiles
 // Cost of a key tile where the unit has two row tiles, and where it has one.
 constexpr int kCostTwo = 3, kCostOne = 2;
 constexpr int kLeastRun = 2;  // key tiles of a run at least
-constexpr int kHeads = 8;     // key tiles whose scales are held
 constexpr float kSlack = 4.f;  // growth of a maximum (base 2) that the accumulators take as it is
 constexpr float kTop = 11.f;   // log2 of the largest weight just after its row's references moved
 
@@ -75,7 +79,8 @@ struct Args {
 // A part: O / l as [D / 4][256 rows][4], m [256], l [256].
 __host__ __device__ constexpr size_t part_floats(int d) { return (size_t)kUnitRows * (d + 2); }
 
-// How the key tiles of all units (unit = key head * row_blocks + row block) are dealt.
+// How the key tiles of all units (unit = key head * row_blocks + row block) are dealt.  Tiles of
+// all units together are below 2^31 (the host's check).
 struct Deal {
   int tiles;      // key tiles of the prefix
   int runs;       // that are not empty
@@ -89,12 +94,12 @@ struct Deal {
     runs = tiles == 0 ? 0 : (int)max(1ll, min((long long)a.runs, most));
   }
   // First tile (unit * tiles + key tile) of run c.
-  __device__ __forceinline__ long long begin(const Args& a, int c) const {
-    if (c >= runs) return (long long)a.Hkv * a.row_blocks * tiles;
+  __device__ __forceinline__ int begin(const Args& a, int c) const {
+    if (c >= runs) return a.Hkv * a.row_blocks * tiles;
     const long long x = head_cost * a.Hkv * c / runs, h = x / head_cost, y = x - h * head_cost;
     const long long full = (long long)kCostTwo * tiles * (a.row_blocks - 1);
     const long long i = y < full ? y / kCostTwo : (long long)tiles * (a.row_blocks - 1) + (y - full) / last_cost;
-    return h * a.row_blocks * tiles + i;
+    return (int)(h * a.row_blocks * tiles + i);
   }
 };
 
@@ -107,50 +112,68 @@ __device__ __forceinline__ int prefix_length(const Args& a, bool report) {
   return len < 0 ? 0 : (int)cap;
 }
 
-// The part of a run that lies in one unit.
-struct Segment {
-  int unit, h, rb, k0, nk;
-  bool two;  // two row tiles, else the tile's key tiles alternate between the two halves
-  int rows;  // of the unit
+// A run as every role goes through it: key tiles [k0, k0 + nk) of unit (h, rb), `left` tiles behind them.
+struct Walk {
+  int h, rb, k0, nk, left, tiles;
+  __device__ __forceinline__ Walk(const Args& a, const Deal& deal, bool none) {
+    tiles = deal.tiles;
+    const int at = none ? 0 : deal.begin(a, blockIdx.x);
+    left = none ? 0 : deal.begin(a, blockIdx.x + 1) - at;
+    const int unit = at / max(tiles, 1);
+    h = unit / a.row_blocks;
+    rb = unit - h * a.row_blocks;
+    k0 = at - unit * tiles;
+    nk = 0;
+  }
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (left == 0) return false;
+    if (nk > 0) {
+      k0 = 0;
+      if (++rb == a.row_blocks) rb = 0, ++h;
+    }
+    nk = min(tiles - k0, left);
+    left -= nk;
+    return true;
+  }
+  // Two row tiles; else the key tiles alternate between the two halves of the CTA.
+  __device__ __forceinline__ bool two(const Args& a) const { return a.rows - rb * kUnitRows > kBlockM; }
 };
-__device__ __forceinline__ bool next_segment(const Args& a, const Deal& deal, long long& at, long long end, Segment& s) {
-  if (at >= end) return false;
-  s.unit = (int)(at / deal.tiles);
-  s.k0 = (int)(at - (long long)s.unit * deal.tiles);
-  s.nk = (int)min((long long)(deal.tiles - s.k0), end - at);
-  s.h = s.unit / a.row_blocks;
-  s.rb = s.unit - s.h * a.row_blocks;
-  s.rows = min(kUnitRows, a.rows - s.rb * kUnitRows);
-  s.two = s.rows > kBlockM;
-  at += s.nk;
-  return true;
-}
-// Key tiles of half t.
-__device__ __forceinline__ int tiles_of(const Segment& s, int t) { return s.two ? s.nk : (s.nk + 1 - t) / 2; }
 
 // Scales of a key tile in groups of 16 positions, and how many of each are seen.
 struct Head {
   float ks[8], vs[8], log_vs[8];
   int seen[8];
-  int hidden;  // not all are seen
+  int hidden;         // not all are seen
+  unsigned loaded;    // bit per group that has codes
 };
 
 template <int D>
 struct Cfg {
-  static constexpr int kStagesK = 3;
-  static constexpr int kStagesV = D == 128 ? 2 : 3;
-  static constexpr int kChunks = D / 64;
+  static constexpr int kStages = D == 128 ? 2 : 3;  // of K and of V tiles
   static constexpr int kChunkBytes = 128 * 128;
   static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kRawBytes = 128 * D;  // K or V codes of a key tile
+  // Key tiles in the ring of codes; one more where all units have one row tile and the second
+  // one's Q has no need of its place.
+  static constexpr int kRawTiles = D == 128 ? 1 : 4;
+  // Key tiles whose scales are held.  Those of tile g are overwritten when the codes of tile g + kHeads -
+  // kRawTiles - 1 have been read from the ring; then S of the tile kStages + 1 before that one is complete, and
+  // the softmax is past the tile two before that.
+  static constexpr int kHeads = D == 128 ? 8 : 16;
+  static_assert(kHeads - (kRawTiles + 1) - (kStages + 1) - 2 >= 0, "scales stay until the softmax has used them");
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = 2 * kTileBytes;
-  static constexpr int kOffV = kOffK + kStagesK * kTileBytes;
-  static constexpr int kOffHead = kOffV + kStagesV * kTileBytes;
+  static constexpr int kOffRaw = 2 * kTileBytes;
+  static constexpr int kOffK = kOffRaw + 2 * kRawTiles * kRawBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffHead = kOffV + kStages * kTileBytes;
   static constexpr int kOffF = kOffHead + kHeads * (int)sizeof(Head);  // FP32 [2][128]: factor of a row's scores
   static constexpr int kOffBar = (kOffF + 2 * 128 * 4 + 15) / 16 * 16;
-  // k_full, k_empty [K], v_full, v_empty [V], head [kHeads], q [2], s_full [2], p_full [2], o_done [2], final
-  static constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + kHeads + 9;
+  static constexpr int kSlots = 2 * (kRawTiles + 1);
+  // raw_full, raw_empty [slots], k_full, k_empty, v_full, v_empty [stages], head [kHeads], q_raw [8],
+  // q [2], s_full [2], p_full [2], o_done [2], final
+  static constexpr int kNumBars = 2 * kSlots + 4 * kStages + kHeads + 17;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
+  static_assert(kTileBytes == 2 * kRawBytes, "the place of a Q tile holds a key tile's codes");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
   static constexpr uint32_t kTmemCols = 512;
   static __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
@@ -205,12 +228,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* bar_kfull = bars;
-  uint64_t* bar_kempty = bar_kfull + C::kStagesK;
-  uint64_t* bar_vfull = bar_kempty + C::kStagesK;
-  uint64_t* bar_vempty = bar_vfull + C::kStagesV;
-  uint64_t* bar_head = bar_vempty + C::kStagesV;
-  uint64_t* bar_q = bar_head + kHeads;
+  uint64_t* bar_rfull = bars;
+  uint64_t* bar_rempty = bar_rfull + C::kSlots;
+  uint64_t* bar_kfull = bar_rempty + C::kSlots;
+  uint64_t* bar_kempty = bar_kfull + C::kStages;
+  uint64_t* bar_vfull = bar_kempty + C::kStages;
+  uint64_t* bar_vempty = bar_vfull + C::kStages;
+  uint64_t* bar_head = bar_vempty + C::kStages;
+  uint64_t* bar_qraw = bar_head + C::kHeads;
+  uint64_t* bar_q = bar_qraw + 8;
   uint64_t* bar_sfull = bar_q + 2;
   uint64_t* bar_pfull = bar_sfull + 2;
   uint64_t* bar_odone = bar_pfull + 2;
@@ -221,15 +247,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
 
   if (threadIdx.x == 0) {
     tmem_slot[1] = (smem_u32(smem) & 1023u) != 0;
-    for (int s = 0; s < C::kStagesK; ++s) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&bar_rfull[s], 1);
+      mbar_init(&bar_rempty[s], 4);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bar_kfull[s], 128);
       mbar_init(&bar_kempty[s], 1);
-    }
-    for (int s = 0; s < C::kStagesV; ++s) {
       mbar_init(&bar_vfull[s], 128);
       mbar_init(&bar_vempty[s], 1);
     }
-    for (int s = 0; s < kHeads; ++s) mbar_init(&bar_head[s], 8);
+    for (int s = 0; s < C::kHeads; ++s) mbar_init(&bar_head[s], 1);
+    for (int s = 0; s < 8; ++s) mbar_init(&bar_qraw[s], 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar_q[t], 128);
       mbar_init(&bar_sfull[t], 1);
@@ -251,10 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   const bool abort_all = tmem_slot[1] != 0;
   if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
   const int len = prefix_length(a, threadIdx.x == 0 && blockIdx.x == 0);
-  const Deal deal(a, len);
-  long long at = abort_all ? 0 : deal.begin(a, blockIdx.x);
-  const long long end = abort_all ? 0 : deal.begin(a, blockIdx.x + 1);
-  Segment sg;
+  Walk sg(a, Deal(a, len), abort_all);
+  // All units have one row tile: one copy of Q, and a longer ring.
+  const bool one = a.rows <= kBlockM;
+  const int slots = one ? 2 * (C::kRawTiles + 1) : 2 * C::kRawTiles;
+  uint8_t* raw = smem + (one ? C::kTileBytes : C::kOffRaw);
 
   uint8_t* sQ = smem + C::kOffQ;
   uint8_t* sK = smem + C::kOffK;
@@ -262,7 +292,85 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-    if (warp == 1) {
+    if (warp == 0) {
+      // ------------------------------------------------------------ copies
+      // Lane x: group x % 8 (16 positions) of the tile, K in lanes 0 to 7, V in 8 to 15.  Page numbers of
+      // four key tiles are read at a time, scales a tile ahead.
+      const int group = lane & 7;
+      const bool is_v = lane >= 8;
+      const uint8_t* from = is_v ? a.v : a.k;
+      const float* scales = is_v ? a.v_scale : a.k_scale;
+      const int page_mask = (1 << a.page_shift) - 1;
+      bool ok = true;
+      int e = 0, first = -8, ids = -1, ids_next = -1;  // lane x: page of group x % 8 of key tile first + x / 8
+      auto pages_at = [&](int tile) {
+        const long long pos = ((long long)tile + (lane >> 3)) * kBlockN + 16 * group;
+        return pos < len ? __ldcg(a.table + (pos >> a.page_shift)) : -1;
+      };
+      auto page_of = [&](int tile) {
+        if (tile < first || tile >= first + 4) {
+          ids = tile == first + 4 ? ids_next : pages_at(tile);
+          first = tile;
+          ids_next = pages_at(tile + 4);
+          if (((long long)tile + (lane >> 3)) * kBlockN + 16 * group < len && (ids < 0 || ids >= a.P)) {
+            set_fail(ATTN_ERR_INVALID_ARG);
+            ids = -1;
+          }
+        }
+        return __shfl_sync(0xffffffffu, ids, (tile - first) * 8 + group);
+      };
+      bool more = sg.next(a);
+      int id = more ? page_of(sg.k0) : -1;
+      float scale = more && lane < 16 ? __ldcg(scales + (max(id, 0) * a.Hkv + sg.h)) : 0.f;
+      int issued = 0;
+      for (int g = 0; more; ++g) {
+        const int tile = sg.k0 + e, h = sg.h;
+        // K, then V.
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int slot = (2 * g + x) % slots, use = (2 * g + x) / slots;
+          if (use > 0) ok = ok && warp_wait(&bar_rempty[slot], (use - 1) & 1);
+          if (!ok) break;
+          const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
+          ++issued;
+          if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[slot], __popc(loaded) * 16 * D);
+          __syncwarp();
+          if (lane < 16 && is_v == (x == 1) && id >= 0)
+            bulk_load(raw + slot * C::kRawBytes + group * 16 * D,
+                      from + (size_t)(((id * a.Hkv + h) << a.page_shift) + ((16 * group) & page_mask)) * D, 16 * D,
+                      &bar_rfull[slot]);
+        }
+        if (!ok) break;
+        // The slot's last tile, kHeads before, has been through the softmax: the ring's place was free, so the
+        // products S of the tile that many tiles and stages ago are complete.
+        Head& hd = heads[g % C::kHeads];
+        const int seen = id >= 0 ? max(0, min(16, len - (tile * kBlockN + 16 * group))) : 0;
+        const bool hidden = __any_sync(0xffffffffu, seen < 16);
+        const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
+        if (lane < 8) {
+          hd.ks[group] = scale;
+          hd.seen[group] = seen;
+        } else if (lane < 16) {
+          hd.vs[group] = scale;
+          hd.log_vs[group] = fmaxf(__log2f(scale), -126.f);
+        }
+        if (lane == 0) hd.hidden = hidden, hd.loaded = loaded;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_head[g % C::kHeads]);
+        if (++e == sg.nk) {
+          e = 0;
+          more = sg.next(a);
+        }
+        if (more) {
+          id = page_of(sg.k0 + e);
+          // A page that is not seen takes any scale: its positions are hidden.
+          if (lane < 16) scale = __ldcg(scales + (max(id, 0) * a.Hkv + sg.h));
+        }
+      }
+      if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
+      // Do not leave while copies into this CTA's shared memory are in flight.
+      for (int x = max(0, issued - slots); x < issued; ++x) mbar_wait(&bar_rfull[x % slots], (x / slots) & 1);
+    } else if (warp == 1) {
       // ------------------------------------------------------------ products
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, false);
       constexpr uint32_t idesc_pv = idesc_f16(128, D, true);
@@ -270,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       const uint64_t descK = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t descV = sdesc_sw128(smem_u32(sV), C::kChunkBytes, 1024);
       auto issue_s = [&](int t, int st) {
-        const uint64_t a0 = sdesc_add(descQ, t * C::kTileBytes);
+        const uint64_t a0 = sdesc_add(descQ, one ? 0 : t * C::kTileBytes);
         const uint64_t b0 = sdesc_add(descK, st * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -290,20 +398,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       int g = 0, items = 0;
       int pc[2] = {0, 0};
       auto k_ready = [&](int i) {
-        const bool r = warp_wait(&bar_kfull[i % C::kStagesK], (i / C::kStagesK) & 1);
+        const bool r = warp_wait(&bar_kfull[i % C::kStages], (i / C::kStages) & 1);
+        // The threads that wrote the codes leave the fence to this warp: theirs would wait for the loads
+        // that they have in flight.
+        fence_proxy_async_smem();
         tc_fence_after();
         return r;
       };
-      while (ok && next_segment(a, deal, at, end, sg)) {
+      while (ok && sg.next(a)) {
+        const bool two = sg.two(a);
         // S_t's columns are free: the P V products issued before read them first.
-        ok = warp_wait(&bar_q[0], items & 1) && warp_wait(&bar_q[1], items & 1);
+        ok = warp_wait(&bar_q[0], items & 1) && (one || warp_wait(&bar_q[1], items & 1));
         ++items;
-        const int step = sg.two ? 1 : 2;  // key tiles from one of a half's to its next
+        const int step = two ? 1 : 2;  // key tiles from one of a half's to its next
         // S of key tile e, of one half or both.
         auto s_of = [&](int e) {
           if (!k_ready(g + e)) return false;
-          const int st = (g + e) % C::kStagesK;
-          if (sg.two) {
+          const int st = (g + e) % C::kStages;
+          if (two) {
             issue_s(0, st);
             issue_s(1, st);
           } else {
@@ -313,29 +425,30 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           return true;
         };
         ok = ok && s_of(0);
-        if (!sg.two && sg.nk > 1) ok = ok && s_of(1);
+        if (!two && sg.nk > 1) ok = ok && s_of(1);
         for (int e = 0; e < sg.nk && ok; ++e) {
-          const int st = (g + e) % C::kStagesV;
+          const int st = (g + e) % C::kStages;
           const bool more = e + step < sg.nk;
-          ok = warp_wait(&bar_vfull[st], ((g + e) / C::kStagesV) & 1);
-          if (ok && sg.two && more) ok = k_ready(g + e + 1);
+          ok = warp_wait(&bar_vfull[st], ((g + e) / C::kStages) & 1);
+          fence_proxy_async_smem();
+          if (ok && two && more) ok = k_ready(g + e + 1);
           for (int t = 0; t < 2 && ok; ++t) {
-            if (!sg.two && t != (e & 1)) continue;
+            if (!two && t != (e & 1)) continue;
             ok = warp_wait(&bar_pfull[t], pc[t] & 1);
             if (!ok) break;
             ++pc[t];
             tc_fence_after();
             issue_pv(t, st, e >= step);
             if (!more) mma_commit_elect(&bar_odone[t]);
-            if (sg.two && more) issue_s(t, (g + e + 1) % C::kStagesK);
+            if (two && more) issue_s(t, (g + e + 1) % C::kStages);
           }
           if (!ok) break;
           mma_commit_elect(&bar_vempty[st]);
-          if (sg.two && more) mma_commit_elect(&bar_kempty[(g + e + 1) % C::kStagesK]);
-          if (!sg.two && more) ok = s_of(e + 2);
+          if (two && more) mma_commit_elect(&bar_kempty[(g + e + 1) % C::kStages]);
+          if (!two && more) ok = s_of(e + 2);
         }
         // A half without a key tile is told too: it waits for the segment's end before the next.
-        if (ok && !sg.two && sg.nk == 1) mma_commit_elect(&bar_odone[1]);
+        if (ok && !two && sg.nk == 1) mma_commit_elect(&bar_odone[1]);
         g += sg.nk;
       }
       if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
@@ -347,125 +460,65 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCodes));
     // --------------------------------------------------------------- codes
-    // A thread has one 16-byte unit of a row, 128 / kPasses rows of the tile at a time, and
-    // holds the next tile's codes in registers while it waits for room for them.
+    // A thread has one 16-byte unit of a row, kPasses rows of a tile.
     constexpr int kUnits = D / 16, kRows = 128 / kUnits, kPasses = 128 / kRows;
     const int tid = threadIdx.x - 384, unit = tid % kUnits, row = tid / kUnits;
     bool ok = true;
-    long long at_l = at;  // of the tile that is loaded
-    Segment sl;
-    bool more = next_segment(a, deal, at_l, end, sl);
-    int e_l = 0;
-    // Lane x < 8: the page of positions [16 x, 16 x + 16) of key tile sl.k0 + e_l, or -1.
-    auto page_at = [&](int tile) {
-      const long long pos = (long long)tile * kBlockN + 16 * (lane & 7);
-      int id = -1;
-      if (pos < len) {
-        id = __ldcg(a.table + (pos >> a.page_shift));
-        if (id < 0 || id >= a.P) {
-          set_fail(ATTN_ERR_INVALID_ARG);
-          id = -1;
-        }
+    // Slot x of the ring to the tile at `to`, which is free when `empty` has completed its phase.
+    auto convert = [&](int x, unsigned loaded, uint32_t to, uint64_t* empty, int phase) {
+      const int slot = x % slots;
+      if (!warp_wait(&bar_rfull[slot], (x / slots) & 1)) return false;
+      uint4 w[kPasses];
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[p].x), "=r"(w[p].y), "=r"(w[p].z), "=r"(w[p].w)
+                     : "r"(smem_u32(raw) + slot * C::kRawBytes + (p * kRows + row) * D + unit * 16)
+                     : "memory");
       }
-      return id;
-    };
-    uint4 raw_k[kPasses], raw_v[kPasses];
-    int id = -1;
-    auto load = [&](const uint8_t* from, uint4 (&raw)[kPasses]) {
+      if (loaded != 0xffu) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p)
+          if (!((loaded >> ((p * kRows + row) >> 4)) & 1u)) w[p] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_rempty[slot]);
+      if (phase >= 0 && !warp_wait(empty, phase & 1)) return false;
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
         const int r = p * kRows + row;
-        const int page = __shfl_sync(0xffffffffu, id, r >> 4);
-        const int in_page = ((sl.k0 + e_l) * kBlockN + r) & ((1 << a.page_shift) - 1);
-        raw[p] = make_uint4(0u, 0u, 0u, 0u);
-        if (page >= 0)
-          raw[p] = __ldcg(reinterpret_cast<const uint4*>(
-              from + ((((long long)page * a.Hkv + sl.h) << a.page_shift) + in_page) * D + unit * 16));
-      }
-    };
-    auto put = [&](uint8_t* tile, const uint4 (&raw)[kPasses]) {
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int r = p * kRows + row;
-        const uint32_t w[4] = {raw[p].x ^ 0x80808080u, raw[p].y ^ 0x80808080u, raw[p].z ^ 0x80808080u,
-                               raw[p].w ^ 0x80808080u};
-        uint32_t x[8];
+        const uint32_t c[4] = {w[p].x ^ 0x80808080u, w[p].y ^ 0x80808080u, w[p].z ^ 0x80808080u, w[p].w ^ 0x80808080u};
+        uint32_t y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[2 * i] = codes_f16(w[i], 0x4140u);
-          x[2 * i + 1] = codes_f16(w[i], 0x4342u);
+          y[2 * i] = codes_f16(c[i], 0x4140u);
+          y[2 * i + 1] = codes_f16(c[i], 0x4342u);
         }
-        const uint32_t to = smem_u32(tile) + (unit >> 2) * C::kChunkBytes;
-        const uint32_t u = (unit & 3) * 2;
+        const uint32_t at = to + (unit >> 2) * C::kChunkBytes;
         // The eight lanes of a phase have one row of d = 128: those of its second chunk store
-        // their units in the other order, so that all banks are met.
-        if (unit < 4) {
-          st_shared_v4(to + sw128_offset(r, u), x[0], x[1], x[2], x[3]);
-          st_shared_v4(to + sw128_offset(r, u + 1), x[4], x[5], x[6], x[7]);
-        } else {
-          st_shared_v4(to + sw128_offset(r, u + 1), x[4], x[5], x[6], x[7]);
-          st_shared_v4(to + sw128_offset(r, u), x[0], x[1], x[2], x[3]);
-        }
+        // their two units in the other order, so that all banks are met.
+        const uint32_t u = (unit & 3) * 2, swap = unit >> 2;
+        const bool sw = swap != 0;
+        st_shared_v4(at + sw128_offset(r, u + swap), sw ? y[4] : y[0], sw ? y[5] : y[1], sw ? y[6] : y[2],
+                     sw ? y[7] : y[3]);
+        st_shared_v4(at + sw128_offset(r, u + 1 - swap), sw ? y[0] : y[4], sw ? y[1] : y[5], sw ? y[2] : y[6],
+                     sw ? y[3] : y[7]);
       }
+      return true;
     };
-    int id_next = -1;
-    float ks = 0.f, vs = 0.f;
-    auto load_scales = [&]() {
-      if (warp == 12 && lane < 8) {
-        const size_t i = (size_t)max(id, 0) * a.Hkv + sl.h;
-        ks = id >= 0 ? __ldcg(a.k_scale + i) : 0.f;
-        vs = id >= 0 ? __ldcg(a.v_scale + i) : 0.f;
-      }
-    };
-    if (more) {
-      id = page_at(sl.k0);
-      load_scales();
-      load(a.k, raw_k);
-      load(a.v, raw_v);
-    }
-    for (int g = 0; more; ++g) {
-      const int stk = g % C::kStagesK, stv = g % C::kStagesV;
-      // The tile behind this one.
-      Segment sn = sl;
-      int e_n = e_l + 1;
-      bool more_n = true;
-      if (e_n == sl.nk) {
-        e_n = 0;
-        more_n = next_segment(a, deal, at_l, end, sn);
-      }
-      id_next = more_n ? page_at(sn.k0 + e_n) : -1;
-      if (g >= C::kStagesK) ok = warp_wait(&bar_kempty[stk], (g / C::kStagesK - 1) & 1);
-      if (!ok) break;
-      if (warp == 12 && lane < 8) {
-        // The slot's last tile, kHeads before, has been through the softmax: the products S of
-        // kStagesK tiles ago are complete, and were issued behind P V of the tile before.
-        Head& hd = heads[g % kHeads];
-        const int pos = (sl.k0 + e_l) * kBlockN + 16 * lane;
-        const int seen = id >= 0 ? max(0, min(16, len - pos)) : 0;
-        hd.ks[lane] = ks;
-        hd.vs[lane] = vs;
-        hd.log_vs[lane] = fmaxf(__log2f(vs), -126.f);
-        hd.seen[lane] = seen;
-        const bool hidden = __any_sync(0xffu, seen < 16);
-        if (lane == 0) hd.hidden = hidden;
-        mbar_arrive(&bar_head[g % kHeads]);
-      }
-      put(sK + stk * C::kTileBytes, raw_k);
-      fence_proxy_async_smem();
-      mbar_arrive(&bar_kfull[stk]);
-      if (g >= C::kStagesV) ok = warp_wait(&bar_vempty[stv], (g / C::kStagesV - 1) & 1);
-      if (!ok) break;
-      put(sV + stv * C::kTileBytes, raw_v);
-      fence_proxy_async_smem();
-      mbar_arrive(&bar_vfull[stv]);
-      sl = sn;
-      e_l = e_n;
-      more = more_n;
-      id = id_next;
-      if (more) {
-        load_scales();
-        load(a.k, raw_k);
-        load(a.v, raw_v);
+    int g = 0;
+    while (ok && sg.next(a)) {
+      for (int e = 0; e < sg.nk; ++e, ++g) {
+        const int st = g % C::kStages, phase = g / C::kStages - 1;
+        ok = warp_wait(&bar_head[g % C::kHeads], (g / C::kHeads) & 1);
+        if (!ok) break;
+        const unsigned loaded = heads[g % C::kHeads].loaded;
+        ok = convert(2 * g, loaded, smem_u32(sK) + st * C::kTileBytes, &bar_kempty[st], phase);
+        if (!ok) break;
+        mbar_arrive(&bar_kfull[st]);
+        ok = convert(2 * g + 1, loaded, smem_u32(sV) + st * C::kTileBytes, &bar_vempty[st], phase);
+        if (!ok) break;
+        mbar_arrive(&bar_vfull[st]);
       }
     }
     if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
@@ -479,36 +532,50 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     const uint32_t tO = tmem + lane_off + C::col_o(t);
     bool ok = true;
     int sc = 0, oc = 0;  // S tiles consumed, segments completed
-    int g = 0;           // key tiles of the segments before
-    while (ok && next_segment(a, deal, at, end, sg)) {
-      const int first = sg.rb * kUnitRows + (sg.two ? t * kBlockM : 0);  // the tile's first row
+    int g = 0, items = 0;  // key tiles and number of the segments before
+    while (ok && sg.next(a)) {
+      const bool two = sg.two(a);
+      const int first = sg.rb * kUnitRows + (two ? t * kBlockM : 0);  // the tile's first row
       const int have = min(kBlockM, a.rows - first);                     // and how many it has
       // -------------------------------------------------------- Q rows
-      // This warp's 32 rows, kLanes lanes a row.  The products that read the rows before are
-      // complete: the softmax has had their results.
-      {
+      // This warp's 32 rows, a lane each, are copied to their places in the tile and there divided and
+      // swizzled (which moves units within 128 bytes), kLanes lanes a row.  The products that read
+      // the rows before are complete: the softmax has had their results, of both halves where they share them.
+      if (!one || t == 0) {
+        if (one && items > 0) {
+          ok = warp_wait(&bar_odone[1], (items - 1) & 1);
+          if (!ok) break;
+        }
+        const uint32_t tile_q = smem_u32(sQ) + t * C::kTileBytes;
+        fence_proxy_async_smem();
+        if (lane == 0) mbar_arrive_expect_tx(&bar_qraw[warp - 4], max(0, min(32, have - w0)) * D * 2);
+        __syncwarp();
+        if (r < have) {
+          int b, tok, gg;
+          row_of(a, first + r, b, tok, gg);
+          const uint16_t* from = a.q + b * a.q_batch + tok * a.q_token + (long long)(sg.h * a.G + gg) * a.q_head;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            bulk_load(sQ + t * C::kTileBytes + c * C::kChunkBytes + r * 128, from + c * 64, 128, &bar_qraw[warp - 4]);
+        }
+        ok = warp_wait(&bar_qraw[warp - 4], items & 1);
+        if (!ok) break;
         constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kAtOnce;
         const int u = lane % kLanes;
-        uint4 x[kTurns];
-#pragma unroll
+        const uint32_t chunk = tile_q + (u >> 3) * C::kChunkBytes;
+#pragma unroll 4
         for (int i = 0; i < kTurns; ++i) {
           const int rr = w0 + i * kAtOnce + lane / kLanes;
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < have) {
-            int b, tok, gg;
-            row_of(a, first + rr, b, tok, gg);
-            x[i] = __ldcg(reinterpret_cast<const uint4*>(a.q + b * a.q_batch + tok * a.q_token +
-                                                         (long long)(sg.h * a.G + gg) * a.q_head + u * 8));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-          const int rr = w0 + i * kAtOnce + lane / kLanes;
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          if (rr < have)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(chunk + rr * 128 + (u & 7) * 16)
+                         : "memory");
           float m = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+          for (int k = 0; k < 4; ++k)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
 #pragma unroll
           for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
           // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
@@ -518,22 +585,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             y[k] = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          st_shared_v4(smem_u32(sQ) + t * C::kTileBytes + (u >> 3) * C::kChunkBytes + sw128_offset(rr, u & 7), y[0],
-                       y[1], y[2], y[3]);
+          // (All lanes of the row have read it: the maximum needed them.)
+          st_shared_v4(chunk + sw128_offset(rr, u & 7), y[0], y[1], y[2], y[3]);
           if (u == 0) s_f[t * 128 + rr] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
         }
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive(&bar_q[t]);
       }
-      const float f = s_f[t * 128 + r];
-      const int n = tiles_of(sg, t);
+      ++items;
+      // (One copy: half 1 reads the factors after the first scores, which waited for all of Q.)
+      float f = 0.f;
+      const int n = two ? sg.nk : (sg.nk + 1 - t) / 2;  // key tiles of this half
       const bool idle = w0 >= have;  // none of the warp's rows is one
       float m_ref = -INFINITY, E = 0.f, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
         ok = warp_wait(&bar_sfull[t], (sc + j) & 1);
-        const int tile = g + (sg.two ? j : 2 * j + t);
-        if (ok) ok = warp_wait(&bar_head[tile % kHeads], (tile / kHeads) & 1);
+        const int tile = g + (two ? j : 2 * j + t);
+        if (ok) ok = warp_wait(&bar_head[tile % C::kHeads], (tile / C::kHeads) & 1);
         if (!ok) break;
         tc_fence_after();
         if (idle) {
@@ -541,59 +610,62 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           mbar_arrive(&bar_pfull[t]);
           continue;
         }
-        const Head& hd = heads[tile % kHeads];
-        uint32_t s[4][32];
+        if (j == 0) f = s_f[(one ? 0 : t * 128) + r];
+        const Head& hd = heads[tile % C::kHeads];
+        // The scores are read from TMEM twice, 64 columns at a time: for their maxima, then for the
+        // weights.  Held in between they would take more registers than there are (and spills go past an L1
+        // that shared memory leaves no room).
+        auto scores = [&](int half, uint32_t (&s)[2][32]) {
+          tmem_ld32(tS + half * 64, s[0]);
+          tmem_ld32(tS + half * 64 + 32, s[1]);
+          tmem_wait_ld();
+          reg_fence(s[0]);
+          reg_fence(s[1]);
+          if (hd.hidden) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
-        tmem_wait_ld();
+            for (int i = 0; i < 4; ++i) {
+              const int seen = hd.seen[half * 4 + i];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence(s[c]);
-        // Scores in base 2.
-        constexpr int kGroups = 128 / GROUP;
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          const float k = f * hd.ks[i * GROUP / 16];
-          const uint64_t k2 = f2_pack(k, k);
-#pragma unroll
-          for (int x = i * GROUP; x < (i + 1) * GROUP; x += 2) {
-            float lo, hi;
-            f2_unpack(mul2(f2_pack(__uint_as_float(s[x >> 5][x & 31]), __uint_as_float(s[x >> 5][(x & 31) + 1])), k2),
-                      lo, hi);
-            s[x >> 5][x & 31] = __float_as_uint(lo);
-            s[x >> 5][(x & 31) + 1] = __float_as_uint(hi);
+              for (int x = 0; x < 16; ++x)
+                if (x >= seen) s[i >> 1][(i & 1) * 16 + x] = __float_as_uint(-INFINITY);
+            }
           }
-        }
-        if (hd.hidden) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int seen = hd.seen[i];
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (x >= seen) s[i >> 1][(i & 1) * 16 + x] = __float_as_uint(-INFINITY);
-          }
-        }
+        };
+        // Factor of a group's scores (base 2); not 0, so that hidden ones stay -inf.
+        auto factor = [&](int group) { return fmaxf(f * hd.ks[group * (GROUP / 16)], 0x1p-126f); };
+        constexpr int kHalf = 64 / GROUP;  // groups of 64 columns
         float mt = -INFINITY, mw = -INFINITY;  // largest score and largest log2 of a weight
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t s[2][32];
+          scores(half, s);
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          const int x0 = i * GROUP;
-          float m = fmaxf(__uint_as_float(s[x0 >> 5][x0 & 31]), __uint_as_float(s[x0 >> 5][(x0 & 31) + 1]));
+          for (int i = 0; i < kHalf; ++i) {
+            const int x0 = i * GROUP;
+            float m = fmaxf(__uint_as_float(s[x0 >> 5][x0 & 31]), __uint_as_float(s[x0 >> 5][(x0 & 31) + 1]));
 #pragma unroll
-          for (int x = x0 + 2; x < x0 + GROUP; x += 2)
-            m = fmax3(m, __uint_as_float(s[x >> 5][x & 31]), __uint_as_float(s[x >> 5][(x & 31) + 1]));
-          mt = fmaxf(mt, m);
-          mw = fmaxf(mw, m + hd.log_vs[i * GROUP / 16]);
+            for (int x = x0 + 2; x < x0 + GROUP; x += 2)
+              m = fmax3(m, __uint_as_float(s[x >> 5][x & 31]), __uint_as_float(s[x >> 5][(x & 31) + 1]));
+            m *= factor(half * kHalf + i);
+            mt = fmaxf(mt, m);
+            mw = fmaxf(mw, m + hd.log_vs[(half * kHalf + i) * (GROUP / 16)]);
+          }
         }
-        // The largest weight so far is 2^(m_ref - (E - kTop)) or less by kSlack.
-        if (__any_sync(0xffffffffu, fmaxf(mt, mw + (E - kTop)) > m_ref + kSlack)) {
-          const float m_new = fmaxf(m_ref, mt);
-          const bool some = m_new != -INFINITY;
-          const float w_new = fmaxf(m_ref - (E - kTop), mw);
-          const float e_new = some ? fminf(rintf(m_new - w_new) + kTop, 126.f) : 0.f;
-          const float back = some ? m_ref - m_new : 0.f;
-          l_run *= ex2(back);
-          const float f_o = ex2(back + (e_new - E));
-          m_ref = m_new;
-          E = e_new;
+        // The largest weight so far is 2^(m_ref - (E - kTop)) or less by kSlack.  Rows whose references
+        // stay have factors of 1: no row's bits depend on another's.
+        const bool moves = fmaxf(mt, mw + (E - kTop)) > m_ref + kSlack;
+        if (__any_sync(0xffffffffu, moves)) {
+          float f_o = 1.f;
+          if (moves) {
+            const float m_new = fmaxf(m_ref, mt);  // not -inf
+            const float w_new = fmaxf(m_ref - (E - kTop), mw);
+            const float e_new = fminf(rintf(m_new - w_new) + kTop, 126.f);
+            const float back = m_ref - m_new;
+            l_run *= ex2(back);
+            f_o = ex2(back + (e_new - E));
+            m_ref = m_new;
+            E = e_new;
+          }
           if (j > 0) {
             const uint64_t f2 = f2_pack(f_o, f_o);
 #pragma unroll
@@ -615,24 +687,44 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         }
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         const float up = power2(E);
+        // The fma below leaves the rounding of the largest score's product, half its last bit, in the
+        // exponent.  From 2^24 on that could take a weight out of FP16: a row's products are rounded first then.
+        const bool large = fabsf(m_use) >= 0x1p24f;
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
         uint64_t sums2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sums2[i] = 0ull;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t s[2][32];
+          scores(half, s);
+          float k[kHalf];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+          for (int i = 0; i < kHalf; ++i) k[i] = factor(half * kHalf + i);
+          if (__any_sync(0xffffffffu, large)) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float v = fminf(hd.vs[(c * 32 + 2 * i) / GROUP * (GROUP / 16)] * up, 0x1p127f);
-            float x0, x1;
-            f2_unpack(add2(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), nm2), x0, x1);
-            const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
-            sums2[i & 3] = add2(sums2[i & 3], p2);
-            f2_unpack(mul2(p2, f2_pack(v, v)), x0, x1);
-            pk[i] = pack_f16x2(x0, x1);
+            for (int x = 0; x < 64; ++x)
+              s[x >> 5][x & 31] = __float_as_uint(__uint_as_float(s[x >> 5][x & 31]) * (large ? k[x / GROUP] : 1.f));
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) k[i] = large ? 1.f : k[i];
           }
-          tmem_st16(tS + c * 16, pk);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int group = (c * 32 + 2 * i) / GROUP;
+              const float v = fminf(hd.vs[(half * kHalf + group) * (GROUP / 16)] * up, 0x1p127f);
+              float x0, x1;
+              f2_unpack(fma2(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])),
+                             f2_pack(k[group], k[group]), nm2), x0, x1);
+              const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
+              sums2[i & 3] = add2(sums2[i & 3], p2);
+              f2_unpack(mul2(p2, f2_pack(v, v)), x0, x1);
+              pk[i] = pack_f16x2(x0, x1);
+            }
+            tmem_st16(tS + half * 32 + c * 16, pk);
+          }
         }
         float sums[8];
 #pragma unroll
@@ -650,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       if (!ok) break;
       ++oc;
       tc_fence_after();
-      float* part = a.parts + (size_t)(blockIdx.x + sg.unit) * part_floats(D);
+      float* part = a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D);
       const int pr = t * kBlockM + r;  // row within the part
       const float inv = inverse(l_run), down = power2(-E);
       if (!idle) {
@@ -706,9 +798,9 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a)
   if (rb * kUnitRows + rows0 >= a.rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Deal deal(a, prefix_length(a, false));
-  const long long from = (long long)unit * deal.tiles, to = from + deal.tiles;
-  const long long mine = threadIdx.x < deal.runs ? deal.begin(a, threadIdx.x) : to;
-  int c0 = __syncthreads_count(mine <= from && (int)threadIdx.x < deal.runs) - 1;
+  const int from = unit * deal.tiles, to = from + deal.tiles;
+  const int mine = threadIdx.x < deal.runs ? deal.begin(a, threadIdx.x) : to;
+  const int c0 = __syncthreads_count(mine <= from && (int)threadIdx.x < deal.runs) - 1;
   const int c1 = __syncthreads_count(mine < to) - 1;
   const int r = rows0 + lane, row = rb * kUnitRows + r;
   if (row >= a.rows) return;
