@@ -396,56 +396,46 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       };
       bool ok = true;
       int g = 0, items = 0;
-      int pc[2] = {0, 0};
-      auto k_ready = [&](int i) {
-        const bool r = warp_wait(&bar_kfull[i % C::kStages], (i / C::kStages) & 1);
-        // The threads that wrote the codes leave the fence to this warp: theirs would wait for the loads
-        // that they have in flight.
-        fence_proxy_async_smem();
-        tc_fence_after();
-        return r;
-      };
+      unsigned pc = 0;  // bit t: phase of P_t
       while (ok && sg.next(a)) {
         const bool two = sg.two(a);
         // S_t's columns are free: the P V products issued before read them first.
         ok = warp_wait(&bar_q[0], items & 1) && (one || warp_wait(&bar_q[1], items & 1));
         ++items;
-        const int step = two ? 1 : 2;  // key tiles from one of a half's to its next
-        // S of key tile e, of one half or both.
-        auto s_of = [&](int e) {
-          if (!k_ready(g + e)) return false;
-          const int st = (g + e) % C::kStages;
-          if (two) {
-            issue_s(0, st);
-            issue_s(1, st);
-          } else {
-            issue_s(e & 1, st);
-          }
-          mma_commit_elect(&bar_kempty[st]);
-          return true;
-        };
-        ok = ok && s_of(0);
-        if (!two && sg.nk > 1) ok = ok && s_of(1);
-        for (int e = 0; e < sg.nk && ok; ++e) {
-          const int st = (g + e) % C::kStages;
-          const bool more = e + step < sg.nk;
-          ok = warp_wait(&bar_vfull[st], ((g + e) / C::kStages) & 1);
-          fence_proxy_async_smem();
-          if (ok && two && more) ok = k_ready(g + e + 1);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (!two && t != (e & 1)) continue;
-            ok = warp_wait(&bar_pfull[t], pc[t] & 1);
-            if (!ok) break;
-            ++pc[t];
-            tc_fence_after();
-            issue_pv(t, st, e >= step);
-            if (!more) mma_commit_elect(&bar_odone[t]);
-            if (two && more) issue_s(t, (g + e + 1) % C::kStages);
+        // Step e: P V of key tile e - lag, then S of key tile e, of both halves, or of the half whose turn it is.
+        const int lag = two ? 1 : 2;
+#pragma unroll 1
+        for (int e = 0; e < sg.nk + lag && ok; ++e) {
+          const int i = e - lag;  // the tile of P V
+          const bool pv = i >= 0, qk = e < sg.nk;
+          const int sv = pv ? (g + i) % C::kStages : 0, sk = (g + e) % C::kStages;
+#pragma unroll 1
+          for (int t = two ? 0 : e & 1; t < (two ? 2 : (e & 1) + 1) && ok; ++t) {
+            const bool first = !two || t == 0;
+            if (pv) {
+              // The threads that wrote the codes leave the fence to this warp.
+              if (first) ok = warp_wait(&bar_vfull[sv], ((g + i) / C::kStages) & 1);
+              ok = ok && warp_wait(&bar_pfull[t], (pc >> t) & 1);
+              if (!ok) break;
+              pc ^= 1u << t;
+              if (first) fence_proxy_async_smem();
+              tc_fence_after();
+              issue_pv(t, sv, i >= lag);
+              if (!qk) mma_commit_elect(&bar_odone[t]);
+            }
+            if (qk) {
+              if (first) {
+                ok = warp_wait(&bar_kfull[sk], ((g + e) / C::kStages) & 1);
+                if (!ok) break;
+                fence_proxy_async_smem();
+                tc_fence_after();
+              }
+              issue_s(t, sk);
+            }
           }
           if (!ok) break;
-          mma_commit_elect(&bar_vempty[st]);
-          if (two && more) mma_commit_elect(&bar_kempty[(g + e + 1) % C::kStages]);
-          if (!two && more) ok = s_of(e + 2);
+          if (pv) mma_commit_elect(&bar_vempty[sv]);
+          if (qk) mma_commit_elect(&bar_kempty[sk]);
         }
         // A half without a key tile is told too: it waits for the segment's end before the next.
         if (ok && !two && sg.nk == 1) mma_commit_elect(&bar_odone[1]);
@@ -465,6 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     const int tid = threadIdx.x - 384, unit = tid % kUnits, row = tid / kUnits;
     bool ok = true;
     // Slot x of the ring to the tile at `to`, which is free when `empty` has completed its phase.
+    const uint32_t swap = unit >> 2, u = (unit & 3) * 2;
+    // The eight lanes of a phase have one row of d = 128: those of its second chunk store their two
+    // units in the other order, so that all banks are met.  (All rows of a thread have the same swizzle.)
+    const uint32_t to0 = swap * C::kChunkBytes + sw128_offset(row, u + swap);
+    const uint32_t to1 = swap * C::kChunkBytes + sw128_offset(row, u + 1 - swap);
     auto convert = [&](int x, unsigned loaded, uint32_t to, uint64_t* empty, int phase) {
       const int slot = x % slots;
       if (!warp_wait(&bar_rfull[slot], (x / slots) & 1)) return false;
@@ -486,23 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       if (phase >= 0 && !warp_wait(empty, phase & 1)) return false;
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
-        const int r = p * kRows + row;
-        const uint32_t c[4] = {w[p].x ^ 0x80808080u, w[p].y ^ 0x80808080u, w[p].z ^ 0x80808080u, w[p].w ^ 0x80808080u};
-        uint32_t y[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[2 * i] = codes_f16(c[i], 0x4140u);
-          y[2 * i + 1] = codes_f16(c[i], 0x4342u);
-        }
-        const uint32_t at = to + (unit >> 2) * C::kChunkBytes;
-        // The eight lanes of a phase have one row of d = 128: those of its second chunk store
-        // their two units in the other order, so that all banks are met.
-        const uint32_t u = (unit & 3) * 2, swap = unit >> 2;
-        const bool sw = swap != 0;
-        st_shared_v4(at + sw128_offset(r, u + swap), sw ? y[4] : y[0], sw ? y[5] : y[1], sw ? y[6] : y[2],
-                     sw ? y[7] : y[3]);
-        st_shared_v4(at + sw128_offset(r, u + 1 - swap), sw ? y[0] : y[4], sw ? y[1] : y[5], sw ? y[2] : y[6],
-                     sw ? y[3] : y[7]);
+        const uint32_t c[4] = {(swap ? w[p].z : w[p].x) ^ 0x80808080u, (swap ? w[p].w : w[p].y) ^ 0x80808080u,
+                               (swap ? w[p].x : w[p].z) ^ 0x80808080u, (swap ? w[p].y : w[p].w) ^ 0x80808080u};
+        st_shared_v4(to + to0 + p * kRows * 128, codes_f16(c[0], 0x4140u), codes_f16(c[0], 0x4342u),
+                     codes_f16(c[1], 0x4140u), codes_f16(c[1], 0x4342u));
+        st_shared_v4(to + to1 + p * kRows * 128, codes_f16(c[2], 0x4140u), codes_f16(c[2], 0x4342u),
+                     codes_f16(c[3], 0x4140u), codes_f16(c[3], 0x4342u));
       }
       return true;
     };
@@ -513,12 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         ok = warp_wait(&bar_head[g % C::kHeads], (g / C::kHeads) & 1);
         if (!ok) break;
         const unsigned loaded = heads[g % C::kHeads].loaded;
-        ok = convert(2 * g, loaded, smem_u32(sK) + st * C::kTileBytes, &bar_kempty[st], phase);
+#pragma unroll 1
+        for (int x = 0; x < 2 && ok; ++x) {  // K, V
+          uint64_t* full = (x == 0 ? bar_kfull : bar_vfull) + st;
+          ok = convert(2 * g + x, loaded, smem_u32(x == 0 ? sK : sV) + st * C::kTileBytes, full + C::kStages, phase);
+          if (ok) mbar_arrive(full);
+        }
         if (!ok) break;
-        mbar_arrive(&bar_kfull[st]);
-        ok = convert(2 * g + 1, loaded, smem_u32(sV) + st * C::kTileBytes, &bar_vempty[st], phase);
-        if (!ok) break;
-        mbar_arrive(&bar_vfull[st]);
       }
     }
     if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
@@ -612,6 +597,23 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         }
         if (j == 0) f = s_f[(one ? 0 : t * 128) + r];
         const Head& hd = heads[tile % C::kHeads];
+        // What is rare changes the scores where they lie, a group at a time: positions that are not seen.
+        if (hd.hidden) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int seen = hd.seen[i];
+            if (seen == 16) continue;
+            uint32_t s[16];
+            tmem_ld16(tS + 16 * i, s);
+            tmem_wait_ld();
+            reg_fence(s);
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (x >= seen) s[x] = __float_as_uint(-INFINITY);
+            tmem_st16(tS + 16 * i, s);
+          }
+          tmem_wait_st();
+        }
         // The scores are read from TMEM twice, 64 columns at a time: for their maxima, then for the
         // weights.  Held in between they would take more registers than there are (and spills go past an L1
         // that shared memory leaves no room).
@@ -621,15 +623,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           tmem_wait_ld();
           reg_fence(s[0]);
           reg_fence(s[1]);
-          if (hd.hidden) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int seen = hd.seen[half * 4 + i];
-#pragma unroll
-              for (int x = 0; x < 16; ++x)
-                if (x >= seen) s[i >> 1][(i & 1) * 16 + x] = __float_as_uint(-INFINITY);
-            }
-          }
         };
         // Factor of a group's scores (base 2); not 0, so that hidden ones stay -inf.
         auto factor = [&](int group) { return fmaxf(f * hd.ks[group * (GROUP / 16)], 0x1p-126f); };
@@ -690,37 +683,48 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         // The fma below leaves the rounding of the largest score's product, half its last bit, in the
         // exponent.  From 2^24 on that could take a weight out of FP16: a row's products are rounded first then.
         const bool large = fabsf(m_use) >= 0x1p24f;
+        if (__any_sync(0xffffffffu, large)) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const float k = large ? factor(i * 16 / GROUP) : 1.f;
+            uint32_t s[16];
+            tmem_ld16(tS + 16 * i, s);
+            tmem_wait_ld();
+            reg_fence(s);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * k);
+            tmem_st16(tS + 16 * i, s);
+          }
+          tmem_wait_st();
+        }
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
         uint64_t sums2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sums2[i] = 0ull;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
+          uint64_t k2[kHalf], v2[kHalf];
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) {
+            const float k = large ? 1.f : factor(half * kHalf + i);
+            const float v = fminf(hd.vs[(half * kHalf + i) * (GROUP / 16)] * up, 0x1p127f);
+            k2[i] = f2_pack(k, k);
+            v2[i] = f2_pack(v, v);
+          }
           uint32_t s[2][32];
           scores(half, s);
-          float k[kHalf];
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) k[i] = factor(half * kHalf + i);
-          if (__any_sync(0xffffffffu, large)) {
-#pragma unroll
-            for (int x = 0; x < 64; ++x)
-              s[x >> 5][x & 31] = __float_as_uint(__uint_as_float(s[x >> 5][x & 31]) * (large ? k[x / GROUP] : 1.f));
-#pragma unroll
-            for (int i = 0; i < kHalf; ++i) k[i] = large ? 1.f : k[i];
-          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int group = (c * 32 + 2 * i) / GROUP;
-              const float v = fminf(hd.vs[(half * kHalf + group) * (GROUP / 16)] * up, 0x1p127f);
               float x0, x1;
               f2_unpack(fma2(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])),
-                             f2_pack(k[group], k[group]), nm2), x0, x1);
+                             k2[group], nm2), x0, x1);
               const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
               sums2[i & 3] = add2(sums2[i & 3], p2);
-              f2_unpack(mul2(p2, f2_pack(v, v)), x0, x1);
+              f2_unpack(mul2(p2, v2[group]), x0, x1);
               pk[i] = pack_f16x2(x0, x1);
             }
             tmem_st16(tS + half * 32 + c * 16, pk);
