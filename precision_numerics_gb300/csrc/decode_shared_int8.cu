@@ -16,12 +16,12 @@
 // 128 rows by 128 positions, accumulators in TMEM.  A CTA (one per SM) has two row tiles that
 // share each tile of keys; with up to 128 rows it has one, and its two halves take the
 // even and the odd key tiles of it.  Roles of the warps:
-//   warp 0            asks for the codes of the pages (bulk copies to a ring in shared memory) and
-//                     for their scales
-//   warps 12-15       codes to FP16, from the ring to swizzled tiles
-//   warp 1            issues the products
-//   warps 4-7, 8-11   softmax of row tile (or half) 0 and 1, one thread a row; also their Q rows
-//                     and the results' way out
+//   copies (1 warp)    asks for the codes of the pages (bulk copies to a ring in shared memory) and
+//                      for their scales
+//   codes (8 warps)    codes of K and of V to FP16, from the ring to swizzled tiles
+//   products (1 warp)  issues them
+//   softmax (8 warps)  a thread for each row of the two tiles (or halves); also their Q rows and the
+//                      results' way out
 // Loads to registers are avoided where much is in flight: shared memory leaves L1 28 KB, and codes that
 // were loaded through it kept the warps that ask for them waiting (a key tile took 3.9 us).
 // The tiles of all (key head, row block) units, one behind the other, are dealt to the CTAs
@@ -29,10 +29,10 @@
 //
 // Numerics, as in decode_int8.cu: codes are exact in FP16; Q becomes FP16 after division by a
 // power of two of its row's maximum (exact down to 2^-17 of it); the weights p vs of the
-// values' codes are FP16 after a row's own power of two 2^E, by which its largest weight so far
-// is 2^11 to 2^15, so that they keep 11 bits down to 2^-25 of it.  m and E follow the
-// running maxima of s and of s + log2(vs) when one has grown by more than 2^4 (the accumulators
-// in TMEM are rescaled then, by the softmax's threads).  Sums and statistics are FP32.
+// values' codes are FP16 relative to a row's own W, by which its largest weight so far is 2^6 or more
+// (kTop), so that they keep 11 bits down to 2^-20 of it.  W and the maximum that the row sum is relative to
+// follow the running maxima of s + log2(vs) and of s only when the weights would grow too large: the
+// accumulators in TMEM are rescaled then, by the softmax's threads.  Sums and statistics are FP32.
 #include <math.h>
 #include <stdint.h>
 
@@ -47,17 +47,25 @@ static __device__ unsigned int g_status_shared;
 
 namespace {
 
-constexpr int kThreads = 512;
-// Registers a thread of the four warpgroups: products, softmax (two), codes.
-constexpr int kRegsMma = 96, kRegsSoftmax = 160, kRegsCodes = 96;
-static_assert(kRegsMma + 2 * kRegsSoftmax + kRegsCodes <= 512, "setmaxnreg split exceeds the launch pool");
-static_assert(kRegsMma <= 128 && kRegsCodes <= 128 && kRegsSoftmax >= 128, "setmaxnreg directions");
+// Warps 0 to 7 softmax, 8 to 11 K's codes, 12 to 15 V's, 16 copies, 17 products (and two that have nothing
+// to do: a warpgroup has four).
+constexpr int kSoftmaxWarps = 8, kCodeWarps = 4, kCopyWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 32 * 20;
+// Registers a thread at launch (five warps a quarter of an SM), and of the warpgroups of each kind.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsCodes = 56, kRegsMma = 64;
+static_assert(2 * kRegsSoftmax + 2 * kRegsCodes + kRegsMma <= 5 * kRegsLaunch,
+              "setmaxnreg split exceeds the launch pool");
+static_assert(kRegsMma <= kRegsLaunch && kRegsCodes <= kRegsLaunch && kRegsSoftmax >= kRegsLaunch,
+              "setmaxnreg directions");
 constexpr int kUnitRows = 256;  // rows of a unit: two tiles
 // Cost of a key tile where the unit has two row tiles, and where it has one.
 constexpr int kCostTwo = 3, kCostOne = 2;
 constexpr int kLeastRun = 2;  // key tiles of a run at least
-constexpr float kSlack = 4.f;  // growth of a maximum (base 2) that the accumulators take as it is
-constexpr float kTop = 11.f;   // log2 of the largest weight just after its row's references moved
+// The largest weight of a row just after its reference W moved is 2^kTop, so the 128 weights of a tile sum to
+// 2^(kTop + 7) or less; W moves again when a tile's could sum to more than kMost, which FP16 still holds.
+constexpr float kTop = 6.f, kMost = 65000.f;
+constexpr float kLeastScale = -104.f;  // log2 of the least value scale whose weights reach 2^kTop
+constexpr float kMostSum = 0x1p40f;  // of a tile's weights relative to the row's maximum so far
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_shared, code); }
 
@@ -79,6 +87,11 @@ struct Args {
 // A part: O / l as [D / 4][256 rows][4], m [256], l [256].
 __host__ __device__ constexpr size_t part_floats(int d) { return (size_t)kUnitRows * (d + 2); }
 
+// x / y, in 32 bits where they suffice.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  return x <= 0xffffffffll && y <= 0xffffffffll ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+
 // How the key tiles of all units (unit = key head * row_blocks + row block) are dealt.  Tiles of
 // all units together are below 2^31 (the host's check).
 struct Deal {
@@ -90,15 +103,16 @@ struct Deal {
     tiles = (len + kBlockN - 1) / kBlockN;
     last_cost = a.rows - (a.row_blocks - 1) * kUnitRows <= kBlockM ? kCostOne : kCostTwo;
     head_cost = (long long)tiles * (kCostTwo * (a.row_blocks - 1) + last_cost);
-    const long long most = head_cost * a.Hkv / (kLeastRun * kCostTwo);
+    const long long most = divide(head_cost * a.Hkv, kLeastRun * kCostTwo);
     runs = tiles == 0 ? 0 : (int)max(1ll, min((long long)a.runs, most));
   }
   // First tile (unit * tiles + key tile) of run c.
   __device__ __forceinline__ int begin(const Args& a, int c) const {
     if (c >= runs) return a.Hkv * a.row_blocks * tiles;
-    const long long x = head_cost * a.Hkv * c / runs, h = x / head_cost, y = x - h * head_cost;
+    const long long x = divide(head_cost * a.Hkv * c, runs), h = divide(x, head_cost), y = x - h * head_cost;
     const long long full = (long long)kCostTwo * tiles * (a.row_blocks - 1);
-    const long long i = y < full ? y / kCostTwo : (long long)tiles * (a.row_blocks - 1) + (y - full) / last_cost;
+    const long long i =
+        y < full ? divide(y, kCostTwo) : (long long)tiles * (a.row_blocks - 1) + divide(y - full, last_cost);
     return (int)(h * a.row_blocks * tiles + i);
   }
 };
@@ -141,10 +155,11 @@ struct Walk {
 
 // Scales of a key tile in groups of 16 positions, and how many of each are seen.
 struct Head {
-  float ks[8], vs[8], log_vs[8];
-  int seen[8];
-  int hidden;         // not all are seen
-  unsigned loaded;    // bit per group that has codes
+  float ks[8], vs[8];
+  float v_most;  // the largest of vs
+  uint8_t seen[8];
+  int hidden;       // not all are seen
+  unsigned loaded;  // bit per group that has codes
 };
 
 template <int D>
@@ -166,8 +181,8 @@ struct Cfg {
   static constexpr int kOffK = kOffRaw + 2 * kRawTiles * kRawBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffHead = kOffV + kStages * kTileBytes;
-  static constexpr int kOffF = kOffHead + kHeads * (int)sizeof(Head);  // FP32 [2][128]: factor of a row's scores
-  static constexpr int kOffBar = (kOffF + 2 * 128 * 4 + 15) / 16 * 16;
+  static constexpr int kOffE = kOffHead + kHeads * (int)sizeof(Head);  // int8 [2][128]: exponent of a row's power of two
+  static constexpr int kOffBar = (kOffE + 2 * 128 + 15) / 16 * 16;
   static constexpr int kSlots = 2 * (kRawTiles + 1);
   // raw_full, raw_empty [slots], k_full, k_empty, v_full, v_empty [stages], head [kHeads], q_raw [8],
   // q [2], s_full [2], p_full [2], o_done [2], final
@@ -190,9 +205,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two of four codes as FP16: the byte c + 128 under the exponent of 1024 is 1152 + c.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t sel) {
-  const uint32_t x = __byte_perm(u, 0x64646464u, sel);
+// Codes 0 and 2 of four, or 1 and 3 of them shifted by a byte, as FP16: the byte c + 128 under the
+// exponent of 1024 is 1152 + c.  (Q's elements are put in the same order, and O's come out of it.)
+__device__ __forceinline__ uint32_t codes_f16(uint32_t u) {
+  const uint32_t x = (u & 0x00FF00FFu) ^ 0x64806480u;
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64806480u));
   return r;
@@ -209,9 +225,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 // 1 / L, or 0 where a row has seen nothing.  A NaN stays one.
 __device__ __forceinline__ float inverse(float L) { return L == 0.f ? 0.f : 1.f / L; }
-// 2^e for a whole e in [-126, 127].
-__device__ __forceinline__ float power2(float e) { return __uint_as_float((uint32_t)((int)e + 127) << 23); }
-
 // Sequence, token and head of row r of key head h's rows.
 __device__ __forceinline__ void row_of(const Args& a, int r, int& b, int& t, int& g) {
   const int x = r / a.G;
@@ -225,7 +238,9 @@ template <int D, int GROUP>
 __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // What decides where a warp goes comes from a shuffle, which tells the compiler that it is the same in
+  // all lanes: the products' descriptors then stay in uniform registers.
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* bar_rfull = bars;
@@ -242,44 +257,44 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   uint64_t* bar_odone = bar_pfull + 2;
   uint64_t* bar_final = bar_odone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
-  float* s_f = reinterpret_cast<float*>(smem + C::kOffF);
+  int8_t* s_e = reinterpret_cast<int8_t*>(smem + C::kOffE);
   Head* heads = reinterpret_cast<Head*>(smem + C::kOffHead);
 
   if (threadIdx.x == 0) {
     tmem_slot[1] = (smem_u32(smem) & 1023u) != 0;
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&bar_rfull[s], 1);
-      mbar_init(&bar_rempty[s], 4);
+      mbar_init(&bar_rempty[s], kCodeWarps);
     }
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&bar_kfull[s], 128);
+      mbar_init(&bar_kfull[s], kCodeWarps);
       mbar_init(&bar_kempty[s], 1);
-      mbar_init(&bar_vfull[s], 128);
+      mbar_init(&bar_vfull[s], kCodeWarps);
       mbar_init(&bar_vempty[s], 1);
     }
     for (int s = 0; s < C::kHeads; ++s) mbar_init(&bar_head[s], 1);
     for (int s = 0; s < 8; ++s) mbar_init(&bar_qraw[s], 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bar_q[t], 128);
+      mbar_init(&bar_q[t], 4);
       mbar_init(&bar_sfull[t], 1);
-      mbar_init(&bar_pfull[t], 128);
+      mbar_init(&bar_pfull[t], 4);
       mbar_init(&bar_odone[t], 1);
     }
     mbar_init(bar_final, 1);
     fence_mbar_init();
   }
-  if (warp == 2) {
+  if (warp == kCopyWarp) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   griddep_wait();
-  const bool abort_all = tmem_slot[1] != 0;
+  const bool abort_all = __any_sync(0xffffffffu, tmem_slot[1] != 0);
   if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
-  const int len = prefix_length(a, threadIdx.x == 0 && blockIdx.x == 0);
+  const int len = __shfl_sync(0xffffffffu, prefix_length(a, threadIdx.x == 0 && blockIdx.x == 0), 0);
   Walk sg(a, Deal(a, len), abort_all);
   // All units have one row tile: one copy of Q, and a longer ring.
   const bool one = a.rows <= kBlockM;
@@ -290,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   uint8_t* sK = smem + C::kOffK;
   uint8_t* sV = smem + C::kOffV;
 
-  if (warp < 4) {
+  if (warp >= kCopyWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-    if (warp == 0) {
+    if (warp == kCopyWarp) {
       // ------------------------------------------------------------ copies
       // Lane x: group x % 8 (16 positions) of the tile, K in lanes 0 to 7, V in 8 to 15.  Page numbers of
       // four key tiles are read at a time, scales a tile ahead.
@@ -347,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         const int seen = id >= 0 ? max(0, min(16, len - (tile * kBlockN + 16 * group))) : 0;
         const bool hidden = __any_sync(0xffffffffu, seen < 16);
         const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
+        const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, is_v && lane < 16 ? __float_as_uint(scale) : 0u));
         if (lane < 8) {
           hd.ks[group] = scale;
-          hd.seen[group] = seen;
+          hd.seen[group] = (uint8_t)seen;
         } else if (lane < 16) {
           hd.vs[group] = scale;
-          hd.log_vs[group] = fmaxf(__log2f(scale), -126.f);
         }
-        if (lane == 0) hd.hidden = hidden, hd.loaded = loaded;
+        if (lane == 0) hd.v_most = most, hd.hidden = hidden, hd.loaded = loaded;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_head[g % C::kHeads]);
         if (++e == sg.nk) {
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
       // Do not leave while copies into this CTA's shared memory are in flight.
       for (int x = max(0, issued - slots); x < issued; ++x) mbar_wait(&bar_rfull[x % slots], (x / slots) & 1);
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, false);
       constexpr uint32_t idesc_pv = idesc_f16(128, D, true);
@@ -391,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         const uint64_t b0 = sdesc_add(descV, st * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < kBlockN / 16; ++kk)
-          mma_ts_elect(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, sdesc_add(b0, kk * 2048), idesc_pv,
-                       (acc || kk > 0) ? 1u : 0u);
+          mma_ts_elect(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, sdesc_add(b0, kk * 2048),
+                       idesc_pv, (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
       int g = 0, items = 0;
@@ -413,12 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           for (int t = two ? 0 : e & 1; t < (two ? 2 : (e & 1) + 1) && ok; ++t) {
             const bool first = !two || t == 0;
             if (pv) {
-              // The threads that wrote the codes leave the fence to this warp.
               if (first) ok = warp_wait(&bar_vfull[sv], ((g + i) / C::kStages) & 1);
               ok = ok && warp_wait(&bar_pfull[t], (pc >> t) & 1);
               if (!ok) break;
               pc ^= 1u << t;
-              if (first) fence_proxy_async_smem();
               tc_fence_after();
               issue_pv(t, sv, i >= lag);
               if (!qk) mma_commit_elect(&bar_odone[t]);
@@ -427,7 +440,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
               if (first) {
                 ok = warp_wait(&bar_kfull[sk], ((g + e) / C::kStages) & 1);
                 if (!ok) break;
-                fence_proxy_async_smem();
                 tc_fence_after();
               }
               issue_s(t, sk);
@@ -447,70 +459,80 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       mbar_wait(bar_final, 0);
     }
     __syncwarp();
-  } else if (warp >= 12) {
+  } else if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCodes));
     // --------------------------------------------------------------- codes
-    // A thread has one 16-byte unit of a row, kPasses rows of a tile.
+    // A thread has one 16-byte unit of a row, kPasses rows of a tile.  The eight lanes of a phase have
+    // 128 bytes of codes that meet all banks, and so do the units that they become: those of two rows
+    // with units 0, 2, 4, 6 each, which the swizzle of an odd row moves to the odd places (d = 128: units of
+    // the first chunk of one row and of the second of the other).
     constexpr int kUnits = D / 16, kRows = 128 / kUnits, kPasses = 128 / kRows;
-    const int tid = threadIdx.x - 384, unit = tid % kUnits, row = tid / kUnits;
+    const int unit = lane % kUnits, pair = lane >> 3;
+    const int kv = (warp - kSoftmaxWarps) / kCodeWarps;  // K or V
+    const int row = warp % kCodeWarps * (kRows / 4) +
+                    (D == 128 ? (pair >> 1) * 2 + ((unit >> 2) ^ (pair & 1)) : lane / kUnits);
     bool ok = true;
+    const uint32_t from = smem_u32(raw) + row * D + unit * 16;
+    const uint32_t to0 = (unit >> 2) * C::kChunkBytes + sw128_offset(row, (unit & 3) * 2);
+    const uint32_t to1 = to0 ^ 16u;  // the odd unit beside it
     // Slot x of the ring to the tile at `to`, which is free when `empty` has completed its phase.
-    const uint32_t swap = unit >> 2, u = (unit & 3) * 2;
-    // The eight lanes of a phase have one row of d = 128: those of its second chunk store their two
-    // units in the other order, so that all banks are met.  (All rows of a thread have the same swizzle.)
-    const uint32_t to0 = swap * C::kChunkBytes + sw128_offset(row, u + swap);
-    const uint32_t to1 = swap * C::kChunkBytes + sw128_offset(row, u + 1 - swap);
     auto convert = [&](int x, unsigned loaded, uint32_t to, uint64_t* empty, int phase) {
       const int slot = x % slots;
       if (!warp_wait(&bar_rfull[slot], (x / slots) & 1)) return false;
-      uint4 w[kPasses];
+      constexpr int kBatch = 4;
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[p].x), "=r"(w[p].y), "=r"(w[p].z), "=r"(w[p].w)
-                     : "r"(smem_u32(raw) + slot * C::kRawBytes + (p * kRows + row) * D + unit * 16)
-                     : "memory");
-      }
-      if (loaded != 0xffu) {
+      for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+        uint4 w[kBatch];
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p)
-          if (!((loaded >> ((p * kRows + row) >> 4)) & 1u)) w[p] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_rempty[slot]);
-      if (phase >= 0 && !warp_wait(empty, phase & 1)) return false;
+        for (int i = 0; i < kBatch; ++i) {
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                       : "r"(from + slot * C::kRawBytes + (p0 + i) * kRows * D)
+                       : "memory");
+        }
+        if (loaded != 0xffu) {
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const uint32_t c[4] = {(swap ? w[p].z : w[p].x) ^ 0x80808080u, (swap ? w[p].w : w[p].y) ^ 0x80808080u,
-                               (swap ? w[p].x : w[p].z) ^ 0x80808080u, (swap ? w[p].y : w[p].w) ^ 0x80808080u};
-        st_shared_v4(to + to0 + p * kRows * 128, codes_f16(c[0], 0x4140u), codes_f16(c[0], 0x4342u),
-                     codes_f16(c[1], 0x4140u), codes_f16(c[1], 0x4342u));
-        st_shared_v4(to + to1 + p * kRows * 128, codes_f16(c[2], 0x4140u), codes_f16(c[2], 0x4342u),
-                     codes_f16(c[3], 0x4140u), codes_f16(c[3], 0x4342u));
+          for (int i = 0; i < kBatch; ++i)
+            if (!((loaded >> (((p0 + i) * kRows + row) >> 4)) & 1u)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (p0 + kBatch == kPasses) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_rempty[slot]);
+        }
+        if (p0 == 0 && phase >= 0 && !warp_wait(empty, phase & 1)) return false;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const uint32_t at = to + (p0 + i) * kRows * 128;
+          st_shared_v4(at + to0, codes_f16(w[i].x), codes_f16(w[i].x >> 8), codes_f16(w[i].y), codes_f16(w[i].y >> 8));
+          st_shared_v4(at + to1, codes_f16(w[i].z), codes_f16(w[i].z >> 8), codes_f16(w[i].w), codes_f16(w[i].w >> 8));
+        }
       }
       return true;
     };
+    uint64_t* bar_full = kv == 0 ? bar_kfull : bar_vfull;  // the empty ones are behind them
+    const uint32_t tiles = smem_u32(kv == 0 ? sK : sV);
     int g = 0;
     while (ok && sg.next(a)) {
       for (int e = 0; e < sg.nk; ++e, ++g) {
-        const int st = g % C::kStages, phase = g / C::kStages - 1;
+        const int st = g % C::kStages;
         ok = warp_wait(&bar_head[g % C::kHeads], (g / C::kHeads) & 1);
         if (!ok) break;
-        const unsigned loaded = heads[g % C::kHeads].loaded;
-#pragma unroll 1
-        for (int x = 0; x < 2 && ok; ++x) {  // K, V
-          uint64_t* full = (x == 0 ? bar_kfull : bar_vfull) + st;
-          ok = convert(2 * g + x, loaded, smem_u32(x == 0 ? sK : sV) + st * C::kTileBytes, full + C::kStages, phase);
-          if (ok) mbar_arrive(full);
-        }
+        ok = convert(2 * g + kv, heads[g % C::kHeads].loaded, tiles + st * C::kTileBytes, bar_full + C::kStages + st,
+                     g / C::kStages - 1);
         if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_full + st);
       }
     }
     if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------- softmax
-    const int t = (warp - 4) >> 2, w0 = (warp & 3) * 32;
+    // A thread has a row of tile (or half) t: its maximum and sum so far, the weights of the row sum relative to
+    // that maximum, and the reference W (in base 2) of the weights that are multiplied with the codes, and
+    // so of the accumulators.
+    const int t = warp >> 2, w0 = (warp & 3) * 32;
     const int r = w0 + lane;  // row within the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)w0 << 16;
     const uint32_t tS = tmem + lane_off + C::col_s(t);
@@ -521,19 +543,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     while (ok && sg.next(a)) {
       const bool two = sg.two(a);
       const int first = sg.rb * kUnitRows + (two ? t * kBlockM : 0);  // the tile's first row
-      const int have = min(kBlockM, a.rows - first);                     // and how many it has
+      const int have = min(kBlockM, a.rows - first);                  // and how many it has
       // -------------------------------------------------------- Q rows
       // This warp's 32 rows, a lane each, are copied to their places in the tile and there divided and
       // swizzled (which moves units within 128 bytes), kLanes lanes a row.  The products that read
       // the rows before are complete: the softmax has had their results, of both halves where they share them.
       if (!one || t == 0) {
+        uint64_t* bar = &bar_qraw[warp];
         if (one && items > 0) {
           ok = warp_wait(&bar_odone[1], (items - 1) & 1);
           if (!ok) break;
         }
-        const uint32_t tile_q = smem_u32(sQ) + t * C::kTileBytes;
         fence_proxy_async_smem();
-        if (lane == 0) mbar_arrive_expect_tx(&bar_qraw[warp - 4], max(0, min(32, have - w0)) * D * 2);
+        if (lane == 0) mbar_arrive_expect_tx(bar, max(0, min(32, have - w0)) * D * 2);
         __syncwarp();
         if (r < have) {
           int b, tok, gg;
@@ -541,13 +563,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           const uint16_t* from = a.q + b * a.q_batch + tok * a.q_token + (long long)(sg.h * a.G + gg) * a.q_head;
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            bulk_load(sQ + t * C::kTileBytes + c * C::kChunkBytes + r * 128, from + c * 64, 128, &bar_qraw[warp - 4]);
+            bulk_load(sQ + t * C::kTileBytes + c * C::kChunkBytes + r * 128, from + c * 64, 128, bar);
         }
-        ok = warp_wait(&bar_qraw[warp - 4], items & 1);
+        ok = warp_wait(bar, items & 1);
         if (!ok) break;
         constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kAtOnce;
         const int u = lane % kLanes;
-        const uint32_t chunk = tile_q + (u >> 3) * C::kChunkBytes;
+        const uint32_t chunk = smem_u32(sQ) + t * C::kTileBytes + (u >> 3) * C::kChunkBytes;
 #pragma unroll 4
         for (int i = 0; i < kTurns; ++i) {
           const int rr = w0 + i * kAtOnce + lane / kLanes;
@@ -557,186 +579,174 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                          : "r"(chunk + rr * 128 + (u & 7) * 16)
                          : "memory");
-          float m = 0.f;
+          float x[8], m = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+          for (int k = 0; k < 4; ++k) {
+            x[2 * k] = __uint_as_float(w[k] << 16);
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+            m = fmaxf(m, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+          }
 #pragma unroll
           for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
           // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
           const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u) - 127, -126), 126);
           const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          uint32_t y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[k] = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          // (All lanes of the row have read it: the maximum needed them.)
-          st_shared_v4(chunk + sw128_offset(rr, u & 7), y[0], y[1], y[2], y[3]);
-          if (u == 0) s_f[t * 128 + rr] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+          // (All lanes of the row have read it: the maximum needed them.)  Elements in the codes' order.
+          st_shared_v4(chunk + sw128_offset(rr, u & 7), pack_f16x2(x[0] * down, x[2] * down),
+                       pack_f16x2(x[1] * down, x[3] * down), pack_f16x2(x[4] * down, x[6] * down),
+                       pack_f16x2(x[5] * down, x[7] * down));
+          if (u == 0) s_e[t * 128 + rr] = (int8_t)e;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        mbar_arrive(&bar_q[t]);
+        if (lane == 0) mbar_arrive(&bar_q[t]);
       }
       ++items;
-      // (One copy: half 1 reads the factors after the first scores, which waited for all of Q.)
-      float f = 0.f;
+      float f = 0.f;  // factor of the row's scores, known when the first ones are: they waited for all of Q
       const int n = two ? sg.nk : (sg.nk + 1 - t) / 2;  // key tiles of this half
       const bool idle = w0 >= have;  // none of the warp's rows is one
-      float m_ref = -INFINITY, E = 0.f, l_run = 0.f;
+      float m_ref = -INFINITY, W = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
         ok = warp_wait(&bar_sfull[t], (sc + j) & 1);
         const int tile = g + (two ? j : 2 * j + t);
         if (ok) ok = warp_wait(&bar_head[tile % C::kHeads], (tile / C::kHeads) & 1);
         if (!ok) break;
         tc_fence_after();
-        if (idle) {
-          tc_fence_before();
-          mbar_arrive(&bar_pfull[t]);
-          continue;
-        }
-        if (j == 0) f = s_f[(one ? 0 : t * 128) + r];
-        const Head& hd = heads[tile % C::kHeads];
-        // What is rare changes the scores where they lie, a group at a time: positions that are not seen.
-        if (hd.hidden) {
+        if (!idle) {
+          if (j == 0) f = a.scale_log2 * __uint_as_float((uint32_t)(127 + s_e[(one ? 0 : t * 128) + r]) << 23);
+          const Head& hd = heads[tile % C::kHeads];
+          // Changes scores where they lie, 16 at a time; for what is rare.
+          auto change = [&](auto&& to) {
 #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const int seen = hd.seen[i];
-            if (seen == 16) continue;
-            uint32_t s[16];
-            tmem_ld16(tS + 16 * i, s);
-            tmem_wait_ld();
-            reg_fence(s);
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (x >= seen) s[x] = __float_as_uint(-INFINITY);
-            tmem_st16(tS + 16 * i, s);
-          }
-          tmem_wait_st();
-        }
-        // The scores are read from TMEM twice, 64 columns at a time: for their maxima, then for the
-        // weights.  Held in between they would take more registers than there are (and spills go past an L1
-        // that shared memory leaves no room).
-        auto scores = [&](int half, uint32_t (&s)[2][32]) {
-          tmem_ld32(tS + half * 64, s[0]);
-          tmem_ld32(tS + half * 64 + 32, s[1]);
-          tmem_wait_ld();
-          reg_fence(s[0]);
-          reg_fence(s[1]);
-        };
-        // Factor of a group's scores (base 2); not 0, so that hidden ones stay -inf.
-        auto factor = [&](int group) { return fmaxf(f * hd.ks[group * (GROUP / 16)], 0x1p-126f); };
-        constexpr int kHalf = 64 / GROUP;  // groups of 64 columns
-        float mt = -INFINITY, mw = -INFINITY;  // largest score and largest log2 of a weight
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t s[2][32];
-          scores(half, s);
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            const int x0 = i * GROUP;
-            float m = fmaxf(__uint_as_float(s[x0 >> 5][x0 & 31]), __uint_as_float(s[x0 >> 5][(x0 & 31) + 1]));
-#pragma unroll
-            for (int x = x0 + 2; x < x0 + GROUP; x += 2)
-              m = fmax3(m, __uint_as_float(s[x >> 5][x & 31]), __uint_as_float(s[x >> 5][(x & 31) + 1]));
-            m *= factor(half * kHalf + i);
-            mt = fmaxf(mt, m);
-            mw = fmaxf(mw, m + hd.log_vs[(half * kHalf + i) * (GROUP / 16)]);
-          }
-        }
-        // The largest weight so far is 2^(m_ref - (E - kTop)) or less by kSlack.  Rows whose references
-        // stay have factors of 1: no row's bits depend on another's.
-        const bool moves = fmaxf(mt, mw + (E - kTop)) > m_ref + kSlack;
-        if (__any_sync(0xffffffffu, moves)) {
-          float f_o = 1.f;
-          if (moves) {
-            const float m_new = fmaxf(m_ref, mt);  // not -inf
-            const float w_new = fmaxf(m_ref - (E - kTop), mw);
-            const float e_new = fminf(rintf(m_new - w_new) + kTop, 126.f);
-            const float back = m_ref - m_new;
-            l_run *= ex2(back);
-            f_o = ex2(back + (e_new - E));
-            m_ref = m_new;
-            E = e_new;
-          }
-          if (j > 0) {
-            const uint64_t f2 = f2_pack(f_o, f_o);
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(tO + c * 16, o);
+            for (int i = 0; i < 8; ++i) {
+              uint32_t s[16];
+              tmem_ld16(tS + 16 * i, s);
               tmem_wait_ld();
-              reg_fence(o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float lo, hi;
-                f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), f2), lo, hi);
-                o[2 * i] = __float_as_uint(lo);
-                o[2 * i + 1] = __float_as_uint(hi);
-              }
-              tmem_st16(tO + c * 16, o);
+              reg_fence(s);
+              to(i, s);
+              tmem_st16(tS + 16 * i, s);
             }
-          }
-        }
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const float up = power2(E);
-        // The fma below leaves the rounding of the largest score's product, half its last bit, in the
-        // exponent.  From 2^24 on that could take a weight out of FP16: a row's products are rounded first then.
-        const bool large = fabsf(m_use) >= 0x1p24f;
-        if (__any_sync(0xffffffffu, large)) {
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const float k = large ? factor(i * 16 / GROUP) : 1.f;
-            uint32_t s[16];
-            tmem_ld16(tS + 16 * i, s);
-            tmem_wait_ld();
-            reg_fence(s);
+            tmem_wait_st();
+          };
+          if (hd.hidden)
+            change([&](int i, uint32_t (&s)[16]) {
+              const int seen = hd.seen[i];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * k);
-            tmem_st16(tS + 16 * i, s);
+              for (int x = 0; x < 16; ++x)
+                if (x >= seen) s[x] = __float_as_uint(-INFINITY);
+            });
+          // Factor of the scores of group i of 16 (base 2); not 0, so that hidden ones stay -inf.
+          bool rounded = false;  // the row's scores have been multiplied with it
+          auto factor = [&](int i) { return rounded ? 1.f : fmaxf(f * hd.ks[i], 0x1p-126f); };
+          // The weights are formed with the references of the tiles before, without a look at the maximum first.
+          // Where they could be too large (which the tile's sum tells), and in the first tile, the row's
+          // references move to the maximum, the accumulators with them, and the weights are formed again.
+          // Other rows of the warp form the same ones again: no row's bits depend on another's.
+          bool moves = j == 0, again = j == 0;
+          float sum;
+          uint32_t pk[64];
+          while (true) {
+            if (again) {
+              float mt = -INFINITY, mw = -INFINITY;  // largest score and largest log2 of a weight
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {
+                uint32_t s[16];
+                tmem_ld16(tS + 16 * i, s);
+                tmem_wait_ld();
+                reg_fence(s);
+                float m = __uint_as_float(s[0]);
+#pragma unroll
+                for (int x = 1; x < 15; x += 2) m = fmax3(m, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                m = fmaxf(m, __uint_as_float(s[15])) * factor(i);
+                mt = fmaxf(mt, m);
+                mw = fmaxf(mw, m + fmaxf(__log2f(hd.vs[i]), kLeastScale));
+              }
+              float f_o = 1.f;
+              if (moves && mt > -INFINITY) {
+                const float m_new = fmaxf(m_ref, mt), W_new = fmaxf(W, mw - kTop);
+                l_run *= ex2(m_ref - m_new);
+                f_o = ex2(W - W_new);
+                m_ref = m_new;
+                W = W_new;
+              }
+              if (j > 0) {
+                const uint64_t f2 = f2_pack(f_o, f_o);
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + c * 16, o);
+                  tmem_wait_ld();
+                  reg_fence(o);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    float lo, hi;
+                    f2_unpack(mul2(f2_pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), f2), lo, hi);
+                    o[2 * i] = __float_as_uint(lo);
+                    o[2 * i + 1] = __float_as_uint(hi);
+                  }
+                  tmem_st16(tO + c * 16, o);
+                }
+              }
+            }
+            const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+            const float up = W == -INFINITY ? 1.f : ex2(m_use - W);
+            // The fma below leaves the rounding of the largest score's product, half its last bit, in the exponent.
+            // From 2^24 on that could take a weight out of FP16: such a row's products are rounded first.
+            const bool large = !rounded && fabsf(m_use) >= 0x1p24f;
+            if (__any_sync(0xffffffffu, large)) {
+              change([&](int i, uint32_t (&s)[16]) {
+                const float k = large ? factor(i) : 1.f;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * k);
+              });
+              rounded = rounded || large;
+            }
+            const uint64_t nm2 = f2_pack(-m_use, -m_use);
+            uint64_t sums2[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums2[i] = 0ull;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_ld32(tS + c * 32, s);
+              uint64_t k2[32 / GROUP], v2[32 / GROUP];
+#pragma unroll
+              for (int i = 0; i < 32 / GROUP; ++i) {
+                const int group = c * 2 + i;
+                const float k = factor(group), v = fminf(hd.vs[group] * up, 0x1p127f);
+                k2[i] = f2_pack(k, k);
+                v2[i] = f2_pack(v, v);
+              }
+              tmem_wait_ld();
+              reg_fence(s);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float x0, x1;
+                f2_unpack(fma2(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), k2[2 * i / GROUP],
+                               nm2), x0, x1);
+                const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
+                sums2[i & 3] = add2(sums2[i & 3], p2);
+                f2_unpack(mul2(p2, v2[2 * i / GROUP]), x0, x1);
+                pk[c * 16 + i] = pack_f16x2(x0, x1);
+              }
+            }
+            float sums[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(sums2[i], sums[2 * i], sums[2 * i + 1]);
+            sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
+            if (again) break;
+            moves = !(sum * fminf(hd.v_most * up, 0x1p127f) <= kMost && sum <= kMostSum);
+            again = __any_sync(0xffffffffu, moves);
+            if (!again) break;
           }
+          l_run += sum;
+          tmem_st32(tS, reinterpret_cast<uint32_t(&)[32]>(pk[0]));
+          tmem_st32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(pk[32]));
           tmem_wait_st();
         }
-        const uint64_t nm2 = f2_pack(-m_use, -m_use);
-        uint64_t sums2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums2[i] = 0ull;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint64_t k2[kHalf], v2[kHalf];
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            const float k = large ? 1.f : factor(half * kHalf + i);
-            const float v = fminf(hd.vs[(half * kHalf + i) * (GROUP / 16)] * up, 0x1p127f);
-            k2[i] = f2_pack(k, k);
-            v2[i] = f2_pack(v, v);
-          }
-          uint32_t s[2][32];
-          scores(half, s);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int group = (c * 32 + 2 * i) / GROUP;
-              float x0, x1;
-              f2_unpack(fma2(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])),
-                             k2[group], nm2), x0, x1);
-              const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
-              sums2[i & 3] = add2(sums2[i & 3], p2);
-              f2_unpack(mul2(p2, v2[group]), x0, x1);
-              pk[i] = pack_f16x2(x0, x1);
-            }
-            tmem_st16(tS + half * 32 + c * 16, pk);
-          }
-        }
-        float sums[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f2_unpack(sums2[i], sums[2 * i], sums[2 * i + 1]);
-        l_run += ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
-        tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar_pfull[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_pfull[t]);
       }
       if (!ok) break;
       sc += n;
@@ -746,11 +756,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       if (!ok) break;
       ++oc;
       tc_fence_after();
-      float* part = a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D);
-      const int pr = t * kBlockM + r;  // row within the part
-      const float inv = inverse(l_run), down = power2(-E);
       if (!idle) {
-#pragma unroll
+        float* part = a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D);
+        const int pr = t * kBlockM + r;  // row within the part
+        const float inv = inverse(l_run), down = W == -INFINITY ? 0.f : ex2(W - m_ref);
+#pragma unroll 2
         for (int c = 0; c < D / 16; ++c) {
           uint32_t o[16];
           if (n > 0) {
@@ -761,17 +771,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (n > 0)
-              y = make_float4(__uint_as_float(o[4 * i]) * inv * down, __uint_as_float(o[4 * i + 1]) * inv * down,
-                              __uint_as_float(o[4 * i + 2]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
+            if (n > 0)  // columns in the codes' order
+              y = make_float4(__uint_as_float(o[4 * i]) * inv * down, __uint_as_float(o[4 * i + 2]) * inv * down,
+                              __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
             *reinterpret_cast<float4*>(part + ((size_t)(c * 4 + i) * kUnitRows + pr) * 4) = y;
           }
         }
         part[D * kUnitRows + pr] = m_ref;
         part[(D + 1) * kUnitRows + pr] = l_run;
       }
-      // O_t has been read: the next segment's first P V, which overwrites it, waits for this
-      // warpgroup's next P.
+      // O_t has been read: the next segment's first P V, which overwrites it, waits for these warps' next P.
       tc_fence_before();
     }
     if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
@@ -779,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) {
+  if (warp == kCopyWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
