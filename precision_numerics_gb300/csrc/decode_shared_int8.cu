@@ -33,6 +33,7 @@
 // (kTop), so that they keep 11 bits down to 2^-20 of it.  W and the maximum that the row sum is relative to
 // follow the running maxima of s + log2(vs) and of s only when the weights would grow too large: the
 // accumulators in TMEM are rescaled then, by the softmax's threads.  Sums and statistics are FP32.
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -52,7 +53,7 @@ namespace {
 constexpr int kSoftmaxWarps = 8, kCodeWarps = 4, kCopyWarp = 16, kMmaWarp = 17;
 constexpr int kThreads = 32 * 20;
 // Registers a thread at launch (five warps a quarter of an SM), and of the warpgroups of each kind.
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsCodes = 56, kRegsMma = 64;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 160, kRegsCodes = 48, kRegsMma = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsCodes + kRegsMma <= 5 * kRegsLaunch,
               "setmaxnreg split exceeds the launch pool");
 static_assert(kRegsMma <= kRegsLaunch && kRegsCodes <= kRegsLaunch && kRegsSoftmax >= kRegsLaunch,
@@ -78,6 +79,7 @@ struct Args {
   int B, n_q, H, Hkv, G, P, page_shift, blocks;
   int rows, row_blocks, runs;
   float scale_log2;
+  int* starts;  // [runs + 2]: each run's first tile, all tiles, and the key tiles of the prefix
   float* parts;
   const float* own;  // O / l [B n_q H][D], m [B n_q H], l [B n_q H] of the own parts
   uint16_t* o;
@@ -88,34 +90,27 @@ struct Args {
 __host__ __device__ constexpr size_t part_floats(int d) { return (size_t)kUnitRows * (d + 2); }
 
 // x / y, in 32 bits where they suffice.
-__device__ __forceinline__ long long divide(long long x, long long y) {
-  return x <= 0xffffffffll && y <= 0xffffffffll ? (long long)((unsigned)x / (unsigned)y) : x / y;
+__device__ __forceinline__ long long divide(long long x, int y) {
+  return x <= 0xffffffffll ? (long long)((unsigned)x / (unsigned)y) : x / y;
 }
 
-// How the key tiles of all units (unit = key head * row_blocks + row block) are dealt.  Tiles of
-// all units together are below 2^31 (the host's check).
-struct Deal {
-  int tiles;      // key tiles of the prefix
-  int runs;       // that are not empty
-  int last_cost;  // of a key tile of a head's last unit
-  long long head_cost;
-  __device__ __forceinline__ Deal(const Args& a, int len) {
-    tiles = (len + kBlockN - 1) / kBlockN;
-    last_cost = a.rows - (a.row_blocks - 1) * kUnitRows <= kBlockM ? kCostOne : kCostTwo;
-    head_cost = (long long)tiles * (kCostTwo * (a.row_blocks - 1) + last_cost);
-    const long long most = divide(head_cost * a.Hkv, kLeastRun * kCostTwo);
-    runs = tiles == 0 ? 0 : (int)max(1ll, min((long long)a.runs, most));
+// How the key tiles of all units (unit = key head * row_blocks + row block) are dealt to the runs.  Tiles of
+// all units together are below 2^31 (the host's check), and cost kCostTwo, or kCostOne in a head's last
+// unit where that has one row tile.  First tile (unit * tiles + key tile) of run c:
+__device__ __forceinline__ int run_begin(const Args& a, int tiles, int c) {
+  const int before = tiles * (a.row_blocks - 1);  // tiles of a head before its last unit
+  const int last_cost = a.rows - (a.row_blocks - 1) * kUnitRows <= kBlockM ? kCostOne : kCostTwo;
+  if (a.row_blocks == 1 || last_cost == kCostTwo) {  // all cost the same
+    const int all = tiles * a.row_blocks * a.Hkv, runs = min(a.runs, max(all / kLeastRun, 1));
+    return c >= runs ? all : (int)divide((long long)all * c, runs);
   }
-  // First tile (unit * tiles + key tile) of run c.
-  __device__ __forceinline__ int begin(const Args& a, int c) const {
-    if (c >= runs) return a.Hkv * a.row_blocks * tiles;
-    const long long x = divide(head_cost * a.Hkv * c, runs), h = divide(x, head_cost), y = x - h * head_cost;
-    const long long full = (long long)kCostTwo * tiles * (a.row_blocks - 1);
-    const long long i =
-        y < full ? divide(y, kCostTwo) : (long long)tiles * (a.row_blocks - 1) + divide(y - full, last_cost);
-    return (int)(h * a.row_blocks * tiles + i);
-  }
-};
+  const long long head_cost = (long long)before * kCostTwo + (long long)tiles * last_cost, all = head_cost * a.Hkv;
+  const int runs = (int)max(1ll, min((long long)a.runs, all / (kLeastRun * kCostTwo)));
+  if (c >= runs) return tiles * a.row_blocks * a.Hkv;
+  const long long x = divide(all * c, runs), h = x / head_cost, y = x - h * head_cost;
+  const long long full = (long long)before * kCostTwo;
+  return (int)(h * a.row_blocks * tiles + (y < full ? y / kCostTwo : before + (y - full) / last_cost));
+}
 
 // The prefix's length as it is used; one that the table has no room for is cut and reported.
 __device__ __forceinline__ int prefix_length(const Args& a, bool report) {
@@ -128,15 +123,17 @@ __device__ __forceinline__ int prefix_length(const Args& a, bool report) {
 
 // A run as every role goes through it: key tiles [k0, k0 + nk) of unit (h, rb), `left` tiles behind them.
 struct Walk {
-  int h, rb, k0, nk, left, tiles;
-  __device__ __forceinline__ Walk(const Args& a, const Deal& deal, bool none) {
-    tiles = deal.tiles;
-    const int at = none ? 0 : deal.begin(a, blockIdx.x);
-    left = none ? 0 : deal.begin(a, blockIdx.x + 1) - at;
-    const int unit = at / max(tiles, 1);
-    h = unit / a.row_blocks;
+  int h, rb, k0, nk, left, tiles, start;
+  __device__ __forceinline__ Walk(const Args& a, int len, bool none) {
+    tiles = none ? 0 : (len + kBlockN - 1) / kBlockN;
+    // Lane 1 finds where the next run begins.
+    const int at = run_begin(a, tiles, blockIdx.x + (threadIdx.x & 1));
+    start = __shfl_sync(0xffffffffu, at, 0);
+    left = __shfl_sync(0xffffffffu, at, 1) - start;
+    const int unit = (unsigned)start / (unsigned)max(tiles, 1);
+    h = a.row_blocks == 1 ? unit : unit / a.row_blocks;
     rb = unit - h * a.row_blocks;
-    k0 = at - unit * tiles;
+    k0 = start - unit * tiles;
     nk = 0;
   }
   __device__ __forceinline__ bool next(const Args& a) {
@@ -184,9 +181,9 @@ struct Cfg {
   static constexpr int kOffE = kOffHead + kHeads * (int)sizeof(Head);  // int8 [2][128]: exponent of a row's power of two
   static constexpr int kOffBar = (kOffE + 2 * 128 + 15) / 16 * 16;
   static constexpr int kSlots = 2 * (kRawTiles + 1);
-  // raw_full, raw_empty [slots], k_full, k_empty, v_full, v_empty [stages], head [kHeads], q_raw [8],
-  // q [2], s_full [2], p_full [2], o_done [2], final
-  static constexpr int kNumBars = 2 * kSlots + 4 * kStages + kHeads + 17;
+  // raw_full, raw_empty [slots], k_full, k_empty, v_full, v_empty [stages], head [kHeads], q [2],
+  // s_full [2], p_full [2], o_done [2], final
+  static constexpr int kNumBars = 2 * kSlots + 4 * kStages + kHeads + 9;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
   static_assert(kTileBytes == 2 * kRawBytes, "the place of a Q tile holds a key tile's codes");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
@@ -250,8 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   uint64_t* bar_vfull = bar_kempty + C::kStages;
   uint64_t* bar_vempty = bar_vfull + C::kStages;
   uint64_t* bar_head = bar_vempty + C::kStages;
-  uint64_t* bar_qraw = bar_head + C::kHeads;
-  uint64_t* bar_q = bar_qraw + 8;
+  uint64_t* bar_q = bar_head + C::kHeads;
   uint64_t* bar_sfull = bar_q + 2;
   uint64_t* bar_pfull = bar_sfull + 2;
   uint64_t* bar_odone = bar_pfull + 2;
@@ -273,7 +269,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       mbar_init(&bar_vempty[s], 1);
     }
     for (int s = 0; s < C::kHeads; ++s) mbar_init(&bar_head[s], 1);
-    for (int s = 0; s < 8; ++s) mbar_init(&bar_qraw[s], 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar_q[t], 4);
       mbar_init(&bar_sfull[t], 1);
@@ -295,7 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   const bool abort_all = __any_sync(0xffffffffu, tmem_slot[1] != 0);
   if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
   const int len = __shfl_sync(0xffffffffu, prefix_length(a, threadIdx.x == 0 && blockIdx.x == 0), 0);
-  Walk sg(a, Deal(a, len), abort_all);
+  Walk sg(a, len, abort_all);
+  if (threadIdx.x == 32 * kCopyWarp) {
+    a.starts[blockIdx.x] = sg.start;
+    if (blockIdx.x == gridDim.x - 1) {
+      a.starts[a.runs] = sg.start + sg.left;
+      a.starts[a.runs + 1] = sg.tiles;
+    }
+  }
   // All units have one row tile: one copy of Q, and a longer ring.
   const bool one = a.rows <= kBlockM;
   const int slots = one ? 2 * (C::kRawTiles + 1) : 2 * C::kRawTiles;
@@ -545,57 +547,59 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       const int first = sg.rb * kUnitRows + (two ? t * kBlockM : 0);  // the tile's first row
       const int have = min(kBlockM, a.rows - first);                  // and how many it has
       // -------------------------------------------------------- Q rows
-      // This warp's 32 rows, a lane each, are copied to their places in the tile and there divided and
-      // swizzled (which moves units within 128 bytes), kLanes lanes a row.  The products that read
-      // the rows before are complete: the softmax has had their results, of both halves where they share them.
+      // This warp's 32 rows, kLanes lanes a row and kBatch loads of a lane in flight, divided by a power of two
+      // and swizzled.  The products that read the rows before are complete: the softmax has had their results,
+      // of both halves where they share them.
       if (!one || t == 0) {
-        uint64_t* bar = &bar_qraw[warp];
+        int b, tok, gg;
+        row_of(a, min(first + r, a.rows - 1), b, tok, gg);  // each lane finds a row
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(
+            a.q + b * a.q_batch + tok * a.q_token + (long long)(sg.h * a.G + gg) * a.q_head);
         if (one && items > 0) {
           ok = warp_wait(&bar_odone[1], (items - 1) & 1);
           if (!ok) break;
         }
-        fence_proxy_async_smem();
-        if (lane == 0) mbar_arrive_expect_tx(bar, max(0, min(32, have - w0)) * D * 2);
-        __syncwarp();
-        if (r < have) {
-          int b, tok, gg;
-          row_of(a, first + r, b, tok, gg);
-          const uint16_t* from = a.q + b * a.q_batch + tok * a.q_token + (long long)(sg.h * a.G + gg) * a.q_head;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            bulk_load(sQ + t * C::kTileBytes + c * C::kChunkBytes + r * 128, from + c * 64, 128, bar);
-        }
-        ok = warp_wait(bar, items & 1);
-        if (!ok) break;
-        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kAtOnce;
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
         const int u = lane % kLanes;
         const uint32_t chunk = smem_u32(sQ) + t * C::kTileBytes + (u >> 3) * C::kChunkBytes;
-#pragma unroll 4
-        for (int i = 0; i < kTurns; ++i) {
-          const int rr = w0 + i * kAtOnce + lane / kLanes;
-          uint32_t w[4] = {0u, 0u, 0u, 0u};
-          if (rr < have)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(chunk + rr * 128 + (u & 7) * 16)
-                         : "memory");
-          float x[8], m = 0.f;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += kBatch * kAtOnce) {
+          uint4 x[kBatch];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[2 * k] = __uint_as_float(w[k] << 16);
-            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-            m = fmaxf(m, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+          for (int k = 0; k < kBatch; ++k)
+            x[k] = __ldcg(reinterpret_cast<const uint4*>(
+                              __shfl_sync(0xffffffffu, mine, i0 + k * kAtOnce + lane / kLanes)) + u);
+          float m[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            m[k] = 0.f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              m[k] = fmax3(m[k], fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xFFFF0000u)));
           }
 #pragma unroll
-          for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-          // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
-          const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u) - 127, -126), 126);
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          // (All lanes of the row have read it: the maximum needed them.)  Elements in the codes' order.
-          st_shared_v4(chunk + sw128_offset(rr, u & 7), pack_f16x2(x[0] * down, x[2] * down),
-                       pack_f16x2(x[1] * down, x[3] * down), pack_f16x2(x[4] * down, x[6] * down),
-                       pack_f16x2(x[5] * down, x[7] * down));
-          if (u == 0) s_e[t * 128 + rr] = (int8_t)e;
+          for (int off = kLanes / 2; off > 0; off >>= 1)
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], off));
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int rr = w0 + i0 + k * kAtOnce + lane / kLanes;
+            // 2^e <= m < 2^(e+1), e within the range whose negative is a normal exponent.
+            const int e = min(max((int)((__float_as_uint(m[k]) >> 23) & 255u) - 127, -126), 126);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            float y[8];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              y[2 * z] = __uint_as_float(w[z] << 16) * down;
+              y[2 * z + 1] = __uint_as_float(w[z] & 0xFFFF0000u) * down;
+            }
+            // Elements in the codes' order.
+            st_shared_v4(chunk + sw128_offset(rr, u & 7), pack_f16x2(y[0], y[2]), pack_f16x2(y[1], y[3]),
+                         pack_f16x2(y[4], y[6]), pack_f16x2(y[5], y[7]));
+            if (u == 0) s_e[t * 128 + rr] = (int8_t)e;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -606,10 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       const int n = two ? sg.nk : (sg.nk + 1 - t) / 2;  // key tiles of this half
       const bool idle = w0 >= have;  // none of the warp's rows is one
       float m_ref = -INFINITY, W = -INFINITY, l_run = 0.f;
+      float minus_m = 0.f, up = 1.f;  // -m_ref and 2^(m_ref - W), once the row has seen something
+      bool any_large = false;         // of the warp's rows' maxima
       for (int j = 0; j < n; ++j) {
+        // (The tile's scales are there as well: the codes' warps waited for them, the products for the codes.)
         ok = warp_wait(&bar_sfull[t], (sc + j) & 1);
         const int tile = g + (two ? j : 2 * j + t);
-        if (ok) ok = warp_wait(&bar_head[tile % C::kHeads], (tile / C::kHeads) & 1);
         if (!ok) break;
         tc_fence_after();
         if (!idle) {
@@ -628,13 +634,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             }
             tmem_wait_st();
           };
-          if (hd.hidden)
+          uint32_t s[32];
+          tmem_ld32(tS, s);
+          if (hd.hidden) {
+            tmem_wait_ld();
             change([&](int i, uint32_t (&s)[16]) {
               const int seen = hd.seen[i];
 #pragma unroll
               for (int x = 0; x < 16; ++x)
                 if (x >= seen) s[x] = __float_as_uint(-INFINITY);
             });
+            tmem_ld32(tS, s);
+          }
           // Factor of the scores of group i of 16 (base 2); not 0, so that hidden ones stay -inf.
           bool rounded = false;  // the row's scores have been multiplied with it
           auto factor = [&](int i) { return rounded ? 1.f : fmaxf(f * hd.ks[i], 0x1p-126f); };
@@ -642,11 +653,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           // Where they could be too large (which the tile's sum tells), and in the first tile, the row's
           // references move to the maximum, the accumulators with them, and the weights are formed again.
           // Other rows of the warp form the same ones again: no row's bits depend on another's.
+          // The fma below leaves the rounding of the largest score's product, half its last bit, in the exponent.
+          // From 2^24 on that could take a weight out of FP16: such a row's products are rounded first.
+          auto round_large = [&]() {
+            const bool large = !rounded && fabsf(minus_m) >= 0x1p24f;
+            tmem_wait_ld();
+            change([&](int i, uint32_t (&s)[16]) {
+              const float k = large ? factor(i) : 1.f;
+#pragma unroll
+              for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * k);
+            });
+            rounded = rounded || large;
+            tmem_ld32(tS, s);
+          };
+          if (any_large) round_large();
           bool moves = j == 0, again = j == 0;
           float sum;
           uint32_t pk[64];
           while (true) {
             if (again) {
+              tmem_wait_ld();
               float mt = -INFINITY, mw = -INFINITY;  // largest score and largest log2 of a weight
 #pragma unroll 1
               for (int i = 0; i < 8; ++i) {
@@ -668,6 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                 f_o = ex2(W - W_new);
                 m_ref = m_new;
                 W = W_new;
+                minus_m = -m_new;
+                up = ex2(m_new - W_new);
               }
               if (j > 0) {
                 const uint64_t f2 = f2_pack(f_o, f_o);
@@ -687,28 +715,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                   tmem_st16(tO + c * 16, o);
                 }
               }
+              any_large = __any_sync(0xffffffffu, fabsf(minus_m) >= 0x1p24f);
+              if (any_large)
+                round_large();
+              else
+                tmem_ld32(tS, s);
             }
-            const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-            const float up = W == -INFINITY ? 1.f : ex2(m_use - W);
-            // The fma below leaves the rounding of the largest score's product, half its last bit, in the exponent.
-            // From 2^24 on that could take a weight out of FP16: such a row's products are rounded first.
-            const bool large = !rounded && fabsf(m_use) >= 0x1p24f;
-            if (__any_sync(0xffffffffu, large)) {
-              change([&](int i, uint32_t (&s)[16]) {
-                const float k = large ? factor(i) : 1.f;
-#pragma unroll
-                for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * k);
-              });
-              rounded = rounded || large;
-            }
-            const uint64_t nm2 = f2_pack(-m_use, -m_use);
+            const uint64_t nm2 = f2_pack(minus_m, minus_m);
             uint64_t sums2[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sums2[i] = 0ull;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_ld32(tS + c * 32, s);
+              if (c > 0) tmem_ld32(tS + c * 32, s);
               uint64_t k2[32 / GROUP], v2[32 / GROUP];
 #pragma unroll
               for (int i = 0; i < 32 / GROUP; ++i) {
@@ -735,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             for (int i = 0; i < 4; ++i) f2_unpack(sums2[i], sums[2 * i], sums[2 * i + 1]);
             sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
             if (again) break;
-            moves = !(sum * fminf(hd.v_most * up, 0x1p127f) <= kMost && sum <= kMostSum);
+            moves = m_ref == -INFINITY || !(sum * fminf(hd.v_most * up, 0x1p127f) <= kMost && sum <= kMostSum);
             again = __any_sync(0xffffffffu, moves);
             if (!again) break;
           }
@@ -760,22 +779,21 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         float* part = a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D);
         const int pr = t * kBlockM + r;  // row within the part
         const float inv = inverse(l_run), down = W == -INFINITY ? 0.f : ex2(W - m_ref);
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[16];
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
           if (n > 0) {
-            tmem_ld16(tO + c * 16, o);
+            tmem_ld32(tO + c * 32, o);
             tmem_wait_ld();
             reg_fence(o);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (n > 0)  // columns in the codes' order
-              y = make_float4(__uint_as_float(o[4 * i]) * inv * down, __uint_as_float(o[4 * i + 2]) * inv * down,
-                              __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
-            *reinterpret_cast<float4*>(part + ((size_t)(c * 4 + i) * kUnitRows + pr) * 4) = y;
-          }
+          for (int i = 0; i < 8; ++i)  // columns in the codes' order
+            *reinterpret_cast<float4*>(part + ((size_t)(c * 8 + i) * kUnitRows + pr) * 4) =
+                make_float4(__uint_as_float(o[4 * i]) * inv * down, __uint_as_float(o[4 * i + 2]) * inv * down,
+                            __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
         }
         part[D * kUnitRows + pr] = m_ref;
         part[(D + 1) * kUnitRows + pr] = l_run;
@@ -794,88 +812,106 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   }
 }
 
-__device__ __forceinline__ float4 weighted(const float4& x, float inv, float l) {
-  return make_float4(x.x * inv * l, x.y * inv * l, x.z * inv * l, x.w * inv * l);
-}
-
-// Joins the parts of 32 rows of a unit and their own part.  A lane has a row, a warp D / 8
-// of the columns; the order of the sums is that of the runs.
-constexpr int kJoinRows = 32, kJoinThreads = 256;
+// Joins the parts of 32 rows of a unit and their own part, 4 columns a warp; a lane has a row.  First every
+// warp takes some of the parts' maxima and sums, then all of them its columns, whose loads wait for nothing
+// else.  The order of the sums is that of the runs.
+constexpr int kJoinRows = 32, kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
+constexpr int kJoinBatch = 8;    // parts whose loads a thread has in flight together
+constexpr int kJoinShares = 64;  // parts whose shares of the rows are held
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a) {
-  constexpr int kQuads = D / 32;  // of columns a thread
+  __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32], s_share[kJoinShares][32];
+  constexpr int kQuads = D / 4 / kJoinWarps;
   griddep_launch_dependents();
   griddep_wait();
-  const int unit = blockIdx.x / (kUnitRows / kJoinRows), rows0 = blockIdx.x % (kUnitRows / kJoinRows) * kJoinRows;
+  unsigned x = blockIdx.x;
+  const int quad = x % kQuads * kJoinWarps, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  x /= kQuads;
+  const int rows0 = x % (kUnitRows / kJoinRows) * kJoinRows, unit = x / (kUnitRows / kJoinRows);
   const int h = unit / a.row_blocks, rb = unit - h * a.row_blocks;
   if (rb * kUnitRows + rows0 >= a.rows) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Deal deal(a, prefix_length(a, false));
-  const int from = unit * deal.tiles, to = from + deal.tiles;
-  const int mine = threadIdx.x < deal.runs ? deal.begin(a, threadIdx.x) : to;
-  const int c0 = __syncthreads_count(mine <= from && (int)threadIdx.x < deal.runs) - 1;
-  const int c1 = __syncthreads_count(mine < to) - 1;
-  const int r = rows0 + lane, row = rb * kUnitRows + r;
-  if (row >= a.rows) return;
-  const bool two = a.rows - rb * kUnitRows > kBlockM;
+  const int begin = (int)threadIdx.x < a.runs ? __ldcg(a.starts + threadIdx.x) : INT_MAX;
+  const int tiles = __ldcg(a.starts + a.runs + 1);
+  const int r = rows0 + lane, row = min(rb * kUnitRows + r, a.rows - 1);
   int b, tok, gg;
   row_of(a, row, b, tok, gg);
   const size_t out = ((size_t)b * a.n_q + tok) * a.H + h * a.G + gg;
   const size_t all = (size_t)a.B * a.n_q * a.H;
-  float M = __ldcg(a.own + all * D + out), L = __ldcg(a.own + all * D + all + out);
-  float4 o[kQuads];
+  const int col = (quad + warp) * 4;
+  const float own_m = __ldcg(a.own + all * D + out), own_l = __ldcg(a.own + all * (D + 1) + out);
+  const float4 own_o = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col));
+  // The runs that the unit's tiles are in.  (Runs without a tile begin where the tiles end.)
+  const int from = unit * tiles, to = from + tiles;
+  const int c0 = __syncthreads_count(begin <= from) - 1, c1 = __syncthreads_count(begin < to) - 1;
+  // A unit with one row tile has two parts a run, beside one another.
+  const int halves = a.rows - rb * kUnitRows > kBlockM ? 1 : 2;
+  const int n = tiles == 0 ? 0 : (c1 - c0 + 1) * halves;
+  const float* parts = a.parts + (size_t)(c0 + unit) * part_floats(D);
+  auto part = [&](int i) { return halves == 1 ? parts + i * part_floats(D) + r
+                                              : parts + (i >> 1) * part_floats(D) + (r + (i & 1) * kBlockM); };
+  auto load4 = [&](int i) {
+    const float* p = halves == 1 ? parts + i * part_floats(D) : parts + (i >> 1) * part_floats(D);
+    return __ldcg(reinterpret_cast<const float4*>(p) + (col / 4) * kUnitRows + r + (halves == 1 ? 0 : (i & 1) * kBlockM));
+  };
+
+  float M = warp == 0 ? own_m : -INFINITY, L = warp == 0 ? own_l : 0.f;
+  for (int i0 = warp; i0 < n; i0 += kJoinBatch * kJoinWarps) {
+    float m[kJoinBatch], l[kJoinBatch];
 #pragma unroll
-  for (int i = 0; i < kQuads; ++i)
-    o[i] = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + (warp * kQuads + i) * 4));
-  const int halves = two ? 1 : 2;
-  const int n = deal.runs == 0 ? 0 : (c1 - c0 + 1) * halves;
-  constexpr int kBatch = 4;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    float m[kBatch], l[kBatch];
-    float4 x[kBatch][kQuads];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      m[k] = -INFINITY, l[k] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) x[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + k < n) {
-        const int c = c0 + (i0 + k) / halves;
-        const int pr = r + (i0 + k) % halves * kBlockM;
-        const float* part = a.parts + (size_t)(c + unit) * part_floats(D);
-        m[k] = __ldcg(part + D * kUnitRows + pr);
-        l[k] = __ldcg(part + (D + 1) * kUnitRows + pr);
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i)
-          x[k][i] = __ldcg(reinterpret_cast<const float4*>(part + ((size_t)(warp * kQuads + i) * kUnitRows + pr) * 4));
-      }
+    for (int k = 0; k < kJoinBatch; ++k) {
+      const int i = i0 + k * kJoinWarps;
+      m[k] = i < n ? __ldcg(part(i) + D * kUnitRows) : -INFINITY;
+      l[k] = i < n ? __ldcg(part(i) + (D + 1) * kUnitRows) : 0.f;
     }
     float m_new = M;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) m_new = fmaxf(m_new, m[k]);
+    for (int k = 0; k < kJoinBatch; ++k) m_new = fmaxf(m_new, m[k]);
     const float m_use = m_new == -INFINITY ? 0.f : m_new;
-    const float before = L * ex2(M - m_use);
+    L *= ex2(M - m_use);
     M = m_new;
-    L = before;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) L += l[k] *= ex2(m[k] - m_use);
-    const float inv = inverse(L);
-    // Values times 1 / L, then times their weight: the two factors' product could fall below FP32's
-    // range where a small weight meets large values.
-#pragma unroll
-    for (int i = 0; i < kQuads; ++i) o[i] = weighted(o[i], inv, before);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const float4 y = weighted(x[k][i], inv, l[k]);
-        o[i].x += y.x, o[i].y += y.y, o[i].z += y.z, o[i].w += y.w;
-      }
+    for (int k = 0; k < kJoinBatch; ++k) L += l[k] * ex2(m[k] - m_use);
   }
-  uint16_t* to_o = a.o + out * D + warp * kQuads * 4;
+  s_m[warp][lane] = M;
+  s_l[warp][lane] = L;
+  __syncthreads();
+  M = s_m[0][lane];
 #pragma unroll
-  for (int i = 0; i < kQuads; ++i)
-    *reinterpret_cast<uint2*>(to_o + 4 * i) = make_uint2(pack_bf16x2(o[i].x, o[i].y), pack_bf16x2(o[i].z, o[i].w));
-  if (warp == 0) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+  for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w][lane]);
+  const float m_use = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) L += s_l[w][lane] * ex2(s_m[w][lane] - m_use);
+  // Values times 1 / L, then times their weight: the two factors' product could fall below FP32's range
+  // where a small weight meets large values.
+  const float inv = inverse(L);
+  auto add = [&](float4& o, const float4& v, float l) {
+    o.x += v.x * inv * l, o.y += v.y * inv * l, o.z += v.z * inv * l, o.w += v.w * inv * l;
+  };
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  add(o, own_o, own_l * ex2(own_m - m_use));
+  for (int i0 = 0; i0 < n; i0 += kJoinShares) {
+    const int some = min(kJoinShares, n - i0);
+    if (i0 > 0) __syncthreads();
+    for (int i = warp; i < some; i += kJoinWarps)
+      s_share[i][lane] = __ldcg(part(i0 + i) + (D + 1) * kUnitRows) * ex2(__ldcg(part(i0 + i) + D * kUnitRows) - m_use);
+    float4 y[kJoinBatch];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) y[k] = i + k < some ? load4(i0 + i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    fetch(0);
+    __syncthreads();
+    for (int i = 0; i < some; i += kJoinBatch) {
+      if (i > 0) fetch(i);
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k)
+        if (i + k < some) add(o, y[k], s_share[i + k][lane]);
+    }
+  }
+  if (rb * kUnitRows + r >= a.rows) return;
+  *reinterpret_cast<uint2*>(a.o + out * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  if (col == 0) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // Runs that the prefix's tiles are dealt in: one CTA an SM.  (The full device's count where
@@ -886,13 +922,14 @@ int shared_runs() {
 }
 
 struct Layout {
-  size_t parts, decode, bytes;  // byte offsets; the own part is at 0
+  size_t starts, parts, decode, bytes;  // byte offsets; the own part is at 0
 };
 Layout layout(const PagedCache& c, int n_q, int H) {
   const size_t all = (size_t)c.B * n_q * H, rows = all / c.Hkv;
   const size_t units = (size_t)c.Hkv * ((rows + kUnitRows - 1) / kUnitRows);
   Layout w;
-  w.parts = align256(all * (c.d + 2) * sizeof(float));
+  w.starts = align256(all * (c.d + 2) * sizeof(float));
+  w.parts = w.starts + align256((shared_runs() + 2) * sizeof(int));
   w.decode = w.parts + align256((units + shared_runs()) * part_floats(c.d) * sizeof(float));
   w.bytes = w.decode + decode_workspace_bytes(c, n_q, H);
   return w;
@@ -930,6 +967,7 @@ cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const 
   a.runs = shared_runs();
   a.scale_log2 = scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
+  a.starts = reinterpret_cast<int*>(ws + w.starts);
   a.parts = reinterpret_cast<float*>(ws + w.parts);
   a.own = reinterpret_cast<const float*>(ws);
   a.o = static_cast<uint16_t*>(o), a.lse = lse;
@@ -942,7 +980,7 @@ cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const 
   err = launch_decode_int8(c, q, strides, lens, nullptr, nullptr, n_q, H, scale, ws + w.decode, stream,
                            reinterpret_cast<float*>(ws));
   if (err != cudaSuccess) return err;
-  const unsigned blocks = (unsigned)(a.Hkv * a.row_blocks) * (kUnitRows / kJoinRows);
+  const unsigned blocks = (unsigned)(a.Hkv * a.row_blocks) * (kUnitRows / kJoinRows) * (c.d / 4 / kJoinWarps);
   auto join = c.d == 128 ? shared_join_kernel<128> : shared_join_kernel<64>;
   return launch_pdl(join, dim3(blocks), dim3(kJoinThreads), 0, stream, a);
 }
