@@ -311,77 +311,72 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == kCopyWarp) {
       // ------------------------------------------------------------ copies
-      // Lane x: group x % 8 (16 positions) of the tile, K in lanes 0 to 7, V in 8 to 15.  Page numbers of
-      // four key tiles are read at a time, scales a tile ahead.
+      // Key tiles by fours: lane x has the page of group x % 8 (16 positions) of the x / 8-th tile, and its
+      // scales.  Pages are read two fours ahead, scales one: both take as long as a tile.
       const int group = lane & 7;
-      const bool is_v = lane >= 8;
-      const uint8_t* from = is_v ? a.v : a.k;
-      const float* scales = is_v ? a.v_scale : a.k_scale;
       const int page_mask = (1 << a.page_shift) - 1;
       bool ok = true;
-      int e = 0, first = -8, ids = -1, ids_next = -1;  // lane x: page of group x % 8 of key tile first + x / 8
+      // The page of a group: one whose first position is seen, as a whole, or -1.
       auto pages_at = [&](int tile) {
-        const long long pos = ((long long)tile + (lane >> 3)) * kBlockN + 16 * group;
+        const long long pos = (((long long)tile + (lane >> 3)) * kBlockN + 16 * group) & ~(long long)page_mask;
         return pos < len ? __ldcg(a.table + (pos >> a.page_shift)) : -1;
       };
-      auto page_of = [&](int tile) {
-        if (tile < first || tile >= first + 4) {
-          ids = tile == first + 4 ? ids_next : pages_at(tile);
-          first = tile;
-          ids_next = pages_at(tile + 4);
-          if (((long long)tile + (lane >> 3)) * kBlockN + 16 * group < len && (ids < 0 || ids >= a.P)) {
-            set_fail(ATTN_ERR_INVALID_ARG);
-            ids = -1;
-          }
+      auto checked = [&](int tile, int id) {
+        const long long pos = (((long long)tile + (lane >> 3)) * kBlockN + 16 * group) & ~(long long)page_mask;
+        if (pos < len && (id < 0 || id >= a.P)) {
+          set_fail(ATTN_ERR_INVALID_ARG);
+          return -1;
         }
-        return __shfl_sync(0xffffffffu, ids, (tile - first) * 8 + group);
+        return id;
       };
-      bool more = sg.next(a);
-      int id = more ? page_of(sg.k0) : -1;
-      float scale = more && lane < 16 ? __ldcg(scales + (max(id, 0) * a.Hkv + sg.h)) : 0.f;
-      int issued = 0;
-      for (int g = 0; more; ++g) {
-        const int tile = sg.k0 + e, h = sg.h;
-        // K, then V.
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int slot = (2 * g + x) % slots, use = (2 * g + x) / slots;
-          if (use > 0) ok = ok && warp_wait(&bar_rempty[slot], (use - 1) & 1);
-          if (!ok) break;
-          const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
-          ++issued;
-          if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[slot], __popc(loaded) * 16 * D);
-          __syncwarp();
-          if (lane < 16 && is_v == (x == 1) && id >= 0)
-            bulk_load(raw + slot * C::kRawBytes + group * 16 * D,
-                      from + (size_t)(((id * a.Hkv + h) << a.page_shift) + ((16 * group) & page_mask)) * D, 16 * D,
-                      &bar_rfull[slot]);
-        }
-        if (!ok) break;
-        // The slot's last tile, kHeads before, has been through the softmax: the ring's place was free, so the
-        // products S of the tile that many tiles and stages ago are complete.
-        Head& hd = heads[g % C::kHeads];
-        const int seen = id >= 0 ? max(0, min(16, len - (tile * kBlockN + 16 * group))) : 0;
-        const bool hidden = __any_sync(0xffffffffu, seen < 16);
-        const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
-        const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, is_v && lane < 16 ? __float_as_uint(scale) : 0u));
-        if (lane < 8) {
-          hd.ks[group] = scale;
-          hd.seen[group] = (uint8_t)seen;
-        } else if (lane < 16) {
-          hd.vs[group] = scale;
-        }
-        if (lane == 0) hd.v_most = most, hd.hidden = hidden, hd.loaded = loaded;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_head[g % C::kHeads]);
-        if (++e == sg.nk) {
-          e = 0;
-          more = sg.next(a);
-        }
-        if (more) {
-          id = page_of(sg.k0 + e);
-          // A page that is not seen takes any scale: its positions are hidden.
-          if (lane < 16) scale = __ldcg(scales + (max(id, 0) * a.Hkv + sg.h));
+      int issued = 0, g = 0;
+      while (ok && sg.next(a)) {
+        // A page that is not seen takes any scale: its positions are hidden.
+        auto scale_at = [&](const float* scales, int id) { return __ldcg(scales + (max(id, 0) * a.Hkv + sg.h)); };
+        int ids = checked(sg.k0, pages_at(sg.k0)), ids_next = pages_at(sg.k0 + 4);
+        float ks = scale_at(a.k_scale, ids), vs = scale_at(a.v_scale, ids);
+        for (int e0 = 0; e0 < sg.nk && ok; e0 += 4) {
+          const int ids_after = pages_at(sg.k0 + e0 + 8);
+          ids_next = checked(sg.k0 + e0 + 4, ids_next);
+          const float ks_next = scale_at(a.k_scale, ids_next), vs_next = scale_at(a.v_scale, ids_next);
+          for (int e = e0; e < min(e0 + 4, sg.nk); ++e, ++g) {
+            const int lanes = (e - e0) * 8;  // those of the tile
+            const int id = __shfl_sync(0xffffffffu, ids, lanes + group);
+            const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
+            // K, then V: a copy a page.
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              const int slot = issued % slots, use = issued / slots;
+              if (use > 0) ok = ok && warp_wait(&bar_rempty[slot], (use - 1) & 1);
+              if (!ok) break;
+              ++issued;
+              if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[slot], __popc(loaded) * 16 * D);
+              __syncwarp();
+              if (lane < 8 && id >= 0 && ((16 * group) & page_mask) == 0)
+                bulk_load(raw + slot * C::kRawBytes + group * 16 * D,
+                          (x == 0 ? a.k : a.v) + (size_t)((id * a.Hkv + sg.h) << a.page_shift) * D,
+                          min(page_mask + 1, kBlockN) * D, &bar_rfull[slot]);
+            }
+            if (!ok) break;
+            // The slot's last tile, kHeads before, has been through the softmax: the ring's place was free, so the
+            // products S of the tile that many tiles and stages ago are complete.
+            Head& hd = heads[g % C::kHeads];
+            const int seen = id >= 0 ? max(0, min(16, len - ((sg.k0 + e) * kBlockN + 16 * group))) : 0;
+            const bool hidden = __any_sync(0xffffffffu, seen < 16);
+            const float k = __shfl_sync(0xffffffffu, ks, lanes + group), v = __shfl_sync(0xffffffffu, vs, lanes + group);
+            const float most =
+                __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+            if (lane < 8) {
+              hd.ks[group] = k;
+              hd.vs[group] = v;
+              hd.seen[group] = (uint8_t)seen;
+            }
+            if (lane == 0) hd.v_most = most, hd.hidden = hidden, hd.loaded = loaded;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_head[g % C::kHeads]);
+          }
+          ids = ids_next, ids_next = ids_after;
+          ks = ks_next, vs = vs_next;
         }
       }
       if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
@@ -559,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           ok = warp_wait(&bar_odone[1], (items - 1) & 1);
           if (!ok) break;
         }
-        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 32 / kAtOnce;
         const int u = lane % kLanes;
         const uint32_t chunk = smem_u32(sQ) + t * C::kTileBytes + (u >> 3) * C::kChunkBytes;
 #pragma unroll 1
