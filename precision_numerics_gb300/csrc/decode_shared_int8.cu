@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
         }
         return id;
       };
-      int issued = 0, g = 0;
+      int g = 0, slot = 0;
+      unsigned use = 0;  // rounds of the ring so far
       while (ok && sg.next(a)) {
         // A page that is not seen takes any scale: its positions are hidden.
         auto scale_at = [&](const float* scales, int id) { return __ldcg(scales + (max(id, 0) * a.Hkv + sg.h)); };
@@ -346,16 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             // K, then V: a copy a page.
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
-              const int slot = issued % slots, use = issued / slots;
-              if (use > 0) ok = ok && warp_wait(&bar_rempty[slot], (use - 1) & 1);
+              if (use > 0) ok = warp_wait(&bar_rempty[slot], (use - 1) & 1);
               if (!ok) break;
-              ++issued;
               if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[slot], __popc(loaded) * 16 * D);
               __syncwarp();
               if (lane < 8 && id >= 0 && ((16 * group) & page_mask) == 0)
                 bulk_load(raw + slot * C::kRawBytes + group * 16 * D,
                           (x == 0 ? a.k : a.v) + (size_t)((id * a.Hkv + sg.h) << a.page_shift) * D,
                           min(page_mask + 1, kBlockN) * D, &bar_rfull[slot]);
+              if (++slot == slots) slot = 0, ++use;
             }
             if (!ok) break;
             // The slot's last tile, kHeads before, has been through the softmax: the ring's place was free, so the
@@ -381,7 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       }
       if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
       // Do not leave while copies into this CTA's shared memory are in flight.
-      for (int x = max(0, issued - slots); x < issued; ++x) mbar_wait(&bar_rfull[x % slots], (x / slots) & 1);
+      for (int x = 0; x < slots; ++x) {
+        const unsigned uses = use + (x < slot ? 1 : 0);
+        if (uses > 0) mbar_wait(&bar_rfull[x], (uses - 1) & 1);
+      }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, false);
@@ -472,10 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     const uint32_t from = smem_u32(raw) + row * D + unit * 16;
     const uint32_t to0 = (unit >> 2) * C::kChunkBytes + sw128_offset(row, (unit & 3) * 2);
     const uint32_t to1 = to0 ^ 16u;  // the odd unit beside it
-    // Slot x of the ring to the tile at `to`, which is free when `empty` has completed its phase.
-    auto convert = [&](int x, unsigned loaded, uint32_t to, uint64_t* empty, int phase) {
-      const int slot = x % slots;
-      if (!warp_wait(&bar_rfull[slot], (x / slots) & 1)) return false;
+    // A slot of the ring to the tile at `to`, which is free when `empty` has completed its phase.
+    auto convert = [&](int slot, unsigned round, unsigned loaded, uint32_t to, uint64_t* empty, int phase) {
+      if (!warp_wait(&bar_rfull[slot], round & 1)) return false;
       constexpr int kBatch = 4;
 #pragma unroll
       for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
@@ -508,18 +510,21 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     };
     uint64_t* bar_full = kv == 0 ? bar_kfull : bar_vfull;  // the empty ones are behind them
     const uint32_t tiles = smem_u32(kv == 0 ? sK : sV);
-    int g = 0;
+    int slot = kv, hd = 0, st = 0;  // places in the ring, among the scales and the tiles
+    unsigned round = 0, hd_round = 0, st_round = 0;
     while (ok && sg.next(a)) {
-      for (int e = 0; e < sg.nk; ++e, ++g) {
-        const int st = g % C::kStages;
-        ok = warp_wait(&bar_head[g % C::kHeads], (g / C::kHeads) & 1);
+      for (int e = 0; e < sg.nk; ++e) {
+        ok = warp_wait(&bar_head[hd], hd_round & 1);
         if (!ok) break;
-        ok = convert(2 * g + kv, heads[g % C::kHeads].loaded, tiles + st * C::kTileBytes, bar_full + C::kStages + st,
-                     g / C::kStages - 1);
+        ok = convert(slot, round, heads[hd].loaded, tiles + st * C::kTileBytes, bar_full + C::kStages + st,
+                     (int)st_round - 1);
         if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_full + st);
+        if ((slot += 2) >= slots) slot = kv, ++round;
+        if (++hd == C::kHeads) hd = 0, ++hd_round;
+        if (++st == C::kStages) st = 0, ++st_round;
       }
     }
     if (!ok && lane == 0) set_fail(ATTN_ERR_TIMEOUT);
