@@ -75,13 +75,13 @@ struct Args {
   long long q_batch, q_token, q_head;
   const uint8_t *k, *v;
   const float *k_scale, *v_scale;
-  const int *table, *len;  // of the prefix
+  const int *table, *len;  // of the prefix; or [B][blocks] and [B], of the own positions
   int B, n_q, H, Hkv, G, P, page_shift, blocks;
   int rows, row_blocks, runs;
   float scale_log2;
   int* starts;  // [runs + 2]: each run's first tile, all tiles, and the key tiles of the prefix
   float* parts;
-  const float* own;  // O / l [B n_q H][D], m [B n_q H], l [B n_q H] of the own parts
+  float* own;  // O / l [B n_q H][D], m [B n_q H], l [B n_q H] of the own parts
   uint16_t* o;
   float* lse;
 };
@@ -112,19 +112,27 @@ __device__ __forceinline__ int run_begin(const Args& a, int tiles, int c) {
   return (int)(h * a.row_blocks * tiles + (y < full ? y / kCostTwo : before + (y - full) / last_cost));
 }
 
-// The prefix's length as it is used; one that the table has no room for is cut and reported.
-__device__ __forceinline__ int prefix_length(const Args& a, bool report) {
-  const int len = __ldcg(a.len);
+// A length as it is used; one that the table has no room for is cut and reported.
+__device__ __forceinline__ int checked_length(const Args& a, int len, bool report) {
   const long long cap = (long long)a.blocks << a.page_shift;
   if (len >= 0 && len <= cap) return len;
   if (report) set_fail(ATTN_ERR_INVALID_ARG);
   return len < 0 ? 0 : (int)cap;
 }
 
-// A run as every role goes through it: key tiles [k0, k0 + nk) of unit (h, rb), `left` tiles behind them.
+// What a CTA does, as every role goes through it: key tiles [k0, k0 + nk) for rows of block rb of key head h.
+// OWN false: its run over the prefix, `left` tiles behind these.  OWN true: every gridDim.x-th (sequence, key
+// head, row block) over the sequence's own positions, of which there may be none.
+template <bool OWN>
 struct Walk {
-  int h, rb, k0, nk, left, tiles, start;
-  __device__ __forceinline__ Walk(const Args& a, int len, bool none) {
+  int b, h, rb, k0, nk, len, left, tiles, start;
+  __device__ __forceinline__ Walk(const Args& a, bool none) : b(0), nk(0) {
+    if constexpr (OWN) {
+      k0 = tiles = start = len = 0;
+      left = none ? INT_MAX : (int)blockIdx.x;
+      return;
+    }
+    len = __shfl_sync(0xffffffffu, checked_length(a, __ldcg(a.len), threadIdx.x == 0 && blockIdx.x == 0), 0);
     tiles = none ? 0 : (len + kBlockN - 1) / kBlockN;
     // Lane 1 finds where the next run begins.
     const int at = run_begin(a, tiles, blockIdx.x + (threadIdx.x & 1));
@@ -134,9 +142,20 @@ struct Walk {
     h = a.row_blocks == 1 ? unit : unit / a.row_blocks;
     rb = unit - h * a.row_blocks;
     k0 = start - unit * tiles;
-    nk = 0;
   }
   __device__ __forceinline__ bool next(const Args& a) {
+    if constexpr (OWN) {
+      const int copies = a.Hkv * a.row_blocks;
+      b = left / copies;
+      if (b >= a.B) return false;
+      const int copy = left - b * copies;
+      h = copy / a.row_blocks;
+      rb = copy - h * a.row_blocks;
+      len = __shfl_sync(0xffffffffu, checked_length(a, __ldcg(a.len + b), true), 0);
+      nk = (len + kBlockN - 1) / kBlockN;
+      left += gridDim.x;
+      return true;
+    }
     if (left == 0) return false;
     if (nk > 0) {
       k0 = 0;
@@ -147,7 +166,7 @@ struct Walk {
     return true;
   }
   // Two row tiles; else the key tiles alternate between the two halves of the CTA.
-  __device__ __forceinline__ bool two(const Args& a) const { return a.rows - rb * kUnitRows > kBlockM; }
+  __device__ __forceinline__ bool two(const Args& a) const { return OWN || a.rows - rb * kUnitRows > kBlockM; }
 };
 
 // Scales of a key tile in groups of 16 positions, and how many of each are seen.
@@ -231,7 +250,7 @@ __device__ __forceinline__ void row_of(const Args& a, int r, int& b, int& t, int
 }
 
 // GROUP: positions that share a page's scales for certain (16, or 32 in pages of 32 and more).
-template <int D, int GROUP>
+template <int D, int GROUP, bool OWN>
 __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -289,9 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   griddep_wait();
   const bool abort_all = __any_sync(0xffffffffu, tmem_slot[1] != 0);
   if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
-  const int len = __shfl_sync(0xffffffffu, prefix_length(a, threadIdx.x == 0 && blockIdx.x == 0), 0);
-  Walk sg(a, len, abort_all);
-  if (threadIdx.x == 32 * kCopyWarp) {
+  Walk<OWN> sg(a, abort_all);
+  if (!OWN && threadIdx.x == 32 * kCopyWarp) {
     a.starts[blockIdx.x] = sg.start;
     if (blockIdx.x == gridDim.x - 1) {
       a.starts[a.runs] = sg.start + sg.left;
@@ -299,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     }
   }
   // All units have one row tile: one copy of Q, and a longer ring.
-  const bool one = a.rows <= kBlockM;
+  const bool one = !OWN && a.rows <= kBlockM;
   const int slots = one ? 2 * (C::kRawTiles + 1) : 2 * C::kRawTiles;
   uint8_t* raw = smem + (one ? C::kTileBytes : C::kOffRaw);
 
@@ -317,13 +335,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       const int page_mask = (1 << a.page_shift) - 1;
       bool ok = true;
       // The page of a group: one whose first position is seen, as a whole, or -1.
+      auto first_at = [&](int tile) {
+        return (((long long)tile + (lane >> 3)) * kBlockN + 16 * group) & ~(long long)page_mask;
+      };
       auto pages_at = [&](int tile) {
-        const long long pos = (((long long)tile + (lane >> 3)) * kBlockN + 16 * group) & ~(long long)page_mask;
-        return pos < len ? __ldcg(a.table + (pos >> a.page_shift)) : -1;
+        const long long pos = first_at(tile);
+        return pos < sg.len ? __ldcg(a.table + (size_t)sg.b * a.blocks + (pos >> a.page_shift)) : -1;
       };
       auto checked = [&](int tile, int id) {
-        const long long pos = (((long long)tile + (lane >> 3)) * kBlockN + 16 * group) & ~(long long)page_mask;
-        if (pos < len && (id < 0 || id >= a.P)) {
+        if (first_at(tile) < sg.len && (id < 0 || id >= a.P)) {
           set_fail(ATTN_ERR_INVALID_ARG);
           return -1;
         }
@@ -361,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             // The slot's last tile, kHeads before, has been through the softmax: the ring's place was free, so the
             // products S of the tile that many tiles and stages ago are complete.
             Head& hd = heads[g % C::kHeads];
-            const int seen = id >= 0 ? max(0, min(16, len - ((sg.k0 + e) * kBlockN + 16 * group))) : 0;
+            const int seen = id >= 0 ? max(0, min(16, sg.len - ((sg.k0 + e) * kBlockN + 16 * group))) : 0;
             const bool hidden = __any_sync(0xffffffffu, seen < 16);
             const float k = __shfl_sync(0xffffffffu, ks, lanes + group), v = __shfl_sync(0xffffffffu, vs, lanes + group);
             const float most =
@@ -413,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       int g = 0, items = 0;
       unsigned pc = 0;  // bit t: phase of P_t
       while (ok && sg.next(a)) {
+        if (OWN && sg.nk == 0) continue;
         const bool two = sg.two(a);
         // S_t's columns are free: the P V products issued before read them first.
         ok = warp_wait(&bar_q[0], items & 1) && (one || warp_wait(&bar_q[1], items & 1));
@@ -546,13 +567,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       const bool two = sg.two(a);
       const int first = sg.rb * kUnitRows + (two ? t * kBlockM : 0);  // the tile's first row
       const int have = min(kBlockM, a.rows - first);                  // and how many it has
+      // This thread's row: its sequence, token and head of the group.
+      int b, tok, gg;
+      row_of(a, max(min(first + r, a.rows - 1), 0), b, tok, gg);
+      if (OWN) b = sg.b;
+      const size_t own_row = ((size_t)b * a.n_q + tok) * a.H + sg.h * a.G + gg, own_rows = (size_t)a.B * a.n_q * a.H;
+      if (OWN && sg.nk == 0) {
+        if (r < have) {
+#pragma unroll 4
+          for (int c = 0; c < D / 4; ++c)
+            reinterpret_cast<float4*>(a.own + own_row * D)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          a.own[own_rows * D + own_row] = -INFINITY;
+          a.own[own_rows * (D + 1) + own_row] = 0.f;
+        }
+        continue;
+      }
       // -------------------------------------------------------- Q rows
       // This warp's 32 rows, kLanes lanes a row and kBatch loads of a lane in flight, divided by a power of two
       // and swizzled.  The products that read the rows before are complete: the softmax has had their results,
       // of both halves where they share them.
       if (!one || t == 0) {
-        int b, tok, gg;
-        row_of(a, min(first + r, a.rows - 1), b, tok, gg);  // each lane finds a row
         const unsigned long long mine = reinterpret_cast<unsigned long long>(
             a.q + b * a.q_batch + tok * a.q_token + (long long)(sg.h * a.G + gg) * a.q_head);
         if (one && items > 0) {
@@ -636,10 +670,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           };
           uint32_t s[32];
           tmem_ld32(tS, s);
-          if (hd.hidden) {
+          // Own positions from `shown` on are those of later tokens.
+          const int shown = OWN ? sg.len - a.n_q + tok + 1 - j * kBlockN : kBlockN;
+          if (hd.hidden || (OWN && sg.len - a.n_q + 1 < (j + 1) * kBlockN)) {
             tmem_wait_ld();
             change([&](int i, uint32_t (&s)[16]) {
-              const int seen = hd.seen[i];
+              const int seen = OWN ? min((int)hd.seen[i], shown - 16 * i) : hd.seen[i];
 #pragma unroll
               for (int x = 0; x < 16; ++x)
                 if (x >= seen) s[x] = __float_as_uint(-INFINITY);
@@ -776,8 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       ++oc;
       tc_fence_after();
       if (!idle) {
-        float* part = a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D);
-        const int pr = t * kBlockM + r;  // row within the part
+        // Columns c of a row are `step` floats apart by fours; the maximum and the sum `rows` apart.
+        float* part = OWN ? a.own + own_row * D
+                          : a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D) +
+                                (t * kBlockM + r) * 4;
+        constexpr int step = OWN ? 4 : kUnitRows * 4;
+        float* sums = OWN ? a.own + own_rows * D + own_row
+                          : a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D) +
+                                D * kUnitRows + t * kBlockM + r;
+        const size_t rows = OWN ? own_rows : kUnitRows;
         const float inv = inverse(l_run), down = W == -INFINITY ? 0.f : ex2(W - m_ref);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -791,12 +834,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)  // columns in the codes' order
-            *reinterpret_cast<float4*>(part + ((size_t)(c * 8 + i) * kUnitRows + pr) * 4) =
-                make_float4(__uint_as_float(o[4 * i]) * inv * down, __uint_as_float(o[4 * i + 2]) * inv * down,
-                            __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
+            if (!OWN || r < have)
+              *reinterpret_cast<float4*>(part + (c * 8 + i) * step) =
+                  make_float4(__uint_as_float(o[4 * i]) * inv * down, __uint_as_float(o[4 * i + 2]) * inv * down,
+                              __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
         }
-        part[D * kUnitRows + pr] = m_ref;
-        part[(D + 1) * kUnitRows + pr] = l_run;
+        if (!OWN || r < have) {
+          sums[0] = m_ref;
+          sums[rows] = l_run;
+        }
       }
       // O_t has been read: the next segment's first P V, which overwrites it, waits for these warps' next P.
       tc_fence_before();
@@ -812,21 +858,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   }
 }
 
-// Joins the parts of 32 rows of a unit and their own part, 4 columns a warp; a lane has a row.  First every
-// warp takes some of the parts' maxima and sums, then all of them its columns, whose loads wait for nothing
-// else.  The order of the sums is that of the runs.
+// Joins the parts of 32 rows of a unit and their own part, 4 columns a warp and turn; a lane has a row.  First every
+// warp takes some of the parts' maxima and sums, then all of them their columns, whose loads wait for nothing
+// else.  SPLIT warps share the parts of the same columns where there are many of them.  A CTA takes all columns in
+// turns where there are enough rows to fill the SMs (then gridDim.x is one for each 32 rows).  The order of the
+// sums is that of the runs.
 constexpr int kJoinRows = 32, kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 constexpr int kJoinBatch = 8;    // parts whose loads a thread has in flight together
 constexpr int kJoinShares = 64;  // parts whose shares of the rows are held
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a) {
+template <int D, int SPLIT>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a, int turns) {
   __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32], s_share[kJoinShares][32];
-  constexpr int kQuads = D / 4 / kJoinWarps;
+  __shared__ float4 s_o[SPLIT > 1 ? kJoinWarps : 1][32];
+  constexpr int kQuads = kJoinWarps / SPLIT;      // of columns at a time
+  constexpr int kTurns = D / 4 / kQuads;
   griddep_launch_dependents();
   griddep_wait();
-  unsigned x = blockIdx.x;
-  const int quad = x % kQuads * kJoinWarps, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  x /= kQuads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % SPLIT;
+  const int per = kTurns / turns;  // CTAs for the same rows
+  int turn = blockIdx.x % per * turns;
+  const unsigned x = blockIdx.x / per;
   const int rows0 = x % (kUnitRows / kJoinRows) * kJoinRows, unit = x / (kUnitRows / kJoinRows);
   const int h = unit / a.row_blocks, rb = unit - h * a.row_blocks;
   if (rb * kUnitRows + rows0 >= a.rows) return;
@@ -837,9 +888,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a)
   row_of(a, row, b, tok, gg);
   const size_t out = ((size_t)b * a.n_q + tok) * a.H + h * a.G + gg;
   const size_t all = (size_t)a.B * a.n_q * a.H;
-  const int col = (quad + warp) * 4;
   const float own_m = __ldcg(a.own + all * D + out), own_l = __ldcg(a.own + all * (D + 1) + out);
-  const float4 own_o = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col));
   // The runs that the unit's tiles are in.  (Runs without a tile begin where the tiles end.)
   const int from = unit * tiles, to = from + tiles;
   const int c0 = __syncthreads_count(begin <= from) - 1, c1 = __syncthreads_count(begin < to) - 1;
@@ -847,12 +896,11 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a)
   const int halves = a.rows - rb * kUnitRows > kBlockM ? 1 : 2;
   const int n = tiles == 0 ? 0 : (c1 - c0 + 1) * halves;
   const float* parts = a.parts + (size_t)(c0 + unit) * part_floats(D);
-  auto part = [&](int i) { return halves == 1 ? parts + i * part_floats(D) + r
-                                              : parts + (i >> 1) * part_floats(D) + (r + (i & 1) * kBlockM); };
-  auto load4 = [&](int i) {
-    const float* p = halves == 1 ? parts + i * part_floats(D) : parts + (i >> 1) * part_floats(D);
-    return __ldcg(reinterpret_cast<const float4*>(p) + (col / 4) * kUnitRows + r + (halves == 1 ? 0 : (i & 1) * kBlockM));
-  };
+  // Part i, and the row's place in it.
+  auto part = [&](int i) { return parts + (halves == 1 ? i : i >> 1) * part_floats(D); };
+  auto place = [&](int i) { return halves == 1 ? r : r + (i & 1) * kBlockM; };
+  auto max_of = [&](int i) { return __ldcg(part(i) + D * kUnitRows + place(i)); };
+  auto sum_of = [&](int i) { return __ldcg(part(i) + (D + 1) * kUnitRows + place(i)); };
 
   float M = warp == 0 ? own_m : -INFINITY, L = warp == 0 ? own_l : 0.f;
   for (int i0 = warp; i0 < n; i0 += kJoinBatch * kJoinWarps) {
@@ -860,8 +908,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a)
 #pragma unroll
     for (int k = 0; k < kJoinBatch; ++k) {
       const int i = i0 + k * kJoinWarps;
-      m[k] = i < n ? __ldcg(part(i) + D * kUnitRows) : -INFINITY;
-      l[k] = i < n ? __ldcg(part(i) + (D + 1) * kUnitRows) : 0.f;
+      m[k] = i < n ? max_of(i) : -INFINITY;
+      l[k] = i < n ? sum_of(i) : 0.f;
     }
     float m_new = M;
 #pragma unroll
@@ -884,34 +932,66 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a)
   for (int w = 0; w < kJoinWarps; ++w) L += s_l[w][lane] * ex2(s_m[w][lane] - m_use);
   // Values times 1 / L, then times their weight: the two factors' product could fall below FP32's range
   // where a small weight meets large values.
-  const float inv = inverse(L);
+  const float inv = inverse(L), own_share = own_l * ex2(own_m - m_use);
   auto add = [&](float4& o, const float4& v, float l) {
     o.x += v.x * inv * l, o.y += v.y * inv * l, o.z += v.z * inv * l, o.w += v.w * inv * l;
   };
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  add(o, own_o, own_l * ex2(own_m - m_use));
-  for (int i0 = 0; i0 < n; i0 += kJoinShares) {
-    const int some = min(kJoinShares, n - i0);
-    if (i0 > 0) __syncthreads();
-    for (int i = warp; i < some; i += kJoinWarps)
-      s_share[i][lane] = __ldcg(part(i0 + i) + (D + 1) * kUnitRows) * ex2(__ldcg(part(i0 + i) + D * kUnitRows) - m_use);
-    float4 y[kJoinBatch];
-    auto fetch = [&](int i) {
-#pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) y[k] = i + k < some ? load4(i0 + i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    fetch(0);
+  auto shares = [&](int i0, int some) {
+    for (int i = warp; i < some; i += kJoinWarps) s_share[i][lane] = sum_of(i0 + i) * ex2(max_of(i0 + i) - m_use);
+  };
+  const bool few = n <= kJoinShares;
+  if (few) {
+    shares(0, n);
     __syncthreads();
-    for (int i = 0; i < some; i += kJoinBatch) {
-      if (i > 0) fetch(i);
+  }
+  for (int k = 0; k < turns; ++k, ++turn) {
+    const int col = (turn * kQuads + warp / SPLIT) * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (share == 0) add(o, __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col)), own_share);
+    for (int i0 = 0; i0 < n; i0 += kJoinShares) {
+      const int some = min(kJoinShares, n - i0);
+      if (!few) {
+        __syncthreads();
+        shares(i0, some);
+        __syncthreads();
+      }
+      for (int i = share; i < some; i += kJoinBatch * SPLIT) {
+        float4 y[kJoinBatch];
 #pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k)
-        if (i + k < some) add(o, y[k], s_share[i + k][lane]);
+        for (int z = 0; z < kJoinBatch; ++z)
+          if (i + z * SPLIT < some)
+            y[z] = __ldcg(reinterpret_cast<const float4*>(part(i0 + i + z * SPLIT)) + (col / 4) * kUnitRows +
+                          place(i0 + i + z * SPLIT));
+#pragma unroll
+        for (int z = 0; z < kJoinBatch; ++z)
+          if (i + z * SPLIT < some) add(o, y[z], s_share[i + z * SPLIT][lane]);
+      }
+    }
+    if constexpr (SPLIT > 1) {
+      if (k > 0) __syncthreads();
+      s_o[warp][lane] = o;
+      __syncthreads();
+      if (share > 0) continue;
+#pragma unroll
+      for (int w = 1; w < SPLIT; ++w) {
+        const float4 y = s_o[warp + w][lane];
+        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+      }
+    }
+    if (rb * kUnitRows + r < a.rows) {
+      *reinterpret_cast<uint2*>(a.o + out * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+      if (col == 0) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     }
   }
-  if (rb * kUnitRows + r >= a.rows) return;
-  *reinterpret_cast<uint2*>(a.o + out * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-  if (col == 0) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+}
+
+template <int D>
+cudaError_t launch_join(const Args& a, cudaStream_t stream) {
+  const unsigned units = (unsigned)(a.Hkv * a.row_blocks), groups = units * (kUnitRows / kJoinRows);
+  if (units * (a.rows <= kBlockM ? 16 : 32) <= (unsigned)a.runs)  // 32 parts a unit and more
+    return launch_pdl(shared_join_kernel<D, 4>, dim3(groups * (D / 8)), dim3(kJoinThreads), 0, stream, a, 1);
+  const int all = D / 4 / kJoinWarps, turns = groups >= 4u * a.runs ? all : 1;
+  return launch_pdl(shared_join_kernel<D, 1>, dim3(groups * (all / turns)), dim3(kJoinThreads), 0, stream, a, turns);
 }
 
 // Runs that the prefix's tiles are dealt in: one CTA an SM.  (The full device's count where
@@ -935,15 +1015,28 @@ Layout layout(const PagedCache& c, int n_q, int H) {
   return w;
 }
 
-template <int D, int GROUP>
-cudaError_t launch_prefix(const Args& a, cudaStream_t stream) {
+template <int D, int GROUP, bool OWN>
+cudaError_t launch_prefix(const Args& a, unsigned grid, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kernel = shared_prefix_kernel<D, GROUP>;
+  auto kernel = shared_prefix_kernel<D, GROUP, OWN>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
-  return launch_pdl(kernel, dim3(a.runs), dim3(kThreads), C::kSmemBytes, stream, a);
+  return launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, a);
 }
+
+template <bool OWN>
+cudaError_t launch_prefix(const Args& a, int d, int page, unsigned grid, cudaStream_t stream) {
+  if (d == 128)
+    return page >= 32 ? launch_prefix<128, 32, OWN>(a, grid, stream) : launch_prefix<128, 16, OWN>(a, grid, stream);
+  return page >= 32 ? launch_prefix<64, 32, OWN>(a, grid, stream) : launch_prefix<64, 16, OWN>(a, grid, stream);
+}
+
+// Rows of a sequence and key head from which on its own positions are this file's kernel's as well, where there are
+// enough units to fill the SMs: attn_decode_int8's goes over the positions for every 32 rows, but splits long ones.
+// (32 sequences of 300 to 1000 positions, 8 key heads of 128, in all with a prefix of 128: 36 rows 74.5 us and
+// 74.4 so, 64 rows 86 and 76, 256 rows 201 and 112; 4 sequences of 4000 positions, 4 key heads, 128 rows 64 and 77.)
+constexpr int kOwnRows = 64;
 
 }  // namespace
 
@@ -969,20 +1062,20 @@ cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const 
   char* ws = static_cast<char*>(workspace);
   a.starts = reinterpret_cast<int*>(ws + w.starts);
   a.parts = reinterpret_cast<float*>(ws + w.parts);
-  a.own = reinterpret_cast<const float*>(ws);
+  a.own = reinterpret_cast<float*>(ws);
   a.o = static_cast<uint16_t*>(o), a.lse = lse;
-  cudaError_t err = cudaErrorInvalidValue;
-  if (c.d == 128)
-    err = c.page >= 32 ? launch_prefix<128, 32>(a, stream) : launch_prefix<128, 16>(a, stream);
+  cudaError_t err = launch_prefix<false>(a, c.d, c.page, a.runs, stream);
+  if (err != cudaSuccess) return err;
+  Args own = a;
+  own.table = c.table, own.len = lens, own.blocks = c.max_blocks;
+  own.rows = n_q * a.G;
+  own.row_blocks = (own.rows - 1) / kUnitRows + 1;
+  if (own.rows >= kOwnRows && (long long)c.B * c.Hkv * own.row_blocks >= a.runs)
+    err = launch_prefix<true>(own, c.d, c.page, a.runs, stream);
   else
-    err = c.page >= 32 ? launch_prefix<64, 32>(a, stream) : launch_prefix<64, 16>(a, stream);
+    err = launch_decode_int8(c, q, strides, lens, nullptr, nullptr, n_q, H, scale, ws + w.decode, stream, a.own);
   if (err != cudaSuccess) return err;
-  err = launch_decode_int8(c, q, strides, lens, nullptr, nullptr, n_q, H, scale, ws + w.decode, stream,
-                           reinterpret_cast<float*>(ws));
-  if (err != cudaSuccess) return err;
-  const unsigned blocks = (unsigned)(a.Hkv * a.row_blocks) * (kUnitRows / kJoinRows) * (c.d / 4 / kJoinWarps);
-  auto join = c.d == 128 ? shared_join_kernel<128> : shared_join_kernel<64>;
-  return launch_pdl(join, dim3(blocks), dim3(kJoinThreads), 0, stream, a);
+  return c.d == 128 ? launch_join<128>(a, stream) : launch_join<64>(a, stream);
 }
 
 cudaError_t status_word_shared(void** word) { return cudaGetSymbolAddress(word, g_status_shared); }
