@@ -254,7 +254,7 @@ size_t attn_decode_shared_int8_workspace_bytes(int B, int n_q, int H, int H_kv, 
                                                int prefix_blocks, int max_blocks) {
   if (check_shared(B, n_q, H, H_kv, d, page_size, prefix_blocks, max_blocks) != ATTN_OK) return 0;
   PagedCache c = {nullptr, nullptr, nullptr, nullptr, nullptr, B, H_kv, d, 1, page_size, max_blocks};
-  return decode_shared_workspace_bytes(c, n_q, H);
+  return decode_shared_workspace_bytes(c, n_q, H, prefix_blocks);
 }
 
 attn_status attn_decode_shared_int8(const void* q, long long q_batch_stride, long long q_token_stride,
@@ -279,10 +279,12 @@ attn_status attn_decode_shared_int8(const void* q, long long q_batch_stride, lon
   ATTN_CHECK(ptr(seqlens, "seqlens", 4));
   ATTN_CHECK(ptr(o, "o"));
   ATTN_CHECK(ptr(lse, "lse", 4));
-  const size_t need = decode_shared_workspace_bytes(c, n_q, H);
-  if (workspace_bytes < need)
-    return fail(ATTN_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
-  ATTN_CHECK(ptr(workspace, "workspace", 256));
+  const size_t need = decode_shared_workspace_bytes(c, n_q, H, prefix_blocks);
+  if (need > 0) {
+    if (workspace_bytes < need)
+      return fail(ATTN_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    ATTN_CHECK(ptr(workspace, "workspace", 256));
+  }
   if (encode_tiled_fn() == nullptr)
     return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
   const long long strides[3] = {q_batch_stride, q_token_stride, q_head_stride};

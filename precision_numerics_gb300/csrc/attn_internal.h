@@ -149,8 +149,14 @@ size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H);
 cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides,
                                const int* lens, void* o, float* lse, int n_q, int H, float scale,
                                void* workspace, cudaStream_t stream, float* whole = nullptr);
-// The same over a prefix that all sequences share and each one's own positions (c.table, lens).
-size_t decode_shared_workspace_bytes(const PagedCache& c, int n_q, int H);
+// The same with the pages of a prefix ahead of every sequence's own (pre_blocks >= 1), read once a sequence.
+size_t decode_prefix_workspace_bytes(const PagedCache& c, int n_q, int H, int pre_blocks);
+cudaError_t launch_decode_prefix_int8(const PagedCache& c, const void* q, const long long* strides,
+                                      const int* pre_table, int pre_blocks, const int* pre_len, const int* lens,
+                                      void* o, float* lse, int n_q, int H, float scale, void* workspace,
+                                      cudaStream_t stream);
+// Over a prefix that all sequences share, read once for many of them, and each one's own positions (c.table, lens).
+size_t decode_shared_workspace_bytes(const PagedCache& c, int n_q, int H, int prefix_blocks);
 cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const long long* strides,
                                       const int* prefix_table, int prefix_blocks, const int* prefix_len,
                                       const int* lens, void* o, float* lse, int n_q, int H, float scale,

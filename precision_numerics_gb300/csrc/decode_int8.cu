@@ -261,7 +261,18 @@ struct Args {
   // rows, for a caller that joins them with others.
   float* whole;
   size_t whole_rows;
+  // With a prefix that all sequences begin with (PRE): its pages, its length, and their number.
+  const int *pre_table, *pre_len;
+  int pre_blocks;
 };
+
+// The prefix as the sequences have it (PRE): `len` positions, then none up to a whole tile, from where on a
+// sequence's own are counted.
+struct Prefix {
+  int len, end;
+};
+template <bool PRE>
+__device__ __forceinline__ Prefix prefix_of(const Args& a);
 
 // A part in the workspace: O [rows][D] divided by l, m [rows], l [rows], FP32.
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
@@ -305,6 +316,16 @@ __device__ __forceinline__ int checked(const Args& a, int len) {
   return len;
 }
 
+template <bool PRE>
+__device__ __forceinline__ Prefix prefix_of(const Args& a) {
+  if constexpr (!PRE) return Prefix{0, 0};
+  const int len = __ldcg(a.pre_len);
+  const long long cap = (long long)a.pre_blocks << a.page_shift;
+  const int cut = len < 0 ? 0 : (int)min((long long)len, cap);
+  if (cut != len) set_fail(ATTN_ERR_INVALID_ARG);
+  return Prefix{cut, (cut + kTile - 1) / kTile * kTile};
+}
+
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + kTile - 1) / kTile); }
 
 // Cost of a segment: kSegmentCost, then one per tile.
@@ -313,6 +334,7 @@ __device__ __forceinline__ int cost_of(int len) { return len > 0 ? tiles_of(len)
 // A position in a CTA's run: tiles [ta, tb) of (sequence b, key head h, row block
 // rb), cost `left` behind them.
 struct Walk {
+  int before;  // positions of a prefix, which lengths count in
   int b, h, rb, len, ta, tb;
   int len_next;  // of sequence b + 1, read ahead, not yet checked
   long long left;
@@ -334,7 +356,7 @@ struct Walk {
         h = 0;
         do {
           if (++b >= a.B) return false;
-          len = checked(a, len_next);
+          len = before + checked(a, len_next);
           len_next = read_length(a, b + 1);
         } while (len == 0);
       }
@@ -351,8 +373,9 @@ __device__ __forceinline__ long long divide(long long x, int y) {
 
 // Sequences without a position have no tile: their rows are empty.  The CTAs take
 // them by turns; len_first is the unchecked length of sequence blockIdx.x.
-template <int D>
-__device__ __forceinline__ void fill_empty(const Args& a, int len_first) {
+template <int D, bool PRE>
+__device__ __forceinline__ void fill_empty(const Args& a, int len_first, int before) {
+  if (PRE && before > 0) return;
   const int copies = a.Hkv * a.row_blocks;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (checked(a, b == blockIdx.x ? len_first : read_length(a, b)) > 0) continue;
@@ -386,7 +409,7 @@ __device__ __forceinline__ long long scan_before(long long x, long long* s_warp,
   return upto - x;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool PRE>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const Args a) {
@@ -424,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   griddep_wait();
   if (!ok && threadIdx.x == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
+  const Prefix pre = prefix_of<PRE>(a);
   Walk sg;
+  sg.before = pre.end;
   int len_first = 1;
   long long per = 0;  // cost of a run
   if (a.parts == nullptr) {
@@ -433,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.rb = x % a.row_blocks;
     sg.h = (x / a.row_blocks) % a.Hkv;
     sg.b = x / a.row_blocks / a.Hkv;
-    sg.len = checked(a, read_length(a, sg.b));
+    sg.len = pre.end + checked(a, read_length(a, sg.b));
     sg.len_next = 0;
     sg.ta = 0;
     sg.tb = tiles_of(sg.len);
@@ -448,10 +473,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     long long* s_warp = reinterpret_cast<long long*>(s_merge);
     int* s_longest = reinterpret_cast<int*>(s_l);
     const long long copies = (long long)a.Hkv * a.row_blocks;
-    auto len_at = [&](int b) { return checked(a, read_length(a, b)); };
+    // (Threads behind the last sequence have none, of a prefix neither.)
+    auto len_at = [&](int b) { return b < a.B ? pre.end + checked(a, read_length(a, b)) : 0; };
     const int len_mine = read_length(a, threadIdx.x);
     len_first = read_length(a, blockIdx.x);  // for fill_empty, after the first loads are under way
-    int len = checked(a, len_mine);
+    int len = (int)threadIdx.x < a.B ? pre.end + checked(a, len_mine) : 0;
     long long total, sum;
     long long ahead = scan_before(cost_of(len), s_warp, total);
     const long long first = total;
@@ -496,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     __syncthreads();
     if (!a.by_segment && threadIdx.x == 0) a.chains[blockIdx.x] = Chain{0, 0, 0, 0};
     if (st.x < 0) {  // more CTAs than runs
-      fill_empty<D>(a, len_first);
+      fill_empty<D, PRE>(a, len_first, pre.end);
       return;
     }
     sg.b = st.x;
@@ -507,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.len_next = read_length(a, sg.b + 1);
     sg.take(st.w);
     if (sg.tb == sg.ta) {  // the run ends before the segment's first tile
-      fill_empty<D>(a, len_first);
+      fill_empty<D, PRE>(a, len_first, pre.end);
       return;
     }
   }
@@ -528,10 +554,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     id0 = id1 = -1;
     const long long pos = ((long long)lw.ta + warp + (long long)kWarps * (ld_k + lane)) * kTile;
     if (ld_k + lane < ld_n) {
-      const int* row = a.table + (size_t)lw.b * a.max_blocks;
-      const bool second = pos + 16 < lw.len;
-      id0 = __ldcg(row + (pos >> a.page_shift));
-      id1 = second ? __ldcg(row + ((pos + 16) >> a.page_shift)) : -1;
+      const bool in_prefix = PRE && pos < pre.end;
+      const int* row = in_prefix ? a.pre_table : a.table + (size_t)lw.b * a.max_blocks;
+      const long long at = PRE && !in_prefix ? pos - pre.end : pos;
+      const bool second = in_prefix ? pos + 16 < pre.len : pos + 16 < lw.len;
+      id0 = __ldcg(row + (at >> a.page_shift));
+      id1 = second ? __ldcg(row + ((at + 16) >> a.page_shift)) : -1;
       const bool fine0 = id0 >= 0 && id0 < a.P, fine1 = id1 >= 0 && id1 < a.P;
       if (!fine0 || (second && !fine1)) set_fail(ATTN_ERR_INVALID_ARG);
       if (!fine0) id0 = -1;
@@ -568,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       if (a.page >= kTile) {
         mbar_arrive_expect_tx(bar, p0 >= 0 ? C::kStageBytes : 0);
         if (p0 >= 0) {
-          const int in_page = ((lw.ta + warp + kWarps * ld_k) * kTile) & (a.page - 1);
+          const int pos = (lw.ta + warp + kWarps * ld_k) * kTile;
+          const int in_page = (PRE && pos >= pre.end ? pos - pre.end : pos) & (a.page - 1);
           const int row = ((p0 * a.Hkv + lw.h) << a.page_shift) + in_page;
           tma_load_2d(dst, &tmK, bar, 0, row);
           tma_load_2d(dst + C::kHalfBytes, &tmV, bar, 0, row);
@@ -616,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   if (more) look_up();
 #pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) issue();
-  if (a.parts != nullptr) fill_empty<D>(a, len_first);
+  if (a.parts != nullptr) fill_empty<D, PRE>(a, len_first, pre.end);
 
   uint32_t used = 0;
   bool last_segment = false;
@@ -649,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                        pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down));
       if (c == 0) {
         s_f[8 * n + g] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-        s_last[8 * n + g] = have ? sg.len - a.n_q + t : -1;
+        s_last[8 * n + g] = have ? max(sg.len - a.n_q + t, PRE ? pre.end - 1 : -1) : -1;
       }
     }
     __syncthreads();
@@ -724,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
       // Scores in base 2; positions behind a row's last one are hidden.
       const int pos0 = (sg.ta + warp + kWarps * k) * kTile;
-      const bool hide = pos0 + kTile - 1 > sg.len - a.n_q || flags != 3u;
+      const bool hide = pos0 + kTile - 1 > sg.len - a.n_q || flags != 3u ||
+                        (PRE && pos0 < pre.end && pos0 + kTile > pre.len);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -738,7 +768,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if (pos0 + h * 16 + (x >> 1) * 8 + g > my_last(n, x & 1) || !((flags >> h) & 1u)) s[h][n][x] = -INFINITY;
+            {
+              const int pos = pos0 + h * 16 + (x >> 1) * 8 + g;
+              if (pos > my_last(n, x & 1) || !((flags >> h) & 1u) || (PRE && pos >= pre.len && pos < pre.end))
+                s[h][n][x] = -INFINITY;
+            }
         // A half that was not loaded has no weights: any scale will do.
         if (!(flags & 1u)) vsc[0] = flags != 0u ? vsc[1] : 0.f;
         if (!(flags & 2u)) vsc[1] = vsc[0];
@@ -1114,11 +1148,11 @@ bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool PRE>
 cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, unsigned runs,
                         cudaStream_t stream) {
   using C = Cfg<D, NT>;
-  auto kernel = decode_int8_kernel<D, NT>;
+  auto kernel = decode_int8_kernel<D, NT, PRE>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
@@ -1146,7 +1180,7 @@ int row_tiles(int rows) { return ceil_div(rows, 8 * row_passes(rows)); }
 
 // Clusters of `size` CTAs that the device holds at a time (the GPCs' SMs do not divide by
 // every size).
-template <int D, int NT>
+template <int D, int NT, bool PRE>
 int clusters_held(int size) {
   using C = Cfg<D, NT>;
   constexpr int kDevices = 16;
@@ -1155,7 +1189,7 @@ int clusters_held(int size) {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < kDevices && (n = known[dev][size].load(std::memory_order_relaxed)) > 0) return n - 1;
-  auto kernel = decode_int8_kernel<D, NT>;
+  auto kernel = decode_int8_kernel<D, NT, PRE>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)size, 1, 1};
@@ -1174,9 +1208,9 @@ int clusters_held(int size) {
   return n;
 }
 
-int clusters_held(int d, int nt, int size) {
+int clusters_held(int d, int nt, int size, bool pre) {
 #define ATTN_DECODE_CASE(DD, TT) \
-  if (d == DD && nt == TT) return clusters_held<DD, TT>(size);
+  if (d == DD && nt == TT) return pre ? clusters_held<DD, TT, true>(size) : clusters_held<DD, TT, false>(size);
   ATTN_DECODE_CASE(64, 1)
   ATTN_DECODE_CASE(64, 2)
   ATTN_DECODE_CASE(64, 3)
@@ -1196,14 +1230,14 @@ bool splits(const PagedCache& c) { return (long long)c.max_blocks * c.page > (lo
 // key heads of 128: 16.5 -> 13.4 us; one of 2000, 8 heads: 8.4 -> 7.3), the runs use all CTAs
 // and even out ragged lengths.  By the longest sequences that the table has room for: a
 // share against the run if the lengths were half of that.
-int cluster_size(const PagedCache& c, int n_q, int H) {
+int cluster_size(const PagedCache& c, int n_q, int H, bool pre) {
   const int rows = n_q * (H / c.Hkv), nt = row_tiles(rows);
   const long long tiles = (long long)c.max_blocks * c.page / kTile;
   const long long segments = (long long)c.B * c.Hkv * row_passes(rows), runs = decode_runs(c.d, nt);
   if (tiles <= kLoneTiles) return 0;  // (250 positions 5.9 us, 6.5 in clusters; 500 7.8 and 5.9)
   for (long long size = std::min({runs / segments, (long long)kMaxCluster, tiles / 4}); size >= 2; --size) {
     if (tiles / size - tiles * segments / (2 * runs) > kClusterTiles) return 0;
-    if (clusters_held(c.d, nt, (int)size) >= segments) return (int)size;
+    if (clusters_held(c.d, nt, (int)size, pre) >= segments) return (int)size;
   }
   return 0;
 }
@@ -1215,9 +1249,20 @@ size_t decode_workspace_bytes(const PagedCache& c, int n_q, int H) {
   return align256(runs * 2 * part_floats(c.d, 8 * nt) * sizeof(float)) + runs * sizeof(Chain);
 }
 
-cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides, const int* lens,
-                               void* o, float* lse, int n_q, int H, float scale, void* workspace,
-                               cudaStream_t stream, float* whole) {
+namespace {
+
+// The cache as the choice of how to split the work has it: with room for the prefix in every row of the table.
+PagedCache with_prefix(const PagedCache& c, int pre_blocks) {
+  PagedCache room = c;
+  room.max_blocks += pre_blocks;
+  return room;
+}
+
+cudaError_t launch_any(const PagedCache& c, const void* q, const long long* strides, const int* pre_table,
+                       int pre_blocks, const int* pre_len, const int* lens, void* o, float* lse, int n_q, int H,
+                       float scale, void* workspace, cudaStream_t stream, float* whole) {
+  const bool pre = pre_blocks > 0;
+  const PagedCache room = with_prefix(c, pre_blocks);
   Args a;
   a.q = static_cast<const uint16_t*>(q);
   a.q_batch = strides[0];
@@ -1229,6 +1274,7 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   a.lens = lens;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
+  a.pre_table = pre_table, a.pre_len = pre_len, a.pre_blocks = pre_blocks;
   a.whole = whole;
   a.whole_rows = (size_t)c.B * n_q * H;
   a.B = c.B, a.n_q = n_q, a.H = H, a.Hkv = c.Hkv, a.G = H / c.Hkv, a.P = c.P, a.page = c.page;
@@ -1242,8 +1288,8 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   const int nt = row_tiles(n_q * a.G);
   a.by_segment = 0;
   unsigned runs = 0;
-  a.cluster = cluster_size(c, n_q, H);
-  if (a.cluster == 0 && !splits(c)) a.cluster = 1;
+  a.cluster = cluster_size(room, n_q, H, pre);
+  if (a.cluster == 0 && !splits(room)) a.cluster = 1;
   if (a.cluster == 0) {
     runs = decode_runs(c.d, nt);
     a.by_segment = (long long)a.B * a.Hkv * a.row_blocks <= runs;
@@ -1253,8 +1299,10 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   }
   CUtensorMap mk, mv;
   if (!make_tmap_codes(&mk, c.k, c) || !make_tmap_codes(&mv, c.v, c)) return cudaErrorInvalidValue;
-#define ATTN_DECODE_CASE(DD, TT) \
-  if (c.d == DD && nt == TT) return launch_impl<DD, TT>(mk, mv, a, runs, stream);
+#define ATTN_DECODE_CASE(DD, TT)                                                       \
+  if (c.d == DD && nt == TT)                                                            \
+    return pre ? launch_impl<DD, TT, true>(mk, mv, a, runs, stream)                     \
+               : launch_impl<DD, TT, false>(mk, mv, a, runs, stream);
   ATTN_DECODE_CASE(64, 1)
   ATTN_DECODE_CASE(64, 2)
   ATTN_DECODE_CASE(64, 3)
@@ -1265,6 +1313,26 @@ cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long lo
   ATTN_DECODE_CASE(128, 4)
 #undef ATTN_DECODE_CASE
   return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_int8(const PagedCache& c, const void* q, const long long* strides, const int* lens,
+                               void* o, float* lse, int n_q, int H, float scale, void* workspace,
+                               cudaStream_t stream, float* whole) {
+  return launch_any(c, q, strides, nullptr, 0, nullptr, lens, o, lse, n_q, H, scale, workspace, stream, whole);
+}
+
+size_t decode_prefix_workspace_bytes(const PagedCache& c, int n_q, int H, int pre_blocks) {
+  return decode_workspace_bytes(with_prefix(c, pre_blocks), n_q, H);
+}
+
+cudaError_t launch_decode_prefix_int8(const PagedCache& c, const void* q, const long long* strides,
+                                      const int* pre_table, int pre_blocks, const int* pre_len, const int* lens,
+                                      void* o, float* lse, int n_q, int H, float scale, void* workspace,
+                                      cudaStream_t stream) {
+  return launch_any(c, q, strides, pre_table, pre_blocks, pre_len, lens, o, lse, n_q, H, scale, workspace, stream,
+                    nullptr);
 }
 
 cudaError_t status_word_decode(void** word) { return cudaGetSymbolAddress(word, g_status_decode); }

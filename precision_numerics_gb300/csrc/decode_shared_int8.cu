@@ -515,10 +515,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           for (int i = 0; i < kBatch; ++i)
             if (!((loaded >> (((p0 + i) * kRows + row) >> 4)) & 1u)) w[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-        if (p0 + kBatch == kPasses) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_rempty[slot]);
-        }
         if (p0 == 0 && phase >= 0 && !warp_wait(empty, phase & 1)) return false;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -527,6 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           st_shared_v4(at + to1, codes_f16(w[i].z), codes_f16(w[i].z >> 8), codes_f16(w[i].w), codes_f16(w[i].w >> 8));
         }
       }
+      // Only now: what was asked for last has arrived where it has been used.  (An arrival right behind the loads
+      // let copies overwrite codes that were still to be read.)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_rempty[slot]);
       return true;
     };
     uint64_t* bar_full = kv == 0 ? bar_kfull : bar_vfull;  // the empty ones are behind them
@@ -668,19 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             }
             tmem_wait_st();
           };
-          uint32_t s[32];
-          tmem_ld32(tS, s);
           // Own positions from `shown` on are those of later tokens.
           const int shown = OWN ? sg.len - a.n_q + tok + 1 - j * kBlockN : kBlockN;
           if (hd.hidden || (OWN && sg.len - a.n_q + 1 < (j + 1) * kBlockN)) {
-            tmem_wait_ld();
             change([&](int i, uint32_t (&s)[16]) {
               const int seen = OWN ? min((int)hd.seen[i], shown - 16 * i) : hd.seen[i];
 #pragma unroll
               for (int x = 0; x < 16; ++x)
                 if (x >= seen) s[x] = __float_as_uint(-INFINITY);
             });
-            tmem_ld32(tS, s);
           }
           // Factor of the scores of group i of 16 (base 2); not 0, so that hidden ones stay -inf.
           bool rounded = false;  // the row's scores have been multiplied with it
@@ -693,14 +689,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           // From 2^24 on that could take a weight out of FP16: such a row's products are rounded first.
           auto round_large = [&]() {
             const bool large = !rounded && fabsf(minus_m) >= 0x1p24f;
-            tmem_wait_ld();
             change([&](int i, uint32_t (&s)[16]) {
               const float k = large ? factor(i) : 1.f;
 #pragma unroll
               for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * k);
             });
             rounded = rounded || large;
-            tmem_ld32(tS, s);
           };
           if (any_large) round_large();
           bool moves = j == 0, again = j == 0;
@@ -708,7 +702,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           uint32_t pk[64];
           while (true) {
             if (again) {
-              tmem_wait_ld();
               float mt = -INFINITY, mw = -INFINITY;  // largest score and largest log2 of a weight
 #pragma unroll 1
               for (int i = 0; i < 8; ++i) {
@@ -752,10 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                 }
               }
               any_large = __any_sync(0xffffffffu, fabsf(minus_m) >= 0x1p24f);
-              if (any_large)
-                round_large();
-              else
-                tmem_ld32(tS, s);
+              if (any_large) round_large();
             }
             const uint64_t nm2 = f2_pack(minus_m, minus_m);
             uint64_t sums2[4];
@@ -763,7 +753,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             for (int i = 0; i < 4; ++i) sums2[i] = 0ull;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              if (c > 0) tmem_ld32(tS + c * 32, s);
               uint64_t k2[32 / GROUP], v2[32 / GROUP];
 #pragma unroll
               for (int i = 0; i < 32 / GROUP; ++i) {
@@ -772,6 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                 k2[i] = f2_pack(k, k);
                 v2[i] = f2_pack(v, v);
               }
+              // (Nothing may come between the loads and the wait: the compiler takes the registers for loaded, and
+              // could move them.)
+              uint32_t s[32];
+              tmem_ld32(tS + c * 32, s);
               tmem_wait_ld();
               reg_fence(s);
 #pragma unroll
@@ -1001,20 +994,6 @@ int shared_runs() {
   return std::min(sms > 0 ? sms : 152, kJoinThreads);
 }
 
-struct Layout {
-  size_t starts, parts, decode, bytes;  // byte offsets; the own part is at 0
-};
-Layout layout(const PagedCache& c, int n_q, int H) {
-  const size_t all = (size_t)c.B * n_q * H, rows = all / c.Hkv;
-  const size_t units = (size_t)c.Hkv * ((rows + kUnitRows - 1) / kUnitRows);
-  Layout w;
-  w.starts = align256(all * (c.d + 2) * sizeof(float));
-  w.parts = w.starts + align256((shared_runs() + 2) * sizeof(int));
-  w.decode = w.parts + align256((units + shared_runs()) * part_floats(c.d) * sizeof(float));
-  w.bytes = w.decode + decode_workspace_bytes(c, n_q, H);
-  return w;
-}
-
 template <int D, int GROUP, bool OWN>
 cudaError_t launch_prefix(const Args& a, unsigned grid, cudaStream_t stream) {
   using C = Cfg<D>;
@@ -1038,14 +1017,59 @@ cudaError_t launch_prefix(const Args& a, int d, int page, unsigned grid, cudaStr
 // 74.4 so, 64 rows 86 and 76, 256 rows 201 and 112; 4 sequences of 4000 positions, 4 key heads, 128 rows 64 and 77.)
 constexpr int kOwnRows = 64;
 
+struct Layout {
+  size_t starts, parts, decode, bytes;  // byte offsets; the own part is at 0
+};
+Layout layout(const PagedCache& c, int n_q, int H) {
+  const size_t all = (size_t)c.B * n_q * H, rows = all / c.Hkv;
+  const size_t units = (size_t)c.Hkv * ((rows + kUnitRows - 1) / kUnitRows);
+  Layout w;
+  w.starts = align256(all * (c.d + 2) * sizeof(float));
+  w.parts = w.starts + align256((shared_runs() + 2) * sizeof(int));
+  w.decode = w.parts + align256((units + shared_runs()) * part_floats(c.d) * sizeof(float));
+  w.bytes = w.decode + decode_workspace_bytes(c, n_q, H);
+  return w;
+}
+
+// Whether the own positions are this file's kernel's too.
+bool own_by_units(const PagedCache& c, int n_q, int H) {
+  const long long rows = (long long)n_q * (H / c.Hkv);
+  return rows >= kOwnRows && c.B * c.Hkv * ((rows - 1) / kUnitRows + 1) >= shared_runs();
+}
+
+// Whether the prefix is read once a sequence, by attn_decode_int8's kernel in one launch with the own positions,
+// instead of once for 256 rows.  That saves two launches and a join, 14 us, so it is worth it for short
+// prefixes and few sequences.  By the length that the prefix's table has room for, at these costs in ns for
+// 1000 positions and key head: of a pass of up to 8, 16, 24 or 32 rows of a sequence, and of a unit of one row
+// tile and of two.  Measured with 1 to 64 sequences of 1 to 64 rows a key head (us, by sequence and by unit; 8 key
+// heads of 128): 1 x 102400 42 and 69; 2 x 25600 24 and 33; 4 x 25600 36 and 33; 8 x 6400 23.5 and 22.3; 64 x 400 20
+// and 27; 64 x 1600 39 and 33; 16 x 1600 with 20 rows 24 and 31, 16 x 6400 56 and 35.
+bool reads_by_sequence(const PagedCache& c, int n_q, int H, int prefix_blocks) {
+  const long long rows = (long long)n_q * (H / c.Hkv), all = rows * c.B;
+  const double positions = 1e-3 * prefix_blocks * c.page * c.Hkv;
+  if ((long long)(prefix_blocks + (long long)c.max_blocks) * c.page > INT_MAX - 4096 || own_by_units(c, n_q, H)) return false;
+  const double pass[2][4] = {{22, 28, 36, 48}, {31, 40, 53, 69}}, unit[2][2] = {{43, 70}, {55, 90}};
+  const int wide = c.d == 128;
+  const long long passes = (rows + 31) / 32, units = (all - 1) / kUnitRows + 1, last = all - (units - 1) * kUnitRows;
+  const double by_sequence = pass[wide][((rows + passes - 1) / passes - 1) / 8] * passes * c.B;
+  const double by_unit = unit[wide][1] * (units - 1) + unit[wide][last > kBlockM];
+  return (by_sequence - by_unit) * positions < 14000;
+}
+
 }  // namespace
 
-size_t decode_shared_workspace_bytes(const PagedCache& c, int n_q, int H) { return layout(c, n_q, H).bytes; }
+size_t decode_shared_workspace_bytes(const PagedCache& c, int n_q, int H, int prefix_blocks) {
+  if (reads_by_sequence(c, n_q, H, prefix_blocks)) return decode_prefix_workspace_bytes(c, n_q, H, prefix_blocks);
+  return layout(c, n_q, H).bytes;
+}
 
 cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const long long* strides,
                                       const int* prefix_table, int prefix_blocks, const int* prefix_len,
                                       const int* lens, void* o, float* lse, int n_q, int H, float scale,
                                       void* workspace, cudaStream_t stream) {
+  if (reads_by_sequence(c, n_q, H, prefix_blocks))
+    return launch_decode_prefix_int8(c, q, strides, prefix_table, prefix_blocks, prefix_len, lens, o, lse, n_q, H,
+                                     scale, workspace, stream);
   const Layout w = layout(c, n_q, H);
   Args a;
   a.q = static_cast<const uint16_t*>(q);
@@ -1070,7 +1094,7 @@ cudaError_t launch_decode_shared_int8(const PagedCache& c, const void* q, const 
   own.table = c.table, own.len = lens, own.blocks = c.max_blocks;
   own.rows = n_q * a.G;
   own.row_blocks = (own.rows - 1) / kUnitRows + 1;
-  if (own.rows >= kOwnRows && (long long)c.B * c.Hkv * own.row_blocks >= a.runs)
+  if (own_by_units(c, n_q, H))
     err = launch_prefix<true>(own, c.d, c.page, a.runs, stream);
   else
     err = launch_decode_int8(c, q, strides, lens, nullptr, nullptr, n_q, H, scale, ws + w.decode, stream, a.own);

@@ -16,7 +16,14 @@ def make(n0, lens, Hkv, page, d, seed=0, width=None):
     return Cache(pages, Hkv, page, d, tables[1:], seed=seed, width=width), tables[0] or [0]
 
 
-def call(A, q, c, pre, n0, lens, **kw):  # noqa: N803
+# Which kernels read the prefix follows from the room in its table: as wide as it needs (one launch, the prefix read
+# once a sequence, for the small ones here), or so wide that it is read once for 256 rows.
+WIDE = 1 << 23
+WIDTHS = pytest.mark.parametrize("room", [0, WIDE])
+
+
+def call(A, q, c, pre, n0, lens, room=0, **kw):  # noqa: N803
+    pre = pre + [-1] * (room // c.codes[0].shape[2])
     return A.attn_decode_shared_int8(q, *c.gpu[:4], ints(pre), ints([n0]), c.gpu[4], ints(lens), **kw)
 
 
@@ -63,12 +70,13 @@ LENS = [0, 1, 2, 15, 16, 17, 64, 130]
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
 @pytest.mark.parametrize("n0", [0, 1, 127, 128, 129, 1000])
 @pytest.mark.parametrize("heads,n_q", [((2, 2), 1), ((14, 2), 2), ((12, 3), 5), ((64, 1), 1)])
-def test_shared(A, heads, n_q, n0, page, d):
+@WIDTHS
+def test_shared(A, room, heads, n_q, n0, page, d):
     """One row tile and two, full and ragged (8 to 512 rows a key head); sequences with less than n_q positions."""
     H, Hkv = heads
     c, pre = make(n0, LENS, Hkv, page, d)
     q = normal((len(LENS), n_q, H, d), 1)
-    o, lse = call(A, q.cuda(), c, pre, n0, LENS)
+    o, lse = call(A, q.cuda(), c, pre, n0, LENS, room)
     A.attn_check_status()
     check(c, pre, n0, q, LENS, 1 / math.sqrt(d), o, lse)
 
@@ -76,12 +84,13 @@ def test_shared(A, heads, n_q, n0, page, d):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("B,G,n_q", [(1, 1, 1), (1, 1, 127), (1, 1, 128), (1, 1, 129), (1, 1, 255), (1, 1, 256), (3, 1, 86),
                                      (5, 4, 13), (3, 3, 29), (3, 5, 33), (2, 64, 5)])
-def test_rows(A, B, G, n_q, d):
+@WIDTHS
+def test_rows(A, room, B, G, n_q, d):
     """Rows at the tiles' and units' borders: the last unit with one tile behind units with two, and with both."""
     Hkv, page, n0, lens = 2, 32, 700, [n_q + 5 * b for b in range(B)]
     c, pre = make(n0, lens, Hkv, page, d)
     q = normal((B, n_q, Hkv * G, d), 1)
-    o, lse = call(A, q.cuda(), c, pre, n0, lens)
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room)
     A.attn_check_status()
     check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse)
 
@@ -100,23 +109,69 @@ def test_long_prefixes(A, B, H, Hkv, n0, d):
 
 
 @pytest.mark.parametrize("width", [2, 40, 300])
-def test_own_histories(A, width):
+@WIDTHS
+def test_own_histories(A, room, width):
     """The own part in each of its forms (a CTA a segment, clusters, runs), ragged."""
     H, Hkv, d, page, n0 = 8, 2, 128, 32, 500
     lens = [min(n, width * page) for n in (9000, 1, 0, 700, 33, 5000)]
     c, pre = make(n0, lens, Hkv, page, d, width=width)
     q = normal((len(lens), 2, H, d), 1)
-    o, lse = call(A, q.cuda(), c, pre, n0, lens)
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room)
     A.attn_check_status()
     check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse)
 
 
-def test_matches_decode_of_joined_histories(A):
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 64), (128, 32), (128, 128)])
+@pytest.mark.parametrize("B,G,n_q", [(80, 4, 16), (40, 8, 33), (170, 64, 1), (80, 2, 200)])
+@pytest.mark.parametrize("n0", [0, 40, 1000])
+def test_many_new_tokens(A, n0, B, G, n_q, d, page):
+    """64 rows a sequence and key head and more, of many sequences: own positions by units of 256 rows; sequences of
+    fewer positions than new tokens, of none, with a page that is not there and a length out of range."""
+    Hkv = 2 if B < 160 else 1
+    lens = [(n_q + 37 * b) % 400 for b in range(B)]
+    lens[3], lens[4], lens[5] = 0, 1, max(1, n_q - 1)
+    c, pre = make(n0, lens, Hkv, page, d)
+    q = normal((B, n_q, Hkv * G, d), 1)
+    o, lse = call(A, q.cuda(), c, pre, n0, lens)
+    A.attn_check_status()
+    scale = 1 / math.sqrt(d)
+    check(c, pre, n0, q, lens, scale, o, lse, shown=(0, 3, 4, 5, 9, B - 1))
+    again = call(A, q.cuda(), c, pre, n0, lens)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    at = next(b for b in range(10, B) if lens[b] > page)
+    c.gpu[4][at, 0] = c.codes[0].shape[0]
+    wrong = list(lens)
+    wrong[7] = -5
+    o, lse = call(A, q.cuda(), c, pre, n0, wrong)
+    with pytest.raises(A.AttnError, match="out of range"):
+        A.attn_check_status()
+    wrong[7] = 0
+    check(c, pre, n0, q, wrong, scale, o, lse, shown=(0, 7, at - 1))
+    # As if the page's codes were in the prefix's place: only the rest of the sequence is seen.
+    n = lens[at] - page
+    part, part_lse = call(A, q[at:at + 1].cuda(), _Only(c, at), pre, n0, [n])
+    A.attn_check_status()
+    # Both within 2^-8 of a value for its rounding and 2^-11 for the weights'; values are below 127 * 0.021.
+    assert ((o[at].double() - part[0].double()).abs() <= 2.0 ** -7 * part[0].double().abs() + 2.0 ** -10 * 2.7).all()
+    live = ~part_lse[0].isinf() & ~lse[at].isinf()
+    assert (lse[at] - part_lse[0])[live].abs().max() <= 2.0 ** -16 if live.any() else True
+
+
+class _Only:
+    """Sequence b of a cache without its first page."""
+
+    def __init__(self, c, b):
+        self.codes = c.codes
+        self.gpu = (*c.gpu[:4], c.gpu[4][b:b + 1, 1:].contiguous())
+
+
+@WIDTHS
+def test_matches_decode_of_joined_histories(A, room):
     """A prefix that ends with a page: attn_decode_int8 over both parts in one table, within both roundings."""
     H, Hkv, d, page, n0, lens = 8, 2, 64, 16, 320, [5, 40, 100]
     c, pre = make(n0, lens, Hkv, page, d)
     q = normal((3, 1, H, d), 1).cuda()
-    o, lse = call(A, q, c, pre, n0, lens)
+    o, lse = call(A, q, c, pre, n0, lens, room)
     width = 20 + c.gpu[4].shape[1]
     table = ints([(pre + t + [-1] * width)[:width] for t in c.tables])
     o2, lse2 = A.attn_decode_int8(q, *c.gpu[:4], table, ints([n0 + n for n in lens]))
@@ -126,53 +181,55 @@ def test_matches_decode_of_joined_histories(A):
     assert (lse - lse2).abs().max() <= 2.0 ** -17
 
 
-def test_views_bad_pages_and_lengths(A):
+@WIDTHS
+def test_views_bad_pages_and_lengths(A, room):
     """q as a view of a fused projection; a page out of range is not seen, lengths are cut, both are reported."""
     H, Hkv, d, page, n0, lens = 8, 2, 128, 32, 300, [70, 100, 20]
     c, pre = make(n0, lens, Hkv, page, d)
     qkv = normal((3, 2, H + 2 * Hkv, d), 2)
     q = qkv[:, :, :H]
     scale = 1 / math.sqrt(d)
-    o, lse = call(A, qkv.cuda()[:, :, :H], c, pre, n0, lens)
+    o, lse = call(A, qkv.cuda()[:, :, :H], c, pre, n0, lens, room)
     A.attn_check_status()
     check(c, pre, n0, q, lens, scale, o, lse)
     strided = q.transpose(0, 2).contiguous().cuda().transpose(0, 2)
-    again = call(A, strided, c, pre, n0, lens)
+    again = call(A, strided, c, pre, n0, lens, room)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
     A.attn_check_status()
     for wrong in (-1, c.codes[0].shape[0], 2 ** 31 - 1):
         bad = list(pre)
         bad[4] = wrong
-        o, lse = call(A, q.cuda(), c, bad, n0, lens)
-        with pytest.raises(A.AttnError, match="prefix [1-9]"):
+        o, lse = call(A, q.cuda(), c, bad, n0, lens, room)
+        with pytest.raises(A.AttnError, match="out of range"):
             A.attn_check_status()
         # As if that page were not in the prefix.
         check(c, pre[:4] + pre[5:], n0 - page, q, lens, scale, o, lse)
-    o, lse = call(A, q.cuda(), c, pre, 10 ** 6, lens)
-    with pytest.raises(A.AttnError, match="prefix [1-9]"):
+    o, lse = call(A, q.cuda(), c, pre, 10 ** 6, lens, room)
+    with pytest.raises(A.AttnError, match="out of range"):
         A.attn_check_status()
     check(c, pre, len(pre) * page, q, lens, scale, o, lse)
-    o, lse = call(A, q.cuda(), c, pre, -3, lens)
-    with pytest.raises(A.AttnError, match="prefix [1-9]"):
+    o, lse = call(A, q.cuda(), c, pre, -3, lens, room)
+    with pytest.raises(A.AttnError, match="out of range"):
         A.attn_check_status()
     check(c, pre, 0, q, lens, scale, o, lse)
     for wrong in (10 ** 6, -3):
-        o, lse = call(A, q.cuda(), c, pre, n0, [70, 100, wrong])
-        with pytest.raises(A.AttnError, match="decode [1-9]"):
+        o, lse = call(A, q.cuda(), c, pre, n0, [70, 100, wrong], room)
+        with pytest.raises(A.AttnError, match="out of range"):
             A.attn_check_status()
         check(c, pre, n0, q, lens, scale, o, lse, shown=(0, 1))
     A.attn_check_status()
 
 
-def test_nan_rows_reach_no_other(A):
+@WIDTHS
+def test_nan_rows_reach_no_other(A, room):
     H, Hkv, d, page, n0, lens = 16, 2, 64, 16, 400, [30, 7, 12] * 8
     c, pre = make(n0, lens, Hkv, page, d)
     q = normal((len(lens), 1, H, d), 1)
-    good, good_lse = call(A, q.cuda(), c, pre, n0, lens)
+    good, good_lse = call(A, q.cuda(), c, pre, n0, lens, room)
     bad = q.clone()
     bad[5, 0, 3, 7] = torch.nan
     bad[9, 0, 8, 0] = torch.inf
-    o, lse = call(A, bad.cuda(), c, pre, n0, lens)
+    o, lse = call(A, bad.cuda(), c, pre, n0, lens, room)
     A.attn_check_status()
     for b, h in ((5, 3), (9, 8)):
         assert o[b, 0, h].isnan().all() and lse[b, 0, h].isnan()
@@ -186,7 +243,8 @@ SPREAD = [(64, 1, 1), (128, 4, 1), (64, 4, 3), (128, 8, 9)]
 @pytest.mark.parametrize("d,G,n_q", SPREAD)
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("n0", [300, 5000])
-def test_value_scales_of_every_ratio(A, n0, page, d, G, n_q):
+@WIDTHS
+def test_value_scales_of_every_ratio(A, room, n0, page, d, G, n_q):
     """Value scales spread over 2^90 from page to page, one of them 0, and scores over some tens."""
     Hkv, lens = 2, [200, 90, 30]
     c, pre = make(n0, lens, Hkv, page, d)
@@ -195,7 +253,7 @@ def test_value_scales_of_every_ratio(A, n0, page, d, G, n_q):
     c.scales[1][pre[1]] = 0
     c.upload()
     q = normal((len(lens), n_q, Hkv * G, d), 1) * 2
-    o, lse = call(A, q.cuda(), c, pre, n0, lens)
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room)
     A.attn_check_status()
     check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse)
 
@@ -203,7 +261,8 @@ def test_value_scales_of_every_ratio(A, n0, page, d, G, n_q):
 @pytest.mark.parametrize("d,G,n_q", SPREAD)
 @pytest.mark.parametrize("n0", [600, 4000])
 @pytest.mark.parametrize("where", ["prefix", "own"])
-def test_small_weights_of_large_values(A, where, n0, d, G, n_q):
+@WIDTHS
+def test_small_weights_of_large_values(A, room, where, n0, d, G, n_q):
     """The first 128 positions of the prefix, or all own ones, have weights of about 2^-118 of the row's largest and
     value scales 2^140 times the others': O is theirs."""
     Hkv, page, lens = 1, 32, [n_q + 60, n_q + 1]
@@ -218,7 +277,7 @@ def test_small_weights_of_large_values(A, where, n0, d, G, n_q):
     c.upload()
     q = normal((2, n_q, Hkv * G, d), 1)
     q[..., 0] = 592.0  # 100 * 0.002 * 592 = 118.4
-    o, lse = call(A, q.cuda(), c, pre, n0, lens, scale=math.log(2.0))
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room, scale=math.log(2.0))
     A.attn_check_status()
     check(c, pre, n0, q, lens, math.log(2.0), o, lse)
 
@@ -226,7 +285,8 @@ def test_small_weights_of_large_values(A, where, n0, d, G, n_q):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("big", [40, 100])
 @pytest.mark.parametrize("jump", [20.0, 100.0, 150.0])
-def test_maximum_that_leaps(A, jump, big, d):
+@WIDTHS
+def test_maximum_that_leaps(A, room, jump, big, d):
     """The score's maximum leaps where the value scale falls by 2^60 to 2^200, in both halves and tiles."""
     Hkv, page, n0, lens = 1, 32, 2000, [40, 40]
     for G in (2, 80):
@@ -242,7 +302,7 @@ def test_maximum_that_leaps(A, jump, big, d):
         H = G if G <= 64 else 64
         q = normal((2, n_q, Hkv * H, d), 1)
         q[..., 0] = jump
-        o, lse = call(A, q.cuda(), c, pre, n0, lens, scale=math.log(2.0))
+        o, lse = call(A, q.cuda(), c, pre, n0, lens, room, scale=math.log(2.0))
         A.attn_check_status()
         assert o.isfinite().all()
         if jump < 126 or big == 40:  # else weights of p < 2^-126, which count as 0, would matter
@@ -252,7 +312,8 @@ def test_maximum_that_leaps(A, jump, big, d):
 @pytest.mark.parametrize("top", [2.0 ** 24 + 2, 2.0 ** 26, 2.0 ** 27 + 512, -(2.0 ** 25) - 100])
 @pytest.mark.parametrize("d,G,n_q", [(64, 1, 1), (128, 4, 5), (64, 64, 3)])
 @pytest.mark.parametrize("n0", [200, 9000])
-def test_scores_beyond_the_exponent(A, n0, d, G, n_q, top):
+@WIDTHS
+def test_scores_beyond_the_exponent(A, room, n0, d, G, n_q, top):
     """The largest score in base 2 is `top`, where FP32 no longer holds whole numbers: one key of the own part and two of
     the prefix have it, far above all others, and the same value row, which is O exactly."""
     page, Hkv, lens = 32, 2, [n_q + 40, n_q]
@@ -268,7 +329,7 @@ def test_scores_beyond_the_exponent(A, n0, d, G, n_q, top):
     c.upload()
     q = torch.zeros((2, n_q, Hkv * G, d), dtype=BF)
     q[..., 0] = 2.0 ** 10
-    o, lse = call(A, q.cuda(), c, pre, n0, lens, scale=math.log(2.0))
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room, scale=math.log(2.0))
     A.attn_check_status()
     want = (row.double() * 0.25).repeat_interleave(G, 0)
     # The weights 1/3 of the parts sum to 1 within 2^-22, which O's rounding to BF16 (the row is a BF16 number) drops.
@@ -278,39 +339,43 @@ def test_scores_beyond_the_exponent(A, n0, d, G, n_q, top):
 
 
 @pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** 90])
-def test_queries_of_extreme_size(A, size):
+@WIDTHS
+def test_queries_of_extreme_size(A, room, size):
     """q and the keys' scales that only their products bring back into range."""
     H, Hkv, d, page, n0, lens = 8, 2, 64, 32, 500, [20, 60]
     c, pre = make(n0, lens, Hkv, page, d)
     c.scales[0] /= size
     c.upload()
     q = normal((2, 1, H, d), 1) * size
-    o, lse = call(A, q.cuda(), c, pre, n0, lens)
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room)
     A.attn_check_status()
     check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse)
 
 
-def test_largest_values(A):
+@WIDTHS
+def test_largest_values(A, room):
     """Values up to 2^127: no sum on the way overflows."""
     H, Hkv, d, page, n0, lens = 8, 2, 128, 32, 3000, [50, 3]
     c, pre = make(n0, lens, Hkv, page, d)
     c.scales[1][:] = 2.0 ** 120
     c.upload()
     q = normal((2, 1, H, d), 1)
-    o, lse = call(A, q.cuda(), c, pre, n0, lens)
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room)
     A.attn_check_status()
     check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse)
 
 
-def test_the_same_call_twice_in_a_graph_and_on_two_streams(A):
+@WIDTHS
+def test_the_same_call_twice_in_a_graph_and_on_two_streams(A, room):
     H, Hkv, d, page, n0 = 16, 2, 128, 64, 4000
     lens = [1 + 61 * b % 200 for b in range(20)]
     c, pre = make(n0, lens, Hkv, page, d)
     q = normal((len(lens), 1, H, d), 1).cuda()
-    first = call(A, q, c, pre, n0, lens)
-    second = call(A, q, c, pre, n0, lens, scale=1 / math.sqrt(d))
+    first = call(A, q, c, pre, n0, lens, room)
+    second = call(A, q, c, pre, n0, lens, room, scale=1 / math.sqrt(d))
     assert all(torch.equal(x, y) for x, y in zip(first, second))
-    args = ints(pre), ints([n0]), c.gpu[4], ints(lens)
+    table = pre + [-1] * (room // page)
+    args = ints(table), ints([n0]), c.gpu[4], ints(lens)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
     for stream in (side, side.cuda_stream):
@@ -326,7 +391,7 @@ def test_the_same_call_twice_in_a_graph_and_on_two_streams(A):
     assert all(torch.equal(x, y) for got in outs for x, y in zip(first, got))
     # Captured, then replayed on another prefix and other lengths.
     o, lse = torch.zeros_like(first[0]), torch.zeros_like(first[1])
-    ws = torch.empty(A.attn_decode_shared_int8_workspace_bytes(20, 1, H, Hkv, d, page, len(pre), c.gpu[4].shape[1]),
+    ws = torch.empty(1 + A.attn_decode_shared_int8_workspace_bytes(20, 1, H, Hkv, d, page, len(table), c.gpu[4].shape[1]),
                      dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -342,6 +407,23 @@ def test_the_same_call_twice_in_a_graph_and_on_two_streams(A):
         check(c, pre, n1, q.cpu(), other, 1 / math.sqrt(d), o, lse, shown=(0, 3, 19))
 
 
+@pytest.mark.parametrize("d,page", [(128, 128), (128, 16), (64, 64)])
+@pytest.mark.parametrize("B,H,Hkv,n_q,n0,own", [(64, 32, 8, 1, 8000, 1), (64, 32, 8, 1, 8000, 100), (16, 32, 8, 1, 20000, 9),
+                                               (100, 8, 2, 4, 3000, 4), (80, 8, 2, 16, 0, 2000), (80, 8, 2, 16, 0, 300)])
+def test_same_bits_again_and_again(A, B, H, Hkv, n_q, n0, own, d, page):
+    """Nothing that is read is overwritten early: many calls back to back, in both parts and every form of them, give the
+    same bits."""
+    lens = [own + (37 * b) % 100 if own > 200 else own for b in range(B)]
+    c, pre = make(n0, lens, Hkv, page, d)
+    q = normal((B, n_q, H, d), 1).cuda()
+    args = ints(pre + [-1] * (WIDE // page)), ints([n0]), c.gpu[4], ints(lens)
+    first = A.attn_decode_shared_int8(q, *c.gpu[:4], *args)
+    for _ in range(25):
+        again = A.attn_decode_shared_int8(q, *c.gpu[:4], *args)
+        assert all(torch.equal(x, y) for x, y in zip(first, again))
+    A.attn_check_status()
+
+
 def test_refusals(A):
     c, pre = make(40, [5], 2, 16, 64)
     q = normal((1, 1, 4, 64), 0).cuda()
@@ -355,8 +437,8 @@ def test_refusals(A):
     with pytest.raises(A.AttnError, match="prefix_blocks"):
         A.attn_decode_shared_int8(q, *c.gpu[:4], p[:0], n, c.gpu[4], lens)
     with pytest.raises(A.AttnError, match="workspace"):
-        A.attn_decode_shared_int8(q, *c.gpu[:4], p, n, c.gpu[4], lens, workspace=torch.empty(
-            100, dtype=torch.uint8, device="cuda"))
+        A.attn_decode_shared_int8(q, *c.gpu[:4], ints(pre * 2000), n, c.gpu[4], lens, workspace=torch.empty(
+            100, dtype=torch.uint8, device="cuda"))  # a table that wide is split
     with pytest.raises(A.AttnError, match="multiple of H_kv"):
         A.attn_decode_shared_int8(normal((1, 1, 5, 64), 0).cuda(), *c.gpu[:4], p, n, c.gpu[4], lens)
     A.attn_check_status()
@@ -395,7 +477,7 @@ def test_steps_behind_a_prefix(A):
     lens, cu = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B + 1, dtype=torch.int32, device="cuda")
     slots, positions = (torch.zeros(T, dtype=torch.int32, device="cuda") for _ in range(2))
     o, lse = torch.zeros((B, n_q, H, d), dtype=BF, device="cuda"), torch.zeros((B, n_q, H), device="cuda")
-    ws = torch.empty(A.attn_decode_shared_int8_workspace_bytes(B, n_q, H, Hkv, d, page, len(pre), width),
+    ws = torch.empty(1 + A.attn_decode_shared_int8_workspace_bytes(B, n_q, H, Hkv, d, page, len(pre), width),
                      dtype=torch.uint8, device="cuda")
     prefix, prefix_len = ints(pre), ints([n0])
 

@@ -67,9 +67,12 @@ def test_shared_arguments(lib):
     assert _shared(lib, q=None) == BAD
     assert _shared(lib, q=24) == BAD
     assert _shared(lib, B=2**23, n_q=256, H=8) == BAD
-    need = lib.attn_decode_shared_int8_workspace_bytes(2, 1, 8, 2, 64, 16, 5, 4)
-    # The own part's means and sums, and a part of 256 rows for every run and unit at least.
-    assert need >= 2 * 8 * 66 * 4 + 3 * 256 * 66 * 4
+    # A short prefix is read by sequence, without a workspace; 64 sequences behind 2^20 positions need the own part's means
+    # and sums, and a part of 256 rows for every run and unit at least.
+    assert lib.attn_decode_shared_int8_workspace_bytes(2, 1, 8, 2, 64, 16, 5, 4) == 0
+    need = lib.attn_decode_shared_int8_workspace_bytes(64, 1, 8, 2, 64, 16, 2**16, 4)
+    assert need >= 64 * 8 * 66 * 4 + 3 * 256 * 66 * 4
+    assert _shared(lib, B=64, prefix_blocks=2**16, ws_bytes=need - 1) == BAD
     assert lib.attn_decode_shared_int8_workspace_bytes(2, 1, 8, 3, 64, 16, 5, 4) == 0
     assert lib.attn_decode_shared_int8_workspace_bytes(2, 1, 8, 2, 64, 16, 0, 4) == 0
 
