@@ -11,11 +11,12 @@
 // is packed token cu[b] + i, position held + i, row table[b][position / page] * page + position %
 // page of the pool.
 //
-// Nothing is computed but sums, and the bytes are few: what bounds it is the chain of dependent
-// loads (lengths, their sums, table entries, stack, slots).  So one launch does it all: a CTA, or
-// a cluster of them that work in step where there are many pages or tokens; each scans all
-// lengths (1024 at a time) and then takes its share of the pages, found by bisection in the sums.
-// Slots of more tokens than a cluster writes quickly are a second kernel's.
+// Nothing is computed but sums, and the bytes are few: what bounds it is the chain of dependent loads
+// (lengths, table entries, stack, slots) with their barriers.  So one launch does it all: a CTA, or a cluster of
+// them that work in step where there are many pages or tokens.  Each scans all lengths, kThreads at a time, and
+// takes its share of the pages and tokens, which it finds by bisection in the sums.  Tokens take their pages
+// from where the table gets them, not from the table.  Slots of more tokens than a cluster writes quickly are
+// a second kernel's.
 #include <limits.h>
 #include <stdint.h>
 
@@ -30,11 +31,12 @@ static __device__ unsigned int g_status_tables;
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kFew = 256, kThreads = 1024;  // threads of a CTA where up to kFew sequences have few tokens, and else
 constexpr int kMany = 8;             // CTAs of a cluster
-constexpr int kAlone = 4096;         // tokens, or sequences' pages at most, that one CTA handles
+constexpr int kAlone = 8192;         // tokens that one CTA handles
+constexpr int kAlonePages = 65536;   // and the room for pages in the table
 constexpr int kSlotsInside = 65536;  // tokens whose slots the cluster writes
-constexpr int kAtOnce = 4;           // pages a thread moves with their loads in flight together
+constexpr int kAtOnce = 4;           // pages or tokens of a thread with their loads in flight together
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_tables, code); }
 
@@ -71,36 +73,58 @@ struct Move {
   __device__ __forceinline__ int tokens() const { return max(wanted - held, 0); }
 };
 
-// Sum over the CTA's threads before this one; all: over every thread.
-__device__ __forceinline__ long long scan_before(long long x, long long* s_warp, long long& all) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long upto = x;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += y;
-  }
-  __syncthreads();
-  if (lane == 31) s_warp[warp] = upto;
-  __syncthreads();
-  long long w = s_warp[lane];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, w, off);
-    if (lane >= off) w += y;
-  }
-  all = __shfl_sync(0xffffffffu, w, 31);
-  return upto - x + (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
-}
-
-// The last of the kThreads starts that is i or less.
+// The last of the N starts that is i or less.
+template <int N>
 __device__ __forceinline__ int find(const long long* s_start, long long i) {
   int at = 0;
 #pragma unroll
-  for (int step = kThreads / 2; step > 0; step >>= 1)
+  for (int step = N / 2; step > 0; step >>= 1)
     if (s_start[at + step] <= i) at += step;
   return at;
 }
+
+// N sequences from b0 on: where each one's needed and released pages and its new tokens begin, and their ends.
+template <int N>
+struct Chunk {
+  long long need[N + 1], released[N + 1], tokens[N + 1];
+  int held[N], wanted[N];
+  long long warp[3][N / 32];
+
+  __device__ __forceinline__ void scan(const Move& m) {
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    long long x[3] = {m.need(), m.released(), m.tokens()};
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const long long y = __shfl_up_sync(0xffffffffu, x[k], off);
+        if (lane >= off) x[k] += y;
+      }
+    __syncthreads();  // what was here before has been read
+    if (lane == 31)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) warp[k][w] = x[k];
+    __syncthreads();
+    long long before[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      long long y = lane < N / 32 ? warp[k][lane] : 0;
+#pragma unroll
+      for (int off = 1; off < N / 32; off <<= 1) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, off);
+        if (lane >= off) y += z;
+      }
+      before[k] = w > 0 ? __shfl_sync(0xffffffffu, y, w - 1) : 0;
+    }
+    if (tid == 0) need[0] = released[0] = tokens[0] = 0;
+    need[tid + 1] = before[0] + x[0];
+    released[tid + 1] = before[1] + x[1];
+    tokens[tid + 1] = before[2] + x[2];
+    held[tid] = m.held;
+    wanted[tid] = m.wanted;
+    __syncthreads();
+  }
+};
 
 // Slot and position of packed token tok, of sequence b.
 __device__ __forceinline__ int2 slot_of(const Tables& t, int b, int tok) {
@@ -151,72 +175,51 @@ __device__ __forceinline__ void put_slots(const Tables& t, int first, int total,
   }
 }
 
-__global__ void __launch_bounds__(kThreads) cache_reserve_kernel(const Tables t, int slots_inside) {
-  __shared__ long long s_warp[32], s_start[kThreads];
+template <int N>
+__global__ void __launch_bounds__(N) cache_reserve_kernel(const Tables t, int slots_inside) {
+  __shared__ Chunk<N> s;
+  __shared__ long long s_sum[N / 32];
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x;
-  const bool first_cta = blockIdx.x == 0;
-  const unsigned ctas = cluster_size(), threads = ctas * kThreads;
-  const unsigned gtid = blockIdx.x * kThreads + tid;
+  const bool first_cta = blockIdx.x == 0, single = t.B <= N;
+  const unsigned threads = cluster_size() * N, gtid = blockIdx.x * N + tid;
   int n = __ldcg(t.n_free);
-  const Move mine(t, tid, first_cta);  // of the first kThreads sequences
+  const Move mine(t, tid, first_cta);  // of the first N sequences
   if (n < 0 || n > t.P) {
     if (first_cta && tid == 0) set_fail(ATTN_ERR_INVALID_ARG);
     n = min(max(n, 0), t.P);
   }
-  // Released pages, all of them.
-  long long released = 0, sum;
-  for (int b0 = 0; b0 < t.B; b0 += kThreads) {
-    scan_before((b0 == 0 ? mine : Move(t, b0 + tid, false)).released(), s_warp, sum);
-    released += sum;
+  const int up = (1 << t.page_shift) - 1;
+  s.scan(mine);
+  long long released = s.released[N];  // by all sequences
+  if (!single) {
+    long long x = 0;
+    for (int b = tid; b < t.B; b += N) x += Move(t, b, b >= N && first_cta).released();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if ((tid & 31) == 0) s_sum[tid >> 5] = x;
+    __syncthreads();
+    released = 0;
+    for (int w = 0; w < N / 32; ++w) released += s_sum[w];
   }
   const long long full = n + released, top = min(full, (long long)t.P);
   if (full > t.P && first_cta && tid == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
-  // They go on the stack; lengths and offsets.
-  long long before_released = 0, before_need = 0, before_tokens = 0, served = 0;
-  for (int b0 = 0; b0 < t.B; b0 += kThreads) {
-    const Move m = b0 == 0 ? mine : Move(t, b0 + tid, first_cta);
-    const long long need = before_need + scan_before(m.need(), s_warp, sum) + m.need();
-    before_need += sum;
-    const bool fits = m.need() == 0 || need <= top;
-    long long upto = fits ? need : 0;
-    if (m.need() == 0) upto = 0;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) upto = max(upto, __shfl_xor_sync(0xffffffffu, upto, off));
-    __syncthreads();
-    if ((tid & 31) == 0) s_start[tid >> 5] = upto;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) served = max(served, s_start[w]);
-    if (first_cta) {
-      const long long at = before_tokens + scan_before(m.tokens(), s_warp, sum);
-      before_tokens += sum;
-      if (b0 + tid < t.B) {
-        t.lens[b0 + tid] = fits ? m.wanted : m.held;
-        t.cu[b0 + tid] = (int)min(at, (long long)INT_MAX);
-        if (b0 + tid == t.B - 1) {
-          const long long all = at + m.tokens();
-          t.cu[t.B] = (int)min(all, (long long)INT_MAX);
-          if (all > t.T) set_fail(ATTN_ERR_INVALID_ARG);
-        }
-      }
-    }
-    const long long start = scan_before(m.released(), s_warp, sum);
-    __syncthreads();
-    s_start[tid] = start;
-    __syncthreads();
-    for (long long i0 = gtid; i0 < sum; i0 += (long long)threads * kAtOnce) {
+  // Released pages go on the stack, and the pages of all requests that are served are counted.
+  long long before_released = 0, before_need = 0, served = 0;
+  for (int b0 = 0; b0 < t.B; b0 += N) {
+    if (b0 > 0) s.scan(Move(t, b0 + tid, false));
+    for (long long i0 = gtid; i0 < s.released[N]; i0 += (long long)threads * kAtOnce) {
       int* from[kAtOnce];
       int page[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
         const long long i = i0 + (long long)k * threads;
         from[k] = nullptr;
-        if (i < sum) {
-          const int x = find(s_start, i), b = b0 + x;
-          const int keep = (__ldcg(t.wanted + b) + (1 << t.page_shift) - 1) >> t.page_shift;
-          from[k] = t.table + (size_t)b * t.max_blocks + keep + (i - s_start[x]);
+        if (i < s.released[N]) {
+          const int x = find<N>(s.released, i), keep = (s.wanted[x] + up) >> t.page_shift;
+          from[k] = t.table + (size_t)(b0 + x) * t.max_blocks + keep + (i - s.released[x]);
           page[k] = __ldcg(from[k]);
         }
       }
@@ -232,19 +235,45 @@ __global__ void __launch_bounds__(kThreads) cache_reserve_kernel(const Tables t,
         if (to < t.P) t.free_pages[to] = page[k];
       }
     }
-    before_released += sum;
+    // The last end of a request's pages that the stack reaches.
+    if (before_need <= top) {
+      const long long left = top - before_need;
+      served = before_need + (s.need[N] <= left ? s.need[N] : s.need[find<N>(s.need, left)]);
+    }
+    before_released += s.released[N];
+    before_need += s.need[N];
   }
-  cluster_sync();
+  // Every CTA has read the count and the lengths; what was put on the stack is seen.
+  if (threads > N)
+    cluster_sync();
+  else
+    __syncthreads();
 
-  // The pages that are needed.
+  // Lengths and offsets, the pages that are needed, and the tokens' slots.
+  const long long bottom = top - served;  // of those pages
+  auto stack_at = [&](long long i) {
+    const int page = __ldcg(t.free_pages + bottom + i);
+    if (page >= 0 && page < t.P) return page;
+    set_fail(ATTN_ERR_INVALID_ARG);
+    return -1;
+  };
+  if (first_cta && tid == 0) *t.n_free = (int)bottom;
   before_need = 0;
-  for (int b0 = 0; b0 < t.B; b0 += kThreads) {
-    const Move m = b0 == 0 ? mine : Move(t, b0 + tid, false);
-    const long long start = scan_before(m.need(), s_warp, sum);
-    __syncthreads();
-    s_start[tid] = start;
-    __syncthreads();
-    for (long long i0 = gtid; i0 < sum; i0 += (long long)threads * kAtOnce) {
+  long long before_tokens = 0;
+  for (int b0 = 0; b0 < t.B; b0 += N) {
+    if (!single) s.scan(Move(t, b0 + tid, false));
+    auto fits = [&](int x) { return s.need[x + 1] == s.need[x] || before_need + s.need[x + 1] <= served; };
+    if (first_cta && b0 + tid < t.B) {
+      const int b = b0 + tid;
+      t.lens[b] = fits(tid) ? s.wanted[tid] : s.held[tid];
+      t.cu[b] = (int)min(before_tokens + s.tokens[tid], (long long)INT_MAX);
+      if (b == t.B - 1) {
+        const long long all = before_tokens + s.tokens[tid + 1];
+        t.cu[t.B] = (int)min(all, (long long)INT_MAX);
+        if (all > t.T) set_fail(ATTN_ERR_INVALID_ARG);
+      }
+    }
+    for (long long i0 = gtid; i0 < s.need[N]; i0 += (long long)threads * kAtOnce) {
       int* to[kAtOnce];
       int page[kAtOnce];
 #pragma unroll
@@ -252,32 +281,53 @@ __global__ void __launch_bounds__(kThreads) cache_reserve_kernel(const Tables t,
         const long long i = i0 + (long long)k * threads;
         to[k] = nullptr;
         page[k] = -1;
-        if (i < sum) {
-          const int x = find(s_start, i), b = b0 + x;
-          const int have = (__ldcg(t.held + b) + (1 << t.page_shift) - 1) >> t.page_shift;
-          to[k] = t.table + (size_t)b * t.max_blocks + have + (i - s_start[x]);
-          // A request's pages are served if its last one is: those up to `served`.
-          const long long at = before_need + i;
-          if (at < served) {
-            page[k] = __ldcg(t.free_pages + (top - served + at));
-            if (page[k] < 0 || page[k] >= t.P) {
-              set_fail(ATTN_ERR_INVALID_ARG);
-              page[k] = -1;
-            }
-          }
+        if (i < s.need[N]) {
+          const int x = find<N>(s.need, i), have = (s.held[x] + up) >> t.page_shift;
+          to[k] = t.table + (size_t)(b0 + x) * t.max_blocks + have + (i - s.need[x]);
+          if (before_need + i < served) page[k] = stack_at(before_need + i);
         }
       }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
         if (to[k] != nullptr) *to[k] = page[k];
     }
-    before_need += sum;
+    if (slots_inside) {
+      const long long some = min(s.tokens[N], t.T - before_tokens);
+      for (long long i0 = gtid; i0 < some; i0 += (long long)threads * kAtOnce) {
+        int slot[kAtOnce], pos[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const long long i = i0 + (long long)k * threads;
+          slot[k] = pos[k] = -1;
+          if (i >= some) continue;
+          const int x = find<N>(s.tokens, i), have = (s.held[x] + up) >> t.page_shift;
+          pos[k] = s.held[x] + (int)(i - s.tokens[x]);
+          if (!fits(x)) continue;
+          const int j = pos[k] >> t.page_shift;
+          int page;
+          if (j >= have) {
+            page = stack_at(before_need + s.need[x] + (j - have));
+          } else {
+            page = __ldcg(t.table + (size_t)(b0 + x) * t.max_blocks + j);
+            if (page < 0 || page >= t.P) {
+              set_fail(ATTN_ERR_INVALID_ARG);
+              page = -1;
+            }
+          }
+          if (page >= 0) slot[k] = (page << t.page_shift) + (pos[k] & up);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const long long i = i0 + (long long)k * threads;
+          if (i < some) t.slots[before_tokens + i] = slot[k], t.positions[before_tokens + i] = pos[k];
+        }
+      }
+    }
+    before_need += s.need[N];
+    before_tokens += s.tokens[N];
   }
-  if (first_cta && tid == 0) *t.n_free = (int)(top - served);
-  if (!slots_inside) return;
-  cluster_sync();
-  const int total = min(__ldcg(t.cu + t.B), t.T);
-  for (unsigned i = gtid; i < ((unsigned)t.T + 3) / 4; i += threads) put_slots(t, 4 * i, total, 0, t.B - 1);
+  if (slots_inside)
+    for (long long i = before_tokens + gtid; i < t.T; i += threads) t.slots[i] = t.positions[i] = -1;
 }
 
 // Slots of many tokens: a warp takes kPerWarp of them, whose sequences it bounds first.
@@ -304,11 +354,16 @@ __global__ void __launch_bounds__(kSlotThreads) cache_slots_kernel(const Tables 
 }  // namespace
 
 cudaError_t launch_cache_reserve(const Tables& t, cudaStream_t stream) {
-  const bool many = t.T > kAlone || (long long)t.B * t.max_blocks > kAlone;
+  const long long room = (long long)t.B * t.max_blocks;
   const bool inside = t.T <= kSlotsInside;
-  const unsigned ctas = many ? kMany : 1;
-  cudaError_t err =
-      launch_pdl_cluster(cache_reserve_kernel, dim3(ctas), dim3(kThreads), 0, stream, ctas, t, inside ? 1 : 0);
+  cudaError_t err;
+  if (t.B <= kFew && t.T <= kFew * kAtOnce && room <= kAlonePages)
+    err = launch_pdl(cache_reserve_kernel<kFew>, dim3(1), dim3(kFew), 0, stream, t, 1);
+  else {
+    const unsigned ctas = t.T > kAlone || room > kAlonePages ? kMany : 1;
+    err = launch_pdl_cluster(cache_reserve_kernel<kThreads>, dim3(ctas), dim3(kThreads), 0, stream, ctas, t,
+                             inside ? 1 : 0);
+  }
   if (err != cudaSuccess || inside) return err;
   const unsigned blocks = (unsigned)(((long long)t.T + kSlotThreads / 32 * kPerWarp - 1) / (kSlotThreads / 32 * kPerWarp));
   return launch_pdl(cache_slots_kernel, dim3(blocks), dim3(kSlotThreads), 0, stream, t);
