@@ -126,55 +126,6 @@ struct Chunk {
   }
 };
 
-// Slot and position of packed token tok, of sequence b.
-__device__ __forceinline__ int2 slot_of(const Tables& t, int b, int tok) {
-  const int held = __ldcg(t.held + b), pos = tok - __ldcg(t.cu + b) + held;
-  int slot = -1;
-  if (__ldcg(t.lens + b) > held) {  // served
-    const int page = __ldcg(t.table + (size_t)b * t.max_blocks + (pos >> t.page_shift));
-    if (page >= 0 && page < t.P)
-      slot = (page << t.page_shift) + (pos & ((1 << t.page_shift) - 1));
-    else
-      set_fail(ATTN_ERR_INVALID_ARG);
-  }
-  return make_int2(slot, pos);
-}
-// The sequence of packed token tok < cu[B], among [lo, hi].
-__device__ __forceinline__ int sequence_of(const Tables& t, int tok, int lo, int hi) {
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(t.cu + mid + 1) > tok)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo;
-}
-// Four tokens of a lane from `first` on, of sequences [lo, hi].
-__device__ __forceinline__ void put_slots(const Tables& t, int first, int total, int lo, int hi) {
-  int slot[4], pos[4];
-  int b = first < total ? sequence_of(t, first, lo, hi) : 0;
-  int until = first < total ? __ldcg(t.cu + b + 1) : 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    slot[i] = pos[i] = -1;
-    if (first + i < total) {
-      while (first + i >= until) until = __ldcg(t.cu + ++b + 1);
-      const int2 x = slot_of(t, b, first + i);
-      slot[i] = x.x, pos[i] = x.y;
-    }
-  }
-  if (first + 3 < t.T && (reinterpret_cast<uintptr_t>(t.slots) & 15) == 0 &&
-      (reinterpret_cast<uintptr_t>(t.positions) & 15) == 0) {
-    *reinterpret_cast<int4*>(t.slots + first) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-    *reinterpret_cast<int4*>(t.positions + first) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (first + i < t.T) t.slots[first + i] = slot[i], t.positions[first + i] = pos[i];
-  }
-}
-
 template <int N>
 __global__ void __launch_bounds__(N) cache_reserve_kernel(const Tables t, int slots_inside) {
   __shared__ Chunk<N> s;
@@ -330,25 +281,81 @@ __global__ void __launch_bounds__(N) cache_reserve_kernel(const Tables t, int sl
     for (long long i = before_tokens + gtid; i < t.T; i += threads) t.slots[i] = t.positions[i] = -1;
 }
 
-// Slots of many tokens: a warp takes kPerWarp of them, whose sequences it bounds first.
-constexpr int kSlotThreads = 256, kPerWarp = 512;
+// Slots of many tokens, four a thread: a CTA finds the sequences that its tokens belong to, all threads looking at
+// once, and takes their offsets and lengths into shared memory.
+constexpr int kSlotThreads = 256, kPerCta = 4 * kSlotThreads, kHeld = 1024;
 __global__ void __launch_bounds__(kSlotThreads) cache_slots_kernel(const Tables t) {
+  __shared__ int s_cu[kHeld + 1], s_held[kHeld], s_lens[kHeld];
   griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long at = ((long long)blockIdx.x * (kSlotThreads / 32) + warp) * kPerWarp;
-  if (at >= t.T) return;
+  const int tid = threadIdx.x;
+  const long long at = (long long)blockIdx.x * kPerCta;
   const int first = (int)at, total = min(__ldcg(t.cu + t.B), t.T);
-  int lo = 0, hi = t.B - 1;
-  if (first < total) {
-    // Lanes 0 and 1 find the sequences of the first and the last token.
-    const int x = sequence_of(t, lane == 0 ? first : (int)min(at + kPerWarp, (long long)total) - 1, 0, t.B - 1);
-    lo = __shfl_sync(0xffffffffu, x, 0);
-    hi = __shfl_sync(0xffffffffu, x, 1);
+  const int behind = (int)min(at + kPerCta, (long long)total);  // this CTA's tokens of a sequence: [first, behind)
+  int lo = 0, count = 0;
+  if (first < behind) {
+    // The last sequence that begins at or before `tok`.
+    auto sequence_of = [&](int tok) {
+      int from = 0, n = t.B;
+      while (n > 1) {
+        const int step = (n - 1) / kSlotThreads + 1, b = from + tid * step;
+        const int before = __syncthreads_count(tid * step < n && __ldcg(t.cu + b) <= tok);
+        from += (before - 1) * step;
+        n = min(step, n - (before - 1) * step);
+      }
+      return from;
+    };
+    lo = sequence_of(first);
+    count = sequence_of(behind - 1) - lo + 1;
   }
-#pragma unroll 1
-  for (int i = 4 * lane; i < kPerWarp; i += 128)
-    if (at + i < t.T) put_slots(t, first + i, total, lo, hi);
+  const bool held = count <= kHeld;  // else there are many without a token among them
+  if (held) {
+    for (int i = tid; i < count; i += kSlotThreads) {
+      s_cu[i] = __ldcg(t.cu + lo + i);
+      s_held[i] = __ldcg(t.held + lo + i);
+      s_lens[i] = __ldcg(t.lens + lo + i);
+    }
+    if (tid == 0 && count > 0) s_cu[count] = __ldcg(t.cu + lo + count);
+    __syncthreads();
+  }
+  auto cu_at = [&](int i) { return held ? s_cu[i] : __ldcg(t.cu + lo + i); };
+  const int up = (1 << t.page_shift) - 1;
+  const int mine = first + 4 * tid;
+  int slot[4], pos[4], x = 0;
+  if (mine < behind) {
+    int hi = count - 1;
+    while (x < hi) {  // the first that ends behind `mine`
+      const int mid = (x + hi) >> 1;
+      if (cu_at(mid + 1) > mine)
+        hi = mid;
+      else
+        x = mid + 1;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    slot[i] = pos[i] = -1;
+    if (mine + i >= behind) continue;
+    while (cu_at(x + 1) <= mine + i) ++x;
+    const int before = held ? s_held[x] : __ldcg(t.held + lo + x);
+    const int after = held ? s_lens[x] : __ldcg(t.lens + lo + x);
+    pos[i] = mine + i - cu_at(x) + before;
+    if (after <= before) continue;  // not served
+    const int page = __ldcg(t.table + (size_t)(lo + x) * t.max_blocks + (pos[i] >> t.page_shift));
+    if (page >= 0 && page < t.P)
+      slot[i] = (page << t.page_shift) + (pos[i] & up);
+    else
+      set_fail(ATTN_ERR_INVALID_ARG);
+  }
+  const bool aligned = ((reinterpret_cast<uintptr_t>(t.slots) | reinterpret_cast<uintptr_t>(t.positions)) & 15) == 0;
+  if (aligned && at + 4 * tid + 3 < t.T) {
+    *reinterpret_cast<int4*>(t.slots + mine) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    *reinterpret_cast<int4*>(t.positions + mine) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at + 4 * tid + i < t.T) t.slots[mine + i] = slot[i], t.positions[mine + i] = pos[i];
+  }
 }
 
 }  // namespace
@@ -365,7 +372,7 @@ cudaError_t launch_cache_reserve(const Tables& t, cudaStream_t stream) {
                              inside ? 1 : 0);
   }
   if (err != cudaSuccess || inside) return err;
-  const unsigned blocks = (unsigned)(((long long)t.T + kSlotThreads / 32 * kPerWarp - 1) / (kSlotThreads / 32 * kPerWarp));
+  const unsigned blocks = (unsigned)(((long long)t.T + kPerCta - 1) / kPerCta);
   return launch_pdl(cache_slots_kernel, dim3(blocks), dim3(kSlotThreads), 0, stream, t);
 }
 

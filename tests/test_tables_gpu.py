@@ -84,6 +84,18 @@ def test_many_tokens(A, n, T):
     A.attn_check_status()
 
 
+def test_many_sequences_without_tokens(A):
+    """Slots of many tokens where thousands of sequences between them have none."""
+    page, n = 16, 9000
+    held = [3] * n
+    wanted = [3 + (20000 if b in (2, 4100, 8999) else 1 if b % 3000 == 7 else 0) for b in range(n)]
+    T = new_tokens(held, wanted) + 77
+    books = Books(held, page, -(-20003 // page), free=3 * 1260, seed=3)
+    lens = books.step(A, held, wanted, T)[0].tolist()
+    books.step(A, lens, held, 1)
+    A.attn_check_status()
+
+
 @pytest.mark.parametrize("free", [0, 1, 7, 30, 31, 60])
 def test_scarce_pages(A, free):
     """Requests are served in order as long as pages last; what ends in the same step counts in."""
