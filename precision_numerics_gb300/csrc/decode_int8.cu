@@ -76,6 +76,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;   // positions per tile
 constexpr int kWholeTiles = 16;  // sequences up to this long are not split
+constexpr int kWholeMany = 2048;  // positions up to which many sequences are not split for another join
 constexpr int kLeastRun = 4;     // tiles a CTA takes at least: one a warp
 // Parts that the warps of a row's join have in flight together; a segment has hardly more
 // (one sequence of 114589 positions, 1 key head of 64 and 6 rows: 14.8 us; 21.2 in runs of 4
@@ -1289,7 +1290,12 @@ cudaError_t launch_any(const PagedCache& c, const void* q, const long long* stri
   a.by_segment = 0;
   unsigned runs = 0;
   a.cluster = cluster_size(room, n_q, H, pre);
-  if (a.cluster == 0 && !splits(room)) a.cluster = 1;
+  // Whole segments also where a join follows anyway and there are about as many of them as CTAs, not too long
+  // (64 sequences of 20 to 1500 positions, 8 key heads of 128: 20.4 us and a join of 4, 24.4 without it; 48 of 30 to
+  // 800, 12 key heads of 64: 11.3 and 4, 11.5).
+  const bool many = whole != nullptr && 2ll * a.B * a.Hkv * a.row_blocks >= decode_runs(c.d, nt) &&
+                    (long long)c.max_blocks * c.page <= kWholeMany;
+  if (a.cluster == 0 && (many || !splits(room))) a.cluster = 1;
   if (a.cluster == 0) {
     runs = decode_runs(c.d, nt);
     a.by_segment = (long long)a.B * a.Hkv * a.row_blocks <= runs;

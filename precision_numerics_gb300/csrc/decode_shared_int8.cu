@@ -174,8 +174,7 @@ struct Head {
   float ks[8], vs[8];
   float v_most;  // the largest of vs
   uint8_t seen[8];
-  int hidden;       // not all are seen
-  unsigned loaded;  // bit per group that has codes
+  int hidden;  // not all are seen
 };
 
 template <int D>
@@ -188,10 +187,10 @@ struct Cfg {
   // one's Q has no need of its place.
   static constexpr int kRawTiles = D == 128 ? 1 : 4;
   // Key tiles whose scales are held.  Those of tile g are overwritten when the codes of tile g + kHeads -
-  // kRawTiles - 1 have been read from the ring; then S of the tile kStages + 1 before that one is complete, and
+  // kRawTiles - 2 have been read from the ring; then S of the tile kStages + 1 before that one is complete, and
   // the softmax is past the tile two before that.
   static constexpr int kHeads = D == 128 ? 8 : 16;
-  static_assert(kHeads - (kRawTiles + 1) - (kStages + 1) - 2 >= 0, "scales stay until the softmax has used them");
+  static_assert(kHeads - (kRawTiles + 2) - (kStages + 1) - 2 >= 0, "scales stay until the softmax has used them");
   static constexpr int kOffQ = 0;
   static constexpr int kOffRaw = 2 * kTileBytes;
   static constexpr int kOffK = kOffRaw + 2 * kRawTiles * kRawBytes;
@@ -200,9 +199,8 @@ struct Cfg {
   static constexpr int kOffE = kOffHead + kHeads * (int)sizeof(Head);  // int8 [2][128]: exponent of a row's power of two
   static constexpr int kOffBar = (kOffE + 2 * 128 + 15) / 16 * 16;
   static constexpr int kSlots = 2 * (kRawTiles + 1);
-  // raw_full, raw_empty [slots], k_full, k_empty, v_full, v_empty [stages], head [kHeads], q [2],
-  // s_full [2], p_full [2], o_done [2], final
-  static constexpr int kNumBars = 2 * kSlots + 4 * kStages + kHeads + 9;
+  // raw_full, raw_empty [slots], k_full, k_empty, v_full, v_empty [stages], q [2], s_full [2], p_full [2], o_done [2], final
+  static constexpr int kNumBars = 2 * kSlots + 4 * kStages + 9;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
   static_assert(kTileBytes == 2 * kRawBytes, "the place of a Q tile holds a key tile's codes");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
@@ -265,8 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   uint64_t* bar_kempty = bar_kfull + C::kStages;
   uint64_t* bar_vfull = bar_kempty + C::kStages;
   uint64_t* bar_vempty = bar_vfull + C::kStages;
-  uint64_t* bar_head = bar_vempty + C::kStages;
-  uint64_t* bar_q = bar_head + C::kHeads;
+  uint64_t* bar_q = bar_vempty + C::kStages;
   uint64_t* bar_sfull = bar_q + 2;
   uint64_t* bar_pfull = bar_sfull + 2;
   uint64_t* bar_odone = bar_pfull + 2;
@@ -287,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       mbar_init(&bar_vfull[s], kCodeWarps);
       mbar_init(&bar_vempty[s], 1);
     }
-    for (int s = 0; s < C::kHeads; ++s) mbar_init(&bar_head[s], 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar_q[t], 4);
       mbar_init(&bar_sfull[t], 1);
@@ -364,12 +360,36 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             const int lanes = (e - e0) * 8;  // those of the tile
             const int id = __shfl_sync(0xffffffffu, ids, lanes + group);
             const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
-            // K, then V: a copy a page.
+            const int seen = id >= 0 ? max(0, min(16, sg.len - ((sg.k0 + e) * kBlockN + 16 * group))) : 0;
+            const bool hidden = __any_sync(0xffffffffu, seen < 16);
+            const float k = __shfl_sync(0xffffffffu, ks, lanes + group), v = __shfl_sync(0xffffffffu, vs, lanes + group);
+            const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+            // The scales' slot: its last tile, kHeads before, has been through the softmax.  (The ring's place for
+            // the tile before was free, so the products S of the tile that many tiles and stages ago are complete.)
+            // Whoever waits for the codes, or for what follows from them, sees these.
+            Head& hd = heads[g % C::kHeads];
+            if (lane < 8) {
+              hd.ks[group] = k;
+              hd.vs[group] = v;
+              hd.seen[group] = (uint8_t)seen;
+            }
+            if (lane == 0) hd.v_most = most, hd.hidden = hidden;
+            __syncwarp();
+            // K, then V: a copy a page.  Where there is none the ring's bytes are codes as well, of positions that
+            // are hidden.  With two row tiles and a ring of one key tile K's codes are not taken before V's of the
+            // tile before have been: the products want V first, and the two conversions slow each other (6400
+            // rows of 8 key heads over 12000 positions: 229 us, 242 as they come, 1024 over 32768: 105 and 107.5; with
+            // one row tile it is 56 and 54).
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
               if (use > 0) ok = warp_wait(&bar_rempty[slot], (use - 1) & 1);
+              if (x == 1 && !one && lane == 0) mbar_arrive(&bar_rfull[slot - 1]);
               if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&bar_rfull[slot], __popc(loaded) * 16 * D);
+              if (lane == 0) {
+                const uint32_t bytes = __popc(loaded) * 16 * D;
+                if (x == 1 || one) mbar_arrive_expect_tx(&bar_rfull[slot], bytes);
+                else mbar_expect_tx(&bar_rfull[slot], bytes);
+              }
               __syncwarp();
               if (lane < 8 && id >= 0 && ((16 * group) & page_mask) == 0)
                 bulk_load(raw + slot * C::kRawBytes + group * 16 * D,
@@ -378,22 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
               if (++slot == slots) slot = 0, ++use;
             }
             if (!ok) break;
-            // The slot's last tile, kHeads before, has been through the softmax: the ring's place was free, so the
-            // products S of the tile that many tiles and stages ago are complete.
-            Head& hd = heads[g % C::kHeads];
-            const int seen = id >= 0 ? max(0, min(16, sg.len - ((sg.k0 + e) * kBlockN + 16 * group))) : 0;
-            const bool hidden = __any_sync(0xffffffffu, seen < 16);
-            const float k = __shfl_sync(0xffffffffu, ks, lanes + group), v = __shfl_sync(0xffffffffu, vs, lanes + group);
-            const float most =
-                __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-            if (lane < 8) {
-              hd.ks[group] = k;
-              hd.vs[group] = v;
-              hd.seen[group] = (uint8_t)seen;
-            }
-            if (lane == 0) hd.v_most = most, hd.hidden = hidden, hd.loaded = loaded;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_head[g % C::kHeads]);
           }
           ids = ids_next, ids_next = ids_after;
           ks = ks_next, vs = vs_next;
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
     const uint32_t to0 = (unit >> 2) * C::kChunkBytes + sw128_offset(row, (unit & 3) * 2);
     const uint32_t to1 = to0 ^ 16u;  // the odd unit beside it
     // A slot of the ring to the tile at `to`, which is free when `empty` has completed its phase.
-    auto convert = [&](int slot, unsigned round, unsigned loaded, uint32_t to, uint64_t* empty, int phase) {
+    auto convert = [&](int slot, unsigned round, uint32_t to, uint64_t* empty, int phase) {
       if (!warp_wait(&bar_rfull[slot], round & 1)) return false;
       constexpr int kBatch = 4;
 #pragma unroll
@@ -510,11 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                        : "r"(from + slot * C::kRawBytes + (p0 + i) * kRows * D)
                        : "memory");
         }
-        if (loaded != 0xffu) {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (!((loaded >> (((p0 + i) * kRows + row) >> 4)) & 1u)) w[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
         if (p0 == 0 && phase >= 0 && !warp_wait(empty, phase & 1)) return false;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -523,28 +522,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
           st_shared_v4(at + to1, codes_f16(w[i].z), codes_f16(w[i].z >> 8), codes_f16(w[i].w), codes_f16(w[i].w >> 8));
         }
       }
-      // Only now: what was asked for last has arrived where it has been used.  (An arrival right behind the loads
-      // let copies overwrite codes that were still to be read.)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_rempty[slot]);
       return true;
     };
     uint64_t* bar_full = kv == 0 ? bar_kfull : bar_vfull;  // the empty ones are behind them
     const uint32_t tiles = smem_u32(kv == 0 ? sK : sV);
-    int slot = kv, hd = 0, st = 0;  // places in the ring, among the scales and the tiles
-    unsigned round = 0, hd_round = 0, st_round = 0;
+    int slot = kv, st = 0;  // places in the ring and among the tiles
+    unsigned round = 0, st_round = 0;
     while (ok && sg.next(a)) {
       for (int e = 0; e < sg.nk; ++e) {
-        ok = warp_wait(&bar_head[hd], hd_round & 1);
+        ok = convert(slot, round, tiles + st * C::kTileBytes, bar_full + C::kStages + st, (int)st_round - 1);
         if (!ok) break;
-        ok = convert(slot, round, heads[hd].loaded, tiles + st * C::kTileBytes, bar_full + C::kStages + st,
-                     (int)st_round - 1);
-        if (!ok) break;
+        // Only now: what was read from the ring has arrived where it has been used.  (An arrival right behind
+        // the loads let copies overwrite codes that were still to be read.)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_rempty[slot]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_full + st);
         if ((slot += 2) >= slots) slot = kv, ++round;
-        if (++hd == C::kHeads) hd = 0, ++hd_round;
         if (++st == C::kStages) st = 0, ++st_round;
       }
     }
@@ -647,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       float minus_m = 0.f, up = 1.f;  // -m_ref and 2^(m_ref - W), once the row has seen something
       bool any_large = false;         // of the warp's rows' maxima
       for (int j = 0; j < n; ++j) {
-        // (The tile's scales are there as well: the codes' warps waited for them, the products for the codes.)
+        // (The tile's scales are there as well: they were written before the codes were asked for.)
         ok = warp_wait(&bar_sfull[t], (sc + j) & 1);
         const int tile = g + (two ? j : 2 * j + t);
         if (!ok) break;
@@ -858,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
 // sums is that of the runs.
 constexpr int kJoinRows = 32, kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 constexpr int kJoinBatch = 8;    // parts whose loads a thread has in flight together
-constexpr int kJoinShares = 64;  // parts whose shares of the rows are held
+constexpr int kJoinShares = kJoinBatch * kJoinWarps;  // parts whose shares of the rows are held
 template <int D, int SPLIT>
 __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a, int turns) {
   __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32], s_share[kJoinShares][32];
@@ -895,9 +890,25 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
   auto max_of = [&](int i) { return __ldcg(part(i) + D * kUnitRows + place(i)); };
   auto sum_of = [&](int i) { return __ldcg(part(i) + (D + 1) * kUnitRows + place(i)); };
 
+  // The first columns' parts are asked for before anything is waited for.
+  const bool few = n <= kJoinShares;  // (kJoinBatch parts for each of kJoinWarps warps)
+  const int col0 = (turn * kQuads + warp / SPLIT) * 4;
+  auto columns = [&](int i, int col) {
+    return __ldcg(reinterpret_cast<const float4*>(part(i)) + (col / 4) * kUnitRows + place(i));
+  };
+  float4 y[kJoinBatch];
+  auto fetch = [&](int i0, int i, int some, int col) {
+#pragma unroll
+    for (int z = 0; z < kJoinBatch; ++z)
+      if (i + z * SPLIT < some) y[z] = columns(i0 + i + z * SPLIT, col);
+  };
+  fetch(0, share, min(n, kJoinShares), col0);
+  float4 own_o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (share == 0) own_o = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col0));
+
   float M = warp == 0 ? own_m : -INFINITY, L = warp == 0 ? own_l : 0.f;
-  for (int i0 = warp; i0 < n; i0 += kJoinBatch * kJoinWarps) {
-    float m[kJoinBatch], l[kJoinBatch];
+  float m[kJoinBatch], l[kJoinBatch];
+  for (int i0 = warp; i0 < max(n, 1); i0 += kJoinBatch * kJoinWarps) {
 #pragma unroll
     for (int k = 0; k < kJoinBatch; ++k) {
       const int i = i0 + k * kJoinWarps;
@@ -929,32 +940,28 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
   auto add = [&](float4& o, const float4& v, float l) {
     o.x += v.x * inv * l, o.y += v.y * inv * l, o.z += v.z * inv * l, o.w += v.w * inv * l;
   };
-  auto shares = [&](int i0, int some) {
-    for (int i = warp; i < some; i += kJoinWarps) s_share[i][lane] = sum_of(i0 + i) * ex2(max_of(i0 + i) - m_use);
-  };
-  const bool few = n <= kJoinShares;
   if (few) {
-    shares(0, n);
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k)
+      if (warp + k * kJoinWarps < n) s_share[warp + k * kJoinWarps][lane] = l[k] * ex2(m[k] - m_use);
     __syncthreads();
   }
   for (int k = 0; k < turns; ++k, ++turn) {
     const int col = (turn * kQuads + warp / SPLIT) * 4;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (share == 0) add(o, __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col)), own_share);
+    if (share == 0) {
+      if (k > 0) own_o = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col));
+      add(o, own_o, own_share);
+    }
     for (int i0 = 0; i0 < n; i0 += kJoinShares) {
       const int some = min(kJoinShares, n - i0);
       if (!few) {
         __syncthreads();
-        shares(i0, some);
+        for (int i = warp; i < some; i += kJoinWarps) s_share[i][lane] = sum_of(i0 + i) * ex2(max_of(i0 + i) - m_use);
         __syncthreads();
       }
       for (int i = share; i < some; i += kJoinBatch * SPLIT) {
-        float4 y[kJoinBatch];
-#pragma unroll
-        for (int z = 0; z < kJoinBatch; ++z)
-          if (i + z * SPLIT < some)
-            y[z] = __ldcg(reinterpret_cast<const float4*>(part(i0 + i + z * SPLIT)) + (col / 4) * kUnitRows +
-                          place(i0 + i + z * SPLIT));
+        if (k > 0 || i0 > 0 || i > share) fetch(i0, i, some, col);
 #pragma unroll
         for (int z = 0; z < kJoinBatch; ++z)
           if (i + z * SPLIT < some) add(o, y[z], s_share[i + z * SPLIT][lane]);
@@ -967,8 +974,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
       if (share > 0) continue;
 #pragma unroll
       for (int w = 1; w < SPLIT; ++w) {
-        const float4 y = s_o[warp + w][lane];
-        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+        const float4 z = s_o[warp + w][lane];
+        o.x += z.x, o.y += z.y, o.z += z.z, o.w += z.w;
       }
     }
     if (rb * kUnitRows + r < a.rows) {
@@ -981,7 +988,9 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
 template <int D>
 cudaError_t launch_join(const Args& a, cudaStream_t stream) {
   const unsigned units = (unsigned)(a.Hkv * a.row_blocks), groups = units * (kUnitRows / kJoinRows);
-  if (units * (a.rows <= kBlockM ? 16 : 32) <= (unsigned)a.runs)  // 32 parts a unit and more
+  // Four warps share a row's parts where a unit has many: 32 of two tiles of rows, 8 of one, whose tiles make two
+  // parts each (19 parts of 16 rows: 38.1 us in all, 36.6 shared; 19 of 256 rows 53.5 and 56.8).
+  if (units * (a.rows <= kBlockM ? 8 : 32) <= (unsigned)a.runs)
     return launch_pdl(shared_join_kernel<D, 4>, dim3(groups * (D / 8)), dim3(kJoinThreads), 0, stream, a, 1);
   const int all = D / 4 / kJoinWarps, turns = groups >= 4u * a.runs ? all : 1;
   return launch_pdl(shared_join_kernel<D, 1>, dim3(groups * (all / turns)), dim3(kJoinThreads), 0, stream, a, turns);
