@@ -101,7 +101,12 @@ __device__ __forceinline__ int run_begin(const Args& a, int tiles, int c) {
   const int before = tiles * (a.row_blocks - 1);  // tiles of a head before its last unit
   const int last_cost = a.rows - (a.row_blocks - 1) * kUnitRows <= kBlockM ? kCostOne : kCostTwo;
   if (a.row_blocks == 1 || last_cost == kCostTwo) {  // all cost the same
-    const int all = tiles * a.row_blocks * a.Hkv, runs = min(a.runs, max(all / kLeastRun, 1));
+    const int units = a.row_blocks * a.Hkv, all = tiles * units;
+    int runs = min(a.runs, max(all / kLeastRun, 1));
+    // As many for each unit where that makes no run longer by more than a tile: a run that meets two units pays
+    // for their rows' way in and out twice (16 units of 40 tiles 23 us, 19 with 9 runs each).
+    const int each = runs / units;
+    if (each > 0 && (tiles + each - 1) / each <= all / runs + 1) runs = each * units;
     return c >= runs ? all : (int)divide((long long)all * c, runs);
   }
   const long long head_cost = (long long)before * kCostTwo + (long long)tiles * last_cost, all = head_cost * a.Hkv;
