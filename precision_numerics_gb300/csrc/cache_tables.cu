@@ -16,7 +16,13 @@
 // them that work in step where there are many pages or tokens.  Each scans all lengths, kThreads at a time, and
 // takes its share of the pages and tokens, which it finds by bisection in the sums.  Tokens take their pages
 // from where the table gets them, not from the table.  Slots of more tokens than a cluster writes quickly are
-// a second kernel's.
+// a second kernel's (kSlotsInside).
+//
+// Measured, a call among others: 3 sequences of one new token 3.7 us, 256 5.8 (one CTA of 256 threads, for which
+// __syncthreads and the scan's rounds cost half of what they do for 1024: 17 -> 7.9 us for two calls); 64 prompts of
+// 150 to 4096 tokens 5.7 and 4.9 for their slots, 1000 of 10 to 6000 10.5 and 11.7 (1 M tokens, 8 MB).  With the
+// table written first and the tokens' pages read back from it, behind another barrier, these took 35 and 59 us in
+// place of 18 and 32 with the call that takes the step back.
 #include <limits.h>
 #include <stdint.h>
 
@@ -31,11 +37,18 @@ static __device__ unsigned int g_status_tables;
 
 namespace {
 
-constexpr int kFew = 256, kThreads = 1024;  // threads of a CTA where up to kFew sequences have few tokens, and else
-constexpr int kMany = 8;             // CTAs of a cluster
-constexpr int kAlone = 8192;         // tokens that one CTA handles
-constexpr int kAlonePages = 65536;   // and the room for pages in the table
-constexpr int kSlotsInside = 65536;  // tokens whose slots the cluster writes
+// A small CTA for up to kFew sequences with up to kFew * kAtOnce tokens; else one of kThreads, or with more than
+// kAlone tokens a cluster of kMany.  (A step and its reverse, us, 64 sequences: of a token each 6.5, 8.9 with 1024
+// threads; of 16 7.8 and 9.2; of 64 10.5 by one CTA and 8.6 by the cluster, of 256 19.2 and 9.2; 500 sequences of a token
+// 9.5 and 10.1.)
+constexpr int kFew = 256, kThreads = 1024, kMany = 8, kAlone = 1024;
+// The pages that a call gives back are not known here, but the table's room is: a cluster from 16384 on.  (4096 pages
+// taken and given back 18.3 us by the small CTA and 9.6 by the cluster, 16384 59 and 10.8, 65536 222 and 18.9; 200
+// sequences of a token 7.0 and 10.1.)
+constexpr int kAlonePages = 16384;
+// Tokens whose slots the cluster writes; with more of them a second kernel's CTAs do, which find their tokens' sequences
+// in the offsets (32000 tokens 10.9 us inside and 12.0 so, 64000 15.0 and 12.7, 128000 22.4 and 14.3).
+constexpr int kSlotsInside = 40960;
 constexpr int kAtOnce = 4;           // pages or tokens of a thread with their loads in flight together
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_tables, code); }

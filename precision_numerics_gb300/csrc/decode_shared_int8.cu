@@ -7,8 +7,9 @@
 // with codes ck, cv and the scales ks, vs of position j's page and key head.  Prefix and own
 // part are each reduced to (m, l, O / l), m the largest score, l the sum of exp(s - m), and joined as
 //   m = max m_x,   l = sum_x l_x e^(m_x - m),   O = sum_x (l_x e^(m_x - m) / l) (O / l)_x,
-// means with weights of at most 1.  The own part is attn_decode_int8's (decode_int8.cu); this
-// file has the prefix and the join.
+// means with weights of at most 1.  Three launches: the prefix, the own positions, the join.  The own part is
+// attn_decode_int8's kernel (decode_int8.cu), or with many new tokens this file's (own_by_units); a short prefix of
+// few sequences is read once for each of them by attn_decode_int8's kernel, in one launch (reads_by_sequence).
 //
 // The rows of a key head over the prefix are those of all sequences, tokens and heads of
 // the group, R = B n_q G, so the prefix's codes are read once for 256 of them instead of once a
@@ -22,6 +23,14 @@
 //   products (1 warp)  issues them
 //   softmax (8 warps)  a thread for each row of the two tiles (or halves); also their Q rows and the
 //                      results' way out
+// What bounds it (d = 128).  A key tile of two row tiles takes 1.7 us (3450 clocks): the softmax of a row tile, 1850
+// clocks of eight warps that fill the issue slots by turns, the P V and S that follow it, 1280, and 300 until the
+// other side sees that they are done, while the tensor pipe needs 2048 for both row tiles' products, 2560 with their
+// operands from shared memory.  1024 rows of 8 key heads over 32768 positions take 105 us, 1.31 PFLOP/s, 68% of what
+// a library product reaches; 6400 rows over 12000 229 us, 1.37.  With one row tile the halves' chains run beside one
+// another at 1.3 us a key tile: 16 rows of 8 key heads over 100003 positions 54 us, 3.8 TB/s, 56% of the copy rate.
+// Around the tiles are about 10 us: launch, Q and the first tile's chain of loads, the last tile's, the part of a run
+// (133 KB, FP32); 256 rows over 16000 positions are 6.6 tiles a CTA and 21 us.
 // Loads to registers are avoided where much is in flight: shared memory leaves L1 28 KB, and codes that
 // were loaded through it kept the warps that ask for them waiting (a key tile took 3.9 us).
 // The tiles of all (key head, row block) units, one behind the other, are dealt to the CTAs
@@ -851,6 +860,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   }
 }
 
+// What bounds the join is the latency of its two rounds of loads (runs, then parts) and, with many units, the parts'
+// bytes in L2: 152 parts (20 MB) 9.5 us, 351 of 6400 rows a key
+// head (47 MB, and 27 MB of own parts) 34 us.
 // Joins the parts of 32 rows of a unit and their own part, 4 columns a warp and turn; a lane has a row.  First every
 // warp takes some of the parts' maxima and sums, then all of them their columns, whose loads wait for nothing
 // else.  SPLIT warps share the parts of the same columns where there are many of them.  A CTA takes all columns in
