@@ -682,6 +682,8 @@ def attn_cache_reserve(block_table, held, wanted, free_pages, n_free, page_size,
     _check_ints("wanted", wanted, B)
     _check_ints("free_pages", free_pages)
     _check_ints("n_free", n_free, 1)
+    if T < 0:
+        raise ValueError(f"T must be >= 0 (got {T})")
     outs = []
     for name, t, n in (("lens", lens, B), ("cu_seqlens", cu_seqlens, B + 1), ("slots", slots, T),
                        ("positions", positions, T)):

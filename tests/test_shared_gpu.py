@@ -121,6 +121,38 @@ def test_own_histories(A, room, width):
     check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse)
 
 
+@pytest.mark.parametrize("B,Hkv,G,n_q", [(70, 8, 4, 1), (90, 12, 1, 1), (45, 8, 4, 5), (300, 2, 7, 2)])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("longest", [1500, 2100])
+@WIDTHS
+def test_many_ragged_histories(A, room, longest, B, Hkv, G, n_q, d, page):
+    """About as many segments as CTAs, on both sides of the length up to which they are not split."""
+    lens = [longest, 0, 1] + [(b * b * 13) % longest if b % 5 == 0 else (b * 31) % 90 for b in range(B - 3)]
+    c, pre = make(700, lens, Hkv, page, d)
+    q = normal((B, n_q, Hkv * G, d), 1)
+    o, lse = call(A, q.cuda(), c, pre, 700, lens, room)
+    A.attn_check_status()
+    check(c, pre, 700, q, lens, 1 / math.sqrt(d), o, lse, shown=(0, 1, 2, 8, 33, B - 1))
+
+
+def test_without_the_tensor_binding(A, monkeypatch):
+    from precision_numerics_gb300 import attn
+
+    lens = [9, 60]
+    c, pre = make(300, lens, 2, 16, 64)
+    q = normal((2, 1, 8, 64), 1).cuda()
+    want = call(A, q, c, pre, 300, lens, WIDE)
+    monkeypatch.setattr(attn, "_BINDING", attn._NoBinding)
+    got = call(A, q, c, pre, 300, lens, WIDE)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    o, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    call(A, q, c, pre, 300, lens, WIDE, o=o, lse=lse)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(ValueError):
+        call(A, q, c, pre, 300, lens, o=o.cpu())
+    A.attn_check_status()
+
+
 @pytest.mark.parametrize("d,page", [(64, 16), (64, 64), (128, 32), (128, 128)])
 @pytest.mark.parametrize("B,G,n_q", [(80, 4, 16), (40, 8, 33), (170, 64, 1), (80, 2, 200)])
 @pytest.mark.parametrize("n0", [0, 40, 1000])

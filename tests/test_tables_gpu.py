@@ -234,3 +234,74 @@ def test_in_a_graph(A):
         A.attn_check_status()
         held, wanted = want[0], [(x * 7 + 5) % 80 for x in want[0]]
     assert 0 < reported < 4
+
+
+@pytest.mark.parametrize("T", [1023, 1024, 1025, 40959, 40960, 40961])
+def test_tokens_at_the_kernels_borders(A, T):
+    """Around the numbers of tokens from which a cluster, and then a kernel for the slots, is used; some sequences end."""
+    page, n = 32, 6
+    held = [5, 0, 700, 33, 64, 4000]
+    new = [T // 5, 0, T - T // 5 - T // 7, 0, T // 7, 0]
+    wanted = [h + x for h, x in zip(held, new)]
+    wanted[3] = wanted[5] = 0
+    books = Books(held, page, -(-max(held + wanted) // page) + 2, free=-(-T // page) + n, seed=T)
+    start = [list(r) for r in books.table], books.free
+    lens = books.step(A, held, wanted, T)[0].tolist()
+    assert lens == wanted
+    books.step(A, lens, held, new_tokens(lens, held))
+    assert (books.table, books.free) == start
+    A.attn_check_status()
+
+
+@pytest.mark.parametrize("n,width", [(4, 4096), (4, 4097), (300, 55), (1, 16384), (1, 16385)])
+def test_rooms_at_the_kernels_border(A, n, width):
+    """Around the room for pages from which a cluster is used: all of it is taken, then given back."""
+    page = 16
+    held = [7 * b % 40 for b in range(n)]
+    full = [width * page - (b % 16) for b in range(n)]
+    books = Books(held, page, width, free=n * width, seed=n)
+    T = new_tokens(held, full)
+    lens = books.step(A, held, full, T)[0].tolist()
+    books.step(A, lens, [0] * n, 0)
+    books.step(A, [0] * n, [b % 3 for b in range(n)], n)  # few tokens in a wide table
+    A.attn_check_status()
+
+
+def test_two_at_once(A):
+    """Steps of two pools on two streams at the same time."""
+    held, wanted = lengths(700, 300, 5)
+    T = new_tokens(held, wanted)
+    both = [Books(held, 16, 21, free=700 + 50 * i, seed=i) for i in range(2)]
+    wants = [ref.reserve(b.table, held, wanted, b.stack, b.free, 16, T, b.pages) for b in both]
+    args = ints(held), ints(wanted)
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    gots = []
+    for b, s in zip(both, streams):
+        with torch.cuda.stream(s):
+            gots.append(A.attn_cache_reserve(b.gpu[0], *args, *b.gpu[1:], 16, T))
+    torch.cuda.synchronize()
+    for b, got, want in zip(both, gots, wants):
+        assert [g.tolist() for g in got] == list(want[:4])
+        assert b.gpu[0].tolist() == b.table and b.gpu[1].tolist() == b.stack and b.gpu[2].item() == want[4]
+    A.attn_check_status()
+
+
+def test_without_the_tensor_binding(A, monkeypatch):
+    """The call through ctypes, and host memory, which both ways refuse."""
+    from precision_numerics_gb300 import attn
+
+    held, wanted = [20, 5, 0], [50, 0, 17]
+    T = new_tokens(held, wanted)
+    for binding in (attn._BINDING, attn._NoBinding):
+        monkeypatch.setattr(attn, "_BINDING", binding)
+        Books(held, 16, 5, free=9).step(A, held, wanted, T)
+        Books(held, 16, 5, free=9).step(A, held, wanted, T, slots=torch.zeros(T, dtype=torch.int32, device="cuda"))
+        table, stack, free = Books(held, 16, 5, free=9).gpu
+        for args in ((table.cpu(), ints(held), ints(wanted), stack, free), (table, ints(held), ints(wanted), stack.cpu(), free),
+                     (table, ints(held).cpu().pin_memory(), ints(wanted), stack, free)):
+            with pytest.raises(ValueError):
+                A.attn_cache_reserve(*args, 16, T)
+        with pytest.raises(ValueError, match="T must"):
+            A.attn_cache_reserve(table, ints(held), ints(wanted), stack, free, 16, -1)
+    A.attn_check_status()
