@@ -416,7 +416,7 @@ ATTN_API attn_status attn_decode_int8(const void* q, long long q_batch_stride,
                                       float scale, void* workspace, size_t workspace_bytes,
                                       cudaStream_t stream);
 
-/* Bytes of device workspace attn_decode_shared_int8 needs (0 on invalid arguments). */
+/* Bytes of device workspace attn_decode_shared_int8 needs (0 also on invalid arguments). */
 ATTN_API size_t attn_decode_shared_int8_workspace_bytes(int B, int n_q, int H, int H_kv, int d,
                                                         int page_size, int prefix_blocks,
                                                         int max_blocks);
@@ -424,10 +424,14 @@ ATTN_API size_t attn_decode_shared_int8_workspace_bytes(int B, int n_q, int H, i
 /*
  * attn_decode_int8 for a batch whose sequences all begin with the same prefix_len
  * positions, which the cache holds once: token i of a sequence's newest n_q sees the
- * whole prefix and its own positions j <= seqlens[b] - n_q + i.  The prefix's codes
- * are read once for up to 256 of a key head's B * n_q * H / H_kv query rows.
+ * whole prefix and its own positions j <= seqlens[b] - n_q + i.  The prefix's codes are
+ * read once for up to 256 of a key head's B * n_q * H / H_kv query rows, or once a
+ * sequence, in one launch, where the prefix is short or the sequences are few.
  *   prefix_table  : int32 [prefix_blocks], device: the prefix's pages; position t is
- *                   row t % page_size of page prefix_table[t / page_size].
+ *                   row t % page_size of page prefix_table[t / page_size].  How the
+ *                   prefix is read follows from prefix_blocks and the shape: a table far
+ *                   wider than the prefix gives O within the same bounds, but not always the same
+ *                   bits, and a short prefix some microseconds later.
  *   prefix_len    : int32 [1], device: 0 to prefix_blocks * page_size.
  *   block_table   : int32 [B, max_blocks]: the pages of each sequence's own positions,
  *                   which are counted from 0 behind the prefix (the first of them begins a
