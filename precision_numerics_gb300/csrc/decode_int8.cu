@@ -445,7 +445,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     fence_proxy_async_smem();
   }
   __syncwarp();
-  griddep_wait();
+  // Behind the prefix's kernel (whole != nullptr), which let this one in when all before it was complete, and of which
+  // nothing is used here: its end is waited for by the time this one lets the join in, which reads both's parts.
+  const bool behind = !PRE && a.whole != nullptr;
+  if (!behind) griddep_wait();
   if (!ok && threadIdx.x == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
   const Prefix pre = prefix_of<PRE>(a);
@@ -524,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     if (!a.by_segment && threadIdx.x == 0) a.chains[blockIdx.x] = Chain{0, 0, 0, 0};
     if (st.x < 0) {  // more CTAs than runs
       fill_empty<D, PRE>(a, len_first, pre.end);
+      if (behind) griddep_wait();
       return;
     }
     sg.b = st.x;
@@ -535,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.take(st.w);
     if (sg.tb == sg.ta) {  // the run ends before the segment's first tile
       fill_empty<D, PRE>(a, len_first, pre.end);
+      if (behind) griddep_wait();
       return;
     }
   }
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         ld_n = more ? lw.count(warp) : 0;
       } while (more && ld_n == 0);
       if (!more) {
-        griddep_launch_dependents();
+        if (!behind) griddep_launch_dependents();
         return;
       }
       ld_k = 0;
@@ -896,6 +901,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
 
     // ------------------------------------------------------------------ merge
+    if (behind && !more) {
+      griddep_wait();
+      griddep_launch_dependents();
+    }
     // In a cluster the part stays in shared memory, where the rings were.
     const bool whole = sg.ta == 0 && sg.tb == tiles_of(sg.len) && a.cluster <= 1;
     float* part = nullptr;
@@ -1027,6 +1036,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
     cluster_sync();  // nobody leaves while its part is read
   }
+  if (behind) griddep_wait();
   if (!ok) {
     if (lane == 0) set_fail(ATTN_ERR_TIMEOUT);
     // Do not leave while copies into this CTA's shared memory are in flight.
@@ -1290,10 +1300,12 @@ cudaError_t launch_any(const PagedCache& c, const void* q, const long long* stri
   a.by_segment = 0;
   unsigned runs = 0;
   a.cluster = cluster_size(room, n_q, H, pre);
-  // Whole segments also where a join follows anyway and there are about as many of them as CTAs, not too long
-  // (64 sequences of 20 to 1500 positions, 8 key heads of 128: 20.4 us and a join of 4, 24.4 without it; 48 of 30 to
-  // 800, 12 key heads of 64: 11.3 and 4, 11.5).
-  const bool many = whole != nullptr && 2ll * a.B * a.Hkv * a.row_blocks >= decode_runs(c.d, nt) &&
+  // Whole segments also where a join follows anyway and the slots hold them all at once, half of them or more taken, if
+  // they are not too long (48 sequences of 30 to 800 positions behind 9001, 12 key heads of 64, in all: 27.2 us, split
+  // 28.6; 24 of 9 to 400, 20 rows, 34.9 and 36.1; 64 of 20 to 1500, 8 key heads of 128, 512 segments for 456 slots: 54.5
+  // and 51.2).
+  const long long segments = (long long)a.B * a.Hkv * a.row_blocks, slots = decode_runs(c.d, nt);
+  const bool many = whole != nullptr && segments <= slots && 2 * segments >= slots &&
                     (long long)c.max_blocks * c.page <= kWholeMany;
   if (a.cluster == 0 && (many || !splits(room))) a.cluster = 1;
   if (a.cluster == 0) {

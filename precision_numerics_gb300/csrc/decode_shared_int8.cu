@@ -315,7 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  griddep_wait();
+  // What comes before the call is complete when the prefix's kernel lets the own positions' in, which uses nothing of
+  // it: that kernel waits for the prefix's when it lets the join in, which reads what both have left.
+  if (!OWN) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   const bool abort_all = __any_sync(0xffffffffu, tmem_slot[1] != 0);
   if (threadIdx.x == 0 && abort_all) set_fail(ATTN_ERR_INVALID_ARG);
   Walk<OWN> sg(a, abort_all);
@@ -422,6 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       for (int x = 0; x < slots; ++x) {
         const unsigned uses = use + (x < slot ? 1 : 0);
         if (uses > 0) mbar_wait(&bar_rfull[x], (uses - 1) & 1);
+      }
+      if (OWN) {
+        griddep_wait();
+        griddep_launch_dependents();
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
@@ -878,7 +887,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
   constexpr int kQuads = kJoinWarps / SPLIT;      // of columns at a time
   constexpr int kTurns = D / 4 / kQuads;
   griddep_launch_dependents();
-  griddep_wait();
+  // The prefix's parts are there: every CTA of the kernel over the own positions has waited for them before it let this
+  // one in.
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % SPLIT;
   const int per = kTurns / turns;  // CTAs for the same rows
   int turn = blockIdx.x % per * turns;
@@ -893,7 +903,6 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
   row_of(a, row, b, tok, gg);
   const size_t out = ((size_t)b * a.n_q + tok) * a.H + h * a.G + gg;
   const size_t all = (size_t)a.B * a.n_q * a.H;
-  const float own_m = __ldcg(a.own + all * D + out), own_l = __ldcg(a.own + all * (D + 1) + out);
   // The runs that the unit's tiles are in.  (Runs without a tile begin where the tiles end.)
   const int from = unit * tiles, to = from + tiles;
   const int c0 = __syncthreads_count(begin <= from) - 1, c1 = __syncthreads_count(begin < to) - 1;
@@ -920,10 +929,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
       if (i + z * SPLIT < some) y[z] = columns(i0 + i + z * SPLIT, col);
   };
   fetch(0, share, min(n, kJoinShares), col0);
-  float4 own_o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (share == 0) own_o = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col0));
-
-  float M = warp == 0 ? own_m : -INFINITY, L = warp == 0 ? own_l : 0.f;
+  float M = -INFINITY, L = 0.f;
   float m[kJoinBatch], l[kJoinBatch];
   for (int i0 = warp; i0 < max(n, 1); i0 += kJoinBatch * kJoinWarps) {
 #pragma unroll
@@ -943,12 +949,16 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
   }
   s_m[warp][lane] = M;
   s_l[warp][lane] = L;
+  griddep_wait();
+  const float own_m = __ldcg(a.own + all * D + out), own_l = __ldcg(a.own + all * (D + 1) + out);
+  float4 own_o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (share == 0) own_o = __ldcg(reinterpret_cast<const float4*>(a.own + out * D + col0));
   __syncthreads();
-  M = s_m[0][lane];
+  M = own_m;
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w][lane]);
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w][lane]);
   const float m_use = M == -INFINITY ? 0.f : M;
-  L = 0.f;
+  L = own_l * ex2(own_m - m_use);
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) L += s_l[w][lane] * ex2(s_m[w][lane] - m_use);
   // Values times 1 / L, then times their weight: the two factors' product could fall below FP32's range
