@@ -113,12 +113,32 @@ __device__ __forceinline__ int run_begin(const Args& a, int tiles, int c) {
     const int units = a.row_blocks * a.Hkv, all = tiles * units;
     int runs = min(a.runs, max(all / kLeastRun, 1));
     // As many for each unit where that makes no run longer by more than a tile: a run that meets two units pays
-    // for their rows' way in and out twice (16 units of 40 tiles 23 us, 19 with 9 runs each).
+    // for their rows' way in and out twice (16 units of 40 tiles 23 us, 19 with 9 runs each).  No more of them than
+    // the longest asks for: SMs without one take the own positions meanwhile (64 sequences behind 16000 positions
+    // 51.5 us in all with 19 runs a unit, 49.3 with 18).
     const int each = runs / units;
-    if (each > 0 && (tiles + each - 1) / each <= all / runs + 1) runs = each * units;
+    if (each > 0) {
+      const int most = (tiles + each - 1) / each;
+      if (most <= all / runs + 1) runs = max((tiles + most - 1) / max(most, 1), 1) * units;
+    }
     return c >= runs ? all : (int)divide((long long)all * c, runs);
   }
+  if (tiles == 0) return 0;
   const long long head_cost = (long long)before * kCostTwo + (long long)tiles * last_cost, all = head_cost * a.Hkv;
+  // The same with two costs: the least most that a run takes for which there are runs enough (280 rows of two key heads
+  // over 30000 positions 33.8 us in all, 32.9 so).
+  if (a.row_blocks * a.Hkv <= a.runs && all <= INT_MAX) {
+    const unsigned n = tiles, even = max((unsigned)all / a.runs + 1, (unsigned)(kLeastRun * kCostTwo));
+#pragma unroll 1
+    for (unsigned most = even; most <= even + kCostTwo; ++most) {
+      const unsigned full = a.row_blocks - 1, of_full = (n - 1) / (most / kCostTwo) + 1;
+      const unsigned of_head = full * of_full + (n - 1) / (most / kCostOne) + 1;
+      if (of_head * a.Hkv > (unsigned)a.runs) continue;
+      const unsigned h = c / of_head, x = c - h * of_head, u = min(x / of_full, full), i = x - u * of_full;
+      if (h >= (unsigned)a.Hkv) return tiles * a.row_blocks * a.Hkv;
+      return (h * a.row_blocks + u) * n + n * i / (u < full ? of_full : of_head - full * of_full);
+    }
+  }
   const int runs = (int)max(1ll, min((long long)a.runs, all / (kLeastRun * kCostTwo)));
   if (c >= runs) return tiles * a.row_blocks * a.Hkv;
   const long long x = divide(all * c, runs), h = x / head_cost, y = x - h * head_cost;
