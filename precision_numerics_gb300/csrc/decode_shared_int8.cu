@@ -1095,22 +1095,24 @@ bool own_by_units(const PagedCache& c, int n_q, int H) {
 }
 
 // Whether the prefix is read once a sequence, by attn_decode_int8's kernel in one launch with the own positions,
-// instead of once for 256 rows.  That saves two launches and a join, 14 us, so it is worth it for short
+// instead of once for 256 rows.  That saves two launches and a join, which are worth some us, so it is for short
 // prefixes and few sequences.  By the length that the prefix's table has room for, at these costs in ns for
 // 1000 positions and key head: of a pass of up to 8, 16, 24 or 32 rows of a sequence, and of a unit of one row
-// tile and of two.  Measured with 1 to 64 sequences of 1 to 64 rows a key head (us, by sequence and by unit; 8 key
-// heads of 128): 1 x 102400 42 and 69; 2 x 25600 24 and 33; 4 x 25600 36 and 33; 8 x 6400 23.5 and 22.3; 64 x 400 20
-// and 27; 64 x 1600 39 and 33; 16 x 1600 with 20 rows 24 and 31, 16 x 6400 56 and 35.
+// tile and of two; fitted to 1 to 64 sequences of 1 to 64 rows a key head behind 100 to 102400 positions, of whose 60 and
+// 60 cases it chooses none worse than 1.07 and 1.03 times the better.  (Us, by sequence and by unit; 8 key heads
+// of 128: 1 x 102400 42 and 70; 2 x 25600 24 and 31; 4 x 25600 36 and 31; 8 x 1600 11.3 and 16.6, 8 x 6400 23.5 and 19.7;
+// 64 x 400 20 and 24, 64 x 1600 39 and 25.5; 16 x 400 with 20 rows 14 and 21, 16 x 1600 24.4 and 22.2; d = 64: 8 x 1600
+// 9.4 and 13.4, 8 x 6400 16.4 and 14.0; 64 x 100 8.6 and 18.7, 64 x 400 16.2 and 14.8.)
 bool reads_by_sequence(const PagedCache& c, int n_q, int H, int prefix_blocks) {
   const long long rows = (long long)n_q * (H / c.Hkv), all = rows * c.B;
   const double positions = 1e-3 * prefix_blocks * c.page * c.Hkv;
   if ((long long)(prefix_blocks + (long long)c.max_blocks) * c.page > INT_MAX - 4096 || own_by_units(c, n_q, H)) return false;
-  const double pass[2][4] = {{22, 28, 36, 48}, {31, 40, 53, 69}}, unit[2][2] = {{43, 70}, {55, 90}};
+  const double pass[2][4] = {{22, 28, 36, 48}, {31, 40, 53, 69}}, unit[2][2] = {{44, 70}, {61, 90}};
   const int wide = c.d == 128;
   const long long passes = (rows + 31) / 32, units = (all - 1) / kUnitRows + 1, last = all - (units - 1) * kUnitRows;
   const double by_sequence = pass[wide][((rows + passes - 1) / passes - 1) / 8] * passes * c.B;
   const double by_unit = unit[wide][1] * (units - 1) + unit[wide][last > kBlockM];
-  return (by_sequence - by_unit) * positions < 14000;
+  return (by_sequence - by_unit) * positions < (wide ? 8000 : 4700);
 }
 
 }  // namespace
