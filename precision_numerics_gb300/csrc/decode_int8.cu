@@ -52,6 +52,11 @@
 // the CTAs.  Warps and parts are joined as means with weights of at most 1, so that
 // values up to the largest that a scale allows do not overflow on the way.
 //
+// The kernel also serves attention behind a prefix that a batch shares.  Either (PRE) it goes over the prefix's
+// pages ahead of each sequence's own: the prefix's positions, then none up to a whole tile, then the own ones.  Or
+// decode_shared_int8.cu's kernel has the prefix, and this one leaves (m, l, O / l) of every row for the join with it
+// (whole != nullptr).
+//
 // Measured (d = 128, 8 key heads, pages of 64): 64 sequences of 500 to 16000
 // positions with 4 query rows a key head 102-105 us (5.9 TB/s, 86% of a copy's
 // rate), one of 131000 positions 50 us (5.4 TB/s); d = 64: 58 us and 30 us; with 20
