@@ -1070,9 +1070,10 @@ cudaError_t launch_prefix(const Args& a, int d, int page, unsigned grid, cudaStr
 
 // Rows of a sequence and key head from which on its own positions are this file's kernel's as well, where there are
 // enough units to fill the SMs: attn_decode_int8's goes over the positions for every 32 rows, but splits long ones.
-// (32 sequences of 300 to 1000 positions, 8 key heads of 128, in all with a prefix of 128: 36 rows 74.5 us and
-// 74.4 so, 64 rows 86 and 76, 256 rows 201 and 112; 4 sequences of 4000 positions, 4 key heads, 128 rows 64 and 77.)
-constexpr int kOwnRows = 64;
+// (32 sequences of 333 to 1000 positions behind 8000, 8 key heads of 128, in all: 32 rows 70 us and 77 so, 48 rows 96 and
+// 92, 64 rows 118 and 107, 256 rows 371 and 282; d = 64: 49 and 59, 69.9 and 69.6, 86 and 81, 274 and 217; 4 sequences of
+// 4000 positions, 4 key heads, 128 rows 64 and 77.)
+constexpr int kOwnRows = 33;
 
 struct Layout {
   size_t starts, parts, decode, bytes;  // byte offsets; the own part is at 0
