@@ -1305,12 +1305,11 @@ cudaError_t launch_any(const PagedCache& c, const void* q, const long long* stri
   a.by_segment = 0;
   unsigned runs = 0;
   a.cluster = cluster_size(room, n_q, H, pre);
-  // Whole segments also where a join follows anyway and the slots hold them all at once, half of them or more taken, if
-  // they are not too long (48 sequences of 30 to 800 positions behind 9001, 12 key heads of 64, in all: 27.2 us, split
-  // 28.6; 24 of 9 to 400, 20 rows, 34.9 and 36.1; 64 of 20 to 1500, 8 key heads of 128, 512 segments for 456 slots: 54.5
-  // and 51.2).
-  const long long segments = (long long)a.B * a.Hkv * a.row_blocks, slots = decode_runs(c.d, nt);
-  const bool many = whole != nullptr && segments <= slots && 2 * segments >= slots &&
+  // Whole segments also where a join follows anyway and half of the slots or more have one, if they are not too long:
+  // a launch less (48 sequences of 30 to 800 positions behind 9001, 12 key heads of 64, in all: 27.0 us, split 28.0; 24 of
+  // 9 to 400, 20 rows, 34.3 and 34.4; 64 of 20 to 1500, 8 key heads of 128, 512 segments for 456 slots: 50.6 and 54.7, as a
+  // graph 49.6 and 48.0; 256 of 50 to 1000 157 and 157).
+  const bool many = whole != nullptr && 2ll * a.B * a.Hkv * a.row_blocks >= decode_runs(c.d, nt) &&
                     (long long)c.max_blocks * c.page <= kWholeMany;
   if (a.cluster == 0 && (many || !splits(room))) a.cluster = 1;
   if (a.cluster == 0) {
