@@ -116,7 +116,7 @@ __device__ __forceinline__ int run_begin(const Args& a, int tiles, int c) {
     // As many for each unit where that makes no run longer by more than a tile: a run that meets two units pays
     // for their rows' way in and out twice (16 units of 40 tiles 23 us, 19 with 9 runs each).  No more of them than
     // the longest asks for: SMs without one take the own positions meanwhile (64 sequences behind 16000 positions
-    // 51.5 us in all with 19 runs a unit, 49.3 with 18).
+    // 53.3 us in all with 19 runs a unit, 50.3 with 18).
     const int each = runs / units;
     if (each > 0) {
       const int most = (tiles + each - 1) / each;
