@@ -52,10 +52,10 @@
 // the CTAs.  Warps and parts are joined as means with weights of at most 1, so that
 // values up to the largest that a scale allows do not overflow on the way.
 //
-// The kernel also serves attention behind a prefix that a batch shares.  Either (PRE) it goes over the prefix's
+// The kernel also serves attention behind a prefix that a batch shares.  Either (kWithPrefix) it goes over the prefix's
 // pages ahead of each sequence's own: the prefix's positions, then none up to a whole tile, then the own ones.  Or
 // decode_shared_int8.cu's kernel has the prefix, and this one leaves (m, l, O / l) of every row for the join with it
-// (whole != nullptr).
+// (kBehind; an instance of its own: the choice at run time cost attn_decode_int8 2% with 20 rows).
 //
 // Measured (d = 128, 8 key heads, pages of 64): 64 sequences of 500 to 16000
 // positions with 4 query rows a key head 102-105 us (5.9 TB/s, 86% of a copy's
@@ -263,21 +263,25 @@ struct Args {
   Chain* chains;
   int by_segment;
   unsigned cluster;  // without split mode: CTAs that share a segment
-  // In place of o and lse (else null): O / l [rows][D], m [rows], l [rows], FP32, of all B n_q H
+  // In place of o and lse (kBehind): O / l [rows][D], m [rows], l [rows], FP32, of all B n_q H
   // rows, for a caller that joins them with others.
   float* whole;
   size_t whole_rows;
-  // With a prefix that all sequences begin with (PRE): its pages, its length, and their number.
+  // With a prefix that all sequences begin with (kWithPrefix): its pages, its length, and their number.
   const int *pre_table, *pre_len;
   int pre_blocks;
 };
 
-// The prefix as the sequences have it (PRE): `len` positions, then none up to a whole tile, from where on a
+// What a kernel does besides the sequences' own positions: nothing; it goes over the pages of a prefix ahead of them; or
+// it runs behind the kernel that has the prefix.
+enum Mode { kAlone, kWithPrefix, kBehind };
+
+// The prefix as the sequences have it (kWithPrefix): `len` positions, then none up to a whole tile, from where on a
 // sequence's own are counted.
 struct Prefix {
   int len, end;
 };
-template <bool PRE>
+template <int MODE>
 __device__ __forceinline__ Prefix prefix_of(const Args& a);
 
 // A part in the workspace: O [rows][D] divided by l, m [rows], l [rows], FP32.
@@ -293,16 +297,16 @@ __device__ __forceinline__ size_t out_row(const Args& a, int b, int h, int r) {
 }
 
 // Four columns of a row of the output, and its maximum and sum.
-template <int D>
+template <int D, int MODE>
 __device__ __forceinline__ void put_columns(const Args& a, size_t row, int col, float x, float y, float z, float w) {
-  if (a.whole != nullptr)
+  if constexpr (MODE == kBehind)
     *reinterpret_cast<float4*>(a.whole + row * D + col) = make_float4(x, y, z, w);
   else
     *reinterpret_cast<uint2*>(a.o + row * D + col) = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
 }
-template <int D>
+template <int D, int MODE>
 __device__ __forceinline__ void put_sums(const Args& a, size_t row, float M, float L) {
-  if (a.whole != nullptr) {
+  if constexpr (MODE == kBehind) {
     a.whole[a.whole_rows * D + row] = M;
     a.whole[a.whole_rows * (D + 1) + row] = L;
   } else {
@@ -322,9 +326,9 @@ __device__ __forceinline__ int checked(const Args& a, int len) {
   return len;
 }
 
-template <bool PRE>
+template <int MODE>
 __device__ __forceinline__ Prefix prefix_of(const Args& a) {
-  if constexpr (!PRE) return Prefix{0, 0};
+  if constexpr (MODE != kWithPrefix) return Prefix{0, 0};
   const int len = __ldcg(a.pre_len);
   const long long cap = (long long)a.pre_blocks << a.page_shift;
   const int cut = len < 0 ? 0 : (int)min((long long)len, cap);
@@ -379,16 +383,21 @@ __device__ __forceinline__ long long divide(long long x, int y) {
 
 // Sequences without a position have no tile: their rows are empty.  The CTAs take
 // them by turns; len_first is the unchecked length of sequence blockIdx.x.
-template <int D, bool PRE>
+template <int D, int MODE>
 __device__ __forceinline__ void fill_empty(const Args& a, int len_first, int before) {
-  if (PRE && before > 0) return;
+  if (MODE == kWithPrefix && before > 0) return;
   const int copies = a.Hkv * a.row_blocks;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (checked(a, b == blockIdx.x ? len_first : read_length(a, b)) > 0) continue;
     const size_t row = (size_t)b * a.n_q * a.H;
-    for (int i = threadIdx.x; i < a.n_q * a.H * (D / 4); i += kThreads)
-      put_columns<D>(a, row + i / (D / 4), i % (D / 4) * 4, 0.f, 0.f, 0.f, 0.f);
-    for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) put_sums<D>(a, row + i, -INFINITY, 0.f);
+    if constexpr (MODE == kBehind) {
+      for (int i = threadIdx.x; i < a.n_q * a.H * (D / 4); i += kThreads)
+        reinterpret_cast<float4*>(a.whole + row * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+      for (int i = threadIdx.x; i < a.n_q * a.H * (D / 8); i += kThreads)
+        reinterpret_cast<uint4*>(a.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (int i = threadIdx.x; i < a.n_q * a.H; i += kThreads) put_sums<D, MODE>(a, row + i, -INFINITY, 0.f);
     if (a.by_segment)
       for (int i = threadIdx.x; i < copies; i += kThreads) a.chains[(long long)b * copies + i] = Chain{0, 0, 0, 0};
   }
@@ -415,12 +424,13 @@ __device__ __forceinline__ long long scan_before(long long x, long long* s_warp,
   return upto - x;
 }
 
-template <int D, int NT, bool PRE>
+template <int D, int NT, int MODE>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const Args a) {
   using C = Cfg<D, NT>;
   constexpr int kRows = C::kRows;
+  constexpr bool PRE = MODE == kWithPrefix, behind = MODE == kBehind;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -450,13 +460,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     fence_proxy_async_smem();
   }
   __syncwarp();
-  // Behind the prefix's kernel (whole != nullptr), which let this one in when all before it was complete, and of which
+  // Behind the prefix's kernel, which let this one in when all before it was complete, and of which
   // nothing is used here: its end is waited for by the time this one lets the join in, which reads both's parts.
-  const bool behind = !PRE && a.whole != nullptr;
   if (!behind) griddep_wait();
   if (!ok && threadIdx.x == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
-  const Prefix pre = prefix_of<PRE>(a);
+  const Prefix pre = prefix_of<MODE>(a);
   Walk sg;
   sg.before = pre.end;
   int len_first = 1;
@@ -483,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     int* s_longest = reinterpret_cast<int*>(s_l);
     const long long copies = (long long)a.Hkv * a.row_blocks;
     // (Threads behind the last sequence have none, of a prefix neither.)
-    auto len_at = [&](int b) { return b < a.B ? pre.end + checked(a, read_length(a, b)) : 0; };
+    auto len_at = [&](int b) { return PRE && b >= a.B ? 0 : pre.end + checked(a, read_length(a, b)); };
     const int len_mine = read_length(a, threadIdx.x);
     len_first = read_length(a, blockIdx.x);  // for fill_empty, after the first loads are under way
-    int len = (int)threadIdx.x < a.B ? pre.end + checked(a, len_mine) : 0;
+    int len = PRE && (int)threadIdx.x >= a.B ? 0 : pre.end + checked(a, len_mine);
     long long total, sum;
     long long ahead = scan_before(cost_of(len), s_warp, total);
     const long long first = total;
@@ -531,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     __syncthreads();
     if (!a.by_segment && threadIdx.x == 0) a.chains[blockIdx.x] = Chain{0, 0, 0, 0};
     if (st.x < 0) {  // more CTAs than runs
-      fill_empty<D, PRE>(a, len_first, pre.end);
+      fill_empty<D, MODE>(a, len_first, pre.end);
       if (behind) griddep_wait();
       return;
     }
@@ -543,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     sg.len_next = read_length(a, sg.b + 1);
     sg.take(st.w);
     if (sg.tb == sg.ta) {  // the run ends before the segment's first tile
-      fill_empty<D, PRE>(a, len_first, pre.end);
+      fill_empty<D, MODE>(a, len_first, pre.end);
       if (behind) griddep_wait();
       return;
     }
@@ -656,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   if (more) look_up();
 #pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) issue();
-  if (a.parts != nullptr) fill_empty<D, PRE>(a, len_first, pre.end);
+  if (a.parts != nullptr) fill_empty<D, MODE>(a, len_first, pre.end);
 
   uint32_t used = 0;
   bool last_segment = false;
@@ -689,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                        pack_f16x2(__uint_as_float(w[ks].y << 16) * down, __uint_as_float(w[ks].y & 0xFFFF0000u) * down));
       if (c == 0) {
         s_f[8 * n + g] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-        s_last[8 * n + g] = have ? max(sg.len - a.n_q + t, PRE ? pre.end - 1 : -1) : -1;
+        s_last[8 * n + g] = !have ? -1 : PRE ? max(sg.len - a.n_q + t, pre.end - 1) : sg.len - a.n_q + t;
       }
     }
     __syncthreads();
@@ -963,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           part[kRows * D + r] = M;
           part[kRows * D + kRows + r] = L;
         } else if (rr < rows_total) {
-          put_sums<D>(a, out_row(a, sg.b, sg.h, rr), M, L);
+          put_sums<D, MODE>(a, out_row(a, sg.b, sg.h, rr), M, L);
         }
       }
       // Pairs of columns, moved by four for every second row, so that the 16 lanes
@@ -996,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         if (!whole) {
           *reinterpret_cast<float4*>(part + r * D + at + part4 * 4) = make_float4(v[0], v[1], v[2], v[3]);
         } else if (rr < rows_total) {
-          put_columns<D>(a, out_row(a, sg.b, sg.h, rr), at + part4 * 4, v[0], v[1], v[2], v[3]);
+          put_columns<D, MODE>(a, out_row(a, sg.b, sg.h, rr), at + part4 * 4, v[0], v[1], v[2], v[3]);
         }
       }
     }
@@ -1035,8 +1044,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
       if (rr < rows_total) {
         const size_t row = out_row(a, sg.b, sg.h, rr);
-        put_columns<D>(a, row, col, v.x, v.y, v.z, v.w);
-        if (col == 0) put_sums<D>(a, row, M, L);
+        put_columns<D, MODE>(a, row, col, v.x, v.y, v.z, v.w);
+        if (col == 0) put_sums<D, MODE>(a, row, M, L);
       }
     }
     cluster_sync();  // nobody leaves while its part is read
@@ -1053,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 // another's: grid (chains, groups of rows).  Either a warp takes a row (SHARED false, where
 // there are many chains of a few parts), or all of a CTA's warps share one and take its
 // parts in turn (few chains of many).  The order of the sums is that of the parts.
-template <int D, bool SHARED>
+template <int D, bool SHARED, int MODE>
 __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_kernel(const Args a, int rows) {
   constexpr int kJoinWarps = SHARED ? kJoinShared : 8, per_row = SHARED ? kJoinWarps : 1;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
@@ -1136,12 +1145,12 @@ __global__ void __launch_bounds__(32 * (SHARED ? kJoinShared : 8)) decode_join_k
   const size_t row = out_row(a, ch.y, ch.z / a.row_blocks, rr);
   const int col = lane * (D / 32);
   if constexpr (D == 128)
-    put_columns<D>(a, row, col, o[0], o[1], o[2], o[3]);
-  else if (a.whole != nullptr)
+    put_columns<D, MODE>(a, row, col, o[0], o[1], o[2], o[3]);
+  else if constexpr (MODE == kBehind)
     *reinterpret_cast<float2*>(a.whole + row * D + col) = make_float2(o[0], o[1]);
   else
     *reinterpret_cast<uint32_t*>(a.o + row * D + col) = pack_bf16x2(o[0], o[1]);
-  if (lane == 0) put_sums<D>(a, row, M, L);
+  if (lane == 0) put_sums<D, MODE>(a, row, M, L);
 }
 
 // Runs the tiles are dealt in: the CTAs that the SMs hold at a time.  (The full
@@ -1164,11 +1173,11 @@ bool make_tmap_codes(CUtensorMap* map, const void* base, const PagedCache& c) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT, bool PRE>
+template <int D, int NT, int MODE>
 cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, unsigned runs,
                         cudaStream_t stream) {
   using C = Cfg<D, NT>;
-  auto kernel = decode_int8_kernel<D, NT, PRE>;
+  auto kernel = decode_int8_kernel<D, NT, MODE>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_smem(kernel, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
@@ -1182,8 +1191,8 @@ cudaError_t launch_impl(const CUtensorMap& mk, const CUtensorMap& mv, const Args
   const int rows = std::min(C::kRows, a.n_q * a.G);
   const unsigned chains = a.by_segment ? (unsigned)segments : runs;
   if (shared)
-    return launch_pdl(decode_join_kernel<D, true>, dim3(chains, rows), dim3(32 * kJoinShared), 0, stream, a, C::kRows);
-  return launch_pdl(decode_join_kernel<D, false>, dim3(chains, ceil_div(rows, 8)), dim3(256), 0, stream, a, C::kRows);
+    return launch_pdl(decode_join_kernel<D, true, MODE>, dim3(chains, rows), dim3(32 * kJoinShared), 0, stream, a, C::kRows);
+  return launch_pdl(decode_join_kernel<D, false, MODE>, dim3(chains, ceil_div(rows, 8)), dim3(256), 0, stream, a, C::kRows);
 }
 
 
@@ -1196,7 +1205,7 @@ int row_tiles(int rows) { return ceil_div(rows, 8 * row_passes(rows)); }
 
 // Clusters of `size` CTAs that the device holds at a time (the GPCs' SMs do not divide by
 // every size).
-template <int D, int NT, bool PRE>
+template <int D, int NT, int MODE>
 int clusters_held(int size) {
   using C = Cfg<D, NT>;
   constexpr int kDevices = 16;
@@ -1205,7 +1214,7 @@ int clusters_held(int size) {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < kDevices && (n = known[dev][size].load(std::memory_order_relaxed)) > 0) return n - 1;
-  auto kernel = decode_int8_kernel<D, NT, PRE>;
+  auto kernel = decode_int8_kernel<D, NT, MODE>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)size, 1, 1};
@@ -1224,9 +1233,12 @@ int clusters_held(int size) {
   return n;
 }
 
-int clusters_held(int d, int nt, int size, bool pre) {
+int clusters_held(int d, int nt, int size, Mode mode) {
 #define ATTN_DECODE_CASE(DD, TT) \
-  if (d == DD && nt == TT) return pre ? clusters_held<DD, TT, true>(size) : clusters_held<DD, TT, false>(size);
+  if (d == DD && nt == TT)                                               \
+    return mode == kAlone        ? clusters_held<DD, TT, kAlone>(size)      \
+           : mode == kWithPrefix ? clusters_held<DD, TT, kWithPrefix>(size) \
+                                 : clusters_held<DD, TT, kBehind>(size);
   ATTN_DECODE_CASE(64, 1)
   ATTN_DECODE_CASE(64, 2)
   ATTN_DECODE_CASE(64, 3)
@@ -1246,14 +1258,14 @@ bool splits(const PagedCache& c) { return (long long)c.max_blocks * c.page > (lo
 // key heads of 128: 16.5 -> 13.4 us; one of 2000, 8 heads: 8.4 -> 7.3), the runs use all CTAs
 // and even out ragged lengths.  By the longest sequences that the table has room for: a
 // share against the run if the lengths were half of that.
-int cluster_size(const PagedCache& c, int n_q, int H, bool pre) {
+int cluster_size(const PagedCache& c, int n_q, int H, Mode mode) {
   const int rows = n_q * (H / c.Hkv), nt = row_tiles(rows);
   const long long tiles = (long long)c.max_blocks * c.page / kTile;
   const long long segments = (long long)c.B * c.Hkv * row_passes(rows), runs = decode_runs(c.d, nt);
   if (tiles <= kLoneTiles) return 0;  // (250 positions 5.9 us, 6.5 in clusters; 500 7.8 and 5.9)
   for (long long size = std::min({runs / segments, (long long)kMaxCluster, tiles / 4}); size >= 2; --size) {
     if (tiles / size - tiles * segments / (2 * runs) > kClusterTiles) return 0;
-    if (clusters_held(c.d, nt, (int)size, pre) >= segments) return (int)size;
+    if (clusters_held(c.d, nt, (int)size, mode) >= segments) return (int)size;
   }
   return 0;
 }
@@ -1277,7 +1289,7 @@ PagedCache with_prefix(const PagedCache& c, int pre_blocks) {
 cudaError_t launch_any(const PagedCache& c, const void* q, const long long* strides, const int* pre_table,
                        int pre_blocks, const int* pre_len, const int* lens, void* o, float* lse, int n_q, int H,
                        float scale, void* workspace, cudaStream_t stream, float* whole) {
-  const bool pre = pre_blocks > 0;
+  const Mode mode = pre_blocks > 0 ? kWithPrefix : whole != nullptr ? kBehind : kAlone;
   const PagedCache room = with_prefix(c, pre_blocks);
   Args a;
   a.q = static_cast<const uint16_t*>(q);
@@ -1304,12 +1316,12 @@ cudaError_t launch_any(const PagedCache& c, const void* q, const long long* stri
   const int nt = row_tiles(n_q * a.G);
   a.by_segment = 0;
   unsigned runs = 0;
-  a.cluster = cluster_size(room, n_q, H, pre);
+  a.cluster = cluster_size(room, n_q, H, mode);
   // Whole segments also where a join follows anyway and half of the slots or more have one, if they are not too long:
   // a launch less (48 sequences of 30 to 800 positions behind 9001, 12 key heads of 64, in all: 27.0 us, split 28.0; 24 of
   // 9 to 400, 20 rows, 34.3 and 34.4; 64 of 20 to 1500, 8 key heads of 128, 512 segments for 456 slots: 50.6 and 54.7, as a
   // graph 49.6 and 48.0; 256 of 50 to 1000 157 and 157).
-  const bool many = whole != nullptr && 2ll * a.B * a.Hkv * a.row_blocks >= decode_runs(c.d, nt) &&
+  const bool many = mode == kBehind && 2ll * a.B * a.Hkv * a.row_blocks >= decode_runs(c.d, nt) &&
                     (long long)c.max_blocks * c.page <= kWholeMany;
   if (a.cluster == 0 && (many || !splits(room))) a.cluster = 1;
   if (a.cluster == 0) {
@@ -1323,8 +1335,9 @@ cudaError_t launch_any(const PagedCache& c, const void* q, const long long* stri
   if (!make_tmap_codes(&mk, c.k, c) || !make_tmap_codes(&mv, c.v, c)) return cudaErrorInvalidValue;
 #define ATTN_DECODE_CASE(DD, TT)                                                       \
   if (c.d == DD && nt == TT)                                                            \
-    return pre ? launch_impl<DD, TT, true>(mk, mv, a, runs, stream)                     \
-               : launch_impl<DD, TT, false>(mk, mv, a, runs, stream);
+    return mode == kAlone        ? launch_impl<DD, TT, kAlone>(mk, mv, a, runs, stream)      \
+           : mode == kWithPrefix ? launch_impl<DD, TT, kWithPrefix>(mk, mv, a, runs, stream) \
+                                 : launch_impl<DD, TT, kBehind>(mk, mv, a, runs, stream);
   ATTN_DECODE_CASE(64, 1)
   ATTN_DECODE_CASE(64, 2)
   ATTN_DECODE_CASE(64, 3)
