@@ -20,7 +20,7 @@
 //
 // Measured, a call among others: 3 sequences of one new token 3.7 us, 256 5.8 (one CTA of 256 threads, for which
 // __syncthreads and the scan's rounds cost half of what they do for 1024: 17 -> 7.9 us for two calls); 64 prompts of
-// 150 to 4096 tokens 5.7 and 4.9 for their slots, 1000 of 10 to 6000 10.5 and 11.7 (1 M tokens, 8 MB).  With the
+// 150 to 4096 tokens 5.7 and 4.4 for their slots, 1000 of 10 to 6000 10.5 and 10.5 (1 M tokens, 8 MB).  With the
 // table written first and the tokens' pages read back from it, behind another barrier, these took 35 and 59 us in
 // place of 18 and 32 with the call that takes the step back.
 #include <limits.h>
@@ -307,19 +307,25 @@ __global__ void __launch_bounds__(kSlotThreads) cache_slots_kernel(const Tables 
   const int behind = (int)min(at + kPerCta, (long long)total);  // this CTA's tokens of a sequence: [first, behind)
   int lo = 0, count = 0;
   if (first < behind) {
-    // The last sequence that begins at or before `tok`.
-    auto sequence_of = [&](int tok) {
-      int from = 0, n = t.B;
-      while (n > 1) {
-        const int step = (n - 1) / kSlotThreads + 1, b = from + tid * step;
-        const int before = __syncthreads_count(tid * step < n && __ldcg(t.cu + b) <= tok);
-        from += (before - 1) * step;
-        n = min(step, n - (before - 1) * step);
+    // The last sequences that begin at or before the first and the last of them, both at once.
+    int from[2] = {0, 0}, n[2] = {t.B, t.B};
+    while (n[0] > 1 || n[1] > 1) {
+      int step[2];
+      bool before[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        step[x] = (n[x] - 1) / kSlotThreads + 1;
+        before[x] = tid * step[x] < n[x] && __ldcg(t.cu + from[x] + tid * step[x]) <= (x == 0 ? first : behind - 1);
       }
-      return from;
-    };
-    lo = sequence_of(first);
-    count = sequence_of(behind - 1) - lo + 1;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int skip = (__syncthreads_count(before[x]) - 1) * step[x];
+        from[x] += skip;
+        n[x] = min(step[x], n[x] - skip);
+      }
+    }
+    lo = from[0];
+    count = from[1] - lo + 1;
   }
   const bool held = count <= kHeld;  // else there are many without a token among them
   if (held) {
@@ -345,18 +351,29 @@ __global__ void __launch_bounds__(kSlotThreads) cache_slots_kernel(const Tables 
         x = mid + 1;
     }
   }
+  // The pages of all four are asked for before any is used.
+  const int* entry[4];
+  int page[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     slot[i] = pos[i] = -1;
+    entry[i] = nullptr;
     if (mine + i >= behind) continue;
     while (cu_at(x + 1) <= mine + i) ++x;
     const int before = held ? s_held[x] : __ldcg(t.held + lo + x);
     const int after = held ? s_lens[x] : __ldcg(t.lens + lo + x);
     pos[i] = mine + i - cu_at(x) + before;
-    if (after <= before) continue;  // not served
-    const int page = __ldcg(t.table + (size_t)(lo + x) * t.max_blocks + (pos[i] >> t.page_shift));
-    if (page >= 0 && page < t.P)
-      slot[i] = (page << t.page_shift) + (pos[i] & up);
+    if (after > before)  // served
+      entry[i] = t.table + (size_t)(lo + x) * t.max_blocks + (pos[i] >> t.page_shift);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (entry[i] != nullptr) page[i] = __ldcg(entry[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (entry[i] == nullptr) continue;
+    if (page[i] >= 0 && page[i] < t.P)
+      slot[i] = (page[i] << t.page_shift) + (pos[i] & up);
     else
       set_fail(ATTN_ERR_INVALID_ARG);
   }
