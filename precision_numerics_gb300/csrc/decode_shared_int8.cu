@@ -76,7 +76,12 @@ constexpr int kLeastRun = 2;  // key tiles of a run at least
 // 2^(kTop + 7) or less; W moves again when a tile's could sum to more than kMost, which FP16 still holds.
 constexpr float kTop = 6.f, kMost = 65000.f;
 constexpr float kLeastScale = -104.f;  // log2 of the least value scale whose weights reach 2^kTop
-constexpr float kMostSum = 0x1p40f;  // of a tile's weights relative to the row's maximum so far
+constexpr float kMostSum = 0x1p40f;  // of a tile's weights relative to the row's m
+// A row's m moves to its maximum less kLow.  Its W lies above s + log2(vs) - kTop of all positions, so 2^(m - W) vs stays
+// below 2^(kTop + 126 - kLow), which FP32 holds, for every position whose weight in the row's sum, e^(s - max), is a
+// normal number, whatever the ratio of the value scales.  (Those below count as 0.)
+constexpr float kLow = 8.f, kLowFactor = 0x1p-8f;
+constexpr float kMostFloat = 0x1.fffffep127f;
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_shared, code); }
 
@@ -591,8 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------- softmax
-    // A thread has a row of tile (or half) t: its maximum and sum so far, the weights of the row sum relative to
-    // that maximum, and the reference W (in base 2) of the weights that are multiplied with the codes, and
+    // A thread has a row of tile (or half) t: m_ref, kLow below its maximum when that last moved it, the sum of the
+    // weights relative to it, and the reference W (in base 2) of the weights that are multiplied with the codes, and
     // so of the accumulators.
     const int t = warp >> 2, w0 = (warp & 3) * 32;
     const int r = w0 + lane;  // row within the tile = TMEM lane
@@ -757,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
               }
               float f_o = 1.f;
               if (moves && mt > -INFINITY) {
-                const float m_new = fmaxf(m_ref, mt), W_new = fmaxf(W, mw - kTop);
+                const float m_new = fmaxf(m_ref, mt - kLow), W_new = fmaxf(W, mw - kTop);
                 l_run *= ex2(m_ref - m_new);
                 f_o = ex2(W - W_new);
                 m_ref = m_new;
@@ -796,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
 #pragma unroll
               for (int i = 0; i < 32 / GROUP; ++i) {
                 const int group = c * 2 + i;
-                const float k = factor(group), v = fminf(hd.vs[group] * up, 0x1p127f);
+                const float k = factor(group), v = fminf(hd.vs[group] * up, kMostFloat);
                 k2[i] = f2_pack(k, k);
                 v2[i] = f2_pack(v, v);
               }
@@ -822,7 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             for (int i = 0; i < 4; ++i) f2_unpack(sums2[i], sums[2 * i], sums[2 * i + 1]);
             sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
             if (again) break;
-            moves = m_ref == -INFINITY || !(sum * fminf(hd.v_most * up, 0x1p127f) <= kMost && sum <= kMostSum);
+            // (So does a product that FP32 does not hold.)
+            moves = m_ref == -INFINITY || !(sum * (hd.v_most * up) <= kMost && sum <= kMostSum);
             again = __any_sync(0xffffffffu, moves);
             if (!again) break;
           }
@@ -872,8 +878,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                               __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
         }
         if (!OWN || r < have) {
-          sums[0] = m_ref;
-          sums[rows] = l_run;
+          // As the join and the sum's logarithm have them best, where adding is exact enough.
+          const bool back = fabsf(m_ref) < 0x1p24f;
+          sums[0] = back ? m_ref + kLow : m_ref;
+          sums[rows] = back ? l_run * kLowFactor : l_run;
         }
       }
       // O_t has been read: the next segment's first P V, which overwrites it, waits for these warps' next P.

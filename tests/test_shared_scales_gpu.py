@@ -1,0 +1,58 @@
+"""Attention over a shared prefix: value scales far apart, in every order of the pages and in each of its kernels."""
+import math
+
+import pytest
+
+from test_serving_gpu import A, normal  # noqa: F401
+from test_shared_gpu import WIDE, call, check, make
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def by_units(A, q, Hkv, page, blocks, max_blocks):  # noqa: N803
+    """Whether the prefix is read once for 256 rows: only then the workspace has room for a part of 256 rows for each of
+    the runs, of which there are as many as SMs."""
+    B, n_q, H, d = q.shape
+    return A.attn_decode_shared_int8_workspace_bytes(B, n_q, H, Hkv, d, page, blocks, max_blocks) > 128 * 256 * (d + 2) * 4
+
+
+# Where the two kinds of pages lie: in the prefix, read once for 256 rows (by units of two row tiles, and of one, whose
+# key tiles two halves take by turns) or once a sequence, or among the own positions of many new tokens, by units.
+# (B, Hkv, G, n_q, how often the pattern comes: runs have several key tiles)
+FORMS = {"two": (64, 8, 8, 1, 8), "one": (32, 8, 4, 1, 24), "by sequence": (2, 2, 2, 2, 1), "own": (80, 2, 4, 16, 1)}
+GAPS = [(100, 118), (112, 123), (112, 132), (118, 121), (118, 123), (118, 126), (118, 140), (124, 123), (124, 129)]
+PLACES = [(1, 512), (128, 512), (33, 490), (130, 510), (7, 383)]
+CASES = [(form, *place, *gap, d) for form in FORMS for place in (PLACES[1:3] if form == "one" else PLACES) for gap in GAPS
+         for d in (64, 128) if gap in GAPS[4::4] or d == 128 and form != "one"]
+
+
+@pytest.mark.parametrize("form,count,first,gap,ratio,d", CASES)
+def test_large_values_of_small_weights_last(A, form, count, first, gap, ratio, d):
+    """The pages from position `first` on, `count` positions, have weights of 2^-gap of the row's largest and value scales
+    2^ratio times those before them, so that what they add to O is 2^(ratio - gap) of the others': in the key tile of the
+    others, and in one of their own behind theirs."""
+    B, Hkv, G, n_q, times = FORMS[form]
+    page, n = 16, first + count
+    pages = -(-n // page)
+    n = n if times == 1 else pages * page * times
+    lens = [n - b % 3 for b in range(B)] if form == "own" else [1 + b % 3 for b in range(B)]
+    n0 = 40 if form == "own" else n
+    c, pre = make(n0, lens, Hkv, page, d)
+    c.codes[0].remainder_(9).sub_(4)  # scores stay within some tenths of what channel 0 makes them
+    c.codes[0][..., 0] = 100
+    c.scales[0][:] = 0.002
+    c.scales[1] *= 2.0 ** -40
+    for table in c.tables if form == "own" else [pre]:
+        last = [p for j, p in enumerate(table) if (j % pages + 1) * page > first]
+        c.scales[1][last] *= 2.0 ** (ratio // 2)  # (in two steps: 2^128 is no FP32 number)
+        c.scales[1][last] *= 2.0 ** (ratio - ratio // 2)
+        c.codes[0][last, ..., 0] = 0
+    c.upload()
+    q = normal((B, n_q, Hkv * G, d), 1)
+    q[..., 0] = gap / 0.2  # 100 * 0.002 * gap / 0.2 = gap
+    room = 0 if form == "by sequence" else WIDE
+    assert by_units(A, q, Hkv, page, len(pre) + room // page, c.gpu[4].shape[1]) == (form != "by sequence")
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room, scale=math.log(2.0))
+    A.attn_check_status()
+    check(c, pre, n0, q, lens, math.log(2.0), o, lse, shown=(0, 1, B - 1))
