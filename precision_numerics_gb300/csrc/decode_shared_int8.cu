@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
       int g = 0, slot = 0;
       unsigned use = 0;  // rounds of the ring so far
       while (ok && sg.next(a)) {
-        // A page that is not seen takes any scale: its positions are hidden.
+        // (Where there is no page, page 0's, which is not used.)
         auto scale_at = [&](const float* scales, int id) { return __ldcg(scales + (max(id, 0) * a.Hkv + sg.h)); };
         int ids = checked(sg.k0, pages_at(sg.k0)), ids_next = pages_at(sg.k0 + 4);
         float ks = scale_at(a.k_scale, ids), vs = scale_at(a.v_scale, ids);
@@ -407,7 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
             const unsigned loaded = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
             const int seen = id >= 0 ? max(0, min(16, sg.len - ((sg.k0 + e) * kBlockN + 16 * group))) : 0;
             const bool hidden = __any_sync(0xffffffffu, seen < 16);
-            const float k = __shfl_sync(0xffffffffu, ks, lanes + group), v = __shfl_sync(0xffffffffu, vs, lanes + group);
+            // Positions without a page are hidden, and their scale is 0: another page's must decide nothing.
+            float k = __shfl_sync(0xffffffffu, ks, lanes + group), v = __shfl_sync(0xffffffffu, vs, lanes + group);
+            if (id < 0) k = v = 0.f;
             const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
             // The scales' slot: its last tile, kHeads before, has been through the softmax.  (The ring's place for
             // the tile before was free, so the products S of the tile that many tiles and stages ago are complete.)

@@ -3,7 +3,7 @@ import math
 
 import pytest
 
-from test_serving_gpu import A, normal  # noqa: F401
+from test_serving_gpu import A, Cache, normal, scattered  # noqa: F401
 from test_shared_gpu import WIDE, call, check, make
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +56,43 @@ def test_large_values_of_small_weights_last(A, form, count, first, gap, ratio, d
     o, lse = call(A, q.cuda(), c, pre, n0, lens, room, scale=math.log(2.0))
     A.attn_check_status()
     check(c, pre, n0, q, lens, math.log(2.0), o, lse, shown=(0, 1, B - 1))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (128, 32), (64, 64)])
+@pytest.mark.parametrize("n", [5, 130, 300, 517])
+@pytest.mark.parametrize("absent", [False, True])
+def test_scales_of_pages_in_no_table_decide_nothing(A, form, absent, n, page, d):
+    """Pages that no table names, page 0 among them, hold any scales at all (they may never have been written, or another
+    stream writes them): the last key tile ends inside, and `absent` pages are out of range.  The value scales grow from
+    page to page, so that a row's references have to move in the last tile as well."""
+    B, Hkv, G, n_q, _ = FORMS[form]
+    lens = [n + b % 3 for b in range(B)] if form == "own" else [1 + b % 3 for b in range(B)]
+    n0 = 40 if form == "own" else n
+    tables, pages = scattered([-(-n0 // page)] + [-(-x // page) for x in lens], 7)
+    tables = [[p + 1 for p in t] for t in tables]
+    c = Cache(pages + 1, Hkv, page, d, tables[1:])
+    for table in tables:
+        for j, p in enumerate(table):
+            c.scales[1][p] *= 2.0 ** (3 * j)
+    used = [p for t in tables for p in t]
+    rest = [p for p in range(pages + 1) if p not in set(used)]
+    assert 0 in rest
+    pre = list(tables[0])
+    if absent:
+        (pre if form != "own" else c.tables[0])[n // page // 2] = pages + 1
+        c = Cache(pages + 1, Hkv, page, d, c.tables) if form == "own" else c
+    q = normal((B, n_q, Hkv * G, d), 1).cuda()
+    room, want = 0 if form == "by sequence" else WIDE, None
+    assert by_units(A, q, Hkv, page, len(pre) + room // page, c.gpu[4].shape[1]) == (form != "by sequence")
+    for poison in (0.01, 0.0, -1.0, 2.0 ** 100, torch.inf, -torch.inf, torch.nan):
+        for scales in c.scales:
+            scales[rest] = poison
+        c.upload()
+        got = call(A, q, c, pre, n0, lens, room)
+        if absent:
+            with pytest.raises(A.AttnError, match="out of range"):
+                A.attn_check_status()
+        A.attn_check_status()
+        want = want or got
+        assert got[0].isfinite().all() and all(torch.equal(x, y) for x, y in zip(want, got)), poison
