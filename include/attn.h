@@ -292,8 +292,8 @@ ATTN_API attn_status attn_bwd_noalloc(const void* q, const void* k, const void* 
  * kernels, so a call can be captured in a CUDA graph and replayed on new ones.
  * They cannot be checked before the launch: a value out of range never leads
  * outside the tensors, and attn_check_status() reports ATTN_ERR_INVALID_ARG.  Pages
- * whose number is out of range are neither written nor seen; attn_cache_append_int8
- * leaves out a sequence whose length or start is, and the other calls cut lengths to
+ * whose number is out of range are neither written nor seen; appending leaves out
+ * a sequence whose length or start is, and the other calls cut lengths to
  * what the tensors hold.  A sequence may have no token at all.
  *
  * The cache: codes k_cache, v_cache int8 [num_pages, H_kv, page_size, d],
@@ -364,6 +364,18 @@ ATTN_API attn_status attn_cache_append_int8(const void* k, const void* v, long l
                                             const int* cu_seqlens, const int* starts, int B, int T,
                                             int H_kv, int d, int num_pages, int page_size,
                                             int max_blocks, cudaStream_t stream);
+
+/*
+ * attn_cache_append_int8 without the rows from position lens[b] on (int32 [B], device, 0 or more):
+ * they are neither written nor counted into a scale, and their pages are not looked up.  With the
+ * lens that attn_cache_reserve has written these are the rows of the requests that were not served,
+ * which leave the cache as it was; nothing is reported for them.
+ */
+ATTN_API attn_status attn_cache_append_served_int8(
+    const void* k, const void* v, long long k_token_stride, long long k_head_stride,
+    long long v_token_stride, long long v_head_stride, void* k_cache, void* v_cache, float* k_scale,
+    float* v_scale, const int* block_table, const int* cu_seqlens, const int* starts, const int* lens,
+    int B, int T, int H_kv, int d, int num_pages, int page_size, int max_blocks, cudaStream_t stream);
 
 /*
  * Reads ranges of positions back as values code * scale: packed token
@@ -482,9 +494,10 @@ ATTN_API attn_status attn_decode_shared_int8(
  *   positions   : int32 [T], written: each new token's position in its sequence; -1 behind the
  *                 last token.  More new tokens than T are reported, and the first T written.
  * num_pages * page_size < 2^31.  lens, cu_seqlens, slots and positions, and what is updated, overlap
- * nothing.  attn_cache_append_int8 takes cu_seqlens and held (as starts) for the new rows, and
- * attn_decode_int8 takes lens.  The rows of a request that was not served still go into the room that its
- * last page has if they are appended, unseen but counted into that page's scales.
+ * nothing.  attn_cache_append_served_int8 takes cu_seqlens, held (as starts) and lens for the new
+ * rows, and attn_decode_int8 takes lens.  (attn_cache_append_int8, which has no lens, is for steps whose
+ * requests are all served: it would put the rows of one that was not into the room that its last page has, count
+ * them into that page's scales, and report the pages that they lack.)
  */
 ATTN_API attn_status attn_cache_reserve(int* block_table, const int* held, const int* wanted,
                                         int* free_pages, int* n_free, int* lens, int* cu_seqlens,

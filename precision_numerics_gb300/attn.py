@@ -32,7 +32,7 @@ EXPORTED = ("attn_version", "attn_status_string", "attn_last_error", "attn_fwd",
             "attn_bwd_noalloc", "attn_fwd_stable", "attn_quantize_int8", "attn_fwd_int8",
             "attn_quantize_int8_as_bf16", "attn_fwd_int8_as_bf16",
             "attn_varlen_plan_bytes", "attn_varlen_plan", "attn_varlen_fwd",
-            "attn_cache_append_int8", "attn_cache_read_int8",
+            "attn_cache_append_int8", "attn_cache_append_served_int8", "attn_cache_read_int8",
             "attn_decode_int8_workspace_bytes", "attn_decode_int8",
             "attn_decode_shared_int8_workspace_bytes", "attn_decode_shared_int8", "attn_cache_reserve")
 
@@ -70,6 +70,7 @@ _SIGNATURES = {
     "attn_varlen_plan": (_i, [_vp] + [_i] * 5 + [_vp, _sz, _vp]),
     "attn_varlen_fwd": (_i, [_vp] * 3 + [_ll] * 6 + [_vp, _sz, _vp, _vp] + [_i] * 5 + [_f, _i, _vp]),
     "attn_cache_append_int8": (_i, [_vp] * 2 + [_ll] * 4 + [_vp] * 7 + [_i] * 7 + [_vp]),
+    "attn_cache_append_served_int8": (_i, [_vp] * 2 + [_ll] * 4 + [_vp] * 8 + [_i] * 7 + [_vp]),
     "attn_cache_read_int8": (_i, [_vp] * 9 + [_i] * 8 + [_vp]),
     "attn_decode_int8_workspace_bytes": (_sz, [_i] * 7),
     "attn_decode_int8": (_i, [_vp] + [_ll] * 3 + [_vp] * 8 + [_i] * 8 + [_f, _vp, _sz, _vp]),
@@ -533,12 +534,14 @@ def attn_varlen_fwd(q, k, v, plan, scale=None, causal=True, o=None, lse=None, st
 
 
 def attn_cache_append_int8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, starts,
-                           stream=None):
+                           stream=None, lens=None):
     """Write the packed rows k, v [T,H_kv,d] BF16 behind the starts[b] positions that every
-    sequence holds (see include/attn.h for the scales' rule).  Returns (k_cache, v_cache)."""
+    sequence holds (see include/attn.h for the scales' rule).  With lens int32 [B], as
+    attn_cache_reserve gives it, rows from position lens[b] on are left out: those of a request
+    that got no pages.  Returns (k_cache, v_cache)."""
     if stream is None:
         done = (_BINDING or _binding()).cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
-                                                     cu_seqlens, starts)
+                                                     cu_seqlens, starts, lens)
         if done is not None:
             return done
     B, pages, hk, page, d, blocks = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
@@ -548,10 +551,14 @@ def attn_cache_append_int8(k, v, k_cache, v_cache, k_scale, v_scale, block_table
     _check_rows("v", v, (T, hk, d))
     _check_ints("cu_seqlens", cu_seqlens, B + 1)
     _check_ints("starts", starts, B)
-    _call("attn_cache_append_int8", k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0),
-          v.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-          block_table.data_ptr(), cu_seqlens.data_ptr(), starts.data_ptr(), B, T, hk, d, pages, page,
-          blocks, _stream(stream))
+    ends = ()
+    if lens is not None:
+        _check_ints("lens", lens, B)
+        ends = (lens.data_ptr(),)
+    _call("attn_cache_append_served_int8" if ends else "attn_cache_append_int8", k.data_ptr(), v.data_ptr(),
+          k.stride(0), k.stride(1), v.stride(0), v.stride(1), k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), starts.data_ptr(),
+          *ends, B, T, hk, d, pages, page, blocks, _stream(stream))
     return k_cache, v_cache
 
 
@@ -668,7 +675,8 @@ def attn_cache_reserve(block_table, held, wanted, free_pages, n_free, page_size,
                        slots=None, positions=None, stream=None):
     """Take the sequences from held to wanted positions (int32 [B]): pages move between block_table
     [B,max_blocks] and the stack free_pages [pages] of n_free [1] entries, all int32 and updated.  Returns
-    (lens [B], cu_seqlens [B+1], slots [T], positions [T]) of the step's new tokens, T at most."""
+    (lens [B], cu_seqlens [B+1], slots [T], positions [T]) of the step's new tokens, T at most.
+    attn_cache_append_int8 takes cu_seqlens, held and lens, by which it leaves out what got no pages."""
     if stream is None:
         done = (_BINDING or _binding()).cache_reserve(block_table, held, wanted, free_pages, n_free, page_size, T, lens,
                                                       cu_seqlens, slots, positions)

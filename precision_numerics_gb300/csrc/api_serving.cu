@@ -107,6 +107,29 @@ struct Ints {
   const int* p;
   long long n;
 };
+// attn_cache_append_int8, with the lengths at which rows end where there are any.
+attn_status append(const void* k, const void* v, long long k_token_stride, long long k_head_stride,
+                   long long v_token_stride, long long v_head_stride, void* k_cache, void* v_cache, float* k_scale,
+                   float* v_scale, const int* block_table, const int* cu_seqlens, const int* starts, const int* lens,
+                   bool with_lens, int B, int T, int H_kv, int d, int num_pages, int page_size, int max_blocks,
+                   cudaStream_t stream, const char* what) {
+  PagedCache c;
+  PtrCheck ptr;
+  ATTN_CHECK(check_packed(B, T));
+  const long long strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  const char* names[4] = {"k_token_stride", "k_head_stride", "v_token_stride", "v_head_stride"};
+  for (int i = 0; i < 4; ++i) ATTN_CHECK(check_stride(strides[i], names[i]));
+  ATTN_CHECK(check_cache(k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, d, num_pages, page_size,
+                         max_blocks, ptr, &c));
+  ATTN_CHECK(ptr(cu_seqlens, "cu_seqlens", 4));
+  ATTN_CHECK(ptr(starts, "starts", 4));
+  if (with_lens) ATTN_CHECK(ptr(lens, "lens", 4));
+  if (T == 0) return launched(cudaSuccess, what);
+  ATTN_CHECK(ptr(k, "k"));
+  ATTN_CHECK(ptr(v, "v"));
+  return launched(launch_cache_append_int8(c, k, v, strides, cu_seqlens, starts, lens, T, stream), what);
+}
+
 attn_status check_apart(const Ints& x, const Ints& y) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
   if (a != 0 && b != 0 && x.n > 0 && y.n > 0 && a < b + 4 * (uintptr_t)y.n && b < a + 4 * (uintptr_t)x.n)
@@ -175,21 +198,20 @@ attn_status attn_cache_append_int8(const void* k, const void* v, long long k_tok
                                    float* k_scale, float* v_scale, const int* block_table, const int* cu_seqlens,
                                    const int* starts, int B, int T, int H_kv, int d, int num_pages, int page_size,
                                    int max_blocks, cudaStream_t stream) {
-  PagedCache c;
-  PtrCheck ptr;
-  ATTN_CHECK(check_packed(B, T));
-  const long long strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
-  const char* names[4] = {"k_token_stride", "k_head_stride", "v_token_stride", "v_head_stride"};
-  for (int i = 0; i < 4; ++i) ATTN_CHECK(check_stride(strides[i], names[i]));
-  ATTN_CHECK(check_cache(k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, d, num_pages, page_size,
-                         max_blocks, ptr, &c));
-  ATTN_CHECK(ptr(cu_seqlens, "cu_seqlens", 4));
-  ATTN_CHECK(ptr(starts, "starts", 4));
-  if (T == 0) return launched(cudaSuccess, "attn_cache_append_int8");
-  ATTN_CHECK(ptr(k, "k"));
-  ATTN_CHECK(ptr(v, "v"));
-  return launched(launch_cache_append_int8(c, k, v, strides, cu_seqlens, starts, T, stream),
-                  "attn_cache_append_int8");
+  return append(k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride, k_cache, v_cache, k_scale, v_scale,
+                block_table, cu_seqlens, starts, nullptr, false, B, T, H_kv, d, num_pages, page_size, max_blocks, stream,
+                "attn_cache_append_int8");
+}
+
+attn_status attn_cache_append_served_int8(const void* k, const void* v, long long k_token_stride,
+                                          long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                                          void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                          const int* block_table, const int* cu_seqlens, const int* starts,
+                                          const int* lens, int B, int T, int H_kv, int d, int num_pages, int page_size,
+                                          int max_blocks, cudaStream_t stream) {
+  return append(k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride, k_cache, v_cache, k_scale, v_scale,
+                block_table, cu_seqlens, starts, lens, true, B, T, H_kv, d, num_pages, page_size, max_blocks, stream,
+                "attn_cache_append_served_int8");
 }
 
 attn_status attn_cache_read_int8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,

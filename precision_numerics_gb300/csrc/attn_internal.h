@@ -137,10 +137,11 @@ struct PagedCache {
 // Base-2 logarithm of a page size (16, 32, 64 or 128).
 inline int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
-// strides: token and head stride of the K rows, then of the V rows (elements).
+// strides: token and head stride of the K rows, then of the V rows (elements).  lens: null, or where each
+// sequence's rows end.
 cudaError_t launch_cache_append_int8(const PagedCache& c, const void* k, const void* v,
                                      const long long* strides, const int* cu, const int* starts,
-                                     int T, cudaStream_t stream);
+                                     const int* lens, int T, cudaStream_t stream);
 cudaError_t launch_cache_read_int8(const PagedCache& c, const int* cu, const int* starts, void* k,
                                    void* v, int T, bool fp32, cudaStream_t stream);
 // strides: batch, token and head stride of q (elements).  whole: FP32 means, maxima and sums in place

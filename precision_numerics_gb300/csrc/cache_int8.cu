@@ -28,6 +28,7 @@
 // (by up to page * d bytes a warp, 16 bytes a lane at a time, one after the other).  Which a
 // decoding step meets depends on its values: a scale grows when a new row exceeds all before
 // it in its page and head.
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -204,14 +205,16 @@ __device__ __forceinline__ float scale_for(uint32_t bits) { return __uint_as_flo
 
 // Sequence b's new rows: `first` is its first row of the packed input, n their
 // number, `start` the position of the first.  None where a length in memory is out of
-// range: rows put elsewhere would overwrite what the pages hold.
-__device__ __forceinline__ void new_rows(const int* cu, const int* starts, int b, int T, int& first, int& n,
-                                         int& start) {
+// range: rows put elsewhere would overwrite what the pages hold.  With `lens` none from position lens[b] on
+// either (a request that got no pages holds what it held).
+__device__ __forceinline__ void new_rows(const int* cu, const int* starts, const int* lens, int b, int T, int& first,
+                                         int& n, int& start) {
   const int x = __ldcg(cu + b), y = __ldcg(cu + b + 1), z = __ldcg(starts + b);
-  const bool fine = x >= 0 && y >= x && y <= T && z >= 0;
+  const int end = lens != nullptr ? __ldcg(lens + b) : INT_MAX;
+  const bool fine = x >= 0 && y >= x && y <= T && z >= 0 && end >= 0;
   if (!fine) set_fail(ATTN_ERR_INVALID_ARG);
   first = fine ? x : 0;
-  n = fine ? y - x : 0;
+  n = fine ? max(min(y - x, end - z), 0) : 0;
   start = fine ? z : 0;
 }
 
@@ -220,7 +223,7 @@ struct AppendArgs {
   long long token_stride[2], head_stride[2];
   int8_t* codes[2];
   float* scales[2];
-  const int *table, *cu, *starts;
+  const int *table, *cu, *starts, *lens;  // lens may be null
   int B, T, Hkv, P, page, page_shift, max_blocks;
 };
 
@@ -243,7 +246,7 @@ __device__ __forceinline__ Found find_page(const AppendArgs& a, int item) {
     const int b = b0 + tid;
     int first = 0, n = 0, start = 0, count = 0;
     if (b < a.B) {
-      new_rows(a.cu, a.starts, b, a.T, first, n, start);
+      new_rows(a.cu, a.starts, a.lens, b, a.T, first, n, start);
       if (n > 0) count = ((n - 1 + (start & (a.page - 1))) >> a.page_shift) + 1;
     }
     int upto = count;
@@ -489,7 +492,7 @@ cudaError_t launch_read(const ReadArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_cache_append_int8(const PagedCache& c, const void* k, const void* v,
                                      const long long* strides, const int* cu, const int* starts,
-                                     int T, cudaStream_t stream) {
+                                     const int* lens, int T, cudaStream_t stream) {
   AppendArgs a;
   a.x[0] = static_cast<const uint16_t*>(k);
   a.x[1] = static_cast<const uint16_t*>(v);
@@ -502,6 +505,7 @@ cudaError_t launch_cache_append_int8(const PagedCache& c, const void* k, const v
   a.table = c.table;
   a.cu = cu;
   a.starts = starts;
+  a.lens = lens;
   a.B = c.B, a.T = T, a.Hkv = c.Hkv, a.P = c.P, a.page = c.page, a.max_blocks = c.max_blocks;
   a.page_shift = page_shift(c.page);
   // A token touches one page at most, a sequence of n tokens (n - 1) / page + 2.

@@ -167,17 +167,27 @@ PyObject* varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, starts)
+// (k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, starts, lens)
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Cache c;
-  if (n != 9 || !cache_of(a + 2, &c)) Py_RETURN_NONE;
+  if (n != 10 || !cache_of(a + 2, &c)) Py_RETURN_NONE;
   const Tensor *k = tensor(a[0]), *v = tensor(a[1]), *cu = tensor(a[7]), *starts = tensor(a[8]);
   if (k == nullptr || k->dim() != 3) Py_RETURN_NONE;
   const int64_t T = k->size(0);
   if (T > INT32_MAX || !rows(k, {T, c.hk, c.d}) || !rows(v, {T, c.hk, c.d}) || !ints(cu, c.B + (int64_t)1) ||
       !ints(starts, c.B))
     Py_RETURN_NONE;
+  if (a[9] != Py_None) {
+    const Tensor* lens = tensor(a[9]);
+    if (!ints(lens, c.B)) Py_RETURN_NONE;
+    const attn_status s = attn_cache_append_served_int8(
+        k->data_ptr(), v->data_ptr(), k->stride(0), k->stride(1), v->stride(0), v->stride(1), c.k->data_ptr(),
+        c.v->data_ptr(), (float*)c.ks->data_ptr(), (float*)c.vs->data_ptr(), (const int*)c.table->data_ptr(),
+        (const int*)cu->data_ptr(), (const int*)starts->data_ptr(), (const int*)lens->data_ptr(), c.B, (int)T, c.hk, c.d,
+        c.pages, c.page, c.blocks, stream());
+    return s == ATTN_OK ? PyTuple_Pack(2, a[2], a[3]) : raise("attn_cache_append_served_int8", s);
+  }
   const attn_status s = attn_cache_append_int8(
       k->data_ptr(), v->data_ptr(), k->stride(0), k->stride(1), v->stride(0), v->stride(1), c.k->data_ptr(),
       c.v->data_ptr(), (float*)c.ks->data_ptr(), (float*)c.vs->data_ptr(), (const int*)c.table->data_ptr(),
