@@ -94,7 +94,7 @@ struct Args {
   int B, n_q, H, Hkv, G, P, page_shift, blocks;
   int rows, row_blocks, runs;
   float scale_log2;
-  int* starts;  // [runs + 2]: each run's first tile, all tiles, and the key tiles of the prefix
+  int* starts;  // [runs + 1]: each run's first tile, and the key tiles of the prefix
   float* parts;
   float* own;  // O / l [B n_q H][D], m [B n_q H], l [B n_q H] of the own parts
   uint16_t* o;
@@ -352,10 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   Walk<OWN> sg(a, abort_all);
   if (!OWN && threadIdx.x == 32 * kCopyWarp) {
     a.starts[blockIdx.x] = sg.start;
-    if (blockIdx.x == gridDim.x - 1) {
-      a.starts[a.runs] = sg.start + sg.left;
-      a.starts[a.runs + 1] = sg.tiles;
-    }
+    if (blockIdx.x == 0) a.starts[a.runs] = sg.tiles;
   }
   // All units have one row tile: one copy of Q, and a longer ring.
   const bool one = !OWN && a.rows <= kBlockM;
@@ -928,7 +925,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
   const int h = unit / a.row_blocks, rb = unit - h * a.row_blocks;
   if (rb * kUnitRows + rows0 >= a.rows) return;
   const int begin = (int)threadIdx.x < a.runs ? __ldcg(a.starts + threadIdx.x) : INT_MAX;
-  const int tiles = __ldcg(a.starts + a.runs + 1);
+  const int tiles = __ldcg(a.starts + a.runs);
   const int r = rows0 + lane, row = min(rb * kUnitRows + r, a.rows - 1);
   int b, tok, gg;
   row_of(a, row, b, tok, gg);
@@ -1093,7 +1090,7 @@ Layout layout(const PagedCache& c, int n_q, int H) {
   const size_t units = (size_t)c.Hkv * ((rows + kUnitRows - 1) / kUnitRows);
   Layout w;
   w.starts = align256(all * (c.d + 2) * sizeof(float));
-  w.parts = w.starts + align256((shared_runs() + 2) * sizeof(int));
+  w.parts = w.starts + align256((shared_runs() + 1) * sizeof(int));
   w.decode = w.parts + align256((units + shared_runs()) * part_floats(c.d) * sizeof(float));
   w.bytes = w.decode + decode_workspace_bytes(c, n_q, H);
   return w;
