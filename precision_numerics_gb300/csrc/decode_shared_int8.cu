@@ -1076,11 +1076,15 @@ cudaError_t launch_prefix(const Args& a, int d, int page, unsigned grid, cudaStr
 }
 
 // Rows of a sequence and key head from which on its own positions are this file's kernel's as well, where there are
-// enough units to fill the SMs: attn_decode_int8's goes over the positions for every 32 rows, but splits long ones.
-// (32 sequences of 333 to 1000 positions behind 8000, 8 key heads of 128, in all: 32 rows 70 us and 77 so, 48 rows 96 and
-// 92, 64 rows 118 and 107, 256 rows 371 and 282; d = 64: 49 and 59, 69.9 and 69.6, 86 and 81, 274 and 217; 4 sequences of
-// 4000 positions, 4 key heads, 128 rows 64 and 77.)
-constexpr int kOwnRows = 33;
+// enough units to fill the SMs and, unless the rows fill a unit, the table has no room for more than rows^2 / kOwnRoom
+// positions: attn_decode_int8's goes over the positions for every 32 rows, but deals long histories to all SMs, where a unit
+// is one CTA's from its first key tile to its last.  (20 sequences behind 8000 positions, 8 key heads of 128, us so and by
+// attn_decode_int8's kernel: all of a quarter of a length to it, and one of that length among those of 300 or less.  36 rows
+// and 500: 56 and 51, 53 and 50; 64 rows and 500 73 and 67, 67 and 68, 1000 79 and 80, 74 and 70, 16000 317 and 251, 250 and 90;
+// 128 rows and 2048 129 and 168, 121 and 122, 4096 183 and 208, 146 and 120; 256 rows and 2048 219 and 264, 197 and 202, 16384
+// 437 and 914, 374 and 270; 400 rows and 25600 1058 and 2413, 592 and 510.  d = 64: 48 rows and 500 46 and 43, 46 and 41, 128
+// and 2048 97 and 122, 93 and 91, 256 and 16384 366 and 649, 308 and 195.)
+constexpr int kOwnRows = 64, kOwnRoom = 8;
 
 struct Layout {
   size_t starts, parts, decode, bytes;  // byte offsets; the own part is at 0
@@ -1099,7 +1103,8 @@ Layout layout(const PagedCache& c, int n_q, int H) {
 // Whether the own positions are this file's kernel's too.
 bool own_by_units(const PagedCache& c, int n_q, int H) {
   const long long rows = (long long)n_q * (H / c.Hkv);
-  return rows >= kOwnRows && c.B * c.Hkv * ((rows - 1) / kUnitRows + 1) >= shared_runs();
+  return rows >= kOwnRows && (rows >= kUnitRows || (long long)c.max_blocks * c.page <= rows * rows / kOwnRoom) &&
+         c.B * c.Hkv * ((rows - 1) / kUnitRows + 1) >= shared_runs();
 }
 
 // Whether the prefix is read once a sequence, by attn_decode_int8's kernel in one launch with the own positions,

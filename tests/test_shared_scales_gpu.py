@@ -20,7 +20,7 @@ def by_units(A, q, Hkv, page, blocks, max_blocks):  # noqa: N803
 # Where the two kinds of pages lie: in the prefix, read once for 256 rows (by units of two row tiles, and of one, whose
 # key tiles two halves take by turns) or once a sequence, or among the own positions of many new tokens, by units.
 # (B, Hkv, G, n_q, how often the pattern comes: runs have several key tiles)
-FORMS = {"two": (64, 8, 8, 1, 8), "one": (32, 8, 4, 1, 24), "by sequence": (2, 2, 2, 2, 1), "own": (80, 2, 4, 16, 1)}
+FORMS = {"two": (64, 8, 8, 1, 8), "one": (32, 8, 4, 1, 24), "by sequence": (2, 2, 2, 2, 1), "own": (80, 2, 8, 16, 1)}
 GAPS = [(100, 118), (112, 123), (112, 132), (118, 121), (118, 123), (118, 126), (118, 140), (124, 123), (124, 129)]
 PLACES = [(1, 512), (128, 512), (33, 490), (130, 510), (7, 383)]
 CASES = [(form, *place, *gap, d) for form in FORMS for place in (PLACES[1:3] if form == "one" else PLACES) for gap in GAPS
