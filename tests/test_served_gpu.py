@@ -64,6 +64,28 @@ def test_append_up_to_lens(A, many, page, d, monkeypatch):
     assert fresh.equal()
 
 
+@pytest.mark.parametrize("rows_each", [3, 40])
+def test_append_up_to_lens_many_sequences(A, rows_each):
+    """More sequences than threads look for the pages at a time; a third of them is left out."""
+    B, Hkv, page, d = 700, 2, 16, 64
+    g = torch.Generator().manual_seed(3)
+    starts = torch.randint(0, 50, (B,), generator=g).tolist()
+    lens = torch.randint(0, rows_each, (B,), generator=g).tolist()
+    kept = [0 if b % 3 == 1 else n for b, n in enumerate(lens)]
+    T, cu = sum(lens), sums(lens)
+    assert (T <= 8 * B) == (rows_each == 3)
+    tables, pages = scattered([-(-(s + n) // page) for s, n in zip(starts, kept)], 2)
+    c = Cache(pages, Hkv, page, d, tables, width=6)
+    rows = [normal((T, Hkv, d), 1), normal((T, Hkv, d), 2)]
+    for i in range(2):
+        for b, t in enumerate(c.tables):
+            ref.append(rows[i][cu[b]:cu[b] + kept[b]], c.codes[i], c.scales[i], t, starts[b])
+    A.attn_cache_append_int8(rows[0].cuda(), rows[1].cuda(), *c.gpu, ints(cu), ints(starts),
+                             lens=ints([s + n for s, n in zip(starts, kept)]))
+    A.attn_check_status()
+    assert c.equal()
+
+
 def test_append_up_to_lens_refuses(A):
     c = Cache(4, 2, 16, 64, [[0], [1]])
     x, cu, starts = normal((4, 2, 64), 1).cuda(), ints([0, 2, 4]), ints([0, 0])
