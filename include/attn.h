@@ -443,7 +443,8 @@ ATTN_API size_t attn_decode_shared_int8_workspace_bytes(int B, int n_q, int H, i
  *                   row t % page_size of page prefix_table[t / page_size].  How the
  *                   prefix is read follows from prefix_blocks and the shape: a table far
  *                   wider than the prefix gives O within the same bounds, but not always the same
- *                   bits, and a short prefix some microseconds later.
+ *                   bits, and a short prefix takes up to twice as long (8 key heads of 128: 8 sequences
+ *                   behind 400 positions 8.3 us, in a table for 32768 14.9; 64 behind 100 16 and 30).
  *   prefix_len    : int32 [1], device: 0 to prefix_blocks * page_size.
  *   block_table   : int32 [B, max_blocks]: the pages of each sequence's own positions,
  *                   which are counted from 0 behind the prefix (the first of them begins a

@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   __syncwarp();
   // Behind the prefix's kernel, which let this one in when all before it was complete, and of which
   // nothing is used here: its end is waited for by the time this one lets the join in, which reads both's parts.
+  // (That q, tables and lengths are seen without a wait here is the assumption named in shared_prefix_kernel.)
   if (!behind) griddep_wait();
   if (!ok && threadIdx.x == 0) set_fail(ATTN_ERR_INVALID_ARG);
 
@@ -1317,10 +1318,11 @@ cudaError_t launch_any(const PagedCache& c, const void* q, const long long* stri
   a.by_segment = 0;
   unsigned runs = 0;
   a.cluster = cluster_size(room, n_q, H, mode);
-  // Whole segments also where a join follows anyway and half of the slots or more have one, if they are not too long:
-  // a launch less (48 sequences of 30 to 800 positions behind 9001, 12 key heads of 64, in all: 27.0 us, split 28.0; 24 of
-  // 9 to 400, 20 rows, 34.3 and 34.4; 64 of 20 to 1500, 8 key heads of 128, 512 segments for 456 slots: 50.6 and 54.7, as a
-  // graph 49.6 and 48.0; 256 of 50 to 1000 157 and 157).
+  // Whole segments also where a join follows anyway and half of the slots or more have one, if they are not too long: a
+  // launch less.  That is for calls made one by one, where the host's launches count; replayed as a graph, even runs are
+  // worth up to 3% where the segments are ragged and more than the slots.  (48 sequences of 30 to 800 positions behind
+  // 9001, 12 key heads of 64, in all: 27.0 us, split 28.0; 24 of 9 to 400, 20 rows, 34.3 and 34.4; 64 of 20 to 1500, 8 key
+  // heads of 128, 512 segments for 456 slots: 50.6 and 54.7, as a graph 49.6 and 48.0; 256 of 50 to 1000 157 and 157.)
   const bool many = mode == kBehind && 2ll * a.B * a.Hkv * a.row_blocks >= decode_runs(c.d, nt) &&
                     (long long)c.max_blocks * c.page <= kWholeMany;
   if (a.cluster == 0 && (many || !splits(room))) a.cluster = 1;

@@ -343,6 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // What comes before the call is complete when the prefix's kernel lets the own positions' in, which uses nothing of
   // it: that kernel waits for the prefix's when it lets the join in, which reads what both have left.
+  // (PTX promises the grid that waits that it sees what came before.  That the grid which this one then lets in sees it
+  // too, without a wait of its own, is an assumption: it was complete and in L2 before that grid began, which reads it from
+  // there, by ld.cg and bulk copies.)
   if (!OWN) {
     griddep_wait();
     griddep_launch_dependents();
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
   constexpr int kTurns = D / 4 / kQuads;
   griddep_launch_dependents();
   // The prefix's parts are there: every CTA of the kernel over the own positions has waited for them before it let this
-  // one in.
+  // one in.  (That they are seen without a wait here is the assumption named in shared_prefix_kernel.)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % SPLIT;
   const int per = kTurns / turns;  // CTAs for the same rows
   int turn = blockIdx.x % per * turns;
@@ -1077,13 +1080,13 @@ cudaError_t launch_prefix(const Args& a, int d, int page, unsigned grid, cudaStr
 
 // Rows of a sequence and key head from which on its own positions are this file's kernel's as well, where there are
 // enough units to fill the SMs and, unless the rows fill a unit, the table has no room for more than rows^2 / kOwnRoom
-// positions: attn_decode_int8's goes over the positions for every 32 rows, but deals long histories to all SMs, where a unit
-// is one CTA's from its first key tile to its last.  (20 sequences behind 8000 positions, 8 key heads of 128, us so and by
-// attn_decode_int8's kernel: all of a quarter of a length to it, and one of that length among those of 300 or less.  36 rows
-// and 500: 56 and 51, 53 and 50; 64 rows and 500 73 and 67, 67 and 68, 1000 79 and 80, 74 and 70, 16000 317 and 251, 250 and 90;
-// 128 rows and 2048 129 and 168, 121 and 122, 4096 183 and 208, 146 and 120; 256 rows and 2048 219 and 264, 197 and 202, 16384
-// 437 and 914, 374 and 270; 400 rows and 25600 1058 and 2413, 592 and 510.  d = 64: 48 rows and 500 46 and 43, 46 and 41, 128
-// and 2048 97 and 122, 93 and 91, 256 and 16384 366 and 649, 308 and 195.)
+// positions: attn_decode_int8's goes over the positions for every 32 rows, but deals long histories to all SMs, where a
+// unit is one CTA's from its first key tile to its last.  (20 sequences behind 8000 positions, 8 key heads of 128, us so
+// and by attn_decode_int8's kernel: all of a quarter of a length to it, and one of that length among those of 300 or
+// less.  36 rows and 500: 56 and 51, 53 and 50; 64 rows and 500 73 and 67, 67 and 68, 1000 79 and 80, 74 and 70, 16000 317
+// and 251, 250 and 90; 128 rows and 2048 129 and 168, 121 and 122, 4096 183 and 208, 146 and 120; 256 rows and 2048 219 and
+// 264, 197 and 202, 16384 437 and 914, 374 and 270; 400 rows and 25600 1058 and 2413, 592 and 510.  d = 64: 48 rows and 500
+// 46 and 43, 46 and 41, 128 and 2048 97 and 122, 93 and 91, 256 and 16384 366 and 649, 308 and 195.)
 constexpr int kOwnRows = 64, kOwnRoom = 8;
 
 struct Layout {
