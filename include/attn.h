@@ -498,7 +498,8 @@ ATTN_API attn_status attn_decode_shared_int8(
  * nothing.  attn_cache_append_served_int8 takes cu_seqlens, held (as starts) and lens for the new
  * rows, and attn_decode_int8 takes lens.  (attn_cache_append_int8, which has no lens, is for steps whose
  * requests are all served: it would put the rows of one that was not into the room that its last page has, count
- * them into that page's scales, and report the pages that they lack.)
+ * them into that page's scales, and report the pages that they lack.)  What attention gives for the new
+ * tokens of a request that was not served is of no use: their positions are not there.
  */
 ATTN_API attn_status attn_cache_reserve(int* block_table, const int* held, const int* wanted,
                                         int* free_pages, int* n_free, int* lens, int* cu_seqlens,
