@@ -79,8 +79,10 @@ constexpr float kLeastScale = -104.f;  // log2 of the least value scale whose we
 constexpr float kMostSum = 0x1p40f;  // of a tile's weights relative to the row's m
 // A row's m moves to its maximum less kLow.  Its W lies above s + log2(vs) - kTop of all positions, so 2^(m - W) vs stays
 // below 2^(kTop + 126 - kLow), which FP32 holds, for every position whose weight in the row's sum, e^(s - max), is a
-// normal number, whatever the ratio of the value scales.  (Those below count as 0.)
-constexpr float kLow = 8.f, kLowFactor = 0x1p-8f;
+// normal number, whatever the ratio of the value scales.  (Those below count as 0.)  And W is at most that of the largest
+// vs, so 2^(m - W) is above 2^(kTop - kLow - 128), which FP32 holds too.
+constexpr float kLow = kTop - 2.f, kLowFactor = 1.f / 16;
+static_assert(kLow == 4.f, "kLowFactor is 2^-kLow");
 constexpr float kMostFloat = 0x1.fffffep127f;
 
 __device__ __forceinline__ void set_fail(unsigned int code) { atomicOr(&g_status_shared, code); }
@@ -861,7 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                           : a.parts + (size_t)(blockIdx.x + sg.h * a.row_blocks + sg.rb) * part_floats(D) +
                                 D * kUnitRows + t * kBlockM + r;
         const size_t rows = OWN ? own_rows : kUnitRows;
-        const float inv = inverse(l_run), down = W == -INFINITY ? 0.f : ex2(W - m_ref);
+        // (Relative to kLow above m_ref: 2^(W - m_ref) alone may pass what values next to FP32's end leave.)
+        const float inv = inverse(l_run * kLowFactor), down = W == -INFINITY ? 0.f : ex2(W - m_ref - kLow);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];

@@ -21,7 +21,8 @@ def by_units(A, q, Hkv, page, blocks, max_blocks):  # noqa: N803
 # key tiles two halves take by turns) or once a sequence, or among the own positions of many new tokens, by units.
 # (B, Hkv, G, n_q, how often the pattern comes: runs have several key tiles)
 FORMS = {"two": (64, 8, 8, 1, 8), "one": (32, 8, 4, 1, 24), "by sequence": (2, 2, 2, 2, 1), "own": (80, 2, 8, 16, 1)}
-GAPS = [(100, 118), (112, 123), (112, 132), (118, 121), (118, 123), (118, 126), (118, 140), (124, 123), (124, 129)]
+GAPS = [(100, 118), (112, 123), (112, 132), (118, 121), (118, 123), (118, 126), (118, 140), (124, 123), (124, 129),
+        (125, 130)]
 PLACES = [(1, 512), (128, 512), (33, 490), (130, 510), (7, 383)]
 CASES = [(form, *place, *gap, d) for form in FORMS for place in (PLACES[1:3] if form == "one" else PLACES) for gap in GAPS
          for d in (64, 128) if gap in GAPS[4::4] or d == 128 and form != "one"]
@@ -96,3 +97,27 @@ def test_scales_of_pages_in_no_table_decide_nothing(A, form, absent, n, page, d)
         A.attn_check_status()
         want = want or got
         assert got[0].isfinite().all() and all(torch.equal(x, y) for x, y in zip(want, got)), poison
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [120.0, 126.9, 127.9])
+def test_value_scales_next_to_the_last(A, form, d, size):
+    """Value scales up to FP32's end whose codes are small enough for finite values: +-1 at 2^127.9, +-100 at 2^120."""
+    B, Hkv, G, n_q, times = FORMS[form]
+    page, n = 16, 300 * times
+    lens = [n - b % 3 for b in range(B)] if form == "own" else [1 + b % 3 for b in range(B)]
+    n0 = 40 if form == "own" else n
+    c, pre = make(n0, lens, Hkv, page, d)
+    c.codes[1].remainder_(3).sub_(1)
+    if size == 120.0:
+        c.codes[1].mul_(100)
+    c.scales[1][:] = 2.0 ** size
+    c.upload()
+    q = normal((B, n_q, Hkv * G, d), 1)
+    room = 0 if form == "by sequence" else WIDE
+    assert by_units(A, q, Hkv, page, len(pre) + room // page, c.gpu[4].shape[1]) == (form != "by sequence")
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room)
+    A.attn_check_status()
+    assert o.isfinite().all()
+    check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse, shown=(0, 1, B - 1))
