@@ -883,10 +883,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                               __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
         }
         if (!OWN || r < have) {
-          // As the join and the sum's logarithm have them best, where adding is exact enough.
-          const bool back = fabsf(m_ref) < 0x1p24f;
-          sums[0] = back ? m_ref + kLow : m_ref;
-          sums[rows] = back ? l_run * kLowFactor : l_run;
+          // As the join and the sum's logarithm have them best, where adding is exact enough.  m_ref may lie far below the
+          // maximum where the value scales fall as the scores rise: then m takes the sum's power of two as well, or
+          // 2^(m - M) could be 0 in the join where the sum makes up for it.
+          const bool back = fabsf(m_ref) < 0x1p24f, lags = l_run >= 0x1p20f && fabsf(m_ref) < 0x1p20f;
+          const int e = lags ? (int)(__float_as_uint(l_run) >> 23) - 127 : (int)kLow;
+          sums[0] = back ? m_ref + (float)e : m_ref;
+          sums[rows] = back ? l_run * __uint_as_float((uint32_t)(127 - e) << 23) : l_run;
         }
       }
       // O_t has been read: the next segment's first P V, which overwrites it, waits for these warps' next P.

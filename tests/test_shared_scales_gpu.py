@@ -121,3 +121,41 @@ def test_value_scales_next_to_the_last(A, form, d, size):
     A.attn_check_status()
     assert o.isfinite().all()
     check(c, pre, n0, q, lens, 1 / math.sqrt(d), o, lse, shown=(0, 1, B - 1))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", ["two", "one"])
+def test_parts_whose_maximum_lags(A, form, d):
+    """In the first half of the prefix key tiles of score 0 and of score 31 take turns, with value scales that fall as
+    much but for 2^3, so that a part's reference stays where the first tile left it; the second half has score 155 and value
+    scales 2^124 smaller, so that both halves weigh alike in O.  Weights of 2^-124 are kept."""
+    B, Hkv, G, n_q, times = FORMS[form]
+    page, tiles = 16, 8 * times
+    n0, lens = 128 * tiles, [1 + b % 3 for b in range(B)]
+    c, pre = make(n0, lens, Hkv, page, d)
+    c.codes[0].remainder_(9).sub_(4)
+    c.codes[0][..., 0] = 0
+    c.scales[0][:] = 0.002
+    c.scales[1].fill_(2.0 ** 60)
+    for table in c.tables:  # own positions have a weight of 2^-155 and next to no value
+        c.scales[1][table] = 2.0 ** -100
+    for j, p in enumerate(pre):
+        tile = j // 8
+        if tile >= tiles // 2:
+            c.codes[0][p, ..., 0] = 100
+            c.scales[1][p] *= 2.0 ** -124
+        elif tile % 2:
+            c.codes[1][p] = 100 if j % 8 == 3 else 0
+            if j % 8 == 3:
+                c.codes[0][p, ..., 0] = 20
+        else:
+            c.codes[1][p] = 1 if j % 8 == 2 else 0  # what the weights of 2^-155 are worth stays small
+            if j % 8 == 2:
+                c.scales[1][p] *= 2.0 ** 28
+    c.upload()
+    q = normal((B, n_q, Hkv * G, d), 1)
+    q[..., 0] = 776.0  # 100 * 0.002 * 776 = 155.2
+    assert by_units(A, q, Hkv, page, len(pre) + WIDE // page, c.gpu[4].shape[1])
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, WIDE, scale=math.log(2.0))
+    A.attn_check_status()
+    check(c, pre, n0, q, lens, math.log(2.0), o, lse, shown=(0, 1, B - 1))
