@@ -281,6 +281,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 // 1 / L, or 0 where a row has seen nothing.  A NaN stays one.
 __device__ __forceinline__ float inverse(float L) { return L == 0.f ? 0.f : 1.f / L; }
+// l 2^x, x <= 0, of a part: m may lie far below its largest score where the value scales fall as the scores rise, and l be
+// as much larger, so that 2^x alone could be 0 where the product counts.
+__device__ __forceinline__ float share_of(float l, float x) {
+  const float half = ex2(0.5f * x);
+  return l * half * half;
+}
 // Sequence, token and head of row r of key head h's rows.
 __device__ __forceinline__ void row_of(const Args& a, int r, int& b, int& t, int& g) {
   const int x = r / a.G;
@@ -883,13 +889,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Args a
                               __uint_as_float(o[4 * i + 1]) * inv * down, __uint_as_float(o[4 * i + 3]) * inv * down);
         }
         if (!OWN || r < have) {
-          // As the join and the sum's logarithm have them best, where adding is exact enough.  m_ref may lie far below the
-          // maximum where the value scales fall as the scores rise: then m takes the sum's power of two as well, or
-          // 2^(m - M) could be 0 in the join where the sum makes up for it.
-          const bool back = fabsf(m_ref) < 0x1p24f, lags = l_run >= 0x1p20f && fabsf(m_ref) < 0x1p20f;
-          const int e = lags ? (int)(__float_as_uint(l_run) >> 23) - 127 : (int)kLow;
-          sums[0] = back ? m_ref + (float)e : m_ref;
-          sums[rows] = back ? l_run * __uint_as_float((uint32_t)(127 - e) << 23) : l_run;
+          // As the join and the sum's logarithm have them best, where adding is exact enough.
+          const bool back = fabsf(m_ref) < 0x1p24f;
+          sums[0] = back ? m_ref + kLow : m_ref;
+          sums[rows] = back ? l_run * kLowFactor : l_run;
         }
       }
       // O_t has been read: the next segment's first P V, which overwrites it, waits for these warps' next P.
@@ -995,19 +998,20 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w][lane]);
   const float m_use = M == -INFINITY ? 0.f : M;
-  L = own_l * ex2(own_m - m_use);
+  const float own_share = share_of(own_l, own_m - m_use);
+  L = own_share;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) L += s_l[w][lane] * ex2(s_m[w][lane] - m_use);
   // Values times 1 / L, then times their weight: the two factors' product could fall below FP32's range
   // where a small weight meets large values.
-  const float inv = inverse(L), own_share = own_l * ex2(own_m - m_use);
+  const float inv = inverse(L);
   auto add = [&](float4& o, const float4& v, float l) {
     o.x += v.x * inv * l, o.y += v.y * inv * l, o.z += v.z * inv * l, o.w += v.w * inv * l;
   };
   if (few) {
 #pragma unroll
     for (int k = 0; k < kJoinBatch; ++k)
-      if (warp + k * kJoinWarps < n) s_share[warp + k * kJoinWarps][lane] = l[k] * ex2(m[k] - m_use);
+      if (warp + k * kJoinWarps < n) s_share[warp + k * kJoinWarps][lane] = share_of(l[k], m[k] - m_use);
     __syncthreads();
   }
   for (int k = 0; k < turns; ++k, ++turn) {
@@ -1021,7 +1025,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const Args a,
       const int some = min(kJoinShares, n - i0);
       if (!few) {
         __syncthreads();
-        for (int i = warp; i < some; i += kJoinWarps) s_share[i][lane] = sum_of(i0 + i) * ex2(max_of(i0 + i) - m_use);
+        for (int i = warp; i < some; i += kJoinWarps) s_share[i][lane] = share_of(sum_of(i0 + i), max_of(i0 + i) - m_use);
         __syncthreads();
       }
       for (int i = share; i < some; i += kJoinBatch * SPLIT) {

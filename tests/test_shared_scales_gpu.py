@@ -159,3 +159,33 @@ def test_parts_whose_maximum_lags(A, form, d):
     o, lse = call(A, q.cuda(), c, pre, n0, lens, WIDE, scale=math.log(2.0))
     A.attn_check_status()
     check(c, pre, n0, q, lens, math.log(2.0), o, lse, shown=(0, 1, B - 1))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("course", ["rise", "cancel", "turns"])
+@pytest.mark.parametrize("gap,span,run,d", [(124, 110, 16, 64), (124, 110, 8, 128), (60, 60, 2, 128), (30, 20, 9, 64)])
+def test_scores_and_value_scales_of_opposite_course(A, form, course, gap, span, run, d):
+    """Scores rise by `gap` in base 2 over the positions, `run` pages at a time, while value scales fall by 2^(2 span), or
+    by as much as the scores rise, or both change by turns: the largest weights of the values lie anywhere in the row, at
+    any distance from its largest score, and references lag behind the scores."""
+    B, Hkv, G, n_q, times = FORMS[form]
+    page, n = 16, 407 * times
+    lens = [n - b % 3 for b in range(B)] if form == "own" else [1 + b % 3 for b in range(B)]
+    n0 = 40 if form == "own" else n
+    c, pre = make(n0, lens, Hkv, page, d)
+    c.codes[0].remainder_(9).sub_(4)
+    c.scales[0][:] = 0.002
+    for table in c.tables if form == "own" else [pre]:
+        for j, p in enumerate(table):
+            x = j // run % 2 if course == "turns" else j // run / max(1, (len(table) - 1) // run)
+            c.codes[0][p, ..., 0] = round(100 * x)
+            e = gap / 2 - gap * x if course == "cancel" else span - 2 * span * x
+            c.scales[1][p] *= 2.0 ** e
+    c.upload()
+    q = normal((B, n_q, Hkv * G, d), 1)
+    q[..., 0] = gap / 0.2
+    room = 0 if form == "by sequence" else WIDE
+    assert by_units(A, q, Hkv, page, len(pre) + room // page, c.gpu[4].shape[1]) == (form != "by sequence")
+    o, lse = call(A, q.cuda(), c, pre, n0, lens, room, scale=math.log(2.0))
+    A.attn_check_status()
+    check(c, pre, n0, q, lens, math.log(2.0), o, lse, shown=(0, B - 1))
